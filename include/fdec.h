@@ -91,6 +91,20 @@ typedef struct {
 typedef struct fdec_plan_s* fdec_plan_t;
 
 /*
+ * Rows of a set of tokens: element (token i, head h, dim d) of a 16-bit array at
+ *   base + i*stride_tok + h*stride_head + d
+ * (strides in elements).  A head slice of a fused QKV tensor is one.
+ */
+typedef struct {
+    const void* base;
+    int64_t stride_tok;
+    int64_t stride_head;
+} fdec_rows;
+
+/* Element type of the output rows of fdec_run_selected: fp32, or the query's type. */
+enum { FDEC_OUT_F32 = 0, FDEC_OUT_SAME = 1 };
+
+/*
  * Split-kernel paths.  SIMT: fp32 FMA (every head_dim).  MMA: warp-level
  * tensor-core MMA on 16-row query groups (every head_dim), the decode
  * default.  TC: 5th-generation tensor cores (tcgen05, accumulators in tensor
@@ -292,6 +306,129 @@ fdec_status fdec_append_e4m3(const void* k_new, const void* v_new, int64_t new_s
                              const int32_t* batch_indices, const int32_t* positions, int n_tokens, int num_kv_heads,
                              int head_dim, int page_size, fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_table,
                              int batch, int64_t page_table_stride, uint32_t* device_errors, cudaStream_t stream);
+
+/*
+ * Block-sparse decoding: a query token attends to the pages of its cache that a
+ * cheap bound on their logits selects, not to all of them.  A step is
+ *   fdec_norm_rope_append   the new tokens' rows: norm, rotation, write to the cache
+ *   fdec_page_bounds        min and max of the keys of the pages that changed
+ *   fdec_select_pages       for each query token and KV head, the pages to read
+ *   fdec_run_selected       attention over them
+ * Each is one kernel launch (fdec_run_selected: its plan's launches), allocates
+ * nothing, and may be captured in a CUDA graph.  Their kernels start as
+ * programmatic dependents of the kernel before them on `stream` and touch nothing
+ * before it has completed, so stream order holds as for ordinary launches.
+ * (The pages have no counterpart of these four.)
+ */
+
+/*
+ * RMS norm of every query and key head of the new tokens, rotation by position,
+ * and the paged write of keys and values, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight           (q and k rows, over head_dim)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)          pairs of the first rot_dim elements
+ *   q -> q_out;  k, v -> the cache, as fdec_append writes them (v neither normed nor rotated)
+ * computed in fp32 and rounded once.
+ *   q, k_new, v_new: rows of n_tokens tokens with num_qo_heads, num_kv_heads and
+ *      num_kv_heads heads; q_out: rows for the result, which may be q itself (same
+ *      strides) but not overlap it otherwise.  Rows start on 16-byte boundaries.
+ *   q_weight, k_weight: device [head_dim] of dtype, or NULL (ones).  eps >= 0.
+ *   cos_sin: float32 device [cos_sin_rows][rot_dim]; row t holds rot_dim / 2 cosines,
+ *      then rot_dim / 2 sines, of position t.  NULL when rot_dim is 0.
+ *   rot_dim: a multiple of 16 in [0, head_dim].  interleaved: pairs are elements
+ *      (2e, 2e + 1), else (e, e + rot_dim / 2).
+ *   batch_indices, positions, page_table, page_table_stride: as for fdec_append;
+ *      rope_positions: int32 device [n_tokens], the rows of cos_sin, or NULL (positions).
+ *   kv_dtype: FDEC_KV_SAME, or FDEC_KV_E4M3 (head_dim 128 and 256): the codes stored
+ *      are those of k / k_scale and v / v_scale, rounded to nearest even, saturating at
+ *      448.  Scales are 1 for a 16-bit cache.
+ *   device_errors: optional uint32 device word.  A token with a bad sequence, position
+ *      (or a row outside cos_sin) sets FDEC_DEVERR_SEQ_LEN, one with a bad page id
+ *      FDEC_DEVERR_PAGE_ID; nothing of that token is written, its q_out rows included.
+ * Tokens must not repeat a (sequence, position).
+ */
+fdec_status fdec_norm_rope_append(fdec_rows q, fdec_rows k_new, fdec_rows v_new, const void* q_weight,
+                                  const void* k_weight, float eps, const float* cos_sin, int64_t cos_sin_rows,
+                                  int rot_dim, int interleaved, const int32_t* batch_indices, const int32_t* positions,
+                                  const int32_t* rope_positions, int n_tokens, int num_qo_heads, int num_kv_heads,
+                                  int head_dim, int page_size, fdec_dtype dtype, int kv_dtype, float k_scale,
+                                  float v_scale, fdec_rows q_out, fdec_kv_desc k, fdec_kv_desc v,
+                                  const int32_t* page_table, int batch, int64_t page_table_stride,
+                                  uint32_t* device_errors, cudaStream_t stream);
+
+/*
+ * Elementwise bounds of the keys of pages: for every page that holds a position in
+ * [begins[b], seq_lens[b]) of sequence b and every KV head,
+ *   bounds[page, h, 0, :] = min over the page's slots of positions below seq_lens[b] of K,
+ *   bounds[page, h, 1, :] = max   (a NaN element of a key gives NaN).
+ * The whole page is read again (also its positions before begins[b]).  Other pages'
+ * bounds are not written.  Exact for every type.
+ *   bounds: a 16-bit pool of dtype: element (page, head, side, dim) with side (0: min,
+ *      1: max) in the place of the token; same alignment rules as K.  For an E4M3 cache
+ *      (kv_dtype) the bounds are those of the codes' values, without k_scale.
+ *   begins: int32 device [batch], or NULL (0: all pages of every sequence).
+ *   seq_lens_dev: int32 device [batch]; a negative value or one above
+ *      page_table_stride * page_size sets FDEC_DEVERR_SEQ_LEN and is clamped.
+ *   expected_tokens: about how many tokens seq_lens - begins is at most; sizes the
+ *      launch (1 in a decoding step).  Any value gives the same result.
+ * Two sequences that share a page must agree on it (both past its end, or equal).
+ */
+fdec_status fdec_page_bounds(fdec_kv_desc k, fdec_kv_desc bounds, const int32_t* page_table, int batch,
+                             int64_t page_table_stride, const int32_t* begins, const int32_t* seq_lens_dev,
+                             int num_kv_heads, int head_dim, int page_size, fdec_dtype dtype, int kv_dtype,
+                             int expected_tokens, uint32_t* device_errors, cudaStream_t stream);
+
+/*
+ * Device bytes that fdec_select_pages needs for these sizes, and how many of them, at
+ * the start, must be zero before the first call with it (every call leaves them zero).
+ */
+fdec_status fdec_select_pages_workspace(int batch, int q_len, int num_kv_heads, int64_t max_pages,
+                                        size_t* workspace_bytes, size_t* zero_bytes);
+
+/*
+ * Select pages.  For each query token n = (b, i) and KV head, of the pages that the
+ * token sees (its length is seq_lens[b], or seq_lens[b] - q_len + i + 1 with causal):
+ * the first first_pages and the newest last_pages of them, then those with the largest
+ *   score = sum over the group's query heads of sum_d max(q_d min_d, q_d max_d)
+ * (the largest logit that a key within the page's bounds can have), budget in all;
+ * equal scores go to the lower index, and a NaN score counts as infinite.  The order
+ * is that of the scores summed in 64 bits.  All pages, when there are at most budget.
+ *   q: as for fdec_run (any alignment); bounds: as written by fdec_page_bounds.
+ *   max_pages: the most pages that a sequence has (at most page_table_stride); a length
+ *      above max_pages * page_size or below 0 sets FDEC_DEVERR_SEQ_LEN and is clamped.
+ *   budget >= first_pages + last_pages, last_pages >= 1.
+ *   page_ids: int32 device [batch * q_len][num_kv_heads][budget], the physical pages in
+ *      the order of their positions, -1 past their number.
+ *   counts: int32 device [batch * q_len][num_kv_heads], the tokens in those pages (every
+ *      page but the newest is full; 0 for a token that sees nothing).
+ *   page_indices: like page_ids, with the pages' indices in the sequence; or NULL.
+ *   workspace: see fdec_select_pages_workspace; 256-byte aligned, not shared by calls
+ *      that may overlap.
+ * A candidate's page id outside the bounds sets FDEC_DEVERR_PAGE_ID in device_errors
+ * (optional) and is taken last.
+ */
+fdec_status fdec_select_pages(const void* q, int64_t q_stride_tok, int64_t q_stride_head, fdec_kv_desc bounds,
+                              const int32_t* page_table, int64_t page_table_stride, const int32_t* seq_lens_dev,
+                              int batch, int q_len, int page_size, int num_qo_heads, int num_kv_heads, int head_dim,
+                              fdec_dtype dtype, int causal, int64_t max_pages, int budget, int first_pages,
+                              int last_pages, int32_t* page_ids, int32_t* counts, int32_t* page_indices,
+                              void* workspace, size_t workspace_bytes, uint32_t* device_errors, cudaStream_t stream);
+
+/*
+ * Attention over selected pages: fdec_run_scaled with a page list and a length for each
+ * query token and KV head (of fdec_select_pages, or of the caller's own choice).
+ *   plan: q_len 1, batch = the number of query tokens, capacities = the most tokens a
+ *      list holds (budget * page_size); 16-bit or E4M3 cache.
+ *   page_ids: int32 device [batch][num_kv_heads][page_ids_stride]; counts: int32 device
+ *      [batch][num_kv_heads], the tokens in the list: every page is full but the last.
+ *   out: [batch][num_qo_heads][head_dim] contiguous, 16-byte aligned; out_type
+ *      FDEC_OUT_F32, or FDEC_OUT_SAME (the query's type: one rounding of the fp32 result).
+ * Everything else, an empty list and the device errors (in the workspace) among it, is
+ * as for fdec_run_scaled.
+ */
+fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                              fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_ids, int64_t page_ids_stride,
+                              const int32_t* counts, float scale, float k_scale, float v_scale, void* out,
+                              int out_type, float* lse, void* workspace, cudaStream_t stream);
 
 /* Release a plan (NULL is a no-op). */
 fdec_status fdec_plan_destroy(fdec_plan_t plan);

@@ -23,6 +23,8 @@ __all__ = [
     "fdec_run_static_workspace", "fdec_append", "kv_desc", "library_path", "PagedDecode", "EXPORTED_SYMBOLS",
     "FDEC_F16", "FDEC_BF16", "FDEC_PATH_AUTO", "FDEC_PATH_SIMT", "FDEC_PATH_MMA", "FDEC_PATH_TC",
     "FDEC_KV_SAME", "FDEC_KV_E4M3", "FDEC_KV_Q8_0", "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
+    "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
+    "fdec_run_selected", "FDEC_OUT_F32", "FDEC_OUT_SAME", "Rows", "PageSelect", "SparseDecode",
     "DEVERR_PAGE_ID", "DEVERR_SEQ_LEN", "DEVERR_TIMEOUT",
 ]
 
@@ -32,6 +34,7 @@ _LIB_PATH = os.path.join(_HERE, "libfdec.so")
 FDEC_F16, FDEC_BF16 = 0, 1
 FDEC_PATH_AUTO, FDEC_PATH_SIMT, FDEC_PATH_MMA, FDEC_PATH_TC = 0, 1, 2, 3
 FDEC_KV_SAME, FDEC_KV_E4M3, FDEC_KV_Q8_0 = 0, 1, 2
+FDEC_OUT_F32, FDEC_OUT_SAME = 0, 1
 DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 
 STATUS_NAMES = {
@@ -46,6 +49,8 @@ EXPORTED_SYMBOLS = (
     "fdec_plan_get_info", "fdec_plan_get_splits", "fdec_plan_set_split_event",
     "fdec_read_device_errors", "fdec_last_error", "fdec_version", "fdec_run_static_workspace", "fdec_append",
     "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
+    "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
+    "fdec_run_selected",
 )
 
 
@@ -60,6 +65,12 @@ class KVDesc(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64),
                 ("stride_token", ctypes.c_int64)]
+
+
+class Rows(ctypes.Structure):
+    """fdec_rows: 16-bit rows of tokens, element (token, head, dim) at base + token*stride_tok + head*stride_head + dim."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("stride_tok", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
 
 
 class PlanOpts(ctypes.Structure):
@@ -122,6 +133,19 @@ def _load():
         lib.fdec_append.argtypes = [P, P, I64, I64, P, P, I, I, I, I, KVDesc, KVDesc, P, I, I64, P, P]
         lib.fdec_append_e4m3.restype = I
         lib.fdec_append_e4m3.argtypes = [P, P, I64, I64, P, P, I, I, I, I, KVDesc, KVDesc, P, I, I64, P, P]
+        F, IP = ctypes.c_float, ctypes.POINTER(S)
+        lib.fdec_norm_rope_append.restype = I
+        lib.fdec_norm_rope_append.argtypes = [Rows, Rows, Rows, P, P, F, P, I64, I, I, P, P, P, I, I, I, I, I, I, I, F, F,
+                                              Rows, KVDesc, KVDesc, P, I, I64, P, P]
+        lib.fdec_page_bounds.restype = I
+        lib.fdec_page_bounds.argtypes = [KVDesc, KVDesc, P, I, I64, P, P, I, I, I, I, I, I, P, P]
+        lib.fdec_select_pages_workspace.restype = I
+        lib.fdec_select_pages_workspace.argtypes = [I, I, I, I64, IP, IP]
+        lib.fdec_select_pages.restype = I
+        lib.fdec_select_pages.argtypes = [P, I64, I64, KVDesc, P, I64, P, I, I, I, I, I, I, I, I, I64, I, I, I, P, P, P,
+                                          P, S, P, P]
+        lib.fdec_run_selected.restype = I
+        lib.fdec_run_selected.argtypes = [P, P, I64, I64, KVDesc, KVDesc, P, I64, P, F, F, F, P, I, P, P, P]
         lib.fdec_plan_destroy.restype = I
         lib.fdec_plan_destroy.argtypes = [P]
         lib.fdec_plan_get_info.restype = I
@@ -387,6 +411,219 @@ def fdec_merge_states(o, lse, o_out, lse_out=None, stream=None) -> None:
                                      _stream_handle(stream)))
 
 
+# ---------------------------------------------------------------------------
+# block-sparse decoding
+# ---------------------------------------------------------------------------
+
+def _dtype_of(t) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return FDEC_BF16
+    if t.dtype == torch.float16:
+        return FDEC_F16
+    raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+
+
+def _kv_type_of(t, dtype) -> int:
+    """FDEC_KV_SAME for pools of `dtype`, FDEC_KV_E4M3 for pools of 1-byte codes (float8_e4m3fn or uint8)."""
+    import torch
+
+    if t.dtype == dtype:
+        return FDEC_KV_SAME
+    if t.dtype in (torch.float8_e4m3fn, torch.uint8):
+        return FDEC_KV_E4M3
+    raise ValueError(f"expected a cache of {dtype} or of E4M3 codes, got {t.dtype}")
+
+
+def _rows(t, what: str) -> Rows:
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{what} must be [n, heads, head_dim] with a unit dim stride")
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _int32(t, what: str, dim: int):
+    import torch
+
+    if t.dtype != torch.int32 or t.dim() != dim or (t.numel() > 0 and t.stride(dim - 1) != 1):
+        raise ValueError(f"{what} must be an int32 tensor of {dim} dimension(s) with contiguous rows")
+    return t
+
+
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, batch_indices, positions, q_out, k, v, page_table,
+                          page_size: int, eps: float = 1e-6, interleaved: bool = False, rope_positions=None,
+                          k_scale: float = 1.0, v_scale: float = 1.0, device_errors=None, stream=None) -> None:
+    """RMS norm of the query and key heads of n new tokens, rotation by position, and the paged write of keys and
+    values.  q, q_out [n, Hq, D] and k_new, v_new [n, Hk, D] 16-bit (unit dim stride; slices of a fused QKV tensor
+    will do; q_out may be q); q_weight, k_weight [D] of the same type or None; cos_sin float32 [positions, rot_dim]
+    (rot_dim / 2 cosines, then the sines) or None; batch_indices, positions, rope_positions int32 [n]; k, v the cache
+    views [page, kv_head, slot, dim], 16-bit or E4M3 codes of k / k_scale and v / v_scale."""
+    n, hq, d = q.shape
+    if k_new.shape != v_new.shape or k_new.shape[0] != n or k_new.shape[2] != d or q_out.shape != q.shape:
+        raise ValueError("q, q_out must be [n, Hq, D] and k_new, v_new [n, Hk, D]")
+    hk = k_new.shape[1]
+    dt = _dtype_of(q)
+    for t in (k_new, v_new, q_out):
+        if t.dtype != q.dtype:
+            raise ValueError(f"rows of {q.dtype} and {t.dtype}")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != q.dtype or w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError("weights must be contiguous [head_dim] tensors of the rows' type")
+    import torch
+
+    rot, cos_rows = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
+        cos_rows, rot = cos_sin.shape
+    for t, what in ((batch_indices, "batch_indices"), (positions, "positions"), (rope_positions, "rope_positions")):
+        if t is not None and _int32(t, what, 1).shape[0] != n:
+            raise ValueError(f"{what} must have one entry per token")
+    _int32(page_table, "page_table", 2)
+    kv = _kv_type_of(k, q.dtype)
+    if v.dtype != k.dtype or k.shape[1:] != (hk, page_size, d) or v.shape[1:] != k.shape[1:]:
+        raise ValueError("k and v must be caches [page, Hk, page_size, D] of one type")
+    _same_device(q, k_new, v_new, q_weight, k_weight, cos_sin, batch_indices, positions, rope_positions, q_out, k, v,
+                 page_table, device_errors)
+    _check(_load().fdec_norm_rope_append(
+        _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new"), _ptr(q_weight), _ptr(k_weight), float(eps),
+        _ptr(cos_sin), cos_rows, rot, int(bool(interleaved)), batch_indices.data_ptr(), positions.data_ptr(),
+        _ptr(rope_positions), n, hq, hk, d, page_size, dt, kv, float(k_scale), float(v_scale), _rows(q_out, "q_out"),
+        kv_desc(k), kv_desc(v), page_table.data_ptr(), page_table.shape[0], page_table.stride(0), _ptr(device_errors),
+        _stream_handle(stream)))
+
+
+def fdec_page_bounds(k, bounds, page_table, begins, seq_lens, page_size: int, expected_tokens: int = 0,
+                     device_errors=None, stream=None) -> None:
+    """Write the elementwise minimum and maximum of the keys of every page that holds a position in
+    [begins[b], seq_lens[b]) (begins None: every page) into bounds [page, kv_head, 2, dim] (16-bit; for a cache of
+    E4M3 codes either 16-bit type).  expected_tokens sizes the launch (0: a whole page-table row)."""
+    dt = _dtype_of(bounds)
+    kv = _kv_type_of(k, bounds.dtype)
+    hk, d = k.shape[1], k.shape[3]
+    if k.shape[2] != page_size or bounds.dim() != 4 or bounds.shape[1:] != (hk, 2, d):
+        raise ValueError("need k [page, Hk, page_size, D] and bounds [page, Hk, 2, D]")
+    _int32(page_table, "page_table", 2)
+    batch = page_table.shape[0]
+    for t, what in ((begins, "begins"), (seq_lens, "seq_lens")):
+        if t is not None and _int32(t, what, 1).shape[0] != batch:
+            raise ValueError(f"{what} must have one entry per sequence")
+    _same_device(k, bounds, page_table, begins, seq_lens, device_errors)
+    expected = expected_tokens if expected_tokens > 0 else min(page_table.shape[1] * page_size, 2**31 - 1)
+    _check(_load().fdec_page_bounds(kv_desc(k), kv_desc(bounds), page_table.data_ptr(), batch, page_table.stride(0),
+                                    _ptr(begins), seq_lens.data_ptr(), hk, d, page_size, dt, kv, expected,
+                                    _ptr(device_errors), _stream_handle(stream)))
+
+
+def fdec_select_pages_workspace(batch: int, q_len: int, num_kv_heads: int, max_pages: int):
+    """(bytes of the workspace, bytes at its start that must be zero before the first call)."""
+    total, zero = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_load().fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages, ctypes.byref(total),
+                                               ctypes.byref(zero)))
+    return total.value, zero.value
+
+
+def fdec_select_pages(q, bounds, page_table, seq_lens, page_size: int, max_pages: int, budget: int, page_ids, counts,
+                      page_indices, workspace, first_pages: int = 1, last_pages: int = 1, causal: bool = True,
+                      device_errors=None, stream=None) -> None:
+    """q [B, Q, Hq, D]; bounds [page, Hk, 2, D] of the same type; page_table int32 [B, W]; seq_lens int32 [B];
+    page_ids, page_indices (or None) int32 [B * Q, Hk, budget] and counts int32 [B * Q, Hk] contiguous."""
+    b, q_len, hq, d = q.shape
+    if bounds.dtype != q.dtype or bounds.dim() != 4 or bounds.shape[2:] != (2, d):
+        raise ValueError("bounds must be [page, Hk, 2, D] of q's type")
+    hk = bounds.shape[1]
+    _int32(page_table, "page_table", 2)
+    if page_table.shape[0] != b or _int32(seq_lens, "seq_lens", 1).shape[0] != b or page_table.shape[1] < max_pages:
+        raise ValueError("page_table must be [B, >= max_pages] and seq_lens [B]")
+    for t, shape in ((page_ids, (b * q_len, hk, budget)), (counts, (b * q_len, hk)),
+                     (page_indices, (b * q_len, hk, budget))):
+        if t is not None and (tuple(_int32(t, "output", len(shape)).shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"outputs must be contiguous int32 of shape {shape}")
+    _same_device(q, bounds, page_table, seq_lens, page_ids, counts, page_indices, workspace, device_errors)
+    tok, head = _q_strides(q)
+    _check(_load().fdec_select_pages(
+        q.data_ptr(), tok, head, kv_desc(bounds), page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), b,
+        q_len, page_size, hq, hk, d, _dtype_of(q), int(bool(causal)), max_pages, budget, first_pages, last_pages,
+        page_ids.data_ptr(), counts.data_ptr(), _ptr(page_indices), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _ptr(device_errors), _stream_handle(stream)))
+
+
+def fdec_run_selected(plan: Plan, q, k, v, page_ids, counts, out, lse, workspace, scale: Optional[float] = None,
+                      k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Attention of q [N, 1, Hq, D] over page lists page_ids int32 [N, Hk, W] holding counts int32 [N, Hk] tokens;
+    out [N, 1, Hq, D] float32 or of q's type, lse float32 [N, 1, Hq] or None.  The plan: batch N, q_len 1."""
+    import torch
+
+    n, hk = plan.batch, plan.meta["num_kv_heads"]
+    kd = k if isinstance(k, KVDesc) else kv_desc(k)
+    vd = v if isinstance(v, KVDesc) else kv_desc(v)
+    if not out.is_contiguous() or (lse is not None and not lse.is_contiguous()):
+        raise ValueError("out and lse must be contiguous")
+    if out.dtype not in (torch.float32, q.dtype):
+        raise ValueError(f"out must be float32 or {q.dtype}, got {out.dtype}")
+    want = {"bf16": torch.bfloat16, "f16": torch.float16}[plan.meta["dtype"]]
+    if q.dtype != want or q.shape[0] * q.shape[1] != n:
+        raise ValueError(f"this plan takes {n} query tokens of {want}")
+    if tuple(_int32(page_ids, "page_ids", 3).shape[:2]) != (n, hk) or not page_ids.is_contiguous():
+        raise ValueError("page_ids must be a contiguous int32 [N, Hk, W] tensor")
+    if tuple(_int32(counts, "counts", 2).shape) != (n, hk) or not counts.is_contiguous():
+        raise ValueError("counts must be a contiguous int32 [N, Hk] tensor")
+    tok, head = _q_strides(q)
+    sc = 1.0 / math.sqrt(plan.meta["head_dim"]) if scale is None else float(scale)
+    _check_kv_type(plan, k, v)
+    _check(_load().fdec_run_selected(
+        plan.handle, q.data_ptr(), tok, head, kd, vd, page_ids.data_ptr(), page_ids.shape[2], counts.data_ptr(), sc,
+        float(k_scale), float(v_scale), out.data_ptr(), FDEC_OUT_F32 if out.dtype == torch.float32 else FDEC_OUT_SAME,
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), _stream_handle(stream)))
+
+
+class PageSelect:
+    """Convenience holder of fdec_select_pages: its workspace and outputs, allocated once."""
+
+    def __init__(self, batch, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, max_pages, budget, dtype="bf16",
+                 first_pages=1, last_pages=1, causal=True, device=None):
+        import torch
+
+        self.batch, self.q_len, self.page_size, self.max_pages, self.budget = batch, q_len, page_size, max_pages, budget
+        self.num_qo_heads, self.num_kv_heads, self.head_dim, self.dtype = num_qo_heads, num_kv_heads, head_dim, dtype
+        self.first_pages, self.last_pages, self.causal = first_pages, last_pages, causal
+        total, zero = fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages)
+        device = device or "cuda"
+        self.workspace = torch.empty(total, dtype=torch.uint8, device=device)
+        self.workspace[:zero].zero_()
+        rows = batch * q_len
+        self.page_ids = torch.empty((rows, num_kv_heads, budget), dtype=torch.int32, device=device)
+        self.page_indices = torch.empty_like(self.page_ids)
+        self.counts = torch.empty((rows, num_kv_heads), dtype=torch.int32, device=device)
+        self.errors = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def run(self, q, bounds, page_table, seq_lens, stream=None):
+        """Select; returns (page_ids, counts, page_indices), the holder's own tensors."""
+        if tuple(q.shape) != (self.batch, self.q_len, self.num_qo_heads, self.head_dim):
+            raise ValueError(f"q must be [{self.batch}, {self.q_len}, {self.num_qo_heads}, {self.head_dim}]")
+        fdec_select_pages(q, bounds, page_table, seq_lens, self.page_size, self.max_pages, self.budget, self.page_ids,
+                          self.counts, self.page_indices, self.workspace, self.first_pages, self.last_pages, self.causal,
+                          self.errors, stream)
+        return self.page_ids, self.counts, self.page_indices
+
+    def device_errors(self, clear=True) -> int:
+        """The FDEC_DEVERR_* bits of the calls so far (synchronises)."""
+        flags = int(self.errors.item())
+        if clear:
+            self.errors.zero_()
+        return flags
+
+
 class PagedDecode:
     """Convenience holder: a plan, its torch-allocated workspace, uploaded once."""
 
@@ -413,9 +650,57 @@ class PagedDecode:
             fdec_run_scaled(self.plan, q, k, v, page_table, seq_lens, out, lse, self.workspace, scale,
                             1.0 if k_scale is None else k_scale, 1.0 if v_scale is None else v_scale, stream)
 
+    def run_selected(self, q, k, v, page_ids, counts, out, lse=None, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
+        """fdec_run_selected with this plan (q_len 1, one sequence per query token)."""
+        fdec_run_selected(self.plan, q, k, v, page_ids, counts, out, lse, self.workspace, scale, k_scale, v_scale,
+                          stream)
+
     def device_errors(self, clear=True, stream=None) -> int:
         return fdec_read_device_errors(self.plan, self.workspace, clear, stream)
 
     @property
     def info(self) -> dict:
         return fdec_plan_get_info(self.plan)
+
+
+class SparseDecode:
+    """One layer's block-sparse decoding step over a paged cache, its plan and workspaces allocated once:
+    norm, rotation and append of the new tokens, bounds of the pages they lie in, page selection, attention.
+
+    max_lens: the longest each sequence gets.  Every call takes q_len new tokens of each sequence, seq_lens counting
+    them, in the order of the sequences."""
+
+    def __init__(self, max_lens, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, budget, dtype="bf16",
+                 first_pages=1, last_pages=2, kv_dtype="", device=None):
+        import torch
+
+        batch = len(max_lens)
+        if q_len < 1:
+            raise ValueError("q_len must be >= 1")
+        max_pages = max(1, max(-(-int(n) // page_size) for n in max_lens))
+        self.q_len, self.page_size = q_len, page_size
+        self.select = PageSelect(batch, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, max_pages, budget, dtype,
+                                 first_pages, last_pages, device=device)
+        self.attend = PagedDecode([budget * page_size] * (batch * q_len), 1, page_size, num_qo_heads, num_kv_heads,
+                                  head_dim, dtype, device=device, kv_dtype=kv_dtype)
+        device = self.select.counts.device
+        self.batch_indices = torch.arange(batch, dtype=torch.int32, device=device).repeat_interleave(q_len)
+        self.offsets = torch.arange(-q_len, 0, dtype=torch.int32, device=device)
+
+    def step(self, q, k_new, v_new, q_weight, k_weight, cos_sin, k, v, bounds, page_table, seq_lens, out, lse=None,
+             eps=1e-6, interleaved=False, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
+        """q [B * Q, Hq, D] (normed and rotated in place), k_new, v_new [B * Q, Hk, D], out [B * Q, 1, Hq, D].  With a
+        stream of its own, seq_lens and the rest must be ready on it, and the caller's current stream be that stream."""
+        n, hq, d = q.shape
+        begins = seq_lens - self.q_len
+        positions = (seq_lens[:, None] + self.offsets).reshape(-1)
+        fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, self.batch_indices, positions, q, k, v,
+                              page_table, self.page_size, eps, interleaved, None, k_scale, v_scale, self.select.errors,
+                              stream)
+        fdec_page_bounds(k, bounds, page_table, begins, seq_lens, self.page_size, self.q_len, self.select.errors, stream)
+        ids, counts, _ = self.select.run(q.view(n // self.q_len, self.q_len, hq, d), bounds, page_table, seq_lens, stream)
+        self.attend.run_selected(q.view(n, 1, hq, d), k, v, ids, counts, out, lse, scale, k_scale, v_scale, stream)
+        return out
+
+    def device_errors(self, clear=True, stream=None) -> int:
+        return self.select.device_errors(clear) | self.attend.device_errors(clear, stream)

@@ -166,6 +166,40 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     }
 }
 
+// Two floats rounded to nearest even and packed (low, high) into a 32-bit word.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+// Store output elements idx .. idx + 3 (or idx alone) of an array of `out_type` (OutType).
+// A 16-bit output is one rounding, at the end, of the fp32 result: what the next product
+// of a 16-bit model would round to anyway, at half the bytes.
+__device__ __forceinline__ void store_out4(float* out, int out_type, int64_t idx, float4 v) {
+    if (out_type == 0) {
+        *reinterpret_cast<float4*>(out + idx) = v;
+    } else {
+        const uint2 w = out_type == 1 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                                      : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + idx) = w;
+    }
+}
+
+__device__ __forceinline__ void store_out1(float* out, int out_type, int64_t idx, float v) {
+    if (out_type == 0)
+        out[idx] = v;
+    else if (out_type == 1)
+        reinterpret_cast<__nv_bfloat16*>(out)[idx] = __float2bfloat16_rn(v);
+    else
+        reinterpret_cast<__half*>(out)[idx] = __float2half_rn(v);
+}
+
 template <bool BF16>
 __device__ __forceinline__ float load_16bit(const uint16_t* p) {
     const uint16_t v = *p;

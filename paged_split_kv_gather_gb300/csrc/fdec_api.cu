@@ -7,6 +7,7 @@
 // splits of whole 64-token blocks, the split count follows the machine (SM
 // count) and the batch, and the reduction takes as many passes as needed.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -77,6 +78,41 @@ size_t smem_for_rc(int rc) {
 }  // namespace
 
 namespace fdec {
+
+int record_failure(int status, const char* message) noexcept {
+    try {
+        g_last_error = message;
+    } catch (...) {
+        g_last_error.clear();
+    }
+    return status;
+}
+
+int record_cuda_failure(cudaError_t e, const char* what) noexcept {
+    try {
+        g_last_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+    } catch (...) {
+        g_last_error.clear();
+    }
+    return FDEC_ERR_CUDA;
+}
+
+void clear_failure() noexcept { g_last_error.clear(); }
+
+cudaError_t current_num_sms(int* num_sms) {
+    static std::atomic<int> sms[64];  // 0 = not yet queried
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev >= 0 && dev < 64 ? sms[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) sms[dev].store(n, std::memory_order_relaxed);
+    }
+    *num_sms = n;
+    return cudaSuccess;
+}
 
 size_t split_smem_bytes(int d, int rc) {
     switch (d) {
@@ -658,7 +694,8 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
                             const fdec_kv_desc& k, const fdec_kv_desc& v, const fdec_kv_desc* ks,
                             const fdec_kv_desc* vs, const int32_t* page_table, int64_t page_table_stride,
                             const int32_t* seq_lens_dev, float scale, float k_scale, float v_scale, float* out,
-                            float* lse, void* workspace, cudaStream_t stream) {
+                            float* lse, void* workspace, cudaStream_t stream, bool per_head = false,
+                            int out_type = kOutF32) {
     if (q == nullptr || k.base == nullptr || v.base == nullptr || page_table == nullptr || seq_lens_dev == nullptr ||
         out == nullptr)
         return fail(FDEC_ERR_INVALID_ARG, "null q, K, V, page_table, seq_lens or out");
@@ -735,6 +772,8 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
     sp.page_table = page_table;
     sp.pt_stride = page_table_stride;
     sp.seq_lens = seq_lens_dev;
+    sp.tab_heads = per_head ? p->hk : 1;
+    sp.out_type = out_type;
     sp.capacity = reinterpret_cast<const int32_t*>(ws + p->off_cap);
     sp.items = reinterpret_cast<const WorkItem*>(ws + p->off_items);
     sp.part_o = reinterpret_cast<float*>(ws + p->off_a_o);
@@ -780,6 +819,7 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
         rp.dst_ml = reinterpret_cast<float2*>(ws + (from_a ? p->off_b_ml : p->off_a_ml));
         rp.out = out;
         rp.lse = lse;
+        rp.out_type = out_type;
         rp.hk = p->hk;
         rp.rows = p->rows;
         rp.group = p->group;
@@ -829,6 +869,23 @@ fdec_status fdec_run_q8_0(fdec_plan_t p, const void* q, int64_t q_stride_tok, in
     }
     return run_impl(p, q, q_stride_tok, q_stride_head, k, v, &k_scales, &v_scales, page_table, page_table_stride,
                     seq_lens_dev, scale, 1.f, 1.f, out, lse, workspace, stream);
+}
+
+fdec_status fdec_run_selected(fdec_plan_t p, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                              fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_ids, int64_t page_ids_stride,
+                              const int32_t* counts, float scale, float k_scale, float v_scale, void* out,
+                              int out_type, float* lse, void* workspace, cudaStream_t stream) {
+    g_last_error.clear();
+    if (p == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null plan");
+    if (p->q_len != 1)
+        return fail(FDEC_ERR_INVALID_ARG, "fdec_run_selected needs a plan with q_len 1 (one sequence per query token)");
+    if (p->q8) return fail(FDEC_ERR_UNSUPPORTED, "fdec_run_selected reads 16-bit and E4M3 caches, not q8_0");
+    if (out_type != FDEC_OUT_F32 && out_type != FDEC_OUT_SAME)
+        return fail(FDEC_ERR_INVALID_ARG, "out_type must be FDEC_OUT_F32 or FDEC_OUT_SAME");
+    if (reinterpret_cast<uintptr_t>(out) % 16 != 0) return fail(FDEC_ERR_LAYOUT, "out must be 16-byte aligned");
+    const int type = out_type == FDEC_OUT_F32 ? kOutF32 : (p->dtype == FDEC_BF16 ? kOutBF16 : kOutF16);
+    return run_impl(p, q, q_stride_tok, q_stride_head, k, v, nullptr, nullptr, page_ids, page_ids_stride, counts, scale,
+                    k_scale, v_scale, static_cast<float*>(out), lse, workspace, stream, true, type);
 }
 
 }  // extern "C"
@@ -938,6 +995,7 @@ fdec_status fdec_merge_states(const float* o, const float* lse, int n_states, in
     rp.dst_ml = nullptr;
     rp.out = o_out;
     rp.lse = lse_out;
+    rp.out_type = kOutF32;
     rp.hk = 1;
     rp.rows = rows;
     rp.group = rows;

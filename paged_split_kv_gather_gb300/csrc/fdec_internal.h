@@ -16,6 +16,9 @@ constexpr int kBlockTokens = 64;
 // One pipeline stage carries 32 consecutive tokens of K and V (one per lane).
 constexpr int kStageTokens = 32;
 
+// Type of the output rows: fp32 (fdec_run and its kin), or the query's 16-bit type.
+enum OutType : int { kOutF32 = 0, kOutBF16 = 1, kOutF16 = 2 };
+
 // Work item of the split kernel: sequence, [block_begin, block_end) in 64-token
 // blocks, and the partial slot (-1: the item covers its whole sequence and
 // writes out/lse directly).
@@ -51,6 +54,10 @@ struct SplitParams {
     const int32_t* page_table;
     int64_t pt_stride;
     const int32_t* seq_lens;
+    // 1: one page-table row and length per sequence; hk: one per (sequence, KV head), row
+    // seq * hk + kvh (the pages each head has selected).  table_row() gives the row.
+    int tab_heads;
+    int out_type;              // OutType of `out`
     const int32_t* capacity;   // planned capacity per sequence (workspace copy)
     const WorkItem* items;
     float* part_o;             // [slot][Hk][rows][D]
@@ -80,6 +87,7 @@ struct ReduceParams {
     float2* dst_ml;
     float* out;                // final: [B*Q*Hq][D]
     float* lse;                // final: [B*Q*Hq] or null
+    int out_type;              // OutType of `out`
     int hk, rows, group, q_len, hq, head_dim;
     int normalized_input;      // 1: sources are normalised (o, lse) states (merge_states)
     int src_rows_stride;       // rows per (slot, kv head) in the source arrays
@@ -168,6 +176,83 @@ struct AppendParams {
     int n_tokens, batch, hk, row_bytes, page_shift;
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+
+// Norm, rotation and paged write of new tokens' rows (fdec_norm_rope_append).  Strides
+// in bytes; rows start on 16-byte boundaries.
+struct NormRopeParams {
+    const uint8_t* q;
+    int64_t q_st, q_sh;
+    const uint8_t* k_new;
+    int64_t k_new_st, k_new_sh;
+    const uint8_t* v_new;
+    int64_t v_new_st, v_new_sh;
+    const uint16_t* q_weight;  // [head_dim] or null (ones)
+    const uint16_t* k_weight;
+    const float* cos_sin;      // [cos_rows][rot]: rot / 2 cosines, then rot / 2 sines
+    int64_t cos_rows;
+    const int32_t* batch_indices;
+    const int32_t* positions;
+    const int32_t* rope_positions;  // null: positions
+    uint8_t* q_out;
+    int64_t q_out_st, q_out_sh;
+    const int32_t* page_table;
+    int64_t pt_stride;
+    uint8_t* k_base;
+    int64_t k_pages, k_sp, k_sh, k_st;
+    uint8_t* v_base;
+    int64_t v_pages, v_sp, v_sh, v_st;
+    unsigned* err;
+    int n_tokens, batch, hq, hk, page_shift, rot;
+    float eps, k_scale, v_scale;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, bool bf16, bool kv8, bool pairs, int num_sms,
+                             cudaStream_t s);
+
+// Minimum and maximum of each page's keys (fdec_page_bounds).  Strides in bytes.
+struct BoundsParams {
+    const uint8_t* k_base;
+    int64_t k_pages, k_sp, k_sh, k_st;
+    uint8_t* b_base;           // b_st: bytes from a page's minimum row to its maximum row
+    int64_t b_pages, b_sp, b_sh, b_st;
+    const int32_t* page_table;
+    int64_t pt_stride;
+    const int32_t* begins;     // null: 0
+    const int32_t* seq_lens;
+    unsigned* err;
+    int batch, hk, page_shift, span;
+};
+cudaError_t launch_page_bounds(const BoundsParams& p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s);
+
+// Page selection (fdec_select_pages).  q strides in elements, bounds strides in bytes.
+struct SelectParams {
+    const uint16_t* q;
+    int64_t q_st, q_sh;
+    const uint8_t* b_base;
+    int64_t b_pages, b_sp, b_sh, b_st;
+    const int32_t* page_table;
+    int64_t pt_stride;
+    const int32_t* seq_lens;
+    int32_t* page_ids;         // [rows][budget], rows = batch x q_len x hk
+    int32_t* counts;           // [rows]
+    int32_t* page_indices;     // [rows][budget] or null
+    unsigned* row_count;       // [rows] finished CTAs, and
+    unsigned* row_abs;         // [rows] largest sum of magnitudes: zero between calls
+    float* scores;             // [rows][max_pages]
+    unsigned long long* near_keys;  // [rows][max_pages]
+    unsigned* err;
+    int batch, q_len, hk, group, page_shift, causal;
+    int max_pages, budget, first, last;
+    int chunk, n_chunks;       // set by the launcher
+};
+cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num_sms, cudaStream_t s);
+
+// Shared by the entry points' translation units (defined in fdec_api.cu): record the
+// message of a failed call (never throws) and return its status.
+int record_failure(int status, const char* message) noexcept;
+int record_cuda_failure(cudaError_t e, const char* what) noexcept;
+void clear_failure() noexcept;
+// SM count of the current device, queried once per device.
+cudaError_t current_num_sms(int* num_sms);
 // One task given by value (p.tasks must be null): used by fdec_merge_states.
 cudaError_t launch_reduce_single(const ReduceParams& p, ReduceTask task, cudaStream_t s);
 

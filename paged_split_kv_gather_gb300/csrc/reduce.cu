@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32, 5) reduce_kernel(const Redu
                 const int qi = row / p.group;
                 const int h = kvh * p.group + (row - qi * p.group);
                 const int64_t orow = static_cast<int64_t>(task.seq * p.q_len + qi) * p.hq + h;
-                p.out[orow * D + d] = Lsum > 0.f ? o / Lsum : 0.f;
+                store_out1(p.out, p.out_type, orow * D + d, Lsum > 0.f ? o / Lsum : 0.f);
                 if (d == 0 && p.lse != nullptr) p.lse[orow] = Lsum > 0.f ? (M + log2f(Lsum)) * kLn2 : -INFINITY;
             } else {
                 const int64_t drow = (static_cast<int64_t>(task.dst) * p.hk + kvh) * p.rows + row;

@@ -63,9 +63,14 @@ struct ItemRange {
     bool bad;
 };
 
+// Page-table and length row of a sequence for one KV head (see SplitParams::tab_heads).
+__device__ __forceinline__ int64_t table_row(const SplitParams& p, int seq, int kvh) {
+    return p.tab_heads > 1 ? static_cast<int64_t>(seq) * p.tab_heads + kvh : seq;
+}
+
 template <int TOK = kStageTokens>
-__device__ __forceinline__ ItemRange item_range(const SplitParams& p, const WorkItem& it) {
-    const int L0 = p.seq_lens[it.seq];
+__device__ __forceinline__ ItemRange item_range(const SplitParams& p, const WorkItem& it, int kvh) {
+    const int L0 = p.seq_lens[table_row(p, it.seq, kvh)];
     const int cap = p.capacity[it.seq];
     ItemRange r;
     r.bad = L0 > cap || L0 < 0;
@@ -179,7 +184,7 @@ __device__ __forceinline__ void produce_stages(const SplitParams& p, const CUten
     static_assert(G::ROW_BYTES % 128 == 0, "rows of whole 128-byte regions");
     const int lane = threadIdx.x & 31;
     const int tok_begin = ir.tok_begin;
-    const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.pt_stride;
+    const int32_t* pt = p.page_table + table_row(p, b, kvh) * p.pt_stride;
     const int page_mask = (1 << p.page_shift) - 1;
     int issued = 0;
     bool ok = true;
@@ -368,7 +373,7 @@ __device__ __forceinline__ void merge_and_store(const SplitParams& p, const Work
             const int qi = row / p.group;
             const int h = kvh * p.group + (row - qi * p.group);
             const int64_t orow = static_cast<int64_t>(it.seq * p.q_len + qi) * p.hq + h;
-            p.out[orow * D + d] = Ls > 0.f ? O / Ls * p.v_scale : 0.f;
+            store_out1(p.out, p.out_type, orow * D + d, Ls > 0.f ? O / Ls * p.v_scale : 0.f);
             if (d == 0 && p.lse != nullptr) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
         } else {
             const int64_t prow = (static_cast<int64_t>(it.slot) * p.hk + kvh) * p.rows + row;

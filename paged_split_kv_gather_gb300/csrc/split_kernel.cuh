@@ -126,7 +126,7 @@ split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUte
     // Launched as a programmatic dependent of the kernel before it in the stream: read
     // and write nothing but plan data before that kernel has completed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const ItemRange ir = item_range(p, it);
+    const ItemRange ir = item_range(p, it, kvh);
 
     if (warp == NW) {
         // The producer starts at once: its page-table reads overlap the length and q loads.

@@ -139,10 +139,17 @@ __device__ __forceinline__ void punit_load_item(const SplitParams& p, PUnit& u, 
     }
 }
 
+// Page-table and length row of the unit (see table_row).
+__device__ __forceinline__ int64_t punit_row(const SplitParams& p, const PUnit& u) {
+    if (p.tab_heads == 1) return u.it.x;
+    const int rgc = (p.rows + 15) / 16;
+    return table_row(p, u.it.x, u.unit % (p.hk * rgc) / rgc);
+}
+
 // Page id of TMA box n (BR token rows) of the unit, or -1 past its planned blocks.
 __device__ __forceinline__ int punit_box_page(const SplitParams& p, const PUnit& u, int n, int BR) {
     const int t = u.it.y * kBlockTokens + n * BR;
-    const int32_t* pt = p.page_table + static_cast<int64_t>(u.it.x) * p.pt_stride;
+    const int32_t* pt = p.page_table + punit_row(p, u) * p.pt_stride;
     return (t < u.it.z * kBlockTokens && (t >> p.page_shift) < p.pt_stride) ? __ldg(pt + (t >> p.page_shift)) : -1;
 }
 
@@ -150,7 +157,7 @@ __device__ __forceinline__ int punit_box_page(const SplitParams& p, const PUnit&
 // planned blocks and the table row, so every read is in bounds).
 __device__ __forceinline__ void punit_load_lens_pages(const SplitParams& p, PUnit& u, int lane, int BR,
                                                       bool tma_mode) {
-    u.L0 = __ldg(p.seq_lens + u.it.x);
+    u.L0 = __ldg(p.seq_lens + punit_row(p, u));
     u.cap = p.seq1_bps > 0 ? p.seq1_capacity : __ldg(p.capacity + u.it.x);
     if (tma_mode) {
         u.pid0 = punit_box_page(p, u, lane, BR);
@@ -353,7 +360,7 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
                     }
                 }
                 constexpr int CHUNKS = G::ROW_BYTES / 16;
-                const int32_t* pt = p.page_table + static_cast<int64_t>(seq) * p.pt_stride;
+                const int32_t* pt = p.page_table + table_row(p, seq, kvh) * p.pt_stride;
                 const int t_lane = tok_begin + j * TOK + lane;
                 const bool in_range = t_lane < tok_end;
                 const int my_page = in_range ? __ldg(pt + (t_lane >> p.page_shift)) : -1;
@@ -488,10 +495,10 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
         const int h = u.kvh * p.group + (row - qi * p.group);
         if (u.slot < 0) {
             const int64_t orow = static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h;
-            *reinterpret_cast<float4*>(p.out + orow * D + 4 * c4) =
-                Lr > 0.f ? make_float4(O.x / Lr * p.v_scale, O.y / Lr * p.v_scale, O.z / Lr * p.v_scale,
-                                       O.w / Lr * p.v_scale)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+            store_out4(p.out, p.out_type, orow * D + 4 * c4,
+                       Lr > 0.f ? make_float4(O.x / Lr * p.v_scale, O.y / Lr * p.v_scale, O.z / Lr * p.v_scale,
+                                              O.w / Lr * p.v_scale)
+                                : make_float4(0.f, 0.f, 0.f, 0.f));
         } else {
             const int64_t prow = (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
             *reinterpret_cast<float4*>(p.part_o + prow * D + 4 * c4) =

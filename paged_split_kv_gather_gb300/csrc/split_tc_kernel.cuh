@@ -111,17 +111,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-
 template <int NT, int D, bool BF16>
 __global__ void __launch_bounds__(TcLayout<NT, D, BF16>::THREADS, 1)
 split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmk,
@@ -175,7 +164,7 @@ split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ C
     // Launched as a programmatic dependent of the kernel before it in the stream: read
     // and write nothing but plan data before that kernel has completed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    ItemRange ir = item_range<TOK>(p, it);
+    ItemRange ir = item_range<TOK>(p, it, kvh);
     if (p.causal) {  // no row of this CTA sees past L - Q + (its last q position)
         const int last_row = min(row0 + Lay::ROWS, p.rows) - 1;
         const int lim_max = ir.L - p.q_len + last_row / p.group;
@@ -663,19 +652,22 @@ split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ C
                 tmem_ld32(tmem_o + c0, a);
                 tmem_wait_ld();
                 if (row < p.rows) {
-                    float* dst = it.slot < 0 ? p.out + orow * D + c0 : p.part_o + prow * D + c0;
+                    float* dst = it.slot < 0 ? p.out : p.part_o;
+                    const int64_t at = (it.slot < 0 ? orow : prow) * D + c0;
+                    const int type = it.slot < 0 ? p.out_type : kOutF32;  // partials are fp32
                     const float f = (it.slot < 0 ? inv : 1.f) * p.v_scale;
 #pragma unroll
                     for (int c = 0; c < 32; c += 4)
-                        *reinterpret_cast<float4*>(dst + c) =
-                            make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
+                        store_out4(dst, type, at + c, make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f));
                 }
             }
         } else {
             // nothing visible (or a failed wait): an empty state
             if (row < p.rows) {
-                float* dst = it.slot < 0 ? p.out + orow * D : p.part_o + prow * D;
-                for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                float* dst = it.slot < 0 ? p.out : p.part_o;
+                const int64_t at = (it.slot < 0 ? orow : prow) * D;
+                const int type = it.slot < 0 ? p.out_type : kOutF32;
+                for (int c = 0; c < D; c += 4) store_out4(dst, type, at + c, make_float4(0.f, 0.f, 0.f, 0.f));
             }
             m = -INFINITY;
             l = 0.f;
