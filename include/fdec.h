@@ -314,7 +314,7 @@ fdec_status fdec_append_e4m3(const void* k_new, const void* v_new, int64_t new_s
  *   fdec_page_bounds        min and max of the keys of the pages that changed
  *   fdec_select_pages       for each query token and KV head, the pages to read
  *   fdec_run_selected       attention over them
- * Each is one kernel launch (fdec_run_selected: its plan's launches), allocates
+ * Each is one or two kernel launches (fdec_run_selected: its plan's), allocates
  * nothing, and may be captured in a CUDA graph.  Their kernels start as
  * programmatic dependents of the kernel before them on `stream` and touch nothing
  * before it has completed, so stream order holds as for ordinary launches.
@@ -377,12 +377,9 @@ fdec_status fdec_page_bounds(fdec_kv_desc k, fdec_kv_desc bounds, const int32_t*
                              int num_kv_heads, int head_dim, int page_size, fdec_dtype dtype, int kv_dtype,
                              int expected_tokens, uint32_t* device_errors, cudaStream_t stream);
 
-/*
- * Device bytes that fdec_select_pages needs for these sizes, and how many of them, at
- * the start, must be zero before the first call with it (every call leaves them zero).
- */
+/* Device bytes of workspace that fdec_select_pages needs for these sizes. */
 fdec_status fdec_select_pages_workspace(int batch, int q_len, int num_kv_heads, int64_t max_pages,
-                                        size_t* workspace_bytes, size_t* zero_bytes);
+                                        size_t* workspace_bytes);
 
 /*
  * Select pages.  For each query token n = (b, i) and KV head, of the pages that the

@@ -140,7 +140,7 @@ def _load():
         lib.fdec_page_bounds.restype = I
         lib.fdec_page_bounds.argtypes = [KVDesc, KVDesc, P, I, I64, P, P, I, I, I, I, I, I, P, P]
         lib.fdec_select_pages_workspace.restype = I
-        lib.fdec_select_pages_workspace.argtypes = [I, I, I, I64, IP, IP]
+        lib.fdec_select_pages_workspace.argtypes = [I, I, I, I64, IP]
         lib.fdec_select_pages.restype = I
         lib.fdec_select_pages.argtypes = [P, I64, I64, KVDesc, P, I64, P, I, I, I, I, I, I, I, I, I64, I, I, I, P, P, P,
                                           P, S, P, P]
@@ -525,12 +525,11 @@ def fdec_page_bounds(k, bounds, page_table, begins, seq_lens, page_size: int, ex
                                     _ptr(device_errors), _stream_handle(stream)))
 
 
-def fdec_select_pages_workspace(batch: int, q_len: int, num_kv_heads: int, max_pages: int):
-    """(bytes of the workspace, bytes at its start that must be zero before the first call)."""
-    total, zero = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(_load().fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages, ctypes.byref(total),
-                                               ctypes.byref(zero)))
-    return total.value, zero.value
+def fdec_select_pages_workspace(batch: int, q_len: int, num_kv_heads: int, max_pages: int) -> int:
+    """Bytes of the workspace that fdec_select_pages needs."""
+    total = ctypes.c_size_t()
+    _check(_load().fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages, ctypes.byref(total)))
+    return total.value
 
 
 def fdec_select_pages(q, bounds, page_table, seq_lens, page_size: int, max_pages: int, budget: int, page_ids, counts,
@@ -597,10 +596,9 @@ class PageSelect:
         self.batch, self.q_len, self.page_size, self.max_pages, self.budget = batch, q_len, page_size, max_pages, budget
         self.num_qo_heads, self.num_kv_heads, self.head_dim, self.dtype = num_qo_heads, num_kv_heads, head_dim, dtype
         self.first_pages, self.last_pages, self.causal = first_pages, last_pages, causal
-        total, zero = fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages)
         device = device or "cuda"
-        self.workspace = torch.empty(total, dtype=torch.uint8, device=device)
-        self.workspace[:zero].zero_()
+        self.workspace = torch.empty(fdec_select_pages_workspace(batch, q_len, num_kv_heads, max_pages),
+                                     dtype=torch.uint8, device=device)
         rows = batch * q_len
         self.page_ids = torch.empty((rows, num_kv_heads, budget), dtype=torch.int32, device=device)
         self.page_indices = torch.empty_like(self.page_ids)

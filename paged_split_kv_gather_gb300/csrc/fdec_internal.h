@@ -235,15 +235,17 @@ struct SelectParams {
     int32_t* page_ids;         // [rows][budget], rows = batch x q_len x hk
     int32_t* counts;           // [rows]
     int32_t* page_indices;     // [rows][budget] or null
-    unsigned* row_count;       // [rows] finished CTAs, and
-    unsigned* row_abs;         // [rows] largest sum of magnitudes: zero between calls
-    float* scores;             // [rows][max_pages]
+    float* chunk_abs;          // [rows][abs_stride] each scoring CTA's largest sum of magnitudes
+    int64_t abs_stride;
+    float* scores;             // [rows][score_stride], 16-byte aligned
+    int64_t score_stride;      // max_pages rounded up to a multiple of 4
     unsigned long long* near_keys;  // [rows][max_pages]
     unsigned* err;
     int batch, q_len, hk, group, page_shift, causal;
     int max_pages, budget, first, last;
-    int chunk, n_chunks;       // set by the launcher
+    int head_dim, chunk, n_chunks, chain;  // set by the launcher
 };
+int64_t select_abs_stride(int64_t max_pages);
 cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num_sms, cudaStream_t s);
 
 // Shared by the entry points' translation units (defined in fdec_api.cu): record the

@@ -18,9 +18,14 @@
 // more pages lie between than are still wanted, those few are summed again in 64 bits.
 // (64 bits throughout would be bound by the fp64 units: 1/60 of the fp32 rate.)
 //
-// One launch: a row (query token, KV head) is cut into chunks of pages, one CTA each;
-// the last CTA of a row to finish (a counter per row) selects.  Selection is a radix
-// select of 11 + 11 + 10 bits over the row's scores.
+// Two launches.  score_pages_kernel streams the bounds: a row (query token, KV head) is
+// cut into chunks of pages, one CTA each.  choose_pages_kernel, its programmatic
+// dependent, has one CTA a row: the row's scores go to shared memory, the bin of the
+// K-th largest among 256 over their range is found, and the few scores in that bin are
+// compared with each other.  (Choosing in the row's last CTA to finish scoring, counted
+// by an atomic, was measured first: the count's fences cost every CTA 1.4-2.1 us and the
+// choosing CTAs' registers and shared memory halved what streams beside them: 86 us
+// against the two launches' figure below on the batch of 64.)
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -33,10 +38,12 @@ namespace fdec {
 
 namespace {
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kNear = 256;  // pages near the border that are ranked in shared memory
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kBins = 256;
+constexpr int kNear = 256;  // keys that are compared each with each
+constexpr int kTile = 4096;  // scores that choosing holds in shared memory
+constexpr int kMinChunk = 32;  // pages a scoring CTA has at least
 
 template <int D>
 struct SelShape {
@@ -44,7 +51,10 @@ struct SelShape {
     static constexpr int LPP = D == 64 || D == 192 ? 16 : 32;  // lanes per page
     static constexpr int CPL = CHUNKS / LPP;
     static constexpr int PPW = 32 / LPP;                       // pages per load instruction
-    static constexpr int U = CPL >= 3 ? 2 : 8 / CPL;           // load groups in flight
+    static constexpr int U = CPL == 3 ? 4 : 8 / CPL;           // load groups in flight
+    // Two CTAs an SM: with three (80 registers a thread) the compiler keeps fewer of the
+    // loads in flight (head_dim 192, batch of 64: 94 against 76 us).
+    static constexpr int CTAS = 2;
 };
 
 // Loads that stay where they are written: scores of other CTAs, after their counter.
@@ -53,10 +63,39 @@ __device__ __forceinline__ float ld_cg(const float* p) {
     asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ int ld_cg(const int32_t* p) {
+    int v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_cg(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
+}
+template <bool BF16>
+__device__ __forceinline__ float to_float(uint16_t v) {
+    return unpack2<BF16>(v).x;
+}
+__device__ __forceinline__ float4 ld_cg4(const float* p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float v;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
     return v;
+}
+
+// Maxima of two pairs of 16-bit magnitudes: they order as integers, NaN above infinity.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ float not_nan(float s) { return s != s ? INFINITY : s; }
@@ -75,40 +114,91 @@ __device__ __forceinline__ unsigned long long ordered(double s) {
     return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-// Sum of a value over the CTA, to every thread.
-__device__ __forceinline__ int block_sum(int v, int* s_sum) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sums of two values over a CTA of NW warps, left in every thread's arguments.
+template <int NW>
+__device__ __forceinline__ void block_sum2(int& a, int& b, int* s_a, int* s_b) {
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) {
+        s_a[threadIdx.x >> 5] = a;
+        s_b[threadIdx.x >> 5] = b;
+    }
     __syncthreads();
-    int t = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) t += s_sum[w];
-    return t;
+    const int lane = threadIdx.x & 31;
+    a = __reduce_add_sync(0xffffffffu, lane < NW ? s_a[lane] : 0);
+    b = __reduce_add_sync(0xffffffffu, lane < NW ? s_b[lane] : 0);
 }
 
-struct SelShared {
-    union {
-        int hist[kBins];
-        double weight64[kBins / 2];
-    };
-    unsigned long long near_key[kNear];
-    int near_idx[kNear];
-    float err[kSelWarps];
-    int sum[kSelWarps];
-    int bin, above, near_n, last, cut_idx;
-    unsigned long long cut_key;
+// What both kernels derive from a row's length.
+struct SelRow {
+    int64_t seen;  // tokens that the query sees
+    int M;         // pages of them, <= max_pages
+    int n_cand;    // pages to choose among (0: all are taken, or none is free)
+    int need;      // pages to choose
+    bool all, bad;
 };
 
-// 64-bit score of one page, by one warp.
-template <int D, bool BF16>
+__device__ __forceinline__ SelRow sel_row(const SelectParams& p, int64_t L, int qi) {
+    SelRow r;
+    const int64_t room = static_cast<int64_t>(p.max_pages) << p.page_shift;
+    r.bad = L < 0 || L > room;
+    if (r.bad) L = L < 0 ? 0 : room;
+    r.seen = max(static_cast<int64_t>(0), p.causal ? L - p.q_len + qi + 1 : L);
+    r.M = static_cast<int>((r.seen + (1 << p.page_shift) - 1) >> p.page_shift);
+    r.all = r.M <= p.budget;
+    r.need = r.all ? 0 : p.budget - p.first - p.last;
+    r.n_cand = r.need == 0 ? 0 : r.M - p.first - p.last;  // > need
+    return r;
+}
+
+// Sum over the LPP lanes of a page of N pages' values at once: halves of the values are
+// exchanged for halves of the lanes (N - 1 + log2(LPP / N) shuffles instead of
+// N log2(LPP)).  s[0] of lane l is then the sum of value (l % LPP) * N / LPP.
+template <int N, int O>
+__device__ __forceinline__ void fold(float* s, int lane) {
+    if constexpr (O > 0) {
+        if constexpr (N > 1) {
+            const bool up = (lane & O) != 0;
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const float give = up ? s[k] : s[k + N / 2];
+                const float keep = up ? s[k + N / 2] : s[k];
+                s[k] = keep + __shfl_xor_sync(0xffffffffu, give, O);
+            }
+            fold<N / 2, O / 2>(s, lane);
+        } else {
+            s[0] += __shfl_xor_sync(0xffffffffu, s[0], O);
+            fold<1, O / 2>(s, lane);
+        }
+    }
+}
+
+// 64-bit score of one page, by one warp: 16-byte chunks of the two rows, all in flight.
+template <bool BF16>
 __device__ __forceinline__ double score64(const SelectParams& p, const double* w64, int64_t page, int h, int lane) {
+    constexpr int MAX = 4;  // chunks a lane at head_dim 512
+    const int per_row = p.head_dim / 8, n = 2 * per_row;
+    const uint8_t* rows = p.b_base + page * p.b_sp + h * p.b_sh;
+    uint4 raw[MAX];
+#pragma unroll
+    for (int c = 0; c < MAX; ++c) {
+        const int x = lane + 32 * c, side = x >= per_row ? 1 : 0;
+        raw[c] = x < n ? *reinterpret_cast<const uint4*>(rows + side * p.b_st + (x - side * per_row) * 16)
+                       : make_uint4(0u, 0u, 0u, 0u);
+    }
     double s = 0.0;
-    const uint16_t* rows = reinterpret_cast<const uint16_t*>(p.b_base + page * p.b_sp + h * p.b_sh);
-    for (int e = lane; e < 2 * D; e += 32) {
-        const int side = e / D, d = e - side * D;
-        s += w64[e] * static_cast<double>(load_16bit<BF16>(rows + side * (p.b_st / 2) + d));
+#pragma unroll
+    for (int c = 0; c < MAX; ++c) {
+        const int x = lane + 32 * c;
+        if (x >= n) continue;
+        const uint32_t v[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack2<BF16>(v[k]);
+            s = fma(w64[8 * x + 2 * k], static_cast<double>(f.x), s);
+            s = fma(w64[8 * x + 2 * k + 1], static_cast<double>(f.y), s);
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -116,11 +206,14 @@ __device__ __forceinline__ double score64(const SelectParams& p, const double* w
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, SelShape<D>::CTAS)
+score_pages_kernel(const __grid_constant__ SelectParams p) {
     using S = SelShape<D>;
     constexpr int LPP = S::LPP, CPL = S::CPL, PPW = S::PPW, U = S::U;
-    __shared__ SelShared sm;
-    __shared__ __align__(16) float s_w[2 * D];  // weights of the minimum row, then of the maximum row
+    // Weights of the chunks (of the minimum row, then of the maximum row): elements 0 .. 3
+    // of every chunk, then 4 .. 7 (a warp's 16-byte loads of them meet no bank twice).
+    __shared__ __align__(16) float4 s_w[2][S::CHUNKS];
+    __shared__ float s_abs[kScoreWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / p.n_chunks;  // (sequence, query, KV head)
     const int chunk = static_cast<int>(blockIdx.x - row * p.n_chunks);
@@ -128,158 +221,291 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     const int64_t tok = row / p.hk;
     const int b = static_cast<int>(tok / p.q_len);
     const int qi = static_cast<int>(tok - static_cast<int64_t>(b) * p.q_len);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The choosing kernel may start only once every CTA here has passed its wait: it then
+    // may read this launch's inputs before its own.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    int64_t L = p.seq_lens[b];
-    const int64_t room = static_cast<int64_t>(p.max_pages) << p.page_shift;
-    if (L < 0 || L > room) {
-        if (tid == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
-        L = L < 0 ? 0 : room;
-    }
-    const int64_t seen = max(static_cast<int64_t>(0), p.causal ? L - p.q_len + qi + 1 : L);
-    const int M = static_cast<int>((seen + (1 << p.page_shift) - 1) >> p.page_shift);  // <= max_pages
+    // Requested together: the length, this warp's first page ids, the query rows.
+    const int64_t L = p.seq_lens[b];
     const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.pt_stride;
-    int32_t* ids = p.page_ids + row * p.budget;
-    int32_t* index = p.page_indices != nullptr ? p.page_indices + row * p.budget : nullptr;
-    const bool all = M <= p.budget;
-    const int n_cand = all ? 0 : M - p.first - p.last;  // >= 1: budget >= first + last
-    const int need = all ? 0 : p.budget - p.first - p.last;
-    if (need == 0) {  // nothing to choose
-        if (chunk != 0) return;
-        for (int x = tid; x < p.budget; x += kSelThreads) {
-            const int j = all ? (x < M ? x : -1) : (x < p.first ? x : M - p.budget + x);
-            ids[x] = j >= 0 ? table[j] : -1;
-            if (index != nullptr) index[x] = j;
-        }
-        if (tid == 0)
-            p.counts[row] = static_cast<int32_t>(
-                all ? seen : seen - (static_cast<int64_t>(M - p.budget) << p.page_shift));
-        return;
+    const int sub = lane / LPP, l = lane - sub * LPP;
+    const int begin = chunk * p.chunk;
+    int next_id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = begin + (warp + u * kScoreWarps) * PPW + sub;
+        next_id[u] = p.first + i < p.max_pages && i < begin + p.chunk ? table[p.first + i] : 0;
     }
-    const int n_active = (n_cand + p.chunk - 1) / p.chunk;
-    if (chunk >= n_active) return;
-
-    // ---- the weights of this row's two bound rows
     const uint16_t* q = p.q + tok * p.q_st + static_cast<int64_t>(h) * p.group * p.q_sh;
-    for (int d = tid; d < D; d += kSelThreads) {
+    float q0[8];  // element tid of the group's first eight heads
+#pragma unroll
+    for (int g = 0; g < 8; ++g) q0[g] = tid < D && g < p.group ? load_16bit<BF16>(q + g * p.q_sh + tid) : 0.f;
+    const int n_cand = sel_row(p, L, qi).n_cand;
+    if (begin >= n_cand) return;
+
+    // ---- the weights of the two bound rows
+    for (int d = tid; d < D; d += kScoreThreads) {
         float neg = 0.f, pos = 0.f;
-        for (int g = 0; g < p.group; ++g) {
-            const float v = load_16bit<BF16>(q + g * p.q_sh + d);
-            // a NaN goes into both sums
-            neg += v > 0.f ? 0.f : v;
-            pos += v < 0.f ? 0.f : v;
+        for (int g0 = 0; g0 < p.group; g0 += 8) {
+            if (d != tid || g0 != 0) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    q0[g] = g0 + g < p.group ? load_16bit<BF16>(q + (g0 + g) * p.q_sh + d) : 0.f;
+            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {  // a NaN goes into both sums
+                neg += q0[g] > 0.f ? 0.f : q0[g];
+                pos += q0[g] < 0.f ? 0.f : q0[g];
+            }
         }
-        s_w[d] = neg;
-        s_w[D + d] = pos;
+        float* to = reinterpret_cast<float*>(&s_w[(d >> 2) & 1][d / 8]) + (d & 3);
+        to[0] = neg;
+        to[4 * (D / 8)] = pos;
     }
     __syncthreads();
-    const int sub = lane / LPP, l = lane - sub * LPP;
-    float w[CPL][8];
+    const uint8_t* base = p.b_base + h * p.b_sh;
     int64_t off[CPL];  // byte offset of this lane's chunks in a page's rows
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
-        const int x = l + LPP * c;  // chunk: min row first, then max row
-        const int side = x / (D / 8), k = x - side * (D / 8);
-        off[c] = h * p.b_sh + side * p.b_st + k * 16;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[c][e] = s_w[side * D + 8 * k + e];
+        const int x = l + LPP * c, side = x / (D / 8);
+        off[c] = side * p.b_st + (x - side * (D / 8)) * 16;
     }
 
     // ---- scores of this CTA's pages
-    float* scores = p.scores + row * p.max_pages;
-    const int begin = chunk * p.chunk, end = min(begin + p.chunk, n_cand);
-    float abs_max = 0.f;  // the largest sum of magnitudes that this lane has seen
-    for (int i0 = begin + warp * PPW; i0 < end; i0 += kSelWarps * PPW * U) {
-        int page[U];
+    float* scores = p.scores + row * p.score_stride;
+    const int end = min(begin + p.chunk, n_cand);
+    uint32_t top[CPL][4];  // largest magnitude that each of this lane's elements has had
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[c][k] = 0u;
+    for (int i0 = begin + warp * PPW; i0 < end; i0 += kScoreWarps * PPW * U) {
         uint4 raw[U][CPL];
+        const int id0 = __shfl_sync(0xffffffffu, next_id[0], 0);
+        unsigned bad = 0u;  // groups of this round whose page id is outside the pool: page 0 is read instead
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kSelWarps * PPW + sub;
-            page[u] = -1;
-            if (i < end) {
-                page[u] = table[p.first + i];
-                if (page[u] < 0 || page[u] >= p.b_pages) {
-                    if (l == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
-                    page[u] = -1;
-                }
-            }
+            // groups past the end read the round's first page again; nothing is stored for them
+            const int id = i0 + u * kScoreWarps * PPW + sub < end ? next_id[u] : id0;
+            const bool in = id >= 0 && id < p.b_pages;
+            if (!in) bad |= 1u << u;
+            const uint8_t* rows = base + static_cast<int64_t>(in ? id : 0) * p.b_sp;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) raw[u][c] = *reinterpret_cast<const uint4*>(rows + off[c]);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {  // the ids of the next round travel with this one's rows
+            const int i = i0 + (kScoreWarps * U + u * kScoreWarps) * PPW + sub;
+            next_id[u] = i < end ? table[p.first + i] : 0;
+        }
+        float2 a[U];  // even and odd elements
 #pragma unroll
-            for (int c = 0; c < CPL; ++c)
-                raw[u][c] = page[u] >= 0 ? *reinterpret_cast<const uint4*>(p.b_base + page[u] * p.b_sp + off[c])
-                                         : make_uint4(0u, 0u, 0u, 0u);
+        for (int u = 0; u < U; ++u) a[u] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float s = 0.f, a = 0.f;
+        for (int c = 0; c < CPL; ++c) {
+            // from shared memory each round: as registers they would cost loads in flight
+            const float4 w0 = s_w[0][l + LPP * c], w1 = s_w[1][l + LPP * c];
+            const float2 w[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
+                                 make_float2(w1.z, w1.w)};
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
+            for (int u = 0; u < U; ++u) {
                 const uint32_t v[4] = {raw[u][c].x, raw[u][c].y, raw[u][c].z, raw[u][c].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 f = unpack2<BF16>(v[k]);
-                    s = fmaf(f.x, w[c][2 * k], s);
-                    s = fmaf(f.y, w[c][2 * k + 1], s);
-                    a = fmaf(fabsf(f.x), fabsf(w[c][2 * k]), a);
-                    a = fmaf(fabsf(f.y), fabsf(w[c][2 * k + 1]), a);
+                    a[u] = __ffma2_rn(unpack2<BF16>(v[k]), w[k], a[u]);
+                    top[c][k] = max_u16x2(top[c][k], v[k] & 0x7fff7fffu);
                 }
             }
-            abs_max = max_nan(abs_max, a);
+        }
+        float s[U];
 #pragma unroll
-            for (int o = LPP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const int i = i0 + u * kSelWarps * PPW + sub;
-            if (l == 0 && i < end) scores[i] = page[u] >= 0 ? s : -INFINITY;
+        for (int u = 0; u < U; ++u) s[u] = a[u].x + a[u].y;
+        fold<U, LPP / 2>(s, lane);
+        constexpr int LPU = LPP / U;  // lanes that end up with the same page
+        if (l % LPU == 0) {
+            const int u = l / LPU;
+            const int i = i0 + u * kScoreWarps * PPW + sub;
+            if (i < end) scores[i] = (bad >> u) & 1u ? -INFINITY : s[0];
+        }
+        if (l == 0) {
+            if (bad != 0u && p.err != nullptr) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (((bad >> u) & 1u) && i0 + u * kScoreWarps * PPW + sub < end) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
+            }
         }
     }
-    // The row's largest sum of magnitudes is at most the sum over a page's lanes of each
-    // lane's largest (NaN and infinity carry through).
+    // A page's sum of magnitudes is at most the sum of each element's largest times its
+    // weight (NaN and infinity carry through).
+    float abs_max = 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        const float4 w0 = s_w[0][l + LPP * c], w1 = s_w[1][l + LPP * c];
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 t = unpack2<BF16>(top[c][k]);
+            abs_max += t.x * fabsf(w[2 * k]);
+            abs_max += t.y * fabsf(w[2 * k + 1]);
+        }
+    }
 #pragma unroll
     for (int o = LPP / 2; o > 0; o >>= 1) abs_max += __shfl_xor_sync(0xffffffffu, abs_max, o);
 #pragma unroll
     for (int o = LPP; o < 32; o <<= 1) abs_max = max_nan(abs_max, __shfl_xor_sync(0xffffffffu, abs_max, o));
-    if (lane == 0) sm.err[warp] = abs_max;
-    __threadfence();
+    if (lane == 0) s_abs[warp] = abs_max;
     __syncthreads();
     if (tid == 0) {
-        float a = sm.err[0];
+        float a = s_abs[0];
 #pragma unroll
-        for (int x = 1; x < kSelWarps; ++x) a = max_nan(a, sm.err[x]);
-        atomicMax(p.row_abs + row, __float_as_uint(a) & 0x7fffffffu);  // magnitudes order as integers
-        __threadfence();
-        sm.last = atomicAdd(p.row_count + row, 1u) == static_cast<unsigned>(n_active) - 1u;
+        for (int x = 1; x < kScoreWarps; ++x) a = max_nan(a, s_abs[x]);
+        p.chunk_abs[row * p.abs_stride + chunk] = a;
     }
-    __syncthreads();
-    if (!sm.last) return;
+}
 
-    // ---- this CTA is the row's last: select
-    __threadfence();
-    // Error of an fp32 score: the weights (group - 1 additions of one sign), a chain of
-    // 8 CPL products, log2(LPP) additions; in units of 2^-24 of the sum of magnitudes,
-    // rounded up, with room for the rounding of that sum itself.
-    const float sum_abs = __uint_as_float(atomicAdd(p.row_abs + row, 0u));
-    const float E = sum_abs * ((p.group + 8 * CPL + 8) * 6.0e-8f) + 1e-37f;
-    auto score_of = [&](int i) { return not_nan(ld_cg(scores + i)); };
-    uint32_t prefix = 0;
-    int want = need;  // the want-th largest among those with the prefix
+template <int NW>
+struct ChooseShared {
+    uint32_t key[kTile];  // a tile's scores as ordered integers; then its taken pages
+    double weight64[2 * 512];
+    int hist[kBins];
+    unsigned long long near_key[kNear];
+    int near_idx[kNear];
+    float abs_max[NW];
+    int sum[NW], sum2[NW];
+    uint32_t kmin[NW], kmax[NW];
+    int bin, above, in_bin, near_n, cut_idx;
+    unsigned long long cut_key;
+};
+
+template <bool BF16, int NW>
+__global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_constant__ SelectParams p) {
+    constexpr int NT = NW * 32;
+    static_assert(NT >= kBins && NT >= kNear && NW <= 32, "one bin, one near key a thread");
+    __shared__ __align__(16) ChooseShared<NW> sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    const int h = static_cast<int>(row % p.hk);
+    const int64_t tok = row / p.hk;
+    const int b = static_cast<int>(tok / p.q_len);
+    const int qi = static_cast<int>(tok - static_cast<int64_t>(b) * p.q_len);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The scoring launch's own inputs are complete here (all its CTAs have passed their
+    // wait for whatever came before); they are read past L1, its scores after the wait below.
+    const SelRow r = sel_row(p, ld_cg(p.seq_lens + b), qi);
+    const int n_cand = r.n_cand, need = r.need;
+    const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.pt_stride;
+    int32_t* ids = p.page_ids + row * p.budget;
+    int32_t* index = p.page_indices != nullptr ? p.page_indices + row * p.budget : nullptr;
+    if (tid < kBins) sm.hist[tid] = 0;
+    if (tid == 0) {
+        sm.near_n = 0;
+        if (r.bad && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
+        // all pages but the newest are full
+        p.counts[row] = static_cast<int32_t>(
+            r.all ? r.seen : r.seen - (static_cast<int64_t>(r.M - p.budget) << p.page_shift));
+    }
+    if (need == 0) {  // nothing to choose
+        for (int x = tid; x < p.budget; x += NT) {
+            const int j = r.all ? (x < r.M ? x : -1) : (x < p.first ? x : r.M - p.budget + x);
+            ids[x] = j >= 0 ? ld_cg(table + j) : -1;
+            if (index != nullptr) index[x] = j;
+        }
+        return;
+    }
+    for (int x = tid; x < p.first + p.last; x += NT) {
+        const int to = x < p.first ? x : p.budget - p.last + (x - p.first);
+        const int j = x < p.first ? x : r.M - p.last + (x - p.first);
+        ids[to] = ld_cg(table + j);
+        if (index != nullptr) index[to] = j;
+    }
+    // The weights in 64 bits, for pages near the border (computed while the scoring launch
+    // still runs: 2 us of a call that needs them, if left until it does).
+    const uint16_t* q = p.q + tok * p.q_st + static_cast<int64_t>(h) * p.group * p.q_sh;
+    for (int d = tid; d < p.head_dim; d += NT) {
+        double neg = 0.0, pos = 0.0;
+        for (int g0 = 0; g0 < p.group; g0 += 4) {
+            float x[4];
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const int bits = pass == 2 ? 10 : 11;
-        const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + bits);
-        for (int x = tid; x < kBins; x += kSelThreads) sm.hist[x] = 0;
-        __syncthreads();
-        for (int i = tid; i < n_cand; i += kSelThreads) {
-            const uint32_t k = ordered(score_of(i));
-            if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+            for (int g = 0; g < 4; ++g) x[g] = g0 + g < p.group ? to_float<BF16>(ld_cg(q + (g0 + g) * p.q_sh + d)) : 0.f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                if (!(x[g] > 0.f)) neg += x[g];  // a NaN goes into both sums
+                if (!(x[g] < 0.f)) pos += x[g];
+            }
+        }
+        sm.weight64[d] = neg;
+        sm.weight64[p.head_dim + d] = pos;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores
+    const float* scores = p.scores + row * p.score_stride;
+    // The row's largest sum of magnitudes, reduced with the tile's load below.
+    float sum_abs = 0.f;
+    const int n_active = (n_cand + p.chunk - 1) / p.chunk;
+    for (int x = tid; x < n_active; x += NT) sum_abs = max_nan(sum_abs, p.chunk_abs[row * p.abs_stride + x]);
+    // The row's scores as ordered integers, in shared memory (in tiles of kTile, loaded
+    // again in each pass, for longer rows).  The loops over them are not unrolled: this
+    // code runs once a row, and fetching it costs more than its steps.
+    const int n_tiles = (n_cand + kTile - 1) / kTile;
+    auto load = [&](int t) {
+        const int n = min(kTile, n_cand - t * kTile);
+        const float* src = scores + t * kTile;
+        for (int i = 4 * tid; i < n; i += 4 * NT) {  // whole vectors: the row's stride is a multiple of 4
+            const float4 f = ld_cg4(src + i);
+            *reinterpret_cast<uint4*>(sm.key + i) =  // -0 as 0
+                make_uint4(ordered(not_nan(f.x) + 0.f), ordered(not_nan(f.y) + 0.f), ordered(not_nan(f.z) + 0.f),
+                           ordered(not_nan(f.w) + 0.f));
         }
         __syncthreads();
-        // bins from the top: thread t has bins kBins - 8 t - 1 .. kBins - 8 t - 8
-        constexpr int PER = kBins / kSelThreads;
-        int mine = 0;
+    };
+    // f(key, index) over the row's pages
+    auto each = [&](auto&& f) {
+        for (int t = 0; t < n_tiles; ++t) {
+            if (n_tiles > 1) {
+                __syncthreads();
+                load(t);
+            }
+            const int n = min(kTile, n_cand - t * kTile);
+#pragma unroll 2
+            for (int i = tid; i < n; i += NT) f(sm.key[i], t * kTile + i);
+        }
+    };
+    load(0);
+    uint32_t k_min = ~0u, k_max = 0u;
+    each([&](uint32_t k, int) {
+        k_min = min(k_min, k);
+        k_max = max(k_max, k);
+    });
+    k_min = __reduce_min_sync(0xffffffffu, k_min);
+    k_max = __reduce_max_sync(0xffffffffu, k_max);
 #pragma unroll
-        for (int x = 0; x < PER; ++x) mine += sm.hist[kBins - 1 - (tid * PER + x)];
+    for (int o = 16; o > 0; o >>= 1) sum_abs = max_nan(sum_abs, __shfl_xor_sync(0xffffffffu, sum_abs, o));
+    if (lane == 0) {
+        sm.kmin[warp] = k_min;
+        sm.kmax[warp] = k_max;
+        sm.abs_max[warp] = sum_abs;
+    }
+    __syncthreads();
+    k_min = __reduce_min_sync(0xffffffffu, lane < NW ? sm.kmin[lane] : ~0u);
+    k_max = __reduce_max_sync(0xffffffffu, lane < NW ? sm.kmax[lane] : 0u);
+    // Error of an fp32 score: the weights (group - 1 additions of one sign), a chain of
+    // 4 CPL products in each of two sums, 1 + log2(LPP) additions (at most 16 and 6); in
+    // units of 2^-24 of the sum of magnitudes, with room for the rounding of that sum.
+    sum_abs = sm.abs_max[0];
+    for (int x = 1; x < NW; ++x) sum_abs = max_nan(sum_abs, sm.abs_max[x]);
+    const float E = sum_abs * ((p.group + p.chain + 9) * 6.0e-8f) + 1e-37f;
+    // The want-th largest key in [k_min, k_max]: equal bins over that range, then the bin
+    // it is in, until a bin holds few enough to compare each with each.
+    int want = need;
+    uint32_t kth;
+    while (true) {
+        const int shift = max(0, 24 - __clz(k_max - k_min));  // (k_max - k_min) >> shift < kBins = 256
+        each([&](uint32_t k, int) {
+            if (k >= k_min && k <= k_max) atomicAdd(&sm.hist[(k - k_min) >> shift], 1);
+        });
+        __syncthreads();
+        // bins from the top, one a thread
+        const int mine = tid < kBins ? sm.hist[kBins - 1 - tid] : 0;
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -288,78 +514,76 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         }
         if (lane == 31) sm.sum[warp] = upto;
         __syncthreads();
-        for (int x = 0; x < warp; ++x) upto += sm.sum[x];
-        int before = upto - mine;
-        if (before < want && want <= upto) {
-            for (int x = 0; x < PER; ++x) {
-                const int bin = kBins - 1 - (tid * PER + x);
-                const int n = sm.hist[bin];
-                if (want <= before + n) {
-                    sm.bin = bin;
-                    sm.above = before;
-                    break;
-                }
-                before += n;
-            }
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? sm.sum[lane] : 0);
+        if (tid < kBins && upto - mine < want && want <= upto) {
+            sm.bin = kBins - 1 - tid;
+            sm.above = upto - mine;
+            sm.in_bin = mine;
         }
         __syncthreads();
-        prefix |= static_cast<uint32_t>(sm.bin) << shift;
         want -= sm.above;
+        k_min += static_cast<uint32_t>(sm.bin) << shift;
+        k_max = k_min + ((1u << shift) - 1u);
+        if (shift == 0) {
+            kth = k_min;
+            break;
+        }
+        const int n_bin = sm.in_bin;
+        if (n_bin <= kNear) {
+            each([&](uint32_t k, int) {
+                if (k >= k_min && k <= k_max) sm.near_idx[atomicAdd(&sm.near_n, 1)] = static_cast<int>(k);
+            });
+            __syncthreads();
+            if (tid < n_bin) {
+                const uint32_t k = static_cast<uint32_t>(sm.near_idx[tid]);
+                int more = 0, same = 0;
+                for (int y = 0; y < n_bin; ++y) {
+                    const uint32_t o = static_cast<uint32_t>(sm.near_idx[y]);
+                    more += o > k;
+                    same += o == k;
+                }
+                if (more < want && want <= more + same) sm.bin = static_cast<int>(k);  // equal keys write the same
+            }
+            __syncthreads();
+            kth = static_cast<uint32_t>(sm.bin);
+            break;
+        }
+        if (tid < kBins) sm.hist[tid] = 0;
         __syncthreads();
     }
-    const float T = from_ordered(prefix);
+    const float T = from_ordered(kth);
     const bool sure_E = E < INFINITY;
     // 2 E from T, and a rounding more
-    const float lo = sure_E ? T - 2.5f * E : -INFINITY;
-    const float hi = sure_E ? T + 2.5f * E : INFINITY;
+    const uint32_t lo = sure_E ? ordered(T - 2.5f * E + 0.f) : 1u;
+    const uint32_t hi = sure_E ? ordered(T + 2.5f * E + 0.f) : ~0u;
     int n_hi = 0, n_near = 0;
-    for (int i = tid; i < n_cand; i += kSelThreads) {
-        const float s = score_of(i);
-        n_hi += s > hi;
-        n_near += s >= lo && s <= hi;
-    }
-    n_hi = block_sum(n_hi, sm.sum);
-    n_near = block_sum(n_near, sm.sum);
+    each([&](uint32_t k, int) {
+        n_hi += k > hi;
+        n_near += k >= lo && k <= hi;
+    });
+    block_sum2<NW>(n_hi, n_near, sm.sum, sm.sum2);
     const int take_near = need - n_hi;  // of the pages near the border: 1 .. n_near
     const bool refine = take_near < n_near;
     unsigned long long* key64 = p.near_keys + row * p.max_pages;
     if (refine) {
-        for (int e = tid; e < 2 * D; e += kSelThreads) {
-            const int side = e / D, d = e - side * D;
-            double v = 0.0;
-            for (int g = 0; g < p.group; ++g) {
-                const float x = load_16bit<BF16>(q + g * p.q_sh + d);
-                v += side == 0 ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
-            }
-            sm.weight64[e] = v;
-        }
         if (tid == 0) sm.near_n = 0;
         __syncthreads();
-        for (int i0 = warp * 32; i0 < n_cand; i0 += kSelThreads) {
-            const int i = i0 + lane;
-            const float s = i < n_cand ? score_of(i) : 0.f;
-            unsigned todo = __ballot_sync(0xffffffffu, i < n_cand && s >= lo && s <= hi);
-            while (todo != 0u) {
-                const int x = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int id = table[p.first + i0 + x];
-                const bool ok = id >= 0 && id < p.b_pages;
-                const double v = ok ? not_nan(score64<D, BF16>(p, sm.weight64, id, h, lane))
-                                    : -static_cast<double>(INFINITY);
-                if (lane == 0) {
-                    key64[i0 + x] = ordered(v);
-                    const int at = atomicAdd(&sm.near_n, 1);
-                    if (at < kNear) {
-                        sm.near_key[at] = ordered(v);
-                        sm.near_idx[at] = i0 + x;
-                    }
-                }
+        auto score_at = [&](int i) {
+            const int id = table[p.first + i];
+            return id >= 0 && id < p.b_pages ? ordered(not_nan(score64<BF16>(p, sm.weight64, id, h, lane)))
+                                             : ordered(-static_cast<double>(INFINITY));
+        };
+        if (n_near <= kNear) {
+            each([&](uint32_t k, int i) {
+                if (k >= lo && k <= hi) sm.near_idx[atomicAdd(&sm.near_n, 1)] = i;
+            });
+            __syncthreads();
+            for (int x = warp; x < n_near; x += NW) {
+                const unsigned long long k = score_at(sm.near_idx[x]);
+                if (lane == 0) sm.near_key[x] = k;
             }
-        }
-        __threadfence_block();
-        __syncthreads();
-        if (n_near <= kNear) {  // the rank of each among them
-            for (int x = tid; x < n_near; x += kSelThreads) {
+            __syncthreads();
+            for (int x = tid; x < n_near; x += NT) {  // the rank of each among them
                 const unsigned long long k = sm.near_key[x];
                 const int i = sm.near_idx[x];
                 int rank = 0;
@@ -371,26 +595,38 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 }
             }
         } else {  // many (equal pages, infinities): the key bit by bit, then the index
-            auto near = [&](int i) {
-                const float s = score_of(i);
-                return s >= lo && s <= hi;
+            auto sum_of = [&](int n) {
+                int none = 0;
+                block_sum2<NW>(n, none, sm.sum, sm.sum2);
+                return n;
             };
+            auto near = [&](int i) {
+                const uint32_t k = ordered(not_nan(ld_cg(scores + i)) + 0.f);
+                return k >= lo && k <= hi;
+            };
+            for (int i = warp; i < n_cand; i += NW) {
+                if (!near(i)) continue;
+                const unsigned long long k = score_at(i);
+                if (lane == 0) key64[i] = k;
+            }
+            __threadfence_block();
+            __syncthreads();
             unsigned long long cut = 0;
             for (int bit = 63; bit >= 0; --bit) {
                 const unsigned long long t = cut | (1ull << bit);
                 int n = 0;
-                for (int i = tid; i < n_cand; i += kSelThreads) n += near(i) && key64[i] >= t;
-                if (block_sum(n, sm.sum) >= take_near) cut = t;
+                for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] >= t;
+                if (sum_of(n) >= take_near) cut = t;
             }
             int n = 0;
-            for (int i = tid; i < n_cand; i += kSelThreads) n += near(i) && key64[i] > cut;
-            const int ties = take_near - block_sum(n, sm.sum);  // of those equal to the cut: the first ones
+            for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] > cut;
+            const int ties = take_near - sum_of(n);  // of those equal to the cut: the first ones
             int low = 0, high = n_cand - 1;  // smallest index with `ties` of them at or below it
             while (low < high) {
                 const int mid = (low + high) / 2;
                 n = 0;
-                for (int i = tid; i <= mid; i += kSelThreads) n += near(i) && key64[i] == cut;
-                if (block_sum(n, sm.sum) >= ties)
+                for (int i = tid; i <= mid; i += NT) n += near(i) && key64[i] == cut;
+                if (sum_of(n) >= ties)
                     high = mid;
                 else
                     low = mid + 1;
@@ -402,86 +638,126 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         }
         __syncthreads();
     }
-    auto take = [&](int i) {
-        const float s = score_of(i);
-        if (s > hi) return true;
-        if (!(s >= lo)) return false;
+    auto take = [&](uint32_t k, int i) {
+        if (k > hi) return true;
+        if (k < lo) return false;
         if (!refine) return true;
-        const unsigned long long k = key64[i];
-        return k > sm.cut_key || (k == sm.cut_key && i <= sm.cut_idx);
+        unsigned long long k64 = 0;
+        if (n_near <= kNear) {
+            for (int y = 0; y < n_near; ++y)
+                if (sm.near_idx[y] == i) k64 = sm.near_key[y];
+        } else {
+            k64 = key64[i];
+        }
+        return k64 > sm.cut_key || (k64 == sm.cut_key && i <= sm.cut_idx);
     };
 
-    // ---- write the taken pages in order: each warp a run of the candidates
-    const int seg = (n_cand + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-    const int s0 = min(warp * seg, n_cand), s1 = min(s0 + seg, n_cand);
-    int n_taken = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32) n_taken += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && take(i0 + lane)));
-    __syncthreads();
-    if (lane == 0) sm.sum[warp] = n_taken;
-    __syncthreads();
+    // ---- write the taken pages in order: each warp a run of a tile
+    static_assert(kTile / NT <= 32, "one word of taken flags a lane");
     int at = p.first;
-    for (int x = 0; x < warp; ++x) at += sm.sum[x];
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-        const int i = i0 + lane;
-        const bool t = i < s1 && take(i);
-        const unsigned m = __ballot_sync(0xffffffffu, t);
-        if (t) {
-            const int x = at + __popc(m & ((1u << lane) - 1u));
-            ids[x] = table[p.first + i];
-            if (index != nullptr) index[x] = p.first + i;
+    for (int t = 0; t < n_tiles; ++t) {
+        if (n_tiles > 1) {
+            __syncthreads();
+            load(t);
         }
-        at += __popc(m);
+        const int n = min(kTile, n_cand - t * kTile);
+        const int run = (n + NT - 1) / NT * 32;  // pages a warp, in words of 32
+        const int i0 = warp * run;
+        uint32_t mine = 0u;  // lane x: the flags of word x
+        int n_taken = 0;
+#pragma unroll 1
+        for (int x = 0; x < run / 32; ++x) {
+            const int i = i0 + 32 * x + lane;
+            const uint32_t m = __ballot_sync(0xffffffffu, i < n && take(sm.key[i], t * kTile + i));
+            if (lane == x) mine = m;
+            n_taken += __popc(m);
+        }
+        if (lane == 0) sm.sum[warp] = n_taken;
+        __syncthreads();  // also: every key of the tile has been read
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sm.sum[lane] : 0);
+        const int total = __reduce_add_sync(0xffffffffu, lane < NW ? sm.sum[lane] : 0);
+        int upto = __popc(mine);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        int x = before + upto - __popc(mine);
+        while (mine != 0u) {
+            sm.key[x++] = static_cast<uint32_t>(t * kTile + i0 + 32 * lane + __ffs(mine) - 1);
+            mine &= mine - 1u;
+        }
+        __syncthreads();
+        for (int y = tid; y < total; y += NT) {
+            const int j = p.first + static_cast<int>(sm.key[y]);
+            ids[at + y] = table[j];
+            if (index != nullptr) index[at + y] = j;
+        }
+        at += total;
     }
-    for (int x = tid; x < p.first + p.last; x += kSelThreads) {
-        const int at2 = x < p.first ? x : p.budget - p.last + (x - p.first);
-        const int j = x < p.first ? x : M - p.last + (x - p.first);
-        ids[at2] = table[j];
-        if (index != nullptr) index[at2] = j;
-    }
-    if (tid == 0) {
-        p.counts[row] = static_cast<int32_t>(seen - (static_cast<int64_t>(M - p.budget) << p.page_shift));
-        p.row_count[row] = 0u;  // as the next call expects them
-        p.row_abs[row] = 0u;
-    }
+}
+
+cudaLaunchConfig_t dependent_launch(int64_t blocks, int threads, cudaStream_t s, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 template <int D>
-cudaError_t launch_select_d(const SelectParams& p, int64_t blocks, bool bf16, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-    cfg.blockDim = dim3(kSelThreads, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, select_pages_kernel<D, true>, p)
-                : cudaLaunchKernelEx(&cfg, select_pages_kernel<D, false>, p);
-}
-
-}  // namespace
-
-cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num_sms, cudaStream_t s) {
+cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
     const int64_t cand = std::max(1, p.max_pages - p.first - p.last);
-    // Pages per CTA: enough CTAs to fill the machine several times over (rows differ in
-    // length, and the CTAs that select leave others to stream), none below 32 pages.
-    int64_t chunk = (rows * cand + num_sms * 12 - 1) / (num_sms * 12);
-    chunk = std::min<int64_t>(std::max<int64_t>((chunk + 31) / 32 * 32, 32), (cand + 31) / 32 * 32);
+    // Pages per CTA: one wave of CTAs while that leaves each at most 192 KB to stream;
+    // more CTAs than that for more pages, as rows differ in length.
+    const int64_t wave = static_cast<int64_t>(num_sms) * SelShape<D>::CTAS;
+    int64_t chunk = std::min<int64_t>((rows * cand + wave - 1) / wave, (192 << 10) / (4 * D));
+    chunk = std::min((chunk + kMinChunk - 1) / kMinChunk * kMinChunk, (cand + kMinChunk - 1) / kMinChunk * kMinChunk);
     // at most 2^31 - 1 CTAs
     while (rows * ((cand + chunk - 1) / chunk) > INT32_MAX && chunk < cand) chunk *= 2;
     p.chunk = static_cast<int>(chunk);
     p.n_chunks = static_cast<int>((cand + chunk - 1) / chunk);
-    const int64_t blocks = rows * p.n_chunks;
+    p.chain = 4 * SelShape<D>::CPL;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = dependent_launch(rows * p.n_chunks, kScoreThreads, s, attr);
+    return bf16 ? cudaLaunchKernelEx(&cfg, score_pages_kernel<D, true>, p)
+                : cudaLaunchKernelEx(&cfg, score_pages_kernel<D, false>, p);
+}
+
+template <int NW>
+cudaError_t launch_choose(const SelectParams& p, bool bf16, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg =
+        dependent_launch(static_cast<int64_t>(p.batch) * p.q_len * p.hk, NW * 32, s, attr);
+    return bf16 ? cudaLaunchKernelEx(&cfg, choose_pages_kernel<true, NW>, p)
+                : cudaLaunchKernelEx(&cfg, choose_pages_kernel<false, NW>, p);
+}
+
+}  // namespace
+
+int64_t select_abs_stride(int64_t max_pages) { return (max_pages + kMinChunk - 1) / kMinChunk; }
+
+cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num_sms, cudaStream_t s) {
+    p.head_dim = head_dim;
+    cudaError_t e;
     switch (head_dim) {
-        case 64: return launch_select_d<64>(p, blocks, bf16, s);
-        case 128: return launch_select_d<128>(p, blocks, bf16, s);
-        case 192: return launch_select_d<192>(p, blocks, bf16, s);
-        case 256: return launch_select_d<256>(p, blocks, bf16, s);
-        case 512: return launch_select_d<512>(p, blocks, bf16, s);
+        case 64: e = launch_score<64>(p, bf16, num_sms, s); break;
+        case 128: e = launch_score<128>(p, bf16, num_sms, s); break;
+        case 192: e = launch_score<192>(p, bf16, num_sms, s); break;
+        case 256: e = launch_score<256>(p, bf16, num_sms, s); break;
+        case 512: e = launch_score<512>(p, bf16, num_sms, s); break;
         default: return cudaErrorInvalidValue;
     }
+    if (e != cudaSuccess) return e;
+    // Four times the threads where a row has more pages than 256 threads pass over quickly
+    // and there are few rows.
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
+    return p.max_pages > 1024 && rows <= num_sms ? launch_choose<32>(p, bf16, s) : launch_choose<8>(p, bf16, s);
 }
 
 }  // namespace fdec

@@ -208,35 +208,35 @@ fdec_status fdec_page_bounds(fdec_kv_desc k, fdec_kv_desc bounds, const int32_t*
 
 namespace {
 
-// Workspace of fdec_select_pages: counters and magnitudes first (zero between calls).
+// Workspace of fdec_select_pages: 64-bit keys, scores, magnitudes.
 struct SelectLayout {
-    size_t off_abs, off_scores, off_near, bytes;
+    size_t off_abs, off_scores, bytes;
+    int64_t score_stride;  // floats a row: whole 16-byte vectors
 };
 
 bool select_layout(int64_t rows, int64_t max_pages, SelectLayout* out) {
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     if (rows < 1 || max_pages < 1 || rows > INT32_MAX || max_pages > INT32_MAX) return false;
     const size_t n = static_cast<size_t>(rows), m = static_cast<size_t>(max_pages);
-    out->off_abs = n * 4;
-    out->off_near = up(n * 8);
-    out->off_scores = up(out->off_near + n * m * 8);
-    out->bytes = up(out->off_scores + n * m * 4);
+    out->score_stride = (max_pages + 3) / 4 * 4;
+    out->off_scores = up(n * m * 8);
+    out->off_abs = up(out->off_scores + n * static_cast<size_t>(out->score_stride) * 4);
+    out->bytes = up(out->off_abs + n * static_cast<size_t>(select_abs_stride(max_pages)) * 4);
     return true;
 }
 
 }  // namespace
 
 fdec_status fdec_select_pages_workspace(int batch, int q_len, int num_kv_heads, int64_t max_pages,
-                                        size_t* workspace_bytes, size_t* zero_bytes) {
+                                        size_t* workspace_bytes) {
     clear_failure();
-    if (workspace_bytes == nullptr || zero_bytes == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null output pointer");
-    *workspace_bytes = *zero_bytes = 0;
+    if (workspace_bytes == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null output pointer");
+    *workspace_bytes = 0;
     SelectLayout l;
     if (batch < 1 || q_len < 1 || num_kv_heads < 1 || static_cast<int64_t>(batch) * q_len > INT32_MAX ||
         !select_layout(static_cast<int64_t>(batch) * q_len * num_kv_heads, max_pages, &l))
         return fail(FDEC_ERR_INVALID_ARG, "batch, q_len, num_kv_heads and max_pages must be >= 1 (and rows below 2^31)");
     *workspace_bytes = l.bytes;
-    *zero_bytes = l.off_near;
     return FDEC_OK;
 }
 
@@ -288,10 +288,11 @@ fdec_status fdec_select_pages(const void* q, int64_t q_stride_tok, int64_t q_str
     p.page_ids = page_ids;
     p.counts = counts;
     p.page_indices = page_indices;
-    p.row_count = reinterpret_cast<unsigned*>(ws);
-    p.row_abs = reinterpret_cast<unsigned*>(ws + l.off_abs);
+    p.chunk_abs = reinterpret_cast<float*>(ws + l.off_abs);
+    p.abs_stride = select_abs_stride(max_pages);
     p.scores = reinterpret_cast<float*>(ws + l.off_scores);
-    p.near_keys = reinterpret_cast<unsigned long long*>(ws + l.off_near);
+    p.score_stride = l.score_stride;
+    p.near_keys = reinterpret_cast<unsigned long long*>(ws);
     p.err = device_errors;
     p.batch = batch;
     p.q_len = q_len;
@@ -303,7 +304,7 @@ fdec_status fdec_select_pages(const void* q, int64_t q_stride_tok, int64_t q_str
     p.budget = budget;
     p.first = first_pages;
     p.last = last_pages;
-    p.chunk = p.n_chunks = 0;
+    p.head_dim = p.chunk = p.n_chunks = p.chain = 0;
     int num_sms = 0;
     cudaError_t e = current_num_sms(&num_sms);
     if (e == cudaSuccess) e = launch_select_pages(p, head_dim, dtype == FDEC_BF16, num_sms, stream);

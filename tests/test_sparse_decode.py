@@ -692,8 +692,7 @@ def test_page_bounds_refusals():
 
 def test_select_pages_refusals():
     fn = fd.fdec_select_pages
-    total, zero = fd.fdec_select_pages_workspace(1, 1, 2, 8)
-    assert 0 < zero < total
+    total = fd.fdec_select_pages_workspace(1, 1, 2, 8)
     buf = torch.zeros(total + 256, dtype=torch.uint8)
     ws = buf[(-buf.data_ptr()) % 256:][:total]
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
