@@ -9,6 +9,7 @@ There is no CPU fallback: if the library is not built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -30,6 +31,7 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfdec.so")
+_BINDING_PATH = os.path.join(_HERE, "_sparse_binding.so")
 
 FDEC_F16, FDEC_BF16 = 0, 1
 FDEC_PATH_AUTO, FDEC_PATH_SIMT, FDEC_PATH_MMA, FDEC_PATH_TC = 0, 1, 2, 3
@@ -196,6 +198,9 @@ class Plan:
         self.workspace_bytes = workspace_bytes
         self.batch = batch
         self.meta = meta
+        # what fdec_run_selected checks its tensors against
+        self.shape = (batch, meta["num_qo_heads"], meta["num_kv_heads"], meta["head_dim"], meta["page_size"],
+                      int(meta["dtype"] == "bf16"), 1 if meta["kv_dtype"] else 2)
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
@@ -415,49 +420,28 @@ def fdec_merge_states(o, lse, o_out, lse_out=None, stream=None) -> None:
 # block-sparse decoding
 # ---------------------------------------------------------------------------
 
-def _dtype_of(t) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return FDEC_BF16
-    if t.dtype == torch.float16:
-        return FDEC_F16
-    raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+_binding = None
 
 
-def _kv_type_of(t, dtype) -> int:
-    """FDEC_KV_SAME for pools of `dtype`, FDEC_KV_E4M3 for pools of 1-byte codes (float8_e4m3fn or uint8)."""
-    import torch
+def _sparse():
+    """The compiled marshalling module, its entries set to this library's."""
+    global _binding
+    if _binding is None:
+        lib = _load()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(_BINDING_PATH):
+                    raise RuntimeError(
+                        f"{_BINDING_PATH} is not built: run `python -c 'import __graft_entry__ as g; g.build()'` first")
+                import torch  # noqa: F401  (its libraries are the module's)
 
-    if t.dtype == dtype:
-        return FDEC_KV_SAME
-    if t.dtype in (torch.float8_e4m3fn, torch.uint8):
-        return FDEC_KV_E4M3
-    raise ValueError(f"expected a cache of {dtype} or of E4M3 codes, got {t.dtype}")
-
-
-def _rows(t, what: str) -> Rows:
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{what} must be [n, heads, head_dim] with a unit dim stride")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _int32(t, what: str, dim: int):
-    import torch
-
-    if t.dtype != torch.int32 or t.dim() != dim or (t.numel() > 0 and t.stride(dim - 1) != 1):
-        raise ValueError(f"{what} must be an int32 tensor of {dim} dimension(s) with contiguous rows")
-    return t
-
-
-def _same_device(first, *others) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+                spec = importlib.util.spec_from_file_location("_sparse_binding", _BINDING_PATH)
+                mod = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(mod)
+                mod.set_entries(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.fdec_norm_rope_append, lib.fdec_page_bounds, lib.fdec_select_pages, lib.fdec_run_selected)))
+                _binding = mod
+    return _binding
 
 
 def fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, batch_indices, positions, q_out, k, v, page_table,
@@ -468,39 +452,11 @@ def fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, batch_in
     will do; q_out may be q); q_weight, k_weight [D] of the same type or None; cos_sin float32 [positions, rot_dim]
     (rot_dim / 2 cosines, then the sines) or None; batch_indices, positions, rope_positions int32 [n]; k, v the cache
     views [page, kv_head, slot, dim], 16-bit or E4M3 codes of k / k_scale and v / v_scale."""
-    n, hq, d = q.shape
-    if k_new.shape != v_new.shape or k_new.shape[0] != n or k_new.shape[2] != d or q_out.shape != q.shape:
-        raise ValueError("q, q_out must be [n, Hq, D] and k_new, v_new [n, Hk, D]")
-    hk = k_new.shape[1]
-    dt = _dtype_of(q)
-    for t in (k_new, v_new, q_out):
-        if t.dtype != q.dtype:
-            raise ValueError(f"rows of {q.dtype} and {t.dtype}")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != q.dtype or w.shape != (d,) or not w.is_contiguous()):
-            raise ValueError("weights must be contiguous [head_dim] tensors of the rows' type")
-    import torch
-
-    rot, cos_rows = 0, 0
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
-        cos_rows, rot = cos_sin.shape
-    for t, what in ((batch_indices, "batch_indices"), (positions, "positions"), (rope_positions, "rope_positions")):
-        if t is not None and _int32(t, what, 1).shape[0] != n:
-            raise ValueError(f"{what} must have one entry per token")
-    _int32(page_table, "page_table", 2)
-    kv = _kv_type_of(k, q.dtype)
-    if v.dtype != k.dtype or k.shape[1:] != (hk, page_size, d) or v.shape[1:] != k.shape[1:]:
-        raise ValueError("k and v must be caches [page, Hk, page_size, D] of one type")
-    _same_device(q, k_new, v_new, q_weight, k_weight, cos_sin, batch_indices, positions, rope_positions, q_out, k, v,
-                 page_table, device_errors)
-    _check(_load().fdec_norm_rope_append(
-        _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new"), _ptr(q_weight), _ptr(k_weight), float(eps),
-        _ptr(cos_sin), cos_rows, rot, int(bool(interleaved)), batch_indices.data_ptr(), positions.data_ptr(),
-        _ptr(rope_positions), n, hq, hk, d, page_size, dt, kv, float(k_scale), float(v_scale), _rows(q_out, "q_out"),
-        kv_desc(k), kv_desc(v), page_table.data_ptr(), page_table.shape[0], page_table.stride(0), _ptr(device_errors),
-        _stream_handle(stream)))
+    status = (_binding or _sparse()).norm_rope_append(
+        q, k_new, v_new, q_weight, k_weight, cos_sin, batch_indices, positions, q_out, k, v, page_table, page_size, eps,
+        interleaved, rope_positions, k_scale, v_scale, device_errors, stream)
+    if status:
+        _check(status)
 
 
 def fdec_page_bounds(k, bounds, page_table, begins, seq_lens, page_size: int, expected_tokens: int = 0,
@@ -508,21 +464,10 @@ def fdec_page_bounds(k, bounds, page_table, begins, seq_lens, page_size: int, ex
     """Write the elementwise minimum and maximum of the keys of every page that holds a position in
     [begins[b], seq_lens[b]) (begins None: every page) into bounds [page, kv_head, 2, dim] (16-bit; for a cache of
     E4M3 codes either 16-bit type).  expected_tokens sizes the launch (0: a whole page-table row)."""
-    dt = _dtype_of(bounds)
-    kv = _kv_type_of(k, bounds.dtype)
-    hk, d = k.shape[1], k.shape[3]
-    if k.shape[2] != page_size or bounds.dim() != 4 or bounds.shape[1:] != (hk, 2, d):
-        raise ValueError("need k [page, Hk, page_size, D] and bounds [page, Hk, 2, D]")
-    _int32(page_table, "page_table", 2)
-    batch = page_table.shape[0]
-    for t, what in ((begins, "begins"), (seq_lens, "seq_lens")):
-        if t is not None and _int32(t, what, 1).shape[0] != batch:
-            raise ValueError(f"{what} must have one entry per sequence")
-    _same_device(k, bounds, page_table, begins, seq_lens, device_errors)
-    expected = expected_tokens if expected_tokens > 0 else min(page_table.shape[1] * page_size, 2**31 - 1)
-    _check(_load().fdec_page_bounds(kv_desc(k), kv_desc(bounds), page_table.data_ptr(), batch, page_table.stride(0),
-                                    _ptr(begins), seq_lens.data_ptr(), hk, d, page_size, dt, kv, expected,
-                                    _ptr(device_errors), _stream_handle(stream)))
+    status = (_binding or _sparse()).page_bounds(k, bounds, page_table, begins, seq_lens, page_size, expected_tokens,
+                                                 device_errors, stream)
+    if status:
+        _check(status)
 
 
 def fdec_select_pages_workspace(batch: int, q_len: int, num_kv_heads: int, max_pages: int) -> int:
@@ -537,53 +482,24 @@ def fdec_select_pages(q, bounds, page_table, seq_lens, page_size: int, max_pages
                       device_errors=None, stream=None) -> None:
     """q [B, Q, Hq, D]; bounds [page, Hk, 2, D] of the same type; page_table int32 [B, W]; seq_lens int32 [B];
     page_ids, page_indices (or None) int32 [B * Q, Hk, budget] and counts int32 [B * Q, Hk] contiguous."""
-    b, q_len, hq, d = q.shape
-    if bounds.dtype != q.dtype or bounds.dim() != 4 or bounds.shape[2:] != (2, d):
-        raise ValueError("bounds must be [page, Hk, 2, D] of q's type")
-    hk = bounds.shape[1]
-    _int32(page_table, "page_table", 2)
-    if page_table.shape[0] != b or _int32(seq_lens, "seq_lens", 1).shape[0] != b or page_table.shape[1] < max_pages:
-        raise ValueError("page_table must be [B, >= max_pages] and seq_lens [B]")
-    for t, shape in ((page_ids, (b * q_len, hk, budget)), (counts, (b * q_len, hk)),
-                     (page_indices, (b * q_len, hk, budget))):
-        if t is not None and (tuple(_int32(t, "output", len(shape)).shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"outputs must be contiguous int32 of shape {shape}")
-    _same_device(q, bounds, page_table, seq_lens, page_ids, counts, page_indices, workspace, device_errors)
-    tok, head = _q_strides(q)
-    _check(_load().fdec_select_pages(
-        q.data_ptr(), tok, head, kv_desc(bounds), page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), b,
-        q_len, page_size, hq, hk, d, _dtype_of(q), int(bool(causal)), max_pages, budget, first_pages, last_pages,
-        page_ids.data_ptr(), counts.data_ptr(), _ptr(page_indices), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _ptr(device_errors), _stream_handle(stream)))
+    status = (_binding or _sparse()).select_pages(
+        q, bounds, page_table, seq_lens, page_size, max_pages, budget, page_ids, counts, page_indices, workspace,
+        first_pages, last_pages, causal, device_errors, stream)
+    if status:
+        _check(status)
 
 
 def fdec_run_selected(plan: Plan, q, k, v, page_ids, counts, out, lse, workspace, scale: Optional[float] = None,
                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Attention of q [N, 1, Hq, D] over page lists page_ids int32 [N, Hk, W] holding counts int32 [N, Hk] tokens;
     out [N, 1, Hq, D] float32 or of q's type, lse float32 [N, 1, Hq] or None.  The plan: batch N, q_len 1."""
-    import torch
-
-    n, hk = plan.batch, plan.meta["num_kv_heads"]
-    kd = k if isinstance(k, KVDesc) else kv_desc(k)
-    vd = v if isinstance(v, KVDesc) else kv_desc(v)
-    if not out.is_contiguous() or (lse is not None and not lse.is_contiguous()):
-        raise ValueError("out and lse must be contiguous")
-    if out.dtype not in (torch.float32, q.dtype):
-        raise ValueError(f"out must be float32 or {q.dtype}, got {out.dtype}")
-    want = {"bf16": torch.bfloat16, "f16": torch.float16}[plan.meta["dtype"]]
-    if q.dtype != want or q.shape[0] * q.shape[1] != n:
-        raise ValueError(f"this plan takes {n} query tokens of {want}")
-    if tuple(_int32(page_ids, "page_ids", 3).shape[:2]) != (n, hk) or not page_ids.is_contiguous():
-        raise ValueError("page_ids must be a contiguous int32 [N, Hk, W] tensor")
-    if tuple(_int32(counts, "counts", 2).shape) != (n, hk) or not counts.is_contiguous():
-        raise ValueError("counts must be a contiguous int32 [N, Hk] tensor")
-    tok, head = _q_strides(q)
-    sc = 1.0 / math.sqrt(plan.meta["head_dim"]) if scale is None else float(scale)
-    _check_kv_type(plan, k, v)
-    _check(_load().fdec_run_selected(
-        plan.handle, q.data_ptr(), tok, head, kd, vd, page_ids.data_ptr(), page_ids.shape[2], counts.data_ptr(), sc,
-        float(k_scale), float(v_scale), out.data_ptr(), FDEC_OUT_F32 if out.dtype == torch.float32 else FDEC_OUT_SAME,
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), _stream_handle(stream)))
+    shape = plan.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(shape[3])
+    status = (_binding or _sparse()).run_selected(plan.handle, shape, q, k, v, page_ids, counts, out, lse, workspace,
+                                                  scale, k_scale, v_scale, stream)
+    if status:
+        _check(status)
 
 
 class PageSelect:

@@ -21,6 +21,9 @@ LIB = os.path.join(PKG, "libfdec.so")
 # Benchmark helper (end-to-end steps timed from C), linked against LIB; not part of the ABI.
 E2E_SRC = os.path.join(PKG, "e2e", "e2e_loop.cu")
 E2E_LIB = os.path.join(PKG, "libfdec_e2e.so")
+# Compiled marshalling of the block-sparse entry points (host code against torch's headers).
+BINDING_SRC = os.path.join(PKG, "binding", "sparse_binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_sparse_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -64,9 +67,11 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         os.replace(obj + ".tmp", obj)
         return obj, True
 
-    n = jobs or min(len(srcs), os.cpu_count() or 4)
+    n = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=n) as ex:
+        binding = ex.submit(_build_binding, force)
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     objs = [o for o, _ in results]
     rebuilt = any(r for _, r in results)
     if rebuilt or force or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
@@ -91,6 +96,30 @@ def _build_e2e(nvcc: str, force: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"building the e2e helper failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, E2E_LIB)
+
+
+def _build_binding(force: bool) -> None:
+    """_sparse_binding.so: needs the torch it runs under (headers and libraries), no GPU."""
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(ROOT, "include", "fdec.h")))
+    if not force and os.path.exists(BINDING_LIB) and os.path.getmtime(BINDING_LIB) >= newest:
+        return
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(base, "lib")
+    tmp = BINDING_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{p}" for p in include],
+           BINDING_SRC, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the sparse binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
 
 
 if __name__ == "__main__":
