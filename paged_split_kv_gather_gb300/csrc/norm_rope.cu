@@ -9,12 +9,19 @@
 //
 // The sum of squares, the norm and the rotation are fp32 and the result is rounded
 // once, as it is stored.  HBM-bound: a token's rows are read once and written once.
-// A row of D elements is held by D/8 lanes (16 bytes each; 3 or 2 chunks per lane at
-// head_dim 192 and 512), so a load instruction of a warp covers up to four whole rows
-// and the sum of squares is a shuffle among the lanes of a row.
+// A lane holds two 16-byte chunks of a row, those whose elements rotate together (c and
+// c + rot/16; chunks past rot pair up among themselves), so nothing but the sum of
+// squares crosses lanes, and weight x cosine, weight x sine are computed once a token
+// and kept for its rows: a row then costs two packed products and a scaling per
+// element pair.  (The first form, one chunk a lane with the partner's chunk, weight and
+// angle read again for every row, was bound by instructions.)  GB300, 32768 tokens of
+// 32/8 heads of 128 (822 MB): 141 us, 5.8 TB/s, 0.86 of the measured copy bandwidth; the
+// first form 269 us.  One token: 2.8 us a call in a stream, which is launch and three
+// dependent reads (position, page id, angle).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -27,171 +34,240 @@ namespace fdec {
 namespace {
 
 constexpr int kRowsThreads = 256;
+constexpr int kRowsCtas = 2;  // an SM: 128 registers a thread
 
 template <int D>
 struct RowLanes {
-    static constexpr int CHUNKS = D / 8;
-    static constexpr int LPR = D == 192 ? 8 : (CHUNKS > 32 ? 32 : CHUNKS);  // lanes per row
-    static constexpr int CPL = CHUNKS / LPR;                                // chunks per lane
-    static constexpr int RPW = 32 / LPR;                                    // rows per warp
+    static constexpr int PAIRS = D / 16;                                          // chunk pairs of a row
+    static constexpr int LPR = PAIRS <= 4 ? 4 : PAIRS <= 8 ? 8 : PAIRS <= 16 ? 16 : 32;  // lanes per row
+    static constexpr int RPW = 32 / LPR;                                          // rows per warp
 };
 
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void unpack8(const uint4& w, float2 (&x)[4]) {
+    x[0] = unpack2<BF16>(w.x);
+    x[1] = unpack2<BF16>(w.y);
+    x[2] = unpack2<BF16>(w.z);
+    x[3] = unpack2<BF16>(w.w);
+}
+
+// Eight values rounded to E4M3 codes (saturating at 448).
+__device__ __forceinline__ uint2 codes8(const float2 (&x)[4]) {
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<BF16>(v[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+    for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(x[i], __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// One lane's coefficients for the q rows or the k rows of a token: output chunk 0 is
+// x0 a0 + m0 b0 and chunk 1 is x1 a1 + m1 b1, with m the other element of each pair.
+struct Coef {
+    float2 a0[4], b0[4], a1[4], b1[4];
+};
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void make_coef(Coef& f, const uint16_t* weight, const float* cs, int half, int c0, int c1,
+                                          bool rotated, float factor) {
+    float2 w0[4], w1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w0[k] = w1[k] = make_float2(1.f, 1.f);
+    if (weight != nullptr) {
+        unpack8<BF16>(*reinterpret_cast<const uint4*>(weight + 8 * c0), w0);
+        unpack8<BF16>(*reinterpret_cast<const uint4*>(weight + 8 * c1), w1);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w0[k].x *= factor, w0[k].y *= factor, w1[k].x *= factor, w1[k].y *= factor;
+        f.a0[k] = w0[k], f.a1[k] = w1[k];
+        f.b0[k] = f.b1[k] = make_float2(0.f, 0.f);
+    }
+    if (!rotated) return;
+    if constexpr (INTER) {  // pairs within a chunk: four angles each
+        const float4 p0 = *reinterpret_cast<const float4*>(cs + 4 * c0), q0 = *reinterpret_cast<const float4*>(cs + half + 4 * c0);
+        const float4 p1 = *reinterpret_cast<const float4*>(cs + 4 * c1), q1 = *reinterpret_cast<const float4*>(cs + half + 4 * c1);
+        const float cc0[4] = {p0.x, p0.y, p0.z, p0.w}, ss0[4] = {q0.x, q0.y, q0.z, q0.w};
+        const float cc1[4] = {p1.x, p1.y, p1.z, p1.w}, ss1[4] = {q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f.a0[k] = make_float2(w0[k].x * cc0[k], w0[k].y * cc0[k]);
+            f.b0[k] = make_float2(-w0[k].y * ss0[k], w0[k].x * ss0[k]);
+            f.a1[k] = make_float2(w1[k].x * cc1[k], w1[k].y * cc1[k]);
+            f.b1[k] = make_float2(-w1[k].y * ss1[k], w1[k].x * ss1[k]);
+        }
+    } else {  // element e of chunk 0 with element e of chunk 1: eight angles
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            const float4 p = *reinterpret_cast<const float4*>(cs + 8 * c0 + 4 * k2);
+            const float4 q = *reinterpret_cast<const float4*>(cs + half + 8 * c0 + 4 * k2);
+            const float2 cc[2] = {make_float2(p.x, p.y), make_float2(p.z, p.w)};
+            const float2 ss[2] = {make_float2(q.x, q.y), make_float2(q.z, q.w)};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int k = 2 * k2 + y;
+                f.a0[k] = make_float2(w0[k].x * cc[y].x, w0[k].y * cc[y].y);
+                f.b0[k] = make_float2(-w1[k].x * ss[y].x, -w1[k].y * ss[y].y);
+                f.a1[k] = make_float2(w1[k].x * cc[y].x, w1[k].y * cc[y].y);
+                f.b1[k] = make_float2(w0[k].x * ss[y].x, w0[k].y * ss[y].y);
+            }
+        }
     }
 }
 
-// Eight values divided by the scale and rounded to E4M3 codes (saturating at 448).
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const __nv_fp8x2_storage_t c =
-            __nv_cvt_float2_to_fp8x2(make_float2(x[i] / scale, x[i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-        w[i >> 2] |= static_cast<uint32_t>(c) << (8 * (i & 3));
-    }
-    return make_uint2(w[0], w[1]);
-}
-
-template <int D, bool BF16, bool KV8, bool PAIRS>
-__global__ void __launch_bounds__(kRowsThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int wpt) {
+// U: row groups a warp loads at once, the next U while it computes these.
+template <int D, bool BF16, bool KV8, bool INTER, int U>
+__global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int wpt) {
     using R = RowLanes<D>;
-    constexpr int CPL = R::CPL, LPR = R::LPR, RPW = R::RPW;
+    constexpr int LPR = R::LPR, RPW = R::RPW;
     const int lane = threadIdx.x & 31;
     const int sub = lane / LPR, l = lane - sub * LPR;
     const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int rows = p.hq + 2 * p.hk;
-    const int groups = (rows + RPW - 1) / RPW;
+    const int64_t n_work = static_cast<int64_t>(p.n_tokens) * wpt;
     const int half = p.rot / 2;
     const int page_mask = (1 << p.page_shift) - 1;
+    const bool on = l < R::PAIRS;  // head_dim 192 leaves 4 of 16 lanes idle
+    const int n_rot = p.rot / 16;  // chunk pairs that rotate
+    const bool rotated = l < n_rot;
+    const int c0 = rotated ? l : n_rot + l;
+    const int c1 = rotated ? l + n_rot : c0 + (D / 16 - n_rot);
+    // Row groups of the q, k and v rows; a warp takes every wpt-th over all three.
+    const int groups_q = (p.hq + RPW - 1) / RPW, groups_kv = (p.hk + RPW - 1) / RPW;
 
     // A programmatic dependent of the kernel before it on the stream (the projection):
     // nothing is read or written before that kernel has completed.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    for (int64_t w = warp0; w < static_cast<int64_t>(p.n_tokens) * wpt; w += nwarps) {
+    int b_next = 0, t_next = 0, rt_next = 0;
+    auto fetch = [&](int64_t w) {
+        if (w >= n_work) return;
+        const int64_t i = w / wpt;
+        b_next = p.batch_indices[i];
+        t_next = p.positions[i];
+        rt_next = p.rope_positions != nullptr ? p.rope_positions[i] : t_next;
+    };
+    fetch(warp0);
+    for (int64_t w = warp0; w < n_work; w += nwarps) {
         const int64_t i = w / wpt;
         const int part = static_cast<int>(w - i * wpt);
-        const int b = p.batch_indices[i];
-        const int t = p.positions[i];
-        const int rt = p.rope_positions != nullptr ? p.rope_positions[i] : t;
+        const int b = b_next, t = t_next, rt = rt_next;
+        fetch(w + nwarps);
         const int pi = t >> p.page_shift;
         if (t < 0 || pi >= p.pt_stride || b < 0 || b >= p.batch || (p.rot > 0 && (rt < 0 || rt >= p.cos_rows))) {
             if (lane == 0 && part == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
             continue;
         }
         const int page = p.page_table[static_cast<int64_t>(b) * p.pt_stride + pi];
-        if (page < 0 || page >= p.k_pages || page >= p.v_pages) {
+        // Not waited for here: the query rows' loads do not depend on it, only what is stored.
+        const bool page_ok = page >= 0 && page < p.k_pages && page < p.v_pages;
+        const int64_t slot = t & page_mask;
+        const float* cs = p.cos_sin + static_cast<int64_t>(rt) * p.rot;
+        // this warp's first group of the kind whose groups start at `from`
+        auto first_group = [&](int from) {
+            const int back = part - from;
+            return back >= 0 ? back : back + (-back + wpt - 1) / wpt * wpt;
+        };
+        // The q rows or the k rows: norm and rotation of rows h < heads at src + h * src_h.
+        auto normed = [&](const uint8_t* src, int64_t src_h, uint8_t* dst, int64_t dst_h, int heads, int from, int groups,
+                          const uint16_t* weight, float factor, auto codes) {
+            constexpr bool CODES = decltype(codes)::value;
+            int g = first_group(from);
+            if (g >= groups) return;
+            uint4 r0[U], r1[U], n0[U], n1[U];
+            auto load = [&](int at, uint4 (&a)[U], uint4 (&c)[U]) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = (at + u * wpt) * RPW + sub;
+                    a[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (on && h < heads) {
+                        a[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c0);
+                        c[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c1);
+                    }
+                }
+            };
+            load(g, r0, r1);
+            Coef f;
+            if (on) make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated, factor);
+            for (; g < groups; g += U * wpt) {
+                // (a lane stores only chunks that it has loaded itself, so q_out may be q)
+                load(g + U * wpt, n0, n1);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float2 x0[4], x1[4];
+                    unpack8<BF16>(r0[u], x0);
+                    unpack8<BF16>(r1[u], x1);
+                    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s2 = __ffma2_rn(x1[k], x1[k], __ffma2_rn(x0[k], x0[k], s2));
+                    float sum = s2.x + s2.y;
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    const float rs = rsqrtf(sum * (1.f / D) + p.eps);
+                    const float2 rs2 = make_float2(rs, rs);
+                    float2 y0[4], y1[4];
+                    if (rotated) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 m0 = INTER ? make_float2(x0[k].y, x0[k].x) : x1[k];
+                            const float2 m1 = INTER ? make_float2(x1[k].y, x1[k].x) : x0[k];
+                            y0[k] = __fmul2_rn(__ffma2_rn(x0[k], f.a0[k], __fmul2_rn(m0, f.b0[k])), rs2);
+                            y1[k] = __fmul2_rn(__ffma2_rn(x1[k], f.a1[k], __fmul2_rn(m1, f.b1[k])), rs2);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            y0[k] = __fmul2_rn(__fmul2_rn(x0[k], f.a0[k]), rs2);
+                            y1[k] = __fmul2_rn(__fmul2_rn(x1[k], f.a1[k]), rs2);
+                        }
+                    }
+                    const int h = (g + u * wpt) * RPW + sub;
+                    if (!on || h >= heads || !page_ok) continue;
+                    uint8_t* to = dst + h * dst_h;
+                    if constexpr (CODES) {
+                        *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(y0);
+                        *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(y1);
+                    } else {
+                        *reinterpret_cast<uint4*>(to + 16 * c0) =
+                            make_uint4(pack2<BF16>(y0[0].x, y0[0].y), pack2<BF16>(y0[1].x, y0[1].y),
+                                       pack2<BF16>(y0[2].x, y0[2].y), pack2<BF16>(y0[3].x, y0[3].y));
+                        *reinterpret_cast<uint4*>(to + 16 * c1) =
+                            make_uint4(pack2<BF16>(y1[0].x, y1[0].y), pack2<BF16>(y1[1].x, y1[1].y),
+                                       pack2<BF16>(y1[2].x, y1[2].y), pack2<BF16>(y1[3].x, y1[3].y));
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) r0[u] = n0[u], r1[u] = n1[u];
+            }
+        };
+        normed(p.q + i * p.q_st, p.q_sh, p.q_out + i * p.q_out_st, p.q_out_sh, p.hq, 0, groups_q, p.q_weight, 1.f,
+               std::false_type{});
+        normed(p.k_new + i * p.k_new_st, p.k_new_sh, p.k_base + page * p.k_sp + slot * p.k_st, p.k_sh, p.hk, groups_q,
+               groups_kv, p.k_weight, p.k_inv, std::bool_constant<KV8>{});
+        if (!page_ok) {
             if (lane == 0 && part == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
             continue;
         }
-        const int64_t slot = t & page_mask;
-        const float* cs = p.cos_sin + static_cast<int64_t>(rt) * p.rot;
-        for (int g = part; g < groups; g += wpt) {
-            const int r = g * RPW + sub;
-            const bool live = r < rows;
-            const int kind = r < p.hq ? 0 : (r < p.hq + p.hk ? 1 : 2);  // q, k or v row
-            const int h = kind == 0 ? r : (kind == 1 ? r - p.hq : r - p.hq - p.hk);
-            const uint8_t* src = kind == 0 ? p.q + i * p.q_st + h * p.q_sh
-                                           : (kind == 1 ? p.k_new + i * p.k_new_st + h * p.k_new_sh
-                                                        : p.v_new + i * p.v_new_st + h * p.v_new_sh);
-            const uint16_t* weight = kind == 0 ? p.q_weight : p.k_weight;
-            uint4 raw[CPL], mate[CPL];
-            float sum = 0.f;
+        // The v rows: as they are, or scaled and rounded to codes.
+        const uint8_t* src = p.v_new + i * p.v_new_st;
+        uint8_t* dst = p.v_base + page * p.v_sp + slot * p.v_st;
+        for (int g = first_group(groups_q + groups_kv); g < groups_kv; g += wpt) {
+            const int h = g * RPW + sub;
+            if (!on || h >= p.hk) continue;
+            const uint4 r0 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c0);
+            const uint4 r1 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c1);
+            uint8_t* to = dst + h * p.v_sh;
+            if constexpr (KV8) {
+                const float2 inv = make_float2(p.v_inv, p.v_inv);
+                float2 x0[4], x1[4];
+                unpack8<BF16>(r0, x0);
+                unpack8<BF16>(r1, x1);
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const int e0 = 8 * (l + LPR * j);
-                raw[j] = mate[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (live) {
-                    raw[j] = *reinterpret_cast<const uint4*>(src + 2 * e0);
-                    // the other half of this chunk's pairs (rot / 2 is a multiple of 8)
-                    if (!PAIRS && kind < 2 && e0 < p.rot)
-                        mate[j] = *reinterpret_cast<const uint4*>(src + 2 * (e0 < half ? e0 + half : e0 - half));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                float x[8];
-                unpack8<BF16>(raw[j], x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-            }
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float rs = rsqrtf(sum * (1.f / D) + p.eps);
-            __syncwarp();  // every lane has read its row (q_out may be q)
-            if (!live) continue;
-            uint8_t* dst = kind == 0 ? p.q_out + i * p.q_out_st + h * p.q_out_sh
-                                     : (kind == 1 ? p.k_base + page * p.k_sp + h * p.k_sh + slot * p.k_st
-                                                  : p.v_base + page * p.v_sp + h * p.v_sh + slot * p.v_st);
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const int e0 = 8 * (l + LPR * j);
-                if (kind == 2) {
-                    if constexpr (KV8) {
-                        float x[8];
-                        unpack8<BF16>(raw[j], x);
-                        *reinterpret_cast<uint2*>(dst + e0) = codes8(x, p.v_scale);
-                    } else {
-                        *reinterpret_cast<uint4*>(dst + 2 * e0) = raw[j];
-                    }
-                    continue;
-                }
-                float x[8], wt[8];
-                unpack8<BF16>(raw[j], x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) wt[e] = 1.f;
-                if (weight != nullptr) unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(weight + e0)), wt);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= rs * wt[e];
-                if (e0 < p.rot) {
-                    if constexpr (PAIRS) {
-                        const float4 c = *reinterpret_cast<const float4*>(cs + e0 / 2);
-                        const float4 s = *reinterpret_cast<const float4*>(cs + half + e0 / 2);
-                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = x[2 * e], bb = x[2 * e + 1];
-                            x[2 * e] = a * cc[e] - bb * ss[e];
-                            x[2 * e + 1] = bb * cc[e] + a * ss[e];
-                        }
-                    } else {
-                        const int f0 = e0 < half ? e0 : e0 - half;  // index of the pairs
-                        const float sign = e0 < half ? -1.f : 1.f;
-                        float m[8];
-                        unpack8<BF16>(mate[j], m);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) wt[e] = 1.f;
-                        if (weight != nullptr)
-                            unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(weight + (e0 < half ? e0 + half : f0))), wt);
-#pragma unroll
-                        for (int q4 = 0; q4 < 2; ++q4) {
-                            const float4 c = *reinterpret_cast<const float4*>(cs + f0 + 4 * q4);
-                            const float4 s = *reinterpret_cast<const float4*>(cs + half + f0 + 4 * q4);
-                            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int k = 4 * q4 + e;
-                                x[k] = x[k] * cc[e] + sign * (m[k] * (rs * wt[k])) * ss[e];
-                            }
-                        }
-                    }
-                }
-                if (KV8 && kind == 1) {
-                    *reinterpret_cast<uint2*>(dst + e0) = codes8(x, p.k_scale);
-                } else {
-                    *reinterpret_cast<uint4*>(dst + 2 * e0) =
-                        make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
-                                   pack2<BF16>(x[6], x[7]));
-                }
+                for (int k = 0; k < 4; ++k) x0[k] = __fmul2_rn(x0[k], inv), x1[k] = __fmul2_rn(x1[k], inv);
+                *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(x0);
+                *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(x1);
+            } else {
+                *reinterpret_cast<uint4*>(to + 16 * c0) = r0;
+                *reinterpret_cast<uint4*>(to + 16 * c1) = r1;
             }
         }
     }
@@ -200,16 +276,20 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_kernel(const __grid_co
 template <int D, bool BF16, bool KV8>
 cudaError_t launch_rows(const NormRopeParams& p, bool pairs, int num_sms, cudaStream_t s) {
     using R = RowLanes<D>;
-    const int groups = (p.hq + 2 * p.hk + R::RPW - 1) / R::RPW;
-    const int64_t full_warps = static_cast<int64_t>(num_sms) * 8 * (kRowsThreads / 32);
-    // Warps per token: one while the tokens alone fill the machine, else enough that
-    // they do (a warp then takes every wpt-th group of rows).
+    const int groups = (p.hq + R::RPW - 1) / R::RPW + 2 * ((p.hk + R::RPW - 1) / R::RPW);
+    const int64_t slots = static_cast<int64_t>(num_sms) * kRowsCtas * (kRowsThreads / 32);
+    // Warps per token: one while the tokens alone take half of the machine's warps, else
+    // enough that they do (a warp then takes every wpt-th group of rows, and computes the
+    // token's coefficients again: 2036 tokens take 12.6 us with one warp each, 14.5 with two).
     int wpt = 1;
-    while (wpt < groups && static_cast<int64_t>(p.n_tokens) * wpt < full_warps) wpt *= 2;
+    while (wpt < groups && static_cast<int64_t>(p.n_tokens) * wpt * 2 <= slots) wpt *= 2;
     wpt = std::min(wpt, groups);
+    // A warp has two groups at most: the form without loads ahead is shorter code, which a
+    // call of a few tokens mostly waits to fetch (64 tokens: 3.2 against 3.6 us).
+    const bool single = groups <= 2 * wpt;
     const int64_t warps = static_cast<int64_t>(p.n_tokens) * wpt;
     const int64_t blocks =
-        std::min<int64_t>((warps * 32 + kRowsThreads - 1) / kRowsThreads, static_cast<int64_t>(num_sms) * 8);
+        std::min<int64_t>((warps * 32 + kRowsThreads - 1) / kRowsThreads, static_cast<int64_t>(num_sms) * kRowsCtas);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
     cfg.blockDim = dim3(kRowsThreads, 1, 1);
@@ -219,8 +299,11 @@ cudaError_t launch_rows(const NormRopeParams& p, bool pairs, int num_sms, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true>, p, wpt)
-                 : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false>, p, wpt);
+    if (single)
+        return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true, 1>, p, wpt)
+                     : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false, 1>, p, wpt);
+    return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true, 2>, p, wpt)
+                 : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false, 2>, p, wpt);
 }
 
 template <int D>

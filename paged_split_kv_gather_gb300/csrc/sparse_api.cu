@@ -86,9 +86,10 @@ fdec_status fdec_norm_rope_append(fdec_rows q, fdec_rows k_new, fdec_rows v_new,
     if (rot_dim > 0 && (cos_sin == nullptr || cos_sin_rows < 1))
         return fail(FDEC_ERR_INVALID_ARG, "rot_dim > 0 needs a cos_sin table");
     const bool kv8 = kv_dtype == FDEC_KV_E4M3;
-    if (kv8 ? !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f)
-            : (k_scale != 1.f || v_scale != 1.f))
-        return fail(FDEC_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0 (and 1 for a 16-bit cache)");
+    const auto scale_ok = [](float x) { return x > 0.f && std::isfinite(x) && std::isfinite(1.f / x); };
+    if (kv8 ? !scale_ok(k_scale) || !scale_ok(v_scale) : (k_scale != 1.f || v_scale != 1.f))
+        return fail(FDEC_ERR_INVALID_ARG,
+                    "k_scale and v_scale must be > 0 with a finite reciprocal (and 1 for a 16-bit cache)");
     if (n_tokens == 0) return FDEC_OK;
     if (batch_indices == nullptr || positions == nullptr || page_table == nullptr)
         return fail(FDEC_ERR_INVALID_ARG, "null batch_indices, positions or page_table");
@@ -146,8 +147,10 @@ fdec_status fdec_norm_rope_append(fdec_rows q, fdec_rows k_new, fdec_rows v_new,
     p.page_shift = page_shift_of(page_size);
     p.rot = rot_dim;
     p.eps = eps;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
+    // The division by a scale is one by its reciprocal, rounded: the codes' own step is
+    // 2^19 of those roundings.
+    p.k_inv = 1.f / k_scale;
+    p.v_inv = 1.f / v_scale;
     int num_sms = 0;
     cudaError_t e = current_num_sms(&num_sms);
     if (e == cudaSuccess) e = launch_norm_rope(p, head_dim, dtype == FDEC_BF16, kv8, interleaved != 0, num_sms, stream);
