@@ -159,6 +159,11 @@ struct fdec_plan_s {
     int path = FDEC_PATH_SIMT;
     bool persistent = false;  // MMA path over 16-bit caches: resident CTAs take work units
     int n_units = 0, persist_grid = 0;
+    // Shares of fdec_run_selected (SplitParams::shares): their grid (0: planned items) and
+    // regions, behind the rest of the workspace (base_ws_bytes), which is all that the
+    // other entry points use.
+    int share_grid = 0, share_cap = -1;
+    size_t off_share_rec = 0, off_share_o = 0, off_share_ml = 0, base_ws_bytes = 0;
     int rc = 1, row_groups = 1;
     int blocks_per_split = 1, fanin = 64, num_sms = 0, ctas_per_sm = 1;
     int max_pages_needed = 0;  // max_b ceil(capacity_b / page_size)
@@ -598,6 +603,24 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
     off = align_up(off + per_slot_o * p->slots_b);
     p->off_b_ml = off;
     off = align_up(off + per_slot_ml * p->slots_b);
+    p->base_ws_bytes = off;
+    // Every producer warp passes over all lists' lengths to find its share: up to 4096 of
+    // them, 128 a lane.
+    if (p->persistent && q_len == 1 && static_cast<long long>(batch) * num_kv_heads <= 4096) {
+        long long blocks = 0;
+        for (int nb : nblocks) blocks += nb;
+        blocks *= static_cast<long long>(num_kv_heads) * p->row_groups;
+        p->share_grid = static_cast<int>(std::min<long long>(blocks, static_cast<long long>(num_sms) * p->ctas_per_sm));
+        p->share_cap = std::all_of(p->capacity.begin(), p->capacity.end(), [&](int32_t c) { return c == p->capacity[0]; })
+                           ? p->capacity[0]
+                           : -1;
+        p->off_share_rec = off;
+        off = align_up(off + sizeof(int2) * batch * num_kv_heads * p->row_groups);
+        p->off_share_o = off;
+        off = align_up(off + sizeof(float) * 2 * p->share_grid * kMmaRows * head_dim);
+        p->off_share_ml = off;
+        off = align_up(off + sizeof(float2) * 2 * p->share_grid * kMmaRows);
+    }
     p->ws_bytes = off;
 
     p->meta.assign(p->meta_bytes, 0);
@@ -801,6 +824,40 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
                                 (q_stride_head * 2) % 16 == 0;
     const dim3 grid(static_cast<unsigned>(p->items.size()), static_cast<unsigned>(p->hk),
                     static_cast<unsigned>(p->row_groups));
+    const bool shares = per_head && p->share_grid > 0 && q_rows_aligned;
+    sp.shares = shares ? 1 : 0;
+    sp.n_lists = p->batch * p->hk;
+    sp.share_cap = p->share_cap;
+    sp.share_rec = reinterpret_cast<int2*>(ws + p->off_share_rec);
+    sp.share_o = reinterpret_cast<float*>(ws + p->off_share_o);
+    sp.share_ml = reinterpret_cast<float2*>(ws + p->off_share_ml);
+    if (shares) {
+        cudaError_t e = launch_split_mma_persist(sp, p->tmap_k, p->tmap_v, p->head_dim, p->dtype == FDEC_BF16,
+                                                 dim3(static_cast<unsigned>(p->share_grid), 1, 1), stream, true);
+        if (e != cudaSuccess) return fail_cuda(e, "launching the split kernel");
+        if (p->split_event != nullptr) {
+            e = cudaEventRecord(p->split_event, stream);
+            if (e != cudaSuccess) return fail_cuda(e, "recording the split event");
+        }
+        ShareMergeParams mp;
+        mp.rec = sp.share_rec;
+        mp.o = sp.share_o;
+        mp.ml = sp.share_ml;
+        mp.out = out;
+        mp.lse = lse;
+        mp.out_type = out_type;
+        mp.hk = p->hk;
+        mp.rows = p->rows;
+        mp.group = p->group;
+        mp.hq = p->hq;
+        mp.head_dim = p->head_dim;
+        mp.units = p->batch * p->hk * p->row_groups;
+        mp.row_groups = p->row_groups;
+        mp.grid = p->share_grid;
+        e = launch_share_merge(mp, stream);
+        if (e != cudaSuccess) return fail_cuda(e, "launching the merge of the shares");
+        return FDEC_OK;
+    }
     cudaError_t e = dispatch_split(p, sp, grid, stream, true, p->persistent && q_rows_aligned);
     if (e != cudaSuccess) return fail_cuda(e, "launching the split kernel");
     if (p->split_event != nullptr) {
@@ -1043,8 +1100,8 @@ extern "C" fdec_status fdec_run_static_workspace(fdec_plan_t p, const void* q, i
                                                  const int32_t* seq_lens_dev, float scale, float* out, float* lse,
                                                  cudaStream_t stream) {
     if (p == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null plan");
-    if (p->ws_bytes > kStaticWorkspaceBytes)
-        return fail(FDEC_ERR_WORKSPACE, "this plan needs " + std::to_string(p->ws_bytes) +
+    if (p->base_ws_bytes > kStaticWorkspaceBytes)
+        return fail(FDEC_ERR_WORKSPACE, "this plan needs " + std::to_string(p->base_ws_bytes) +
                                             " bytes of workspace but the built-in array holds " +
                                             std::to_string(kStaticWorkspaceBytes) +
                                             "; use fdec_run with a workspace of your own");

@@ -73,6 +73,15 @@ struct SplitParams {
     // ticket counter (advanced by exactly n_units per launch).
     int n_units;
     unsigned long long* ticket;
+    // Shares (fdec_run_selected): instead of planned items, CTA c takes the c-th of grid
+    // equal runs of the 64-token blocks that the lists hold at run time (see
+    // split_persist_kernel.cuh).  0: planned items.
+    int shares;
+    int n_lists;               // batch x hk
+    int share_cap;             // the capacity of every sequence if they are equal, else -1
+    int2* share_rec;           // [n_lists x row groups] first and last CTA of each unit
+    float* share_o;            // [2 grid][16][D] partials: 2 c: a unit begun before CTA c, 2 c + 1: one that goes on
+    float2* share_ml;          // [2 grid][16]
     // One sequence (batch 1): its work items are runs of seq1_bps blocks in order, so
     // a unit's item follows from its index with no table read (0: read the table).
     int seq1_bps, seq1_blocks, seq1_capacity;
@@ -154,6 +163,17 @@ constexpr int kTcStageTokens = 64;
 size_t split_smem_bytes(int head_dim, int rc);
 int split_threads(int head_dim);
 int split_max_rc(int head_dim);
+
+// Merge of the units that shares have cut (SplitParams::shares): after the split launch.
+struct ShareMergeParams {
+    const int2* rec;
+    const float* o;            // [2 grid][16][D]
+    const float2* ml;          // [2 grid][16]
+    float* out;
+    float* lse;                // or null
+    int out_type, hk, rows, group, hq, head_dim, units, row_groups, grid;
+};
+cudaError_t launch_share_merge(const ShareMergeParams& p, cudaStream_t s);
 
 int reduce_warps_per_unit(int max_count);
 cudaError_t launch_reduce(const ReduceParams& p, int num_tasks, cudaStream_t s);

@@ -135,6 +135,106 @@ __global__ void __launch_bounds__(kReduceWarps * 32, 5) reduce_kernel(const Redu
     }
 }
 
+// Join the parts of the units that shares have cut (SplitParams::shares).  One CTA per
+// unit and row: a unit within one CTA's share is finished already and its CTA returns at
+// once; else the warps stride over the parts, each lane holding D / 32 elements, and are
+// merged in shared memory in warp order.  Parts of a unit: slot 2 c + 1 of its first CTA,
+// then slot 2 c of every later one.
+template <int EPL>  // elements a lane: head_dim / 32
+__global__ void __launch_bounds__(kReduceWarps * 32) share_merge_kernel(const ShareMergeParams p) {
+    constexpr float kLn2 = 0.69314718055994530942f;
+    constexpr int D = EPL * 32;
+    constexpr int U = EPL <= 4 ? 4 : 2;  // parts in flight a warp
+    __shared__ float s_o[kReduceWarps][D];
+    __shared__ float2 s_ml[kReduceWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x, r = blockIdx.y;
+    const int list = unit / p.row_groups, row = (unit - list * p.row_groups) * 16 + r;
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 c = p.rec[unit];
+    const int parts = c.y - c.x + 1;
+    // (a record outside the grid: the split kernel gave up on a wait and wrote none)
+    if (parts <= 1 || c.x < 0 || c.y >= p.grid || row >= p.rows) return;
+    float m = -INFINITY, l = 0.f, acc[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    for (int k0 = warp; k0 < parts; k0 += kReduceWarps * U) {
+        float2 ml[U];
+        float o[U][EPL];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * kReduceWarps;
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) o[u][e] = 0.f;
+            if (k < parts) {
+                const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c.x + 1 : 2 * (c.x + k)) * 16 + r;
+                ml[u] = p.ml[at];
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) o[u][e] = p.o[at * D + e * 32 + lane];
+            }
+        }
+        float mx = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+        if (mx == -INFINITY) continue;
+        const float a = exp2_approx(m - mx);  // 0 while m is -inf
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] *= a;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = ml[u].x == -INFINITY ? 0.f : exp2_approx(ml[u].x - mx);
+            l += w * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) acc[e] += w * o[u][e];
+        }
+        m = mx;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_o[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    float M = -INFINITY, Ls = 0.f, w[kReduceWarps];
+#pragma unroll
+    for (int x = 0; x < kReduceWarps; ++x) M = fmaxf(M, s_ml[x].x);
+#pragma unroll
+    for (int x = 0; x < kReduceWarps; ++x) {
+        w[x] = s_ml[x].x == -INFINITY ? 0.f : exp2_approx(s_ml[x].x - M);
+        Ls += w[x] * s_ml[x].y;
+    }
+    const int seq = list / p.hk, h = (list - seq * p.hk) * p.group + row;  // q_len is 1
+    const int64_t orow = static_cast<int64_t>(seq) * p.hq + h;
+    for (int d = threadIdx.x; d < D; d += kReduceWarps * 32) {
+        float o = 0.f;
+#pragma unroll
+        for (int x = 0; x < kReduceWarps; ++x) o += w[x] * s_o[x][d];
+        store_out1(p.out, p.out_type, orow * D + d, Ls > 0.f ? o / Ls : 0.f);
+    }
+    if (threadIdx.x == 0 && p.lse != nullptr) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+}
+
+cudaError_t launch_share_merge(const ShareMergeParams& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.units), static_cast<unsigned>(p.rows < 16 ? p.rows : 16), 1);
+    cfg.blockDim = dim3(kReduceWarps * 32, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (p.head_dim) {
+        case 64: return cudaLaunchKernelEx(&cfg, share_merge_kernel<2>, p);
+        case 128: return cudaLaunchKernelEx(&cfg, share_merge_kernel<4>, p);
+        case 192: return cudaLaunchKernelEx(&cfg, share_merge_kernel<6>, p);
+        case 256: return cudaLaunchKernelEx(&cfg, share_merge_kernel<8>, p);
+        case 512: return cudaLaunchKernelEx(&cfg, share_merge_kernel<16>, p);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
 // Warps per unit for tasks of up to `max_count` partials: enough that each warp
 // takes at most kReducePerWarp (one round trip), at most all of the CTA's.
 int reduce_warps_per_unit(int max_count) {

@@ -33,6 +33,15 @@
 //     buffers; a tag per ring slot names the unit buffer and j (2 j + buffer).  The next unit's
 //     ticket, work item, length and first page ids are fetched while the last
 //     three stages of the current unit are issued.
+//   Shares: where the lengths are known only to the device and differ (the page lists of
+//     block-sparse decoding), planned items leave CTAs idle: a batch of 64 ragged lists of
+//     up to 2048 tokens took 72-78 us for 333 MB.  With p.shares the units are the lists
+//     themselves (x row groups), their blocks are numbered through, and CTA c streams the
+//     c-th of grid equal runs of them.  The producer finds its run from the
+//     lists' lengths (one pass of the warp over them); a unit counts kUnitCost blocks more
+//     than it has.  A unit that one CTA covers is
+//     finished there; the others' parts go to two slots per CTA and share_merge_kernel
+//     (reduce.cu) joins them in order, so results still depend on the lengths alone.
 //   - a consumer warp resets its state at its first stage of a unit and, at its
 //     last, writes its (m, l, O) into that stage's slot (kept, not released) and
 //     counts itself in; the third warp to arrive merges the three states, writes
@@ -153,12 +162,104 @@ __device__ __forceinline__ int punit_box_page(const SplitParams& p, const PUnit&
     return (t < u.it.z * kBlockTokens && (t >> p.page_shift) < p.pt_stride) ? __ldg(pt + (t >> p.page_shift)) : -1;
 }
 
+// What a unit costs besides its blocks (its queries, its padding stages, its merge, the
+// pipeline's hand-over), in blocks: shares are cut by blocks + kUnitCost a unit.  Measured
+// on 64 x 8 lists, every second of 2048 tokens and the others of 64: 54 us, counting 0
+// blocks 74, 1 block 66, 2 blocks 59, 6 blocks 56.
+constexpr int kUnitCost = 3;
+
+// Blocks of list x (sequence x / hk, KV head x % hk), at least one: an empty list's unit
+// writes its empty result.
+__device__ __forceinline__ int list_cap(const SplitParams& p, int x) {
+    return p.share_cap >= 0 ? p.share_cap : __ldg(p.capacity + x / p.hk);
+}
+__device__ __forceinline__ int blocks_of(int L, int cap) {
+    return max(1, (max(0, min(L, cap)) + kBlockTokens - 1) / kBlockTokens);
+}
+
+// A CTA's share.  Every unit has blocks + kUnitCost positions, numbered through; CTA c has
+// those from c total / grid.  Position kUnitCost + b of a unit stands for its block b, the
+// positions before for its block 0: so consecutive CTAs continue a unit where the last
+// one stops, and a CTA whose positions are all in front of one block has nothing.
+struct Share {
+    int64_t start;  // first position of the current unit
+    int64_t end;    // end of the share
+    int64_t total;  // positions of all units
+    int grid;       // CTAs that take part: all, or as many as there are positions
+};
+
+// This CTA's part of unit u.unit, from its block `begin`, as a work item: its slot is -1
+// (the whole unit) or one of this CTA's two.  Empty: it.y == it.z.
+__device__ __forceinline__ void share_item(PUnit& u, const Share& sh, int begin, int upi) {
+    const int nb = blocks_of(u.L0, u.cap);
+    const int64_t left = sh.end - sh.start;  // positions from the unit's first to the share's end
+    const int end = left >= nb + kUnitCost ? nb : max(0, static_cast<int>(left) - kUnitCost);
+    const int c = blockIdx.x;
+    u.it = make_int4(u.unit / upi, begin, end, begin > 0 ? 2 * c : (end < nb ? 2 * c + 1 : -1));
+}
+
+// Find this CTA's share and its first part (the producer warp).
+__device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Share& sh, int lane) {
+    const int rgc = (p.rows + 15) / 16;
+    const int upi = p.hk * rgc;
+    const int seg = (p.n_lists + 31) / 32;  // lists of one lane
+    const int x0 = lane * seg, x1 = min(x0 + seg, p.n_lists);
+    int64_t mine = 0;
+#pragma unroll 8
+    for (int x = x0; x < x1; ++x) mine += blocks_of(__ldg(p.seq_lens + x), list_cap(p, x)) + kUnitCost;
+    mine *= rgc;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    sh.total = __shfl_sync(0xffffffffu, upto, 31);
+    sh.grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
+    u.unit = -1;
+    if (static_cast<int>(blockIdx.x) >= sh.grid) return;
+    const int64_t pos = sh.total * blockIdx.x / sh.grid;
+    sh.end = sh.total * (blockIdx.x + 1) / sh.grid;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > pos)) - 1;
+    int64_t before = __shfl_sync(0xffffffffu, upto - mine, owner);
+    const int owner_end = min(owner * seg + seg, p.n_lists);
+    for (int x = owner * seg; x < owner_end; x += 32) {  // the owner's lists, 32 at a time
+        const bool in = x + lane < owner_end;
+        const int L = in ? __ldg(p.seq_lens + x + lane) : 0;
+        const int cap = in ? list_cap(p, x + lane) : 0;
+        const int weight = in ? (blocks_of(L, cap) + kUnitCost) : 0;
+        int64_t sum = static_cast<int64_t>(weight) * rgc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > pos);
+        if (hit != 0u) {
+            const int at = __ffs(hit) - 1;
+            const int w = __shfl_sync(0xffffffffu, weight, at);
+            const int64_t first = before + __shfl_sync(0xffffffffu, sum, at) - static_cast<int64_t>(w) * rgc;
+            const int rg = static_cast<int>((pos - first) / w);
+            u.unit = (x + at) * rgc + rg;
+            u.L0 = __shfl_sync(0xffffffffu, L, at);
+            u.cap = __shfl_sync(0xffffffffu, cap, at);
+            sh.start = first + static_cast<int64_t>(rg) * w;
+            share_item(u, sh, max(0, static_cast<int>(pos - sh.start) - kUnitCost), upi);
+            if (u.it.y >= u.it.z) u.unit = -1;
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
 // Length and first page ids (before the length is known: bounded by the item's
 // planned blocks and the table row, so every read is in bounds).
 __device__ __forceinline__ void punit_load_lens_pages(const SplitParams& p, PUnit& u, int lane, int BR,
                                                       bool tma_mode) {
-    u.L0 = __ldg(p.seq_lens + punit_row(p, u));
-    u.cap = p.seq1_bps > 0 ? p.seq1_capacity : __ldg(p.capacity + u.it.x);
+    if (!p.shares) {  // (a share's unit has them: its item follows from its length)
+        u.L0 = __ldg(p.seq_lens + punit_row(p, u));
+        u.cap = p.seq1_bps > 0 ? p.seq1_capacity : __ldg(p.capacity + u.it.x);
+    }
     if (tma_mode) {
         u.pid0 = punit_box_page(p, u, lane, BR);
         u.pid1 = punit_box_page(p, u, 32 + lane, BR);
@@ -171,7 +272,7 @@ template <int D, int S, int NP, int QBUFS, bool BOXMAJ>
 __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtensorMap* tmk, const CUtensorMap* tmv,
                                               uint64_t* full, uint64_t* empty, uint64_t* qfree, int* tag,
                                               UnitMeta* um, uint16_t* qbuf, uint8_t* stages, bool tma_mode,
-                                              PUnit cur) {
+                                              PUnit cur, Share sh) {
     using G = StageGeom<D>;
     constexpr int RC = 16;
     constexpr int TOK = kStageTokens;
@@ -179,7 +280,7 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
     const int rgc = (p.rows + RC - 1) / RC;
     const int upi = p.hk * rgc;                           // units per work item
     const int n_units = p.n_units;
-    const int n_dyn = n_units - static_cast<int>(gridDim.x);  // units handed out by the ticket counter
+    const int n_dyn = p.shares ? 0 : n_units - static_cast<int>(gridDim.x);  // units handed out by the ticket counter
     const int page_mask = (1 << p.page_shift) - 1;
     const int BR = tma_mode ? min(1 << p.page_shift, TOK) : 1;  // token rows per TMA box
     const int NB = TOK / BR;                                      // boxes per stage
@@ -211,6 +312,28 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
     // requested, 3 length and page ids requested.
     int ahead = 0;
     auto advance = [&]() {
+        if (p.shares) {  // the next unit follows in the numbering, while the share goes on
+            if (ahead == 0) {
+                const int64_t next = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
+                if (next + kUnitCost < sh.end) {  // at least its first block
+                    nxt.unit = cur.unit + 1;
+                    nxt.L0 = __ldg(p.seq_lens + nxt.unit / rgc);
+                    nxt.cap = list_cap(p, nxt.unit / rgc);
+                    ahead = 1;
+                } else {
+                    ahead = 3;
+                }
+            } else if (ahead == 1) {
+                Share at = sh;
+                at.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
+                share_item(nxt, at, 0, upi);
+                ahead = 2;
+            } else if (ahead == 2) {
+                load_lens_pages(nxt);
+                ahead = 3;
+            }
+            return;
+        }
         if (ahead == 0) {
             if (n_dyn > 0) {
                 take();
@@ -265,6 +388,11 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
                 ok = false;
                 break;
             }
+        }
+        if (p.shares && lane == 0 && cur.it.y == 0) {
+            // The unit begins here; position x is in the largest CTA c with c total / grid <= x.
+            const int64_t past = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
+            p.share_rec[cur.unit] = make_int2(blockIdx.x, static_cast<int>((past * sh.grid - 1) / sh.total));
         }
         if (lane == 0) {
             UnitMeta m;
@@ -386,6 +514,7 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
         }
         if (!ok) break;
         while (ahead < 3) advance();
+        sh.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
         cur = nxt;
         nxt.unit = -1;
         ahead = 0;
@@ -464,7 +593,10 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
                 p.lse[static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h] =
                     Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
         } else {
-            p.part_ml[(static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row] = make_float2(M, Ls);
+            if (p.shares)
+                p.share_ml[u.slot * RC + lane] = make_float2(M, Ls);
+            else
+                p.part_ml[(static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row] = make_float2(M, Ls);
         }
     }
     const int total = nrows * C4;
@@ -500,8 +632,8 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
                                               O.w / Lr * p.v_scale)
                                 : make_float4(0.f, 0.f, 0.f, 0.f));
         } else {
-            const int64_t prow = (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
-            *reinterpret_cast<float4*>(p.part_o + prow * D + 4 * c4) =
+            const int64_t prow = p.shares ? u.slot * RC + r : (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
+            *reinterpret_cast<float4*>((p.shares ? p.share_o : p.part_o) + prow * D + 4 * c4) =
                 make_float4(O.x * p.v_scale, O.y * p.v_scale, O.z * p.v_scale, O.w * p.v_scale);
         }
     }
@@ -546,15 +678,20 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
     // before the set-up below, so that those round trips overlap it.
     PUnit first;
     first.unit = -1;
+    Share share = {0, 0, 1, 1};
     if (warp == NW) {
-        first.unit = blockIdx.x;
-        punit_load_item(p, first, p.hk * ((p.rows + RC - 1) / RC));  // plan data
+        if (!p.shares) {
+            first.unit = blockIdx.x;
+            punit_load_item(p, first, p.hk * ((p.rows + RC - 1) / RC));  // plan data
+        }
         // Launched as a programmatic dependent of the kernel before it in the stream (a
         // no-op without one): every input (lengths, page table, q, K, V) and every output
         // it may still read or write is touched only after that kernel has completed.  The
         // consumers' reads and writes follow the producer's stages.
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        punit_load_lens_pages(p, first, lane, tma_mode ? min(1 << p.page_shift, kStageTokens) : 1, tma_mode);
+        if (p.shares) share_first(p, first, share, lane);
+        if (first.unit >= 0)
+            punit_load_lens_pages(p, first, lane, tma_mode ? min(1 << p.page_shift, kStageTokens) : 1, tma_mode);
     }
     if (threadIdx.x == 0) {
         // Stage barriers: TMA stages complete on one expect-tx arrival; small-page stages
@@ -582,7 +719,7 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
             prefetch_tmap(&tmv);
         }
         produce_units<D, S, NP, QBUFS, Lay::BOXMAJ>(p, &tmk, &tmv, full, empty, qfree, tag, um, qbuf, stages, tma_mode,
-                                                    first);
+                                                    first, share);
         return;
     }
 

@@ -503,7 +503,8 @@ def test_run_selected(case, out_type):
 @pytest.mark.parametrize("path", [fd.FDEC_PATH_SIMT, fd.FDEC_PATH_MMA, fd.FDEC_PATH_TC])
 @pytest.mark.parametrize("blocks_per_split", [0, 1])
 def test_run_selected_on_every_path_equals_run_of_the_same_pages(path, blocks_per_split):
-    """With every head given the sequence's own pages, the result is fdec_run's, bit for bit."""
+    """With every head given the sequence's own pages, the result is fdec_run's (bit for bit where the work is cut
+    alike), and the same in every run."""
     rows, hq, hk, d, page, budget = 3, 32, 2, 128, 16, 20
     k, v = make_pool(80, hk, page, d, "bf16", "hnd", 4)
     ids, counts = selected_lists(rows, 1, page, budget, 80, seed=4)
@@ -513,7 +514,13 @@ def test_run_selected_on_every_path_equals_run_of_the_same_pages(path, blocks_pe
     la, lb = (torch.full((rows, 1, hq), float("nan"), device="cuda") for _ in range(2))
     pd.run(q, k, v, i32(ids[:, 0]), i32(counts[:, 0]), a, la)
     pd.run_selected(q, k, v, i32(ids.repeat(hk, 1)), i32(counts.repeat(hk, 1)), b, lb)
-    assert pd.device_errors() == 0 and torch.equal(a, b) and torch.equal(la, lb)
+    assert pd.device_errors() == 0
+    if path != fd.FDEC_PATH_MMA:  # which cuts the lists into shares by their run-time lengths
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    else:
+        again, lagain = torch.empty_like(b), torch.empty_like(lb)
+        pd.run_selected(q, k, v, i32(ids.repeat(hk, 1)), i32(counts.repeat(hk, 1)), again, lagain)
+        assert torch.equal(again, b) and torch.equal(lagain, lb)
     ref = attend_reference(q, k, v, ids.repeat(hk, 1), counts.repeat(hk, 1), 1 / math.sqrt(d))
     assert_attention(b, lb, *ref)
     short = torch.empty((rows, 1, hq, d), dtype=torch.bfloat16, device="cuda")
