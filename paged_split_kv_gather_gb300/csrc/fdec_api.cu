@@ -796,6 +796,7 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
     sp.pt_stride = page_table_stride;
     sp.seq_lens = seq_lens_dev;
     sp.tab_heads = per_head ? p->hk : 1;
+    sp.per_head = per_head ? 1 : 0;
     sp.out_type = out_type;
     sp.capacity = reinterpret_cast<const int32_t*>(ws + p->off_cap);
     sp.items = reinterpret_cast<const WorkItem*>(ws + p->off_items);
@@ -824,7 +825,10 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
                                 (q_stride_head * 2) % 16 == 0;
     const dim3 grid(static_cast<unsigned>(p->items.size()), static_cast<unsigned>(p->hk),
                     static_cast<unsigned>(p->row_groups));
-    const bool shares = per_head && p->share_grid > 0 && q_rows_aligned;
+    // Shares balance lists of unknown lengths and cost a second launch; where every list is
+    // one planned unit and has a CTA of its own there is nothing to balance.
+    const bool shares = per_head && p->share_grid > 0 && q_rows_aligned &&
+                        !(p->passes.empty() && p->n_units <= p->persist_grid);
     sp.shares = shares ? 1 : 0;
     sp.n_lists = p->batch * p->hk;
     sp.share_cap = p->share_cap;

@@ -57,6 +57,7 @@ struct SplitParams {
     // 1: one page-table row and length per sequence; hk: one per (sequence, KV head), row
     // seq * hk + kvh (the pages each head has selected).  table_row() gives the row.
     int tab_heads;
+    int per_head;              // 1: fdec_run_selected (also where hk is 1)
     int out_type;              // OutType of `out`
     const int32_t* capacity;   // planned capacity per sequence (workspace copy)
     const WorkItem* items;

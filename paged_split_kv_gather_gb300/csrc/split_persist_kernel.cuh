@@ -198,6 +198,14 @@ __device__ __forceinline__ void share_item(PUnit& u, const Share& sh, int begin,
     u.it = make_int4(u.unit / upi, begin, end, begin > 0 ? 2 * c : (end < nb ? 2 * c + 1 : -1));
 }
 
+// a * b / c of non-negative numbers, in 32 bits where they suffice (a 64-bit division is
+// about 0.3 us of the producer's start).
+__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int64_t c) {
+    const int64_t ab = a * b;
+    if (ab <= INT32_MAX && c <= INT32_MAX) return static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
+    return ab / c;
+}
+
 // Find this CTA's share and its first part (the producer warp).
 __device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Share& sh, int lane) {
     const int rgc = (p.rows + 15) / 16;
@@ -205,7 +213,7 @@ __device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Shar
     const int seg = (p.n_lists + 31) / 32;  // lists of one lane
     const int x0 = lane * seg, x1 = min(x0 + seg, p.n_lists);
     int64_t mine = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int x = x0; x < x1; ++x) mine += blocks_of(__ldg(p.seq_lens + x), list_cap(p, x)) + kUnitCost;
     mine *= rgc;
     int64_t upto = mine;
@@ -218,8 +226,8 @@ __device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Shar
     sh.grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
     u.unit = -1;
     if (static_cast<int>(blockIdx.x) >= sh.grid) return;
-    const int64_t pos = sh.total * blockIdx.x / sh.grid;
-    sh.end = sh.total * (blockIdx.x + 1) / sh.grid;
+    const int64_t pos = mul_div(sh.total, blockIdx.x, sh.grid);
+    sh.end = mul_div(sh.total, blockIdx.x + 1, sh.grid);
     const int owner = __ffs(__ballot_sync(0xffffffffu, upto > pos)) - 1;
     int64_t before = __shfl_sync(0xffffffffu, upto - mine, owner);
     const int owner_end = min(owner * seg + seg, p.n_lists);
@@ -239,7 +247,7 @@ __device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Shar
             const int at = __ffs(hit) - 1;
             const int w = __shfl_sync(0xffffffffu, weight, at);
             const int64_t first = before + __shfl_sync(0xffffffffu, sum, at) - static_cast<int64_t>(w) * rgc;
-            const int rg = static_cast<int>((pos - first) / w);
+            const int rg = rgc == 1 ? 0 : static_cast<int>((pos - first) / w);
             u.unit = (x + at) * rgc + rg;
             u.L0 = __shfl_sync(0xffffffffu, L, at);
             u.cap = __shfl_sync(0xffffffffu, cap, at);
@@ -392,7 +400,9 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
         if (p.shares && lane == 0 && cur.it.y == 0) {
             // The unit begins here; position x is in the largest CTA c with c total / grid <= x.
             const int64_t past = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
-            p.share_rec[cur.unit] = make_int2(blockIdx.x, static_cast<int>((past * sh.grid - 1) / sh.total));
+            // (past grid - 1) / total, in mul_div's 32 bits where they suffice
+            const int64_t n = past * sh.grid - 1;
+            p.share_rec[cur.unit] = make_int2(blockIdx.x, static_cast<int>(mul_div(n, 1, sh.total)));
         }
         if (lane == 0) {
             UnitMeta m;
@@ -573,6 +583,7 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
     constexpr int C4 = D / 4;
     const int nrows = min(RC, p.rows - u.row0);
     float M = -INFINITY, Ls = 0.f, e[NP];
+    int64_t dst = 0;  // first element of row `lane` in its destination
 #pragma unroll
     for (int w = 0; w < NP; ++w) e[w] = 0.f;
     if (lane < nrows) {
@@ -589,52 +600,79 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
         const int qi = row / p.group;
         const int h = u.kvh * p.group + (row - qi * p.group);
         if (u.slot < 0) {
-            if (p.lse != nullptr)
-                p.lse[static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h] =
-                    Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+            const int64_t orow = static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h;
+            if (p.lse != nullptr) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+            dst = orow * D;
+        } else if (p.shares) {
+            p.share_ml[u.slot * RC + lane] = make_float2(M, Ls);
+            dst = (static_cast<int64_t>(u.slot) * RC + lane) * D;
         } else {
-            if (p.shares)
-                p.share_ml[u.slot * RC + lane] = make_float2(M, Ls);
-            else
-                p.part_ml[(static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row] = make_float2(M, Ls);
+            const int64_t prow = (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
+            p.part_ml[prow] = make_float2(M, Ls);
+            dst = prow * D;
         }
     }
-    const int total = nrows * C4;
-    for (int x0 = 0; x0 < total; x0 += 32) {
-        const int x = x0 + lane;
-        const int r = min(x, total - 1) / C4;
-        const float Mr = __shfl_sync(0xffffffffu, M, r);
-        const float Lr = __shfl_sync(0xffffffffu, Ls, r);
-        float er[NP];
+    // Finished rows are O / L * v_scale; with per_head one division a row, v_scale / L.
+    const float norm = p.per_head ? (Ls > 0.f ? p.v_scale / Ls : 0.f) : Ls;
+    // Row by row, RU rows' loads together and a row's values broadcast from its lane once:
+    // this one warp's chain of instructions is what a unit's end costs.  (Column group by
+    // column group, with the row's values and addresses worked out for each: 13 us a unit
+    // at head_dim 512, 3.6 us at 128 with 8 rows.)
+    constexpr int LW = C4 < 32 ? C4 : 32;     // lanes of a row
+    constexpr int RS = 32 / LW;               // rows side by side
+    constexpr int CG = (C4 + LW - 1) / LW;    // column groups of a lane
+    constexpr int RU = CG >= 2 ? 2 : 4;
+    const int sub = lane / LW, c0 = lane - sub * LW;
+    float* const to = u.slot < 0 ? p.out : (p.shares ? p.share_o : p.part_o);
+    for (int r0 = 0; r0 < nrows; r0 += RS * RU) {
+        float4 v[RU][CG][NP];
 #pragma unroll
-        for (int w = 0; w < NP; ++w) er[w] = __shfl_sync(0xffffffffu, e[w], r);
-        if (x >= total) continue;
-        const int c4 = x - r * C4;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (Mr != -INFINITY) {
+        for (int k = 0; k < RU; ++k) {
+            const int r = min(r0 + k * RS + sub, nrows - 1);
 #pragma unroll
-            for (int w = 0; w < NP; ++w) {
-                const int c = 4 * c4;
-                const float4 v = *reinterpret_cast<const float4*>(o_w[w] + (c / DH) * O_HALF + r * O_ROW + c % DH);
-                O.x += v.x * er[w];
-                O.y += v.y * er[w];
-                O.z += v.z * er[w];
-                O.w += v.w * er[w];
+            for (int g = 0; g < CG; ++g) {
+                const int c = 4 * min(c0 + g * LW, C4 - 1);
+#pragma unroll
+                for (int w = 0; w < NP; ++w)
+                    v[k][g][w] = *reinterpret_cast<const float4*>(o_w[w] + (c / DH) * O_HALF + r * O_ROW + c % DH);
             }
         }
-        const int row = u.row0 + r;
-        const int qi = row / p.group;
-        const int h = u.kvh * p.group + (row - qi * p.group);
-        if (u.slot < 0) {
-            const int64_t orow = static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h;
-            store_out4(p.out, p.out_type, orow * D + 4 * c4,
-                       Lr > 0.f ? make_float4(O.x / Lr * p.v_scale, O.y / Lr * p.v_scale, O.z / Lr * p.v_scale,
-                                              O.w / Lr * p.v_scale)
-                                : make_float4(0.f, 0.f, 0.f, 0.f));
-        } else {
-            const int64_t prow = p.shares ? u.slot * RC + r : (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
-            *reinterpret_cast<float4*>((p.shares ? p.share_o : p.part_o) + prow * D + 4 * c4) =
-                make_float4(O.x * p.v_scale, O.y * p.v_scale, O.z * p.v_scale, O.w * p.v_scale);
+#pragma unroll
+        for (int k = 0; k < RU; ++k) {
+            const int r = r0 + k * RS + sub, from = min(r, nrows - 1);
+            const float Mr = __shfl_sync(0xffffffffu, M, from);
+            const float n = __shfl_sync(0xffffffffu, norm, from);
+            const int64_t at = __shfl_sync(0xffffffffu, dst, from);
+            float er[NP];
+#pragma unroll
+            for (int w = 0; w < NP; ++w) er[w] = __shfl_sync(0xffffffffu, e[w], from);
+            if (r >= nrows) continue;
+#pragma unroll
+            for (int g = 0; g < CG; ++g) {
+                const int c4 = c0 + g * LW;
+                if (C4 % LW != 0 && c4 >= C4) continue;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (Mr != -INFINITY) {
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) {
+                        O.x += v[k][g][w].x * er[w];
+                        O.y += v[k][g][w].y * er[w];
+                        O.z += v[k][g][w].z * er[w];
+                        O.w += v[k][g][w].w * er[w];
+                    }
+                }
+                if (u.slot >= 0) {
+                    O = make_float4(O.x * p.v_scale, O.y * p.v_scale, O.z * p.v_scale, O.w * p.v_scale);
+                    *reinterpret_cast<float4*>(to + at + 4 * c4) = O;
+                } else if (p.per_head) {
+                    store_out4(to, p.out_type, at + 4 * c4, make_float4(O.x * n, O.y * n, O.z * n, O.w * n));
+                } else {
+                    *reinterpret_cast<float4*>(to + at + 4 * c4) =
+                        n > 0.f ? make_float4(O.x / n * p.v_scale, O.y / n * p.v_scale, O.z / n * p.v_scale,
+                                              O.w / n * p.v_scale)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
         }
     }
 }
