@@ -159,7 +159,7 @@ struct fdec_plan_s {
     int path = FDEC_PATH_SIMT;
     bool persistent = false;  // MMA path over 16-bit caches: resident CTAs take work units
     int n_units = 0, persist_grid = 0;
-    // Shares of fdec_run_selected (SplitParams::shares): their grid (0: planned items) and
+    // Shares of fdec_run_selected (SelectedParams::shares): their grid (0: planned items) and
     // regions, behind the rest of the workspace (base_ws_bytes), which is all that the
     // other entry points use.
     int share_grid = 0, share_cap = -1;
@@ -261,7 +261,7 @@ int choose_blocks_per_split(const std::vector<int>& nblocks, int copies, int slo
     return best;
 }
 
-cudaError_t dispatch_split(const fdec_plan_s* p, const SplitParams& sp, dim3 grid, cudaStream_t stream, bool launch,
+cudaError_t dispatch_split(const fdec_plan_s* p, const SelectedParams& sp, dim3 grid, cudaStream_t stream, bool launch,
                            bool persist = false) {
     const bool bf16 = p->dtype == FDEC_BF16;
     const CUtensorMap& tk = p->tmap_k;
@@ -686,7 +686,7 @@ fdec_status fdec_plan_upload(fdec_plan_t p, void* workspace, cudaStream_t stream
     if (cap != cudaStreamCaptureStatusNone)
         return fail(FDEC_ERR_CAPTURING, "fdec_plan_upload must not run while the stream is capturing");
     // Set the split kernel's shared-memory attribute here, outside any capture.
-    SplitParams none{};
+    SelectedParams none{};
     e = dispatch_split(p, none, dim3(1, 1, 1), stream, false);
     if (e == cudaSuccess && p->persistent) e = dispatch_split(p, none, dim3(1, 1, 1), stream, false, true);
     if (e != cudaSuccess) return fail_cuda(e, "preparing the split kernel");
@@ -770,7 +770,7 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
         p->maps_valid = true;
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    SplitParams sp;
+    SelectedParams sp;
     sp.q = static_cast<const uint16_t*>(q);
     sp.q_stride_tok = q_stride_tok;
     sp.q_stride_head = q_stride_head;
@@ -801,7 +801,6 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
     sp.page_table = page_table;
     sp.pt_stride = page_table_stride;
     sp.seq_lens = seq_lens_dev;
-    sp.tab_heads = per_head ? p->hk : 1;
     sp.per_head = per_head ? 1 : 0;
     sp.out_type = out_type;
     sp.capacity = reinterpret_cast<const int32_t*>(ws + p->off_cap);

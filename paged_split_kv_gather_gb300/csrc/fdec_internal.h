@@ -54,11 +54,6 @@ struct SplitParams {
     const int32_t* page_table;
     int64_t pt_stride;
     const int32_t* seq_lens;
-    // 1: one page-table row and length per sequence; hk: one per (sequence, KV head), row
-    // seq * hk + kvh (the pages each head has selected).  table_row() gives the row.
-    int tab_heads;
-    int per_head;              // 1: fdec_run_selected (also where hk is 1)
-    int out_type;              // OutType of `out`
     const int32_t* capacity;   // planned capacity per sequence (workspace copy)
     const WorkItem* items;
     float* part_o;             // [slot][Hk][rows][D]
@@ -74,18 +69,27 @@ struct SplitParams {
     // ticket counter (advanced by exactly n_units per launch).
     int n_units;
     unsigned long long* ticket;
-    // Shares (fdec_run_selected): instead of planned items, CTA c takes the c-th of grid
-    // equal runs of the 64-token blocks that the lists hold at run time (see
-    // split_persist_kernel.cuh).  0: planned items.
+    // One sequence (batch 1): its work items are runs of seq1_bps blocks in order, so
+    // a unit's item follows from its index with no table read (0: read the table).
+    int seq1_bps, seq1_blocks, seq1_capacity;
+};
+
+// fdec_run_selected: page-table row and length seq * hk + kvh are those of the pages that
+// KV head kvh of query token seq has selected.  The split kernels are compiled apart for
+// these parameters: as run-time branches of one build the differences cost the other
+// calls up to 6 us (cold instruction fetches) of a flushed 2048-token decode.
+struct SelectedParams : SplitParams {
+    int per_head;              // 1: run as selected; 0: as the SplitParams that they contain
+    int out_type;              // OutType of `out`
+    // Shares: instead of planned items, CTA c takes the c-th of grid equal runs of the
+    // 64-token blocks that the lists hold at run time (see split_persist_kernel.cuh).
+    // 0: planned items.
     int shares;
     int n_lists;               // batch x hk
     int share_cap;             // the capacity of every sequence if they are equal, else -1
     int2* share_rec;           // [n_lists x row groups] first and last CTA of each unit
     float* share_o;            // [2 grid][16][D] partials: 2 c: a unit begun before CTA c, 2 c + 1: one that goes on
     float2* share_ml;          // [2 grid][16]
-    // One sequence (batch 1): its work items are runs of seq1_bps blocks in order, so
-    // a unit's item follows from its index with no table read (0: read the table).
-    int seq1_bps, seq1_blocks, seq1_capacity;
 };
 
 struct ReduceParams {
@@ -107,27 +111,31 @@ struct ReduceParams {
 // Launch the split kernel for head_dim D (defined in split_d<D>.cu); rc is the
 // compile-time query-row group.  With launch == false only the kernel's
 // shared-memory attribute is set (done at upload, outside any capture).
-cudaError_t launch_split_d64(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d64(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch);
-cudaError_t launch_split_d128(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d128(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch);
-cudaError_t launch_split_d192(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d192(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch);
-cudaError_t launch_split_d256(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d256(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch);
-cudaError_t launch_split_d512(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d512(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch);
 
 // The tensor-core split kernel (head_dim 64, 128, 192, 256, 512; query rows in
 // groups of 16).  kv8: K/V stored as E4M3 codes (head_dim 128 and 256).
-cudaError_t launch_split_mma(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+cudaError_t launch_split_mma(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
                              bool bf16, bool kv8, dim3 grid, cudaStream_t s, bool launch);
+cudaError_t launch_split_mma_selected(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                                      bool bf16, bool kv8, dim3 grid, cudaStream_t s, bool launch);
 size_t split_mma_smem_bytes(int head_dim, bool kv8);
 // The persistent form of the tensor-core split kernel (16-bit caches, every head_dim;
 // q rows 16-byte aligned): CTAs stay resident and take work units until none is left,
 // so a unit's pipeline fill is paid once per CTA and not once per work item.
-cudaError_t launch_split_mma_persist(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+cudaError_t launch_split_mma_persist(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
                                      bool bf16, dim3 grid, cudaStream_t s, bool launch);
+cudaError_t launch_split_mma_persist_selected(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                              int head_dim, bool bf16, dim3 grid, cudaStream_t s, bool launch);
 inline bool split_mma_persist_supported(int head_dim) {
     return head_dim == 64 || head_dim == 128 || head_dim == 192 || head_dim == 256 || head_dim == 512;
 }
@@ -149,7 +157,7 @@ constexpr int kMmaRows = 16;
 // The tcgen05 dense-query split kernel (head_dim 64, 128, 192, 256; `tiles` 128-row
 // query tiles per CTA: 1 or 2 for head_dim 64 and 128, 1 above; 64-token stages: its
 // tensor maps use boxes of min(page_size, 64) token rows).
-cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles, int head_dim,
+cudaError_t launch_split_tc(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles, int head_dim,
                             bool bf16, dim3 grid, cudaStream_t s, bool launch);
 size_t split_tc_smem_bytes(int tiles, int head_dim);
 int split_tc_threads(int tiles, bool bf16);
@@ -165,7 +173,7 @@ size_t split_smem_bytes(int head_dim, int rc);
 int split_threads(int head_dim);
 int split_max_rc(int head_dim);
 
-// Merge of the units that shares have cut (SplitParams::shares): after the split launch.
+// Merge of the units that shares have cut (SelectedParams::shares): after the split launch.
 struct ShareMergeParams {
     const int2* rec;
     const float* o;            // [2 grid][16][D]

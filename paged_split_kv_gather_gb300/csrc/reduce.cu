@@ -38,6 +38,8 @@ __device__ __forceinline__ float2 source_ml(const ReduceParams& p, int64_t idx) 
     return p.src_ml[idx];
 }
 
+// HALF: a 16-bit output (p.out_type), for fdec_run_selected.
+template <bool HALF>
 __global__ void __launch_bounds__(kReduceWarps * 32, 5) reduce_kernel(const ReduceParams p, int num_tasks,
                                                                    ReduceTask single) {
     constexpr float kLn2 = 0.69314718055994530942f;
@@ -123,7 +125,10 @@ __global__ void __launch_bounds__(kReduceWarps * 32, 5) reduce_kernel(const Redu
                 const int qi = row / p.group;
                 const int h = kvh * p.group + (row - qi * p.group);
                 const int64_t orow = static_cast<int64_t>(task.seq * p.q_len + qi) * p.hq + h;
-                store_out1(p.out, p.out_type, orow * D + d, Lsum > 0.f ? o / Lsum : 0.f);
+                if constexpr (HALF)
+                    store_out1(p.out, p.out_type, orow * D + d, Lsum > 0.f ? o / Lsum : 0.f);
+                else
+                    p.out[orow * D + d] = Lsum > 0.f ? o / Lsum : 0.f;
                 if (d == 0 && p.lse != nullptr) p.lse[orow] = Lsum > 0.f ? (M + log2f(Lsum)) * kLn2 : -INFINITY;
             } else {
                 const int64_t drow = (static_cast<int64_t>(task.dst) * p.hk + kvh) * p.rows + row;
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32, 5) reduce_kernel(const Redu
     }
 }
 
-// Join the parts of the units that shares have cut (SplitParams::shares).  One CTA per
+// Join the parts of the units that shares have cut (SelectedParams::shares).  One CTA per
 // unit and row: a unit within one CTA's share is finished already and its CTA returns at
 // once; else the warps stride over the parts, each lane holding D / 32 elements, and are
 // merged in shared memory in warp order.  Parts of a unit: slot 2 c + 1 of its first CTA,
@@ -261,12 +266,13 @@ cudaError_t launch_reduce(const ReduceParams& p, int num_tasks, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, reduce_kernel, p, num_tasks, ReduceTask{0, 0, 0, -1});
+    return p.out_type == kOutF32 ? cudaLaunchKernelEx(&cfg, reduce_kernel<false>, p, num_tasks, ReduceTask{0, 0, 0, -1})
+                                 : cudaLaunchKernelEx(&cfg, reduce_kernel<true>, p, num_tasks, ReduceTask{0, 0, 0, -1});
 }
 
 cudaError_t launch_reduce_single(const ReduceParams& p, ReduceTask task, cudaStream_t s) {
     dim3 grid(reduce_grid_x(p), 1, 1);
-    reduce_kernel<<<grid, kReduceWarps * 32, 0, s>>>(p, 1, task);
+    reduce_kernel<false><<<grid, kReduceWarps * 32, 0, s>>>(p, 1, task);
     return cudaGetLastError();
 }
 

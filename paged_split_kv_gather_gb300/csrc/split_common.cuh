@@ -63,13 +63,21 @@ struct ItemRange {
     bool bad;
 };
 
-// Page-table and length row of a sequence for one KV head (see SplitParams::tab_heads).
-__device__ __forceinline__ int64_t table_row(const SplitParams& p, int seq, int kvh) {
-    return p.tab_heads > 1 ? static_cast<int64_t>(seq) * p.tab_heads + kvh : seq;
+// Parameters P of a kernel: SplitParams, or SelectedParams (fdec_run_selected).
+template <typename P>
+constexpr bool kSelected = std::is_base_of_v<SelectedParams, P>;
+
+// Page-table and length row of a sequence for one KV head.
+template <typename P>
+__device__ __forceinline__ int64_t table_row(const P& p, int seq, int kvh) {
+    if constexpr (kSelected<P>)
+        return static_cast<int64_t>(seq) * p.hk + kvh;
+    else
+        return seq;
 }
 
-template <int TOK = kStageTokens>
-__device__ __forceinline__ ItemRange item_range(const SplitParams& p, const WorkItem& it, int kvh) {
+template <int TOK = kStageTokens, typename P>
+__device__ __forceinline__ ItemRange item_range(const P& p, const WorkItem& it, int kvh) {
     const int L0 = p.seq_lens[table_row(p, it.seq, kvh)];
     const int cap = p.capacity[it.seq];
     ItemRange r;
@@ -174,8 +182,8 @@ __device__ __forceinline__ void copy_scale_rows(const SplitParams& p, uint8_t* s
 // box spans all regions) instead of one box per region into the region-major layout:
 // a TMA instruction costs about the same whatever its size, and with one box per region
 // the producer's issue time bounded the stream at page sizes 8 and 16.
-template <int D, int S, int TOK = kStageTokens, int EB = 2, int SCB = 0, bool BOXMAJ = false>
-__device__ __forceinline__ void produce_stages(const SplitParams& p, const CUtensorMap* tmk, const CUtensorMap* tmv, uint64_t* full,
+template <int D, int S, int TOK = kStageTokens, int EB = 2, int SCB = 0, bool BOXMAJ = false, typename P>
+__device__ __forceinline__ void produce_stages(const P& p, const CUtensorMap* tmk, const CUtensorMap* tmv, uint64_t* full,
                                uint64_t* empty, uint8_t* stages, int b, int kvh, const ItemRange& ir,
                                bool tma_mode, uint8_t* sc_ring = nullptr) {
     using G = StageGeom<D, TOK, EB>;
@@ -348,8 +356,8 @@ __device__ __forceinline__ void zero_v_tail(uint8_t* stage, int nv, int tid = th
 // O is scaled by v_scale (the value scale of a quantised cache, 1 otherwise): the
 // LSE merge is linear in O, so partials may carry it.
 // NTHREADS consumer threads (from thread 0) share the work.
-template <int NW, int RC, int D, int NTHREADS = NW * 32>
-__device__ __forceinline__ void merge_and_store(const SplitParams& p, const WorkItem& it, int kvh, int row0,
+template <int NW, int RC, int D, int NTHREADS = NW * 32, typename P>
+__device__ __forceinline__ void merge_and_store(const P& p, const WorkItem& it, int kvh, int row0,
                                                 const float* sm_m, const float* sm_l, const float* sm_o) {
     constexpr float kLn2 = 0.69314718055994530942f;
     for (int idx = threadIdx.x; idx < RC * D; idx += NTHREADS) {
@@ -373,7 +381,10 @@ __device__ __forceinline__ void merge_and_store(const SplitParams& p, const Work
             const int qi = row / p.group;
             const int h = kvh * p.group + (row - qi * p.group);
             const int64_t orow = static_cast<int64_t>(it.seq * p.q_len + qi) * p.hq + h;
-            store_out1(p.out, p.out_type, orow * D + d, Ls > 0.f ? O / Ls * p.v_scale : 0.f);
+            if constexpr (kSelected<P>)
+                store_out1(p.out, p.out_type, orow * D + d, Ls > 0.f ? O / Ls * p.v_scale : 0.f);
+            else
+                p.out[orow * D + d] = Ls > 0.f ? O / Ls * p.v_scale : 0.f;
             if (d == 0 && p.lse != nullptr) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
         } else {
             const int64_t prow = (static_cast<int64_t>(it.slot) * p.hk + kvh) * p.rows + row;

@@ -3,7 +3,7 @@
 
 namespace fdec {
 
-cudaError_t launch_split_d64(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
+cudaError_t launch_split_d64(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc,
                                bool bf16, dim3 grid, cudaStream_t s, bool launch) {
     return launch_split_d<64>(p, tk, tv, rc, bf16, grid, s, launch);
 }

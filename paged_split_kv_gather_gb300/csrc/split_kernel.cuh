@@ -88,9 +88,9 @@ __device__ __forceinline__ void load_p_pairs(const float2* src, float2 (&pr)[RC]
     }
 }
 
-template <int D, int RC, bool BF16>
+template <int D, int RC, bool BF16, typename P>
 __global__ void __launch_bounds__(SplitLayout<D, RC>::THREADS, 1)
-split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmk,
+split_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
              const __grid_constant__ CUtensorMap tmv) {
     using Lay = SplitLayout<D, RC>;
     constexpr int NW = Lay::NW;
@@ -323,8 +323,8 @@ split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUte
     merge_and_store<NW, RC, D>(p, it, kvh, row0, sm_m, sm_l, sm_o);
 }
 
-template <int D, int RC, bool BF16>
-cudaError_t launch_split_one(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+template <int D, int RC, bool BF16, typename P>
+cudaError_t launch_split_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                              cudaStream_t stream, bool launch) {
     using Lay = SplitLayout<D, RC>;
     static unsigned long long attr_done = 0;  // one bit per device
@@ -332,7 +332,7 @@ cudaError_t launch_split_one(const SplitParams& p, const CUtensorMap& tk, const 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(split_kernel<D, RC, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(split_kernel<D, RC, BF16, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Lay::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
@@ -348,22 +348,22 @@ cudaError_t launch_split_one(const SplitParams& p, const CUtensorMap& tk, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_kernel<D, RC, BF16>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, split_kernel<D, RC, BF16, P>, p, tk, tv);
 }
 
-template <int D, bool BF16>
-cudaError_t launch_split_rc(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc, dim3 grid,
+template <int D, bool BF16, typename P>
+cudaError_t launch_split_rc(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc, dim3 grid,
                             cudaStream_t s, bool launch) {
     constexpr int RCMAX = SplitShape<D>::RCMAX;
     switch (rc) {
-        case 1: return launch_split_one<D, 1, BF16>(p, tk, tv, grid, s, launch);
-        case 2: return launch_split_one<D, 2, BF16>(p, tk, tv, grid, s, launch);
-        case 4: return launch_split_one<D, 4, BF16>(p, tk, tv, grid, s, launch);
+        case 1: return launch_split_one<D, 1, BF16, P>(p, tk, tv, grid, s, launch);
+        case 2: return launch_split_one<D, 2, BF16, P>(p, tk, tv, grid, s, launch);
+        case 4: return launch_split_one<D, 4, BF16, P>(p, tk, tv, grid, s, launch);
         case 8:
-            if constexpr (RCMAX >= 8) return launch_split_one<D, 8, BF16>(p, tk, tv, grid, s, launch);
+            if constexpr (RCMAX >= 8) return launch_split_one<D, 8, BF16, P>(p, tk, tv, grid, s, launch);
             break;
         case 16:
-            if constexpr (RCMAX >= 16) return launch_split_one<D, 16, BF16>(p, tk, tv, grid, s, launch);
+            if constexpr (RCMAX >= 16) return launch_split_one<D, 16, BF16, P>(p, tk, tv, grid, s, launch);
             break;
         default: break;
     }
@@ -371,10 +371,16 @@ cudaError_t launch_split_rc(const SplitParams& p, const CUtensorMap& tk, const C
 }
 
 template <int D>
-cudaError_t launch_split_d(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc, bool bf16,
+cudaError_t launch_split_d(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int rc, bool bf16,
                            dim3 grid, cudaStream_t s, bool launch) {
-    return bf16 ? launch_split_rc<D, true>(p, tk, tv, rc, grid, s, launch)
-                : launch_split_rc<D, false>(p, tk, tv, rc, grid, s, launch);
+    const SplitParams& q = p;  // the run that is not selected
+    if (!launch || p.per_head) {
+        const cudaError_t e = bf16 ? launch_split_rc<D, true>(p, tk, tv, rc, grid, s, launch)
+                                   : launch_split_rc<D, false>(p, tk, tv, rc, grid, s, launch);
+        if (e != cudaSuccess || launch) return e;
+    }
+    return bf16 ? launch_split_rc<D, true>(q, tk, tv, rc, grid, s, launch)
+                : launch_split_rc<D, false>(q, tk, tv, rc, grid, s, launch);
 }
 
 }  // namespace fdec

@@ -4,39 +4,13 @@
 
 namespace fdec {
 
-cudaError_t launch_split_mma(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+cudaError_t launch_split_mma(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
                              bool bf16, bool kv8, dim3 grid, cudaStream_t s, bool launch) {
-    if (kv8) {
-        switch (head_dim) {
-            case 128:
-                return bf16 ? launch_split_mma_one<128, true, true>(p, tk, tv, grid, s, launch)
-                            : launch_split_mma_one<128, false, true>(p, tk, tv, grid, s, launch);
-            case 256:
-                return bf16 ? launch_split_mma_one<256, true, true>(p, tk, tv, grid, s, launch)
-                            : launch_split_mma_one<256, false, true>(p, tk, tv, grid, s, launch);
-            default:
-                return cudaErrorInvalidValue;
-        }
+    if (!launch || p.per_head) {  // set-up (plan upload): both forms' kernel attributes
+        const cudaError_t e = launch_split_mma_selected(p, tk, tv, head_dim, bf16, kv8, grid, s, launch);
+        if (e != cudaSuccess || launch) return e;
     }
-    switch (head_dim) {
-        case 64:
-            return bf16 ? launch_split_mma_one<64, true>(p, tk, tv, grid, s, launch)
-                        : launch_split_mma_one<64, false>(p, tk, tv, grid, s, launch);
-        case 128:
-            return bf16 ? launch_split_mma_one<128, true>(p, tk, tv, grid, s, launch)
-                        : launch_split_mma_one<128, false>(p, tk, tv, grid, s, launch);
-        case 192:
-            return bf16 ? launch_split_mma_one<192, true>(p, tk, tv, grid, s, launch)
-                        : launch_split_mma_one<192, false>(p, tk, tv, grid, s, launch);
-        case 256:
-            return bf16 ? launch_split_mma_one<256, true>(p, tk, tv, grid, s, launch)
-                        : launch_split_mma_one<256, false>(p, tk, tv, grid, s, launch);
-        case 512:
-            return bf16 ? launch_split_mma_one<512, true>(p, tk, tv, grid, s, launch)
-                        : launch_split_mma_one<512, false>(p, tk, tv, grid, s, launch);
-        default:
-            return cudaErrorInvalidValue;
-    }
+    return launch_mma(static_cast<const SplitParams&>(p), tk, tv, head_dim, bf16, kv8, grid, s, launch);
 }
 
 size_t split_mma_smem_bytes(int head_dim, bool kv8) {

@@ -586,9 +586,9 @@ struct MmaWarp {
     }
 };
 
-template <int D, bool BF16, bool KV8, bool Q8 = false>
+template <int D, bool BF16, bool KV8, bool Q8, typename P>
 __global__ void __launch_bounds__(MmaLayout<D, KV8, Q8>::THREADS, MmaLayout<D, KV8, Q8>::CTAS_PER_SM)
-split_mma_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmk,
+split_mma_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv) {
     using Lay = MmaLayout<D, KV8, Q8>;
     using W = MmaWarp<D, BF16, KV8, Q8>;
@@ -764,8 +764,8 @@ split_mma_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ 
     merge_and_store<NP, RC, D, NW * 32>(p, it, kvh, row0, sm_m, sm_l, sm_o);
 }
 
-template <int D, bool BF16, bool KV8 = false, bool Q8 = false>
-cudaError_t launch_split_mma_one(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+template <int D, bool BF16, bool KV8 = false, bool Q8 = false, typename P>
+cudaError_t launch_split_mma_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                                  cudaStream_t stream, bool launch) {
     using Lay = MmaLayout<D, KV8, Q8>;
     static unsigned long long attr_done = 0;  // one bit per device
@@ -773,7 +773,7 @@ cudaError_t launch_split_mma_one(const SplitParams& p, const CUtensorMap& tk, co
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(split_mma_kernel<D, BF16, KV8, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(split_mma_kernel<D, BF16, KV8, Q8, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Lay::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
@@ -789,7 +789,43 @@ cudaError_t launch_split_mma_one(const SplitParams& p, const CUtensorMap& tk, co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_mma_kernel<D, BF16, KV8, Q8>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, split_mma_kernel<D, BF16, KV8, Q8, P>, p, tk, tv);
+}
+
+template <typename P>
+cudaError_t launch_mma(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                             bool bf16, bool kv8, dim3 grid, cudaStream_t s, bool launch) {
+    if (kv8) {
+        switch (head_dim) {
+            case 128:
+                return bf16 ? launch_split_mma_one<128, true, true>(p, tk, tv, grid, s, launch)
+                            : launch_split_mma_one<128, false, true>(p, tk, tv, grid, s, launch);
+            case 256:
+                return bf16 ? launch_split_mma_one<256, true, true>(p, tk, tv, grid, s, launch)
+                            : launch_split_mma_one<256, false, true>(p, tk, tv, grid, s, launch);
+            default:
+                return cudaErrorInvalidValue;
+        }
+    }
+    switch (head_dim) {
+        case 64:
+            return bf16 ? launch_split_mma_one<64, true>(p, tk, tv, grid, s, launch)
+                        : launch_split_mma_one<64, false>(p, tk, tv, grid, s, launch);
+        case 128:
+            return bf16 ? launch_split_mma_one<128, true>(p, tk, tv, grid, s, launch)
+                        : launch_split_mma_one<128, false>(p, tk, tv, grid, s, launch);
+        case 192:
+            return bf16 ? launch_split_mma_one<192, true>(p, tk, tv, grid, s, launch)
+                        : launch_split_mma_one<192, false>(p, tk, tv, grid, s, launch);
+        case 256:
+            return bf16 ? launch_split_mma_one<256, true>(p, tk, tv, grid, s, launch)
+                        : launch_split_mma_one<256, false>(p, tk, tv, grid, s, launch);
+        case 512:
+            return bf16 ? launch_split_mma_one<512, true>(p, tk, tv, grid, s, launch)
+                        : launch_split_mma_one<512, false>(p, tk, tv, grid, s, launch);
+        default:
+            return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace fdec

@@ -149,14 +149,28 @@ __device__ __forceinline__ void punit_load_item(const SplitParams& p, PUnit& u, 
 }
 
 // Page-table and length row of the unit (see table_row).
-__device__ __forceinline__ int64_t punit_row(const SplitParams& p, const PUnit& u) {
-    if (p.tab_heads == 1) return u.it.x;
-    const int rgc = (p.rows + 15) / 16;
-    return table_row(p, u.it.x, u.unit % (p.hk * rgc) / rgc);
+template <typename P>
+__device__ __forceinline__ int64_t punit_row(const P& p, const PUnit& u) {
+    if constexpr (kSelected<P>) {
+        const int rgc = (p.rows + 15) / 16;
+        return table_row(p, u.it.x, u.unit % (p.hk * rgc) / rgc);
+    } else {
+        return u.it.x;
+    }
+}
+
+// Whether the launch runs shares.
+template <typename P>
+__device__ __forceinline__ bool in_shares(const P& p) {
+    if constexpr (kSelected<P>)
+        return p.shares != 0;
+    else
+        return false;
 }
 
 // Page id of TMA box n (BR token rows) of the unit, or -1 past its planned blocks.
-__device__ __forceinline__ int punit_box_page(const SplitParams& p, const PUnit& u, int n, int BR) {
+template <typename P>
+__device__ __forceinline__ int punit_box_page(const P& p, const PUnit& u, int n, int BR) {
     const int t = u.it.y * kBlockTokens + n * BR;
     const int32_t* pt = p.page_table + punit_row(p, u) * p.pt_stride;
     return (t < u.it.z * kBlockTokens && (t >> p.page_shift) < p.pt_stride) ? __ldg(pt + (t >> p.page_shift)) : -1;
@@ -170,7 +184,7 @@ constexpr int kUnitCost = 3;
 
 // Blocks of list x (sequence x / hk, KV head x % hk), at least one: an empty list's unit
 // writes its empty result.
-__device__ __forceinline__ int list_cap(const SplitParams& p, int x) {
+__device__ __forceinline__ int list_cap(const SelectedParams& p, int x) {
     return p.share_cap >= 0 ? p.share_cap : __ldg(p.capacity + x / p.hk);
 }
 __device__ __forceinline__ int blocks_of(int L, int cap) {
@@ -207,7 +221,7 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int b, int64_t c) {
 }
 
 // Find this CTA's share and its first part (the producer warp).
-__device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Share& sh, int lane) {
+__device__ __forceinline__ void share_first(const SelectedParams& p, PUnit& u, Share& sh, int lane) {
     const int rgc = (p.rows + 15) / 16;
     const int upi = p.hk * rgc;
     const int seg = (p.n_lists + 31) / 32;  // lists of one lane
@@ -262,9 +276,10 @@ __device__ __forceinline__ void share_first(const SplitParams& p, PUnit& u, Shar
 
 // Length and first page ids (before the length is known: bounded by the item's
 // planned blocks and the table row, so every read is in bounds).
-__device__ __forceinline__ void punit_load_lens_pages(const SplitParams& p, PUnit& u, int lane, int BR,
+template <typename P>
+__device__ __forceinline__ void punit_load_lens_pages(const P& p, PUnit& u, int lane, int BR,
                                                       bool tma_mode) {
-    if (!p.shares) {  // (a share's unit has them: its item follows from its length)
+    if (!in_shares(p)) {  // (a share's unit has them: its item follows from its length)
         u.L0 = __ldg(p.seq_lens + punit_row(p, u));
         u.cap = p.seq1_bps > 0 ? p.seq1_capacity : __ldg(p.capacity + u.it.x);
     }
@@ -276,8 +291,8 @@ __device__ __forceinline__ void punit_load_lens_pages(const SplitParams& p, PUni
 
 // The producer warp of the persistent kernel.  `first`: the CTA's first unit, its
 // loads issued before the CTA's set-up so that they overlap it.
-template <int D, int S, int NP, int QBUFS, bool BOXMAJ>
-__device__ __forceinline__ void produce_units(const SplitParams& p, const CUtensorMap* tmk, const CUtensorMap* tmv,
+template <int D, int S, int NP, int QBUFS, bool BOXMAJ, typename P>
+__device__ __forceinline__ void produce_units(const P& p, const CUtensorMap* tmk, const CUtensorMap* tmv,
                                               uint64_t* full, uint64_t* empty, uint64_t* qfree, int* tag,
                                               UnitMeta* um, uint16_t* qbuf, uint8_t* stages, bool tma_mode,
                                               PUnit cur, Share sh) {
@@ -288,7 +303,7 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
     const int rgc = (p.rows + RC - 1) / RC;
     const int upi = p.hk * rgc;                           // units per work item
     const int n_units = p.n_units;
-    const int n_dyn = p.shares ? 0 : n_units - static_cast<int>(gridDim.x);  // units handed out by the ticket counter
+    const int n_dyn = in_shares(p) ? 0 : n_units - static_cast<int>(gridDim.x);  // units handed out by the ticket counter
     const int page_mask = (1 << p.page_shift) - 1;
     const int BR = tma_mode ? min(1 << p.page_shift, TOK) : 1;  // token rows per TMA box
     const int NB = TOK / BR;                                      // boxes per stage
@@ -320,27 +335,29 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
     // requested, 3 length and page ids requested.
     int ahead = 0;
     auto advance = [&]() {
-        if (p.shares) {  // the next unit follows in the numbering, while the share goes on
-            if (ahead == 0) {
-                const int64_t next = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
-                if (next + kUnitCost < sh.end) {  // at least its first block
-                    nxt.unit = cur.unit + 1;
-                    nxt.L0 = __ldg(p.seq_lens + nxt.unit / rgc);
-                    nxt.cap = list_cap(p, nxt.unit / rgc);
-                    ahead = 1;
-                } else {
+        if constexpr (kSelected<P>) {
+            if (p.shares) {  // the next unit follows in the numbering, while the share goes on
+                if (ahead == 0) {
+                    const int64_t next = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
+                    if (next + kUnitCost < sh.end) {  // at least its first block
+                        nxt.unit = cur.unit + 1;
+                        nxt.L0 = __ldg(p.seq_lens + nxt.unit / rgc);
+                        nxt.cap = list_cap(p, nxt.unit / rgc);
+                        ahead = 1;
+                    } else {
+                        ahead = 3;
+                    }
+                } else if (ahead == 1) {
+                    Share at = sh;
+                    at.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
+                    share_item(nxt, at, 0, upi);
+                    ahead = 2;
+                } else if (ahead == 2) {
+                    load_lens_pages(nxt);
                     ahead = 3;
                 }
-            } else if (ahead == 1) {
-                Share at = sh;
-                at.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
-                share_item(nxt, at, 0, upi);
-                ahead = 2;
-            } else if (ahead == 2) {
-                load_lens_pages(nxt);
-                ahead = 3;
+                return;
             }
-            return;
         }
         if (ahead == 0) {
             if (n_dyn > 0) {
@@ -397,12 +414,14 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
                 break;
             }
         }
-        if (p.shares && lane == 0 && cur.it.y == 0) {
-            // The unit begins here; position x is in the largest CTA c with c total / grid <= x.
-            const int64_t past = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
-            // (past grid - 1) / total, in mul_div's 32 bits where they suffice
-            const int64_t n = past * sh.grid - 1;
-            p.share_rec[cur.unit] = make_int2(blockIdx.x, static_cast<int>(mul_div(n, 1, sh.total)));
+        if constexpr (kSelected<P>) {
+            if (p.shares && lane == 0 && cur.it.y == 0) {
+                // The unit begins here; position x is in the largest CTA c with c total / grid <= x.
+                const int64_t past = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
+                // (past grid - 1) / total, in mul_div's 32 bits where they suffice
+                const int64_t n = past * sh.grid - 1;
+                p.share_rec[cur.unit] = make_int2(blockIdx.x, static_cast<int>(mul_div(n, 1, sh.total)));
+            }
         }
         if (lane == 0) {
             UnitMeta m;
@@ -524,7 +543,7 @@ __device__ __forceinline__ void produce_units(const SplitParams& p, const CUtens
         }
         if (!ok) break;
         while (ahead < 3) advance();
-        sh.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
+        if constexpr (kSelected<P>) sh.start += blocks_of(cur.L0, cur.cap) + kUnitCost;
         cur = nxt;
         nxt.unit = -1;
         ahead = 0;
@@ -583,6 +602,82 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
     constexpr int C4 = D / 4;
     const int nrows = min(RC, p.rows - u.row0);
     float M = -INFINITY, Ls = 0.f, e[NP];
+#pragma unroll
+    for (int w = 0; w < NP; ++w) e[w] = 0.f;
+    if (lane < nrows) {
+#pragma unroll
+        for (int w = 0; w < NP; ++w) M = fmaxf(M, ml[w * RC + lane].x);
+        if (M != -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < NP; ++w) {
+                e[w] = exp2_approx(ml[w * RC + lane].x - M);
+                Ls += ml[w * RC + lane].y * e[w];
+            }
+        }
+        const int row = u.row0 + lane;
+        const int qi = row / p.group;
+        const int h = u.kvh * p.group + (row - qi * p.group);
+        if (u.slot < 0) {
+            if (p.lse != nullptr)
+                p.lse[static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h] =
+                    Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+        } else {
+            p.part_ml[(static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row] = make_float2(M, Ls);
+        }
+    }
+    const int total = nrows * C4;
+    for (int x0 = 0; x0 < total; x0 += 32) {
+        const int x = x0 + lane;
+        const int r = min(x, total - 1) / C4;
+        const float Mr = __shfl_sync(0xffffffffu, M, r);
+        const float Lr = __shfl_sync(0xffffffffu, Ls, r);
+        float er[NP];
+#pragma unroll
+        for (int w = 0; w < NP; ++w) er[w] = __shfl_sync(0xffffffffu, e[w], r);
+        if (x >= total) continue;
+        const int c4 = x - r * C4;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (Mr != -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < NP; ++w) {
+                const int c = 4 * c4;
+                const float4 v = *reinterpret_cast<const float4*>(o_w[w] + (c / DH) * O_HALF + r * O_ROW + c % DH);
+                O.x += v.x * er[w];
+                O.y += v.y * er[w];
+                O.z += v.z * er[w];
+                O.w += v.w * er[w];
+            }
+        }
+        const int row = u.row0 + r;
+        const int qi = row / p.group;
+        const int h = u.kvh * p.group + (row - qi * p.group);
+        if (u.slot < 0) {
+            const int64_t orow = static_cast<int64_t>(u.seq * p.q_len + qi) * p.hq + h;
+            *reinterpret_cast<float4*>(p.out + orow * D + 4 * c4) =
+                Lr > 0.f ? make_float4(O.x / Lr * p.v_scale, O.y / Lr * p.v_scale, O.z / Lr * p.v_scale,
+                                       O.w / Lr * p.v_scale)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            const int64_t prow = (static_cast<int64_t>(u.slot) * p.hk + u.kvh) * p.rows + row;
+            *reinterpret_cast<float4*>(p.part_o + prow * D + 4 * c4) =
+                make_float4(O.x * p.v_scale, O.y * p.v_scale, O.z * p.v_scale, O.w * p.v_scale);
+        }
+    }
+}
+
+// merge_unit for fdec_run_selected: 16-bit or fp32 rows, one division a row, the partials
+// of a cut unit in its CTA's slots; and quicker, in more code.  Row by row, RU rows' loads
+// together and a row's values broadcast from its lane once: this one warp's chain of
+// instructions is what a unit's end costs (column group by column group as above, with
+// the row's values and addresses worked out for each: 13 us a unit at head_dim 512, 3.6 us
+// at 128 with 8 rows).
+template <int D, int NP, int RC, int DH, int O_ROW, int O_HALF>
+__device__ __forceinline__ void merge_unit_selected(const SelectedParams& p, const UnitMeta& u, const float2* ml,
+                                           const float* const (&o_w)[NP], int lane) {
+    constexpr float kLn2 = 0.69314718055994530942f;
+    constexpr int C4 = D / 4;
+    const int nrows = min(RC, p.rows - u.row0);
+    float M = -INFINITY, Ls = 0.f, e[NP];
     int64_t dst = 0;  // first element of row `lane` in its destination
 #pragma unroll
     for (int w = 0; w < NP; ++w) e[w] = 0.f;
@@ -612,12 +707,7 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
             dst = prow * D;
         }
     }
-    // Finished rows are O / L * v_scale; with per_head one division a row, v_scale / L.
-    const float norm = p.per_head ? (Ls > 0.f ? p.v_scale / Ls : 0.f) : Ls;
-    // Row by row, RU rows' loads together and a row's values broadcast from its lane once:
-    // this one warp's chain of instructions is what a unit's end costs.  (Column group by
-    // column group, with the row's values and addresses worked out for each: 13 us a unit
-    // at head_dim 512, 3.6 us at 128 with 8 rows.)
+    const float norm = Ls > 0.f ? p.v_scale / Ls : 0.f;
     constexpr int LW = C4 < 32 ? C4 : 32;     // lanes of a row
     constexpr int RS = 32 / LW;               // rows side by side
     constexpr int CG = (C4 + LW - 1) / LW;    // column groups of a lane
@@ -664,22 +754,17 @@ __device__ __forceinline__ void merge_unit(const SplitParams& p, const UnitMeta&
                 if (u.slot >= 0) {
                     O = make_float4(O.x * p.v_scale, O.y * p.v_scale, O.z * p.v_scale, O.w * p.v_scale);
                     *reinterpret_cast<float4*>(to + at + 4 * c4) = O;
-                } else if (p.per_head) {
-                    store_out4(to, p.out_type, at + 4 * c4, make_float4(O.x * n, O.y * n, O.z * n, O.w * n));
                 } else {
-                    *reinterpret_cast<float4*>(to + at + 4 * c4) =
-                        n > 0.f ? make_float4(O.x / n * p.v_scale, O.y / n * p.v_scale, O.z / n * p.v_scale,
-                                              O.w / n * p.v_scale)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                    store_out4(to, p.out_type, at + 4 * c4, make_float4(O.x * n, O.y * n, O.z * n, O.w * n));
                 }
             }
         }
     }
 }
 
-template <int D, bool BF16, bool BM>
+template <int D, bool BF16, bool BM, typename P>
 __global__ void __launch_bounds__(PersistLayout<D, BM>::THREADS, PersistLayout<D, BM>::CTAS_PER_SM)
-split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmk,
+split_mma_persist_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv) {
     using Lay = PersistLayout<D, BM>;
     using W = MmaWarp<D, BF16, false, false, Lay::BOXMAJ>;
@@ -718,7 +803,7 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
     first.unit = -1;
     Share share = {0, 0, 1, 1};
     if (warp == NW) {
-        if (!p.shares) {
+        if (!in_shares(p)) {
             first.unit = blockIdx.x;
             punit_load_item(p, first, p.hk * ((p.rows + RC - 1) / RC));  // plan data
         }
@@ -727,8 +812,10 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
         // it may still read or write is touched only after that kernel has completed.  The
         // consumers' reads and writes follow the producer's stages.
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (p.shares) share_first(p, first, share, lane);
-        if (first.unit >= 0)
+        if constexpr (kSelected<P>) {
+            if (p.shares) share_first(p, first, share, lane);
+        }
+        if (!in_shares(p) || first.unit >= 0)
             punit_load_lens_pages(p, first, lane, tma_mode ? min(1 << p.page_shift, kStageTokens) : 1, tma_mode);
     }
     if (threadIdx.x == 0) {
@@ -841,7 +928,10 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
         for (int w = 0; w < NP; ++w)
             o_w[w] = reinterpret_cast<const float*>(stages + ((kept0 + w) % S) * G::STAGE_BYTES + Lay::O_BASE);
         const UnitMeta u = um[cb];
-        merge_unit<D, NP, RC, DH, Lay::O_ROW, Lay::O_HALF>(p, u, ml, o_w, lane);
+        if constexpr (kSelected<P>)
+            merge_unit_selected<D, NP, RC, DH, Lay::O_ROW, Lay::O_HALF>(p, u, ml, o_w, lane);
+        else
+            merge_unit<D, NP, RC, DH, Lay::O_ROW, Lay::O_HALF>(p, u, ml, o_w, lane);
         __syncwarp();
         if (lane == 0) {
             cnt[cb] = 0;
@@ -854,8 +944,8 @@ split_mma_persist_kernel(const __grid_constant__ SplitParams p, const __grid_con
     if (!ok && lane == 0) atomicOr(p.err, FDEC_DEVERR_TIMEOUT);
 }
 
-template <int D, bool BF16, bool BM>
-cudaError_t launch_split_mma_persist_one(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+template <int D, bool BF16, bool BM, typename P>
+cudaError_t launch_split_mma_persist_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                          dim3 grid, cudaStream_t stream, bool launch) {
     using Lay = PersistLayout<D, BM>;
     static unsigned long long attr_done = 0;  // one bit per device
@@ -863,7 +953,7 @@ cudaError_t launch_split_mma_persist_one(const SplitParams& p, const CUtensorMap
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(split_mma_persist_kernel<D, BF16, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(split_mma_persist_kernel<D, BF16, BM, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Lay::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
@@ -881,7 +971,44 @@ cudaError_t launch_split_mma_persist_one(const SplitParams& p, const CUtensorMap
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_mma_persist_kernel<D, BF16, BM>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, split_mma_persist_kernel<D, BF16, BM, P>, p, tk, tv);
+}
+
+template <int D, typename P>
+cudaError_t launch_persist_d(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, bool bf16,
+                                   dim3 grid, cudaStream_t s, bool launch) {
+    if (!launch) {  // set-up only (plan upload): both layouts' kernel attributes
+        cudaError_t e = bf16 ? launch_split_mma_persist_one<D, true, true>(p, tk, tv, grid, s, false)
+                             : launch_split_mma_persist_one<D, false, true>(p, tk, tv, grid, s, false);
+        if (e != cudaSuccess) return e;
+        return bf16 ? launch_split_mma_persist_one<D, true, false>(p, tk, tv, grid, s, false)
+                    : launch_split_mma_persist_one<D, false, false>(p, tk, tv, grid, s, false);
+    }
+    const bool small_pages = p.page_shift == 3 || p.page_shift == 4;  // several TMA boxes per stage
+    if (small_pages)
+        return bf16 ? launch_split_mma_persist_one<D, true, true>(p, tk, tv, grid, s, true)
+                    : launch_split_mma_persist_one<D, false, true>(p, tk, tv, grid, s, true);
+    return bf16 ? launch_split_mma_persist_one<D, true, false>(p, tk, tv, grid, s, true)
+                : launch_split_mma_persist_one<D, false, false>(p, tk, tv, grid, s, true);
+}
+
+template <typename P>
+cudaError_t launch_persist(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim, bool bf16,
+                                  dim3 grid, cudaStream_t s, bool launch) {
+    switch (head_dim) {
+        case 64:
+            return launch_persist_d<64>(p, tk, tv, bf16, grid, s, launch);
+        case 128:
+            return launch_persist_d<128>(p, tk, tv, bf16, grid, s, launch);
+        case 192:
+            return launch_persist_d<192>(p, tk, tv, bf16, grid, s, launch);
+        case 256:
+            return launch_persist_d<256>(p, tk, tv, bf16, grid, s, launch);
+        case 512:
+            return launch_persist_d<512>(p, tk, tv, bf16, grid, s, launch);
+        default:
+            return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace fdec

@@ -5,16 +5,13 @@
 
 namespace fdec {
 
-cudaError_t launch_split_tc_wide(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+cudaError_t launch_split_tc_wide(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
                                  bool bf16, dim3 grid, cudaStream_t s, bool launch);
 size_t split_tc_wide_smem_bytes(int head_dim);
 
-cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles, int head_dim,
-                            bool bf16, dim3 grid, cudaStream_t s, bool launch) {
-    if (head_dim == 192 || head_dim == 256) {
-        if (tiles != 1) return cudaErrorInvalidValue;
-        return launch_split_tc_wide(p, tk, tv, head_dim, bf16, grid, s, launch);
-    }
+template <typename P>
+static cudaError_t launch_tc(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles, int head_dim, bool bf16,
+                             dim3 grid, cudaStream_t s, bool launch) {
     if (head_dim == 64) {
         if (tiles == 1)
             return bf16 ? launch_split_tc_one<1, 64, true>(p, tk, tv, grid, s, launch)
@@ -32,6 +29,19 @@ cudaError_t launch_split_tc(const SplitParams& p, const CUtensorMap& tk, const C
                         : launch_split_tc_one<2, 128, false>(p, tk, tv, grid, s, launch);
     }
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_split_tc(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int tiles,
+                            int head_dim, bool bf16, dim3 grid, cudaStream_t s, bool launch) {
+    if (head_dim == 192 || head_dim == 256) {
+        if (tiles != 1) return cudaErrorInvalidValue;
+        return launch_split_tc_wide(p, tk, tv, head_dim, bf16, grid, s, launch);
+    }
+    if (!launch || p.per_head) {  // set-up (plan upload): both forms' kernel attributes
+        const cudaError_t e = launch_tc(p, tk, tv, tiles, head_dim, bf16, grid, s, launch);
+        if (e != cudaSuccess || launch) return e;
+    }
+    return launch_tc(static_cast<const SplitParams&>(p), tk, tv, tiles, head_dim, bf16, grid, s, launch);
 }
 
 size_t split_tc_smem_bytes(int tiles, int head_dim) {

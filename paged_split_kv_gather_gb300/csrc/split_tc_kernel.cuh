@@ -111,9 +111,9 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-template <int NT, int D, bool BF16>
+template <int NT, int D, bool BF16, typename P>
 __global__ void __launch_bounds__(TcLayout<NT, D, BF16>::THREADS, 1)
-split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmk,
+split_tc_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
     constexpr bool CONV = BF16;  // bf16 caches: V slices converted to f16 where exact
     using Lay = TcLayout<NT, D, CONV>;
@@ -652,22 +652,36 @@ split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ C
                 tmem_ld32(tmem_o + c0, a);
                 tmem_wait_ld();
                 if (row < p.rows) {
-                    float* dst = it.slot < 0 ? p.out : p.part_o;
-                    const int64_t at = (it.slot < 0 ? orow : prow) * D + c0;
-                    const int type = it.slot < 0 ? p.out_type : kOutF32;  // partials are fp32
                     const float f = (it.slot < 0 ? inv : 1.f) * p.v_scale;
+                    float* dst = it.slot < 0 ? p.out + orow * D + c0 : p.part_o + prow * D + c0;
+                    if constexpr (kSelected<P>) {
+                        if (it.slot < 0 && p.out_type != kOutF32) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4)
+                                store_out4(p.out, p.out_type, orow * D + c0 + c,
+                                           make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f));
+                            continue;
+                        }
+                    }
 #pragma unroll
                     for (int c = 0; c < 32; c += 4)
-                        store_out4(dst, type, at + c, make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f));
+                        *reinterpret_cast<float4*>(dst + c) =
+                            make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
                 }
             }
         } else {
             // nothing visible (or a failed wait): an empty state
             if (row < p.rows) {
-                float* dst = it.slot < 0 ? p.out : p.part_o;
-                const int64_t at = (it.slot < 0 ? orow : prow) * D;
-                const int type = it.slot < 0 ? p.out_type : kOutF32;
-                for (int c = 0; c < D; c += 4) store_out4(dst, type, at + c, make_float4(0.f, 0.f, 0.f, 0.f));
+                float* dst = it.slot < 0 ? p.out + orow * D : p.part_o + prow * D;
+                bool half_width = false;
+                if constexpr (kSelected<P>) half_width = it.slot < 0 && p.out_type != kOutF32;
+                if (half_width) {
+                    if constexpr (kSelected<P>)
+                        for (int c = 0; c < D; c += 4)
+                            store_out4(p.out, p.out_type, orow * D + c, make_float4(0.f, 0.f, 0.f, 0.f));
+                } else {
+                    for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
             }
             m = -INFINITY;
             l = 0.f;
@@ -689,15 +703,15 @@ split_tc_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ C
     }
 }
 
-template <int NT, int D, bool BF16>
-cudaError_t launch_split_tc_one(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+template <int NT, int D, bool BF16, typename P>
+cudaError_t launch_split_tc_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                                 cudaStream_t stream, bool launch) {
     static unsigned long long attr_done = 0;  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(split_tc_kernel<NT, D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(split_tc_kernel<NT, D, BF16, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  TcLayout<NT, D, BF16>::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
@@ -713,7 +727,7 @@ cudaError_t launch_split_tc_one(const SplitParams& p, const CUtensorMap& tk, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_tc_kernel<NT, D, BF16>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, split_tc_kernel<NT, D, BF16, P>, p, tk, tv);
 }
 
 }  // namespace fdec

@@ -5,8 +5,9 @@
 
 namespace fdec {
 
-cudaError_t launch_split_tc_wide(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
-                                 bool bf16, dim3 grid, cudaStream_t s, bool launch) {
+template <typename P>
+static cudaError_t launch_wide(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim, bool bf16, dim3 grid,
+                               cudaStream_t s, bool launch) {
     if (head_dim == 192)
         return bf16 ? launch_split_tc_one<1, 192, true>(p, tk, tv, grid, s, launch)
                     : launch_split_tc_one<1, 192, false>(p, tk, tv, grid, s, launch);
@@ -14,6 +15,15 @@ cudaError_t launch_split_tc_wide(const SplitParams& p, const CUtensorMap& tk, co
         return bf16 ? launch_split_tc_one<1, 256, true>(p, tk, tv, grid, s, launch)
                     : launch_split_tc_one<1, 256, false>(p, tk, tv, grid, s, launch);
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_split_tc_wide(const SelectedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int head_dim,
+                                 bool bf16, dim3 grid, cudaStream_t s, bool launch) {
+    if (!launch || p.per_head) {  // set-up (plan upload): both forms' kernel attributes
+        const cudaError_t e = launch_wide(p, tk, tv, head_dim, bf16, grid, s, launch);
+        if (e != cudaSuccess || launch) return e;
+    }
+    return launch_wide(static_cast<const SplitParams&>(p), tk, tv, head_dim, bf16, grid, s, launch);
 }
 
 size_t split_tc_wide_smem_bytes(int head_dim) {
