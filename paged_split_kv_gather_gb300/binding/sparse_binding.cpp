@@ -84,14 +84,20 @@ int as_int(int64_t v) {
     return static_cast<int>(v);
 }
 
+// The stride of a dimension; 0 for one of a single index, whose stride may be anything.
+int64_t step(const Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
+// Entries between two rows of a page table.
+int64_t table_stride(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
 fdec_kv_desc pool(const Tensor& t) {
     need(t.dim() == 4 && t.stride(3) == 1, "caches must be 4-D [page, kv_head, slot, dim] with a unit dim stride");
-    return {t.data_ptr(), t.size(0), t.stride(0), t.stride(1), t.stride(2)};
+    return {t.data_ptr(), t.size(0), step(t, 0), step(t, 1), step(t, 2)};
 }
 
 fdec_rows rows(const Tensor& t) {
     need(t.dim() == 3 && t.stride(2) == 1, "rows must be [n, heads, head_dim] with a unit dim stride");
-    return {t.data_ptr(), t.stride(0), t.stride(1)};
+    return {t.data_ptr(), step(t, 0), step(t, 1)};
 }
 
 const int32_t* index(const Tensor& t, int64_t dim, const char* what) {
@@ -117,12 +123,12 @@ uint32_t* error_word(const Tensor& t) {
 void q_strides(const Tensor& q, int64_t* tok, int64_t* head) {
     need(q.dim() == 4 && q.stride(3) == 1, "q must be [B, Q, Hq, D] with a unit head_dim stride");
     if (q.size(1) == 1) {
-        *tok = q.stride(0);
+        *tok = step(q, 0);
     } else {
         need(q.size(0) <= 1 || q.stride(0) == q.size(1) * q.stride(1), "q tokens must flatten to one stride (b*q_len + i)");
         *tok = q.stride(1);
     }
-    *head = q.stride(2);
+    *head = step(q, 2);
 }
 
 decltype(&fdec_norm_rope_append) g_norm_rope_append = nullptr;
@@ -189,7 +195,7 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                   cs.defined() ? as_int(cs.size(1)) : 0, PyObject_IsTrue(a[14]), bi_p, pos_p, rope_p,
                                   as_int(n), as_int(hq), as_int(hk), as_int(d), page_size, dtype, kv, real(a[16]),
                                   real(a[17]), rows(q_out), pool(k), pool(v), table_p, as_int(table.size(0)),
-                                  table.stride(0), error_word(errors), stream_of(a[19]));
+                                  table_stride(table), error_word(errors), stream_of(a[19]));
     });
 }
 
@@ -215,7 +221,7 @@ PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         int64_t expected = integer(a[6]);
         if (expected <= 0) expected = table.size(1) * page_size;
         if (expected > INT32_MAX) expected = INT32_MAX;
-        return g_page_bounds(pool(k), pool(bounds), table_p, as_int(table.size(0)), table.stride(0), begins_p, lens_p,
+        return g_page_bounds(pool(k), pool(bounds), table_p, as_int(table.size(0)), table_stride(table), begins_p, lens_p,
                              as_int(k.size(1)), as_int(k.size(3)), page_size, dtype, kv, static_cast<int>(expected),
                              error_word(errors), stream_of(a[8]));
     });
@@ -253,7 +259,7 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         need(counts.size(0) == b * q_len && counts.size(1) == hk && counts.is_contiguous(),
              "counts must be contiguous [B * Q, Hk]");
         on(q, {&bounds, &table, &lens, &ids, &counts, &indices, &ws, &errors});
-        return g_select_pages(q.data_ptr(), tok, head, pool(bounds), table_p, table.stride(0), lens_p, as_int(b),
+        return g_select_pages(q.data_ptr(), tok, head, pool(bounds), table_p, table_stride(table), lens_p, as_int(b),
                               as_int(q_len), page_size, as_int(hq), as_int(hk), as_int(d), dtype,
                               PyObject_IsTrue(a[13]), max_pages, budget, small(a[11], "first_pages"),
                               small(a[12], "last_pages"), static_cast<int32_t*>(ids.data_ptr()),

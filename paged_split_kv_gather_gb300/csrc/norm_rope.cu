@@ -278,12 +278,23 @@ cudaError_t launch_rows(const NormRopeParams& p, bool pairs, int num_sms, cudaSt
     using R = RowLanes<D>;
     const int groups = (p.hq + R::RPW - 1) / R::RPW + 2 * ((p.hk + R::RPW - 1) / R::RPW);
     const int64_t slots = static_cast<int64_t>(num_sms) * kRowsCtas * (kRowsThreads / 32);
-    // Warps per token: one while the tokens alone take half of the machine's warps, else
-    // enough that they do (a warp then takes every wpt-th group of rows, and computes the
-    // token's coefficients again: 2036 tokens take 12.6 us with one warp each, 14.5 with two).
-    int wpt = 1;
-    while (wpt < groups && static_cast<int64_t>(p.n_tokens) * wpt * 2 <= slots) wpt *= 2;
-    wpt = std::min(wpt, groups);
+    // Warps per token (a warp takes every wpt-th group of rows, and computes the token's
+    // coefficients again): all the groups' own while they fit the machine at once, else the
+    // number with the least (rounds of the machine) x (a token's set-up, about four groups,
+    // + a warp's groups).  One warp each, 2036 tokens take 12.6 us, with two 14.5; but 2457
+    // tokens of 24 groups, a little over one round, 38.7 us with one.
+    int wpt = groups;
+    if (static_cast<int64_t>(p.n_tokens) * groups > slots) {
+        int64_t best = INT64_MAX;
+        for (int w = 1; w <= std::min(groups, 8); ++w) {
+            const int64_t rounds = (static_cast<int64_t>(p.n_tokens) * w + slots - 1) / slots;
+            const int64_t cost = rounds * (4 + (groups + w - 1) / w);
+            if (cost < best) {
+                best = cost;
+                wpt = w;
+            }
+        }
+    }
     // A warp has two groups at most: the form without loads ahead is shorter code, which a
     // call of a few tokens mostly waits to fetch (64 tokens: 3.2 against 3.6 us).
     const bool single = groups <= 2 * wpt;

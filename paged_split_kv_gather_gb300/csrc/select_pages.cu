@@ -27,6 +27,7 @@
 // choosing CTAs' registers and shared memory halved what streams beside them: 86 us
 // against the two launches' figure below on the batch of 64.)
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -51,10 +52,14 @@ struct SelShape {
     static constexpr int LPP = D == 64 || D == 192 ? 16 : 32;  // lanes per page
     static constexpr int CPL = CHUNKS / LPP;
     static constexpr int PPW = 32 / LPP;                       // pages per load instruction
-    static constexpr int U = CPL == 3 ? 4 : 8 / CPL;           // load groups in flight
-    // Two CTAs an SM: with three (80 registers a thread) the compiler keeps fewer of the
-    // loads in flight (head_dim 192, batch of 64: 94 against 76 us).
-    static constexpr int CTAS = 2;
+    static constexpr int U = CPL <= 1 ? 8 : CPL <= 3 ? 4 : 2;  // page groups of a round
+    // Rounds of a warp that its ring of shared memory holds, all but one of them in flight
+    // while it computes: 12 or 16 loads of 16 bytes a thread beside those computed on.  As
+    // registers there was room for 8 to 12 and none beside (a batch of 64 ragged rows, the
+    // whole call: 71 us; rounds of half the size 68, of a quarter 80; this 66).
+    static constexpr int R = 24 / (U * CPL);
+    static constexpr int CTAS = 2;  // resident an SM
+    static constexpr int SMEM = R * U * CPL * kScoreThreads * 16;
 };
 
 // Loads that stay where they are written: scores of other CTAs, after their counter.
@@ -231,12 +236,16 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.pt_stride;
     const int sub = lane / LPP, l = lane - sub * LPP;
     const int begin = chunk * p.chunk;
-    int next_id[U];
+    // Ids of this warp's round k (0 where there is none).
+    auto load_ids = [&](int k, int stop, int (&id)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = begin + (warp + u * kScoreWarps) * PPW + sub;
-        next_id[u] = p.first + i < p.max_pages && i < begin + p.chunk ? table[p.first + i] : 0;
-    }
+        for (int u = 0; u < U; ++u) {
+            const int i = begin + (warp + (k * U + u) * kScoreWarps) * PPW + sub;
+            id[u] = i < stop ? table[p.first + i] : 0;
+        }
+    };
+    int id[U];
+    load_ids(0, min(begin + p.chunk, p.max_pages - p.first), id);
     const uint16_t* q = p.q + tok * p.q_st + static_cast<int64_t>(h) * p.group * p.q_sh;
     float q0[8];  // element tid of the group's first eight heads
 #pragma unroll
@@ -280,41 +289,53 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     for (int c = 0; c < CPL; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) top[c][k] = 0u;
-    for (int i0 = begin + warp * PPW; i0 < end; i0 += kScoreWarps * PPW * U) {
-        uint4 raw[U][CPL];
-        const int id0 = __shfl_sync(0xffffffffu, next_id[0], 0);
-        unsigned bad = 0u;  // groups of this round whose page id is outside the pool: page 0 is read instead
+    // The bounds come through a ring in shared memory of which each thread reads only what
+    // it has copied itself: its own copies' completion is all it waits for.
+    extern __shared__ __align__(16) uint4 ring[];
+    const int n_rounds = max(0, (end - (begin + warp * PPW) + kScoreWarps * PPW * U - 1) / (kScoreWarps * PPW * U));
+    uint64_t bad = 0u;  // per round in flight, U bits: groups whose page id is outside the pool (page 0 is read)
+    auto issue = [&](int k) {
+        bad <<= U;
+        if (k < n_rounds) {
+            const int id0 = __shfl_sync(0xffffffffu, id[0], 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            // groups past the end read the round's first page again; nothing is stored for them
-            const int id = i0 + u * kScoreWarps * PPW + sub < end ? next_id[u] : id0;
-            const bool in = id >= 0 && id < p.b_pages;
-            if (!in) bad |= 1u << u;
-            const uint8_t* rows = base + static_cast<int64_t>(in ? id : 0) * p.b_sp;
+            for (int u = 0; u < U; ++u) {
+                // groups past the end read the round's first page again; nothing is stored for them
+                const int i = begin + (warp + (k * U + u) * kScoreWarps) * PPW + sub;
+                const int from = i < end ? id[u] : id0;
+                const bool in = from >= 0 && from < p.b_pages;
+                if (!in) bad |= 1u << u;
+                const uint8_t* rows = base + static_cast<int64_t>(in ? from : 0) * p.b_sp;
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) raw[u][c] = *reinterpret_cast<const uint4*>(rows + off[c]);
+                for (int c = 0; c < CPL; ++c)
+                    cp_async_16(smem_addr(&ring[(((k % S::R) * U + u) * CPL + c) * kScoreThreads + tid]), rows + off[c]);
+            }
+            load_ids(k + 1, end, id);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {  // the ids of the next round travel with this one's rows
-            const int i = i0 + (kScoreWarps * U + u * kScoreWarps) * PPW + sub;
-            next_id[u] = i < end ? table[p.first + i] : 0;
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int k = 0; k < S::R - 1; ++k) issue(k);
+#pragma unroll 1
+    for (int k = 0; k < n_rounds; ++k) {
+        issue(k + S::R - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::R - 1) : "memory");
         float2 a[U];  // even and odd elements
 #pragma unroll
         for (int u = 0; u < U; ++u) a[u] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            // from shared memory each round: as registers they would cost loads in flight
             const float4 w0 = s_w[0][l + LPP * c], w1 = s_w[1][l + LPP * c];
             const float2 w[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
                                  make_float2(w1.z, w1.w)};
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t v[4] = {raw[u][c].x, raw[u][c].y, raw[u][c].z, raw[u][c].w};
+                const uint4 raw = ring[(((k % S::R) * U + u) * CPL + c) * kScoreThreads + tid];
+                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    a[u] = __ffma2_rn(unpack2<BF16>(v[k]), w[k], a[u]);
-                    top[c][k] = max_u16x2(top[c][k], v[k] & 0x7fff7fffu);
+                for (int e = 0; e < 4; ++e) {
+                    a[u] = __ffma2_rn(unpack2<BF16>(v[e]), w[e], a[u]);
+                    top[c][e] = max_u16x2(top[c][e], v[e] & 0x7fff7fffu);
                 }
             }
         }
@@ -323,16 +344,13 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
         for (int u = 0; u < U; ++u) s[u] = a[u].x + a[u].y;
         fold<U, LPP / 2>(s, lane);
         constexpr int LPU = LPP / U;  // lanes that end up with the same page
+        const unsigned out = static_cast<unsigned>(bad >> (U * (S::R - 1))) & ((1u << U) - 1u);
         if (l % LPU == 0) {
             const int u = l / LPU;
-            const int i = i0 + u * kScoreWarps * PPW + sub;
-            if (i < end) scores[i] = (bad >> u) & 1u ? -INFINITY : s[0];
-        }
-        if (l == 0) {
-            if (bad != 0u && p.err != nullptr) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (((bad >> u) & 1u) && i0 + u * kScoreWarps * PPW + sub < end) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
+            const int i = begin + (warp + (k * U + u) * kScoreWarps) * PPW + sub;
+            if (i < end) {
+                scores[i] = (out >> u) & 1u ? -INFINITY : s[0];
+                if (((out >> u) & 1u) && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
             }
         }
     }
@@ -709,6 +727,19 @@ cudaLaunchConfig_t dependent_launch(int64_t blocks, int threads, cudaStream_t s,
     return cfg;
 }
 
+// Allow the scoring kernel its shared memory, once per kernel and device.
+template <int D, bool BF16>
+cudaError_t allow_score_smem() {
+    static std::atomic<unsigned long long> done{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) & (1ull << dev))) return cudaSuccess;
+    e = cudaFuncSetAttribute(score_pages_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SelShape<D>::SMEM);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
 template <int D>
 cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
@@ -726,7 +757,10 @@ cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s
     p.n_chunks = static_cast<int>((cand + chunk - 1) / chunk);
     p.chain = 4 * SelShape<D>::CPL;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = dependent_launch(rows * p.n_chunks, kScoreThreads, s, attr);
+    cudaLaunchConfig_t cfg = dependent_launch(rows * p.n_chunks, kScoreThreads, s, attr);
+    cfg.dynamicSmemBytes = SelShape<D>::SMEM;
+    const cudaError_t e = bf16 ? allow_score_smem<D, true>() : allow_score_smem<D, false>();
+    if (e != cudaSuccess) return e;
     return bf16 ? cudaLaunchKernelEx(&cfg, score_pages_kernel<D, true>, p)
                 : cudaLaunchKernelEx(&cfg, score_pages_kernel<D, false>, p);
 }

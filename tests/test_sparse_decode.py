@@ -456,6 +456,7 @@ ATTEND = [
     ("bf16", "", 128, 64, 2, 16, 21, 3, "hnd"), ("f16", "", 256, 70, 2, 64, 6, 3, "nhd"),
     ("bf16", "fp8", 128, 32, 8, 16, 40, 5, "nhd"), ("f16", "fp8", 256, 8, 2, 64, 11, 5, "hnd"),
     ("bf16", "fp8", 128, 40, 2, 128, 3, 3, "interleaved"), ("f16", "", 128, 2, 2, 256, 20, 40, "hnd"),
+    ("f16", "", 64, 4, 4, 64, 10, 1000, "hnd"), ("bf16", "", 64, 5, 1, 8, 65, 33, "nhd"),
 ]
 
 
@@ -747,3 +748,118 @@ def test_run_selected_refusals():
             fn(stream=0, **{**ok, key: value})
     assert lib.fdec_run_selected(None, None, 0, 0, fd.KVDesc(), fd.KVDesc(), None, 0, None, 1.0, 1.0, 1.0, None, 0, None,
                                  None, None) == 1  # a null plan
+
+
+# ------------------------------------------------------------------------------- layouts, offsets, random shapes
+
+@gpu
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 elements: the last pages are written, bounded, scored and attended to."""
+    hk, d, page, pages = 8, 512, 16, 70000
+    k = torch.empty(pages, hk, page, d, dtype=torch.bfloat16, device="cuda")  # 4.6e9 elements
+    v = torch.empty_like(k)
+    assert k.numel() > 2 ** 32
+    own = np.concatenate([np.arange(pages - 150, pages), [3]])
+    k[torch.as_tensor(own).cuda()] = torch.randn(151, hk, page, d, device="cuda").bfloat16()
+    v[torch.as_tensor(own).cuda()] = torch.randn(151, hk, page, d, device="cuda").bfloat16()
+    table = np.random.default_rng(1).permutation(own)[None]
+    L = 151 * page - 3
+    qkv = torch.randn(1, 8 + 2 * hk, d, device="cuda").bfloat16()
+    q_out = torch.empty(1, 8, d, dtype=torch.bfloat16, device="cuda")
+    fd.fdec_norm_rope_append(qkv[:, :8], qkv[:, 8:16], qkv[:, 16:], None, None, None, i32([0]), i32([L - 1]), q_out, k, v,
+                             i32(table), page)
+    where = int(table[0, (L - 1) // page])
+    assert torch.equal(v[where, :, (L - 1) % page], qkv[0, 16:])
+    bounds = torch.zeros(pages, hk, 2, d, dtype=torch.bfloat16, device="cuda")
+    fd.fdec_page_bounds(k, bounds, i32(table), None, i32([L]), page)
+    for j in (0, 77, 150):
+        rows = k[int(table[0, j]), :, : min(page, L - j * page)]
+        assert torch.equal(bounds[int(table[0, j])], torch.stack([rows.amin(1), rows.amax(1)], 1))
+    q = q_out.view(1, 1, 8, d)
+    sel = fd.PageSelect(1, 1, page, 8, hk, d, 151, 30, "bf16")
+    ids, counts, index = sel.run(q, bounds, i32(table), i32([L]))
+    rows_of = torch.as_tensor(table[0]).cuda()
+    want = select_reference(q, bounds[rows_of].contiguous(), np.arange(151)[None], [L], page, 30, 1, 1, True)
+    assert np.array_equal(index.cpu().numpy(), want[2]) and np.array_equal(counts.cpu().numpy(), want[1])
+    pd = fd.PagedDecode([30 * page], 1, page, 8, hk, d, "bf16")
+    out, lse = torch.empty(1, 1, 8, d, device="cuda"), torch.empty(1, 1, 8, device="cuda")
+    pd.run_selected(q, k, v, ids, counts, out, lse)
+    assert pd.device_errors() == 0
+    local = index.cpu().numpy()
+    ref = attend_reference(q, k[rows_of].contiguous(), v[rows_of].contiguous(), local, counts.cpu().numpy(), 1 / math.sqrt(d))
+    assert_attention(out, lse, *ref)
+
+
+@gpu
+def test_select_pages_of_other_layouts():
+    """q off 16 bytes and head-major, bounds with the two sides apart, a page table wider than max_pages."""
+    t, d, hk, hq, width = torch.float16, 128, 2, 8, 60
+    table = np.random.default_rng(3).permutation(120).reshape(2, 60)
+    wide = np.concatenate([table, np.full((2, 9), -1)], 1)
+    lens = [60 * 16, 41 * 16 + 3]
+    plain = bounds_like(120, hk, d, t, 4)
+    sides = plain.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)      # [2, pages, Hk, D]
+    heads = plain.transpose(0, 1).contiguous().transpose(0, 1)              # [Hk, pages, 2, D]
+    q = torch.randn(2, 1, hq, d, generator=torch.Generator().manual_seed(5)).to(t).cuda()
+    odd = torch.zeros(q.numel() + 1, dtype=t, device="cuda")[1:].view(q.shape)
+    odd.copy_(q)
+    major = q.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)          # [Hq, B, Q, D]
+    want = select_reference(q, plain, table, lens, 16, 12, 1, 2, True)
+    for qq in (q, odd, major):
+        for bb in (plain, sides, heads):
+            got = run_select(qq, bb, wide, lens, 16, 12, 1, 2, max_pages=width)
+            for a, c in zip(got, want):
+                assert np.array_equal(a, c)
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(24))
+def test_random_steps(seed):
+    """Random shapes through the four operators in turn, each against its formula on what the last one wrote."""
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([64, 128, 128, 192, 256, 512]))
+    kv = "fp8" if d in (128, 256) and rng.random() < 0.4 else ""
+    dtype = str(rng.choice(["bf16", "f16"]))
+    hk = int(rng.integers(1, 5))
+    hq = hk * int(rng.choice([1, 2, 3, 4, 8, 17]))
+    page = int(rng.choice([1, 2, 4, 8, 16, 32, 64, 128, 256]))
+    seqs, q_len = int(rng.integers(1, 6)), int(rng.choice([1, 1, 2, 5]))
+    width = int(rng.integers(3, 40))
+    lens = [int(x) for x in rng.integers(q_len, width * page + 1, seqs)] if width * page > q_len else [q_len] * seqs
+    width = max(width, -(-q_len // page))
+    first, last = int(rng.integers(0, 3)), int(rng.integers(1, 4))
+    budget = first + last + int(rng.integers(0, 12))
+    rot = int(rng.choice([0, 16, d // 2, d]))
+    layout = str(rng.choice(["hnd", "nhd", "interleaved"]))
+    t = DT[dtype]
+    pages = seqs * width + 1
+    k, v = make_pool(pages, hk, page, d, kv or dtype, layout, seed)
+    table = rng.permutation(pages)[: seqs * width].reshape(seqs, width)
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(seqs * q_len, hq + 2 * hk, d, generator=g).to(t).cuda()
+    raw = qkv.clone()
+    qw = (1 + 0.2 * torch.randn(d, generator=g)).to(t).cuda() if rng.random() < 0.7 else None
+    cos_sin = None
+    if rot:
+        ang = np.arange(width * page)[:, None] * 10000.0 ** (-np.arange(rot // 2) / (rot // 2))
+        cos_sin = torch.as_tensor(np.concatenate([np.cos(ang), np.sin(ang)], 1), dtype=torch.float32).cuda()
+    bounds = torch.zeros(pages, hk, 2, d, dtype=t, device="cuda")
+    fd.fdec_page_bounds(k, bounds, i32(table), None, i32(lens) - q_len, page)
+    ks, vs = (0.125, 0.0625) if kv else (1.0, 1.0)
+    inter = bool(rng.random() < 0.5)
+    sd = fd.SparseDecode([width * page] * seqs, q_len, page, hq, hk, d, budget, dtype, first, last, kv_dtype=kv)
+    out = torch.empty(seqs * q_len, 1, hq, d, dtype=t, device="cuda")
+    lse = torch.empty(seqs * q_len, 1, hq, device="cuda")
+    sd.step(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], qw, qw, cos_sin, k, v, bounds, i32(table), i32(lens), out,
+            lse, interleaved=inter, k_scale=ks, v_scale=vs)
+    assert sd.device_errors() == 0
+    pos = np.concatenate([np.arange(L - q_len, L) for L in lens])
+    assert_rounded(qkv[:, :hq].clone(), *norm_rope_reference(raw[:, :hq], qw, cos_sin, pos, inter, 1e-6))
+    fresh = torch.zeros_like(bounds)
+    fd.fdec_page_bounds(k, fresh, i32(table), None, i32(lens), page)
+    assert torch.equal(fresh, bounds)
+    q = qkv[:, :hq]
+    ids, counts, _ = select_reference(q.reshape(seqs, q_len, hq, d), bounds, table, lens, page, budget, first, last, True)
+    assert np.array_equal(sd.select.page_ids.cpu().numpy(), ids) and np.array_equal(sd.select.counts.cpu().numpy(), counts)
+    ref = attend_reference(q.reshape(-1, 1, hq, d), k.float() * ks, v.float() * vs, ids, counts, 1 / math.sqrt(d))
+    assert_attention(out, lse, *ref)
