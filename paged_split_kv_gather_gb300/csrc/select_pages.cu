@@ -21,11 +21,14 @@
 // Two launches.  score_pages_kernel streams the bounds: a row (query token, KV head) is
 // cut into chunks of pages, one CTA each.  choose_pages_kernel, its programmatic
 // dependent, has one CTA a row: the row's scores go to shared memory, the bin of the
-// K-th largest among 256 over their range is found, and the few scores in that bin are
-// compared with each other.  (Choosing in the row's last CTA to finish scoring, counted
-// by an atomic, was measured first: the count's fences cost every CTA 1.4-2.1 us and the
-// choosing CTAs' registers and shared memory halved what streams beside them: 86 us
-// against the two launches' figure below on the batch of 64.)
+// K-th largest among 256 over their range is found, and the few scores in and near that
+// bin are compared with each other.  (Choosing in the row's last CTA to finish scoring,
+// counted by an atomic, was measured first: the count's fences cost every CTA 1.4-2.1 us,
+// and the choosing CTAs' registers and shared memory took from what streams beside them.)
+//
+// GB300, us a call in a stream of calls: 4 rows of 4096 pages (head_dim 128) 9.8, of
+// which scoring 3 and choosing 5; 64 x 8 ragged rows of up to 2048 pages (head_dim 192,
+// 308 MB) 66, scoring 56 of them at 5.5 TB/s; 16 query tokens x 8 heads of 512 pages 13.2.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -210,22 +213,26 @@ __device__ __forceinline__ double score64(const SelectParams& p, const double* w
     return s;
 }
 
-template <int D, bool BF16>
+// QB: query tokens of a sequence that one CTA scores against the pages it reads, 1, 2 or 4
+// (with more of them in the call, q_len / QB such groups).
+template <int D, bool BF16, int QB>
 __global__ void __launch_bounds__(kScoreThreads, SelShape<D>::CTAS)
 score_pages_kernel(const __grid_constant__ SelectParams p) {
     using S = SelShape<D>;
     constexpr int LPP = S::LPP, CPL = S::CPL, PPW = S::PPW, U = S::U;
     // Weights of the chunks (of the minimum row, then of the maximum row): elements 0 .. 3
     // of every chunk, then 4 .. 7 (a warp's 16-byte loads of them meet no bank twice).
-    __shared__ __align__(16) float4 s_w[2][S::CHUNKS];
-    __shared__ float s_abs[kScoreWarps];
+    __shared__ __align__(16) float4 s_w[QB][2][S::CHUNKS];
+    __shared__ float s_abs[QB][kScoreWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / p.n_chunks;  // (sequence, query, KV head)
-    const int chunk = static_cast<int>(blockIdx.x - row * p.n_chunks);
-    const int h = static_cast<int>(row % p.hk);
-    const int64_t tok = row / p.hk;
-    const int b = static_cast<int>(tok / p.q_len);
-    const int qi = static_cast<int>(tok - static_cast<int64_t>(b) * p.q_len);
+    const int64_t unit = blockIdx.x / p.n_chunks;  // (sequence, group of query tokens, KV head)
+    const int chunk = static_cast<int>(blockIdx.x - unit * p.n_chunks);
+    const int h = static_cast<int>(unit % p.hk);
+    const int64_t seq_group = unit / p.hk;
+    const int q_groups = (p.q_len + QB - 1) / QB;
+    const int b = static_cast<int>(seq_group / q_groups);
+    const int qi = static_cast<int>(seq_group - static_cast<int64_t>(b) * q_groups) * QB;  // the first of them
+    const int64_t tok = static_cast<int64_t>(b) * p.q_len + qi;
     // The choosing kernel may start only once every CTA here has passed its wait: it then
     // may read this launch's inputs before its own.
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -250,27 +257,38 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     float q0[8];  // element tid of the group's first eight heads
 #pragma unroll
     for (int g = 0; g < 8; ++g) q0[g] = tid < D && g < p.group ? load_16bit<BF16>(q + g * p.q_sh + tid) : 0.f;
-    const int n_cand = sel_row(p, L, qi).n_cand;
-    if (begin >= n_cand) return;
+    int end[QB], end_all = 0;  // where this chunk ends for each query token (it may not begin)
+#pragma unroll
+    for (int y = 0; y < QB; ++y) {
+        const int n = qi + y < p.q_len ? sel_row(p, L, qi + y).n_cand : 0;
+        end[y] = min(begin + p.chunk, n);
+        end_all = max(end_all, end[y]);
+    }
+    if (begin >= end_all) return;
 
     // ---- the weights of the two bound rows
-    for (int d = tid; d < D; d += kScoreThreads) {
-        float neg = 0.f, pos = 0.f;
-        for (int g0 = 0; g0 < p.group; g0 += 8) {
-            if (d != tid || g0 != 0) {
 #pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    q0[g] = g0 + g < p.group ? load_16bit<BF16>(q + (g0 + g) * p.q_sh + d) : 0.f;
-            }
+    for (int y = 0; y < QB; ++y) {
+        const uint16_t* qy = q + y * p.q_st;
+        const bool there = qi + y < p.q_len;
+        for (int d = tid; d < D; d += kScoreThreads) {
+            float neg = 0.f, pos = 0.f;
+            for (int g0 = 0; g0 < p.group; g0 += 8) {
+                if (y != 0 || d != tid || g0 != 0) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {  // a NaN goes into both sums
-                neg += q0[g] > 0.f ? 0.f : q0[g];
-                pos += q0[g] < 0.f ? 0.f : q0[g];
+                    for (int g = 0; g < 8; ++g)
+                        q0[g] = there && g0 + g < p.group ? load_16bit<BF16>(qy + (g0 + g) * p.q_sh + d) : 0.f;
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {  // a NaN goes into both sums
+                    neg += q0[g] > 0.f ? 0.f : q0[g];
+                    pos += q0[g] < 0.f ? 0.f : q0[g];
+                }
             }
+            float* to = reinterpret_cast<float*>(&s_w[y][(d >> 2) & 1][d / 8]) + (d & 3);
+            to[0] = neg;
+            to[4 * (D / 8)] = pos;
         }
-        float* to = reinterpret_cast<float*>(&s_w[(d >> 2) & 1][d / 8]) + (d & 3);
-        to[0] = neg;
-        to[4 * (D / 8)] = pos;
     }
     __syncthreads();
     const uint8_t* base = p.b_base + h * p.b_sh;
@@ -282,8 +300,8 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     }
 
     // ---- scores of this CTA's pages
-    float* scores = p.scores + row * p.score_stride;
-    const int end = min(begin + p.chunk, n_cand);
+    float* scores = p.scores + (tok * p.hk + h) * p.score_stride;
+    const int64_t q_step = p.hk * p.score_stride;  // to the next query token's scores
     uint32_t top[CPL][4];  // largest magnitude that each of this lane's elements has had
 #pragma unroll
     for (int c = 0; c < CPL; ++c)
@@ -292,7 +310,7 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     // The bounds come through a ring in shared memory of which each thread reads only what
     // it has copied itself: its own copies' completion is all it waits for.
     extern __shared__ __align__(16) uint4 ring[];
-    const int n_rounds = max(0, (end - (begin + warp * PPW) + kScoreWarps * PPW * U - 1) / (kScoreWarps * PPW * U));
+    const int n_rounds = max(0, (end_all - (begin + warp * PPW) + kScoreWarps * PPW * U - 1) / (kScoreWarps * PPW * U));
     uint64_t bad = 0u;  // per round in flight, U bits: groups whose page id is outside the pool (page 0 is read)
     auto issue = [&](int k) {
         bad <<= U;
@@ -302,7 +320,7 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
             for (int u = 0; u < U; ++u) {
                 // groups past the end read the round's first page again; nothing is stored for them
                 const int i = begin + (warp + (k * U + u) * kScoreWarps) * PPW + sub;
-                const int from = i < end ? id[u] : id0;
+                const int from = i < end_all ? id[u] : id0;
                 const bool in = from >= 0 && from < p.b_pages;
                 if (!in) bad |= 1u << u;
                 const uint8_t* rows = base + static_cast<int64_t>(in ? from : 0) * p.b_sp;
@@ -310,7 +328,7 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
                 for (int c = 0; c < CPL; ++c)
                     cp_async_16(smem_addr(&ring[(((k % S::R) * U + u) * CPL + c) * kScoreThreads + tid]), rows + off[c]);
             }
-            load_ids(k + 1, end, id);
+            load_ids(k + 1, end_all, id);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -320,65 +338,76 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
     for (int k = 0; k < n_rounds; ++k) {
         issue(k + S::R - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(S::R - 1) : "memory");
-        float2 a[U];  // even and odd elements
+        float2 a[QB][U];  // even and odd elements
 #pragma unroll
-        for (int u = 0; u < U; ++u) a[u] = make_float2(0.f, 0.f);
+        for (int y = 0; y < QB; ++y)
+#pragma unroll
+            for (int u = 0; u < U; ++u) a[y][u] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            const float4 w0 = s_w[0][l + LPP * c], w1 = s_w[1][l + LPP * c];
-            const float2 w[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
-                                 make_float2(w1.z, w1.w)};
+            float2 w[QB][4];
+#pragma unroll
+            for (int y = 0; y < QB; ++y) {
+                const float4 w0 = s_w[y][0][l + LPP * c], w1 = s_w[y][1][l + LPP * c];
+                w[y][0] = make_float2(w0.x, w0.y), w[y][1] = make_float2(w0.z, w0.w);
+                w[y][2] = make_float2(w1.x, w1.y), w[y][3] = make_float2(w1.z, w1.w);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint4 raw = ring[(((k % S::R) * U + u) * CPL + c) * kScoreThreads + tid];
                 const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    a[u] = __ffma2_rn(unpack2<BF16>(v[e]), w[e], a[u]);
+                    const float2 f = unpack2<BF16>(v[e]);
+#pragma unroll
+                    for (int y = 0; y < QB; ++y) a[y][u] = __ffma2_rn(f, w[y][e], a[y][u]);
                     top[c][e] = max_u16x2(top[c][e], v[e] & 0x7fff7fffu);
                 }
             }
         }
-        float s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u] = a[u].x + a[u].y;
-        fold<U, LPP / 2>(s, lane);
         constexpr int LPU = LPP / U;  // lanes that end up with the same page
         const unsigned out = static_cast<unsigned>(bad >> (U * (S::R - 1))) & ((1u << U) - 1u);
-        if (l % LPU == 0) {
-            const int u = l / LPU;
-            const int i = begin + (warp + (k * U + u) * kScoreWarps) * PPW + sub;
-            if (i < end) {
-                scores[i] = (out >> u) & 1u ? -INFINITY : s[0];
-                if (((out >> u) & 1u) && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
-            }
+        const int u_mine = l / LPU;
+        const int i = begin + (warp + (k * U + u_mine) * kScoreWarps) * PPW + sub;
+        const bool out_mine = (out >> u_mine) & 1u;
+#pragma unroll
+        for (int y = 0; y < QB; ++y) {
+            float s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) s[u] = a[y][u].x + a[y][u].y;
+            fold<U, LPP / 2>(s, lane);
+            if (l % LPU == 0 && i < end[y]) scores[y * q_step + i] = out_mine ? -INFINITY : s[0];
         }
+        if (l % LPU == 0 && i < end_all && out_mine && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
     }
     // A page's sum of magnitudes is at most the sum of each element's largest times its
     // weight (NaN and infinity carry through).
-    float abs_max = 0.f;
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-        const float4 w0 = s_w[0][l + LPP * c], w1 = s_w[1][l + LPP * c];
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    for (int y = 0; y < QB; ++y) {
+        float abs_max = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 t = unpack2<BF16>(top[c][k]);
-            abs_max += t.x * fabsf(w[2 * k]);
-            abs_max += t.y * fabsf(w[2 * k + 1]);
+        for (int c = 0; c < CPL; ++c) {
+            const float4 w0 = s_w[y][0][l + LPP * c], w1 = s_w[y][1][l + LPP * c];
+            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 t = unpack2<BF16>(top[c][k]);
+                abs_max += t.x * fabsf(w[2 * k]);
+                abs_max += t.y * fabsf(w[2 * k + 1]);
+            }
         }
+#pragma unroll
+        for (int o = LPP / 2; o > 0; o >>= 1) abs_max += __shfl_xor_sync(0xffffffffu, abs_max, o);
+#pragma unroll
+        for (int o = LPP; o < 32; o <<= 1) abs_max = max_nan(abs_max, __shfl_xor_sync(0xffffffffu, abs_max, o));
+        if (lane == 0) s_abs[y][warp] = abs_max;
     }
-#pragma unroll
-    for (int o = LPP / 2; o > 0; o >>= 1) abs_max += __shfl_xor_sync(0xffffffffu, abs_max, o);
-#pragma unroll
-    for (int o = LPP; o < 32; o <<= 1) abs_max = max_nan(abs_max, __shfl_xor_sync(0xffffffffu, abs_max, o));
-    if (lane == 0) s_abs[warp] = abs_max;
     __syncthreads();
-    if (tid == 0) {
-        float a = s_abs[0];
+    if (tid < QB && qi + tid < p.q_len) {
+        float a = s_abs[tid][0];
 #pragma unroll
-        for (int x = 1; x < kScoreWarps; ++x) a = max_nan(a, s_abs[x]);
-        p.chunk_abs[row * p.abs_stride + chunk] = a;
+        for (int x = 1; x < kScoreWarps; ++x) a = max_nan(a, s_abs[tid][x]);
+        p.chunk_abs[((tok + tid) * p.hk + h) * p.abs_stride + chunk] = a;
     }
 }
 
@@ -388,11 +417,12 @@ struct ChooseShared {
     double weight64[2 * 512];
     int hist[kBins];
     unsigned long long near_key[kNear];
+    uint32_t near_k32[kNear];
     int near_idx[kNear];
     float abs_max[NW];
-    int sum[NW], sum2[NW];
-    uint32_t kmin[NW], kmax[NW];
-    int bin, above, in_bin, near_n, cut_idx;
+    int sum[NW], sum2[NW], sum_hi[NW], sum_taken[NW];  // one use each: no barrier between uses
+    uint32_t kmin[NW], kmax[NW], cut32;
+    int bin, above, near_n, cut_idx;
     unsigned long long cut_key;
 };
 
@@ -465,14 +495,19 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
     // again in each pass, for longer rows).  The loops over them are not unrolled: this
     // code runs once a row, and fetching it costs more than its steps.
     const int n_tiles = (n_cand + kTile - 1) / kTile;
+    uint32_t r_min = ~0u, r_max = 0u;  // range of what this thread has loaded
     auto load = [&](int t) {
         const int n = min(kTile, n_cand - t * kTile);
         const float* src = scores + t * kTile;
         for (int i = 4 * tid; i < n; i += 4 * NT) {  // whole vectors: the row's stride is a multiple of 4
             const float4 f = ld_cg4(src + i);
-            *reinterpret_cast<uint4*>(sm.key + i) =  // -0 as 0
-                make_uint4(ordered(not_nan(f.x) + 0.f), ordered(not_nan(f.y) + 0.f), ordered(not_nan(f.z) + 0.f),
-                           ordered(not_nan(f.w) + 0.f));
+            const uint4 k = make_uint4(ordered(not_nan(f.x) + 0.f), ordered(not_nan(f.y) + 0.f),  // -0 as 0
+                                       ordered(not_nan(f.z) + 0.f), ordered(not_nan(f.w) + 0.f));
+            *reinterpret_cast<uint4*>(sm.key + i) = k;
+            r_min = min(r_min, k.x), r_max = max(r_max, k.x);
+            if (i + 1 < n) r_min = min(r_min, k.y), r_max = max(r_max, k.y);
+            if (i + 2 < n) r_min = min(r_min, k.z), r_max = max(r_max, k.z);
+            if (i + 3 < n) r_min = min(r_min, k.w), r_max = max(r_max, k.w);
         }
         __syncthreads();
     };
@@ -488,14 +523,11 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
             for (int i = tid; i < n; i += NT) f(sm.key[i], t * kTile + i);
         }
     };
-    load(0);
-    uint32_t k_min = ~0u, k_max = 0u;
-    each([&](uint32_t k, int) {
-        k_min = min(k_min, k);
-        k_max = max(k_max, k);
-    });
-    k_min = __reduce_min_sync(0xffffffffu, k_min);
-    k_max = __reduce_max_sync(0xffffffffu, k_max);
+    for (int t = 0; t < n_tiles; ++t) {
+        if (t > 0) __syncthreads();
+        load(t);
+    }
+    uint32_t k_min = __reduce_min_sync(0xffffffffu, r_min), k_max = __reduce_max_sync(0xffffffffu, r_max);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum_abs = max_nan(sum_abs, __shfl_xor_sync(0xffffffffu, sum_abs, o));
     if (lane == 0) {
@@ -509,13 +541,18 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
     // Error of an fp32 score: the weights (group - 1 additions of one sign), a chain of
     // 4 CPL products in each of two sums, 1 + log2(LPP) additions (at most 16 and 6); in
     // units of 2^-24 of the sum of magnitudes, with room for the rounding of that sum.
-    sum_abs = sm.abs_max[0];
-    for (int x = 1; x < NW; ++x) sum_abs = max_nan(sum_abs, sm.abs_max[x]);
+    sum_abs = lane < NW ? sm.abs_max[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum_abs = max_nan(sum_abs, __shfl_xor_sync(0xffffffffu, sum_abs, o));
     const float E = sum_abs * ((p.group + p.chain + 9) * 6.0e-8f) + 1e-37f;
-    // The want-th largest key in [k_min, k_max]: equal bins over that range, then the bin
-    // it is in, until a bin holds few enough to compare each with each.
-    int want = need;
-    uint32_t kth;
+    const bool sure_E = E < INFINITY;
+    const float margin = 2.5f * E;  // 2 E, and a rounding more
+    unsigned long long* key64 = p.near_keys + row * p.max_pages;
+    // The want-th largest key T lies in [k_min, k_max]: 256 equal bins over that range and
+    // the one that T is in, until few keys lie within the margin of that bin.  Keys above
+    // (`hi`) are taken, keys below (`lo`) are not.
+    int want = need, n_near, take_near;
+    uint32_t lo, hi;
     while (true) {
         const int shift = max(0, 24 - __clz(k_max - k_min));  // (k_max - k_min) >> shift < kBins = 256
         each([&](uint32_t k, int) {
@@ -536,75 +573,68 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
         if (tid < kBins && upto - mine < want && want <= upto) {
             sm.bin = kBins - 1 - tid;
             sm.above = upto - mine;
-            sm.in_bin = mine;
         }
         __syncthreads();
         want -= sm.above;
         k_min += static_cast<uint32_t>(sm.bin) << shift;
         k_max = k_min + ((1u << shift) - 1u);
-        if (shift == 0) {
-            kth = k_min;
-            break;
-        }
-        const int n_bin = sm.in_bin;
-        if (n_bin <= kNear) {
-            each([&](uint32_t k, int) {
-                if (k >= k_min && k <= k_max) sm.near_idx[atomicAdd(&sm.near_n, 1)] = static_cast<int>(k);
-            });
-            __syncthreads();
-            if (tid < n_bin) {
-                const uint32_t k = static_cast<uint32_t>(sm.near_idx[tid]);
-                int more = 0, same = 0;
-                for (int y = 0; y < n_bin; ++y) {
-                    const uint32_t o = static_cast<uint32_t>(sm.near_idx[y]);
-                    more += o > k;
-                    same += o == k;
+        lo = sure_E ? ordered(from_ordered(k_min) - margin + 0.f) : 1u;
+        hi = sure_E ? ordered(from_ordered(k_max) + margin + 0.f) : ~0u;
+        int n_hi = 0;
+        each([&](uint32_t k, int i) {
+            n_hi += k > hi;
+            if (k >= lo && k <= hi) {
+                const int x = atomicAdd(&sm.near_n, 1);
+                if (x < kNear) {
+                    sm.near_k32[x] = k;
+                    sm.near_idx[x] = i;
                 }
-                if (more < want && want <= more + same) sm.bin = static_cast<int>(k);  // equal keys write the same
             }
-            __syncthreads();
-            kth = static_cast<uint32_t>(sm.bin);
-            break;
-        }
-        if (tid < kBins) sm.hist[tid] = 0;
+        });
+        n_hi = __reduce_add_sync(0xffffffffu, n_hi);
+        if (lane == 0) sm.sum_hi[warp] = n_hi;
         __syncthreads();
-    }
-    const float T = from_ordered(kth);
-    const bool sure_E = E < INFINITY;
-    // 2 E from T, and a rounding more
-    const uint32_t lo = sure_E ? ordered(T - 2.5f * E + 0.f) : 1u;
-    const uint32_t hi = sure_E ? ordered(T + 2.5f * E + 0.f) : ~0u;
-    int n_hi = 0, n_near = 0;
-    each([&](uint32_t k, int) {
-        n_hi += k > hi;
-        n_near += k >= lo && k <= hi;
-    });
-    block_sum2<NW>(n_hi, n_near, sm.sum, sm.sum2);
-    const int take_near = need - n_hi;  // of the pages near the border: 1 .. n_near
-    const bool refine = take_near < n_near;
-    unsigned long long* key64 = p.near_keys + row * p.max_pages;
-    if (refine) {
+        n_hi = __reduce_add_sync(0xffffffffu, lane < NW ? sm.sum_hi[lane] : 0);
+        n_near = sm.near_n;
+        take_near = need - n_hi;  // of the keys near the border: 1 .. n_near
+        if (n_near <= kNear || shift == 0) break;
+        __syncthreads();  // everybody has read the counts
+        if (tid < kBins) sm.hist[tid] = 0;
         if (tid == 0) sm.near_n = 0;
         __syncthreads();
-        auto score_at = [&](int i) {
-            const int id = table[p.first + i];
-            return id >= 0 && id < p.b_pages ? ordered(not_nan(score64<BF16>(p, sm.weight64, id, h, lane)))
-                                             : ordered(-static_cast<double>(INFINITY));
-        };
-        if (n_near <= kNear) {
-            each([&](uint32_t k, int i) {
-                if (k >= lo && k <= hi) sm.near_idx[atomicAdd(&sm.near_n, 1)] = i;
-            });
-            __syncthreads();
+    }
+    auto score_at = [&](int i) {
+        const int id = table[p.first + i];
+        return id >= 0 && id < p.b_pages ? ordered(not_nan(score64<BF16>(p, sm.weight64, id, h, lane)))
+                                         : ordered(-static_cast<double>(INFINITY));
+    };
+    bool refine = true;  // whether the order near the border is that of 64-bit scores
+    if (n_near <= kNear) {
+        int rank = 0;  // of this thread's key among them
+        if (tid < n_near) {
+            const uint32_t k = sm.near_k32[tid];
+            const int i = sm.near_idx[tid];
+            for (int y = 0; y < n_near; ++y)
+                rank += sm.near_k32[y] > k || (sm.near_k32[y] == k && sm.near_idx[y] < i);
+            if (rank == take_near - 1) sm.cut32 = k;
+        }
+        __syncthreads();
+        const float T = from_ordered(sm.cut32);
+        const uint32_t lo_T = sure_E ? ordered(T - margin + 0.f) : 1u;
+        const uint32_t hi_T = sure_E ? ordered(T + margin + 0.f) : ~0u;
+        // fp32 decides unless a key that it leaves out lies within the margin of T
+        refine = __syncthreads_or(tid < n_near && rank >= take_near && sm.near_k32[tid] >= lo_T);
+        if (refine) {
             for (int x = warp; x < n_near; x += NW) {
-                const unsigned long long k = score_at(sm.near_idx[x]);
+                const uint32_t k32 = sm.near_k32[x];
+                const unsigned long long k = k32 > hi_T ? ~0ull : k32 < lo_T ? 0ull : score_at(sm.near_idx[x]);
                 if (lane == 0) sm.near_key[x] = k;
             }
             __syncthreads();
-            for (int x = tid; x < n_near; x += NT) {  // the rank of each among them
-                const unsigned long long k = sm.near_key[x];
-                const int i = sm.near_idx[x];
-                int rank = 0;
+            if (tid < n_near) {
+                const unsigned long long k = sm.near_key[tid];
+                const int i = sm.near_idx[tid];
+                rank = 0;
                 for (int y = 0; y < n_near; ++y)
                     rank += sm.near_key[y] > k || (sm.near_key[y] == k && sm.near_idx[y] < i);
                 if (rank == take_near - 1) {
@@ -612,54 +642,55 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
                     sm.cut_idx = i;
                 }
             }
-        } else {  // many (equal pages, infinities): the key bit by bit, then the index
-            auto sum_of = [&](int n) {
-                int none = 0;
-                block_sum2<NW>(n, none, sm.sum, sm.sum2);
-                return n;
-            };
-            auto near = [&](int i) {
-                const uint32_t k = ordered(not_nan(ld_cg(scores + i)) + 0.f);
-                return k >= lo && k <= hi;
-            };
-            for (int i = warp; i < n_cand; i += NW) {
-                if (!near(i)) continue;
-                const unsigned long long k = score_at(i);
-                if (lane == 0) key64[i] = k;
-            }
-            __threadfence_block();
             __syncthreads();
-            unsigned long long cut = 0;
-            for (int bit = 63; bit >= 0; --bit) {
-                const unsigned long long t = cut | (1ull << bit);
-                int n = 0;
-                for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] >= t;
-                if (sum_of(n) >= take_near) cut = t;
-            }
+        }
+    } else {  // many (equal pages, infinities): the 64-bit key bit by bit, then the index
+        auto sum_of = [&](int n) {
+            int none = 0;
+            block_sum2<NW>(n, none, sm.sum, sm.sum2);
+            return n;
+        };
+        auto near = [&](int i) {
+            const uint32_t k = ordered(not_nan(ld_cg(scores + i)) + 0.f);
+            return k >= lo && k <= hi;
+        };
+        for (int i = warp; i < n_cand; i += NW) {
+            if (!near(i)) continue;
+            const unsigned long long k = score_at(i);
+            if (lane == 0) key64[i] = k;
+        }
+        __threadfence_block();
+        __syncthreads();
+        unsigned long long cut = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+            const unsigned long long t = cut | (1ull << bit);
             int n = 0;
-            for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] > cut;
-            const int ties = take_near - sum_of(n);  // of those equal to the cut: the first ones
-            int low = 0, high = n_cand - 1;  // smallest index with `ties` of them at or below it
-            while (low < high) {
-                const int mid = (low + high) / 2;
-                n = 0;
-                for (int i = tid; i <= mid; i += NT) n += near(i) && key64[i] == cut;
-                if (sum_of(n) >= ties)
-                    high = mid;
-                else
-                    low = mid + 1;
-            }
-            if (tid == 0) {
-                sm.cut_key = cut;
-                sm.cut_idx = low;
-            }
+            for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] >= t;
+            if (sum_of(n) >= take_near) cut = t;
+        }
+        int n = 0;
+        for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] > cut;
+        const int ties = take_near - sum_of(n);  // of those equal to the cut: the first ones
+        int low = 0, high = n_cand - 1;  // smallest index with `ties` of them at or below it
+        while (low < high) {
+            const int mid = (low + high) / 2;
+            n = 0;
+            for (int i = tid; i <= mid; i += NT) n += near(i) && key64[i] == cut;
+            if (sum_of(n) >= ties)
+                high = mid;
+            else
+                low = mid + 1;
+        }
+        if (tid == 0) {
+            sm.cut_key = cut;
+            sm.cut_idx = low;
         }
         __syncthreads();
     }
     auto take = [&](uint32_t k, int i) {
         if (k > hi) return true;
         if (k < lo) return false;
-        if (!refine) return true;
+        if (!refine) return k >= sm.cut32;
         unsigned long long k64 = 0;
         if (n_near <= kNear) {
             for (int y = 0; y < n_near; ++y)
@@ -690,10 +721,10 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
             if (lane == x) mine = m;
             n_taken += __popc(m);
         }
-        if (lane == 0) sm.sum[warp] = n_taken;
+        if (lane == 0) sm.sum_taken[warp] = n_taken;
         __syncthreads();  // also: every key of the tile has been read
-        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sm.sum[lane] : 0);
-        const int total = __reduce_add_sync(0xffffffffu, lane < NW ? sm.sum[lane] : 0);
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sm.sum_taken[lane] : 0);
+        const int total = __reduce_add_sync(0xffffffffu, lane < NW ? sm.sum_taken[lane] : 0);
         int upto = __popc(mine);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -728,21 +759,22 @@ cudaLaunchConfig_t dependent_launch(int64_t blocks, int threads, cudaStream_t s,
 }
 
 // Allow the scoring kernel its shared memory, once per kernel and device.
-template <int D, bool BF16>
+template <int D, bool BF16, int QB>
 cudaError_t allow_score_smem() {
     static std::atomic<unsigned long long> done{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && (done.load(std::memory_order_acquire) & (1ull << dev))) return cudaSuccess;
-    e = cudaFuncSetAttribute(score_pages_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SelShape<D>::SMEM);
+    e = cudaFuncSetAttribute(score_pages_kernel<D, BF16, QB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SelShape<D>::SMEM);
     if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
     return e;
 }
 
-template <int D>
-cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
+template <int D, int QB>
+cudaError_t launch_score_q(SelectParams& p, bool bf16, int num_sms, cudaStream_t s) {
+    const int64_t rows = static_cast<int64_t>(p.batch) * ((p.q_len + QB - 1) / QB) * p.hk;
     const int64_t cand = std::max(1, p.max_pages - p.first - p.last);
     // Pages per CTA: one wave of CTAs while that leaves each at most 384 KB to stream;
     // more CTAs than that for more pages, as rows differ in length.  (A batch of 64:
@@ -759,10 +791,16 @@ cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = dependent_launch(rows * p.n_chunks, kScoreThreads, s, attr);
     cfg.dynamicSmemBytes = SelShape<D>::SMEM;
-    const cudaError_t e = bf16 ? allow_score_smem<D, true>() : allow_score_smem<D, false>();
+    const cudaError_t e = bf16 ? allow_score_smem<D, true, QB>() : allow_score_smem<D, false, QB>();
     if (e != cudaSuccess) return e;
-    return bf16 ? cudaLaunchKernelEx(&cfg, score_pages_kernel<D, true>, p)
-                : cudaLaunchKernelEx(&cfg, score_pages_kernel<D, false>, p);
+    return bf16 ? cudaLaunchKernelEx(&cfg, score_pages_kernel<D, true, QB>, p)
+                : cudaLaunchKernelEx(&cfg, score_pages_kernel<D, false, QB>, p);
+}
+
+template <int D>
+cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s) {
+    if (p.q_len >= 3) return launch_score_q<D, 4>(p, bf16, num_sms, s);
+    return p.q_len == 2 ? launch_score_q<D, 2>(p, bf16, num_sms, s) : launch_score_q<D, 1>(p, bf16, num_sms, s);
 }
 
 template <int NW>
@@ -790,10 +828,12 @@ cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num
         default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
-    // Four times the threads where a row has more pages than 256 threads pass over quickly
-    // and there are few rows.
+    // More threads a row where there are at most as many rows as SMs: 4 rows of 4096 pages
+    // take 9.8 us with 1024 threads each, 10.3 with 512, 12.1 with 256; 128 rows of 512 pages
+    // 13.8 with 512, 14.5 with 256.  (512 rows of up to 2048 pages: 72 with 512, 67 with 256.)
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
-    return p.max_pages > 1024 && rows <= num_sms ? launch_choose<32>(p, bf16, s) : launch_choose<8>(p, bf16, s);
+    if (rows > num_sms) return launch_choose<8>(p, bf16, s);
+    return p.max_pages > 1024 ? launch_choose<32>(p, bf16, s) : launch_choose<16>(p, bf16, s);
 }
 
 }  // namespace fdec
