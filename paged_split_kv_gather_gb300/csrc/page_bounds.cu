@@ -8,6 +8,8 @@
 // read once (2 D bytes a token), its two rows written.  A page and KV head is one unit:
 // one warp, or the four warps of a CTA where there are too few units to fill the
 // machine (a batch's newest pages); D/8 lanes hold a row, several rows in flight.
+// GB300: the pages of 131072 tokens, 4 heads of 128 (138 MB), 23.1 us, 0.88 of the
+// measured copy bandwidth; the newest pages of 64 sequences 2.7 us.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -180,9 +182,12 @@ template <int D, bool BF16, bool KV8>
 cudaError_t launch_bounds(const BoundsParams& p, int num_sms, cudaStream_t s) {
     using S = BoundsShape<D, BF16, KV8>;
     const int64_t units = static_cast<int64_t>(p.batch) * p.span * p.hk;
-    // Four warps for one page where its rows are more than one round of loads of a warp
-    // and single warps would leave the machine empty.
-    const bool wide = (1 << p.page_shift) > S::RPW * S::U && units < static_cast<int64_t>(num_sms) * 16;
+    // Four warps for one page where its rows are more than one round of a warp's loads and
+    // single warps would leave the machine empty, or are eight rounds and more.  Measured
+    // (head_dim 128, us, four warps / one): 8 pages of 64 tokens 1.9 / 2.9, 512 of 256
+    // 4.4 / 7.6, 2400 of 256 15.9 / 18.6; 2048 of 64 5.0 / 4.3, 8192 of 64 23.9 / 23.1.
+    const int rounds = (1 << p.page_shift) / (S::RPW * S::U);
+    const bool wide = rounds >= 8 || (rounds >= 2 && units < static_cast<int64_t>(num_sms) * 8);
     const int64_t blocks = wide ? units : (units + kBoundsWarps - 1) / kBoundsWarps;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);

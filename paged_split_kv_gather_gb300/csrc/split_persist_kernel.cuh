@@ -35,7 +35,8 @@
 //     three stages of the current unit are issued.
 //   Shares: where the lengths are known only to the device and differ (the page lists of
 //     block-sparse decoding), planned items leave CTAs idle: a batch of 64 ragged lists of
-//     up to 2048 tokens took 72-78 us for 333 MB.  With p.shares the units are the lists
+//     up to 2048 tokens took 72-78 us for 333 MB (62 in shares, 5.4 TB/s with the merge's
+//     launch; without that and the start 6.2).  With p.shares the units are the lists
 //     themselves (x row groups), their blocks are numbered through, and CTA c streams the
 //     c-th of grid equal runs of them.  The producer finds its run from the
 //     lists' lengths (one pass of the warp over them); a unit counts kUnitCost blocks more
