@@ -167,6 +167,10 @@ struct fdec_plan_s {
     int rc = 1, row_groups = 1;
     int blocks_per_split = 1, fanin = 64, num_sms = 0, ctas_per_sm = 1;
     int max_pages_needed = 0;  // max_b ceil(capacity_b / page_size)
+    // E4M3 lists of fdec_run_selected run a plan of their own, uploaded behind this one (null: this one).
+    fdec_plan_s* selected = nullptr;
+    size_t off_selected = 0;
+    ~fdec_plan_s() { delete selected; }
     std::vector<int32_t> capacity;
     std::vector<int32_t> splits;  // per sequence
     std::vector<WorkItem> items;
@@ -627,6 +631,33 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
         p->off_share_ml = off;
         off = align_up(off + sizeof(float2) * 2 * p->share_grid * kMmaRows);
     }
+    if (kv8 && !q8 && q_len == 1 && o.blocks_per_split == 0) {
+        // Splits of equal length, as many a list as the resident CTAs hold (one more where
+        // that leaves under a third of a list out): lists of unknown lengths gain nothing from
+        // the odd splits that the planner balances, and a code cache's CTA starts for more than
+        // the planner counts.  Measured, us against the planner's splits: 16 x 8 lists of 2048
+        // tokens 20.8 / 25.7, ragged 20.3 / 21.8; 64 x 8 of 2048 ragged 44 / 55, full 72 / 69;
+        // 16 x 4 of 4096 at head_dim 256 30.8 / 31.3; 30 x 4 of 3200 23.5 / 24.2; the same from
+        // 32 lists down.
+        const double lists = static_cast<double>(batch) * num_kv_heads * p->row_groups;
+        const int n = std::max(1, static_cast<int>(slots / lists + 0.35));
+        const int max_blocks = *std::max_element(nblocks.begin(), nblocks.end());
+        const int bps = (max_blocks + n - 1) / n;
+        if (bps != p->blocks_per_split) {
+            fdec_plan_opts so = o;
+            so.blocks_per_split = bps;
+            so.num_sms = num_sms;
+            size_t bytes = 0;
+            const fdec_status st = fdec_plan(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads,
+                                             head_dim, dtype, causal, &so, &p->selected, &bytes);
+            if (st != FDEC_OK) {
+                delete p;
+                return st;
+            }
+            p->off_selected = off;
+            off = align_up(off + bytes);
+        }
+    }
     p->ws_bytes = off;
 
     p->meta.assign(p->meta_bytes, 0);
@@ -672,6 +703,7 @@ fdec_status fdec_plan_get_splits(fdec_plan_t p, int32_t* splits, int batch) {
 fdec_status fdec_plan_set_split_event(fdec_plan_t p, cudaEvent_t event) {
     if (p == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null plan");
     p->split_event = event;
+    if (p->selected != nullptr) p->selected->split_event = event;
     return FDEC_OK;
 }
 
@@ -695,6 +727,8 @@ fdec_status fdec_plan_upload(fdec_plan_t p, void* workspace, cudaStream_t stream
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail_cuda(e, "uploading the plan");
     p->uploaded = workspace;
+    if (p->selected != nullptr)
+        return fdec_plan_upload(p->selected, static_cast<uint8_t*>(workspace) + p->off_selected, stream);
     return FDEC_OK;
 }
 
@@ -706,6 +740,12 @@ fdec_status fdec_read_device_errors(fdec_plan_t p, void* workspace, uint32_t* fl
     if (e == cudaSuccess && clear) e = cudaMemsetAsync(ws + p->off_err, 0, sizeof(v), stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
+    if (p->selected != nullptr) {
+        uint32_t more = 0;
+        const fdec_status st = fdec_read_device_errors(p->selected, ws + p->off_selected, &more, clear, stream);
+        if (st != FDEC_OK) return st;
+        v |= more;
+    }
     *flags = v;
     return FDEC_OK;
 }
@@ -947,6 +987,10 @@ fdec_status fdec_run_selected(fdec_plan_t p, const void* q, int64_t q_stride_tok
         return fail(FDEC_ERR_INVALID_ARG, "out_type must be FDEC_OUT_F32 or FDEC_OUT_SAME");
     if (reinterpret_cast<uintptr_t>(out) % 16 != 0) return fail(FDEC_ERR_LAYOUT, "out must be 16-byte aligned");
     const int type = out_type == FDEC_OUT_F32 ? kOutF32 : (p->dtype == FDEC_BF16 ? kOutBF16 : kOutF16);
+    if (p->selected != nullptr && workspace != nullptr && workspace == p->uploaded) {
+        workspace = static_cast<uint8_t*>(workspace) + p->off_selected;
+        p = p->selected;
+    }
     return run_impl(p, q, q_stride_tok, q_stride_head, k, v, nullptr, nullptr, page_ids, page_ids_stride, counts, scale,
                     k_scale, v_scale, static_cast<float*>(out), lse, workspace, stream, true, type);
 }

@@ -863,3 +863,30 @@ def test_random_steps(seed):
     assert np.array_equal(sd.select.page_ids.cpu().numpy(), ids) and np.array_equal(sd.select.counts.cpu().numpy(), counts)
     ref = attend_reference(q.reshape(-1, 1, hq, d), k.float() * ks, v.float() * vs, ids, counts, 1 / math.sqrt(d))
     assert_attention(out, lse, *ref)
+
+
+@gpu
+def test_run_selected_over_e4m3_lists_in_splits_of_their_own():
+    """128 lists of 2048 tokens: the planner's splits (of fdec_run_scaled) and those of the lists differ; both run from
+    one plan and workspace, and the device errors of either are read."""
+    rows, hq, hk, d, page, budget = 16, 16, 8, 128, 16, 128
+    k, v = make_pool(400, hk, page, d, "fp8", "nhd", 6)
+    ids, counts = selected_lists(rows, hk, page, budget, 400, seed=6)
+    q = torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(7)).half().cuda()
+    pd = fd.PagedDecode([budget * page] * rows, 1, page, hq, hk, d, "f16", kv_dtype="fp8")
+    out, lse = torch.empty(rows, 1, hq, d, device="cuda"), torch.empty(rows, 1, hq, device="cuda")
+    pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse, k_scale=0.125, v_scale=0.25)
+    assert pd.device_errors() == 0
+    ref = attend_reference(q, k.float() * 0.125, v.float() * 0.25, ids, counts, 1 / math.sqrt(d))
+    assert_attention(out, lse, *ref)
+    pd.run(q, k, v, i32(ids[:, 0]), i32(counts[:, 0]), out, lse, k_scale=0.125, v_scale=0.25)
+    assert pd.device_errors() == 0
+    ref = attend_reference(q, k.float() * 0.125, v.float() * 0.25, ids[:, :1].repeat(hk, 1), counts[:, :1].repeat(hk, 1),
+                           1 / math.sqrt(d))
+    assert_attention(out, lse, *ref)
+    bad = ids.copy()
+    bad[0, 0, 3] = 400
+    pd.run_selected(q, k, v, i32(bad), i32(counts), out, lse)
+    assert pd.device_errors() == fd.DEVERR_PAGE_ID and pd.device_errors() == 0
+    pd.run(q, k, v, i32(bad[:, 0]), i32(counts[:, 0]), out, lse, k_scale=0.125, v_scale=0.25)
+    assert pd.device_errors() == fd.DEVERR_PAGE_ID
