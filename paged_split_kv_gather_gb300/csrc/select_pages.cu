@@ -46,7 +46,6 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kBins = 256;
 constexpr int kNear = 256;  // keys that are compared each with each
-constexpr int kTile = 4096;  // scores that choosing holds in shared memory
 constexpr int kMinChunk = 32;  // pages a scoring CTA has at least
 
 template <int D>
@@ -413,7 +412,10 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
 
 template <int NW>
 struct ChooseShared {
-    uint32_t key[kTile];  // a tile's scores as ordered integers; then its taken pages
+    // Scores held at a time, 16 a thread: 4096, 8192 or 16384.  A row that fits is loaded once,
+    // a longer one again in each pass (a row of 8192 pages: 11.8 us whole, 15.2 in halves).
+    static constexpr int TILE = NW * 32 * 16;
+    uint32_t key[TILE];  // a tile's scores as ordered integers; then its taken pages
     double weight64[2 * 512];
     int hist[kBins];
     unsigned long long near_key[kNear];
@@ -430,7 +432,9 @@ template <bool BF16, int NW>
 __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_constant__ SelectParams p) {
     constexpr int NT = NW * 32;
     static_assert(NT >= kBins && NT >= kNear && NW <= 32, "one bin, one near key a thread");
-    __shared__ __align__(16) ChooseShared<NW> sm;
+    constexpr int kTile = ChooseShared<NW>::TILE;
+    extern __shared__ __align__(16) unsigned char choose_smem[];
+    ChooseShared<NW>& sm = *reinterpret_cast<ChooseShared<NW>*>(choose_smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
     const int h = static_cast<int>(row % p.hk);
@@ -803,13 +807,27 @@ cudaError_t launch_score(SelectParams& p, bool bf16, int num_sms, cudaStream_t s
     return p.q_len == 2 ? launch_score_q<D, 2>(p, bf16, num_sms, s) : launch_score_q<D, 1>(p, bf16, num_sms, s);
 }
 
+template <bool BF16, int NW>
+cudaError_t launch_choose_type(const SelectParams& p, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};  // shared memory allowed: one bit per device
+    constexpr int bytes = static_cast<int>(sizeof(ChooseShared<NW>));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (bytes > 48 * 1024 && (dev >= 64 || !(done.load(std::memory_order_acquire) & (1ull << dev)))) {
+        e = cudaFuncSetAttribute(choose_pages_kernel<BF16, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = dependent_launch(static_cast<int64_t>(p.batch) * p.q_len * p.hk, NW * 32, s, attr);
+    cfg.dynamicSmemBytes = bytes;
+    return cudaLaunchKernelEx(&cfg, choose_pages_kernel<BF16, NW>, p);
+}
+
 template <int NW>
 cudaError_t launch_choose(const SelectParams& p, bool bf16, cudaStream_t s) {
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        dependent_launch(static_cast<int64_t>(p.batch) * p.q_len * p.hk, NW * 32, s, attr);
-    return bf16 ? cudaLaunchKernelEx(&cfg, choose_pages_kernel<true, NW>, p)
-                : cudaLaunchKernelEx(&cfg, choose_pages_kernel<false, NW>, p);
+    return bf16 ? launch_choose_type<true, NW>(p, s) : launch_choose_type<false, NW>(p, s);
 }
 
 }  // namespace
@@ -830,9 +848,15 @@ cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num
     if (e != cudaSuccess) return e;
     // More threads a row where there are at most as many rows as SMs: 4 rows of 4096 pages
     // take 9.8 us with 1024 threads each, 10.3 with 512, 12.1 with 256; 128 rows of 512 pages
-    // 13.8 with 512, 14.5 with 256.  (512 rows of up to 2048 pages: 72 with 512, 67 with 256.)
+    // 13.8 with 512, 14.5 with 256.  With more rows 256 threads (512 rows of up to 2048 pages:
+    // 67 against 72 with 512; 608 rows of 4096: 66 against 70), but 512 while two rows an SM
+    // are all there are (304 rows of 4096: 61 against 64) and for pages past 256 threads' tile
+    // (304 rows of 8192: 99 against 108).
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_len * p.hk;
-    if (rows > num_sms) return launch_choose<8>(p, bf16, s);
+    if (rows > num_sms) {
+        const bool wide = p.max_pages > ChooseShared<8>::TILE || (p.max_pages > 2048 && rows <= 2 * num_sms);
+        return wide ? launch_choose<16>(p, bf16, s) : launch_choose<8>(p, bf16, s);
+    }
     return p.max_pages > 1024 ? launch_choose<32>(p, bf16, s) : launch_choose<16>(p, bf16, s);
 }
 

@@ -391,6 +391,17 @@ def test_select_pages_of_a_very_long_sequence():
 
 
 @gpu
+@pytest.mark.parametrize("b", [2, 20])
+def test_select_pages_of_rows_around_a_tile(b):
+    """Rows of about 4096, 8192 and 16384 pages, few (16) and more than one an SM (160)."""
+    pages, lens = 16500, [4096, 16384, 4097, 16385, 8193, 8192, 4098, 16500] + [7, 0, 5000, 12289, 1, 16386, 8194, 300, 4000, 2, 9999, 40]
+    lens = lens[:b] if b > 2 else [16386, 16384]
+    table = np.tile(np.random.default_rng(14).permutation(pages), (b, 1))
+    q = torch.randn(b, 1, 16, 64, generator=torch.Generator().manual_seed(15)).bfloat16().cuda()
+    check_select(q, bounds_like(pages, 8, 64, torch.bfloat16, 16), table, lens, 1, 128, 1, 1)
+
+
+@gpu
 def test_select_pages_flags_lengths_and_page_ids():
     table = np.arange(100).reshape(1, 100)
     q = torch.randn(1, 1, 4, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
