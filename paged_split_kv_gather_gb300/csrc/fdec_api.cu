@@ -158,7 +158,7 @@ struct fdec_plan_s {
     int causal = 0;
     int path = FDEC_PATH_SIMT;
     bool persistent = false;  // MMA path over 16-bit caches: resident CTAs take work units
-    int n_units = 0, persist_grid = 0;
+    int n_units = 0, persist_grid = 0, selected_grid = 0;  // the latter for fdec_run_selected
     // Shares of fdec_run_selected (SelectedParams::shares): their grid (0: planned items) and
     // regions, behind the rest of the workspace (base_ws_bytes), which is all that the
     // other entry points use.
@@ -271,7 +271,8 @@ cudaError_t dispatch_split(const fdec_plan_s* p, const SelectedParams& sp, dim3 
     const CUtensorMap& tk = p->tmap_k;
     const CUtensorMap& tv = p->tmap_v;
     if (persist)
-        return launch_split_mma_persist(sp, tk, tv, p->head_dim, bf16, dim3(static_cast<unsigned>(p->persist_grid), 1, 1),
+        return launch_split_mma_persist(sp, tk, tv, p->head_dim, bf16,
+                                        dim3(static_cast<unsigned>(sp.per_head ? p->selected_grid : p->persist_grid), 1, 1),
                                         stream, launch);
     if (p->path == FDEC_PATH_TC)
         return launch_split_tc(sp, tk, tv, p->rc / kTcRows, p->head_dim, bf16, grid, stream, launch);
@@ -545,6 +546,8 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
     p->slots_a = next_slot;
     p->n_units = static_cast<int>(p->items.size()) * p->hk * p->row_groups;
     p->persist_grid = std::min(p->n_units, num_sms * p->ctas_per_sm);
+    const int selected_slots = num_sms * split_mma_persist_ctas_per_sm_selected(head_dim);
+    p->selected_grid = std::min(p->n_units, selected_slots);
 
     // Reduction passes: level l merges groups of `fanin` slots; levels alternate
     // between region A (even) and region B (odd).
@@ -610,17 +613,29 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
     p->base_ws_bytes = off;
     // Every producer warp passes over all lists' lengths to find its share: up to 4096 of
     // them, 128 a lane.
-    // Shares balance many long lists; short ones and a few are quicker as planned items.
-    // Measured (16-bit, head_dim 128, ragged, us, shares against planned): 512 lists of up to
-    // 2048 tokens 63 / 82, of 1024 39 / 41, of 256 23 / 20; 128 lists of 512 tokens 14 / 14;
-    // 32 lists of 2048 12.4 / 14.0; 4 lists of 4096 13.0 / 11.9.
-    const int max_blocks = *std::max_element(nblocks.begin(), nblocks.end());
+    // Shares cost positions, two parts a CTA and a merge, and save what the planned items
+    // leave idle: their longest chain (rounds of items times an item's blocks) less the mean.
+    // Taken where that is above what they cost: more than a tenth of a block where planned
+    // lists are split too, 2.5 + 300 / head_dim (and a little for every round) where they are
+    // whole and need no merge; fewer than 16 split lists stay planned (their parts are many,
+    // and one merge walks them all: 8 lists of 6144 tokens 12.8 / 11.3 at head_dim 64, 19.4 /
+    // 18.1 at 192, 39 / 42 at 512).  Measured over 517 shapes (4 to 1600 lists of 128 to 2048
+    // tokens, every head_dim, full and ragged): the rule's choice is 0.5 % above the better of
+    // both in the mean, shares always 10.8 %, planned always 4.6 %.  Shares against planned, us:
+    // head_dim 128, 512 lists of up to 2048 tokens 62 / 82, 800 of 640 48 / 41; head_dim 512,
+    // 36 lists of 320 19 / 25, 150 of 640 60 / 51.
     const long long lists = static_cast<long long>(batch) * num_kv_heads;
-    if (p->persistent && q_len == 1 && lists >= 16 && lists <= 4096 && max_blocks >= 8) {
-        long long blocks = 0;
-        for (int nb : nblocks) blocks += nb;
-        blocks *= static_cast<long long>(num_kv_heads) * p->row_groups;
-        p->share_grid = static_cast<int>(std::min<long long>(blocks, static_cast<long long>(num_sms) * p->ctas_per_sm));
+    long long blocks = 0;
+    for (int nb : nblocks) blocks += nb;
+    blocks *= static_cast<long long>(num_kv_heads) * p->row_groups;
+    const int max_blocks = *std::max_element(nblocks.begin(), nblocks.end());
+    const int rounds = (p->n_units + selected_slots - 1) / selected_slots;
+    const double mean = std::max(1.0, static_cast<double>(blocks) / selected_slots);
+    const double saved = static_cast<double>(rounds) * std::min(C, max_blocks) - mean;
+    const bool split = C < max_blocks;
+    const double cost = split ? 0.1 : 2.5 + 300.0 / head_dim + mean / 16;
+    if (p->persistent && q_len == 1 && lists <= 4096 && (!split || lists >= 16) && saved > cost) {
+        p->share_grid = static_cast<int>(std::min<long long>(blocks, selected_slots));
         p->share_cap = std::all_of(p->capacity.begin(), p->capacity.end(), [&](int32_t c) { return c == p->capacity[0]; })
                            ? p->capacity[0]
                            : -1;
@@ -639,9 +654,8 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
         // tokens 20.8 / 25.7, ragged 20.3 / 21.8; 64 x 8 of 2048 ragged 44 / 55, full 72 / 69;
         // 16 x 4 of 4096 at head_dim 256 30.8 / 31.3; 30 x 4 of 3200 23.5 / 24.2; the same from
         // 32 lists down.
-        const double lists = static_cast<double>(batch) * num_kv_heads * p->row_groups;
-        const int n = std::max(1, static_cast<int>(slots / lists + 0.35));
-        const int max_blocks = *std::max_element(nblocks.begin(), nblocks.end());
+        const double units = static_cast<double>(lists) * p->row_groups;
+        const int n = std::max(1, static_cast<int>(slots / units + 0.35));
         const int bps = (max_blocks + n - 1) / n;
         if (bps != p->blocks_per_split) {
             fdec_plan_opts so = o;

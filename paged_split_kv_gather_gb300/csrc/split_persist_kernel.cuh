@@ -84,7 +84,7 @@ struct UnitMeta {
 // launch takes the BM = false instantiation for every other page size, whose row
 // addresses are fixed at compile time (measured: the box-major build, identical in
 // what it does at 64-token pages, ran 10 % slower there at 66-76 splits).
-template <int D, bool BM = true>
+template <int D, bool BM = true, bool SEL = false>
 struct PersistLayout {
     using G = StageGeom<D>;
     static constexpr int RC = 16;                      // query rows per unit (one M tile)
@@ -92,7 +92,8 @@ struct PersistLayout {
     // columns (DH), as in MmaLayout; one CTA per SM (stages of 64 KB).
     static constexpr int DSPLIT = D > 256 ? 2 : 1;
     static constexpr int DH = D / DSPLIT;
-    static constexpr int CTAS_PER_SM = D > 256 ? 1 : 2;  // = split_mma_persist_ctas_per_sm(D)
+    static constexpr int CTAS_PER_SM =
+        SEL ? split_mma_persist_ctas_per_sm_selected(D) : split_mma_persist_ctas_per_sm(D);
     static constexpr bool BOXMAJ = BM && DSPLIT == 1;    // one box per small page
     // Two query buffers (the next unit's rows land while the last one still reads its
     // own) where they fit beside enough stages; one above head_dim 192 (the producer
@@ -105,7 +106,12 @@ struct PersistLayout {
     static constexpr int FIXED = CTRL_BYTES + QBUFS * Q_BYTES + ALIGN_SLACK;
     static constexpr int S_FIT = (BUDGET - FIXED) / G::STAGE_BYTES;
     static constexpr int S = S_FIT > 16 ? 16 : S_FIT;
-    static constexpr int NP = (S - 1) < 3 ? (S - 1) : 3;  // consumer groups (one stage each at a time)
+    // Consumer groups (one stage each at a time).  For page lists two also at head_dim 64 and
+    // 192: a block then needs no padding stage, and at 192 four warps of 255 registers fill the
+    // registers of an SM with two CTAs, so that no CTA starts before the last kernel's have left
+    // (two groups against three, us: 192, 16 lists of 1280 tokens 13.5 / 19.0, 80 of 2560 29.9 /
+    // 35.2; 64, 80 of 2560 17.1 / 19.8, 800 of 640 43 / 50; 128, 16 lists of 2560 13.4 / 12.7).
+    static constexpr int NP = (S - 1) < 3 || (SEL && (D == 64 || D == 192)) ? 2 : 3;
     static constexpr int NW = NP * DSPLIT;                 // consumer warps
     static constexpr int THREADS = (NW + 1) * 32;
     static constexpr int SMEM = FIXED + S * G::STAGE_BYTES;
@@ -764,10 +770,10 @@ __device__ __forceinline__ void merge_unit_selected(const SelectedParams& p, con
 }
 
 template <int D, bool BF16, bool BM, typename P>
-__global__ void __launch_bounds__(PersistLayout<D, BM>::THREADS, PersistLayout<D, BM>::CTAS_PER_SM)
+__global__ void __launch_bounds__(PersistLayout<D, BM, kSelected<P>>::THREADS, PersistLayout<D, BM, kSelected<P>>::CTAS_PER_SM)
 split_mma_persist_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv) {
-    using Lay = PersistLayout<D, BM>;
+    using Lay = PersistLayout<D, BM, kSelected<P>>;
     using W = MmaWarp<D, BF16, false, false, Lay::BOXMAJ>;
     using G = StageGeom<D>;
     constexpr int S = Lay::S;
@@ -948,7 +954,7 @@ split_mma_persist_kernel(const __grid_constant__ P p, const __grid_constant__ CU
 template <int D, bool BF16, bool BM, typename P>
 cudaError_t launch_split_mma_persist_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                          dim3 grid, cudaStream_t stream, bool launch) {
-    using Lay = PersistLayout<D, BM>;
+    using Lay = PersistLayout<D, BM, kSelected<P>>;
     static unsigned long long attr_done = 0;  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
