@@ -656,7 +656,13 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
         // 32 lists down.
         const double units = static_cast<double>(lists) * p->row_groups;
         const int n = std::max(1, static_cast<int>(slots / units + 0.35));
-        const int bps = (max_blocks + n - 1) / n;
+        int bps = (max_blocks + n - 1) / n;
+        // Whole lists where splitting them saves too few blocks to pay for its reduction, which
+        // starts late once the splits are more than the SMs (their CTAs leave it no room): us,
+        // whole against split, head_dim 256, 108 lists of 128 tokens 13.4 / 18.5, of 512 22 / 25,
+        // of 1024 30 / 28.5; head_dim 128, 216 lists of 512 12.6 / 15.2, 16 of 128 6.3 / 7.0.
+        const double ctas = units * ((max_blocks + bps - 1) / bps);
+        if (max_blocks - bps <= (ctas > num_sms ? 5 : head_dim > 128 ? 0 : 2)) bps = max_blocks;
         if (bps != p->blocks_per_split) {
             fdec_plan_opts so = o;
             so.blocks_per_split = bps;
