@@ -119,13 +119,16 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
     using R = RowLanes<D>;
     constexpr int LPR = R::LPR, RPW = R::RPW;
     const int lane = threadIdx.x & 31;
-    const int sub = lane / LPR, l = lane - sub * LPR;
+    const int sub = lane / LPR;
+    // head_dim 192 needs 12 of 16 lanes: the others go along with the last one's chunks, but
+    // add nothing to the sum and store nothing.
+    const bool on = lane - sub * LPR < R::PAIRS;
+    const int l = on ? lane - sub * LPR : R::PAIRS - 1;
     const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t n_work = static_cast<int64_t>(p.n_tokens) * wpt;
     const int half = p.rot / 2;
     const int page_mask = (1 << p.page_shift) - 1;
-    const bool on = l < R::PAIRS;  // head_dim 192 leaves 4 of 16 lanes idle
     const int n_rot = p.rot / 16;  // chunk pairs that rotate
     const bool rotated = l < n_rot;
     const int c0 = rotated ? l : n_rot + l;
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
                 for (int u = 0; u < U; ++u) {
                     const int h = (at + u * wpt) * RPW + sub;
                     a[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (on && h < heads) {
+                    if (h < heads) {
                         a[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c0);
                         c[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c1);
                     }
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
             };
             load(g, r0, r1);
             Coef f;
-            if (on) make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated, factor);
+            make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated, factor);
             for (; g < groups; g += U * wpt) {
                 // (a lane stores only chunks that it has loaded itself, so q_out may be q)
                 load(g + U * wpt, n0, n1);
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
                     float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) s2 = __ffma2_rn(x1[k], x1[k], __ffma2_rn(x0[k], x0[k], s2));
-                    float sum = s2.x + s2.y;
+                    float sum = on ? s2.x + s2.y : 0.f;
 #pragma unroll
                     for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     const float rs = rsqrtf(sum * (1.f / D) + p.eps);
