@@ -113,8 +113,9 @@ __device__ __forceinline__ void make_coef(Coef& f, const uint16_t* weight, const
     }
 }
 
-// U: row groups a warp loads at once, the next U while it computes these.
-template <int D, bool BF16, bool KV8, bool INTER, int U>
+// U: row groups a warp loads at once, the next U while it computes these.  PRE: its first q,
+// k and v rows are requested together.
+template <int D, bool BF16, bool KV8, bool INTER, int U, bool PRE>
 __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int wpt) {
     using R = RowLanes<D>;
     constexpr int LPR = R::LPR, RPW = R::RPW;
@@ -170,25 +171,27 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
             const int back = part - from;
             return back >= 0 ? back : back + (-back + wpt - 1) / wpt * wpt;
         };
-        // The q rows or the k rows: norm and rotation of rows h < heads at src + h * src_h.
+        auto load_rows = [&](const uint8_t* src, int64_t src_h, int heads, int at, uint4 (&a)[U], uint4 (&c)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = (at + u * wpt) * RPW + sub;
+                a[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (h < heads) {
+                    a[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c0);
+                    c[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c1);
+                }
+            }
+        };
+        // The q rows or the k rows: norm and rotation of rows h < heads at src + h * src_h, the
+        // first of them in r0, r1 with PRE.
         auto normed = [&](const uint8_t* src, int64_t src_h, uint8_t* dst, int64_t dst_h, int heads, int from, int groups,
-                          const uint16_t* weight, float factor, auto codes) {
+                          const uint16_t* weight, float factor, auto codes, uint4 (&r0)[U], uint4 (&r1)[U]) {
             constexpr bool CODES = decltype(codes)::value;
             int g = first_group(from);
             if (g >= groups) return;
-            uint4 r0[U], r1[U], n0[U], n1[U];
-            auto load = [&](int at, uint4 (&a)[U], uint4 (&c)[U]) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = (at + u * wpt) * RPW + sub;
-                    a[u] = c[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h < heads) {
-                        a[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c0);
-                        c[u] = *reinterpret_cast<const uint4*>(src + h * src_h + 16 * c1);
-                    }
-                }
-            };
-            load(g, r0, r1);
+            uint4 n0[U], n1[U];
+            auto load = [&](int at, uint4 (&a)[U], uint4 (&c)[U]) { load_rows(src, src_h, heads, at, a, c); };
+            if constexpr (!PRE) load(g, r0, r1);
             Coef f;
             make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated, factor);
             for (; g < groups; g += U * wpt) {
@@ -242,10 +245,17 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
                 for (int u = 0; u < U; ++u) r0[u] = n0[u], r1[u] = n1[u];
             }
         };
+        const int gv0 = first_group(groups_q + groups_kv);
+        uint4 q0[U], q1[U], k0[U], k1[U], v0[U], v1[U];
+        if constexpr (PRE) {
+            load_rows(p.q + i * p.q_st, p.q_sh, p.hq, first_group(0), q0, q1);
+            load_rows(p.k_new + i * p.k_new_st, p.k_new_sh, p.hk, first_group(groups_q), k0, k1);
+            load_rows(p.v_new + i * p.v_new_st, p.v_new_sh, p.hk, gv0, v0, v1);
+        }
         normed(p.q + i * p.q_st, p.q_sh, p.q_out + i * p.q_out_st, p.q_out_sh, p.hq, 0, groups_q, p.q_weight, 1.f,
-               std::false_type{});
+               std::false_type{}, q0, q1);
         normed(p.k_new + i * p.k_new_st, p.k_new_sh, p.k_base + page * p.k_sp + slot * p.k_st, p.k_sh, p.hk, groups_q,
-               groups_kv, p.k_weight, p.k_inv, std::bool_constant<KV8>{});
+               groups_kv, p.k_weight, p.k_inv, std::bool_constant<KV8>{}, k0, k1);
         if (!page_ok) {
             if (lane == 0 && part == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
             continue;
@@ -253,11 +263,16 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
         // The v rows: as they are, or scaled and rounded to codes.
         const uint8_t* src = p.v_new + i * p.v_new_st;
         uint8_t* dst = p.v_base + page * p.v_sp + slot * p.v_st;
-        for (int g = first_group(groups_q + groups_kv); g < groups_kv; g += wpt) {
+        for (int g = gv0; g < groups_kv; g += wpt) {
             const int h = g * RPW + sub;
             if (!on || h >= p.hk) continue;
-            const uint4 r0 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c0);
-            const uint4 r1 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c1);
+            uint4 r0, r1;
+            if (PRE && g == gv0) {
+                r0 = v0[0], r1 = v1[0];
+            } else {
+                r0 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c0);
+                r1 = *reinterpret_cast<const uint4*>(src + h * p.v_new_sh + 16 * c1);
+            }
             uint8_t* to = dst + h * p.v_sh;
             if constexpr (KV8) {
                 const float2 inv = make_float2(p.v_inv, p.v_inv);
@@ -299,8 +314,10 @@ cudaError_t launch_rows(const NormRopeParams& p, bool pairs, int num_sms, cudaSt
         }
     }
     // A warp has two groups at most: the form without loads ahead is shorter code, which a
-    // call of a few tokens mostly waits to fetch (64 tokens: 3.2 against 3.6 us).
-    const bool single = groups <= 2 * wpt;
+    // call of a few tokens mostly waits to fetch (64 tokens: 3.2 against 3.6 us).  Up to four:
+    // its q, k and v rows together, as a token's latency decides (32768 tokens of 4/1 heads of
+    // 128 51 against 62 us; in every call, one token 3.1 against 2.8).
+    const int per_warp = (groups + wpt - 1) / wpt;
     const int64_t warps = static_cast<int64_t>(p.n_tokens) * wpt;
     const int64_t blocks =
         std::min<int64_t>((warps * 32 + kRowsThreads - 1) / kRowsThreads, static_cast<int64_t>(num_sms) * kRowsCtas);
@@ -313,11 +330,16 @@ cudaError_t launch_rows(const NormRopeParams& p, bool pairs, int num_sms, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (single)
-        return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true, 1>, p, wpt)
-                     : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false, 1>, p, wpt);
-    return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true, 2>, p, wpt)
-                 : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false, 2>, p, wpt);
+    auto launch = [&](auto u, auto pre) {
+        constexpr int U = decltype(u)::value;
+        constexpr bool PRE = decltype(pre)::value;
+        return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, true, U, PRE>, p, wpt)
+                     : cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, BF16, KV8, false, U, PRE>, p, wpt);
+    };
+    using One = std::integral_constant<int, 1>;
+    if (per_warp <= 2) return launch(One{}, std::false_type{});
+    if (per_warp <= 4) return launch(One{}, std::true_type{});
+    return launch(std::integral_constant<int, 2>{}, std::false_type{});
 }
 
 template <int D>
