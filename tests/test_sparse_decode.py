@@ -512,6 +512,29 @@ def test_run_selected(case, out_type):
 
 
 @gpu
+@pytest.mark.parametrize("kv,d,hk,group,rows,page,budget", [
+    ("", 512, 3, 4, 12, 32, 10), ("", 512, 1, 8, 5, 64, 5), ("", 256, 4, 4, 12, 16, 30), ("", 192, 4, 2, 9, 64, 10),
+    ("", 128, 8, 20, 12, 8, 90), ("", 64, 8, 4, 40, 64, 12), ("", 64, 1, 33, 70, 16, 41), ("fp8", 256, 4, 8, 27, 16, 16),
+    ("fp8", 128, 8, 4, 27, 64, 4)])
+def test_run_selected_over_lists_of_a_few_blocks(kv, d, hk, group, rows, page, budget):
+    """Lists around the sizes at which the work is cut at run time instead of as planned."""
+    pool_pages, hq = 3 * budget, hk * group
+    k, v = make_pool(pool_pages, hk, page, d, kv or "bf16", "nhd", seed=d)
+    q = torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(rows)).bfloat16().cuda()
+    pd = fd.PagedDecode([budget * page] * rows, 1, page, hq, hk, d, "bf16", kv_dtype=kv)
+    out, lse = torch.empty(rows, 1, hq, d, device="cuda"), torch.empty(rows, 1, hq, device="cuda")
+    for full in (False, True):
+        ids, counts = selected_lists(rows, hk, page, budget, pool_pages, seed=budget)
+        if full:
+            counts[:] = budget * page
+            ids[:] = np.random.default_rng(d).integers(0, pool_pages, ids.shape)
+        out.fill_(float("nan")), lse.fill_(float("nan"))
+        pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse)
+        assert pd.device_errors() == 0
+        assert_attention(out, lse, *attend_reference(q, k.float(), v.float(), ids, counts, 1 / math.sqrt(d)))
+
+
+@gpu
 @pytest.mark.parametrize("path", [fd.FDEC_PATH_SIMT, fd.FDEC_PATH_MMA, fd.FDEC_PATH_TC])
 @pytest.mark.parametrize("blocks_per_split", [0, 1])
 def test_run_selected_on_every_path_equals_run_of_the_same_pages(path, blocks_per_split):
