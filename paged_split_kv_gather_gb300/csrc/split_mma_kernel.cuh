@@ -44,8 +44,9 @@
 // A bf16 query is brought to f16 by scaling each query row by a power of two
 // that puts its largest magnitude in f16's top binade [2^14, 2^15): exact for
 // every element within 2^38 of the row's largest, and the factor is taken back
-// out of the row's logit scale.  P is one f16 value scaled by 2^7.  The cache's
-// k_scale is folded into the logit scale and v_scale into the epilogue.
+// out of the row's logit scale.  P is one f16 value scaled by 2^7 (PAIR: and the
+// f16 of what that rounding left, see MmaWarp).  The cache's k_scale is folded into
+// the logit scale and v_scale into the epilogue.
 #pragma once
 
 #include <type_traits>
@@ -219,7 +220,11 @@ __device__ __forceinline__ float pair_scale(const uint32_t (&w)[NB], int u, int 
 // units) and the work of one 32-token stage.
 // BM: the stages are box-major (see stage_row_offset) with boxes of fewer rows than a
 // stage possible; false: region-major only, with the row addresses fixed at compile time.
-template <int D, bool BF16, bool KV8, bool Q8 = false, bool BM = MmaLayout<D, KV8, Q8>::BOXMAJ>
+// PAIR: P over E4M3 codes as a pair of f16 values, as it is over 16-bit rows (page lists).
+// FOLD: at most 8 query rows, and the residuals of their P take the tile's other 8 rows, so
+// that the pair costs no product; else they have products of their own.
+template <int D, bool BF16, bool KV8, bool Q8 = false, bool BM = MmaLayout<D, KV8, Q8>::BOXMAJ, bool PAIR = false,
+          bool FOLD = false>
 struct MmaWarp {
     using Lay = MmaLayout<D, KV8, Q8>;
     using G = StageGeom<D>;
@@ -229,7 +234,7 @@ struct MmaWarp {
     static constexpr int KSTEPS = D / 16;    // k-steps of S = Q K^T
     static constexpr int NT = DH / 8;        // n-tiles of this warp's O
     static constexpr bool MB = KV8 ? false : BF16;  // operand type of the MMAs (f16 over E4M3 caches)
-    static constexpr bool P1 = KV8;                 // one f16 P (11 bits) instead of a 16-bit hi + lo pair
+    static constexpr bool P1 = KV8 && !PAIR;        // one f16 P (11 bits) instead of a 16-bit hi + lo pair
     static constexpr float kP1Scale = 128.f;        // 2^7
     static constexpr int QREGS = Lay::Q_IN_REGS ? KSTEPS : 1;
 
@@ -346,6 +351,9 @@ struct MmaWarp {
         const __half* sck = reinterpret_cast<const __half*>(scl);  // q8_0: K scales [32][NB], V scales after
         const __half* scv = sck + kStageTokens * NB;
 
+        // (FOLD at head_dim 128: the 8 addresses from it, kept over all stages, would spill)
+        uint32_t k8x = k8_x;
+        if constexpr (FOLD) asm volatile("" : "+r"(k8x));
         // S = Q K^T for the stage's 32 tokens (4 n-tiles of 8)
         float sc[4][4];
 #pragma unroll
@@ -386,13 +394,13 @@ struct MmaWarp {
                     sc[n][3] = fmaf(acc[n][3], d1, sc[n][3]);
                 }
             });
-        } else static_for<0, KSTEPS>([&](auto kk_) {
+        } else static_for<0, KSTEPS>([&, k8x](auto kk_) {
             constexpr int kk = decltype(kk_)::value;
             constexpr int qk = Lay::Q_IN_REGS ? kk : 0;
             if constexpr (KV8) {
                 if constexpr (!Lay::Q_IN_REGS) load_q8(q_s, kk, qa[0]);
                 uint32_t r[4];
-                ldmatrix_x4(kbase + (kk >> 3) * rs() + k8_row + ((static_cast<uint32_t>(kk & 7) << 4) ^ k8_x),
+                ldmatrix_x4(kbase + (kk >> 3) * rs() + k8_row + ((static_cast<uint32_t>(kk & 7) << 4) ^ k8x),
                             r[0], r[1], r[2], r[3]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -419,7 +427,7 @@ struct MmaWarp {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < (FOLD ? 2 : 4); ++e) {
                 const int tok = 8 * n + 2 * tq + (e & 1);
                 float z = sc[n][e] * sl[e >> 1];
                 if (tok >= ((e >> 1) ? vis1 : vis0)) z = -INFINITY;
@@ -432,27 +440,30 @@ struct MmaWarp {
         }
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        if constexpr (!FOLD) {
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        }
         constexpr float kLazyRescale = 8.f;
-        if (__any_sync(0xffffffffu, mx0 > mrow[0] + kLazyRescale || mx1 > mrow[1] + kLazyRescale)) {
+        if (__any_sync(0xffffffffu, mx0 > mrow[0] + kLazyRescale || (!FOLD && mx1 > mrow[1] + kLazyRescale))) {
             const float n0 = fmaxf(mrow[0], mx0), n1 = fmaxf(mrow[1], mx1);
             // 0 when m was -inf and the row now sees a token; 1 for a row that still has seen
             // nothing (the branch is taken for the whole warp when any row grows, and
             // -inf - -inf would be NaN and poison its l)
             const float a0 = n0 == -INFINITY ? 1.f : exp2_approx(mrow[0] - n0);
-            const float a1 = n1 == -INFINITY ? 1.f : exp2_approx(mrow[1] - n1);
+            const float a1 = FOLD || n1 == -INFINITY ? 1.f : exp2_approx(mrow[1] - n1);
             lrow[0] *= a0;
             lrow[1] *= a1;
+            const float ao = FOLD ? a0 : a1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 o[n][0] *= a0;
                 o[n][1] *= a0;
-                o[n][2] *= a1;
-                o[n][3] *= a1;
+                o[n][2] *= ao;
+                o[n][3] *= ao;
             }
             mrow[0] = n0;
-            mrow[1] = n1;
+            if constexpr (!FOLD) mrow[1] = n1;
         }
         const float mu0 = mrow[0] == -INFINITY ? 0.f : mrow[0];
         const float mu1 = mrow[1] == -INFINITY ? 0.f : mrow[1];
@@ -460,22 +471,32 @@ struct MmaWarp {
         for (int n = 0; n < 4; ++n) {
             sc[n][0] = exp2_approx(sc[n][0] - mu0);
             sc[n][1] = exp2_approx(sc[n][1] - mu0);
-            sc[n][2] = exp2_approx(sc[n][2] - mu1);
-            sc[n][3] = exp2_approx(sc[n][3] - mu1);
             lrow[0] += sc[n][0] + sc[n][1];
-            lrow[1] += sc[n][2] + sc[n][3];
+            if constexpr (!FOLD) {
+                sc[n][2] = exp2_approx(sc[n][2] - mu1);
+                sc[n][3] = exp2_approx(sc[n][3] - mu1);
+                lrow[1] += sc[n][2] + sc[n][3];
+            }
         }
         // P as A fragments of two k-steps of 16 tokens: split into high and residual
-        // parts, or (P1) one f16 value scaled by 2^7 (p <= 2^8 by the lazy rescale, so
-        // p 2^7 <= 2^15 fits f16, and small p stay normal); O then carries 2^7.
+        // parts, or (P1) one f16 value.  Over codes P is scaled by 2^7 (p <= 2^8 by the
+        // lazy rescale, so p 2^7 <= 2^15 fits f16, and small p stay normal); O then
+        // carries 2^7.
+        if constexpr (KV8 && !Q8) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] *= kP1Scale;
+        }
         uint32_t ph[2][4], pl[2][4];
 #pragma unroll
         for (int k2 = 0; k2 < 2 && !Q8; ++k2) {
-            if constexpr (P1) {
-                ph[k2][0] = pack_f16x2(sc[2 * k2][0] * kP1Scale, sc[2 * k2][1] * kP1Scale);
-                ph[k2][1] = pack_f16x2(sc[2 * k2][2] * kP1Scale, sc[2 * k2][3] * kP1Scale);
-                ph[k2][2] = pack_f16x2(sc[2 * k2 + 1][0] * kP1Scale, sc[2 * k2 + 1][1] * kP1Scale);
-                ph[k2][3] = pack_f16x2(sc[2 * k2 + 1][2] * kP1Scale, sc[2 * k2 + 1][3] * kP1Scale);
+            if constexpr (KV8 && !P1) {  // (a k-step's pair as it is used: add_pv8)
+            } else if constexpr (P1) {
+                ph[k2][0] = pack_f16x2(sc[2 * k2][0], sc[2 * k2][1]);
+                ph[k2][1] = pack_f16x2(sc[2 * k2][2], sc[2 * k2][3]);
+                ph[k2][2] = pack_f16x2(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]);
+                ph[k2][3] = pack_f16x2(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3]);
             } else {
                 split_pair<MB>(sc[2 * k2][0], sc[2 * k2][1], ph[k2][0], pl[k2][0]);
                 split_pair<MB>(sc[2 * k2][2], sc[2 * k2][3], ph[k2][1], pl[k2][1]);
@@ -542,37 +563,61 @@ struct MmaWarp {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[2 * c + i][e] = fmaf(acc[i][e], up, o[2 * c + i][e]);
             });
+        } else if constexpr (KV8) {
+            add_pv8(sc, ph, vbase);
         } else
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-            if constexpr (KV8) {
-                // chunks c, c + 1 (16 dims each): o[2c] / o[2c+1] hold the even / odd dims of chunk c
-                static_for<0, D / 32>([&](auto cp_) {
-                    constexpr int c = 2 * decltype(cp_)::value;
-                    uint32_t r[4];
-                    ldmatrix_x4_trans(vbase + (c >> 3) * rs() + v8_row[k2] +
-                                          ((static_cast<uint32_t>(c & 7) << 4) ^ v8_x),
-                                      r[0], r[1], r[2], r[3]);
-                    uint32_t ev[4], od[4];  // by matrix: (tokens 0-7 | 8-15) x (chunk c | c + 1)
+            static_for<0, DH / 16>([&](auto jp_) {
+                constexpr int jp = decltype(jp_)::value;  // 16-column group of this warp's half
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_x4_trans(vbase + v_half + (jp >> 2) * rs() + vb_row[k2] + vb_x[jp & 3], b0, b1,
+                                  b2, b3);
+                mma_16816<MB>(o[2 * jp], ph[k2], b0, b1);
+                if constexpr (!P1) mma_16816<MB>(o[2 * jp], pl[k2], b0, b1);
+                mma_16816<MB>(o[2 * jp + 1], ph[k2], b2, b3);
+                if constexpr (!P1) mma_16816<MB>(o[2 * jp + 1], pl[k2], b2, b3);
+            });
+        }
+    }
+
+    // O += P V over a stage of codes at vbase.  sc: P; ph: P rounded (without PAIR).
+    __device__ __forceinline__ void add_pv8(const float (&sc)[4][4], uint32_t (&ph)[2][4], uint32_t vbase) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) e4m3x4_to_f16(__byte_perm(r[m], 0u, 0x3120u), ev[m], od[m]);
-                    mma_16816<false>(o[2 * c], ph[k2], ev[0], ev[1]);
-                    mma_16816<false>(o[2 * c + 1], ph[k2], od[0], od[1]);
-                    mma_16816<false>(o[2 * c + 2], ph[k2], ev[2], ev[3]);
-                    mma_16816<false>(o[2 * c + 3], ph[k2], od[2], od[3]);
-                });
-            } else {
-                static_for<0, DH / 16>([&](auto jp_) {
-                    constexpr int jp = decltype(jp_)::value;  // 16-column group of this warp's half
-                    uint32_t b0, b1, b2, b3;
-                    ldmatrix_x4_trans(vbase + v_half + (jp >> 2) * rs() + vb_row[k2] + vb_x[jp & 3], b0, b1,
-                                      b2, b3);
-                    mma_16816<MB>(o[2 * jp], ph[k2], b0, b1);
-                    if constexpr (!P1) mma_16816<MB>(o[2 * jp], pl[k2], b0, b1);
-                    mma_16816<MB>(o[2 * jp + 1], ph[k2], b2, b3);
-                    if constexpr (!P1) mma_16816<MB>(o[2 * jp + 1], pl[k2], b2, b3);
-                });
+        for (int k2 = 0; k2 < 2; ++k2) {
+            uint32_t pl[4];
+            if constexpr (PAIR) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float* y = sc[2 * k2 + x];
+                    if constexpr (FOLD) {
+                        split_pair<false>(y[0], y[1], ph[k2][2 * x], ph[k2][2 * x + 1]);
+                    } else {
+                        split_pair<false>(y[0], y[1], ph[k2][2 * x], pl[2 * x]);
+                        split_pair<false>(y[2], y[3], ph[k2][2 * x + 1], pl[2 * x + 1]);
+                    }
+                }
             }
+            // chunks c, c + 1 (16 dims each): o[2c] / o[2c+1] hold the even / odd dims of chunk c
+            static_for<0, D / 32>([&](auto cp_) {
+                constexpr int c = 2 * decltype(cp_)::value;
+                uint32_t r[4];
+                ldmatrix_x4_trans(vbase + (c >> 3) * rs() + v8_row[k2] + ((static_cast<uint32_t>(c & 7) << 4) ^ v8_x),
+                                  r[0], r[1], r[2], r[3]);
+                uint32_t ev[4], od[4];  // by matrix: (tokens 0-7 | 8-15) x (chunk c | c + 1)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) e4m3x4_to_f16(__byte_perm(r[m], 0u, 0x3120u), ev[m], od[m]);
+                mma_16816<false>(o[2 * c], ph[k2], ev[0], ev[1]);
+                mma_16816<false>(o[2 * c + 1], ph[k2], od[0], od[1]);
+                mma_16816<false>(o[2 * c + 2], ph[k2], ev[2], ev[3]);
+                mma_16816<false>(o[2 * c + 3], ph[k2], od[2], od[3]);
+                if constexpr (PAIR && !FOLD) {
+                    mma_16816<false>(o[2 * c], pl, ev[0], ev[1]);
+                    mma_16816<false>(o[2 * c + 1], pl, od[0], od[1]);
+                    mma_16816<false>(o[2 * c + 2], pl, ev[2], ev[3]);
+                    mma_16816<false>(o[2 * c + 3], pl, od[2], od[3]);
+                }
+            });
         }
     }
 
@@ -586,12 +631,19 @@ struct MmaWarp {
     }
 };
 
-template <int D, bool BF16, bool KV8, bool Q8, typename P>
+template <int D, bool BF16, bool KV8, bool Q8, typename P, bool FOLD = false>
 __global__ void __launch_bounds__(MmaLayout<D, KV8, Q8>::THREADS, MmaLayout<D, KV8, Q8>::CTAS_PER_SM)
 split_mma_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv) {
     using Lay = MmaLayout<D, KV8, Q8>;
-    using W = MmaWarp<D, BF16, KV8, Q8>;
+    // Page lists take P over codes as a pair, so that fp32 outputs are as near as those of
+    // 16-bit lists: 5e-7 of the result over 2048 tokens; one f16 value, which rounds each
+    // probability by up to 2^-12, gave 1.8e-4.  Folded (FOLD), and without the softmax of
+    // rows that are not there, that is no slower: 128 lists of 2048 tokens, head_dim 128,
+    // 19.8 us against 20.9 with one value; 512 ragged lists 43.0 / 44.5; 64 of 4096 at
+    // head_dim 256 47.7 / 49.8.  With 9 to 16 rows it has products of its own: 64 lists of
+    // 2048 21.0 / 19.4, 512 ragged ones 60.7 / 52.8.
+    using W = MmaWarp<D, BF16, KV8, Q8, Lay::BOXMAJ, KV8 && !Q8 && kSelected<P>, FOLD>;
     using G = StageGeom<D>;
     using GS = typename Lay::GS;
     constexpr int NW = Lay::NW;
@@ -602,7 +654,7 @@ split_mma_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMa
     constexpr int DH = Lay::DH;
     constexpr int NT = W::NT;
     constexpr bool QSCALE = KV8 && BF16;     // bf16 query rows rescaled into f16
-    const float o_out = W::P1 ? 1.f / W::kP1Scale : 1.f;
+    const float o_out = KV8 ? 1.f / W::kP1Scale : 1.f;
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -745,12 +797,20 @@ split_mma_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMa
         // are dims 16c + 4tq + {0, 2} / {1, 3}
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
+            if constexpr (FOLD) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    cw.o[2 * c + x][0] += cw.o[2 * c + x][2];
+                    cw.o[2 * c + x][1] += cw.o[2 * c + x][3];
+                }
+            }
             *reinterpret_cast<float4*>(sm_o + (grp * RC + g) * D + 16 * c + 4 * tq) =
                 make_float4(cw.o[2 * c][0] * o_out, cw.o[2 * c + 1][0] * o_out, cw.o[2 * c][1] * o_out,
                             cw.o[2 * c + 1][1] * o_out);
-            *reinterpret_cast<float4*>(sm_o + (grp * RC + g + 8) * D + 16 * c + 4 * tq) =
-                make_float4(cw.o[2 * c][2] * o_out, cw.o[2 * c + 1][2] * o_out, cw.o[2 * c][3] * o_out,
-                            cw.o[2 * c + 1][3] * o_out);
+            if constexpr (!FOLD)
+                *reinterpret_cast<float4*>(sm_o + (grp * RC + g + 8) * D + 16 * c + 4 * tq) =
+                    make_float4(cw.o[2 * c][2] * o_out, cw.o[2 * c + 1][2] * o_out, cw.o[2 * c][3] * o_out,
+                                cw.o[2 * c + 1][3] * o_out);
         }
     }
 #pragma unroll
@@ -764,16 +824,22 @@ split_mma_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMa
     merge_and_store<NP, RC, D, NW * 32>(p, it, kvh, row0, sm_m, sm_l, sm_o);
 }
 
-template <int D, bool BF16, bool KV8 = false, bool Q8 = false, typename P>
+template <int D, bool BF16, bool KV8 = false, bool Q8 = false, bool FOLD = false, typename P>
 cudaError_t launch_split_mma_one(const P& p, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                                  cudaStream_t stream, bool launch) {
     using Lay = MmaLayout<D, KV8, Q8>;
+    if constexpr (KV8 && !Q8 && !FOLD && kSelected<P>) {  // (set-up: both)
+        if (!launch || p.rows <= 8) {
+            const cudaError_t e = launch_split_mma_one<D, BF16, KV8, Q8, true>(p, tk, tv, grid, stream, launch);
+            if (e != cudaSuccess || launch) return e;
+        }
+    }
     static unsigned long long attr_done = 0;  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(split_mma_kernel<D, BF16, KV8, Q8, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(split_mma_kernel<D, BF16, KV8, Q8, P, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Lay::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
@@ -789,7 +855,7 @@ cudaError_t launch_split_mma_one(const P& p, const CUtensorMap& tk, const CUtens
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_mma_kernel<D, BF16, KV8, Q8, P>, p, tk, tv);
+    return cudaLaunchKernelEx(&cfg, split_mma_kernel<D, BF16, KV8, Q8, P, FOLD>, p, tk, tv);
 }
 
 template <typename P>

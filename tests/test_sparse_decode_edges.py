@@ -1,0 +1,43 @@
+"""Block-sparse decoding where it can go wrong: the precision of attention over code caches, error flags, codes at
+ties, stream order, refusals of tensors that are not on the GPU, plans with and without page lists.
+
+Tolerances are derived beside each test."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_split_kv_gather_gb300 as fd
+from tests.test_sparse_decode import DT, attend_reference, gpu, i32, make_pool, selected_lists
+
+
+# ------------------------------------------------------------------------------------------- attention over codes
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,hq,hk,page,budget,rows", [(128, 8, 2, 16, 3, 40), (256, 8, 2, 16, 3, 40),
+                                                      (128, 16, 8, 16, 128, 16), (256, 8, 4, 64, 40, 5),
+                                                      (128, 24, 2, 16, 5, 30), (256, 64, 2, 32, 20, 3), (128, 70, 2, 64, 30, 4)])
+def test_run_selected_over_codes_keeps_the_probabilities(d, hq, hk, page, budget, rows, dtype):
+    """fp32 outputs over E4M3 lists, as near as those over 16-bit lists.
+
+    Relative to sum p |v| / sum p: the logits are sums of D products in 16 fp32 accumulations of the tensor cores
+    (2^-23 each, of sum |q k| scale log2(e) < 3 for the queries here: 2^-18 at most), the exponential 2^-22, a
+    probability as two f16 values 2^-23, the sum over a list's tokens two of 16 accumulations and the merges 2^-18: in
+    all below 2^-16.  (One f16 value alone is off by up to 2^-12.)"""
+    t = DT[dtype]
+    pool = 2 * budget + 5
+    k, v = make_pool(pool, hk, page, d, "fp8", "nhd", seed=d)
+    ids, counts = selected_lists(rows, hk, page, budget, pool, seed=rows)
+    q = (torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(d)) / 8).to(t).cuda()
+    ks, vs = 0.125, 0.25
+    pd = fd.PagedDecode([budget * page] * rows, 1, page, hq, hk, d, dtype, kv_dtype="fp8")
+    out = torch.full((rows, 1, hq, d), float("nan"), device="cuda")
+    pd.run_selected(q, k, v, i32(ids), i32(counts), out, None, k_scale=ks, v_scale=vs)
+    assert pd.device_errors() == 0
+    kk, vv = k.float() * ks, v.float() * vs
+    ref, _ = attend_reference(q, kk, vv, ids, counts, 1 / math.sqrt(d))
+    mag, _ = attend_reference(q, kk, vv.abs(), ids, counts, 1 / math.sqrt(d))
+    off = np.abs(out.double().cpu().numpy() - ref)
+    assert (off <= 2.0 ** -16 * mag).all(), (off / np.maximum(mag, 1e-30)).max()
