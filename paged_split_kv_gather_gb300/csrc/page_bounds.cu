@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) page_bounds_kernel(const __
     int64_t begin = p.begins != nullptr ? p.begins[b] : 0;
     const int64_t room = p.pt_stride << p.page_shift;
     if (L < 0 || L > room || begin < 0) {
-        if (threadIdx.x == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
+        if (lane == 0 && ww == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
         L = L < 0 ? 0 : min(L, room);
         begin = max(begin, static_cast<int64_t>(0));
     }

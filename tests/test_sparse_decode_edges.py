@@ -41,3 +41,23 @@ def test_run_selected_over_codes_keeps_the_probabilities(d, hq, hk, page, budget
     mag, _ = attend_reference(q, kk, vv.abs(), ids, counts, 1 / math.sqrt(d))
     off = np.abs(out.double().cpu().numpy() - ref)
     assert (off <= 2.0 ** -16 * mag).all(), (off / np.maximum(mag, 1e-30)).max()
+
+
+# ----------------------------------------------------------------------------------------------------- page bounds
+
+@gpu
+@pytest.mark.parametrize("hk,d,page", [(1, 128, 16), (2, 64, 8), (3, 128, 16), (1, 512, 256)])
+@pytest.mark.parametrize("bad", range(6))
+def test_page_bounds_flags_any_one_sequence(hk, d, page, bad):
+    """A bad length or begin of one sequence alone, whichever it is: four of them share a CTA of one-warp units."""
+    k, _ = make_pool(12, hk, page, d, "bf16", "hnd", 1)
+    bounds = torch.zeros(12, hk, 2, d, dtype=torch.bfloat16, device="cuda")
+    table = i32(np.arange(12).reshape(6, 2))
+    for lens, begins in (({bad: 2 * page + 1}, {}), ({bad: -1}, {}), ({}, {bad: -1})):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        fd.fdec_page_bounds(k, bounds, table, i32([begins.get(b, page) for b in range(6)]),
+                            i32([lens.get(b, 2 * page) for b in range(6)]), page, expected_tokens=1, device_errors=err)
+        assert int(err.item()) == fd.DEVERR_SEQ_LEN
+    err.zero_()
+    fd.fdec_page_bounds(k, bounds, table, i32([page] * 6), i32([2 * page] * 6), page, expected_tokens=1, device_errors=err)
+    assert int(err.item()) == 0
