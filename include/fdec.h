@@ -339,8 +339,10 @@ fdec_status fdec_append_e4m3(const void* k_new, const void* v_new, int64_t new_s
  *   batch_indices, positions, page_table, page_table_stride: as for fdec_append;
  *      rope_positions: int32 device [n_tokens], the rows of cos_sin, or NULL (positions).
  *   kv_dtype: FDEC_KV_SAME, or FDEC_KV_E4M3 (head_dim 128 and 256): the codes stored
- *      are those of k / k_scale and v / v_scale, rounded to nearest even, saturating at
- *      448.  Scales are 1 for a 16-bit cache.
+ *      are those of k / k_scale and v / v_scale (fp32 quotients, of k's fp32 result),
+ *      rounded to nearest even, saturating at 448; with a scale outside [2^-60, 2^60] a
+ *      quotient half way between two codes may go either way.  Scales are 1 for a 16-bit
+ *      cache.
  *   device_errors: optional uint32 device word.  A token with a bad sequence, position
  *      (or a row outside cos_sin) sets FDEC_DEVERR_SEQ_LEN, one with a bad page id
  *      FDEC_DEVERR_PAGE_ID; nothing of that token is written, its q_out rows included.

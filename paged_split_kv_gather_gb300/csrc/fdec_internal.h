@@ -237,7 +237,7 @@ struct NormRopeParams {
     int64_t v_pages, v_sp, v_sh, v_st;
     unsigned* err;
     int n_tokens, batch, hq, hk, page_shift, rot;
-    float eps, k_inv, v_inv;   // 1 / k_scale, 1 / v_scale
+    float eps, k_scale, v_scale, k_inv, v_inv;  // inv: 1 / scale
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, bool bf16, bool kv8, bool pairs, int num_sms,
                              cudaStream_t s);

@@ -51,11 +51,30 @@ __device__ __forceinline__ void unpack8(const uint4& w, float2 (&x)[4]) {
     x[3] = unpack2<BF16>(w.w);
 }
 
-// Eight values rounded to E4M3 codes (saturating at 448).
-__device__ __forceinline__ uint2 codes8(const float2 (&x)[4]) {
+// |a| at most 65536, with a's sign; NaN stays NaN.
+__device__ __forceinline__ float at_most_65536(float a) {
+    float v;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(65536.f));
+    return v;
+}
+
+// Eight values divided by the scale and rounded to E4M3 codes (saturating at 448); inv is
+// the rounded 1 / scale.  The quotient is the rounded one: the values are 16-bit ones or
+// products of them, so quotients half way between two codes do occur, and x inv, an ulp
+// off, puts those on the wrong side (scale 7/256: 60 of the finite bf16 values).  It is
+// q + (x - q scale) inv, q = x inv, with fused multiply-adds (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000 processor, 1990): exact residual, hence
+// rounded once, for scales in [2^-60, 2^60].  (32768 tokens of 32/8 heads of 128 137.8 us,
+// with the product alone 135.3, with __fdiv_rn 160.7.)
+__device__ __forceinline__ uint2 codes8(const float2 (&x)[4], float scale, float inv) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __nv_cvt_float2_to_fp8x2(x[i], __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+        float2 q = __fmul2_rn(x[i], make_float2(inv, inv));
+        q = make_float2(at_most_65536(q.x), at_most_65536(q.y));  // (an infinite q would have no residual)
+        const float2 r = __ffma2_rn(q, make_float2(-scale, -scale), x[i]);
+        c[i] = __nv_cvt_float2_to_fp8x2(__ffma2_rn(r, make_float2(inv, inv), q), __NV_SATFINITE, __NV_E4M3);
+    }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
@@ -67,7 +86,7 @@ struct Coef {
 
 template <bool BF16, bool INTER>
 __device__ __forceinline__ void make_coef(Coef& f, const uint16_t* weight, const float* cs, int half, int c0, int c1,
-                                          bool rotated, float factor) {
+                                          bool rotated) {
     float2 w0[4], w1[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w0[k] = w1[k] = make_float2(1.f, 1.f);
@@ -77,7 +96,6 @@ __device__ __forceinline__ void make_coef(Coef& f, const uint16_t* weight, const
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        w0[k].x *= factor, w0[k].y *= factor, w1[k].x *= factor, w1[k].y *= factor;
         f.a0[k] = w0[k], f.a1[k] = w1[k];
         f.b0[k] = f.b1[k] = make_float2(0.f, 0.f);
     }
@@ -185,7 +203,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
         // The q rows or the k rows: norm and rotation of rows h < heads at src + h * src_h, the
         // first of them in r0, r1 with PRE.
         auto normed = [&](const uint8_t* src, int64_t src_h, uint8_t* dst, int64_t dst_h, int heads, int from, int groups,
-                          const uint16_t* weight, float factor, auto codes, uint4 (&r0)[U], uint4 (&r1)[U]) {
+                          const uint16_t* weight, auto codes, uint4 (&r0)[U], uint4 (&r1)[U]) {
             constexpr bool CODES = decltype(codes)::value;
             int g = first_group(from);
             if (g >= groups) return;
@@ -193,7 +211,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
             auto load = [&](int at, uint4 (&a)[U], uint4 (&c)[U]) { load_rows(src, src_h, heads, at, a, c); };
             if constexpr (!PRE) load(g, r0, r1);
             Coef f;
-            make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated, factor);
+            make_coef<BF16, INTER>(f, weight, cs, half, c0, c1, rotated);
             for (; g < groups; g += U * wpt) {
                 // (a lane stores only chunks that it has loaded itself, so q_out may be q)
                 load(g + U * wpt, n0, n1);
@@ -230,8 +248,8 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
                     if (!on || h >= heads || !page_ok) continue;
                     uint8_t* to = dst + h * dst_h;
                     if constexpr (CODES) {
-                        *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(y0);
-                        *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(y1);
+                        *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(y0, p.k_scale, p.k_inv);
+                        *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(y1, p.k_scale, p.k_inv);
                     } else {
                         *reinterpret_cast<uint4*>(to + 16 * c0) =
                             make_uint4(pack2<BF16>(y0[0].x, y0[0].y), pack2<BF16>(y0[1].x, y0[1].y),
@@ -252,10 +270,10 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
             load_rows(p.k_new + i * p.k_new_st, p.k_new_sh, p.hk, first_group(groups_q), k0, k1);
             load_rows(p.v_new + i * p.v_new_st, p.v_new_sh, p.hk, gv0, v0, v1);
         }
-        normed(p.q + i * p.q_st, p.q_sh, p.q_out + i * p.q_out_st, p.q_out_sh, p.hq, 0, groups_q, p.q_weight, 1.f,
+        normed(p.q + i * p.q_st, p.q_sh, p.q_out + i * p.q_out_st, p.q_out_sh, p.hq, 0, groups_q, p.q_weight,
                std::false_type{}, q0, q1);
         normed(p.k_new + i * p.k_new_st, p.k_new_sh, p.k_base + page * p.k_sp + slot * p.k_st, p.k_sh, p.hk, groups_q,
-               groups_kv, p.k_weight, p.k_inv, std::bool_constant<KV8>{}, k0, k1);
+               groups_kv, p.k_weight, std::bool_constant<KV8>{}, k0, k1);
         if (!page_ok) {
             if (lane == 0 && part == 0 && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
             continue;
@@ -275,14 +293,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) norm_rope_kernel(cons
             }
             uint8_t* to = dst + h * p.v_sh;
             if constexpr (KV8) {
-                const float2 inv = make_float2(p.v_inv, p.v_inv);
                 float2 x0[4], x1[4];
                 unpack8<BF16>(r0, x0);
                 unpack8<BF16>(r1, x1);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x0[k] = __fmul2_rn(x0[k], inv), x1[k] = __fmul2_rn(x1[k], inv);
-                *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(x0);
-                *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(x1);
+                *reinterpret_cast<uint2*>(to + 8 * c0) = codes8(x0, p.v_scale, p.v_inv);
+                *reinterpret_cast<uint2*>(to + 8 * c1) = codes8(x1, p.v_scale, p.v_inv);
             } else {
                 *reinterpret_cast<uint4*>(to + 16 * c0) = r0;
                 *reinterpret_cast<uint4*>(to + 16 * c1) = r1;

@@ -147,8 +147,8 @@ fdec_status fdec_norm_rope_append(fdec_rows q, fdec_rows k_new, fdec_rows v_new,
     p.page_shift = page_shift_of(page_size);
     p.rot = rot_dim;
     p.eps = eps;
-    // The division by a scale is one by its reciprocal, rounded: the codes' own step is
-    // 2^19 of those roundings.
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
     p.k_inv = 1.f / k_scale;
     p.v_inv = 1.f / v_scale;
     int num_sms = 0;

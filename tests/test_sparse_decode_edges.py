@@ -61,3 +61,42 @@ def test_page_bounds_flags_any_one_sequence(hk, d, page, bad):
     err.zero_()
     fd.fdec_page_bounds(k, bounds, table, i32([page] * 6), i32([2 * page] * 6), page, expected_tokens=1, device_errors=err)
     assert int(err.item()) == 0
+
+
+# ------------------------------------------------------------------------------------------- norm, rotation, append
+
+def codes_of(x, scale):
+    """E4M3 codes of x / scale, an fp32 division, to nearest even, saturating."""
+    return (x.float() / torch.tensor(scale, dtype=torch.float32)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+@gpu
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("scale", [7 / 256, 15 / 256, 0.03, 0.0234375, 3e-6, 1.7, 2 - 2.0 ** -23, 1 - 2.0 ** -24, 5e7])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_codes_are_those_of_the_quotient(dtype, scale, d):
+    """Every 16-bit value as a value row, bit for bit; as a key those whose quotient's code a product with the
+    reciprocal would miss (ties among them): rows of +-1 with eps 0 have norm 1, so the key is the weight itself."""
+    t = DT[dtype]
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(t)
+    x = torch.cat([x[torch.isfinite(x.float())], torch.tensor([math.inf, -math.inf, math.nan], dtype=t)])
+    s = torch.tensor(scale, dtype=torch.float32)
+    product = (x.float() * (1 / s)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    keys = torch.cat([x[codes_of(x, scale) != product], x[:-3:61]])[:d]
+    weight = torch.ones(d, dtype=t)
+    weight[:len(keys)] = keys
+    n = -(-len(x) // d)
+    v_new = torch.zeros(n * d, dtype=t)
+    v_new[:len(x)] = x
+    v_new = v_new.view(n, 1, d)
+    sign = torch.where(torch.rand(n, 1, d, generator=torch.Generator().manual_seed(1)) < 0.5, -1.0, 1.0).to(t)
+    page = 16
+    pages = -(-n // page)
+    k, v = (torch.zeros(pages, 1, page, d, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    q = torch.zeros(n, 1, d, dtype=t, device="cuda")
+    fd.fdec_norm_rope_append(q, sign.cuda(), v_new.cuda(), None, weight.cuda(), None, i32(np.zeros(n)), i32(np.arange(n)), q,
+                             k, v, i32(np.arange(pages)[None]), page, eps=0.0, k_scale=scale, v_scale=scale)
+    got_k, got_v = (c.view(torch.uint8).reshape(-1, 1, d)[:n].cpu() for c in (k, v))
+    magnitude = lambda c: torch.where((c & 0x7F) == 0, 0, c)  # noqa: E731  (the sign of a zero is not compared)
+    assert torch.equal(magnitude(got_v), magnitude(codes_of(v_new, scale)))
+    assert torch.equal(magnitude(got_k), magnitude(codes_of(sign * weight, scale)))
