@@ -463,6 +463,9 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
             ids[x] = j >= 0 ? ld_cg(table + j) : -1;
             if (index != nullptr) index[x] = j;
         }
+        // The next kernel waits for this grid alone, and it may overwrite what the scoring
+        // CTAs still read: this grid must not complete before them.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     for (int x = tid; x < p.first + p.last; x += NT) {

@@ -3,13 +3,15 @@ ties, stream order, refusals of tensors that are not on the GPU, plans with and 
 
 Tolerances are derived beside each test."""
 import math
+import os
+import re
 
 import numpy as np
 import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from tests.test_sparse_decode import DT, attend_reference, gpu, i32, make_pool, selected_lists
+from tests.test_sparse_decode import DT, attend_reference, bounds_like, gpu, i32, make_pool, select_reference, selected_lists
 
 
 # ------------------------------------------------------------------------------------------- attention over codes
@@ -100,3 +102,61 @@ def test_codes_are_those_of_the_quotient(dtype, scale, d):
     magnitude = lambda c: torch.where((c & 0x7F) == 0, 0, c)  # noqa: E731  (the sign of a zero is not compared)
     assert torch.equal(magnitude(got_v), magnitude(codes_of(v_new, scale)))
     assert torch.equal(magnitude(got_k), magnitude(codes_of(sign * weight, scale)))
+
+
+# ---------------------------------------------------------------------------------------------------- stream order
+
+def kernel_bodies():
+    """(file, name, body) of every __global__ function of the library's sources, comments taken out."""
+    root = os.path.join(os.path.dirname(fd.__file__), "csrc")
+    for name in sorted(os.listdir(root)):
+        text = open(os.path.join(root, name)).read()
+        text = re.sub(r"//[^\n]*", "", text)
+        for m in re.finditer(r"__global__[^;{]*?(\w+)\s*\((?=[^;{]*\{)", text):
+            at = text.index("{", m.end())
+            depth, end = 0, at
+            while True:
+                depth += {"{": 1, "}": -1}.get(text[end], 0)
+                if depth == 0:
+                    break
+                end += 1
+            yield name, re.search(r"(\w+)\s*\((?:const\s|AppendParams)", text[m.start():at]).group(1), text[at:end]
+
+
+def test_dependent_kernels_wait_on_every_way_out():
+    """A kernel that is launched as a programmatic dependent completes only after the kernel before it: no return comes
+    before a wait.  (The kernel after it waits for this one alone.)"""
+    seen = {}
+    for file, name, body in kernel_bodies():
+        if "griddepcontrol.wait" not in body:
+            continue
+        first = body.index("griddepcontrol.wait")
+        for m in re.finditer(r"\breturn;", body):
+            assert m.start() > first, f"{file}: {name} returns before its wait"
+        seen[name] = file
+    assert {"norm_rope_kernel", "page_bounds_kernel", "score_pages_kernel", "choose_pages_kernel", "share_merge_kernel",
+            "reduce_kernel", "split_mma_kernel", "split_mma_persist_kernel"} <= set(seen), seen
+
+
+@gpu
+def test_select_pages_of_short_rows_keeps_stream_order():
+    """Inputs overwritten right after a selection in which every row is short (the scoring has nothing to do), and
+    again after one in which every row is long."""
+    t, d, hk, hq, page, width, budget, b = torch.bfloat16, 128, 2, 8, 16, 64, 12, 40
+    table = np.random.default_rng(3).permutation(b * width).reshape(b, width)
+    bounds = bounds_like(b * width, hk, d, t, 4)
+    q = torch.randn(b, 1, hq, d, generator=torch.Generator().manual_seed(5)).to(t).cuda()
+    short, full = [x % (budget * page + 1) for x in range(0, 5 * b, 5)], [width * page - x for x in range(b)]
+    want = [select_reference(q, bounds, table, n, page, budget, 1, 1, True) for n in (short, full)]
+    tb, lens = i32(table), i32(short)
+    both = [i32(short), i32(full)]
+    sel = fd.PageSelect(b, 1, page, hq, hk, d, width, budget, "bf16")
+    got = []
+    for i in range(60):
+        lens.copy_(both[i % 2])
+        got.append([x.clone() for x in sel.run(q, bounds, tb, lens)])
+    lens.zero_()
+    assert sel.device_errors() == 0
+    for i, out in enumerate(got):
+        for a, w in zip(out, want[i % 2]):
+            assert np.array_equal(a.cpu().numpy(), w), i
