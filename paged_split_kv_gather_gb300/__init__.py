@@ -439,7 +439,8 @@ def _sparse():
                 mod = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(mod)
                 mod.set_entries(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                    lib.fdec_norm_rope_append, lib.fdec_page_bounds, lib.fdec_select_pages, lib.fdec_run_selected)))
+                    lib.fdec_norm_rope_append, lib.fdec_page_bounds, lib.fdec_select_pages, lib.fdec_run_selected,
+                    lib.fdec_internal_checks_only)))
                 _binding = mod
     return _binding
 

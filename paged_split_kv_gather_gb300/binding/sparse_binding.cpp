@@ -4,14 +4,15 @@
 // reading a dozen tensors' pointers, shapes and strides from interpreted code takes
 // 15-25 us a call, from here about 1 us.  Only checks and marshalling: every step of the
 // computation is behind the C ABI, whose functions are given by address (set_entry), so
-// this module and ctypes use one copy of the library.  A check of a tensor's type or
-// shape raises ValueError; the library's own refusals come back as its status.
+// this module and ctypes use one copy of the library.  A check of a tensor's type, shape
+// or device raises ValueError; the library's own refusals come back as its status.
 #include <cstdint>
 #include <stdexcept>
 #include <string>
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "../../include/fdec.h"
@@ -56,8 +57,9 @@ float real(PyObject* o) {
     return static_cast<float>(v);
 }
 
-cudaStream_t stream_of(PyObject* o) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
+// The stream given, or the current one of the tensors' device.
+cudaStream_t stream_of(PyObject* o, c10::Device device) {
+    if (o == Py_None) return device.is_cuda() ? c10::cuda::getCurrentCUDAStream(device.index()).stream() : nullptr;
     if (PyLong_Check(o)) return reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
     PyObject* handle = PyObject_GetAttrString(o, "cuda_stream");
     if (handle == nullptr) throw Bad("");
@@ -135,6 +137,29 @@ decltype(&fdec_norm_rope_append) g_norm_rope_append = nullptr;
 decltype(&fdec_page_bounds) g_page_bounds = nullptr;
 decltype(&fdec_select_pages) g_select_pages = nullptr;
 decltype(&fdec_run_selected) g_run_selected = nullptr;
+void (*g_checks_only)(int) = nullptr;
+constexpr int kChecksOnly = -1;  // the status of a call that has passed its checks and launched nothing
+
+// The library call f(stream) on the device of its tensors.  Tensors that are not on a GPU
+// go through its checks, which touch no element, and are refused where it would launch.
+template <typename F>
+fdec_status on_device(const Tensor& t, PyObject* stream, F&& f) {
+    const cudaStream_t s = stream_of(stream, t.device());
+    if (t.is_cuda()) {
+        const c10::cuda::CUDAGuard guard(t.device());
+        return f(s);
+    }
+    struct ChecksOnly {
+        ChecksOnly() { g_checks_only(1); }
+        ~ChecksOnly() { g_checks_only(0); }
+    };
+    const fdec_status st = [&] {
+        const ChecksOnly scope;
+        return f(s);
+    }();
+    need(static_cast<int>(st) != kChecksOnly, "tensors must be on a CUDA device");
+    return st;
+}
 
 // Run f() -> status; C++ exceptions become Python ones.
 template <typename F>
@@ -190,12 +215,14 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                  k.size(2) == page_size && k.size(3) == d && v.sizes().slice(1) == k.sizes().slice(1),
              "k and v must be caches [page, Hk, page_size, D] of one type");
         on(q, {&k_new, &v_new, &q_weight, &k_weight, &cs, &bi, &pos, &rope, &q_out, &k, &v, &table, &errors});
-        return g_norm_rope_append(rows(q), rows(k_new), rows(v_new), ptr(q_weight), ptr(k_weight), real(a[13]),
-                                  static_cast<const float*>(ptr(cs)), cs.defined() ? cs.size(0) : 0,
-                                  cs.defined() ? as_int(cs.size(1)) : 0, PyObject_IsTrue(a[14]), bi_p, pos_p, rope_p,
-                                  as_int(n), as_int(hq), as_int(hk), as_int(d), page_size, dtype, kv, real(a[16]),
-                                  real(a[17]), rows(q_out), pool(k), pool(v), table_p, as_int(table.size(0)),
-                                  table_stride(table), error_word(errors), stream_of(a[19]));
+        return on_device(q, a[19], [&](cudaStream_t stream) {
+            return g_norm_rope_append(rows(q), rows(k_new), rows(v_new), ptr(q_weight), ptr(k_weight), real(a[13]),
+                                      static_cast<const float*>(ptr(cs)), cs.defined() ? cs.size(0) : 0,
+                                      cs.defined() ? as_int(cs.size(1)) : 0, PyObject_IsTrue(a[14]), bi_p, pos_p, rope_p,
+                                      as_int(n), as_int(hq), as_int(hk), as_int(d), page_size, dtype, kv, real(a[16]),
+                                      real(a[17]), rows(q_out), pool(k), pool(v), table_p, as_int(table.size(0)),
+                                      table_stride(table), error_word(errors), stream);
+        });
     });
 }
 
@@ -221,9 +248,11 @@ PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         int64_t expected = integer(a[6]);
         if (expected <= 0) expected = table.size(1) * page_size;
         if (expected > INT32_MAX) expected = INT32_MAX;
-        return g_page_bounds(pool(k), pool(bounds), table_p, as_int(table.size(0)), table_stride(table), begins_p, lens_p,
-                             as_int(k.size(1)), as_int(k.size(3)), page_size, dtype, kv, static_cast<int>(expected),
-                             error_word(errors), stream_of(a[8]));
+        return on_device(k, a[8], [&](cudaStream_t stream) {
+            return g_page_bounds(pool(k), pool(bounds), table_p, as_int(table.size(0)), table_stride(table), begins_p,
+                                 lens_p, as_int(k.size(1)), as_int(k.size(3)), page_size, dtype, kv,
+                                 static_cast<int>(expected), error_word(errors), stream);
+        });
     });
 }
 
@@ -259,13 +288,15 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         need(counts.size(0) == b * q_len && counts.size(1) == hk && counts.is_contiguous(),
              "counts must be contiguous [B * Q, Hk]");
         on(q, {&bounds, &table, &lens, &ids, &counts, &indices, &ws, &errors});
-        return g_select_pages(q.data_ptr(), tok, head, pool(bounds), table_p, table_stride(table), lens_p, as_int(b),
-                              as_int(q_len), page_size, as_int(hq), as_int(hk), as_int(d), dtype,
-                              PyObject_IsTrue(a[13]), max_pages, budget, small(a[11], "first_pages"),
-                              small(a[12], "last_pages"), static_cast<int32_t*>(ids.data_ptr()),
-                              static_cast<int32_t*>(counts.data_ptr()), static_cast<int32_t*>(ptr(indices)),
-                              ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size(), error_word(errors),
-                              stream_of(a[15]));
+        return on_device(q, a[15], [&](cudaStream_t stream) {
+            return g_select_pages(q.data_ptr(), tok, head, pool(bounds), table_p, table_stride(table), lens_p, as_int(b),
+                                  as_int(q_len), page_size, as_int(hq), as_int(hk), as_int(d), dtype,
+                                  PyObject_IsTrue(a[13]), max_pages, budget, small(a[11], "first_pages"),
+                                  small(a[12], "last_pages"), static_cast<int32_t*>(ids.data_ptr()),
+                                  static_cast<int32_t*>(counts.data_ptr()), static_cast<int32_t*>(ptr(indices)),
+                                  ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size(),
+                                  error_word(errors), stream);
+        });
     });
 }
 
@@ -305,17 +336,21 @@ PyObject* run_selected(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         need(ids.size(0) == n && ids.size(1) == hk && ids.is_contiguous(), "page_ids must be contiguous [N, Hk, W]");
         need(counts.size(0) == n && counts.size(1) == hk && counts.is_contiguous(), "counts must be contiguous [N, Hk]");
         on(q, {&k, &v, &ids, &counts, &out, &lse, &ws});
-        return g_run_selected(plan, q.data_ptr(), tok, head, pool(k), pool(v), ids_p, ids.size(2), counts_p, real(a[10]),
-                              real(a[11]), real(a[12]), out.data_ptr(), f32 ? FDEC_OUT_F32 : FDEC_OUT_SAME,
-                              static_cast<float*>(ptr(lse)), ws.data_ptr(), stream_of(a[13]));
+        return on_device(q, a[13], [&](cudaStream_t stream) {
+            return g_run_selected(plan, q.data_ptr(), tok, head, pool(k), pool(v), ids_p, ids.size(2), counts_p,
+                                  real(a[10]), real(a[11]), real(a[12]), out.data_ptr(),
+                                  f32 ? FDEC_OUT_F32 : FDEC_OUT_SAME, static_cast<float*>(ptr(lse)), ws.data_ptr(),
+                                  stream);
+        });
     });
 }
 
-// The addresses of fdec_norm_rope_append, fdec_page_bounds, fdec_select_pages and fdec_run_selected.
+// The addresses of fdec_norm_rope_append, fdec_page_bounds, fdec_select_pages, fdec_run_selected and
+// fdec_internal_checks_only.
 PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    if (!has(n_args, 4)) return nullptr;
-    void* p[4];
-    for (int i = 0; i < 4; ++i) {
+    if (!has(n_args, 5)) return nullptr;
+    void* p[5];
+    for (int i = 0; i < 5; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -323,6 +358,7 @@ PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     g_page_bounds = reinterpret_cast<decltype(&fdec_page_bounds)>(p[1]);
     g_select_pages = reinterpret_cast<decltype(&fdec_select_pages)>(p[2]);
     g_run_selected = reinterpret_cast<decltype(&fdec_run_selected)>(p[3]);
+    g_checks_only = reinterpret_cast<decltype(g_checks_only)>(p[4]);
     Py_RETURN_NONE;
 }
 

@@ -99,6 +99,10 @@ int record_cuda_failure(cudaError_t e, const char* what) noexcept {
 
 void clear_failure() noexcept { g_last_error.clear(); }
 
+static thread_local bool g_checks_only = false;
+
+bool checks_only() noexcept { return g_checks_only; }
+
 cudaError_t current_num_sms(int* num_sms) {
     static std::atomic<int> sms[64];  // 0 = not yet queried
     int dev = 0;
@@ -812,6 +816,7 @@ static fdec_status run_impl(fdec_plan_t p, const void* q, int64_t q_stride_tok, 
         return fail(FDEC_ERR_LAYOUT, "misaligned q, out or lse");
     if (workspace == nullptr || workspace != p->uploaded)
         return fail(FDEC_ERR_WORKSPACE, "workspace is not the buffer this plan was uploaded to");
+    if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
 
     if (p->page_size >= 8 && !(p->maps_valid && same_desc(p->map_k, k) && same_desc(p->map_v, v))) {
         const int stage_rows = p->path == FDEC_PATH_TC ? kTcStageTokens : kStageTokens;
@@ -993,6 +998,9 @@ fdec_status fdec_run_q8_0(fdec_plan_t p, const void* q, int64_t q_stride_tok, in
     return run_impl(p, q, q_stride_tok, q_stride_head, k, v, &k_scales, &v_scales, page_table, page_table_stride,
                     seq_lens_dev, scale, 1.f, 1.f, out, lse, workspace, stream);
 }
+
+// Not part of the ABI: see checks_only.
+void fdec_internal_checks_only(int on) { fdec::g_checks_only = on != 0; }
 
 fdec_status fdec_run_selected(fdec_plan_t p, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
                               fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_ids, int64_t page_ids_stride,

@@ -287,6 +287,11 @@ cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num
 int record_failure(int status, const char* message) noexcept;
 int record_cuda_failure(cudaError_t e, const char* what) noexcept;
 void clear_failure() noexcept;
+// Whether this thread's calls stop where they would launch, with kChecksOnly as their
+// status: how the binding has tensors refused that are not on a GPU, after every other
+// check of theirs (see sparse_binding.cpp).
+constexpr int kChecksOnly = -1;
+bool checks_only() noexcept;
 // SM count of the current device, queried once per device.
 cudaError_t current_num_sms(int* num_sms);
 // One task given by value (p.tasks must be null): used by fdec_merge_states.

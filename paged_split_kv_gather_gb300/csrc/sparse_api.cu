@@ -151,6 +151,7 @@ fdec_status fdec_norm_rope_append(fdec_rows q, fdec_rows k_new, fdec_rows v_new,
     p.v_scale = v_scale;
     p.k_inv = 1.f / k_scale;
     p.v_inv = 1.f / v_scale;
+    if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
     int num_sms = 0;
     cudaError_t e = current_num_sms(&num_sms);
     if (e == cudaSuccess) e = launch_norm_rope(p, head_dim, dtype == FDEC_BF16, kv8, interleaved != 0, num_sms, stream);
@@ -201,6 +202,7 @@ fdec_status fdec_page_bounds(fdec_kv_desc k, fdec_kv_desc bounds, const int32_t*
     p.span = static_cast<int>(std::max<int64_t>(1, std::min({pages, page_table_stride, most})));
     if (static_cast<int64_t>(batch) * num_kv_heads > (int64_t{1} << 30))
         return fail(FDEC_ERR_UNSUPPORTED, "batch x num_kv_heads too large");
+    if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
     int num_sms = 0;
     cudaError_t e = current_num_sms(&num_sms);
     if (e == cudaSuccess)
@@ -308,6 +310,7 @@ fdec_status fdec_select_pages(const void* q, int64_t q_stride_tok, int64_t q_str
     p.first = first_pages;
     p.last = last_pages;
     p.head_dim = p.chunk = p.n_chunks = p.chain = 0;
+    if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
     int num_sms = 0;
     cudaError_t e = current_num_sms(&num_sms);
     if (e == cudaSuccess) e = launch_select_pages(p, head_dim, dtype == FDEC_BF16, num_sms, stream);

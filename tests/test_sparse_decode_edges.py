@@ -11,7 +11,8 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from tests.test_sparse_decode import DT, attend_reference, bounds_like, gpu, i32, make_pool, select_reference, selected_lists
+from tests.test_sparse_decode import (DT, attend_reference, bounds_like, cpu_rows, gpu, i32, make_pool, select_reference,
+                                       selected_lists)
 
 
 # ------------------------------------------------------------------------------------------- attention over codes
@@ -160,3 +161,47 @@ def test_select_pages_of_short_rows_keeps_stream_order():
     for i, out in enumerate(got):
         for a, w in zip(out, want[i % 2]):
             assert np.array_equal(a.cpu().numpy(), w), i
+
+
+# ---------------------------------------------------------------------------------------------- refusals (no device)
+
+def test_tensors_that_are_not_on_a_gpu_are_refused():
+    """Well-formed calls on host tensors: past every check of the library's own, and refused before a launch."""
+    def refused(fn, *args, **kw):
+        for stream in (0, None):
+            with pytest.raises(ValueError, match="CUDA device"):
+                fn(*args, stream=stream, **kw)
+
+    rows = cpu_rows()
+    refused(fd.fdec_norm_rope_append, **rows)
+    k, bounds = torch.zeros(4, 2, 16, 64, dtype=torch.float16), torch.zeros(4, 2, 2, 64, dtype=torch.float16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    refused(fd.fdec_page_bounds, k, bounds, i(1, 4), None, i(1), 16)
+    total = fd.fdec_select_pages_workspace(1, 1, 2, 8)
+    buf = torch.zeros(total + 256, dtype=torch.uint8)
+    ws = buf[(-buf.data_ptr()) % 256:][:total]
+    refused(fd.fdec_select_pages, torch.zeros(1, 1, 4, 64, dtype=torch.float16), bounds, i(1, 8), i(1), 16, 8, 4, i(1, 2, 4),
+            i(1, 2), None, ws)
+    # the library's own refusals come first, and later calls of the thread are not held back
+    with pytest.raises(fd.FdecError):
+        fd.fdec_page_bounds(k[..., :60], bounds[..., :60], i(1, 4), None, i(1), 16, stream=0)
+    with pytest.raises(ValueError):
+        fd.fdec_page_bounds(k, bounds, i(1, 4), None, i(1), 16, device_errors=torch.zeros(1).double(), stream=0)
+    fd.fdec_norm_rope_append(stream=0, **cpu_rows(n=0))  # no token: nothing to refuse
+
+
+@gpu
+def test_calls_use_the_current_stream_of_the_tensors_device():
+    """After refusals on host tensors, a call on the GPU still launches, on the stream that is current."""
+    test_tensors_that_are_not_on_a_gpu_are_refused()
+    k, _ = make_pool(4, 2, 16, 64, "f16", "hnd", 3)
+    bounds = torch.zeros(4, 2, 2, 64, dtype=torch.float16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    table, lens = i32(np.arange(4)[None]), i32([64])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fd.fdec_page_bounds(k, bounds, table, None, lens, 16)
+        copy = bounds.clone()
+    side.synchronize()
+    assert torch.equal(copy, torch.stack([k.amin(2), k.amax(2)], 2))
