@@ -287,6 +287,7 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         index(counts, 2, "counts");
         need(counts.size(0) == b * q_len && counts.size(1) == hk && counts.is_contiguous(),
              "counts must be contiguous [B * Q, Hk]");
+        need(ws.is_contiguous(), "workspace must be contiguous");
         on(q, {&bounds, &table, &lens, &ids, &counts, &indices, &ws, &errors});
         return on_device(q, a[15], [&](cudaStream_t stream) {
             return g_select_pages(q.data_ptr(), tok, head, pool(bounds), table_p, table_stride(table), lens_p, as_int(b),

@@ -205,3 +205,14 @@ def test_calls_use_the_current_stream_of_the_tensors_device():
         copy = bounds.clone()
     side.synchronize()
     assert torch.equal(copy, torch.stack([k.amin(2), k.amax(2)], 2))
+
+
+def test_a_workspace_of_repeated_bytes_is_refused():
+    """numel bytes that are not all there: a tensor expanded from one byte."""
+    total = fd.fdec_select_pages_workspace(1, 1, 2, 8)
+    buf = torch.zeros(512, dtype=torch.uint8)
+    at = (-buf.data_ptr()) % 256
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="contiguous"):
+        fd.fdec_select_pages(torch.zeros(1, 1, 4, 64, dtype=torch.float16), torch.zeros(4, 2, 2, 64, dtype=torch.float16),
+                             i(1, 8), i(1), 16, 8, 4, i(1, 2, 4), i(1, 2), None, buf[at:at + 1].expand(total), stream=0)
