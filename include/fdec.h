@@ -186,6 +186,19 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
                       size_t* workspace_bytes);
 
 /*
+ * fdec_plan for calls of fdec_run_selected (q_len 1: one sequence per query token;
+ * 16-bit or E4M3 caches).  The workspace also holds what runs lists of lengths that only
+ * the device knows: for 16-bit caches, where the work is cut at run time, two partial rows
+ * of 16 x head_dim floats for every resident CTA (5 to 10 MB at 152 SMs); for E4M3 caches the
+ * lists' own splits.  Everything else that takes a plan takes this one too.
+ * fdec_run_selected also runs plans of fdec_plan, with their splits: the lists then cost
+ * what the longest would (64 x 8 ragged lists of up to 2048 tokens 82 us instead of 62).
+ */
+fdec_status fdec_plan_selected(const int32_t* seq_lens_host, int batch, int page_size, int num_qo_heads,
+                               int num_kv_heads, int head_dim, fdec_dtype dtype, const fdec_plan_opts* opts,
+                               fdec_plan_t* out_plan, size_t* workspace_bytes);
+
+/*
  * Copy the plan's work lists into `workspace` (>= workspace_bytes, 256-byte
  * aligned, device memory) and clear its device error word.  Must not be called
  * while `stream` is capturing (FDEC_ERR_CAPTURING).  Blocks until the copy is done.
@@ -415,8 +428,9 @@ fdec_status fdec_select_pages(const void* q, int64_t q_stride_tok, int64_t q_str
 /*
  * Attention over selected pages: fdec_run_scaled with a page list and a length for each
  * query token and KV head (of fdec_select_pages, or of the caller's own choice).
- *   plan: q_len 1, batch = the number of query tokens, capacities = the most tokens a
- *      list holds (budget * page_size); 16-bit or E4M3 cache.
+ *   plan: of fdec_plan_selected (or of fdec_plan with q_len 1, at a cost in time: see
+ *      there), batch = the number of query tokens, capacities = the most tokens a list
+ *      holds (budget * page_size); 16-bit or E4M3 cache.
  *   page_ids: int32 device [batch][num_kv_heads][page_ids_stride]; counts: int32 device
  *      [batch][num_kv_heads], the tokens in the list: every page is full but the last.
  *   out: [batch][num_qo_heads][head_dim] contiguous, 16-byte aligned; out_type
@@ -434,6 +448,15 @@ fdec_status fdec_plan_destroy(fdec_plan_t plan);
 
 /* Report what the plan decided. */
 fdec_status fdec_plan_get_info(fdec_plan_t plan, fdec_plan_info* info);
+
+/* What fdec_run_selected does with a plan. */
+typedef struct {
+    int page_lists;        /* 1: planned by fdec_plan_selected */
+    int share_ctas;        /* CTAs that take equal shares of the lists; 0: planned splits */
+    int blocks_per_split;  /* of the planned splits */
+    int launches;          /* kernel launches per fdec_run_selected */
+} fdec_selected_info;
+fdec_status fdec_plan_get_selected_info(fdec_plan_t plan, fdec_selected_info* info);
 
 /* Per-sequence split counts (batch entries). */
 fdec_status fdec_plan_get_splits(fdec_plan_t plan, int32_t* splits, int batch);

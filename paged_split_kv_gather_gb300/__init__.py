@@ -25,7 +25,7 @@ __all__ = [
     "FDEC_F16", "FDEC_BF16", "FDEC_PATH_AUTO", "FDEC_PATH_SIMT", "FDEC_PATH_MMA", "FDEC_PATH_TC",
     "FDEC_KV_SAME", "FDEC_KV_E4M3", "FDEC_KV_Q8_0", "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
     "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
-    "fdec_run_selected", "FDEC_OUT_F32", "FDEC_OUT_SAME", "Rows", "PageSelect", "SparseDecode",
+    "fdec_run_selected", "fdec_plan_get_selected_info", "FDEC_OUT_F32", "FDEC_OUT_SAME", "Rows", "PageSelect", "SparseDecode",
     "DEVERR_PAGE_ID", "DEVERR_SEQ_LEN", "DEVERR_TIMEOUT",
 ]
 
@@ -52,7 +52,7 @@ EXPORTED_SYMBOLS = (
     "fdec_read_device_errors", "fdec_last_error", "fdec_version", "fdec_run_static_workspace", "fdec_append",
     "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
     "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
-    "fdec_run_selected",
+    "fdec_run_selected", "fdec_plan_selected", "fdec_plan_get_selected_info",
 )
 
 
@@ -78,6 +78,11 @@ class Rows(ctypes.Structure):
 class PlanOpts(ctypes.Structure):
     _fields_ = [("blocks_per_split", ctypes.c_int), ("reducer_fanin", ctypes.c_int),
                 ("path", ctypes.c_int), ("num_sms", ctypes.c_int), ("kv_dtype", ctypes.c_int)]
+
+
+class SelectedInfo(ctypes.Structure):
+    _fields_ = [("page_lists", ctypes.c_int), ("share_ctas", ctypes.c_int), ("blocks_per_split", ctypes.c_int),
+                ("launches", ctypes.c_int)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -146,6 +151,10 @@ def _load():
         lib.fdec_select_pages.restype = I
         lib.fdec_select_pages.argtypes = [P, I64, I64, KVDesc, P, I64, P, I, I, I, I, I, I, I, I, I64, I, I, I, P, P, P,
                                           P, S, P, P]
+        lib.fdec_plan_selected.restype = I
+        lib.fdec_plan_selected.argtypes = [P, I, I, I, I, I, I, ctypes.POINTER(PlanOpts), ctypes.POINTER(P), IP]
+        lib.fdec_plan_get_selected_info.restype = I
+        lib.fdec_plan_get_selected_info.argtypes = [P, ctypes.POINTER(SelectedInfo)]
         lib.fdec_run_selected.restype = I
         lib.fdec_run_selected.argtypes = [P, P, I64, I64, KVDesc, KVDesc, P, I64, P, F, F, F, P, I, P, P, P]
         lib.fdec_plan_destroy.restype = I
@@ -210,9 +219,11 @@ class Plan:
 
 def fdec_plan(seq_lens: Sequence[int], q_len: int, page_size: int, num_qo_heads: int, num_kv_heads: int,
               head_dim: int, dtype: str = "bf16", causal: bool = False, blocks_per_split: int = 0,
-              reducer_fanin: int = 0, path: int = FDEC_PATH_AUTO, num_sms: int = 0, kv_dtype: str = "") -> Plan:
+              reducer_fanin: int = 0, path: int = FDEC_PATH_AUTO, num_sms: int = 0, kv_dtype: str = "",
+              page_lists: bool = False) -> Plan:
     """kv_dtype: "" (K/V in the q dtype), "fp8" (E4M3 codes; scales go to fdec_run_scaled) or
-    "q8_0" (int8 codes with binary16 block scales; see fdec_run_q8_0)."""
+    "q8_0" (int8 codes with binary16 block scales; see fdec_run_q8_0).  page_lists: a plan of
+    fdec_plan_selected, with the workspace that fdec_run_selected runs ragged lists in (q_len 1)."""
     lib = _load()
     lens = np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32).reshape(-1))
     kvd = {"": FDEC_KV_SAME, "fp8": FDEC_KV_E4M3, "q8_0": FDEC_KV_Q8_0}[kv_dtype]
@@ -220,9 +231,15 @@ def fdec_plan(seq_lens: Sequence[int], q_len: int, page_size: int, num_qo_heads:
     handle = ctypes.c_void_p()
     ws = ctypes.c_size_t()
     dt = {"f16": FDEC_F16, "bf16": FDEC_BF16}[dtype]
-    _check(lib.fdec_plan(lens.ctypes.data, lens.shape[0], q_len, page_size, num_qo_heads, num_kv_heads,
-                         head_dim, dt, int(bool(causal)), ctypes.byref(opts), ctypes.byref(handle),
-                         ctypes.byref(ws)))
+    if page_lists:
+        if q_len != 1:
+            raise ValueError("page_lists needs q_len 1 (one sequence per query token)")
+        _check(lib.fdec_plan_selected(lens.ctypes.data, lens.shape[0], page_size, num_qo_heads, num_kv_heads, head_dim, dt,
+                                      ctypes.byref(opts), ctypes.byref(handle), ctypes.byref(ws)))
+    else:
+        _check(lib.fdec_plan(lens.ctypes.data, lens.shape[0], q_len, page_size, num_qo_heads, num_kv_heads,
+                             head_dim, dt, int(bool(causal)), ctypes.byref(opts), ctypes.byref(handle),
+                             ctypes.byref(ws)))
     meta = dict(q_len=q_len, page_size=page_size, num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads,
                 head_dim=head_dim, dtype=dtype, causal=causal, capacity=lens.copy(), kv_dtype=kv_dtype)
     return Plan(handle.value, ws.value, lens.shape[0], meta)
@@ -242,6 +259,13 @@ def fdec_plan_get_info(plan: Plan) -> dict:
     info = PlanInfo()
     _check(_load().fdec_plan_get_info(plan.handle, ctypes.byref(info)))
     return info.as_dict()
+
+
+def fdec_plan_get_selected_info(plan: Plan) -> dict:
+    """What fdec_run_selected does with the plan: page_lists, share_ctas, blocks_per_split, launches."""
+    info = SelectedInfo()
+    _check(_load().fdec_plan_get_selected_info(plan.handle, ctypes.byref(info)))
+    return {name: getattr(info, name) for name, _ in SelectedInfo._fields_}
 
 
 def fdec_plan_get_splits(plan: Plan) -> np.ndarray:
@@ -540,14 +564,19 @@ class PageSelect:
 
 
 class PagedDecode:
-    """Convenience holder: a plan, its torch-allocated workspace, uploaded once."""
+    """Convenience holder: a plan, its torch-allocated workspace, uploaded once.
+
+    page_lists: whether the plan is also one for run_selected, which takes more workspace (see
+    fdec_plan_selected); None: wherever run_selected can be called."""
 
     def __init__(self, capacities, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, dtype="bf16",
-                 causal=False, device=None, stream=None, **opts):
+                 causal=False, device=None, stream=None, page_lists=None, **opts):
         import torch
 
+        if page_lists is None:
+            page_lists = q_len == 1 and opts.get("kv_dtype", "") != "q8_0"
         self.plan = fdec_plan(capacities, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,
-                              causal, **opts)
+                              causal, page_lists=page_lists, **opts)
         self.workspace = torch.empty(max(self.plan.workspace_bytes, 256), dtype=torch.uint8,
                                      device=device or "cuda")
         fdec_plan_upload(self.plan, self.workspace, stream)

@@ -163,6 +163,7 @@ struct fdec_plan_s {
     int path = FDEC_PATH_SIMT;
     bool persistent = false;  // MMA path over 16-bit caches: resident CTAs take work units
     int n_units = 0, persist_grid = 0, selected_grid = 0;  // the latter for fdec_run_selected
+    bool page_lists = false;  // planned by fdec_plan_selected
     // Shares of fdec_run_selected (SelectedParams::shares): their grid (0: planned items) and
     // regions, behind the rest of the workspace (base_ws_bytes), which is all that the
     // other entry points use.
@@ -393,9 +394,10 @@ const char* fdec_last_error(void) { return g_last_error.c_str(); }
 
 const char* fdec_version(void) { return "fdec 0.1.0 (sm_103a)"; }
 
-fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int page_size, int num_qo_heads,
-                      int num_kv_heads, int head_dim, fdec_dtype dtype, int causal, const fdec_plan_opts* opts,
-                      fdec_plan_t* out_plan, size_t* workspace_bytes) {
+// page_lists: with the regions and splits of fdec_run_selected.
+static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len, int page_size, int num_qo_heads,
+                             int num_kv_heads, int head_dim, fdec_dtype dtype, int causal, const fdec_plan_opts* opts,
+                             bool page_lists, fdec_plan_t* out_plan, size_t* workspace_bytes) {
     g_last_error.clear();
     if (out_plan == nullptr || workspace_bytes == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null output pointer");
     *out_plan = nullptr;
@@ -638,7 +640,8 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
     const double saved = static_cast<double>(rounds) * std::min(C, max_blocks) - mean;
     const bool split = C < max_blocks;
     const double cost = split ? 0.1 : 2.5 + 300.0 / head_dim + mean / 16;
-    if (p->persistent && q_len == 1 && lists <= 4096 && (!split || lists >= 16) && saved > cost) {
+    p->page_lists = page_lists;
+    if (page_lists && p->persistent && lists <= 4096 && (!split || lists >= 16) && saved > cost) {
         p->share_grid = static_cast<int>(std::min<long long>(blocks, selected_slots));
         p->share_cap = std::all_of(p->capacity.begin(), p->capacity.end(), [&](int32_t c) { return c == p->capacity[0]; })
                            ? p->capacity[0]
@@ -650,7 +653,7 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
         p->off_share_ml = off;
         off = align_up(off + sizeof(float2) * 2 * p->share_grid * kMmaRows);
     }
-    if (kv8 && !q8 && q_len == 1 && o.blocks_per_split == 0) {
+    if (page_lists && kv8 && o.blocks_per_split == 0) {
         // Splits of equal length, as many a list as the resident CTAs hold (one more where
         // that leaves under a third of a list out): lists of unknown lengths gain nothing from
         // the odd splits that the planner balances, and a code cache's CTA starts for more than
@@ -672,8 +675,8 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
             so.blocks_per_split = bps;
             so.num_sms = num_sms;
             size_t bytes = 0;
-            const fdec_status st = fdec_plan(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads,
-                                             head_dim, dtype, causal, &so, &p->selected, &bytes);
+            const fdec_status st = plan_impl(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads,
+                                             head_dim, dtype, causal, &so, false, &p->selected, &bytes);
             if (st != FDEC_OK) {
                 delete p;
                 return st;
@@ -696,6 +699,26 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
     return FDEC_OK;
 }
 
+fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int page_size, int num_qo_heads,
+                      int num_kv_heads, int head_dim, fdec_dtype dtype, int causal, const fdec_plan_opts* opts,
+                      fdec_plan_t* out_plan, size_t* workspace_bytes) {
+    return plan_impl(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, causal, opts,
+                     false, out_plan, workspace_bytes);
+}
+
+fdec_status fdec_plan_selected(const int32_t* seq_lens_host, int batch, int page_size, int num_qo_heads,
+                               int num_kv_heads, int head_dim, fdec_dtype dtype, const fdec_plan_opts* opts,
+                               fdec_plan_t* out_plan, size_t* workspace_bytes) {
+    g_last_error.clear();
+    if (opts != nullptr && opts->kv_dtype == FDEC_KV_Q8_0) {
+        if (out_plan != nullptr) *out_plan = nullptr;
+        if (workspace_bytes != nullptr) *workspace_bytes = 0;
+        return fail(FDEC_ERR_UNSUPPORTED, "fdec_run_selected reads 16-bit and E4M3 caches, not q8_0");
+    }
+    return plan_impl(seq_lens_host, batch, 1, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, 0, opts, true,
+                     out_plan, workspace_bytes);
+}
+
 fdec_status fdec_plan_destroy(fdec_plan_t plan) {
     delete plan;
     return FDEC_OK;
@@ -715,6 +738,17 @@ fdec_status fdec_plan_get_info(fdec_plan_t p, fdec_plan_info* info) {
     info->launches = 1 + static_cast<int>(p->passes.size());
     info->num_sms = p->num_sms;
     info->workspace_bytes = p->ws_bytes;
+    return FDEC_OK;
+}
+
+fdec_status fdec_plan_get_selected_info(fdec_plan_t p, fdec_selected_info* info) {
+    if (p == nullptr || info == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null argument");
+    const fdec_plan_s* run = p->selected != nullptr ? p->selected : p;
+    std::memset(info, 0, sizeof(*info));
+    info->page_lists = p->page_lists ? 1 : 0;
+    info->share_ctas = run->share_grid;
+    info->blocks_per_split = run->blocks_per_split;
+    info->launches = run->share_grid > 0 ? 2 : 1 + static_cast<int>(run->passes.size());
     return FDEC_OK;
 }
 

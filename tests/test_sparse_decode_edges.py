@@ -11,8 +11,8 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from tests.test_sparse_decode import (DT, attend_reference, bounds_like, cpu_rows, gpu, i32, make_pool, select_reference,
-                                       selected_lists)
+from tests.test_sparse_decode import (DT, assert_attention, attend_reference, bounds_like, cpu_rows, gpu, i32, make_pool,
+                                       select_reference, selected_lists)
 
 
 # ------------------------------------------------------------------------------------------- attention over codes
@@ -216,3 +216,46 @@ def test_a_workspace_of_repeated_bytes_is_refused():
     with pytest.raises(ValueError, match="contiguous"):
         fd.fdec_select_pages(torch.zeros(1, 1, 4, 64, dtype=torch.float16), torch.zeros(4, 2, 2, 64, dtype=torch.float16),
                              i(1, 8), i(1), 16, 8, 4, i(1, 2, 4), i(1, 2), None, buf[at:at + 1].expand(total), stream=0)
+
+
+# ------------------------------------------------------------------------------------ plans with and without page lists
+
+def test_plans_without_page_lists_have_no_workspace_for_them():
+    """The workspace of fdec_plan is that of its splits: (capacities, page, Hq, Hk, D, cache) and bytes at 152 SMs."""
+    for caps, page, hq, hk, d, kv, want in (
+            ([2048] * 64, 64, 32, 8, 512, "", 8424960), ([32768] * 64, 64, 32, 8, 128, "", 5331456),
+            ([262144], 64, 32, 4, 128, "", 1266688), ([700] * 5, 16, 4, 1, 64, "", 59904),
+            ([2048] * 16, 16, 32, 8, 128, "fp8", 1066752), ([4096] * 16, 64, 16, 4, 256, "fp8", 1323008)):
+        plan = fd.fdec_plan(caps, 1, page, hq, hk, d, num_sms=152, kv_dtype=kv)
+        info = fd.fdec_plan_get_selected_info(plan)
+        assert plan.workspace_bytes == want and not info["page_lists"] and not info["share_ctas"]
+        # all that the other entry points see of a plan for page lists is the same
+        lists = fd.fdec_plan(caps, 1, page, hq, hk, d, num_sms=152, kv_dtype=kv, page_lists=True)
+        a, b = fd.fdec_plan_get_info(plan), fd.fdec_plan_get_info(lists)
+        more = b.pop("workspace_bytes") - a.pop("workspace_bytes")
+        assert a == b and np.array_equal(fd.fdec_plan_get_splits(plan), fd.fdec_plan_get_splits(lists))
+        assert fd.fdec_plan_get_selected_info(lists)["page_lists"] == 1 and 0 <= more < 11 << 20
+    info = fd.fdec_plan_get_selected_info(fd.fdec_plan([2048] * 64, 1, 16, 32, 8, 128, num_sms=152, page_lists=True))
+    assert info["page_lists"] == 1 and info["share_ctas"] == 304 and info["launches"] == 2
+    with pytest.raises(ValueError):
+        fd.fdec_plan([64], 2, 16, 4, 2, 64, num_sms=152, page_lists=True)
+    with pytest.raises(fd.FdecError) as e:
+        fd.fdec_plan([64], 1, 16, 4, 2, 128, num_sms=152, page_lists=True, kv_dtype="q8_0")
+    assert e.value.status_name == "FDEC_ERR_UNSUPPORTED"
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["", "fp8"])
+def test_run_selected_with_either_kind_of_plan(kv):
+    rows, hq, hk, d, page, budget = 24, 16, 4, 128, 16, 60
+    k, v = make_pool(2 * budget, hk, page, d, kv or "bf16", "hnd", 3)
+    ids, counts = selected_lists(rows, hk, page, budget, 2 * budget, seed=2)
+    q = torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    ref = attend_reference(q, k.float() * 0.125, v.float() * 0.25, ids, counts, 1 / math.sqrt(d))
+    for page_lists in (True, False, None):
+        pd = fd.PagedDecode([budget * page] * rows, 1, page, hq, hk, d, "bf16", kv_dtype=kv, page_lists=page_lists)
+        assert fd.fdec_plan_get_selected_info(pd.plan)["page_lists"] == (page_lists is not False)
+        out, lse = torch.empty(rows, 1, hq, d, device="cuda"), torch.empty(rows, 1, hq, device="cuda")
+        pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse, k_scale=0.125, v_scale=0.25)
+        assert pd.device_errors() == 0
+        assert_attention(out, lse, *ref)
