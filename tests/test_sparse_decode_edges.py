@@ -259,3 +259,74 @@ def test_run_selected_with_either_kind_of_plan(kv):
         pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse, k_scale=0.125, v_scale=0.25)
         assert pd.device_errors() == 0
         assert_attention(out, lse, *ref)
+
+
+# ------------------------------------------------------------------------------------------------- shares of lists
+
+@gpu
+@pytest.mark.parametrize("d,hq,hk,page,rows,caps", [
+    (128, 32, 8, 16, 40, (2048, 64, 640, 1)), (64, 4, 4, 64, 64, (640, 1280)), (192, 8, 4, 8, 33, (1280, 320, 0)),
+    (256, 16, 4, 32, 12, (960, 128)), (512, 8, 4, 32, 12, (640, 128)), (128, 40, 2, 16, 30, (2048, 100, 300))])
+def test_run_selected_over_lists_of_unequal_capacities(d, hq, hk, page, rows, caps):
+    """Shares of lists whose capacities differ (each is read on the device), ragged, full and empty, the same in every
+    run whatever ran before."""
+    cap = [caps[r % len(caps)] for r in range(rows)]
+    width = max(1, -(-max(cap) // page))
+    pool = 2 * width + 3
+    k, v = make_pool(pool, hk, page, d, "bf16", "nhd", seed=d)
+    q = torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(rows)).bfloat16().cuda()
+    pd = fd.PagedDecode(cap, 1, page, hq, hk, d, "bf16", path=fd.FDEC_PATH_MMA)
+    assert fd.fdec_plan_get_selected_info(pd.plan)["share_ctas"] > 0
+    results = []
+    for kind in ("ragged", "full", "empty", "ragged"):
+        rng = np.random.default_rng(d)
+        ids = rng.integers(0, pool, (rows, hk, width)).astype(np.int32)
+        full = np.repeat(np.asarray(cap)[:, None], hk, 1)
+        counts = {"full": full, "empty": 0 * full}.get(kind, rng.integers(0, full + 1)).astype(np.int32)
+        out, lse = torch.full((rows, 1, hq, d), math.nan, device="cuda"), torch.full((rows, 1, hq), math.nan, device="cuda")
+        pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse)
+        assert pd.device_errors() == 0
+        assert_attention(out, lse, *attend_reference(q, k, v, ids, counts, 1 / math.sqrt(d)))
+        results.append((out, lse))
+    assert torch.equal(results[0][0], results[3][0]) and torch.equal(results[0][1], results[3][1])
+    # counts above one list's capacity are clamped to it, and flagged
+    over = np.asarray(counts)
+    over[0] = cap[0] + 1
+    pd.run_selected(q, k, v, i32(ids), i32(over), out, lse)
+    assert pd.device_errors() == fd.DEVERR_SEQ_LEN
+    over[0] = cap[0]
+    assert_attention(out, lse, *attend_reference(q, k, v, ids, over, 1 / math.sqrt(d)))
+
+
+@gpu
+def test_run_selected_of_more_lists_than_shares_count():
+    """4096 lists run in shares, 4100 as planned (every fourth token's lists longer than the others')."""
+    d, page, width = 64, 64, 10
+    k, v = make_pool(40, 4, page, d, "f16", "hnd", seed=1)
+    for rows in (1024, 1025):
+        ids, counts = selected_lists(rows, 4, page, width, 40, seed=rows)
+        cap = np.asarray([page if r % 4 else width * page for r in range(rows)], dtype=np.int32)
+        counts = np.minimum(counts, cap[:, None])
+        q = torch.randn(rows, 1, 4, d, generator=torch.Generator().manual_seed(rows)).half().cuda()
+        pd = fd.PagedDecode(cap, 1, page, 4, 4, d, "f16")
+        assert (fd.fdec_plan_get_selected_info(pd.plan)["share_ctas"] > 0) == (rows == 1024)
+        out, lse = torch.full((rows, 1, 4, d), math.nan, device="cuda"), torch.full((rows, 1, 4), math.nan, device="cuda")
+        pd.run_selected(q, k, v, i32(ids), i32(counts), out, lse)
+        assert pd.device_errors() == 0
+        assert_attention(out, lse, *attend_reference(q, k, v, ids, counts, 1 / math.sqrt(d)))
+
+
+@gpu
+def test_run_selected_as_planned_equals_run_bit_for_bit():
+    """Planned splits of one block: the partials and the reduction are fdec_run's."""
+    rows, hq, hk, d, page, budget = 3, 32, 2, 128, 16, 20
+    k, v = make_pool(80, hk, page, d, "bf16", "hnd", 4)
+    ids, counts = selected_lists(rows, 1, page, budget, 80, seed=4)
+    q = torch.randn(rows, 1, hq, d, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    pd = fd.PagedDecode([budget * page] * rows, 1, page, hq, hk, d, "bf16", path=fd.FDEC_PATH_MMA, blocks_per_split=1)
+    assert fd.fdec_plan_get_selected_info(pd.plan)["share_ctas"] == 0
+    a, b = (torch.full((rows, 1, hq, d), math.nan, device="cuda") for _ in range(2))
+    la, lb = (torch.full((rows, 1, hq), math.nan, device="cuda") for _ in range(2))
+    pd.run(q, k, v, i32(ids[:, 0]), i32(counts[:, 0]), a, la)
+    pd.run_selected(q, k, v, i32(ids.repeat(hk, 1)), i32(counts.repeat(hk, 1)), b, lb)
+    assert pd.device_errors() == 0 and torch.equal(a, b) and torch.equal(la, lb)
