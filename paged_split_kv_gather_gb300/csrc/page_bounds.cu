@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) page_bounds_kernel(const __
                 const int r = min(r0 + u * WPU * RPW + sub, n - 1);
 #pragma unroll
                 for (int c = 0; c < CPL; ++c)
-                    raw[u][c] = __ldg(reinterpret_cast<const uint4*>(rows + r * p.k_st + 16 * (l + LPR * c)));
+                    raw[u][c] = *reinterpret_cast<const uint4*>(rows + r * p.k_st + 16 * (l + LPR * c));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)

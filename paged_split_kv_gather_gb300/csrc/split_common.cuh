@@ -67,6 +67,18 @@ struct ItemRange {
 template <typename P>
 constexpr bool kSelected = std::is_base_of_v<SelectedParams, P>;
 
+// Loads of a call's inputs.  Page lists and their counts come from the kernel just before,
+// beside which this one may be resident, so for SelectedParams they are not read-only loads
+// (__ldg: of data that nobody writes during the kernel) but ordinary ones, which stay
+// behind the kernel's wait.
+template <typename P, typename T>
+__device__ __forceinline__ T load_input(const T* p) {
+    if constexpr (kSelected<P>)
+        return *p;
+    else
+        return __ldg(p);
+}
+
 // Page-table and length row of a sequence for one KV head.
 template <typename P>
 __device__ __forceinline__ int64_t table_row(const P& p, int seq, int kvh) {
@@ -106,7 +118,8 @@ struct QChunks {
     static constexpr int PER = (CH + NTHREADS - 1) / NTHREADS;
     uint4 v[PER];
 
-    __device__ __forceinline__ void load(const SplitParams& p, int b, int kvh, int row0, int tid) {
+    template <typename P>
+    __device__ __forceinline__ void load(const P& p, int b, int kvh, int row0, int tid) {
         const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | static_cast<uintptr_t>(p.q_stride_tok * 2) |
                            static_cast<uintptr_t>(p.q_stride_head * 2)) & 15u) == 0;
 #pragma unroll
@@ -121,13 +134,13 @@ struct QChunks {
                 const uint16_t* src = p.q + static_cast<int64_t>(b * p.q_len + qi) * p.q_stride_tok +
                                       static_cast<int64_t>(h) * p.q_stride_head + (idx - r * (D / 8)) * 8;
                 if (vec) {
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(src));
+                    v[i] = load_input<P>(reinterpret_cast<const uint4*>(src));
                 } else {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w[e] = static_cast<uint32_t>(__ldg(src + 2 * e)) |
-                               (static_cast<uint32_t>(__ldg(src + 2 * e + 1)) << 16);
+                        w[e] = static_cast<uint32_t>(load_input<P>(src + 2 * e)) |
+                               (static_cast<uint32_t>(load_input<P>(src + 2 * e + 1)) << 16);
                     v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
@@ -207,7 +220,7 @@ __device__ __forceinline__ void produce_stages(const P& p, const CUtensorMap* tm
         const int NB = TOK / BR;
         auto box_page = [&](int n) -> int {
             const int t = tok_begin + n * BR;
-            return (t < ir.tok_end_alloc && (t >> p.page_shift) < p.pt_stride) ? __ldg(pt + (t >> p.page_shift)) : -1;
+            return (t < ir.tok_end_alloc && (t >> p.page_shift) < p.pt_stride) ? load_input<P>(pt + (t >> p.page_shift)) : -1;
         };
         int pid = box_page(lane);
         int pid_next = box_page(32 + lane);
@@ -282,7 +295,7 @@ __device__ __forceinline__ void produce_stages(const P& p, const CUtensorMap* tm
             for (int rb = 0; rb < TOK; rb += 32) {  // 32 rows at a time: lane = row for the page lookup
                 const int t_lane = tok_begin + i * TOK + rb + lane;
                 const bool in_range = t_lane < tok_end;
-                const int my_page = in_range ? __ldg(pt + (t_lane >> p.page_shift)) : -1;
+                const int my_page = in_range ? load_input<P>(pt + (t_lane >> p.page_shift)) : -1;
                 const bool valid = in_range && my_page >= 0 && my_page < p.k_pages && my_page < p.v_pages;
                 if (in_range && !valid) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
                 for (int idx = lane; idx < 32 * CHUNKS; idx += 32) {

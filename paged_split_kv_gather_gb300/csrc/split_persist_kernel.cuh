@@ -180,7 +180,7 @@ template <typename P>
 __device__ __forceinline__ int punit_box_page(const P& p, const PUnit& u, int n, int BR) {
     const int t = u.it.y * kBlockTokens + n * BR;
     const int32_t* pt = p.page_table + punit_row(p, u) * p.pt_stride;
-    return (t < u.it.z * kBlockTokens && (t >> p.page_shift) < p.pt_stride) ? __ldg(pt + (t >> p.page_shift)) : -1;
+    return (t < u.it.z * kBlockTokens && (t >> p.page_shift) < p.pt_stride) ? load_input<P>(pt + (t >> p.page_shift)) : -1;
 }
 
 // What a unit costs besides its blocks (its queries, its padding stages, its merge, the
@@ -235,7 +235,7 @@ __device__ __forceinline__ void share_first(const SelectedParams& p, PUnit& u, S
     const int x0 = lane * seg, x1 = min(x0 + seg, p.n_lists);
     int64_t mine = 0;
 #pragma unroll 16
-    for (int x = x0; x < x1; ++x) mine += blocks_of(__ldg(p.seq_lens + x), list_cap(p, x)) + kUnitCost;
+    for (int x = x0; x < x1; ++x) mine += blocks_of(p.seq_lens[x], list_cap(p, x)) + kUnitCost;
     mine *= rgc;
     int64_t upto = mine;
 #pragma unroll
@@ -254,7 +254,7 @@ __device__ __forceinline__ void share_first(const SelectedParams& p, PUnit& u, S
     const int owner_end = min(owner * seg + seg, p.n_lists);
     for (int x = owner * seg; x < owner_end; x += 32) {  // the owner's lists, 32 at a time
         const bool in = x + lane < owner_end;
-        const int L = in ? __ldg(p.seq_lens + x + lane) : 0;
+        const int L = in ? p.seq_lens[x + lane] : 0;
         const int cap = in ? list_cap(p, x + lane) : 0;
         const int weight = in ? (blocks_of(L, cap) + kUnitCost) : 0;
         int64_t sum = static_cast<int64_t>(weight) * rgc;
@@ -287,7 +287,7 @@ template <typename P>
 __device__ __forceinline__ void punit_load_lens_pages(const P& p, PUnit& u, int lane, int BR,
                                                       bool tma_mode) {
     if (!in_shares(p)) {  // (a share's unit has them: its item follows from its length)
-        u.L0 = __ldg(p.seq_lens + punit_row(p, u));
+        u.L0 = load_input<P>(p.seq_lens + punit_row(p, u));
         u.cap = p.seq1_bps > 0 ? p.seq1_capacity : __ldg(p.capacity + u.it.x);
     }
     if (tma_mode) {
@@ -348,7 +348,7 @@ __device__ __forceinline__ void produce_units(const P& p, const CUtensorMap* tmk
                     const int64_t next = sh.start + blocks_of(cur.L0, cur.cap) + kUnitCost;
                     if (next + kUnitCost < sh.end) {  // at least its first block
                         nxt.unit = cur.unit + 1;
-                        nxt.L0 = __ldg(p.seq_lens + nxt.unit / rgc);
+                        nxt.L0 = p.seq_lens[nxt.unit / rgc];
                         nxt.cap = list_cap(p, nxt.unit / rgc);
                         ahead = 1;
                     } else {
@@ -527,7 +527,7 @@ __device__ __forceinline__ void produce_units(const P& p, const CUtensorMap* tmk
                 const int32_t* pt = p.page_table + table_row(p, seq, kvh) * p.pt_stride;
                 const int t_lane = tok_begin + j * TOK + lane;
                 const bool in_range = t_lane < tok_end;
-                const int my_page = in_range ? __ldg(pt + (t_lane >> p.page_shift)) : -1;
+                const int my_page = in_range ? load_input<P>(pt + (t_lane >> p.page_shift)) : -1;
                 const bool valid = in_range && my_page >= 0 && my_page < p.k_pages && my_page < p.v_pages;
                 if (in_range && !valid) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
                 for (int idx = lane; idx < 32 * CHUNKS; idx += 32) {

@@ -139,6 +139,17 @@ def test_dependent_kernels_wait_on_every_way_out():
             "reduce_kernel", "split_mma_kernel", "split_mma_persist_kernel"} <= set(seen), seen
 
 
+def test_dependent_kernels_read_fresh_data_with_ordinary_loads():
+    """Read-only loads are for data that nobody writes while the kernel is resident; a dependent kernel is resident
+    beside the one that writes its inputs."""
+    root = os.path.join(os.path.dirname(fd.__file__), "csrc")
+    for name in ("norm_rope.cu", "page_bounds.cu", "select_pages.cu"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(root, name)).read())
+        assert "__ldg" not in text and ".nc." not in text, name
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(root, "split_persist_kernel.cuh")).read())
+    assert not re.search(r"__ldg\([^;]*(seq_lens|pt \+|page_table)", text)
+
+
 @gpu
 def test_select_pages_of_short_rows_keeps_stream_order():
     """Inputs overwritten right after a selection in which every row is short (the scoring has nothing to do), and
