@@ -404,6 +404,10 @@ fdec_status fdec_select_pages_workspace(int batch, int q_len, int num_kv_heads, 
  * (the largest logit that a key within the page's bounds can have), budget in all;
  * equal scores go to the lower index, and a NaN score counts as infinite.  The order
  * is that of the scores summed in 64 bits.  All pages, when there are at most budget.
+ * The score is computed as sum_d [max_d sum_h max(q_d, 0) + min_d sum_h min(q_d, 0)], the
+ * same for finite bounds; with an infinite one, 0 x infinity is NaN, and the page is taken.
+ * More than 256 pages whose scores lie within fp32 rounding of the border (pages of equal
+ * bounds that are not zero) cost about 0.2 us each, where a page costs 2 ns otherwise.
  *   q: as for fdec_run (any alignment); bounds: as written by fdec_page_bounds.
  *   max_pages: the most pages that a sequence has (at most page_table_stride); a length
  *      above max_pages * page_size or below 0 sets FDEC_DEVERR_SEQ_LEN and is clamped.

@@ -16,7 +16,12 @@
 // fp32 scores come with a bound E on their error (below), the K-th largest score T of
 // the row puts every page above T + 2E in and every page below T - 2E out, and where
 // more pages lie between than are still wanted, those few are summed again in 64 bits.
-// (64 bits throughout would be bound by the fp64 units: 1/60 of the fp32 rate.)
+// (64 bits throughout would be bound by the fp64 units: 1/60 of the fp32 rate.)  E is of the
+// finite terms: infinite and NaN ones decide a score exactly.  Where one hides the bound of
+// a chunk, the choosing CTA reads that chunk once more (4096 pages, one of them with a NaN:
+// 40 us; of 16384 56); where scores are exact, as with weights of 0 or pages of zeros, ties are
+// found by index (13 us, 30 us).  Only many pages of equal or nearly equal nonzero scores
+// around the border are all scored in 64 bits, by their row's CTA: 0.2 us a page.
 //
 // Two launches.  score_pages_kernel streams the bounds: a row (query token, KV head) is
 // cut into chunks of pages, one CTA each.  choose_pages_kernel, its programmatic
@@ -105,6 +110,14 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// The magnitudes of two 16-bit elements, 0 where they are not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_u16x2(uint32_t w) {
+    constexpr uint32_t INF = BF16 ? 0x7f80u : 0x7c00u;
+    const uint32_t m = w & 0x7fff7fffu;
+    return ((m & 0xffffu) < INF ? m & 0xffffu : 0u) | ((m >> 16) < INF ? m & 0xffff0000u : 0u);
+}
+
 __device__ __forceinline__ float not_nan(float s) { return s != s ? INFINITY : s; }
 __device__ __forceinline__ double not_nan(double s) { return s != s ? static_cast<double>(INFINITY) : s; }
 
@@ -119,22 +132,6 @@ __device__ __forceinline__ float from_ordered(uint32_t k) {
 __device__ __forceinline__ unsigned long long ordered(double s) {
     const unsigned long long b = __double_as_longlong(s + 0.0);  // -0 as 0
     return (b >> 63) ? ~b : b | (1ull << 63);
-}
-
-// Sums of two values over a CTA of NW warps, left in every thread's arguments.
-template <int NW>
-__device__ __forceinline__ void block_sum2(int& a, int& b, int* s_a, int* s_b) {
-    a = __reduce_add_sync(0xffffffffu, a);
-    b = __reduce_add_sync(0xffffffffu, b);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        s_a[threadIdx.x >> 5] = a;
-        s_b[threadIdx.x >> 5] = b;
-    }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    a = __reduce_add_sync(0xffffffffu, lane < NW ? s_a[lane] : 0);
-    b = __reduce_add_sync(0xffffffffu, lane < NW ? s_b[lane] : 0);
 }
 
 // What both kernels derive from a row's length.
@@ -210,6 +207,66 @@ __device__ __forceinline__ double score64(const SelectParams& p, const double* w
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
+}
+
+// An upper bound, for one of nw warps, of the finite terms' sums of magnitudes: of the chunks
+// where infinite or NaN terms hid it (this warp's pages are read once more), and of the others.
+// Such terms make their page's score infinite or NaN however it is summed; only the finite
+// ones' sums have an error to bound.
+// (Finding it while scoring was measured first: a select and an addition more for every word
+// cost each call 1-3 %, a second pass in the scoring kernel's registers its spills.)
+template <bool BF16>
+__device__ __noinline__ float finite_magnitudes(const SelectParams& p, const double* w64, const float* chunk_abs,
+                                                const int32_t* table, int h, int n_cand, int nw) {
+    constexpr int U = 2;  // pages in flight: few registers, which the kernel pays in every call
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_row = p.head_dim / 8;
+    float sum = 0.f, others = 0.f;
+#pragma unroll 1
+    for (int x = lane; x < 2 * per_row; x += 32) {  // this lane's 16-byte chunks of the two rows
+        const int side = x >= per_row ? 1 : 0;
+        const uint8_t* rows = p.b_base + h * p.b_sh + side * p.b_st + (x - side * per_row) * 16;
+        uint32_t top[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int begin = 0; begin < n_cand; begin += p.chunk) {
+            const float known = ld_cg(chunk_abs + begin / p.chunk);
+            if (known < INFINITY) {
+                others = fmaxf(others, known);
+                continue;
+            }
+            const int end = min(begin + p.chunk, n_cand);
+#pragma unroll 1
+            for (int i = begin + warp; i < end; i += nw * U) {
+                uint4 raw[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int id = i + u * nw < end ? table[p.first + i + u * nw] : -1;
+                    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (id >= 0 && id < p.b_pages) raw[u] = *reinterpret_cast<const uint4*>(rows + id * p.b_sp);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    top[0] = max_u16x2(top[0], finite_u16x2<BF16>(raw[u].x));
+                    top[1] = max_u16x2(top[1], finite_u16x2<BF16>(raw[u].y));
+                    top[2] = max_u16x2(top[2], finite_u16x2<BF16>(raw[u].z));
+                    top[3] = max_u16x2(top[3], finite_u16x2<BF16>(raw[u].w));
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 t = unpack2<BF16>(top[k]);
+            const float wx = fabsf(__double2float_rn(w64[8 * x + 2 * k]));
+            const float wy = fabsf(__double2float_rn(w64[8 * x + 2 * k + 1]));
+            if (wx < INFINITY) sum += t.x * wx;
+            if (wy < INFINITY) sum += t.y * wy;
+        }
+    }
+    __syncwarp();
+    others = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(others)));  // (not negative)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return fmaxf(fmaxf(sum, others), 1.2e-38f);
 }
 
 // QB: query tokens of a sequence that one CTA scores against the pages it reads, 1, 2 or 4
@@ -380,7 +437,11 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
         if (l % LPU == 0 && i < end_all && out_mine && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
     }
     // A page's sum of magnitudes is at most the sum of each element's largest times its
-    // weight (NaN and infinity carry through).
+    // weight (NaN and infinity carry through); 0 only where all elements are.
+    uint32_t any = 0u;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) any |= top[c][0] | top[c][1] | top[c][2] | top[c][3];
+    const float least = any != 0u ? 1.2e-38f : 0.f;
 #pragma unroll
     for (int y = 0; y < QB; ++y) {
         float abs_max = 0.f;
@@ -395,6 +456,7 @@ score_pages_kernel(const __grid_constant__ SelectParams p) {
                 abs_max += t.y * fabsf(w[2 * k + 1]);
             }
         }
+        abs_max = max_nan(abs_max, least);
 #pragma unroll
         for (int o = LPP / 2; o > 0; o >>= 1) abs_max += __shfl_xor_sync(0xffffffffu, abs_max, o);
 #pragma unroll
@@ -422,14 +484,16 @@ struct ChooseShared {
     uint32_t near_k32[kNear];
     int near_idx[kNear];
     float abs_max[NW];
-    int sum[NW], sum2[NW], sum_hi[NW], sum_taken[NW];  // one use each: no barrier between uses
+    int sum[NW], sum_hi[NW], sum_taken[NW];  // one use each: no barrier between uses
     uint32_t kmin[NW], kmax[NW], cut32;
     int bin, above, near_n, cut_idx;
     unsigned long long cut_key;
 };
 
+// (The bounds on CTAs an SM: the registers without finite_magnitudes, which is rarely called;
+// with 64 instead of 48 at 8 warps a batch of 64 x 8 rows took 43 us instead of 40.)
 template <bool BF16, int NW>
-__global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(NW * 32, NW == 8 ? 5 : NW == 16 ? 2 : 1) choose_pages_kernel(const __grid_constant__ SelectParams p) {
     constexpr int NT = NW * 32;
     static_assert(NT >= kBins && NT >= kNear && NW <= 32, "one bin, one near key a thread");
     constexpr int kTile = ChooseShared<NW>::TILE;
@@ -547,11 +611,31 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
     k_max = __reduce_max_sync(0xffffffffu, lane < NW ? sm.kmax[lane] : 0u);
     // Error of an fp32 score: the weights (group - 1 additions of one sign), a chain of
     // 4 CPL products in each of two sums, 1 + log2(LPP) additions (at most 16 and 6); in
-    // units of 2^-24 of the sum of magnitudes, with room for the rounding of that sum.
+    // units of 2^-24 of the sum of magnitudes, with room for the rounding of that sum (and
+    // 1e-37 for products below the normal range).  0 where every finite term is.
     sum_abs = lane < NW ? sm.abs_max[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum_abs = max_nan(sum_abs, __shfl_xor_sync(0xffffffffu, sum_abs, o));
-    const float E = sum_abs * ((p.group + p.chain + 9) * 6.0e-8f) + 1e-37f;
+    // Whether f(w) holds for a weight of the row (of all threads, to all threads).
+    auto any_weight = [&](auto&& f) {
+        bool is = false;
+        for (int d = tid; d < 2 * p.head_dim; d += NT) is = is || f(sm.weight64[d]);
+        return __syncthreads_or(is) != 0;
+    };
+    if (!(sum_abs < INFINITY)) {
+        if (any_weight([](double w) { return w != w; })) {
+            sum_abs = 0.f;  // every score is NaN
+        } else if (!any_weight([](double w) { return fabs(w) > 1.7e38 && fabs(w) < static_cast<double>(INFINITY); })) {
+            // (else a weight is finite, but perhaps not in 32 bits)
+            const float mine = finite_magnitudes<BF16>(p, sm.weight64, p.chunk_abs + row * p.abs_stride, table, h, n_cand, NW);
+            if (lane == 0) sm.abs_max[warp] = mine;
+            __syncthreads();
+            sum_abs = lane < NW ? sm.abs_max[lane] : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum_abs = fmaxf(sum_abs, __shfl_xor_sync(0xffffffffu, sum_abs, o));
+        }
+    }
+    const float E = sum_abs == 0.f ? 0.f : sum_abs * ((p.group + p.chain + 9) * 6.0e-8f) + 1e-37f;
     const bool sure_E = E < INFINITY;
     const float margin = 2.5f * E;  // 2 E, and a rounding more
     unsigned long long* key64 = p.near_keys + row * p.max_pages;
@@ -560,11 +644,8 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
     // (`hi`) are taken, keys below (`lo`) are not.
     int want = need, n_near, take_near;
     uint32_t lo, hi;
-    while (true) {
-        const int shift = max(0, 24 - __clz(k_max - k_min));  // (k_max - k_min) >> shift < kBins = 256
-        each([&](uint32_t k, int) {
-            if (k >= k_min && k <= k_max) atomicAdd(&sm.hist[(k - k_min) >> shift], 1);
-        });
+    // The bin of sm.hist that the want-th largest key is in (sm.bin), and how many lie above it.
+    auto find_bin = [&]() {
         __syncthreads();
         // bins from the top, one a thread
         const int mine = tid < kBins ? sm.hist[kBins - 1 - tid] : 0;
@@ -582,9 +663,16 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
             sm.above = upto - mine;
         }
         __syncthreads();
+    };
+    while (true) {
+        const int shift = max(0, 24 - __clz(k_max - k_min));  // (k_max - k_min) >> shift < kBins = 256
+        each([&](uint32_t k, int) {
+            if (k >= k_min && k <= k_max) atomicAdd(&sm.hist[(k - k_min) >> shift], 1);
+        });
+        find_bin();
         want -= sm.above;
         k_min += static_cast<uint32_t>(sm.bin) << shift;
-        k_max = k_min + ((1u << shift) - 1u);
+        k_max -= k_max - k_min > (1u << shift) - 1u ? k_max - k_min - ((1u << shift) - 1u) : 0u;
         lo = sure_E ? ordered(from_ordered(k_min) - margin + 0.f) : 1u;
         hi = sure_E ? ordered(from_ordered(k_max) + margin + 0.f) : ~0u;
         int n_hi = 0;
@@ -651,53 +739,67 @@ __global__ void __launch_bounds__(NW * 32) choose_pages_kernel(const __grid_cons
             }
             __syncthreads();
         }
-    } else {  // many (equal pages, infinities): the 64-bit key bit by bit, then the index
-        auto sum_of = [&](int n) {
-            int none = 0;
-            block_sum2<NW>(n, none, sm.sum, sm.sum2);
-            return n;
-        };
+    } else {  // many: equal pages, queries of zeros
         auto near = [&](int i) {
             const uint32_t k = ordered(not_nan(ld_cg(scores + i)) + 0.f);
             return k >= lo && k <= hi;
         };
-        for (int i = warp; i < n_cand; i += NW) {
-            if (!near(i)) continue;
-            const unsigned long long k = score_at(i);
-            if (lane == 0) key64[i] = k;
-        }
-        __threadfence_block();
-        __syncthreads();
+        // Scores without a finite term, or of weights that are all 0, and infinite ones (the
+        // margin then reaches no other) are exact, and those near the border equal: their order
+        // is that of the indices.
+        refine = !(sure_E && (E == 0.f || !(fabsf(from_ordered(k_max)) < INFINITY) ||
+                              !any_weight([](double w) { return w != 0.0; })));
         unsigned long long cut = 0;
-        for (int bit = 63; bit >= 0; --bit) {
-            const unsigned long long t = cut | (1ull << bit);
-            int n = 0;
-            for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] >= t;
-            if (sum_of(n) >= take_near) cut = t;
+        int ties = take_near;  // of those equal to the cut: the first ones
+        if (refine) {
+            for (int i = warp; i < n_cand; i += NW) {
+                if (!near(i)) continue;
+                const unsigned long long k = score_at(i);
+                if (lane == 0) key64[i] = k;
+            }
+            __threadfence_block();
+            want = take_near;
+            for (int shift = 56; shift >= 0; shift -= 8) {  // the key's bytes from the top
+                __syncthreads();
+                if (tid < kBins) sm.hist[tid] = 0;
+                __syncthreads();
+                for (int i = tid; i < n_cand; i += NT)
+                    if (near(i) && (shift == 56 || key64[i] >> (shift + 8) == cut))
+                        atomicAdd(&sm.hist[(key64[i] >> shift) & 255], 1);
+                find_bin();
+                want -= sm.above;
+                cut = cut << 8 | static_cast<unsigned long long>(sm.bin);
+            }
+            ties = want;
         }
-        int n = 0;
-        for (int i = tid; i < n_cand; i += NT) n += near(i) && key64[i] > cut;
-        const int ties = take_near - sum_of(n);  // of those equal to the cut: the first ones
-        int low = 0, high = n_cand - 1;  // smallest index with `ties` of them at or below it
-        while (low < high) {
-            const int mid = (low + high) / 2;
-            n = 0;
-            for (int i = tid; i <= mid; i += NT) n += near(i) && key64[i] == cut;
-            if (sum_of(n) >= ties)
-                high = mid;
-            else
-                low = mid + 1;
+        // The index of the last tie taken: each thread counts those of a run of pages.
+        auto tie = [&](int i) { return near(i) && (!refine || key64[i] == cut); };
+        const int seg = (n_cand + NT - 1) / NT;
+        const int from = tid * seg, to = min(from + seg, n_cand);
+        int mine = 0;
+        for (int i = from; i < to; ++i) mine += tie(i);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        if (tid == 0) {
+        __syncthreads();
+        if (lane == 31) sm.sum[warp] = upto;
+        __syncthreads();
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? sm.sum[lane] : 0);
+        if (upto - mine < ties && ties <= upto) {
+            int n = upto - mine, i = from;
+            while (n += tie(i), n < ties) ++i;
             sm.cut_key = cut;
-            sm.cut_idx = low;
+            sm.cut_idx = i;
         }
         __syncthreads();
     }
     auto take = [&](uint32_t k, int i) {
         if (k > hi) return true;
         if (k < lo) return false;
-        if (!refine) return k >= sm.cut32;
+        if (!refine) return n_near <= kNear ? k >= sm.cut32 : i <= sm.cut_idx;
         unsigned long long k64 = 0;
         if (n_near <= kNear) {
             for (int y = 0; y < n_near; ++y)

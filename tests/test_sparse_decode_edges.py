@@ -11,8 +11,8 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from tests.test_sparse_decode import (DT, assert_attention, attend_reference, bounds_like, cpu_rows, gpu, i32, make_pool,
-                                       select_reference, selected_lists)
+from tests.test_sparse_decode import (DT, assert_attention, attend_reference, bounds_like, check_select, cpu_rows, gpu, i32,
+                                       make_pool, select_reference, selected_lists)
 
 
 # ------------------------------------------------------------------------------------------- attention over codes
@@ -341,3 +341,130 @@ def test_run_selected_as_planned_equals_run_bit_for_bit():
     pd.run(q, k, v, i32(ids[:, 0]), i32(counts[:, 0]), a, la)
     pd.run_selected(q, k, v, i32(ids.repeat(hk, 1)), i32(counts.repeat(hk, 1)), b, lb)
     assert pd.device_errors() == 0 and torch.equal(a, b) and torch.equal(la, lb)
+
+
+# --------------------------------------------------------------------------------------------------- page selection
+
+def special_bounds(kind, pages, hk, d, t, seed):
+    """Bounds of `pages` pages of which some hold what `kind` says; the pages that do."""
+    b = bounds_like(pages, hk, d, t, seed)
+    rng = np.random.default_rng(seed)
+    some = torch.as_tensor(np.sort(rng.choice(pages, max(1, pages // 2), replace=False))).cuda()
+    one = some[len(some) // 2:len(some) // 2 + 1]
+    if kind == "one nan":
+        b[one, :, 0, 3] = math.nan
+    elif kind == "one infinity":
+        b[one, :, 1, 3] = math.inf
+    elif kind == "many nan":
+        b[some, :, :, d - 1] = math.nan
+    elif kind == "many infinities":
+        b[some, :, 1] = math.inf
+        b[some, :, 0] = -math.inf
+    elif kind == "many minus infinities":  # both rows, so that every query is led to -inf or NaN
+        b[some] = -math.inf
+    elif kind == "all of them":
+        third = len(some) // 3
+        b[some[:third], :, 1, 0] = math.inf
+        b[some[third:2 * third], :, :, 1] = -math.inf
+        b[some[2 * third:], 0, 0, 2] = math.nan
+    elif kind == "zeros":
+        b[:] = 0
+    elif kind == "many zeros":
+        b[some] = 0
+    elif kind == "largest":
+        b[some, :, 1, :2] = torch.finfo(t).max
+    return b
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["one nan", "one infinity", "many nan", "many infinities", "many minus infinities",
+                                  "all of them", "zeros", "many zeros", "largest"])
+@pytest.mark.parametrize("dtype,d,hq,hk,q_len,pages", [("bf16", 128, 8, 2, 1, 1500), ("f16", 64, 4, 4, 2, 700),
+                                                       ("bf16", 192, 4, 2, 4, 900), ("f16", 512, 6, 2, 1, 640),
+                                                       ("bf16", 256, 8, 1, 3, 5000)])
+def test_select_pages_of_special_bounds(dtype, d, hq, hk, q_len, pages, kind):
+    t = DT[dtype]
+    table = np.random.default_rng(pages).permutation(2 * pages).reshape(2, pages)
+    bounds = special_bounds(kind, 2 * pages, hk, d, t, seed=pages)
+    g = torch.Generator().manual_seed(d)
+    q = torch.randn(2, q_len, hq, d, generator=g)
+    lens = [pages * 16, pages * 16 - 70]
+    for budget in (12, pages // 2 - 20, pages - 30):
+        check_select(q.to(t).cuda(), bounds, table, lens, 16, budget, 1, 2)
+    check_select(q.abs().to(t).cuda(), bounds, table, lens, 16, 40, 0, 1)  # weights of one sign: 0 x infinity is NaN
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", ["zero", "nan", "infinity", "minus infinity", "largest", "smallest"])
+def test_select_pages_of_special_queries(dtype, kind):
+    """One head (its group's scores are all NaN or infinite), one element, or every element; weights that are finite
+    in 64 bits alone."""
+    t = DT[dtype]
+    value = {"zero": 0.0, "nan": math.nan, "infinity": math.inf, "minus infinity": -math.inf,
+             "largest": torch.finfo(t).max, "smallest": torch.finfo(t).smallest_normal}[kind]
+    pages, hq, hk, d = 900, 8, 2, 128
+    table = np.random.default_rng(1).permutation(pages).reshape(1, pages)
+    q = torch.randn(1, 1, hq, d, generator=torch.Generator().manual_seed(2)).to(t)
+    element, head, every = q.clone(), q.clone(), torch.full_like(q, value)
+    element[0, 0, 1, 5] = value
+    head[0, 0, 6] = value
+    for bounds in (bounds_like(pages, hk, d, t, 3), special_bounds("all of them", pages, hk, d, t, 4),
+                   special_bounds("many zeros", pages, hk, d, t, 5)):
+        for x in (element, head, every):
+            for budget in (20, 500):
+                check_select(x.cuda(), bounds, table, [pages * 16 - 1], 16, budget, 1, 1)
+
+
+@gpu
+def test_select_pages_leaves_bad_page_ids_behind_many_nan_pages():
+    """Infinite scores of more pages than are compared each with each, and pages outside the pool, in one row."""
+    pages, budget = 2000, 700
+    bounds = bounds_like(pages, 1, 64, torch.float16, 2)
+    bounds[400:1000, :, 1, 7] = math.nan
+    q = torch.randn(1, 1, 4, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
+    table = np.arange(pages)[None]
+    bad = table.copy()
+    bad[0, [3, 555, 1500]] = [pages, -9, 1 << 30]
+    want = select_reference(q, bounds, table, [pages * 16], 16, budget + 3, 1, 1, True)[2][0, 0]
+    want = [j for j in want if j not in (3, 555, 1500)]
+    sel = fd.PageSelect(1, 1, 16, 4, 1, 64, pages, budget, "f16")
+    index = sel.run(q, bounds, i32(bad), i32([pages * 16]))[2].cpu().numpy()[0, 0]
+    assert sel.device_errors() == fd.DEVERR_PAGE_ID
+    assert not np.isin([3, 555, 1500], index).any()
+    # (of the reference's budget + 3 pages, those that are not the bad ones, without its last free ones)
+    scores = lambda j: math.inf if 400 <= j < 1000 else 0  # noqa: E731
+    assert [j for j in want if scores(j)] == [j for j in index if scores(j)] and set(index) <= set(want)
+
+
+@gpu
+def test_special_values_do_not_make_a_row_slow():
+    """One bad key in a long cache, an unwritten cache, a padded query: the call stays within a few times the ordinary
+    one (it was a hundred times).  4096 pages, four rows; the best of several replays."""
+    pages, hq, hk, d = 4096, 32, 4, 128
+    table, lens = i32(np.random.default_rng(1).permutation(pages)[None]), i32([pages * 64])
+    sel = fd.PageSelect(1, 1, 64, hq, hk, d, pages, 64, "bf16", 1, 2)
+    ordinary = torch.randn(1, 1, hq, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+
+    def best(q, bounds):
+        sel.run(q, bounds, table, lens)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                sel.run(q, bounds, table, lens)
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            graph.replay()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    usual = best(ordinary, bounds_like(pages, hk, d, torch.bfloat16, 3))
+    for kind in ("one nan", "one infinity", "zeros"):
+        assert best(ordinary, special_bounds(kind, pages, hk, d, torch.bfloat16, 3)) < 10 * usual, kind
+    for value in (0.0, math.nan):
+        assert best(torch.full_like(ordinary, value), bounds_like(pages, hk, d, torch.bfloat16, 3)) < 10 * usual, value
