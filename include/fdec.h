@@ -192,7 +192,7 @@ fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int pa
  * of 16 x head_dim floats for every resident CTA (5 to 10 MB at 152 SMs); for E4M3 caches the
  * lists' own splits.  Everything else that takes a plan takes this one too.
  * fdec_run_selected also runs plans of fdec_plan, with their splits: the lists then cost
- * what the longest would (64 x 8 ragged lists of up to 2048 tokens 82 us instead of 62).
+ * what the longest would (64 x 8 ragged lists of up to 2048 tokens 80 us instead of 62).
  */
 fdec_status fdec_plan_selected(const int32_t* seq_lens_host, int batch, int page_size, int num_qo_heads,
                                int num_kv_heads, int head_dim, fdec_dtype dtype, const fdec_plan_opts* opts,

@@ -628,7 +628,7 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
     // 18.1 at 192, 39 / 42 at 512).  Measured over 517 shapes (4 to 1600 lists of 128 to 2048
     // tokens, every head_dim, full and ragged): the rule's choice is 0.5 % above the better of
     // both in the mean, shares always 10.8 %, planned always 4.6 %.  Shares against planned, us:
-    // head_dim 128, 512 lists of up to 2048 tokens 62 / 82, 800 of 640 48 / 41; head_dim 512,
+    // head_dim 128, 512 lists of up to 2048 tokens 62 / 80, 800 of 640 48 / 41; head_dim 512,
     // 36 lists of 320 19 / 25, 150 of 640 60 / 51.
     const long long lists = static_cast<long long>(batch) * num_kv_heads;
     long long blocks = 0;
@@ -658,16 +658,18 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
         // that leaves under a third of a list out): lists of unknown lengths gain nothing from
         // the odd splits that the planner balances, and a code cache's CTA starts for more than
         // the planner counts.  Measured, us against the planner's splits: 16 x 8 lists of 2048
-        // tokens 20.8 / 25.7, ragged 20.3 / 21.8; 64 x 8 of 2048 ragged 44 / 55, full 72 / 69;
-        // 16 x 4 of 4096 at head_dim 256 30.8 / 31.3; 30 x 4 of 3200 23.5 / 24.2; the same from
-        // 32 lists down.
+        // tokens 19.8 / 24.8, ragged 19.2 / 21.2; 64 x 8 of 2048 ragged 42.6 / 52.6, but full
+        // 71 / 67; 16 x 4 of 4096 at head_dim 256 34.7 / 33.7; 30 x 4 of 3200 26.2 / 26.0; the
+        // same from 32 lists down.  (It does not count rounds of the machine: 456 full lists of
+        // 2048 take 42 us, 464 67; 108 of 1024 at head_dim 256, in 324 CTAs on 304, 35 / 30.)
         const double units = static_cast<double>(lists) * p->row_groups;
         const int n = std::max(1, static_cast<int>(slots / units + 0.35));
         int bps = (max_blocks + n - 1) / n;
         // Whole lists where splitting them saves too few blocks to pay for its reduction, which
-        // starts late once the splits are more than the SMs (their CTAs leave it no room): us,
-        // whole against split, head_dim 256, 108 lists of 128 tokens 13.4 / 18.5, of 512 22 / 25,
-        // of 1024 30 / 28.5; head_dim 128, 216 lists of 512 12.6 / 15.2, 16 of 128 6.3 / 7.0.
+        // starts late once the splits are more than the SMs (their CTAs leave it no room).  us,
+        // whole against split (with one f16 value a probability), head_dim 256, 108 lists of 128
+        // tokens 13.4 / 18.5, of 512 22 / 25, of 1024 30 / 28.5; head_dim 128, 216 lists of 512
+        // 12.6 / 15.2, 16 of 128 6.3 / 7.0.
         const double ctas = units * ((max_blocks + bps - 1) / bps);
         if (max_blocks - bps <= (ctas > num_sms ? 5 : head_dim > 128 ? 0 : 2)) bps = max_blocks;
         if (bps != p->blocks_per_split) {

@@ -6,8 +6,8 @@
 // for the pages that hold positions [begin, L) of each sequence.  Exact: a minimum
 // rounds nothing, and E4M3 values are 16-bit values.  HBM-bound: a page's keys are
 // read once (2 D bytes a token), its two rows written.  A page and KV head is one unit:
-// one warp, or the four warps of a CTA where there are too few units to fill the
-// machine (a batch's newest pages); D/8 lanes hold a row, several rows in flight.
+// one warp, or the four warps of a CTA for long pages and where there are too few units to
+// fill the machine (a batch's newest pages); D/8 lanes hold a row, several rows in flight.
 // GB300: the pages of 131072 tokens, 4 heads of 128 (138 MB), 23.1 us, 0.88 of the
 // measured copy bandwidth; the newest pages of 64 sequences 2.7 us.
 #include <algorithm>

@@ -31,9 +31,9 @@
 // counted by an atomic, was measured first: the count's fences cost every CTA 1.4-2.1 us,
 // and the choosing CTAs' registers and shared memory took from what streams beside them.)
 //
-// GB300, us a call in a stream of calls: 4 rows of 4096 pages (head_dim 128) 9.8, of
+// GB300, us a call in a stream of calls: 4 rows of 4096 pages (head_dim 128) 10.0, of
 // which scoring 3 and choosing 5; 64 x 8 ragged rows of up to 2048 pages (head_dim 192,
-// 308 MB) 66, scoring 56 of them at 5.5 TB/s; 16 query tokens x 8 heads of 512 pages 13.2.
+// 308 MB) 68, scoring 57 of them at 5.4 TB/s; 16 query tokens x 8 heads of 512 pages 13.3.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -69,7 +69,8 @@ struct SelShape {
     static constexpr int SMEM = R * U * CPL * kScoreThreads * 16;
 };
 
-// Loads that stay where they are written: scores of other CTAs, after their counter.
+// Loads from L2 that stay where they are written, before or after a wait: what the scoring
+// launch read too, and its scores.
 __device__ __forceinline__ float ld_cg(const float* p) {
     float v;
     asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
