@@ -13,7 +13,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <functional>
-#include <new>
+#include <memory>
 #include <queue>
 #include <string>
 #include <vector>
@@ -448,8 +448,8 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
         }
     }
 
-    fdec_plan_s* p = new (std::nothrow) fdec_plan_s();
-    if (p == nullptr) return fail(FDEC_ERR_INVALID_ARG, "out of host memory");
+    std::unique_ptr<fdec_plan_s> owner(new fdec_plan_s());
+    fdec_plan_s* const p = owner.get();
     p->batch = batch;
     p->q_len = q_len;
     p->page_size = page_size;
@@ -501,10 +501,8 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
         threads = split_threads(head_dim);
     }
     p->row_groups = (p->rows + p->rc - 1) / p->rc;
-    if (p->row_groups > 65535 || num_kv_heads > 65535) {
-        delete p;
+    if (p->row_groups > 65535 || num_kv_heads > 65535)
         return fail(FDEC_ERR_UNSUPPORTED, "q_len x group / rows per CTA or num_kv_heads above 65535");
-    }
     p->ctas_per_sm = p->persistent ? split_mma_persist_ctas_per_sm(head_dim)
                                    : std::max(1, std::min(static_cast<int>(233472 / (smem + 1024)), 2048 / threads));
 
@@ -679,10 +677,7 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
             size_t bytes = 0;
             const fdec_status st = plan_impl(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads,
                                              head_dim, dtype, causal, &so, false, &p->selected, &bytes);
-            if (st != FDEC_OK) {
-                delete p;
-                return st;
-            }
+            if (st != FDEC_OK) return st;
             p->off_selected = off;
             off = align_up(off + bytes);
         }
@@ -696,16 +691,24 @@ static fdec_status plan_impl(const int32_t* seq_lens_host, int batch, int q_len,
         std::memcpy(p->meta.data() + p->off_tasks[i], p->passes[i].data(), sizeof(ReduceTask) * p->passes[i].size());
 
     log_plan(p);
-    *out_plan = p;
     *workspace_bytes = p->ws_bytes;
+    *out_plan = owner.release();
     return FDEC_OK;
+}
+
+static fdec_status out_of_memory() noexcept {
+    return static_cast<fdec_status>(record_failure(FDEC_ERR_INVALID_ARG, "out of host memory"));
 }
 
 fdec_status fdec_plan(const int32_t* seq_lens_host, int batch, int q_len, int page_size, int num_qo_heads,
                       int num_kv_heads, int head_dim, fdec_dtype dtype, int causal, const fdec_plan_opts* opts,
                       fdec_plan_t* out_plan, size_t* workspace_bytes) {
-    return plan_impl(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, causal, opts,
-                     false, out_plan, workspace_bytes);
+    try {
+        return plan_impl(seq_lens_host, batch, q_len, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, causal,
+                         opts, false, out_plan, workspace_bytes);
+    } catch (...) {  // (the standard containers' allocations)
+        return out_of_memory();
+    }
 }
 
 fdec_status fdec_plan_selected(const int32_t* seq_lens_host, int batch, int page_size, int num_qo_heads,
@@ -717,8 +720,12 @@ fdec_status fdec_plan_selected(const int32_t* seq_lens_host, int batch, int page
         if (workspace_bytes != nullptr) *workspace_bytes = 0;
         return fail(FDEC_ERR_UNSUPPORTED, "fdec_run_selected reads 16-bit and E4M3 caches, not q8_0");
     }
-    return plan_impl(seq_lens_host, batch, 1, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, 0, opts, true,
-                     out_plan, workspace_bytes);
+    try {
+        return plan_impl(seq_lens_host, batch, 1, page_size, num_qo_heads, num_kv_heads, head_dim, dtype, 0, opts, true,
+                         out_plan, workspace_bytes);
+    } catch (...) {
+        return out_of_memory();
+    }
 }
 
 fdec_status fdec_plan_destroy(fdec_plan_t plan) {

@@ -5,6 +5,8 @@ Tolerances are derived beside each test."""
 import math
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -468,3 +470,29 @@ def test_special_values_do_not_make_a_row_slow():
         assert best(ordinary, special_bounds(kind, pages, hk, d, torch.bfloat16, 3)) < 10 * usual, kind
     for value in (0.0, math.nan):
         assert best(torch.full_like(ordinary, value), bounds_like(pages, hk, d, torch.bfloat16, 3)) < 10 * usual, value
+
+
+_LITTLE_MEMORY = r'''
+import resource, sys
+sys.path.insert(0, sys.argv[1])
+import paged_split_kv_gather_gb300 as fd
+fd.fdec_plan([64], 1, 64, 4, 1, 128, num_sms=152)  # everything is loaded
+now = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (now + (48 << 20), resource.RLIM_INFINITY))
+for page_lists in (False, True):
+    try:
+        fd.fdec_plan([262144] * 4000, 1, 64, 32, 4, 128, blocks_per_split=1, num_sms=152, page_lists=page_lists)
+    except fd.FdecError as e:
+        assert "memory" in str(e), e
+    else:
+        raise AssertionError("planned")
+fd.fdec_plan([64], 1, 64, 4, 1, 128, num_sms=152)
+print("refused")
+'''
+
+
+def test_plans_without_host_memory_are_refused():
+    """The plan's lists do not fit the process: a status, and the process goes on."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _LITTLE_MEMORY, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused" in r.stdout, (r.returncode, r.stdout, r.stderr[-2000:])
