@@ -66,6 +66,9 @@ typedef enum { FDEC_F16 = 0, FDEC_BF16 = 1 } fdec_dtype;
 #define FDEC_DEVERR_PAGE_ID 0x1u       /* a page id outside [0, num_pages): that row was skipped */
 #define FDEC_DEVERR_SEQ_LEN 0x2u       /* seq_lens[b] above the planned capacity (clamped) or < 0 */
 #define FDEC_DEVERR_TIMEOUT 0x4u       /* a bounded pipeline wait gave up; results are invalid */
+#define FDEC_DEVERR_TREE 0x8u          /* a bad parent, token or path of a drafted tree (see there) */
+#define FDEC_DEVERR_NO_PAGES 0x10u     /* fdec_reserve_pages: fewer free pages than were asked for */
+#define FDEC_DEVERR_PROB 0x20u         /* fdec_verify_drafts: a probability outside [0, 2], or a row of zeros */
 
 /*
  * One K or V pool.  Element (page, kv_head, slot, dim) is at
@@ -446,6 +449,182 @@ fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_
                               fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_ids, int64_t page_ids_stride,
                               const int32_t* counts, float scale, float k_scale, float v_scale, void* out,
                               int out_type, float* lse, void* workspace, cudaStream_t stream);
+
+/*
+ * Speculative decoding over a paged cache without the host.  A round drafts a tree of
+ * tokens for every sequence: node 0 is the newest token that stands (its key is not in
+ * the cache yet), node i has the parent parents[i] < i, and node i's key and value lie
+ * at position prefix_len + i of the sequence; its rotation goes by prefix_len + its depth
+ * (rope_positions of fdec_norm_rope_append).  A round is
+ *   fdec_reserve_pages      pages for the nodes (sequences may become forks of others)
+ *   fdec_norm_rope_append   the nodes' rows, per layer
+ *   fdec_run                attention of the nodes to the prefix: seq_lens = prefix_lens,
+ *                           q_len = nodes, not causal
+ *   fdec_tree_attention     attention to the node itself and its ancestors, joined with it
+ *   fdec_verify_drafts      the nodes that stand, and the next token
+ *   fdec_keep_path          their keys and values moved behind the prefix, in all layers
+ * A chain of drafted tokens is the tree with parents[i] = i - 1.  Each is one to three
+ * kernel launches, allocates nothing, and may be captured in a CUDA graph; the kernels
+ * start as programmatic dependents, as those above do.  (The pages have no counterpart of
+ * these four; their speculative decoding is the multi-token query of fdec_run.)
+ *
+ * num_nodes, the nodes per sequence that arrays have room for, is in [1, 64].  node_counts:
+ * int32 device [batch], the nodes of each sequence, or NULL (num_nodes each); a value
+ * outside [0, num_nodes] sets FDEC_DEVERR_SEQ_LEN and is clamped.  parents: int32 device
+ * [batch][num_nodes]; a value outside [-1, i) for node i sets FDEC_DEVERR_TREE and is taken
+ * as -1 (no parent).  device_errors: optional uint32 device word.
+ */
+
+/*
+ * Attention of the nodes of drafted trees to themselves and their ancestors, joined with
+ * the state (o, lse) of their attention to the prefix:
+ *   z_j = scale * k_scale * q_i . K_j,  j over node i, its parent, its parent's parent, ...
+ *   lse = ln(exp(lse_prefix) + sum_j exp(z_j))
+ *   out = exp(lse_prefix - lse) o_prefix + v_scale sum_j exp(z_j - lse) V_j
+ *   q: [batch, num_nodes, Hq, head_dim] 16-bit, as for fdec_run, rows starting on 16-byte
+ *      boundaries (strides multiples of 8 elements).
+ *   k, v, page_table, page_size, head_dim: as for fdec_run; kv_dtype FDEC_KV_SAME, or
+ *      FDEC_KV_E4M3 (head_dim 128 and 256).
+ *   prefix_lens: int32 device [batch]; a negative one sets FDEC_DEVERR_SEQ_LEN and is taken
+ *      as 0.  A node's row past the page table sets FDEC_DEVERR_SEQ_LEN, one in a bad page
+ *      FDEC_DEVERR_PAGE_ID: no node sees it.
+ *   parents: or NULL, a chain.
+ *   o_prefix: float32 device [batch, num_nodes, Hq, head_dim] contiguous, lse_prefix float32
+ *      [batch, num_nodes, Hq], as fdec_run writes them; or both NULL (no prefix).  A state
+ *      with lse = -inf counts for nothing, whatever its o.
+ *   out: contiguous, 16-byte aligned; out_type FDEC_OUT_F32 or FDEC_OUT_SAME; lse: float32 or
+ *      NULL.  out may be o_prefix (FDEC_OUT_F32) and lse lse_prefix; they must not overlap
+ *      otherwise.  Rows of nodes past node_counts are not written.  A row that sees nothing
+ *      gives out = 0 and lse = -inf.  Values of rows that a node does not see never reach it,
+ *      NaN and infinities among them.
+ */
+fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_stride_head, fdec_kv_desc k,
+                                fdec_kv_desc v, const int32_t* page_table, int64_t page_table_stride,
+                                const int32_t* prefix_lens, const int32_t* node_counts, const int32_t* parents,
+                                int batch, int num_nodes, int page_size, int num_qo_heads, int num_kv_heads,
+                                int head_dim, fdec_dtype dtype, int kv_dtype, float scale, float k_scale, float v_scale,
+                                const float* o_prefix, const float* lse_prefix, void* out, int out_type, float* lse,
+                                uint32_t* device_errors, cudaStream_t stream);
+
+/* Element types of probabilities. */
+enum { FDEC_PROB_F16 = 0, FDEC_PROB_BF16 = 1, FDEC_PROB_F32 = 2 };
+
+/*
+ * Verify drafted tokens against the target's probabilities.  With p = the target's row of
+ * node x and q = the draft's row of x (from which x's children were drawn independently),
+ * beginning at x = 0 with s = 0, W = 1, the children c of x are tried in their order:
+ *   c (token t) stands if  uniforms[c] * W * q(t) < max(p(t) - s q(t), 0): x becomes c;
+ *   else  s += W,  W = sum_v max(p(v) - s q(v), 0)
+ * (rejection sampling: after the k-th rejection the target left over is max(p - s q, 0) / W).
+ * When no child stands, the next token is the smallest v with
+ *   sum_{v' <= v} r(v') > uniforms[0] * sum_{v'} r(v'),   r = max(p - s q, 0),
+ * or of r = p where that residual is zero everywhere.  So the tokens are distributed as
+ * the target's own.  Without draft_probs the children count as given (the draft's most likely
+ * tokens, say): q is 1 at the token tried, so c stands if uniforms[c] * W < p(t), and else
+ * loses its weight, W = the sum of p without the tokens tried.  Sums are carried in pairs of
+ * fp32 and in fp64: about 46 bits.
+ *   target_probs: device [batch][num_nodes][vocab] of prob_dtype: element (b, i, v) at
+ *      target_probs + b * target_stride_seq + i * target_stride_node + v (elements).
+ *      Probabilities count as clamped to [0, 2] and NaN as 0; one that is not in there, where
+ *      it is read, sets FDEC_DEVERR_PROB.
+ *   draft_probs: like target_probs, rows of nodes that have children (never the last node's,
+ *      so [batch][num_nodes - 1][vocab] will do); or NULL.
+ *   tokens: int32 device [batch][num_nodes], tokens[b][0] is not read; a token outside
+ *      [0, vocab) sets FDEC_DEVERR_TREE and does not stand.
+ *   parents: as above, or NULL (a chain).  Only nodes that hang together with node 0 count.
+ *   uniforms: float32 device [batch][num_nodes], random numbers in [0, 1) (clamped; NaN as 0).
+ *   path: int32 device [batch][num_nodes], the nodes that stand, 0 first, then -1.
+ *   path_lens: int32 device [batch], their number (node 0 among them; 0 without nodes).
+ *   out_tokens: int32 device [batch][num_nodes]: the tokens of path[1..], then the next
+ *      token (-1 if the target's row is all zeros: FDEC_DEVERR_PROB), then -1.
+ * vocab in [1, 2^24].
+ */
+fdec_status fdec_verify_drafts(const void* target_probs, int64_t target_stride_seq, int64_t target_stride_node,
+                               const void* draft_probs, int64_t draft_stride_seq, int64_t draft_stride_node,
+                               int prob_dtype, const int32_t* tokens, const int32_t* parents,
+                               const int32_t* node_counts, const float* uniforms, int batch, int num_nodes, int vocab,
+                               int32_t* path, int32_t* path_lens, int32_t* out_tokens, uint32_t* device_errors,
+                               cudaStream_t stream);
+
+/*
+ * A stack of pools of one shape, a layer each: row (layer, page, head, slot) of row_bytes
+ * bytes at
+ *   base + layer*stride_layer + page*stride_page + head*stride_head + slot*stride_token
+ * (strides in bytes).  Keys, values, codes or block scales of any type are such rows.
+ * base, strides and row_bytes are multiples of 8; rows of multiples of 16 on 16-byte
+ * boundaries move faster.
+ */
+typedef struct {
+    void* base;
+    int32_t num_layers;
+    int32_t num_heads;
+    int32_t row_bytes;
+    int32_t reserved;      /* 0 */
+    int64_t num_pages;
+    int64_t stride_layer;
+    int64_t stride_page;
+    int64_t stride_head;
+    int64_t stride_token;
+} fdec_cache;
+
+/* The most caches that a call takes: keys and values of 64 layers, each for itself. */
+enum { FDEC_MAX_CACHES = 128 };
+
+/*
+ * Keep the nodes of a path: the row at position prefix_lens[b] + path[b][i] moves to
+ * position prefix_lens[b] + i, for i < path_lens[b], in every layer and head of every cache,
+ * and seq_lens[b] = prefix_lens[b] + path_lens[b] (the next round's prefix).  Positions
+ * behind that keep what they hold.
+ *   path: int32 device [batch][path_stride], increasing in i and >= 0 (as written by
+ *      fdec_verify_drafts), at most 64 entries: num_nodes.
+ *   path_lens: int32 device [batch]; outside [0, num_nodes]: FDEC_DEVERR_SEQ_LEN, clamped.
+ *      A path that is not increasing, or goes past num_nodes - 1, sets FDEC_DEVERR_TREE and
+ *      counts up to there.
+ *   prefix_lens, page_table, device_errors: as for fdec_tree_attention; a row in a bad page
+ *      (for any of the caches) or past the page table is not moved.
+ *   seq_lens: int32 device [batch]; must not overlap prefix_lens.
+ * The pages that hold the moved rows must belong to one sequence alone (fdec_reserve_pages
+ * sees to that).
+ */
+fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32_t* page_table, int batch,
+                           int64_t page_table_stride, int page_size, const int32_t* prefix_lens, const int32_t* path,
+                           int64_t path_stride, const int32_t* path_lens, int num_nodes, int32_t* seq_lens,
+                           uint32_t* device_errors, cudaStream_t stream);
+
+/* Device bytes of workspace that fdec_reserve_pages needs: at most 4 * num_pages + 256 * batch + 256. */
+fdec_status fdec_reserve_pages_workspace(int batch, int64_t num_pages, size_t* workspace_bytes);
+
+/*
+ * Pages for new lengths.  The page tables and the lengths are the whole state of the pool:
+ * a page is in use if an entry below ceil(seq_lens[b] / page_size) of some row b names it,
+ * and free otherwise, so a sequence gives pages back by a shorter length.  For every
+ * sequence b the entries up to ceil(new_lens[b] / page_size) are filled:
+ *   - a sequence that grows keeps its pages and gets free ones for the rest; if its last page
+ *     is only partly filled and another entry names it too, it gets a page of its own with
+ *     the filled rows copied.
+ *   - with sources[b] = a (a != b, seq_lens[b] == 0) b becomes a fork of a, with a's first
+ *     min(seq_lens[a], new_lens[b]) positions: full pages are shared, the filled rows of the
+ *     last one copied.  a itself may grow in the same call, but not be a fork of this call.
+ *   - new_lens[b] <= seq_lens[b] changes nothing (and gives pages back).
+ * Free pages go out in ascending order to the sequences in their order, entries in ascending
+ * order.  A sequence whose pages, with those of all sequences before it, are more than there
+ * are free gets none: its row keeps its entries and FDEC_DEVERR_NO_PAGES is set.
+ *   page_table: int32 device [batch][page_table_stride], updated.  Entries past a length are
+ *      never read.  An entry in use outside [0, num_pages) sets FDEC_DEVERR_PAGE_ID.
+ *   seq_lens, new_lens: int32 device [batch] in [0, page_table_stride * page_size].
+ *   sources: int32 device [batch], a negative one for none; or NULL.  A bad length or source
+ *      sets FDEC_DEVERR_SEQ_LEN, and that sequence is left alone.
+ *   granted: int32 device [batch]: new_lens[b], or seq_lens[b] where it was refused; must not
+ *      overlap the other arrays.
+ *   num_pages: pages of the pool, at most what every cache has, and at most 2^26.
+ *   caches: the rows to copy, num_caches of them (0: only page numbers are dealt with).
+ *   workspace: see fdec_reserve_pages_workspace; 256-byte aligned, not shared by calls that
+ *      may overlap; its contents do not matter.
+ */
+fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_table_stride, int page_size,
+                               const int32_t* seq_lens, const int32_t* new_lens, const int32_t* sources,
+                               int32_t* granted, int64_t num_pages, const fdec_cache* caches, int num_caches,
+                               void* workspace, size_t workspace_bytes, uint32_t* device_errors, cudaStream_t stream);
 
 /* Release a plan (NULL is a no-op). */
 fdec_status fdec_plan_destroy(fdec_plan_t plan);

@@ -26,18 +26,21 @@ __all__ = [
     "FDEC_KV_SAME", "FDEC_KV_E4M3", "FDEC_KV_Q8_0", "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
     "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
     "fdec_run_selected", "fdec_plan_get_selected_info", "FDEC_OUT_F32", "FDEC_OUT_SAME", "Rows", "PageSelect", "SparseDecode",
-    "DEVERR_PAGE_ID", "DEVERR_SEQ_LEN", "DEVERR_TIMEOUT",
+    "fdec_tree_attention", "fdec_verify_drafts", "fdec_keep_path", "fdec_reserve_pages", "fdec_reserve_pages_workspace",
+    "Cache", "TreeDecode", "FDEC_PROB_F16", "FDEC_PROB_BF16", "FDEC_PROB_F32",
+    "DEVERR_PAGE_ID", "DEVERR_SEQ_LEN", "DEVERR_TIMEOUT", "DEVERR_TREE", "DEVERR_NO_PAGES", "DEVERR_PROB",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfdec.so")
-_BINDING_PATH = os.path.join(_HERE, "_sparse_binding.so")
 
 FDEC_F16, FDEC_BF16 = 0, 1
 FDEC_PATH_AUTO, FDEC_PATH_SIMT, FDEC_PATH_MMA, FDEC_PATH_TC = 0, 1, 2, 3
 FDEC_KV_SAME, FDEC_KV_E4M3, FDEC_KV_Q8_0 = 0, 1, 2
 FDEC_OUT_F32, FDEC_OUT_SAME = 0, 1
+FDEC_PROB_F16, FDEC_PROB_BF16, FDEC_PROB_F32 = 0, 1, 2
 DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_TREE, DEVERR_NO_PAGES, DEVERR_PROB = 0x8, 0x10, 0x20
 
 STATUS_NAMES = {
     0: "FDEC_OK", 1: "FDEC_ERR_INVALID_ARG", 2: "FDEC_ERR_LAYOUT", 3: "FDEC_ERR_UNSUPPORTED",
@@ -53,6 +56,7 @@ EXPORTED_SYMBOLS = (
     "fdec_run_scaled", "fdec_append_e4m3", "fdec_run_q8_0",
     "fdec_norm_rope_append", "fdec_page_bounds", "fdec_select_pages", "fdec_select_pages_workspace",
     "fdec_run_selected", "fdec_plan_selected", "fdec_plan_get_selected_info",
+    "fdec_tree_attention", "fdec_verify_drafts", "fdec_keep_path", "fdec_reserve_pages", "fdec_reserve_pages_workspace",
 )
 
 
@@ -73,6 +77,15 @@ class Rows(ctypes.Structure):
     """fdec_rows: 16-bit rows of tokens, element (token, head, dim) at base + token*stride_tok + head*stride_head + dim."""
 
     _fields_ = [("base", ctypes.c_void_p), ("stride_tok", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    """fdec_cache: a stack of pools, row (layer, page, head, slot) of row_bytes bytes; strides in bytes."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("num_layers", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("stride_layer", ctypes.c_int64), ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64)]
 
 
 class PlanOpts(ctypes.Structure):
@@ -157,6 +170,18 @@ def _load():
         lib.fdec_plan_get_selected_info.argtypes = [P, ctypes.POINTER(SelectedInfo)]
         lib.fdec_run_selected.restype = I
         lib.fdec_run_selected.argtypes = [P, P, I64, I64, KVDesc, KVDesc, P, I64, P, F, F, F, P, I, P, P, P]
+        CP = ctypes.POINTER(Cache)
+        lib.fdec_tree_attention.restype = I
+        lib.fdec_tree_attention.argtypes = [P, I64, I64, KVDesc, KVDesc, P, I64, P, P, P, I, I, I, I, I, I, I, I, F, F, F,
+                                            P, P, P, I, P, P, P]
+        lib.fdec_verify_drafts.restype = I
+        lib.fdec_verify_drafts.argtypes = [P, I64, I64, P, I64, I64, I, P, P, P, P, I, I, I, P, P, P, P, P]
+        lib.fdec_keep_path.restype = I
+        lib.fdec_keep_path.argtypes = [CP, I, P, I, I64, I, P, P, I64, P, I, P, P, P]
+        lib.fdec_reserve_pages_workspace.restype = I
+        lib.fdec_reserve_pages_workspace.argtypes = [I, I64, IP]
+        lib.fdec_reserve_pages.restype = I
+        lib.fdec_reserve_pages.argtypes = [P, I, I64, I, P, P, P, P, I64, CP, I, P, S, P, P]
         lib.fdec_plan_destroy.restype = I
         lib.fdec_plan_destroy.argtypes = [P]
         lib.fdec_plan_get_info.restype = I
@@ -445,27 +470,32 @@ def fdec_merge_states(o, lse, o_out, lse_out=None, stream=None) -> None:
 # ---------------------------------------------------------------------------
 
 _binding = None
+_draft_binding = None
+
+
+def _marshalling(name: str, entries):
+    """A compiled marshalling module, its entries set to this library's."""
+    path = os.path.join(_HERE, f"{name}.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built: run `python -c 'import __graft_entry__ as g; g.build()'` first")
+    import torch  # noqa: F401  (its libraries are the module's)
+
+    spec = importlib.util.spec_from_file_location(name, path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_entries(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries))
+    return mod
 
 
 def _sparse():
-    """The compiled marshalling module, its entries set to this library's."""
     global _binding
     if _binding is None:
         lib = _load()
         with _lock:
             if _binding is None:
-                if not os.path.exists(_BINDING_PATH):
-                    raise RuntimeError(
-                        f"{_BINDING_PATH} is not built: run `python -c 'import __graft_entry__ as g; g.build()'` first")
-                import torch  # noqa: F401  (its libraries are the module's)
-
-                spec = importlib.util.spec_from_file_location("_sparse_binding", _BINDING_PATH)
-                mod = importlib.util.module_from_spec(spec)
-                spec.loader.exec_module(mod)
-                mod.set_entries(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                _binding = _marshalling("_sparse_binding", (
                     lib.fdec_norm_rope_append, lib.fdec_page_bounds, lib.fdec_select_pages, lib.fdec_run_selected,
-                    lib.fdec_internal_checks_only)))
-                _binding = mod
+                    lib.fdec_internal_checks_only))
     return _binding
 
 
@@ -648,3 +678,147 @@ class SparseDecode:
 
     def device_errors(self, clear=True, stream=None) -> int:
         return self.select.device_errors(clear) | self.attend.device_errors(clear, stream)
+
+
+# ---------------------------------------------------------------------------
+# speculative decoding
+# ---------------------------------------------------------------------------
+
+def _draft():
+    global _draft_binding
+    if _draft_binding is None:
+        lib = _load()
+        with _lock:
+            if _draft_binding is None:
+                _draft_binding = _marshalling("_draft_binding", (
+                    lib.fdec_tree_attention, lib.fdec_verify_drafts, lib.fdec_keep_path, lib.fdec_reserve_pages,
+                    lib.fdec_internal_checks_only))
+    return _draft_binding
+
+
+def fdec_tree_attention(q, k, v, page_table, prefix_lens, parents, o_prefix, lse_prefix, out, lse, page_size: int,
+                        node_counts=None, scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                        device_errors=None, stream=None) -> None:
+    """Attention of every node of a drafted tree to itself and its ancestors, joined with the state (o_prefix,
+    lse_prefix) of its attention to the prefix.  q [B, N, Hq, D]; k, v the cache views [page, kv_head, slot, dim], node
+    i's row at position prefix_lens[b] + i; parents int32 [B, N] (None: a chain); o_prefix float32 [B, N, Hq, D] and
+    lse_prefix float32 [B, N, Hq] as fdec_run writes them (or both None); out [B, N, Hq, D] float32 or of q's type (may
+    be o_prefix), lse float32 [B, N, Hq] or None; node_counts int32 [B] (None: N each)."""
+    status = (_draft_binding or _draft()).tree_attention(
+        q, k, v, page_table, prefix_lens, parents, o_prefix, lse_prefix, out, lse, page_size, node_counts, scale, k_scale,
+        v_scale, device_errors, stream)
+    if status:
+        _check(status)
+
+
+def fdec_verify_drafts(target_probs, draft_probs, tokens, parents, uniforms, path, path_lens, out_tokens,
+                       node_counts=None, device_errors=None, stream=None) -> None:
+    """Verify drafted tokens: target_probs [B, N, V] and draft_probs [B, N or N - 1, V] (or None) float32, bfloat16 or
+    float16; tokens, parents (None: a chain), path, out_tokens int32 [B, N]; uniforms float32 [B, N], uniforms[:, 0] for
+    the next token; path_lens, node_counts int32 [B]."""
+    status = (_draft_binding or _draft()).verify_drafts(target_probs, draft_probs, tokens, parents, uniforms, path,
+                                                        path_lens, out_tokens, node_counts, device_errors, stream)
+    if status:
+        _check(status)
+
+
+def fdec_keep_path(caches, page_table, prefix_lens, path, path_lens, seq_lens, page_size: int, device_errors=None,
+                   stream=None) -> None:
+    """Move the rows at prefix_lens[b] + path[b][i] to prefix_lens[b] + i in all caches and write the new lengths to
+    seq_lens.  caches: tensors [page, kv_head, slot, dim] or [layer, page, kv_head, slot, dim] of any type."""
+    status = (_draft_binding or _draft()).keep_path(caches, page_table, prefix_lens, path, path_lens, seq_lens, page_size,
+                                                    device_errors, stream)
+    if status:
+        _check(status)
+
+
+def fdec_reserve_pages_workspace(batch: int, num_pages: int) -> int:
+    """Bytes of the workspace that fdec_reserve_pages needs."""
+    total = ctypes.c_size_t()
+    _check(_load().fdec_reserve_pages_workspace(batch, num_pages, ctypes.byref(total)))
+    return total.value
+
+
+def fdec_reserve_pages(page_table, seq_lens, new_lens, granted, num_pages: int, page_size: int, workspace, sources=None,
+                       caches=(), device_errors=None, stream=None) -> None:
+    """Fill page_table int32 [B, W] with pages for new_lens, of those that no entry in use names; granted gets the
+    lengths that there are pages for.  sources int32 [B]: sequences of length 0 that become forks; caches (as for
+    fdec_keep_path): the rows of a shared, partly filled last page are copied there."""
+    status = (_draft_binding or _draft()).reserve_pages(page_table, seq_lens, new_lens, granted, num_pages, page_size,
+                                                        workspace, sources, caches, device_errors, stream)
+    if status:
+        _check(status)
+
+
+class TreeDecode:
+    """Rounds of speculative decoding of a batch, plans and buffers allocated once: pages for the drafted nodes, per
+    layer their rows and attention, the verification, and the accepted path's rows moved behind the prefix.  Every
+    method only launches kernels, so a whole round can be captured in a CUDA graph.
+
+    max_lens: the longest prefix that each sequence gets; num_nodes: the nodes of a tree; num_pages: of the pool."""
+
+    def __init__(self, max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, num_pages, dtype="bf16",
+                 kv_dtype="", device=None):
+        import torch
+
+        batch = len(max_lens)
+        if not 1 <= num_nodes <= 64:
+            raise ValueError("num_nodes must be between 1 and 64")
+        device = device or "cuda"
+        self.batch, self.num_nodes, self.page_size, self.num_pages = batch, num_nodes, page_size, num_pages
+        self.prefix = PagedDecode(max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,
+                                  device=device, page_lists=False, kv_dtype=kv_dtype)
+        self.workspace = torch.empty(fdec_reserve_pages_workspace(batch, num_pages), dtype=torch.uint8, device=device)
+        self.o = torch.empty((batch, num_nodes, num_qo_heads, head_dim), device=device)
+        self.state_lse = torch.empty((batch, num_nodes, num_qo_heads), device=device)
+        self.path = torch.empty((batch, num_nodes), dtype=torch.int32, device=device)
+        self.tokens = torch.empty_like(self.path)
+        self.path_lens, self.granted, self.seq_lens = (torch.empty(batch, dtype=torch.int32, device=device)
+                                                       for _ in range(3))
+        self.errors = torch.zeros(1, dtype=torch.int32, device=device)
+        self.batch_indices = torch.arange(batch, dtype=torch.int32, device=device).repeat_interleave(num_nodes)
+        self.nodes = torch.arange(num_nodes, dtype=torch.int32, device=device)
+
+    def reserve(self, page_table, prefix_lens, caches=(), sources=None, stream=None):
+        """Pages for the nodes behind prefix_lens; returns the lengths granted (prefix_lens[b] + num_nodes)."""
+        fdec_reserve_pages(page_table, prefix_lens, prefix_lens + self.num_nodes, self.granted, self.num_pages,
+                           self.page_size, self.workspace, sources, caches, self.errors, stream)
+        return self.granted
+
+    def attend(self, q, k_new, v_new, q_weight, k_weight, cos_sin, k, v, page_table, prefix_lens, parents, depths, out,
+               lse=None, node_counts=None, eps=1e-6, interleaved=False, scale=None, k_scale=1.0, v_scale=1.0, stream=None):
+        """One layer: q [B * N, Hq, D] (normed and rotated in place), k_new, v_new [B * N, Hk, D]; depths int32 [B, N],
+        the nodes' distance from node 0 (None with parents None: a chain); out [B, N, Hq, D] float32 or of q's type."""
+        n, hq, d = q.shape
+        if depths is None and parents is not None:
+            raise ValueError("a tree's rows are rotated by the depths of its nodes")
+        positions = prefix_lens[:, None] + self.nodes
+        turns = None if depths is None else (prefix_lens[:, None] + depths).reshape(-1)
+        fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, self.batch_indices, positions.reshape(-1), q,
+                              k, v, page_table, self.page_size, eps, interleaved, turns, k_scale, v_scale, self.errors,
+                              stream)
+        rows = q.view(self.batch, self.num_nodes, hq, d)
+        self.prefix.run(rows, k, v, page_table, prefix_lens, self.o, self.state_lse, scale, stream, k_scale, v_scale)
+        fdec_tree_attention(rows, k, v, page_table, prefix_lens, parents, self.o, self.state_lse, out, lse, self.page_size,
+                            node_counts, scale, k_scale, v_scale, self.errors, stream)
+        return out
+
+    def verify(self, target_probs, draft_probs, tokens, parents, uniforms, node_counts=None, stream=None):
+        """Returns (path, path_lens, tokens), the holder's own tensors."""
+        fdec_verify_drafts(target_probs, draft_probs, tokens, parents, uniforms, self.path, self.path_lens, self.tokens,
+                           node_counts, self.errors, stream)
+        return self.path, self.path_lens, self.tokens
+
+    def keep(self, caches, page_table, prefix_lens, stream=None):
+        """Keep the path that verify() found, in all caches; returns the new lengths (the next round's prefix_lens),
+        the holder's own tensor, which the next keep() writes: copy it into prefix_lens."""
+        fdec_keep_path(caches, page_table, prefix_lens, self.path, self.path_lens, self.seq_lens, self.page_size,
+                       self.errors, stream)
+        return self.seq_lens
+
+    def device_errors(self, clear=True, stream=None) -> int:
+        """The FDEC_DEVERR_* bits of the calls so far (synchronises)."""
+        flags = int(self.errors.item())
+        if clear:
+            self.errors.zero_()
+        return flags | self.prefix.device_errors(clear, stream)

@@ -282,6 +282,101 @@ struct SelectParams {
 int64_t select_abs_stride(int64_t max_pages);
 cudaError_t launch_select_pages(SelectParams p, int head_dim, bool bf16, int num_sms, cudaStream_t s);
 
+// Attention of drafted trees joined with the prefix's state (fdec_tree_attention).  q
+// strides in elements, cache strides in bytes.
+struct TreeParams {
+    const uint16_t* q;
+    int64_t q_st, q_sh;
+    const uint8_t* k_base;
+    int64_t k_pages, k_sp, k_sh, k_st;
+    const uint8_t* v_base;
+    int64_t v_pages, v_sp, v_sh, v_st;
+    const int32_t* page_table;
+    int64_t pt_stride;
+    const int32_t* prefix_lens;
+    const int32_t* node_counts;  // null: nodes each
+    const int32_t* parents;      // null: a chain
+    const float* o_prefix;       // [batch][nodes][hq][D] or null
+    const float* lse_prefix;
+    float* out;                  // of out_type (OutType)
+    float* lse;                  // or null
+    unsigned* err;
+    int batch, nodes, hq, hk, group, page_shift, out_type;
+    float scale_log2;            // scale x k_scale x log2(e)
+    float v_scale;
+    int tiles_per_warp;          // set by the launcher
+};
+cudaError_t launch_tree_attention(TreeParams p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s);
+
+// Most nodes of a drafted tree: a node's ancestors are the bits of one 64-bit word.
+constexpr int kMaxNodes = 64;
+
+// Verification of drafted tokens (fdec_verify_drafts).  Strides in elements.
+struct VerifyParams {
+    const void* target;
+    int64_t t_seq, t_node;
+    const void* draft;           // or null
+    int64_t d_seq, d_node;
+    const int32_t* tokens;
+    const int32_t* parents;      // null: a chain
+    const int32_t* node_counts;  // null: nodes each
+    const float* uniforms;
+    int32_t* path;
+    int32_t* path_lens;
+    int32_t* out_tokens;
+    unsigned* err;
+    int batch, nodes, vocab;
+    int chunk;                   // elements of a warp, set by the launcher
+};
+cudaError_t launch_verify_drafts(VerifyParams p, int prob_dtype, int num_sms, cudaStream_t s);
+
+// Caches of a call that moves rows, as kernel arguments.  first_block: blocks of columns
+// of the caches before this one.
+struct CacheRows {
+    uint8_t* base;
+    int64_t s_layer, s_page, s_head, s_token;
+    int layers, heads, row_vecs;  // row_vecs: vectors of a row (16 bytes, or 8 where wide is 0)
+    int wide;
+    int first_block;
+};
+constexpr int kMaxCaches = 128;
+template <int N>
+struct CacheList {
+    CacheRows c[N];
+    int n;
+};
+
+struct KeepParams {
+    const int32_t* page_table;
+    int64_t pt_stride;
+    const int32_t* prefix_lens;
+    const int32_t* path;
+    int64_t path_stride;
+    const int32_t* path_lens;
+    int32_t* seq_lens;
+    unsigned* err;
+    int64_t num_pages;           // the fewest of any cache
+    int batch, nodes, page_shift;
+};
+cudaError_t launch_keep_path(const KeepParams& p, const CacheList<kMaxCaches>& caches, int num_sms, cudaStream_t s);
+
+struct ReserveParams {
+    int32_t* page_table;
+    int64_t pt_stride;
+    const int32_t* seq_lens;
+    const int32_t* new_lens;
+    const int32_t* sources;      // or null
+    int32_t* granted;
+    unsigned* used;              // [words] a bit a page: some entry in use names it
+    unsigned* shared;            // [words] two do
+    int32_t* last_page;          // [batch] the page of a sequence's (its source's) last, partly filled part
+    unsigned* err;
+    int64_t num_pages;
+    int words, batch, page_shift;
+};
+cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCaches>& caches, int num_sms,
+                                 cudaStream_t s);
+
 // Shared by the entry points' translation units (defined in fdec_api.cu): record the
 // message of a failed call (never throws) and return its status.
 int record_failure(int status, const char* message) noexcept;

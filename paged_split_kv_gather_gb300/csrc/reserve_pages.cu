@@ -1,0 +1,269 @@
+// reserve_pages.cu -- pages for new lengths, forks of sequences, pages of their own for
+// shared ones.
+//
+// The page tables and lengths say which pages are in use; nothing else is kept, so
+// nothing can go out of step with them.  Three launches: clear two bit sets of a bit a page;
+// mark every page that an entry in use names (the second set: pages that two name); then
+// each sequence finds its pages for itself: how many pages the sequences before it need, from
+// the lengths, and which bits are its own, from the first bit set (8 KB for 65536 pages).
+// Its CTAs copy the rows that a fork or a shared last page needs.
+//
+// Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/fdec.h"
+#include "cache_rows.cuh"
+#include "fdec_internal.h"
+
+namespace fdec {
+
+namespace {
+
+constexpr int kReserveThreads = kColumnThreads;
+
+// What a sequence asks for.  Entries [first, want) of its row get new pages; a copy fills
+// the first of them with `part` rows of page `last`.
+struct Request {
+    int64_t first, want;
+    int source;
+    int part;
+    bool bad;
+    __device__ __forceinline__ int64_t need() const { return want > first ? want - first : 0; }
+};
+
+__device__ __forceinline__ bool length_ok(const ReserveParams& p, int64_t n) {
+    return n >= 0 && n <= p.pt_stride << p.page_shift;
+}
+
+// The sequence's source (itself if none) and the positions it begins with; source -1: bad.
+__device__ __forceinline__ int source_of(const ReserveParams& p, int b, int64_t* kept, int64_t* own) {
+    const int64_t len = p.seq_lens[b], want = p.new_lens[b];
+    int a = p.sources != nullptr ? p.sources[b] : -1;
+    if (a < 0) a = b;
+    *own = len;
+    if (!length_ok(p, len) || !length_ok(p, want) || a >= p.batch) return -1;
+    if (a == b) {
+        *kept = min(len, want);
+        return b;
+    }
+    const int64_t theirs = p.seq_lens[a];
+    const int up = p.sources[a];
+    if (len != 0 || !length_ok(p, theirs) || (up >= 0 && up != a)) return -1;
+    *kept = min(theirs, want);
+    return a;
+}
+
+__device__ __forceinline__ Request request_of(const ReserveParams& p, int b) {
+    Request r;
+    int64_t kept = 0, own = 0;
+    r.source = source_of(p, b, &kept, &own);
+    r.bad = r.source < 0;
+    r.first = r.want = 0;
+    r.part = 0;
+    if (r.bad) return r;
+    const int64_t mask = (1 << p.page_shift) - 1, want = p.new_lens[b];
+    r.want = (want + mask) >> p.page_shift;
+    if (r.source != b) {
+        r.first = kept >> p.page_shift;
+        r.part = static_cast<int>(kept & mask);
+    } else if (want <= own) {
+        r.first = r.want;
+    } else {
+        r.first = (own + mask) >> p.page_shift;
+        const int page = own & mask ? p.last_page[b] : -1;
+        if (page >= 0 && (p.shared[page >> 5] >> (page & 31) & 1)) {
+            r.first = own >> p.page_shift;
+            r.part = static_cast<int>(own & mask);
+        }
+    }
+    return r;
+}
+
+__global__ void __launch_bounds__(kReserveThreads) reserve_clear_kernel(const ReserveParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = blockIdx.x * kReserveThreads + threadIdx.x; i < p.words; i += gridDim.x * kReserveThreads) {
+        p.used[i] = 0;
+        p.shared[i] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kReserveThreads) reserve_mark_kernel(const ReserveParams p, int blocks) {
+    constexpr int U = 4;
+    const int b = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t* row = p.page_table + b * p.pt_stride;
+    const int64_t room = p.pt_stride << p.page_shift;
+    int64_t len = p.seq_lens[b];
+    unsigned flags = 0;
+    if (!length_ok(p, len)) {
+        flags |= FDEC_DEVERR_SEQ_LEN;
+        len = len < 0 ? 0 : room;
+    }
+    const int64_t entries = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+    for (int64_t j0 = static_cast<int64_t>(blk) * kReserveThreads * U + threadIdx.x; j0 < entries;
+         j0 += static_cast<int64_t>(blocks) * kReserveThreads * U) {
+        int page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t j = j0 + u * kReserveThreads;
+            page[u] = j < entries ? row[j] : -2;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (page[u] == -2 && j0 + u * kReserveThreads >= entries) continue;
+            if (page[u] < 0 || page[u] >= p.num_pages) {
+                flags |= FDEC_DEVERR_PAGE_ID;
+                continue;
+            }
+            const unsigned bit = 1u << (page[u] & 31);
+            if (atomicOr(p.used + (page[u] >> 5), bit) & bit) atomicOr(p.shared + (page[u] >> 5), bit);
+        }
+    }
+    if (blk == 0 && threadIdx.x == 0) {
+        // the page that a copy would read: the rows of the call are written only after this launch
+        int64_t kept = 0, own = 0;
+        const int a = source_of(p, b, &kept, &own);
+        int page = -1;
+        if (a >= 0 && kept & ((1 << p.page_shift) - 1)) page = p.page_table[a * p.pt_stride + (kept >> p.page_shift)];
+        p.last_page[b] = page >= 0 && page < p.num_pages ? page : -1;
+    }
+    if (flags != 0 && p.err != nullptr) atomicOr(p.err, flags);
+}
+
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* s_part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) s_part[warp] = v;
+    __syncthreads();
+    int64_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kReserveThreads / 32; ++w) sum += s_part[w];
+    return sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kReserveThreads)
+    reserve_assign_kernel(const __grid_constant__ ReserveParams p, const __grid_constant__ CacheList<N> caches,
+                          int blocks) {
+    __shared__ int64_t s_part[kReserveThreads / 32];
+    __shared__ int s_page;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Request r = request_of(p, b);
+    if (blk == 0 && tid == 0 && r.bad && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
+    if (blk != 0 && (r.bad || r.part == 0 || r.need() == 0)) return;  // nothing to copy
+
+    int64_t start = 0;  // pages that the sequences before this one take
+    bool enough = true;
+    if (r.need() > 0) {
+        for (int i = tid; i < b; i += kReserveThreads) start += request_of(p, i).need();
+        start = block_sum(start, s_part);
+        // the free pages, a run of words for each thread
+        const int per = (p.words + kReserveThreads - 1) / kReserveThreads;
+        const int w0 = min(p.words, tid * per), w1 = min(p.words, w0 + per);
+        const auto free_bits = [&](int w) {
+            const int64_t behind = p.num_pages - static_cast<int64_t>(w) * 32;  // bits of the last word past the pool
+            return ~p.used[w] & (behind >= 32 ? 0xffffffffu : (1u << behind) - 1);
+        };
+        int64_t mine = 0;
+        for (int w = w0; w < w1; ++w) mine += __popc(free_bits(w));
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_part[warp] = upto;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kReserveThreads / 32; ++w) {
+            if (w < warp) upto += s_part[w];
+            total += s_part[w];
+        }
+        enough = start + r.need() <= total;
+        int64_t at = upto - mine;  // free pages before this thread's
+        if (enough && upto > start && at < start + r.need()) {
+            for (int w = w0; w < w1; ++w) {
+                unsigned bits = free_bits(w);
+                const int count = __popc(bits);
+                if (at + count > start) {
+                    for (; bits != 0 && at < start + r.need(); bits &= bits - 1, ++at) {
+                        if (at < start) continue;
+                        const int page = w * 32 + __ffs(bits) - 1;
+                        if (blk == 0) p.page_table[b * p.pt_stride + r.first + (at - start)] = page;
+                        if (at == start) s_page = page;
+                    }
+                    if (at >= start + r.need()) break;
+                } else {
+                    at += count;
+                }
+            }
+        }
+    }
+    if (blk == 0) {
+        if (tid == 0) {
+            p.granted[b] = r.bad || !enough ? p.seq_lens[b] : p.new_lens[b];
+            if (!enough && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_NO_PAGES);
+        }
+        if (!r.bad && enough && r.source != b)  // a fork shares the full pages
+            for (int64_t j = tid; j < r.first; j += kReserveThreads)
+                p.page_table[b * p.pt_stride + j] = p.page_table[r.source * p.pt_stride + j];
+    }
+    __syncthreads();
+    if (caches.n == 0 || r.bad || !enough || r.part == 0 || r.need() == 0) return;
+    const int of = p.last_page[b], page = s_page;
+    if (of < 0) return;  // (flagged as it was marked)
+    const CacheRows& c = cache_of(caches, blk);
+    const auto from = [&](int i) { return make_int2(of, i); };
+    const auto to = [&](int i) { return make_int2(page, i); };
+    if (c.wide)
+        move_columns<uint4>(c, blk, 0, r.part, from, to);
+    else
+        move_columns<uint2>(c, blk, 0, r.part, from, to);
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch(Kernel kernel, int64_t grid, cudaStream_t s, const Args&... args) {
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kReserveThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int N>
+cudaError_t launch_assign(const ReserveParams& p, const CacheList<kMaxCaches>& caches, cudaStream_t s) {
+    const int64_t blocks = std::max<int64_t>(1, column_blocks(caches));
+    return launch(reserve_assign_kernel<N>, blocks * p.batch, s, p, shorter<N>(caches), static_cast<int>(blocks));
+}
+
+}  // namespace
+
+cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCaches>& caches, int num_sms,
+                                 cudaStream_t s) {
+    const int64_t clear = std::min<int64_t>((p.words + kReserveThreads - 1) / kReserveThreads, num_sms * 4);
+    cudaError_t e = launch(reserve_clear_kernel, clear, s, p);
+    if (e != cudaSuccess) return e;
+    const int64_t row_blocks = (p.pt_stride + kReserveThreads * 4 - 1) / (kReserveThreads * 4);
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(row_blocks, num_sms * 16 / p.batch));
+    e = launch(reserve_mark_kernel, blocks * p.batch, s, p, static_cast<int>(blocks));
+    if (e != cudaSuccess) return e;
+    return caches.n <= 2 ? launch_assign<2>(p, caches, s) : launch_assign<kMaxCaches>(p, caches, s);
+}
+
+}  // namespace fdec

@@ -1,0 +1,478 @@
+// verify_drafts.cu -- verification of drafted tokens against the target's probabilities.
+//
+// The walk through a tree needs p and q at the children's tokens and, whenever a child
+// falls, the sum of what the target has left: W = sum_v max(p(v) - s q(v), 0).  After k
+// falls at one node the target left over is max(p - s q, 0) / W, because
+//   max(max(p - s q, 0) / W - q, 0) = max(p - (s + W) q, 0) / W      (q >= 0),
+// so one number s stands for all of them and every sum reads the same two rows.
+//
+// A cluster of CTAs takes one sequence; each warp sums a run of the vocabulary.  The first
+// CTA walks: it reads all children's p and q at once, decides, and tells the others
+// the next sum (node, s), or the run of the vocabulary in which the next token lies; they
+// send it their sums.  No CTA decides for itself, so they cannot disagree on how often they
+// meet.
+//
+// A token is the first whose cumulative weight passes u W, among 10^5 borders, so sums of
+// fp32 rounding would often give another token than exact ones.  Each term p - s q is
+// taken as a pair of fp32 values (Dekker's and Knuth's error-free sums and products) and
+// added up in pairs, about 46 bits, 20 fp32 instructions a term; fp64 units would need
+// 20 times as long.  Between warps and CTAs sums are fp64, in a fixed order.
+//
+// Bytes: the rows p and q of the last node, once from HBM.
+#include <algorithm>
+#include <cstdint>
+
+#include <cooperative_groups.h>
+
+#include "../../include/fdec.h"
+#include "device_utils.cuh"
+#include "fdec_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace fdec {
+
+namespace {
+
+constexpr int kVerifyWarps = 16;
+constexpr int kVerifyThreads = kVerifyWarps * 32;
+constexpr int kVerifyCluster = 8;  // CTAs of a sequence
+constexpr int kRuns = kVerifyCluster * kVerifyWarps;
+
+enum Op : int { kSum = 0, kDraw = 1, kStop = 2 };
+
+struct Order {       // what the first CTA tells the others
+    int op;
+    int node;        // whose rows
+    int run;         // kDraw: the warp's run of the vocabulary that holds the token
+    int place;       // kDraw: index in out_tokens
+    double s;        // weight of q
+    double target;   // kDraw: cumulative weight to pass, from the run's begin
+    uint64_t gone;   // without draft rows: children whose tokens have lost their weight
+};
+
+__device__ __forceinline__ float value(const float* p) { return *p; }
+__device__ __forceinline__ float value(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ void value4(const float* p, float (&v)[4]) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+__device__ __forceinline__ void value4(const __half* p, float (&v)[4]) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const float2 a = unpack2<false>(x.x), b = unpack2<false>(x.y);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+__device__ __forceinline__ void value4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const float2 a = unpack2<true>(x.x), b = unpack2<true>(x.y);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// A probability as it counts: in [0, 2], NaN as 0.
+__device__ __forceinline__ float bounded(float x, bool& bad) {
+    const float y = fminf(fmaxf(x, 0.f), 2.f);
+    bad |= !(y == x);
+    return y;
+}
+
+// A sum as a pair of fp32 values.
+struct Pair {
+    float hi = 0.f, lo = 0.f;
+    // + (x + e), e small against x
+    __device__ __forceinline__ void add(float x, float e) {
+        const float sum = __fadd_rn(hi, x);
+        const float back = __fsub_rn(sum, hi);
+        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, back)), __fsub_rn(x, back));
+        hi = sum;
+        lo = __fadd_rn(lo, __fadd_rn(err, e));
+    }
+    __device__ __forceinline__ double total() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+};
+
+// max(p - s q, 0) added to a sum, s = s_hi + s_lo.
+__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, float s_hi, float s_lo) {
+    const float t = __fmul_rn(s_hi, q);
+    const float te = __fmaf_rn(s_lo, q, __fmaf_rn(s_hi, q, -t));
+    float d = __fsub_rn(p, t);
+    float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), t), te);  // exact where p >= t, and else d < 0
+    if (!(__fadd_rn(d, e) > 0.f)) d = e = 0.f;
+    sum.add(d, e);
+}
+
+// What is left of the target at token v, in fp64.
+template <typename T>
+__device__ __forceinline__ double rest_at(const T* p, const T* q, int v, double s, const int* tokens, uint64_t gone) {
+    bool bad = false;
+    const double x = bounded(value(p + v), bad);
+    if (q != nullptr) return fmax(x - s * static_cast<double>(bounded(value(q + v), bad)), 0.0);
+    for (uint64_t m = gone; m != 0; m &= m - 1)
+        if (tokens[__ffsll(static_cast<long long>(m)) - 1] == v) return 0.0;
+    return x;
+}
+
+// One warp's sum over tokens [begin, end).
+template <typename T, bool VEC>
+__device__ __forceinline__ double run_sum(const T* p, const T* q, int begin, int end, double s, const int* tokens,
+                                          uint64_t gone, bool& bad) {
+    const int lane = threadIdx.x & 31;
+    Pair sum;
+    if (q == nullptr && gone != 0) {
+        bool hit = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 32 * h;
+            hit |= (gone >> i & 1) && tokens[i] >= begin && tokens[i] < end;
+        }
+        if (__any_sync(0xffffffffu, hit)) {  // a token without weight lies in here
+            for (int v = begin + lane; v < end; v += 32) {
+                const float x = static_cast<float>(rest_at<T>(p, nullptr, v, 0.0, tokens, gone));
+                sum.add(x, 0.f);
+            }
+            return sum.total();
+        }
+    }
+    const float s_hi = static_cast<float>(s), s_lo = static_cast<float>(s - static_cast<double>(s_hi));
+    if constexpr (VEC) {
+        constexpr int U = 4;
+        for (int v0 = begin + lane * 4; v0 < end; v0 += U * 128) {
+            float a[U][4], c[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * 128;
+                a[u][0] = a[u][1] = a[u][2] = a[u][3] = 0.f;
+                c[u][0] = c[u][1] = c[u][2] = c[u][3] = 0.f;
+                if (v < end) {
+                    value4(p + v, a[u]);
+                    if (q != nullptr) value4(q + v, c[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = bounded(a[u][k], bad);
+                    if (q != nullptr)
+                        add_rest(sum, x, bounded(c[u][k], bad), s_hi, s_lo);
+                    else
+                        sum.add(x, 0.f);
+                }
+        }
+    } else {
+        constexpr int U = 8;
+        for (int v0 = begin + lane; v0 < end; v0 += U * 32) {
+            float a[U], c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * 32;
+                a[u] = v < end ? value(p + v) : 0.f;
+                c[u] = v < end && q != nullptr ? value(q + v) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float x = bounded(a[u], bad);
+                if (q != nullptr)
+                    add_rest(sum, x, bounded(c[u], bad), s_hi, s_lo);
+                else
+                    sum.add(x, 0.f);
+            }
+        }
+    }
+    return sum.total();
+}
+
+__device__ __forceinline__ double warp_sum_double(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const VerifyParams p) {
+    __shared__ int s_tok[kMaxNodes], s_par[kMaxNodes], s_path[kMaxNodes];
+    __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes];
+    __shared__ double s_sum[kRuns];       // the first CTA's: every warp's sum
+    __shared__ double s_warp[kVerifyWarps];
+    __shared__ int s_first, s_last;
+    __shared__ Order s_order;
+
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int b = blockIdx.x / kVerifyCluster;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int N = p.nodes;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
+
+    const T* target = static_cast<const T*>(p.target) + static_cast<int64_t>(b) * p.t_seq;
+    const T* draft = p.draft != nullptr ? static_cast<const T*>(p.draft) + static_cast<int64_t>(b) * p.d_seq : nullptr;
+    unsigned flags = 0;
+    int n = p.node_counts != nullptr ? p.node_counts[b] : N;
+    if (n < 0 || n > N) {
+        flags |= FDEC_DEVERR_SEQ_LEN;
+        n = min(max(n, 0), N);
+    }
+    if (tid < kMaxNodes) {
+        const int64_t at = static_cast<int64_t>(b) * N + tid;
+        s_tok[tid] = tid < n && tid > 0 ? p.tokens[at] : -1;
+        if (rank == 0) {
+            int par = tid - 1;
+            if (p.parents != nullptr) par = tid < n ? p.parents[at] : -1;
+            if (par < -1 || par >= tid) {
+                flags |= FDEC_DEVERR_TREE;
+                par = -1;
+            }
+            float u = tid < n ? p.uniforms[at] : 0.f;
+            u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
+            float pv = 0.f, qv = 1.f;
+            if (tid > 0 && tid < n && par >= 0) {
+                const int t = s_tok[tid];
+                if (t < 0 || t >= p.vocab) {
+                    flags |= FDEC_DEVERR_TREE;
+                    par = -1;
+                } else {
+                    bool bad = false;
+                    pv = bounded(value(target + par * p.t_node + t), bad);
+                    if (draft != nullptr) qv = bounded(value(draft + par * p.d_node + t), bad);
+                    if (bad) flags |= FDEC_DEVERR_PROB;
+                }
+            }
+            s_par[tid] = tid < n ? par : -1;
+            s_p[tid] = pv;
+            s_q[tid] = qv;
+            s_u[tid] = u;
+        }
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // and so do the others, whose memory is written next
+
+    // the walk's state, the same in every lane of the first CTA's first warp
+    int x = 0, len = 1;
+    double s = 0.0, W = 1.0;
+    uint64_t gone = 0, left = 0;
+    bool summed = false, whole = false;  // W is the sum of (x, s, gone); of the target's row itself
+    int par0 = -1, par1 = -1, tok0 = -1, tok1 = -1;
+    const bool walks = rank == 0 && warp == 0;
+    const auto children = [&](int node) {
+        return static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == node)) |
+               static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
+    };
+    if (walks) {
+        par0 = s_par[lane], par1 = s_par[lane + 32];
+        tok0 = s_tok[lane], tok1 = s_tok[lane + 32];
+        left = children(0);
+        if (lane == 0) s_path[0] = 0;
+    }
+
+    for (int round = 0; round < kMaxNodes + 3; ++round) {  // (a sum for every node, and two for the draw)
+        if (walks) {
+            Order o;
+            o.op = kStop;
+            o.node = o.run = o.place = 0;
+            o.s = o.target = 0.0;
+            o.gone = 0;
+            if (n > 0) {
+                if (round > 0) {  // the sums that were asked for
+                    constexpr int PER = (kRuns + 31) / 32;
+                    double mine[PER], part = 0.0;
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) part += mine[k] = s_sum[lane * PER + k];
+                    const double upto = warp_scan_double(part);
+                    W = __shfl_sync(0xffffffffu, upto, 31);
+                    summed = true;
+                    if (!(W > 0.0)) left = 0;
+                    if (left == 0 && W > 0.0) {  // draw
+                        const double goal = static_cast<double>(s_u[0]) * W;
+                        int run = -1, last = -1;
+                        double at = upto - part, from = 0.0;
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            if (mine[k] > 0.0) last = lane * PER + k;
+                            if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
+                                run = lane * PER + k;
+                                from = at;
+                            }
+                            at += mine[k];
+                        }
+                        unsigned found = __ballot_sync(0xffffffffu, run >= 0);
+                        o.op = kDraw;
+                        if (found != 0) {
+                            const int who = __ffs(found) - 1;
+                            o.run = __shfl_sync(0xffffffffu, run, who);
+                            o.target = goal - __shfl_sync(0xffffffffu, from, who);
+                        } else {  // (only by rounding: the last run with weight, its last token)
+                            found = __ballot_sync(0xffffffffu, last >= 0);
+                            o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(found));
+                            o.target = 4.0 * W;
+                        }
+                    }
+                }
+                if (o.op != kDraw) {
+                    bool ask = false;
+                    while (left != 0 && !ask) {
+                        const int c = __ffsll(static_cast<long long>(left)) - 1;
+                        left &= left - 1;
+                        const int t = s_tok[c];
+                        double rest = s_p[c];
+                        if (draft != nullptr) {
+                            rest = fmax(rest - s * static_cast<double>(s_q[c]), 0.0);
+                        } else {
+                            const uint64_t same =
+                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok0 == t)) |
+                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok1 == t)) << 32;
+                            if (same & gone) rest = 0.0;
+                        }
+                        if (static_cast<double>(s_u[c]) * W * static_cast<double>(s_q[c]) < rest) {
+                            x = c;
+                            if (lane == 0) s_path[len] = c;
+                            ++len;
+                            s = 0.0, W = 1.0, gone = 0, summed = false;
+                            left = children(c);
+                        } else {
+                            s += W;
+                            gone |= uint64_t{1} << c;
+                            ask = true;
+                        }
+                    }
+                    if (!ask && summed) {  // nothing is left: the target's row itself, if that is not it already
+                        ask = !whole;
+                        whole = true;
+                        s = 0.0, gone = 0;
+                    } else if (!ask) {
+                        ask = whole = true;  // no child has fallen here
+                    }
+                    if (ask) o.op = kSum;
+                }
+                o.node = x;
+                o.s = s;
+                o.gone = gone;
+                o.place = len - 1;
+            }
+            for (int r = lane; r < kVerifyCluster; r += 32) *cluster.map_shared_rank(&s_order, r) = o;
+        }
+        cluster.sync();
+        const Order o = s_order;
+        if (o.op != kSum) break;
+        const T* prow = target + o.node * p.t_node;
+        // (the target's row itself needs no q; a leaf has none)
+        const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
+        const int run = rank * kVerifyWarps + warp;
+        const int64_t begin = static_cast<int64_t>(run) * p.chunk;
+        double sum = 0.0;
+        bool bad = false;
+        if (begin < p.vocab) {
+            const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
+            sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_tok, o.gone, bad);
+            sum = warp_sum_double(sum);
+        }
+        if (bad) flags |= FDEC_DEVERR_PROB;
+        if (lane == 0) cluster.map_shared_rank(s_sum, 0)[run] = sum;
+        cluster.sync();
+    }
+
+    const Order o = s_order;
+    const int64_t out = static_cast<int64_t>(b) * N;
+    if (rank == 0) {
+        if (tid < N) {  // (len is the first warp's: the order's place tells the others)
+            const int steps = n > 0 ? o.place + 1 : 0;
+            p.path[out + tid] = tid < steps ? s_path[tid] : -1;
+            if (tid + 1 < steps)
+                p.out_tokens[out + tid] = s_tok[s_path[tid + 1]];
+            else if (o.op != kDraw || tid != o.place)
+                p.out_tokens[out + tid] = -1;
+            if (tid == 0) p.path_lens[b] = steps;
+        }
+        if (n > 0 && o.op != kDraw) flags |= FDEC_DEVERR_PROB;
+    }
+    if (o.op == kDraw && o.run / kVerifyWarps == rank) {
+        // the run's tokens, a stretch for each thread in their order
+        const T* prow = target + o.node * p.t_node;
+        const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
+        const int64_t begin = static_cast<int64_t>(o.run) * p.chunk;
+        const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
+        const int per = (p.chunk + kVerifyThreads - 1) / kVerifyThreads;
+        const int v0 = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(tid) * per));
+        const int v1 = min(end, v0 + per);
+        double mine = 0.0;
+        for (int v = v0; v < v1; ++v) mine += rest_at<T>(prow, qrow, v, o.s, s_tok, o.gone);
+        double upto = warp_scan_double(mine);
+        if (lane == 31) s_warp[warp] = upto;
+        if (tid == 0) {
+            s_first = kVerifyThreads;
+            s_last = -1;
+        }
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) upto += s_warp[k];
+        if (mine > 0.0) {
+            if (upto > o.target) atomicMin(&s_first, tid);
+            atomicMax(&s_last, tid);
+        }
+        __syncthreads();
+        if (tid == (s_first < kVerifyThreads ? s_first : s_last)) {
+            double at = upto - mine;
+            int token = -1;
+            for (int v = v0; v < v1; ++v) {
+                const double r = rest_at<T>(prow, qrow, v, o.s, s_tok, o.gone);
+                if (r > 0.0) token = v;
+                at += r;
+                if (r > 0.0 && at > o.target) break;
+            }
+            p.out_tokens[out + o.place] = token;
+        }
+    }
+    if (flags != 0 && p.err != nullptr) atomicOr(p.err, flags);
+}
+
+template <typename T>
+bool vectors(const VerifyParams& p) {
+    const auto ok = [](const void* base, int64_t a, int64_t b) {
+        return reinterpret_cast<uintptr_t>(base) % (4 * sizeof(T)) == 0 && a % 4 == 0 && b % 4 == 0;
+    };
+    return p.vocab % 4 == 0 && ok(p.target, p.t_seq, p.t_node) && ok(p.draft, p.d_seq, p.d_node);
+}
+
+template <typename T>
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * kVerifyCluster, 1, 1);
+    cfg.blockDim = dim3(kVerifyThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kVerifyCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return vectors<T>(p) ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, true>, p)
+                         : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_verify_drafts(VerifyParams p, int prob_dtype, int num_sms, cudaStream_t s) {
+    (void)num_sms;
+    p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
+    switch (prob_dtype) {
+        case FDEC_PROB_F16: return launch_verify<__half>(p, s);
+        case FDEC_PROB_BF16: return launch_verify<__nv_bfloat16>(p, s);
+        case FDEC_PROB_F32: return launch_verify<float>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fdec
