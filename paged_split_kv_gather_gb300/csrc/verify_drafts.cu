@@ -34,7 +34,7 @@ namespace fdec {
 
 namespace {
 
-constexpr int kVerifyWarps = 16;
+constexpr int kVerifyWarps = 8;
 constexpr int kVerifyThreads = kVerifyWarps * 32;
 constexpr int kVerifyCluster = 8;  // CTAs of a sequence
 constexpr int kRuns = kVerifyCluster * kVerifyWarps;
@@ -101,15 +101,20 @@ __device__ __forceinline__ void add_rest(Pair& sum, float p, float q, float s_hi
     sum.add(d, e);
 }
 
-// What is left of the target at token v, in fp64.
-template <typename T>
-__device__ __forceinline__ double rest_at(const T* p, const T* q, int v, double s, const int* tokens, uint64_t gone) {
-    bool bad = false;
-    const double x = bounded(value(p + v), bad);
-    if (q != nullptr) return fmax(x - s * static_cast<double>(bounded(value(q + v), bad)), 0.0);
+// Whether token v is that of one of the children `gone`.
+__device__ __forceinline__ bool is_gone(int v, const int* tokens, uint64_t gone) {
     for (uint64_t m = gone; m != 0; m &= m - 1)
-        if (tokens[__ffsll(static_cast<long long>(m)) - 1] == v) return 0.0;
-    return x;
+        if (tokens[__ffsll(static_cast<long long>(m)) - 1] == v) return true;
+    return false;
+}
+
+// What is left of the target at token v, in fp64.
+__device__ __forceinline__ double rest_of(float p, float q, bool drafted, int v, double s, const int* tokens,
+                                          uint64_t gone) {
+    bool bad = false;
+    const double x = bounded(p, bad);
+    if (drafted) return fmax(x - s * static_cast<double>(bounded(q, bad)), 0.0);
+    return is_gone(v, tokens, gone) ? 0.0 : x;
 }
 
 // One warp's sum over tokens [begin, end).
@@ -126,9 +131,16 @@ __device__ __forceinline__ double run_sum(const T* p, const T* q, int begin, int
             hit |= (gone >> i & 1) && tokens[i] >= begin && tokens[i] < end;
         }
         if (__any_sync(0xffffffffu, hit)) {  // a token without weight lies in here
-            for (int v = begin + lane; v < end; v += 32) {
-                const float x = static_cast<float>(rest_at<T>(p, nullptr, v, 0.0, tokens, gone));
-                sum.add(x, 0.f);
+            constexpr int U = 8;
+            for (int v0 = begin + lane; v0 < end; v0 += U * 32) {
+                float a[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) a[u] = v0 + u * 32 < end ? value(p + v0 + u * 32) : 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float x = bounded(a[u], bad);
+                    sum.add(is_gone(v0 + u * 32, tokens, gone) ? 0.f : x, 0.f);
+                }
             }
             return sum.total();
         }
@@ -198,13 +210,174 @@ __device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
     return v;
 }
 
+// The walk of the first CTA.
+struct Walk {
+    double sum[kRuns];  // every warp's sum
+    int tok[kMaxNodes], par[kMaxNodes], path[kMaxNodes];
+    float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // at each node's token, in its parent's rows; its random number
+    double s, W;
+    // Without draft rows: the target's row is summed once, and a token that falls is taken from that sum.  The
+    // difference keeps the sum's absolute error, so that where it is small (exact) the row is summed without the tokens.
+    double row_total, row_gone;
+    uint64_t weighed;   // the children whose tokens make up row_gone, each token once
+    uint64_t gone, left;  // children that have fallen, that are still to try
+    int x, len;
+    bool have_row, exact;
+    bool whole;  // the target's row itself is summed, whatever has fallen
+};
+
+// What comes next: the first CTA's first warp, after the sums that were asked for have come (sums).
+__device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool drafted, int chunk) {
+    const int lane = threadIdx.x & 31;
+    constexpr int PER = (kRuns + 31) / 32;
+    const int par0 = walk.par[lane], par1 = walk.par[lane + 32];
+    const int tok0 = walk.tok[lane], tok1 = walk.tok[lane + 32];
+    const auto children = [&](int node) {
+        return static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == node)) |
+               static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
+    };
+    int x = 0, len = 1;
+    double s = 0.0, W = 1.0, row_total = 0.0, row_gone = 0.0;
+    uint64_t gone = 0, left = 0, weighed = 0;
+    bool have_row = false, exact = false, summed = false, whole = false;
+    if (sums) {
+        x = walk.x, len = walk.len;
+        s = walk.s, W = walk.W, row_total = walk.row_total, row_gone = walk.row_gone;
+        gone = walk.gone, left = walk.left, weighed = walk.weighed;
+        have_row = walk.have_row, exact = walk.exact, whole = walk.whole;
+    } else {
+        left = children(0);
+        if (lane == 0) walk.path[0] = 0;
+    }
+    double mine[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) mine[k] = 0.0;
+    Order o;
+    o.op = kStop;
+    o.node = o.run = o.place = 0;
+    o.s = o.target = 0.0;
+    o.gone = 0;
+    if (n > 0) {
+        bool ask = false;
+        if (sums) {  // the sums that were asked for
+            double part = 0.0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) part += mine[k] = walk.sum[lane * PER + k];
+            W = __shfl_sync(0xffffffffu, warp_scan_double(part), 31);
+            summed = true;
+            if (!drafted && !exact && !whole) {
+                row_total = W;
+                have_row = true;
+                W = row_total - row_gone;
+                if (!(W * 64.0 > row_total)) ask = exact = true;
+            }
+            if (!ask && !(W > 0.0)) left = 0;
+        }
+        while (left != 0 && !ask) {
+            const int c = __ffsll(static_cast<long long>(left)) - 1;
+            left &= left - 1;
+            const int t = walk.tok[c];
+            double rest = walk.p[c];
+            if (drafted) {
+                rest = fmax(rest - s * static_cast<double>(walk.q[c]), 0.0);
+            } else {
+                const uint64_t same = static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok0 == t)) |
+                                      static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok1 == t)) << 32;
+                if (same & gone) rest = 0.0;
+            }
+            if (static_cast<double>(walk.u[c]) * W * static_cast<double>(walk.q[c]) < rest) {
+                x = c;
+                if (lane == 0) walk.path[len] = c;
+                ++len;
+                s = 0.0, W = 1.0, gone = 0, summed = false;
+                row_gone = 0.0, weighed = 0, have_row = exact = false;
+                left = children(c);
+            } else {
+                s += W;
+                gone |= uint64_t{1} << c;
+                if (!drafted && rest > 0.0) {
+                    row_gone += rest;
+                    weighed |= uint64_t{1} << c;
+                }
+                if (!drafted && have_row && !exact && (row_total - row_gone) * 64.0 > row_total)
+                    W = row_total - row_gone;
+                else
+                    ask = true;
+                if (ask && have_row) exact = true;
+            }
+        }
+        if (!ask && summed && W > 0.0) {  // no child stands: draw
+            o.op = kDraw;
+            if (!drafted && !exact && !whole) {
+                for (uint64_t m = weighed; m != 0; m &= m - 1) {
+                    const int c = __ffsll(static_cast<long long>(m)) - 1;
+                    const int run = walk.tok[c] / chunk;
+#pragma unroll
+                    for (int k = 0; k < PER; ++k)
+                        if (run == lane * PER + k) {
+                            const double rest = mine[k] - static_cast<double>(walk.p[c]);
+                            mine[k] = rest > mine[k] * 0x1p-42 ? rest : 0.0;  // (what rounding left is nothing)
+                        }
+                }
+            }
+            double part = 0.0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) part += mine[k];
+            const double upto = warp_scan_double(part);
+            const double goal = static_cast<double>(walk.u[0]) * __shfl_sync(0xffffffffu, upto, 31);
+            int run = -1, last = -1;
+            double at = upto - part, from = 0.0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                if (mine[k] > 0.0) last = lane * PER + k;
+                if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
+                    run = lane * PER + k;
+                    from = at;
+                }
+                at += mine[k];
+            }
+            const unsigned found = __ballot_sync(0xffffffffu, run >= 0);
+            const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
+            if (found != 0) {
+                const int who = __ffs(found) - 1;
+                o.run = __shfl_sync(0xffffffffu, run, who);
+                o.target = goal - __shfl_sync(0xffffffffu, from, who);
+            } else if (any != 0) {  // (only by rounding: the last run with weight, its last token)
+                o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
+                o.target = 4.0 * W;
+            }
+        } else if (!ask) {
+            if (summed) {  // nothing is left: the target's row itself, if that is not it already
+                ask = !whole;
+                s = 0.0, gone = 0;
+            } else {  // no child has fallen here
+                ask = true;
+            }
+            whole = true;
+        }
+        if (ask) o.op = kSum;
+        o.node = x;
+        o.s = s;
+        // (a plain sum of the row first; without its tokens where it must be exact)
+        o.gone = o.op == kSum && !exact ? 0 : gone;
+        o.place = len - 1;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        walk.x = x, walk.len = len;
+        walk.s = s, walk.W = W, walk.row_total = row_total, walk.row_gone = row_gone;
+        walk.gone = gone, walk.left = left, walk.weighed = weighed;
+        walk.have_row = have_row, walk.exact = exact, walk.whole = whole;
+    }
+    __syncwarp();
+    return o;
+}
+
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const VerifyParams p) {
-    __shared__ int s_tok[kMaxNodes], s_par[kMaxNodes], s_path[kMaxNodes];
-    __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes];
-    __shared__ double s_sum[kRuns];       // the first CTA's: every warp's sum
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const VerifyParams p) {
+    __shared__ Walk s_walk;  // the first CTA's
     __shared__ double s_warp[kVerifyWarps];
-    __shared__ int s_first, s_last;
+    __shared__ int s_first, s_last, s_any;
     __shared__ Order s_order;
 
     cg::cluster_group cluster = cg::this_cluster();
@@ -221,25 +394,32 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
     const T* draft = p.draft != nullptr ? static_cast<const T*>(p.draft) + static_cast<int64_t>(b) * p.d_seq : nullptr;
     unsigned flags = 0;
     int n = p.node_counts != nullptr ? p.node_counts[b] : N;
+    int par = tid - 1, tok = -1;
+    float u = 0.f;
+    if (tid < N) {  // (read before n is there)
+        const int64_t at = static_cast<int64_t>(b) * N + tid;
+        tok = p.tokens[at];
+        if (rank == 0) {
+            if (p.parents != nullptr) par = p.parents[at];
+            u = p.uniforms[at];
+        }
+    }
     if (n < 0 || n > N) {
         flags |= FDEC_DEVERR_SEQ_LEN;
         n = min(max(n, 0), N);
     }
     if (tid < kMaxNodes) {
-        const int64_t at = static_cast<int64_t>(b) * N + tid;
-        s_tok[tid] = tid < n && tid > 0 ? p.tokens[at] : -1;
+        s_walk.tok[tid] = tid < n && tid > 0 ? tok : -1;
         if (rank == 0) {
-            int par = tid - 1;
-            if (p.parents != nullptr) par = tid < n ? p.parents[at] : -1;
+            if (tid >= n) par = -1;
             if (par < -1 || par >= tid) {
                 flags |= FDEC_DEVERR_TREE;
                 par = -1;
             }
-            float u = tid < n ? p.uniforms[at] : 0.f;
             u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
             float pv = 0.f, qv = 1.f;
             if (tid > 0 && tid < n && par >= 0) {
-                const int t = s_tok[tid];
+                const int t = tok;
                 if (t < 0 || t >= p.vocab) {
                     flags |= FDEC_DEVERR_TREE;
                     par = -1;
@@ -250,117 +430,22 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
                     if (bad) flags |= FDEC_DEVERR_PROB;
                 }
             }
-            s_par[tid] = tid < n ? par : -1;
-            s_p[tid] = pv;
-            s_q[tid] = qv;
-            s_u[tid] = u;
+            s_walk.par[tid] = tid < n ? par : -1;
+            s_walk.p[tid] = pv;
+            s_walk.q[tid] = qv;
+            s_walk.u[tid] = u;
         }
     }
     __syncthreads();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // and so do the others, whose memory is written next
 
-    // the walk's state, the same in every lane of the first CTA's first warp
-    int x = 0, len = 1;
-    double s = 0.0, W = 1.0;
-    uint64_t gone = 0, left = 0;
-    bool summed = false, whole = false;  // W is the sum of (x, s, gone); of the target's row itself
-    int par0 = -1, par1 = -1, tok0 = -1, tok1 = -1;
     const bool walks = rank == 0 && warp == 0;
-    const auto children = [&](int node) {
-        return static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == node)) |
-               static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
-    };
-    if (walks) {
-        par0 = s_par[lane], par1 = s_par[lane + 32];
-        tok0 = s_tok[lane], tok1 = s_tok[lane + 32];
-        left = children(0);
-        if (lane == 0) s_path[0] = 0;
-    }
 
-    for (int round = 0; round < kMaxNodes + 3; ++round) {  // (a sum for every node, and two for the draw)
+    // (at most two sums for every child and two for the draw)
+    for (int round = 0; round < 2 * kMaxNodes + 3; ++round) {
         if (walks) {
-            Order o;
-            o.op = kStop;
-            o.node = o.run = o.place = 0;
-            o.s = o.target = 0.0;
-            o.gone = 0;
-            if (n > 0) {
-                if (round > 0) {  // the sums that were asked for
-                    constexpr int PER = (kRuns + 31) / 32;
-                    double mine[PER], part = 0.0;
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) part += mine[k] = s_sum[lane * PER + k];
-                    const double upto = warp_scan_double(part);
-                    W = __shfl_sync(0xffffffffu, upto, 31);
-                    summed = true;
-                    if (!(W > 0.0)) left = 0;
-                    if (left == 0 && W > 0.0) {  // draw
-                        const double goal = static_cast<double>(s_u[0]) * W;
-                        int run = -1, last = -1;
-                        double at = upto - part, from = 0.0;
-#pragma unroll
-                        for (int k = 0; k < PER; ++k) {
-                            if (mine[k] > 0.0) last = lane * PER + k;
-                            if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
-                                run = lane * PER + k;
-                                from = at;
-                            }
-                            at += mine[k];
-                        }
-                        unsigned found = __ballot_sync(0xffffffffu, run >= 0);
-                        o.op = kDraw;
-                        if (found != 0) {
-                            const int who = __ffs(found) - 1;
-                            o.run = __shfl_sync(0xffffffffu, run, who);
-                            o.target = goal - __shfl_sync(0xffffffffu, from, who);
-                        } else {  // (only by rounding: the last run with weight, its last token)
-                            found = __ballot_sync(0xffffffffu, last >= 0);
-                            o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(found));
-                            o.target = 4.0 * W;
-                        }
-                    }
-                }
-                if (o.op != kDraw) {
-                    bool ask = false;
-                    while (left != 0 && !ask) {
-                        const int c = __ffsll(static_cast<long long>(left)) - 1;
-                        left &= left - 1;
-                        const int t = s_tok[c];
-                        double rest = s_p[c];
-                        if (draft != nullptr) {
-                            rest = fmax(rest - s * static_cast<double>(s_q[c]), 0.0);
-                        } else {
-                            const uint64_t same =
-                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok0 == t)) |
-                                static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok1 == t)) << 32;
-                            if (same & gone) rest = 0.0;
-                        }
-                        if (static_cast<double>(s_u[c]) * W * static_cast<double>(s_q[c]) < rest) {
-                            x = c;
-                            if (lane == 0) s_path[len] = c;
-                            ++len;
-                            s = 0.0, W = 1.0, gone = 0, summed = false;
-                            left = children(c);
-                        } else {
-                            s += W;
-                            gone |= uint64_t{1} << c;
-                            ask = true;
-                        }
-                    }
-                    if (!ask && summed) {  // nothing is left: the target's row itself, if that is not it already
-                        ask = !whole;
-                        whole = true;
-                        s = 0.0, gone = 0;
-                    } else if (!ask) {
-                        ask = whole = true;  // no child has fallen here
-                    }
-                    if (ask) o.op = kSum;
-                }
-                o.node = x;
-                o.s = s;
-                o.gone = gone;
-                o.place = len - 1;
-            }
+            __syncwarp();
+            const Order o = next_order(s_walk, n, round > 0, draft != nullptr, p.chunk);
             for (int r = lane; r < kVerifyCluster; r += 32) *cluster.map_shared_rank(&s_order, r) = o;
         }
         cluster.sync();
@@ -375,11 +460,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
         bool bad = false;
         if (begin < p.vocab) {
             const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
-            sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_tok, o.gone, bad);
+            sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tok, o.gone, bad);
             sum = warp_sum_double(sum);
         }
         if (bad) flags |= FDEC_DEVERR_PROB;
-        if (lane == 0) cluster.map_shared_rank(s_sum, 0)[run] = sum;
+        if (lane == 0) cluster.map_shared_rank(&s_walk, 0)->sum[run] = sum;
         cluster.sync();
     }
 
@@ -388,9 +473,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
     if (rank == 0) {
         if (tid < N) {  // (len is the first warp's: the order's place tells the others)
             const int steps = n > 0 ? o.place + 1 : 0;
-            p.path[out + tid] = tid < steps ? s_path[tid] : -1;
+            p.path[out + tid] = tid < steps ? s_walk.path[tid] : -1;
             if (tid + 1 < steps)
-                p.out_tokens[out + tid] = s_tok[s_path[tid + 1]];
+                p.out_tokens[out + tid] = s_walk.tok[s_walk.path[tid + 1]];
             else if (o.op != kDraw || tid != o.place)
                 p.out_tokens[out + tid] = -1;
             if (tid == 0) p.path_lens[b] = steps;
@@ -406,13 +491,25 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
         const int per = (p.chunk + kVerifyThreads - 1) / kVerifyThreads;
         const int v0 = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(tid) * per));
         const int v1 = min(end, v0 + per);
+        constexpr int U = 8;
         double mine = 0.0;
-        for (int v = v0; v < v1; ++v) mine += rest_at<T>(prow, qrow, v, o.s, s_tok, o.gone);
+        for (int v = v0; v < v1; v += U) {
+            float a[U], c[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                a[k] = v + k < v1 ? value(prow + v + k) : 0.f;
+                c[k] = v + k < v1 && qrow != nullptr ? value(qrow + v + k) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (v + k < v1) mine += rest_of(a[k], c[k], qrow != nullptr, v + k, o.s, s_walk.tok, o.gone);
+        }
         double upto = warp_scan_double(mine);
         if (lane == 31) s_warp[warp] = upto;
         if (tid == 0) {
             s_first = kVerifyThreads;
             s_last = -1;
+            s_any = p.vocab;
         }
         __syncthreads();
         for (int k = 0; k < warp; ++k) upto += s_warp[k];
@@ -425,12 +522,21 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
             double at = upto - mine;
             int token = -1;
             for (int v = v0; v < v1; ++v) {
-                const double r = rest_at<T>(prow, qrow, v, o.s, s_tok, o.gone);
+                const double r = rest_of(value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, o.s,
+                                         s_walk.tok, o.gone);
                 if (r > 0.0) token = v;
                 at += r;
                 if (r > 0.0 && at > o.target) break;
             }
             p.out_tokens[out + o.place] = token;
+        }
+        if (s_last < 0) {  // (only by rounding: the run has no weight after all; the first token that has some)
+            for (int v = tid; v < p.vocab; v += kVerifyThreads)
+                if (rest_of(value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, o.s, s_walk.tok, o.gone) >
+                    0.0)
+                    atomicMin(&s_any, v);
+            __syncthreads();
+            if (tid == 0) p.out_tokens[out + o.place] = s_any < p.vocab ? s_any : -1;
         }
     }
     if (flags != 0 && p.err != nullptr) atomicOr(p.err, flags);
