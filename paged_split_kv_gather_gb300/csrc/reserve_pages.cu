@@ -165,47 +165,56 @@ __global__ void __launch_bounds__(kReserveThreads)
     if (r.need() > 0) {
         for (int i = tid; i < b; i += kReserveThreads) start += request_of(p, i).need();
         start = block_sum(start, s_part);
-        // the free pages, a run of words for each thread
-        const int per = (p.words + kReserveThreads - 1) / kReserveThreads;
-        const int w0 = min(p.words, tid * per), w1 = min(p.words, w0 + per);
+        // The free pages: a run of words for each warp.  First their number, then, in the runs that hold this
+        // sequence's, page by page.
+        constexpr int kWarps = kReserveThreads / 32, U = 4;
+        const int per = ((p.words + kWarps - 1) / kWarps + 127) / 128 * 128;  // words of a warp
+        const int w0 = min(p.words, warp * per), w1 = min(p.words, w0 + per);
         const auto free_bits = [&](int w) {
             const int64_t behind = p.num_pages - static_cast<int64_t>(w) * 32;  // bits of the last word past the pool
-            return ~p.used[w] & (behind >= 32 ? 0xffffffffu : (1u << behind) - 1);
+            return w < w1 ? ~p.used[w] & (behind >= 32 ? 0xffffffffu : (1u << behind) - 1) : 0u;
         };
-        int64_t mine = 0;
-        for (int w = w0; w < w1; ++w) mine += __popc(free_bits(w));
-        int64_t upto = mine;
+        int mine = 0;  // (at most 2^26)
+        for (int w = w0 + lane; w < w1; w += 32 * U * 2) {
+            unsigned bits[2 * U];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int u = 0; u < 2 * U; ++u) bits[u] = free_bits(w + 32 * u);
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) mine += __popc(bits[u]);
         }
+        mine = __reduce_add_sync(0xffffffffu, mine);
         __syncthreads();
-        if (lane == 31) s_part[warp] = upto;
+        if (lane == 0) s_part[warp] = mine;
         __syncthreads();
-        int64_t total = 0;
+        int64_t total = 0, at = 0;  // free pages; those before this warp's run
 #pragma unroll
-        for (int w = 0; w < kReserveThreads / 32; ++w) {
-            if (w < warp) upto += s_part[w];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += s_part[w];
             total += s_part[w];
         }
-        enough = start + r.need() <= total;
-        int64_t at = upto - mine;  // free pages before this thread's
-        if (enough && upto > start && at < start + r.need()) {
-            for (int w = w0; w < w1; ++w) {
-                unsigned bits = free_bits(w);
+        const int64_t end = start + r.need();
+        enough = end <= total;
+        if (enough && at < end && at + mine > start) {
+            for (int w = w0; w < w1 && at < end; w += 32) {
+                unsigned bits = free_bits(w + lane);
                 const int count = __popc(bits);
-                if (at + count > start) {
-                    for (; bits != 0 && at < start + r.need(); bits &= bits - 1, ++at) {
-                        if (at < start) continue;
-                        const int page = w * 32 + __ffs(bits) - 1;
-                        if (blk == 0) p.page_table[b * p.pt_stride + r.first + (at - start)] = page;
-                        if (at == start) s_page = page;
+                const int all = __reduce_add_sync(0xffffffffu, count);
+                if (at + all > start) {
+                    int upto = count;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += y;
                     }
-                    if (at >= start + r.need()) break;
-                } else {
-                    at += count;
+                    int64_t i = at + upto - count;
+                    for (; bits != 0 && i < end; bits &= bits - 1, ++i) {
+                        if (i < start) continue;
+                        const int page = (w + lane) * 32 + __ffs(bits) - 1;
+                        if (blk == 0) p.page_table[b * p.pt_stride + r.first + (i - start)] = page;
+                        if (i == start) s_page = page;
+                    }
                 }
+                at += all;
             }
         }
     }
