@@ -253,6 +253,20 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
         const int keys = min(n, (min(T * 16 + 15, R - 1)) / g + 1);  // no node sees a later one
         const int nt = (keys + 7) >> 3;
 
+        // the prefix's rows, 64 columns ahead of their use: the first block while S is computed
+        float2 op[2][8];
+        const auto load_prefix = [&](int cb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool has = p.o_prefix != nullptr && lse2[h] != -INFINITY;
+                const float* at = p.o_prefix + row[h] * D + cb * 64 + 2 * t;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    op[h][j] = has ? *reinterpret_cast<const float2*>(at + j * 8) : make_float2(0.f, 0.f);
+            }
+        };
+        load_prefix(0);
+
         float s[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -310,20 +324,15 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
 
         // O in blocks of 64 columns
         const auto finish = [&](int cb, const float (&acc)[8][4]) {
+            const float vs = p.v_scale / kPScale;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (row[h] < 0) continue;
                 const int64_t at = row[h] * D + cb * 64 + 2 * t;
-                const bool has = p.o_prefix != nullptr && lse2[h] != -INFINITY;
-                float2 o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] = has ? *reinterpret_cast<const float2*>(p.o_prefix + at + j * 8) : make_float2(0.f, 0.f);
-                const float vs = p.v_scale / kPScale;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float x = (w[h] * o[j].x + vs * acc[j][2 * h]) * inv[h];
-                    const float y = (w[h] * o[j].y + vs * acc[j][2 * h + 1]) * inv[h];
+                    const float x = (w[h] * op[h][j].x + vs * acc[j][2 * h]) * inv[h];
+                    const float y = (w[h] * op[h][j].y + vs * acc[j][2 * h + 1]) * inv[h];
                     if (p.out_type == kOutF32)
                         *reinterpret_cast<float2*>(p.out + at + j * 8) = make_float2(x, y);
                     else
@@ -345,6 +354,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
                 }
 #pragma unroll 1
             for (int cb = 0; cb < D / 64; ++cb) {
+                if (cb > 0) load_prefix(cb);
                 float acc[8][4];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -370,6 +380,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
             // 0 x infinity and 0 x NaN: a product with a row that is not seen must not be made
 #pragma unroll 1
             for (int cb = 0; cb < D / 64; ++cb) {
+                if (cb > 0) load_prefix(cb);
                 float acc[8][4];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
