@@ -177,7 +177,8 @@ fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_s
     p.group = num_qo_heads / num_kv_heads;
     p.page_shift = page_shift_of(page_size);
     p.out_type = out_type == FDEC_OUT_F32 ? kOutF32 : dtype == FDEC_BF16 ? kOutBF16 : kOutF16;
-    p.scale_log2 = scale_log2;
+    // (never 0: a masked logit, -inf, times it stays -inf)
+    p.scale_log2 = scale_log2 == 0.f ? 1e-38f : scale_log2;
     p.v_scale = v_scale;
     if (static_cast<int64_t>(batch) * num_nodes * num_qo_heads > INT32_MAX)
         return fail(FDEC_ERR_UNSUPPORTED, "batch x num_nodes x num_qo_heads must be below 2^31");

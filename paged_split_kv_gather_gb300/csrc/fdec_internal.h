@@ -304,9 +304,10 @@ struct TreeParams {
     int batch, nodes, hq, hk, group, page_shift, out_type;
     float scale_log2;            // scale x k_scale x log2(e)
     float v_scale;
-    int tiles_per_warp;          // set by the launcher
+    // Set by the launcher: CTAs of a sequence's KV head, or 0: shares of so many tiles, one more in the first.
+    int parts, share, share_more;
 };
-cudaError_t launch_tree_attention(TreeParams p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s);
+cudaError_t launch_tree_attention(const TreeParams& p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s);
 
 // Most nodes of a drafted tree: a node's ancestors are the bits of one 64-bit word.
 constexpr int kMaxNodes = 64;

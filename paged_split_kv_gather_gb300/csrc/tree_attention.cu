@@ -3,22 +3,25 @@
 //   z_j = scale q.K_j over a node and its ancestors, M = max(lse_p, max z),
 //   w = exp(lse_p - M), l = w + sum exp(z_j - M),  out = (w o_p + sum exp(z_j - M) V_j) / l
 //
-// A CTA takes one sequence and KV head and some of its query rows (row = node x group +
-// head).  The tree's keys and values, at most 64 rows, are staged once in shared memory;
-// a warp then takes 16 query rows at a time with mma.sync.m16n8k16: S of 16 x 64 in
-// registers, the ancestors a 64-bit word a node, one maximum and sum (every key is there,
-// so nothing is rescaled), P V in blocks of 64 columns.  The prefix's state enters as one
-// more key, whose value is o_p.
+// A CTA takes a run of a sequence's and KV head's query rows (row = node x group + head).  The
+// tree's keys and values, at most 64 rows, are staged once in shared memory; a warp then takes
+// 16 query rows at a time with mma.sync.m16n8k16: S of 16 x 64 in registers, the ancestors a
+// 64-bit word a node, one maximum and sum (every key is there, so nothing is rescaled), P V in
+// blocks of 64 columns.  The prefix's state enters as one more key, whose value is o_p.
 //
 // Bytes: 2 D of q, 4 D of o_p, 4 D or 2 D of the result for a query row, against 4 D x 64
-// operations or less, so the call is bound by HBM; mma.sync keeps S and P in registers
-// and costs less than the bytes, where a tcgen05 tile of 128 rows would be mostly empty
-// for trees of a few nodes.
+// operations or less: bound by HBM, if anything hides the latencies.  Queries and o_p are
+// therefore copied into shared memory a tile and a block ahead (requested where they are
+// used, or held in registers, 64 trees of 64 nodes took 73 and 52 us; now 42, 4.4 TB/s, with
+// the L1 pipe 60 % busy).  mma.sync keeps S and P in registers; a tcgen05 tile of 128 rows
+// would be mostly empty for trees of a few nodes, and the tensor pipe is not what bounds.
 //
-// The probabilities of a bf16 cache enter P V as three bf16 values (24 bits) and those of
-// an f16 cache as two f16 values (22 bits, scaled by 2^15 so that the small ones stay
-// normal): the result is as good as fp32 sums.  With one value less of each it would be
-// off by 2^-17 (bf16), with a single one by 2^-9.
+// P V multiplies f16 values: V as f16, and each probability as two f16 values (22 bits,
+// and no more than 2^-33 off; scaled by 2^8), which makes the result as good as fp32
+// sums; one value would leave 2^-12.  f16 and E4M3 values are f16 values; a bf16 cache's are
+// rewritten as they are staged, times the power of two that brings the largest of the tree's
+// below 2^15: exact but for values 2^-29 of that and less, which are off by 2^-40 of it.
+// (As bf16, a probability would take three values: 1.5 times the products.)
 #include <algorithm>
 #include <cstdint>
 
@@ -35,13 +38,18 @@ namespace {
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = kTreeWarps * 32;
 
-// Pitches of the staged rows in bytes.  K is read 16 bytes a lane, four lanes a row: rows
-// 64 bytes apart modulo 128 keep the eight lanes of a phase on different banks.  V is read
-// by ldmatrix: rows 16 bytes apart modulo 128.
+// Rows of K and V are staged 16 bytes apart modulo 128, so that the eight rows of an ldmatrix lie on different banks.
+// Behind them each warp has room for the queries of a tile (their first 128 dims) and for 16 x 64 floats of the
+// prefix's rows.
+constexpr int kSlotBytes = 16 * 64 * 4;
 template <int D>
 struct TreeShape {
-    static constexpr int PK = 2 * D + 64, PV = 2 * D + 16;
-    static size_t smem(int nodes) { return static_cast<size_t>((nodes + 15) / 16 * 16) * (PK + PV); }
+    static constexpr int PITCH = 2 * D + 16;
+    static constexpr int QD = D < 128 ? D : 128;
+    static constexpr int Q_BYTES = 16 * QD * 2;
+    static size_t smem(int rows) {  // rows of K and V that are staged
+        return static_cast<size_t>(rows) * 2 * PITCH + kTreeWarps * (Q_BYTES + kSlotBytes);
+    }
 };
 
 // Four E4M3 codes -> two words of 16-bit values (exact).
@@ -62,396 +70,607 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
     return make_uint2(w[0], w[1]);
 }
 
-// Whether one of the two values of a word is infinite or NaN.
-template <bool BF16>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    constexpr uint32_t m = BF16 ? 0x7f80u : 0x7c00u;
-    return (w & m) == m || ((w >> 16) & m) == m;
+// The bits of the larger magnitude in each half (infinities and NaN are the largest).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t w) { return __vmaxu2(a, w & 0x7fff7fffu); }
+
+// x, y as sums of two f16 values each.
+__device__ __forceinline__ void split_two(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack2<false>(x, y);
+    const float2 r = unpack2<false>(hi);
+    lo = pack2<false>(x - r.x, y - r.y);
 }
 
-// x, y as a sum of TERMS 16-bit values each, the largest first.
-template <bool BF16, int TERMS>
-__device__ __forceinline__ void split_terms(float x, float y, uint32_t (&out)[TERMS]) {
-#pragma unroll
-    for (int i = 0; i < TERMS; ++i) {
-        out[i] = pack2<BF16>(x, y);
-        const float2 r = unpack2<BF16>(out[i]);
-        x -= r.x;
-        y -= r.y;
+// mma_16816 into zeros.
+template <bool BF16>
+__device__ __forceinline__ void mma_16816_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
     }
 }
 
-template <int D, bool BF16, bool KV8>
+// S += Q K^T over 32 dims (FIRST: into zeros): a warp's 16 rows and 2 KS tiles of 8 keys.
+template <bool BF16, int KS, bool FIRST>
+__device__ __forceinline__ void add_scores(float (&s)[2 * KS][4], const uint32_t (&a0)[4],
+                                           const uint32_t (&a1)[4], uint32_t k_addr, int pitch) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+        for (int j = 2 * ks; j < 2 * ks + 2; ++j) {
+            uint32_t r0, r1, r2, r3;
+            ldmatrix_x4(k_addr + j * 8 * pitch, r0, r1, r2, r3);
+            if constexpr (FIRST)
+                mma_16816_new<BF16>(s[j], a0, r0, r1);
+            else
+                mma_16816<BF16>(s[j], a0, r0, r1);
+            mma_16816<BF16>(s[j], a1, r2, r3);
+        }
+    }
+}
+
+// Eight columns of V's row j (chunk c of 16 bytes) into shared memory.  Of 16 columns, those of pairs 0, 2, 4, 6 come
+// first, then those of pairs 1, 3, 5, 7: the product's lane t then has columns 4t .. 4t + 3 in its two tiles of 8.
+__device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
+    uint8_t* at = row + (c >> 1) * 32 + (c & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(v.x, v.z);
+    *reinterpret_cast<uint2*>(at + 16) = make_uint2(v.y, v.w);
+}
+
+template <int D, bool BF16, bool KV8, int KS>
 __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const TreeParams p) {
     using S = TreeShape<D>;
-    constexpr int TERMS = BF16 ? 3 : 2;
-    constexpr float kPScale = BF16 ? 1.f : 32768.f;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint64_t s_anc[kMaxNodes];
-    __shared__ int64_t s_k[kMaxNodes], s_v[kMaxNodes];  // byte offsets of the nodes' rows, or -1
-    __shared__ unsigned s_valid[2];
+    constexpr int kPShift = 8;                 // p x 2^8 is split
+    constexpr bool kRewrite = BF16 && !KV8;    // V is not f16 as it is stored
+    constexpr uint32_t kInf = kRewrite ? 0x7f80 : 0x7c00;
+    extern __shared__ __align__(128) uint8_t smem[];
+    // What is known of the trees of the CTA's next kTreeWarps runs of tiles.
+    __shared__ uint64_t s_anc[kTreeWarps][kMaxNodes];                           // a node and its ancestors
+    __shared__ int64_t s_k[kTreeWarps][kMaxNodes], s_v[kTreeWarps][kMaxNodes];  // byte offsets of the nodes' rows
+    __shared__ uint64_t s_valid[kTreeWarps];                                    // nodes whose rows can be read
+    __shared__ int s_count[kTreeWarps];
+    __shared__ unsigned s_max, s_odd[2];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = tid >> 5;
     const int N = p.nodes, g = p.group;
-    const int tiles_max = (N * g + 15) / 16;
-    const int blocks = (tiles_max + kTreeWarps * p.tiles_per_warp - 1) / (kTreeWarps * p.tiles_per_warp);
-    const int blk = blockIdx.x % blocks;
-    const int bh = blockIdx.x / blocks;
-    const int kvh = bh % p.hk, b = bh / p.hk;
+    const int tiles_max = (N * g + 15) / 16;  // of a sequence's KV head
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const bool reports = blk == 0 && kvh == 0 && p.err != nullptr;  // one CTA a sequence
-    int n = p.node_counts != nullptr ? p.node_counts[b] : N;
-    if (n < 0 || n > N) {
-        if (reports && tid == 0) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
-        n = min(max(n, 0), N);
+    // The CTA's tiles: a part of a sequence's KV head, or an equal share of all tiles, a run of them for each sequence
+    // and KV head in it.
+    int at_tile, share_end;
+    const int c = blockIdx.x;
+    if (p.parts > 0) {
+        const int head = c / p.parts, part = c - head * p.parts;
+        at_tile = head * tiles_max + tiles_max * part / p.parts;
+        share_end = head * tiles_max + tiles_max * (part + 1) / p.parts;
+    } else {
+        at_tile = c * p.share + min(c, p.share_more);
+        share_end = at_tile + p.share + (c < p.share_more);
     }
-    const int R = n * g;
-    if (blk * kTreeWarps * p.tiles_per_warp * 16 >= R) return;
+    for (int run = 0; at_tile < share_end; ++run) {
+        const int bh = at_tile / tiles_max;
+        const int b = bh / p.hk, kvh = bh - b * p.hk;
+        const int first = at_tile - bh * tiles_max;
+        const int count = min(share_end - at_tile, tiles_max - first);
+        at_tile += count;
+        __syncthreads();  // what was staged before has been read
+        if (tid == 0) s_max = s_odd[0] = s_odd[1] = 0;
 
-    // ancestors: bits of a node's path, by pointer doubling (a path has at most 63 steps)
-    if (warp == 0) {
-        uint64_t anc[2];
-        int up[2];
+        if (run % kTreeWarps == 0) {
+            // a warp for each of the next runs
+            const int bh_of = bh + warp;
+            if (bh_of == bh || bh_of * tiles_max < share_end) {
+                const int b_of = bh_of / p.hk, kvh_of = bh_of - b_of * p.hk;
+                const bool reports = (warp > 0 || first == 0) && kvh_of == 0 && p.err != nullptr;  // one CTA a sequence
+                unsigned flags = 0;
+                int n = p.node_counts != nullptr ? p.node_counts[b_of] : N;
+                int64_t prefix = p.prefix_lens[b_of];
+                int up[2];
+                int64_t page[2], slot_of[2];
+                bool behind[2];  // past the page table
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = lane + 32 * h;
-            int par = i - 1;
-            if (p.parents != nullptr) par = i < n ? p.parents[static_cast<int64_t>(b) * N + i] : -1;
-            if (par < -1 || par >= i) {
-                if (reports) atomicOr(p.err, FDEC_DEVERR_TREE);
-                par = -1;
+                for (int h = 0; h < 2; ++h) {
+                    const int i = lane + 32 * h;
+                    up[h] = p.parents == nullptr ? i - 1 : i < N ? p.parents[static_cast<int64_t>(b_of) * N + i] : -1;
+                    const int64_t pos = max(prefix, static_cast<int64_t>(0)) + i, pi = pos >> p.page_shift;
+                    slot_of[h] = pos & ((1 << p.page_shift) - 1);
+                    behind[h] = pi >= p.pt_stride;
+                    page[h] = i < N && !behind[h] ? p.page_table[static_cast<int64_t>(b_of) * p.pt_stride + pi] : -1;
+                }
+                if (n < 0 || n > N) {
+                    flags |= FDEC_DEVERR_SEQ_LEN;
+                    n = min(max(n, 0), N);
+                }
+                if (prefix < 0 && n > 0) flags |= FDEC_DEVERR_SEQ_LEN;
+                uint64_t anc[2], valid = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = lane + 32 * h;
+                    if (up[h] < -1 || up[h] >= i) {
+                        if (i < n) flags |= FDEC_DEVERR_TREE;
+                        up[h] = -1;
+                    }
+                    anc[h] = uint64_t{1} << i;
+                    const bool ok = i < n && page[h] >= 0 && page[h] < p.k_pages && page[h] < p.v_pages;
+                    if (i < n && !ok) flags |= behind[h] ? FDEC_DEVERR_SEQ_LEN : FDEC_DEVERR_PAGE_ID;
+                    valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * h);
+                    s_k[warp][i] = page[h] * p.k_sp + slot_of[h] * p.k_st + kvh_of * p.k_sh;
+                    s_v[warp][i] = page[h] * p.v_sp + slot_of[h] * p.v_st + kvh_of * p.v_sh;
+                }
+                // ancestors: bits of a node's path, by pointer doubling (a path has at most 63 steps)
+#pragma unroll
+                for (int step = 0; step < 6; ++step) {
+                    uint64_t a[2];
+                    int u[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int from = up[h] & 31;
+                        const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], from);
+                        const uint64_t a1 = __shfl_sync(0xffffffffu, anc[1], from);
+                        const int u0 = __shfl_sync(0xffffffffu, up[0], from);
+                        const int u1 = __shfl_sync(0xffffffffu, up[1], from);
+                        a[h] = up[h] < 0 ? 0 : up[h] < 32 ? a0 : a1;
+                        u[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        anc[h] |= a[h];
+                        up[h] = u[h];
+                    }
+                }
+                s_anc[warp][lane] = anc[0];
+                s_anc[warp][lane + 32] = anc[1];
+                if (lane == 0) {
+                    s_valid[warp] = valid;
+                    s_count[warp] = n;
+                }
+                if (reports && flags != 0) atomicOr(p.err, flags);
             }
-            up[h] = par;
-            anc[h] = uint64_t{1} << i;
         }
+        __syncthreads();
+        const int known = run % kTreeWarps;
+        const int n = s_count[known], R = n * g;
+        const uint64_t valid = s_valid[known];
+        const int tiles = min((R + 15) / 16, first + count);
+        if (first >= tiles) continue;
+
+        // A warp's tiles of 16 query rows.  What they read is copied ahead of its use into the warp's part of shared
+        // memory: the queries of the next tile once this one's have been multiplied, the prefix's rows in blocks of 64
+        // columns, each once the one before it has been joined.
+        constexpr int CB = D / 64, QD = S::QD;
+        const int gq = lane >> 2, t = lane & 3;
+        const int T0 = first + warp;
+        const int my_tiles = T0 < tiles ? (tiles - T0 + kTreeWarps - 1) / kTreeWarps : 0;
+        const uint32_t q_slot = smem_addr(smem) + 2 * 16 * KS * S::PITCH + warp * (S::Q_BYTES + kSlotBytes);
+        const uint32_t slot = q_slot + S::Q_BYTES;
+        // Lane l: the (token, head) index in out and lse of row l % 16 of a tile (-1 past the last), its node.
+        int rows = -1, nodes = 0;
+        int row[2], node[2];       // of the lane's two rows of S
+        float lse_in[2];
+        const auto query = [&](int row, int node) {
+            const int64_t tok = static_cast<int64_t>(b) * N + node;
+            return p.q + tok * p.q_st + (row - tok * p.hq) * p.q_sh;
+        };
+        const auto next_tile = [&](int it) {
+            const int r = (T0 + it * kTreeWarps) * 16 + (lane & 15);
+            nodes = it < my_tiles && r < R ? r / g : 0;
+            rows = it < my_tiles && r < R ? (b * N + nodes) * p.hq + kvh * g + (r - nodes * g) : -1;
+            if (it < my_tiles) {
+                const uint16_t* mine = query(max(rows, 0), nodes);
+                constexpr int CH = QD / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
 #pragma unroll
-        for (int step = 0; step < 6; ++step) {
-            uint64_t a[2];
-            int u[2];
+                for (int k = 0; k < 16 / RPI; ++k) {
+                    const int r = k * RPI + lane / CH, c = lane % CH;
+                    const uint16_t* from = reinterpret_cast<const uint16_t*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                    const int there = __shfl_sync(0xffffffffu, rows, r) >= 0 ? 16 : 0;  // (zeros past the last row)
+                    const uint32_t to = q_slot + r * QD * 2 + (c ^ (r & 7)) * 16;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + c * 8),
+                                 "r"(there)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int from = up[h] & 31;
-                const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], from), a1 = __shfl_sync(0xffffffffu, anc[1], from);
-                const int u0 = __shfl_sync(0xffffffffu, up[0], from), u1 = __shfl_sync(0xffffffffu, up[1], from);
-                a[h] = up[h] < 0 ? 0 : up[h] < 32 ? a0 : a1;
-                u[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+                row[h] = __shfl_sync(0xffffffffu, rows, gq + 8 * h);
+                node[h] = __shfl_sync(0xffffffffu, nodes, gq + 8 * h);
+                lse_in[h] = row[h] >= 0 && p.lse_prefix != nullptr ? p.lse_prefix[row[h]] : -INFINITY;
             }
+        };
+        const auto request_prefix = [&](int cb, int rows) {
+            if (p.o_prefix != nullptr) {
+                const float* from = p.o_prefix + cb * 64 + (lane & 15) * 4;
+                const uint32_t to = slot + (lane >> 4) * 256;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                anc[h] |= a[h];
-                up[h] = u[h];
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 2 * k + (lane >> 4), row = __shfl_sync(0xffffffffu, rows, r);
+                    // pieces of 64 bytes change places in odd rows, so that two rows' lie on different banks
+                    const uint32_t piece = ((lane & 15) ^ ((r & 1) << 2)) * 16;
+                    if (row >= 0) cp_async_16(to + k * 512 + piece, from + static_cast<int64_t>(row) * D);
+                }
             }
-        }
-        s_anc[lane] = anc[0];
-        s_anc[lane + 32] = anc[1];
-    } else if (warp <= 2) {  // where the nodes' rows lie
-        const int j = tid - 32;
-        bool ok = false;
-        if (j < n) {
-            int64_t prefix = p.prefix_lens[b];
-            if (prefix < 0) {
-                if (reports) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
-                prefix = 0;
-            }
-            const int64_t pos = prefix + j, pi = pos >> p.page_shift;
-            const int64_t slot = pos & ((1 << p.page_shift) - 1);
-            if (pi >= p.pt_stride) {
-                if (reports) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
-            } else {
-                const int64_t page = p.page_table[static_cast<int64_t>(b) * p.pt_stride + pi];
-                ok = page >= 0 && page < p.k_pages && page < p.v_pages;
-                if (!ok && reports) atomicOr(p.err, FDEC_DEVERR_PAGE_ID);
-                s_k[j] = page * p.k_sp + slot * p.k_st + kvh * p.k_sh;
-                s_v[j] = page * p.v_sp + slot * p.v_st + kvh * p.v_sh;
-            }
-        }
-        const unsigned bits = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) s_valid[warp - 1] = bits;
-    }
-    __syncthreads();
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        next_tile(0);
+        request_prefix(0, rows);
 
-    // K and V rows, widened to 16 bits; rows past the tree and unreadable ones are zeros
-    const int rows16 = (n + 15) & ~15;
-    const uint64_t valid = s_valid[0] | static_cast<uint64_t>(s_valid[1]) << 32;
-    uint8_t* sm_k = smem;
-    uint8_t* sm_v = smem + rows16 * S::PK;
-    bool odd = false;  // an infinite or NaN value
-    {
+        // K and V rows, widened to 16 bits; rows past the tree and unreadable ones are zeros
+        constexpr int staged = 16 * KS;
+        uint8_t* sm_k = smem;
+        uint8_t* sm_v = smem + staged * S::PITCH;
+        // Rows of V with an infinite or NaN value are not multiplied as the others (0 times it would reach every row):
+        // they are zeros in shared memory, and are added for the rows that see them.
+        uint32_t most = 0;  // the largest finite magnitude of V's, if not of those
+        const auto note = [&](int j, uint32_t two) {
+            const uint32_t x = max(two & 0xffffu, two >> 16);
+            if (x >= kInf)
+                atomicOr(&s_odd[j >> 5], 1u << (j & 31));
+            else
+                most = max(most, x);
+        };
         constexpr int CH = KV8 ? D / 16 : D / 8;  // 16-byte chunks of a stored row
-        constexpr int U = 4;
-        for (int c0 = tid; c0 < rows16 * CH; c0 += U * kTreeThreads) {
+        constexpr int PER = (staged * CH + kTreeThreads - 1) / kTreeThreads;  // of a thread
+        // V's chunks stay in registers until the largest value is known (but for the widest rows)
+        constexpr bool kHeld = kRewrite && PER <= 16;
+        constexpr int U = PER < 8 ? PER : 8;
+        uint4 held[kHeld ? (PER + U - 1) / U * U : 1];
+#pragma unroll
+        for (int i0 = 0; i0 < PER; i0 += U) {
             uint4 kk[U], vv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * kTreeThreads, j = c / CH;
+                const int c = tid + (i0 + u) * kTreeThreads, j = c / CH;
                 kk[u] = vv[u] = make_uint4(0, 0, 0, 0);
-                if (c < rows16 * CH && (valid >> j & 1)) {
-                    kk[u] = *reinterpret_cast<const uint4*>(p.k_base + s_k[j] + (c - j * CH) * 16);
-                    vv[u] = *reinterpret_cast<const uint4*>(p.v_base + s_v[j] + (c - j * CH) * 16);
+                if (c < staged * CH && (valid >> j & 1)) {
+                    kk[u] = *reinterpret_cast<const uint4*>(p.k_base + s_k[known][j] + (c - j * CH) * 16);
+                    vv[u] = *reinterpret_cast<const uint4*>(p.v_base + s_v[known][j] + (c - j * CH) * 16);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * kTreeThreads, j = c / CH;
-                if (c >= rows16 * CH) break;
+                const int c = tid + (i0 + u) * kTreeThreads, j = c / CH;
+                if (c >= staged * CH) break;
                 if constexpr (KV8) {
                     const uint32_t kw[4] = {kk[u].x, kk[u].y, kk[u].z, kk[u].w};
                     const uint32_t vw[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint2 ka = widen4<BF16>(kw[2 * h]), kb = widen4<BF16>(kw[2 * h + 1]);
-                        const uint2 va = widen4<BF16>(vw[2 * h]), vb = widen4<BF16>(vw[2 * h + 1]);
-                        *reinterpret_cast<uint4*>(sm_k + j * S::PK + (c - j * CH) * 32 + h * 16) =
+                        const uint2 va = widen4<false>(vw[2 * h]), vb = widen4<false>(vw[2 * h + 1]);
+                        *reinterpret_cast<uint4*>(sm_k + j * S::PITCH + (c - j * CH) * 32 + h * 16) =
                             make_uint4(ka.x, ka.y, kb.x, kb.y);
-                        *reinterpret_cast<uint4*>(sm_v + j * S::PV + (c - j * CH) * 32 + h * 16) =
-                            make_uint4(va.x, va.y, vb.x, vb.y);
-                        odd |= not_finite<BF16>(va.x) || not_finite<BF16>(va.y) || not_finite<BF16>(vb.x) ||
-                               not_finite<BF16>(vb.y);
+                        put_values(sm_v + j * S::PITCH, (c - j * CH) * 2 + h, make_uint4(va.x, va.y, vb.x, vb.y));
+                        note(j, larger(larger(larger(larger(0, va.x), va.y), vb.x), vb.y));
                     }
                 } else {
-                    *reinterpret_cast<uint4*>(sm_k + j * S::PK + (c - j * CH) * 16) = kk[u];
-                    *reinterpret_cast<uint4*>(sm_v + j * S::PV + (c - j * CH) * 16) = vv[u];
-                    odd |= not_finite<BF16>(vv[u].x) || not_finite<BF16>(vv[u].y) || not_finite<BF16>(vv[u].z) ||
-                           not_finite<BF16>(vv[u].w);
-                }
-            }
-        }
-    }
-    odd = __syncthreads_or(odd);
-
-    const int gq = lane >> 2, t = lane & 3;
-    const uint32_t k_addr = smem_addr(sm_k) + gq * S::PK + t * 16;
-    const uint32_t v_addr = smem_addr(sm_v) + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::PV + (lane >> 4) * 16;
-    const int tiles = (R + 15) / 16;
-    for (int it = 0; it < p.tiles_per_warp; ++it) {
-        const int T = (blk * p.tiles_per_warp + it) * kTreeWarps + warp;
-        if (T >= tiles) break;
-        // the lane's two rows
-        int64_t row[2];  // (token, head) index of out and lse, -1 past the last row
-        const uint16_t* q[2];
-        uint64_t vis[2];
-        float lse2[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = T * 16 + gq + 8 * h;
-            row[h] = -1;
-            vis[h] = 0;
-            lse2[h] = -INFINITY;
-            q[h] = nullptr;
-            if (r < R) {
-                const int i = r / g, head = kvh * g + (r - i * g);
-                const int64_t tok = static_cast<int64_t>(b) * N + i;
-                row[h] = tok * p.hq + head;
-                q[h] = p.q + tok * p.q_st + head * p.q_sh;
-                vis[h] = s_anc[i] & valid;
-                if (p.lse_prefix != nullptr) lse2[h] = p.lse_prefix[row[h]] * 1.4426950408889634f;
-            }
-        }
-        const int keys = min(n, (min(T * 16 + 15, R - 1)) / g + 1);  // no node sees a later one
-        const int nt = (keys + 7) >> 3;
-
-        // the prefix's rows, 64 columns ahead of their use: the first block while S is computed
-        float2 op[2][8];
-        const auto load_prefix = [&](int cb) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool has = p.o_prefix != nullptr && lse2[h] != -INFINITY;
-                const float* at = p.o_prefix + row[h] * D + cb * 64 + 2 * t;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    op[h][j] = has ? *reinterpret_cast<const float2*>(at + j * 8) : make_float2(0.f, 0.f);
-            }
-        };
-        load_prefix(0);
-
-        float s[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-        // S = Q K^T, 32 dims at a time: lane t of a row's four holds dims 8t .. 8t + 7 of
-        // both operands, so the k order of the products is permuted alike in both
-#pragma unroll 4
-        for (int c = 0; c < D / 32; ++c) {
-            uint4 qa = make_uint4(0, 0, 0, 0), qb = qa;
-            if (q[0] != nullptr) qa = *reinterpret_cast<const uint4*>(q[0] + c * 32 + t * 8);
-            if (q[1] != nullptr) qb = *reinterpret_cast<const uint4*>(q[1] + c * 32 + t * 8);
-            const uint32_t a0[4] = {qa.x, qb.x, qa.y, qb.y}, a1[4] = {qa.z, qb.z, qa.w, qb.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < nt) {
-                    const uint4 kk = lds128<0>(k_addr + j * 8 * S::PK + c * 64);
-                    mma_16816<BF16>(s[j], a0, kk.x, kk.y);
-                    mma_16816<BF16>(s[j], a1, kk.z, kk.w);
-                }
-        }
-
-        float m[2], inv[2], w[2], lse_out[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float top = lse2[h];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool sees = vis[h] >> (j * 8 + 2 * t + e) & 1;
-                    float& z = s[j][2 * h + e];
-                    z = sees ? z * p.scale_log2 : -INFINITY;
-                    top = fmaxf(top, z);
-                }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            m[h] = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& z = s[j][2 * h + e];
-                    z = exp2_approx(z - m[h]);
-                    sum += z;
-                }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            w[h] = exp2_approx(lse2[h] - m[h]);
-            sum += w[h];
-            inv[h] = sum == 0.f ? 0.f : 1.f / sum;
-            lse_out[h] = sum == 0.f ? -INFINITY : m[h] * 0.6931471805599453f + logf(sum);
-        }
-
-        // O in blocks of 64 columns
-        const auto finish = [&](int cb, const float (&acc)[8][4]) {
-            const float vs = p.v_scale / kPScale;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (row[h] < 0) continue;
-                const int64_t at = row[h] * D + cb * 64 + 2 * t;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = (w[h] * op[h][j].x + vs * acc[j][2 * h]) * inv[h];
-                    const float y = (w[h] * op[h][j].y + vs * acc[j][2 * h + 1]) * inv[h];
-                    if (p.out_type == kOutF32)
-                        *reinterpret_cast<float2*>(p.out + at + j * 8) = make_float2(x, y);
+                    *reinterpret_cast<uint4*>(sm_k + j * S::PITCH + (c - j * CH) * 16) = kk[u];
+                    if constexpr (kHeld)
+                        held[i0 + u] = vv[u];
                     else
-                        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at + j * 8) = pack2<BF16>(x, y);
+                        put_values(sm_v + j * S::PITCH, c - j * CH, vv[u]);
+                    note(j, larger(larger(larger(larger(0, vv[u].x), vv[u].y), vv[u].z), vv[u].w));
                 }
             }
-        };
-        if (!odd) {
-            uint32_t pf[4][TERMS][4];
+        }
+        if constexpr (kRewrite) {
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) atomicMax(&s_max, most);
+        }
+        __syncthreads();
+        const uint64_t odd = s_odd[0] | static_cast<uint64_t>(s_odd[1]) << 32;
+        const int up = kRewrite ? min(14 - (static_cast<int>(s_max >> 7) - 127), 100) : 0;
+        const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        const float scale = fabsf(p.scale_log2);
+        if (kRewrite || odd != 0 || p.scale_log2 < 0.f) {
+            if constexpr (kRewrite) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t terms[TERMS];
-                    const float* z = &s[2 * ks + (e >> 1)][2 * (e & 1)];
-                    split_terms<BF16, TERMS>(z[0] * kPScale, z[1] * kPScale, terms);
-#pragma unroll
-                    for (int i = 0; i < TERMS; ++i) pf[ks][i][e] = terms[i];
+                for (int i = 0; i < PER; ++i) {
+                    const int c = tid + i * kTreeThreads, j = c / CH;
+                    if (c >= staged * CH) break;
+                    const auto f16 = [&](uint32_t x) {
+                        const float2 y = unpack2<true>(x);
+                        return pack2<false>(y.x * factor, y.y * factor);
+                    };
+                    if constexpr (kHeld) {
+                        const uint4 v = held[i];
+                        put_values(sm_v + j * S::PITCH, c - j * CH, make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w)));
+                    } else {
+                        uint4* at = reinterpret_cast<uint4*>(sm_v + j * S::PITCH + (c - j * CH) * 16);
+                        const uint4 v = *at;
+                        *at = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
+                    }
                 }
-#pragma unroll 1
-            for (int cb = 0; cb < D / 64; ++cb) {
-                if (cb > 0) load_prefix(cb);
-                float acc[8][4];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    if (ks * 2 < nt) {
-#pragma unroll
-                        for (int dp = 0; dp < 4; ++dp) {
-                            uint32_t r0, r1, r2, r3;
-                            ldmatrix_x4_trans(v_addr + ks * 16 * S::PV + cb * 128 + dp * 32, r0, r1, r2, r3);
-#pragma unroll
-                            for (int i = TERMS - 1; i >= 0; --i) {
-                                mma_16816<BF16>(acc[2 * dp], pf[ks][i], r0, r1);
-                                mma_16816<BF16>(acc[2 * dp + 1], pf[ks][i], r2, r3);
-                            }
-                        }
-                    }
-                finish(cb, acc);
             }
-        } else {
-            // 0 x infinity and 0 x NaN: a product with a row that is not seen must not be made
-#pragma unroll 1
-            for (int cb = 0; cb < D / 64; ++cb) {
-                if (cb > 0) load_prefix(cb);
-                float acc[8][4];
+            if (odd != 0 || p.scale_log2 < 0.f) {
+                __syncthreads();
+                for (int c = tid; c < staged * (D / 8); c += kTreeThreads) {
+                    const int j = c / (D / 8), at = (c - j * (D / 8)) * 16;
+                    if (odd >> j & 1) *reinterpret_cast<uint4*>(sm_v + j * S::PITCH + at) = make_uint4(0, 0, 0, 0);
+                    if (p.scale_log2 < 0.f) {  // the scale's sign goes to K: the largest product is the largest logit
+                        uint4* k = reinterpret_cast<uint4*>(sm_k + j * S::PITCH + at);
+                        const uint4 x = *k;
+                        *k = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        const float v_factor = p.v_scale * exp2f(static_cast<float>(-kPShift - up));  // (the products' scales undone)
+
+        const uint32_t k_addr = smem_addr(sm_k) + (lane & 7) * S::PITCH + (lane >> 3) * 16;
+        const int q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t q_addr = q_slot + q_row * QD * 2;
+        const uint32_t v_addr = smem_addr(sm_v) + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::PITCH + (lane >> 4) * 16;
+        const bool f32 = p.out_type == kOutF32;
+        for (int it = 0; it < my_tiles; ++it) {
+            constexpr int NT = 2 * KS;
+            float s[NT][4];
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();  // the tile's queries are there (the prefix's first block may not be)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+            for (int c = 0; c < QD / 32; ++c) {  // S = Q K^T, 32 dims at a time
+                uint32_t a0[4], a1[4];
+                ldmatrix_x4(q_addr + ((4 * c + (lane >> 4)) ^ (lane & 7)) * 16, a0[0], a0[1], a0[2], a0[3]);
+                ldmatrix_x4(q_addr + ((4 * c + 2 + (lane >> 4)) ^ (lane & 7)) * 16, a1[0], a1[1], a1[2], a1[3]);
+                if (c == 0)
+                    add_scores<BF16, KS, true>(s, a0, a1, k_addr, S::PITCH);
+                else
+                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + c * 64, S::PITCH);
+            }
+            if constexpr (D > QD) {  // the other dims from where they are
+                const uint16_t* from[2] = {query(max(row[0], 0), node[0]) + 2 * t,
+                                           query(max(row[1], 0), node[1]) + 2 * t};
+                const auto word = [&](int h, int d) {
+                    return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
+                };
+#pragma unroll 4
+                for (int d = QD; d < D; d += 32) {
+                    const uint32_t a0[4] = {word(0, d), word(1, d), word(0, d + 8), word(1, d + 8)};
+                    const uint32_t a1[4] = {word(0, d + 16), word(1, d + 16), word(0, d + 24), word(1, d + 24)};
+                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + d * 2, S::PITCH);
+                }
+            }
+
+            float w[2], vs[2], lse_out[2];
+            const int out_row[2] = {row[0], row[1]}, out_node[2] = {node[0], node[1]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t vis = row[h] < 0 ? 0 : s_anc[known][node[h]] & valid;
+                const float before = lse_in[h] * 1.4426950408889634f;
+                // the lane's columns of a tile of 8 keys are 2t and 2t + 1
+                const uint64_t mine = vis >> (2 * t);
+                const uint32_t bits[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
+                float top = -INFINITY;
 #pragma unroll
-                for (int jt = 0; jt < 8; ++jt)
+                for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const int key = jt * 8 + kk, from = (lane & ~3) | (kk >> 1);
-                        const float p0 = __shfl_sync(0xffffffffu, s[jt][kk & 1], from) * kPScale;
-                        const float p1 = __shfl_sync(0xffffffffu, s[jt][2 + (kk & 1)], from) * kPScale;
-                        if (key < keys) {
-                            const bool sees0 = vis[0] >> key & 1, sees1 = vis[1] >> key & 1;
+                    for (int e = 0; e < 2; ++e) {
+                        float& z = s[j][2 * h + e];
+                        if (!(bits[j >> 2] & (1u << ((j & 3) * 8 + e)))) z = -INFINITY;
+                        top = fmaxf(top, z);
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = fmaxf(top * scale, before);
+                const float m = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float2 v = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(
-                                    sm_v + key * S::PV + cb * 128 + j * 16 + t * 4));
-                                if (sees0) {
-                                    acc[j][0] += p0 * v.x;
-                                    acc[j][1] += p0 * v.y;
-                                }
-                                if (sees1) {
-                                    acc[j][2] += p1 * v.x;
-                                    acc[j][3] += p1 * v.y;
-                                }
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float& z = s[j][2 * h + e];
+                        z = exp2_approx(fmaf(z, scale, kPShift - m));
+                        sum += z;
+                    }
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                w[h] = exp2_approx(before - m);
+                sum = sum * (1.f / (1 << kPShift)) + w[h];
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                lse_out[h] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
+                w[h] *= inv;
+                vs[h] = v_factor * inv;
+            }
+            if (p.lse != nullptr && t == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (out_row[h] >= 0) p.lse[out_row[h]] = lse_out[h];
+            }
+            // an empty state counts for nothing, whatever its values
+            const bool empty[2] = {row[0] >= 0 && lse_in[0] == -INFINITY, row[1] >= 0 && lse_in[1] == -INFINITY};
+            const bool states = !__any_sync(0xffffffffu, empty[0] || empty[1]);
+            const int rows_now = rows;
+            __syncwarp();  // the queries have been read
+            next_tile(it + 1);
+
+            uint32_t pf[KS][2][4];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    split_two(s[2 * ks + (e >> 1)][2 * (e & 1)], s[2 * ks + (e >> 1)][2 * (e & 1) + 1], pf[ks][0][e],
+                              pf[ks][1][e]);
+            }
+
+            // O in blocks of 64 columns
+            const auto finish = [&](int cb, const float (&acc)[8][4]) {
+                if (cb == 0)
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");  // (the next queries may be on their way)
+                else
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();  // the warp's copies of the block are there
+                // the lane's columns 16 j + 4 t .. + 3 of the block: its products' tiles 2 j and 2 j + 1
+                const uint32_t from = slot + gq * 256 + t * 16;
+                const auto place = [&](int h, int j) { return from + h * 2048 + (j ^ (gq & 1)) * 64; };
+                if (!states) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (empty[h]) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(place(h, j)), "f"(0.f)
+                                             : "memory");
+                        }
+                }
+                // Rows of V that are not finite: their share is added to the state's, which is weighed here.
+                if (odd != 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float4 o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 x = lds128f<0>(place(h, j));
+                            o[j] = make_float4(w[h] * x.x, w[h] * x.y, w[h] * x.z, w[h] * x.w);
+                        }
+                        for (uint64_t rest = odd; rest != 0; rest &= rest - 1) {
+                            const int key = __ffsll(static_cast<long long>(rest)) - 1;
+                            uint32_t hi = 0, lo = 0;
+#pragma unroll
+                            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (key >> 3 == 2 * ks + e) {  // (through registers: not an index into memory)
+                                        asm volatile("mov.b32 %0, %1;" : "=r"(hi) : "r"(pf[ks][0][2 * e + h]));
+                                        asm volatile("mov.b32 %0, %1;" : "=r"(lo) : "r"(pf[ks][1][2 * e + h]));
+                                    }
+                            const float2 a = unpack2<false>(hi), c = unpack2<false>(lo);
+                            const float pr = __shfl_sync(0xffffffffu, key & 1 ? a.y + c.y : a.x + c.x,
+                                                         (lane & ~3) | ((key & 7) >> 1)) * factor * vs[h];
+                            const uint64_t seen = out_row[h] < 0 ? 0 : s_anc[known][out_node[h]] & valid;
+                            if (!(seen >> key & 1)) continue;
+                            const uint8_t* v_row = p.v_base + s_v[known][key] + (cb * 64 + 4 * t) * (KV8 ? 1 : 2);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint2 v;
+                                if constexpr (KV8)
+                                    v = widen4<false>(*reinterpret_cast<const uint32_t*>(v_row + j * 16));
+                                else
+                                    v = *reinterpret_cast<const uint2*>(v_row + j * 32);
+                                const float2 x = unpack2<BF16 && !KV8>(v.x), y = unpack2<BF16 && !KV8>(v.y);
+                                o[j].x += pr * x.x;
+                                o[j].y += pr * x.y;
+                                o[j].z += pr * y.x;
+                                o[j].w += pr * y.y;
                             }
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(place(h, j)), "f"(o[j].x),
+                                         "f"(o[j].y), "f"(o[j].z), "f"(o[j].w)
+                                         : "memory");
                     }
+                }
+                const float weight[2] = {odd != 0 ? 1.f : w[0], odd != 0 ? 1.f : w[1]};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (out_row[h] < 0) continue;
+                    const int64_t at = static_cast<int64_t>(out_row[h]) * D + cb * 64 + 4 * t;
+                    const auto joined = [&](int j) {
+                        const float4 o = lds128f<0>(place(h, j));
+                        return make_float4(vs[h] * acc[2 * j][2 * h] + weight[h] * o.x,
+                                           vs[h] * acc[2 * j][2 * h + 1] + weight[h] * o.y,
+                                           vs[h] * acc[2 * j + 1][2 * h] + weight[h] * o.z,
+                                           vs[h] * acc[2 * j + 1][2 * h + 1] + weight[h] * o.w);
+                    };
+                    if (f32) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(p.out + at + j * 16) = joined(j);
+                    } else {
+                        uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 x = joined(j);
+                            *reinterpret_cast<uint2*>(out + j * 16) =
+                                make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+                        }
+                    }
+                }
+                __syncwarp();  // and have been read
+                request_prefix(cb + 1 < CB ? cb + 1 : 0, cb + 1 < CB ? rows_now : rows);
+            };
+#pragma unroll 1
+            for (int cb = 0; cb < CB; ++cb) {
+                float acc[8][4];
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                    for (int dp = 0; dp < 4; ++dp) {
+                        uint32_t r0, r1, r2, r3;
+                        ldmatrix_x4_trans(v_addr + ks * 16 * S::PITCH + cb * 128 + dp * 32, r0, r1, r2, r3);
+                        if (ks == 0) {
+                            mma_16816_new<false>(acc[2 * dp], pf[ks][1], r0, r1);
+                            mma_16816_new<false>(acc[2 * dp + 1], pf[ks][1], r2, r3);
+                        } else {
+                            mma_16816<false>(acc[2 * dp], pf[ks][1], r0, r1);
+                            mma_16816<false>(acc[2 * dp + 1], pf[ks][1], r2, r3);
+                        }
+                        mma_16816<false>(acc[2 * dp], pf[ks][0], r0, r1);
+                        mma_16816<false>(acc[2 * dp + 1], pf[ks][0], r2, r3);
+                    }
+                }
                 finish(cb, acc);
             }
         }
-        if (p.lse != nullptr && t == 0) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (row[h] >= 0) p.lse[row[h]] = lse_out[h];
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 }
 
-template <int D, bool BF16, bool KV8>
-cudaError_t launch_tree(TreeParams p, int num_sms, cudaStream_t s) {
+template <int D, bool BF16, bool KV8, int KS>
+cudaError_t launch_tree_one(TreeParams p, int num_sms, cudaStream_t s) {
     static unsigned long long attr_done = 0;  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(tree_attention_kernel<D, BF16, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(TreeShape<D>::smem(kMaxNodes)));
+        e = cudaFuncSetAttribute(tree_attention_kernel<D, BF16, KV8, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(TreeShape<D>::smem(16 * KS)));
         if (e != cudaSuccess) return e;
         if (dev < 64) __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
     }
-    const int tiles = (p.nodes * p.group + 15) / 16;
-    const int64_t warp_tiles = static_cast<int64_t>(p.batch) * p.hk * tiles;
-    const int64_t slots = static_cast<int64_t>(num_sms) * 3 * kTreeWarps;  // warps resident at once
-    p.tiles_per_warp = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>((tiles + kTreeWarps - 1) / kTreeWarps, (warp_tiles + slots - 1) / slots)));
-    const int blocks = (tiles + kTreeWarps * p.tiles_per_warp - 1) / (kTreeWarps * p.tiles_per_warp);
-    const int64_t grid = static_cast<int64_t>(p.batch) * p.hk * blocks;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    // Up to as many sequences' KV heads as CTAs are resident: parts of one each, of a tile for every warp or more, as an
+    // equal share that spans two stages two trees (256 heads of 6 tiles: 7.9 us, 11.2 in shares).  Above, equal
+    // shares: whole heads in a second round would leave most of the machine idle (512 heads of 16 tiles: 42 us, 55 a
+    // head a CTA, 56 in parts).
+    const int64_t heads = static_cast<int64_t>(p.batch) * p.hk, slots = static_cast<int64_t>(num_sms) * 3;
+    const int per_head = (p.nodes * p.group + 15) / 16;
+    const int64_t most = std::min<int64_t>((per_head + kTreeWarps - 1) / kTreeWarps, 2 * slots / heads);
+    p.parts = heads <= slots ? static_cast<int>(most) : 0;
+    const int64_t grid = p.parts > 0 ? heads * p.parts : slots;
+    p.share = static_cast<int>(heads * per_head / slots);
+    p.share_more = static_cast<int>(heads * per_head % slots);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(kTreeThreads, 1, 1);
-    cfg.dynamicSmemBytes = TreeShape<D>::smem(p.nodes);
+    cfg.dynamicSmemBytes = TreeShape<D>::smem(16 * KS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_attention_kernel<D, BF16, KV8>, p);
+    return cudaLaunchKernelEx(&cfg, tree_attention_kernel<D, BF16, KV8, KS>, p);
+}
+
+template <int D, bool BF16, bool KV8>
+cudaError_t launch_tree(const TreeParams& p, int num_sms, cudaStream_t s) {
+    if (p.nodes <= 16) return launch_tree_one<D, BF16, KV8, 1>(p, num_sms, s);
+    if (p.nodes <= 32) return launch_tree_one<D, BF16, KV8, 2>(p, num_sms, s);
+    return launch_tree_one<D, BF16, KV8, 4>(p, num_sms, s);
 }
 
 template <int D>
@@ -466,7 +685,7 @@ cudaError_t launch_tree_d(const TreeParams& p, bool bf16, bool kv8, int num_sms,
 
 }  // namespace
 
-cudaError_t launch_tree_attention(TreeParams p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s) {
+cudaError_t launch_tree_attention(const TreeParams& p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s) {
     switch (head_dim) {
         case 64: return launch_tree_d<64>(p, bf16, kv8, num_sms, s);
         case 128: return launch_tree_d<128>(p, bf16, kv8, num_sms, s);
