@@ -45,10 +45,17 @@ struct Order {       // what the first CTA tells the others
     int op;
     int node;        // whose rows
     int run;         // kDraw: the warp's run of the vocabulary that holds the token
-    int place;       // kDraw: index in out_tokens
+    int place;       // index of the next token in out_tokens
     double s;        // weight of q
     double target;   // kDraw: cumulative weight to pass, from the run's begin
     uint64_t gone;   // without draft rows: children whose tokens have lost their weight
+    // kSum: whether the next token is drawn from these sums, wherever they have weight (last); less those of the
+    // tokens of the children `weighed`, row_gone in all.
+    int last;
+    float u;
+    uint64_t weighed;
+    double row_gone;
+    uint64_t fallen;  // gone, once it is drawn
 };
 
 __device__ __forceinline__ float value(const float* p) { return *p; }
@@ -77,7 +84,7 @@ __device__ __forceinline__ float bounded(float x, bool& bad) {
     return y;
 }
 
-// A sum as a pair of fp32 values.
+// A number as a pair of fp32 values.
 struct Pair {
     float hi = 0.f, lo = 0.f;
     // + (x + e), e small against x
@@ -88,17 +95,55 @@ struct Pair {
         hi = sum;
         lo = __fadd_rn(lo, __fadd_rn(err, e));
     }
-    __device__ __forceinline__ double total() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+    __device__ __forceinline__ bool above(Pair x) const {
+        Pair d = *this;
+        d.add(-x.hi, -x.lo);
+        return __fadd_rn(d.hi, d.lo) > 0.f;
+    }
 };
 
-// max(p - s q, 0) added to a sum, s = s_hi + s_lo.
-__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, float s_hi, float s_lo) {
-    const float t = __fmul_rn(s_hi, q);
-    const float te = __fmaf_rn(s_lo, q, __fmaf_rn(s_hi, q, -t));
-    float d = __fsub_rn(p, t);
-    float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), t), te);  // exact where p >= t, and else d < 0
-    if (!(__fadd_rn(d, e) > 0.f)) d = e = 0.f;
-    sum.add(d, e);
+__device__ __forceinline__ Pair pair_of(double x) {
+    Pair p;
+    p.hi = static_cast<float>(x);
+    p.lo = static_cast<float>(x - static_cast<double>(p.hi));
+    return p;
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, v.hi, o), lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
+        v.add(hi, lo);
+    }
+    return v;
+}
+
+__device__ __forceinline__ Pair warp_scan(Pair v) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float hi = __shfl_up_sync(0xffffffffu, v.hi, o), lo = __shfl_up_sync(0xffffffffu, v.lo, o);
+        if (lane >= o) v.add(hi, lo);
+    }
+    return v;
+}
+
+// max(p - s q, 0) added to a sum.  UNIT: s is 1.
+template <bool UNIT>
+__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, Pair s) {
+    if constexpr (UNIT) {
+        const float t = fminf(q, p);
+        const float d = __fsub_rn(p, t);
+        sum.add(d, __fsub_rn(__fsub_rn(p, d), t));  // (exact: p >= t >= 0)
+    } else {
+        const float t = __fmul_rn(s.hi, q);
+        const float te = __fmaf_rn(s.lo, q, __fmaf_rn(s.hi, q, -t));
+        float d = __fsub_rn(p, t);
+        float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), t), te);  // exact where p >= t, and else d < 0
+        if (!(__fadd_rn(d, e) > 0.f)) d = e = 0.f;
+        sum.add(d, e);
+    }
 }
 
 // Whether token v is that of one of the children `gone`.
@@ -108,44 +153,36 @@ __device__ __forceinline__ bool is_gone(int v, const int* tokens, uint64_t gone)
     return false;
 }
 
-// What is left of the target at token v, in fp64.
-__device__ __forceinline__ double rest_of(float p, float q, bool drafted, int v, double s, const int* tokens,
+// What is left of the target at token v, added to a sum.
+__device__ __forceinline__ void add_token(Pair& sum, float p, float q, bool drafted, int v, Pair s, const int* tokens,
                                           uint64_t gone) {
     bool bad = false;
-    const double x = bounded(p, bad);
-    if (drafted) return fmax(x - s * static_cast<double>(bounded(q, bad)), 0.0);
-    return is_gone(v, tokens, gone) ? 0.0 : x;
+    const float x = bounded(p, bad);
+    if (drafted)
+        add_rest<false>(sum, x, bounded(q, bad), s);
+    else if (!is_gone(v, tokens, gone))
+        sum.add(x, 0.f);
 }
 
-// One warp's sum over tokens [begin, end).
-template <typename T, bool VEC>
-__device__ __forceinline__ double run_sum(const T* p, const T* q, int begin, int end, double s, const int* tokens,
-                                          uint64_t gone, bool& bad) {
+// One lane's part of a warp's sum over tokens [begin, end).  PLAIN: probabilities are taken as they are, and the largest
+// of their bits are noted (as unsigned numbers, all that are not in [0, 2] are above those of 2).
+template <typename T, bool VEC, int MODE, bool PLAIN>  // MODE 0: p, 1: max(p - q, 0), 2: max(p - s q, 0)
+__device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int end, Pair s, uint32_t& most, bool& bad) {
     const int lane = threadIdx.x & 31;
     Pair sum;
-    if (q == nullptr && gone != 0) {
-        bool hit = false;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = lane + 32 * h;
-            hit |= (gone >> i & 1) && tokens[i] >= begin && tokens[i] < end;
+    const auto term = [&](float a, float c) {
+        if constexpr (PLAIN) {
+            most = max(most, __float_as_uint(a));
+            if constexpr (MODE > 0) most = max(most, __float_as_uint(c));
+        } else {
+            a = bounded(a, bad);
+            if constexpr (MODE > 0) c = bounded(c, bad);
         }
-        if (__any_sync(0xffffffffu, hit)) {  // a token without weight lies in here
-            constexpr int U = 8;
-            for (int v0 = begin + lane; v0 < end; v0 += U * 32) {
-                float a[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) a[u] = v0 + u * 32 < end ? value(p + v0 + u * 32) : 0.f;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float x = bounded(a[u], bad);
-                    sum.add(is_gone(v0 + u * 32, tokens, gone) ? 0.f : x, 0.f);
-                }
-            }
-            return sum.total();
-        }
-    }
-    const float s_hi = static_cast<float>(s), s_lo = static_cast<float>(s - static_cast<double>(s_hi));
+        if constexpr (MODE > 0)
+            add_rest<MODE == 1>(sum, a, c, s);
+        else
+            sum.add(a, 0.f);
+    };
     if constexpr (VEC) {
         constexpr int U = 4;
         for (int v0 = begin + lane * 4; v0 < end; v0 += U * 128) {
@@ -157,19 +194,13 @@ __device__ __forceinline__ double run_sum(const T* p, const T* q, int begin, int
                 c[u][0] = c[u][1] = c[u][2] = c[u][3] = 0.f;
                 if (v < end) {
                     value4(p + v, a[u]);
-                    if (q != nullptr) value4(q + v, c[u]);
+                    if constexpr (MODE > 0) value4(q + v, c[u]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = bounded(a[u][k], bad);
-                    if (q != nullptr)
-                        add_rest(sum, x, bounded(c[u][k], bad), s_hi, s_lo);
-                    else
-                        sum.add(x, 0.f);
-                }
+                for (int k = 0; k < 4; ++k) term(a[u][k], c[u][k]);
         }
     } else {
         constexpr int U = 8;
@@ -179,25 +210,58 @@ __device__ __forceinline__ double run_sum(const T* p, const T* q, int begin, int
             for (int u = 0; u < U; ++u) {
                 const int v = v0 + u * 32;
                 a[u] = v < end ? value(p + v) : 0.f;
-                c[u] = v < end && q != nullptr ? value(q + v) : 0.f;
+                c[u] = 0.f;
+                if constexpr (MODE > 0) c[u] = v < end ? value(q + v) : 0.f;
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) term(a[u], c[u]);
+        }
+    }
+    return sum;
+}
+
+template <typename T, bool VEC, int MODE>
+__device__ __forceinline__ Pair mode_sum(const T* p, const T* q, int begin, int end, Pair s, bool& bad) {
+    uint32_t most = 0;
+    Pair sum = lane_sum<T, VEC, MODE, true>(p, q, begin, end, s, most, bad);
+    if (__any_sync(0xffffffffu, most > 0x40000000u)) sum = lane_sum<T, VEC, MODE, false>(p, q, begin, end, s, most, bad);
+    return sum;
+}
+
+// One warp's sum over tokens [begin, end).
+template <typename T, bool VEC>
+__device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, double s, const int* tokens,
+                                        uint64_t gone, bool& bad) {
+    const int lane = threadIdx.x & 31;
+    Pair sum;
+    bool hit = false;  // a token without weight lies in here
+    if (q == nullptr && gone != 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 32 * h;
+            hit |= (gone >> i & 1) && tokens[i] >= begin && tokens[i] < end;
+        }
+    }
+    if (__any_sync(0xffffffffu, hit)) {
+        constexpr int U = 8;
+        for (int v0 = begin + lane; v0 < end; v0 += U * 32) {
+            float a[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) a[u] = v0 + u * 32 < end ? value(p + v0 + u * 32) : 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float x = bounded(a[u], bad);
-                if (q != nullptr)
-                    add_rest(sum, x, bounded(c[u], bad), s_hi, s_lo);
-                else
-                    sum.add(x, 0.f);
+                sum.add(is_gone(v0 + u * 32, tokens, gone) ? 0.f : x, 0.f);
             }
         }
+    } else if (q == nullptr) {
+        sum = mode_sum<T, VEC, 0>(p, q, begin, end, sum, bad);
+    } else if (s == 1.0) {  // the first to fall: nearly all sums
+        sum = mode_sum<T, VEC, 1>(p, q, begin, end, sum, bad);
+    } else {
+        sum = mode_sum<T, VEC, 2>(p, q, begin, end, pair_of(s), bad);
     }
-    return sum.total();
-}
-
-__device__ __forceinline__ double warp_sum_double(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    return warp_sum(sum);
 }
 
 __device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
@@ -212,7 +276,7 @@ __device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
 
 // The walk of the first CTA.
 struct Walk {
-    double sum[kRuns];  // every warp's sum
+    Pair sum[kRuns];  // every warp's sum
     int tok[kMaxNodes], par[kMaxNodes], path[kMaxNodes];
     float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // at each node's token, in its parent's rows; its random number
     double s, W;
@@ -225,6 +289,61 @@ struct Walk {
     bool have_row, exact;
     bool whole;  // the target's row itself is summed, whatever has fallen
 };
+
+// The run of the vocabulary that holds the next token (o.run, o.target), from every warp's sum, less the tokens of the
+// children `weighed`.  A warp; false where the sums have no weight, or not enough to be a difference of sums.
+__device__ __forceinline__ bool draw_run(const Walk& walk, uint64_t weighed, double row_gone, float u, int chunk, Order& o) {
+    const int lane = threadIdx.x & 31;
+    constexpr int PER = (kRuns + 31) / 32;
+    double mine[PER], part = 0.0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) part += mine[k] = walk.sum[lane * PER + k].value();
+    double upto = warp_scan_double(part);
+    double W = __shfl_sync(0xffffffffu, upto, 31);
+    if (weighed != 0) {
+        if (!((W - row_gone) * 64.0 > W)) return false;
+        part = 0.0;
+        for (uint64_t m = weighed; m != 0; m &= m - 1) {
+            const int c = __ffsll(static_cast<long long>(m)) - 1;
+            const int run = walk.tok[c] / chunk;
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                if (run == lane * PER + k) {
+                    const double rest = mine[k] - static_cast<double>(walk.p[c]);
+                    mine[k] = rest > mine[k] * 0x1p-42 ? rest : 0.0;  // (what rounding left is nothing)
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) part += mine[k];
+        upto = warp_scan_double(part);
+        W = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (!(W > 0.0)) return false;
+    const double goal = static_cast<double>(u) * W;
+    int run = -1, last = -1;
+    double at = upto - part, from = 0.0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (mine[k] > 0.0) last = lane * PER + k;
+        if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
+            run = lane * PER + k;
+            from = at;
+        }
+        at += mine[k];
+    }
+    const unsigned found = __ballot_sync(0xffffffffu, run >= 0);
+    const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
+    o.op = kDraw;
+    if (found != 0) {
+        const int who = __ffs(found) - 1;
+        o.run = __shfl_sync(0xffffffffu, run, who);
+        o.target = goal - __shfl_sync(0xffffffffu, from, who);
+    } else {  // (only by rounding: the last run with weight, its last token)
+        o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
+        o.target = 4.0 * W;
+    }
+    return true;
+}
 
 // What comes next: the first CTA's first warp, after the sums that were asked for have come (sums).
 __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool drafted, int chunk) {
@@ -249,20 +368,14 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
         left = children(0);
         if (lane == 0) walk.path[0] = 0;
     }
-    double mine[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) mine[k] = 0.0;
-    Order o;
+    Order o = {};
     o.op = kStop;
-    o.node = o.run = o.place = 0;
-    o.s = o.target = 0.0;
-    o.gone = 0;
     if (n > 0) {
         bool ask = false;
         if (sums) {  // the sums that were asked for
             double part = 0.0;
 #pragma unroll
-            for (int k = 0; k < PER; ++k) part += mine[k] = walk.sum[lane * PER + k];
+            for (int k = 0; k < PER; ++k) part += walk.sum[lane * PER + k].value();
             W = __shfl_sync(0xffffffffu, warp_scan_double(part), 31);
             summed = true;
             if (!drafted && !exact && !whole) {
@@ -306,47 +419,8 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
                 if (ask && have_row) exact = true;
             }
         }
-        if (!ask && summed && W > 0.0) {  // no child stands: draw
-            o.op = kDraw;
-            if (!drafted && !exact && !whole) {
-                for (uint64_t m = weighed; m != 0; m &= m - 1) {
-                    const int c = __ffsll(static_cast<long long>(m)) - 1;
-                    const int run = walk.tok[c] / chunk;
-#pragma unroll
-                    for (int k = 0; k < PER; ++k)
-                        if (run == lane * PER + k) {
-                            const double rest = mine[k] - static_cast<double>(walk.p[c]);
-                            mine[k] = rest > mine[k] * 0x1p-42 ? rest : 0.0;  // (what rounding left is nothing)
-                        }
-                }
-            }
-            double part = 0.0;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) part += mine[k];
-            const double upto = warp_scan_double(part);
-            const double goal = static_cast<double>(walk.u[0]) * __shfl_sync(0xffffffffu, upto, 31);
-            int run = -1, last = -1;
-            double at = upto - part, from = 0.0;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                if (mine[k] > 0.0) last = lane * PER + k;
-                if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
-                    run = lane * PER + k;
-                    from = at;
-                }
-                at += mine[k];
-            }
-            const unsigned found = __ballot_sync(0xffffffffu, run >= 0);
-            const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
-            if (found != 0) {
-                const int who = __ffs(found) - 1;
-                o.run = __shfl_sync(0xffffffffu, run, who);
-                o.target = goal - __shfl_sync(0xffffffffu, from, who);
-            } else if (any != 0) {  // (only by rounding: the last run with weight, its last token)
-                o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
-                o.target = 4.0 * W;
-            }
-        } else if (!ask) {
+        const bool plain = drafted || exact || whole;  // (the sums are those of what is left)
+        if (!ask && !(summed && draw_run(walk, plain ? 0 : weighed, row_gone, walk.u[0], chunk, o))) {  // no child stands
             if (summed) {  // nothing is left: the target's row itself, if that is not it already
                 ask = !whole;
                 s = 0.0, gone = 0;
@@ -355,7 +429,14 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
             }
             whole = true;
         }
-        if (ask) o.op = kSum;
+        if (ask) {
+            o.op = kSum;
+            o.last = left == 0;
+            o.u = walk.u[0];
+            o.weighed = drafted || exact || whole ? 0 : weighed;
+            o.row_gone = row_gone;
+            o.fallen = gone;
+        }
         o.node = x;
         o.s = s;
         // (a plain sum of the row first; without its tokens where it must be exact)
@@ -376,7 +457,7 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const VerifyParams p) {
     __shared__ Walk s_walk;  // the first CTA's
-    __shared__ double s_warp[kVerifyWarps];
+    __shared__ Pair s_warp[kVerifyWarps];
     __shared__ int s_first, s_last, s_any;
     __shared__ Order s_order;
 
@@ -446,7 +527,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
         if (walks) {
             __syncwarp();
             const Order o = next_order(s_walk, n, round > 0, draft != nullptr, p.chunk);
-            for (int r = lane; r < kVerifyCluster; r += 32) *cluster.map_shared_rank(&s_order, r) = o;
+            if (lane < kVerifyCluster) *cluster.map_shared_rank(&s_order, lane) = o;
+            if (round == 0 && draft == nullptr)
+                for (int r = 1; r < kVerifyCluster; ++r) {
+                    Walk* theirs = cluster.map_shared_rank(&s_walk, r);
+                    theirs->p[lane] = s_walk.p[lane];
+                    theirs->p[lane + 32] = s_walk.p[lane + 32];
+                }
         }
         cluster.sync();
         const Order o = s_order;
@@ -456,16 +543,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
         const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
         const int run = rank * kVerifyWarps + warp;
         const int64_t begin = static_cast<int64_t>(run) * p.chunk;
-        double sum = 0.0;
+        Pair sum;
         bool bad = false;
         if (begin < p.vocab) {
             const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
             sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tok, o.gone, bad);
-            sum = warp_sum_double(sum);
         }
         if (bad) flags |= FDEC_DEVERR_PROB;
-        if (lane == 0) cluster.map_shared_rank(&s_walk, 0)->sum[run] = sum;
+        if (lane < kVerifyCluster) cluster.map_shared_rank(&s_walk, lane)->sum[run] = sum;
         cluster.sync();
+        if (o.last) {  // every CTA has all sums and draws alike
+            if (warp == 0) {
+                Order mine = o;
+                mine.gone = o.fallen;
+                const bool drawn = draw_run(s_walk, o.weighed, o.row_gone, o.u, p.chunk, mine);
+                if (lane == 0 && drawn) s_order = mine;
+            }
+            __syncthreads();
+            if (s_order.op == kDraw) break;
+        }
     }
 
     const Order o = s_order;
@@ -492,7 +588,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
         const int v0 = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(tid) * per));
         const int v1 = min(end, v0 + per);
         constexpr int U = 8;
-        double mine = 0.0;
+        const Pair weight = pair_of(o.s), target_sum = pair_of(o.target);
+        Pair mine;
         for (int v = v0; v < v1; v += U) {
             float a[U], c[U];
 #pragma unroll
@@ -502,39 +599,48 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
             }
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (v + k < v1) mine += rest_of(a[k], c[k], qrow != nullptr, v + k, o.s, s_walk.tok, o.gone);
+                if (v + k < v1) add_token(mine, a[k], c[k], qrow != nullptr, v + k, weight, s_walk.tok, o.gone);
         }
-        double upto = warp_scan_double(mine);
-        if (lane == 31) s_warp[warp] = upto;
+        const bool some = mine.hi > 0.f;
+        const Pair scan = warp_scan(mine);
+        if (lane == 31) s_warp[warp] = scan;
         if (tid == 0) {
             s_first = kVerifyThreads;
             s_last = -1;
             s_any = p.vocab;
         }
         __syncthreads();
-        for (int k = 0; k < warp; ++k) upto += s_warp[k];
-        if (mine > 0.0) {
-            if (upto > o.target) atomicMin(&s_first, tid);
+        Pair before;
+        for (int k = 0; k < warp; ++k) before.add(s_warp[k].hi, s_warp[k].lo);
+        Pair upto = before;
+        upto.add(scan.hi, scan.lo);
+        if (some) {
+            if (upto.above(target_sum)) atomicMin(&s_first, tid);
             atomicMax(&s_last, tid);
         }
+        const float prior_hi = __shfl_up_sync(0xffffffffu, scan.hi, 1), prior_lo = __shfl_up_sync(0xffffffffu, scan.lo, 1);
+        if (lane > 0) before.add(prior_hi, prior_lo);
         __syncthreads();
         if (tid == (s_first < kVerifyThreads ? s_first : s_last)) {
-            double at = upto - mine;
             int token = -1;
             for (int v = v0; v < v1; ++v) {
-                const double r = rest_of(value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, o.s,
-                                         s_walk.tok, o.gone);
-                if (r > 0.0) token = v;
-                at += r;
-                if (r > 0.0 && at > o.target) break;
+                Pair here;
+                add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
+                          s_walk.tok, o.gone);
+                if (!(here.hi > 0.f)) continue;
+                token = v;
+                before.add(here.hi, here.lo);
+                if (before.above(target_sum)) break;
             }
             p.out_tokens[out + o.place] = token;
         }
         if (s_last < 0) {  // (only by rounding: the run has no weight after all; the first token that has some)
-            for (int v = tid; v < p.vocab; v += kVerifyThreads)
-                if (rest_of(value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, o.s, s_walk.tok, o.gone) >
-                    0.0)
-                    atomicMin(&s_any, v);
+            for (int v = tid; v < p.vocab; v += kVerifyThreads) {
+                Pair here;
+                add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
+                          s_walk.tok, o.gone);
+                if (here.hi > 0.f) atomicMin(&s_any, v);
+            }
             __syncthreads();
             if (tid == 0) p.out_tokens[out + o.place] = s_any < p.vocab ? s_any : -1;
         }
