@@ -6,19 +6,23 @@
 //   max(max(p - s q, 0) / W - q, 0) = max(p - (s + W) q, 0) / W      (q >= 0),
 // so one number s stands for all of them and every sum reads the same two rows.
 //
-// A cluster of CTAs takes one sequence; each warp sums a run of the vocabulary.  The first
-// CTA walks: it reads all children's p and q at once, decides, and tells the others
-// the next sum (node, s), or the run of the vocabulary in which the next token lies; they
-// send it their sums.  No CTA decides for itself, so they cannot disagree on how often they
-// meet.
+// A cluster of eight CTAs takes one sequence; each warp sums a run of the vocabulary.  The first
+// CTA reads what the walk goes by, all children's p and q among it, and copies it into the
+// others' shared memory; every warp's sum goes to all CTAs.  Each CTA then walks for itself on the
+// same bits, so all of them agree, even on inputs that change under them: a sum costs one
+// barrier of the cluster, and the draw none.  (Orders of the first CTA to the others, a second
+// barrier a sum: 17.2 us instead of 14.6 for 16 trees.)
 //
 // A token is the first whose cumulative weight passes u W, among 10^5 borders, so sums of
 // fp32 rounding would often give another token than exact ones.  Each term p - s q is
 // taken as a pair of fp32 values (Dekker's and Knuth's error-free sums and products) and
-// added up in pairs, about 46 bits, 20 fp32 instructions a term; fp64 units would need
-// 20 times as long.  Between warps and CTAs sums are fp64, in a fixed order.
+// added up in pairs, about 46 bits, 13 to 20 fp32 instructions a term.  fp64 units do two
+// products a clock and SM here: with the warps' sums and the search in a run in fp64 alone,
+// 64 rows of 131072 took 31 us instead of 21.
 //
-// Bytes: the rows p and q of the last node, once from HBM.
+// Bytes: the rows p and q of the last node, once from HBM.  64 sequences, p and q of 131072 in
+// fp32: 20 us, 3.0 TB/s; all sequences read their tokens, sum and search at the same time,
+// so 8 us of latencies (what one sequence takes) come on top of the 9 us for the bytes.
 #include <algorithm>
 #include <cstdint>
 
@@ -37,11 +41,11 @@ namespace {
 constexpr int kVerifyWarps = 8;
 constexpr int kVerifyThreads = kVerifyWarps * 32;
 constexpr int kVerifyCluster = 8;  // CTAs of a sequence
-constexpr int kRuns = kVerifyCluster * kVerifyWarps;
+constexpr int kRuns = kVerifyCluster * kVerifyWarps;  // of the vocabulary: a warp's each
 
 enum Op : int { kSum = 0, kDraw = 1, kStop = 2 };
 
-struct Order {       // what the first CTA tells the others
+struct Order {       // what comes next
     int op;
     int node;        // whose rows
     int run;         // kDraw: the warp's run of the vocabulary that holds the token
@@ -49,13 +53,6 @@ struct Order {       // what the first CTA tells the others
     double s;        // weight of q
     double target;   // kDraw: cumulative weight to pass, from the run's begin
     uint64_t gone;   // without draft rows: children whose tokens have lost their weight
-    // kSum: whether the next token is drawn from these sums, wherever they have weight (last); less those of the
-    // tokens of the children `weighed`, row_gone in all.
-    int last;
-    float u;
-    uint64_t weighed;
-    double row_gone;
-    uint64_t fallen;  // gone, once it is drawn
 };
 
 __device__ __forceinline__ float value(const float* p) { return *p; }
@@ -146,27 +143,33 @@ __device__ __forceinline__ void add_rest(Pair& sum, float p, float q, Pair s) {
     }
 }
 
+// A drafted token as the walk sees it.
+struct Node {
+    int tok, par;
+    float p, q, u;  // at its token, in its parent's rows; its random number
+};
+
 // Whether token v is that of one of the children `gone`.
-__device__ __forceinline__ bool is_gone(int v, const int* tokens, uint64_t gone) {
+__device__ __forceinline__ bool is_gone(int v, const Node* nodes, uint64_t gone) {
     for (uint64_t m = gone; m != 0; m &= m - 1)
-        if (tokens[__ffsll(static_cast<long long>(m)) - 1] == v) return true;
+        if (nodes[__ffsll(static_cast<long long>(m)) - 1].tok == v) return true;
     return false;
 }
 
 // What is left of the target at token v, added to a sum.
-__device__ __forceinline__ void add_token(Pair& sum, float p, float q, bool drafted, int v, Pair s, const int* tokens,
+__device__ __forceinline__ void add_token(Pair& sum, float p, float q, bool drafted, int v, Pair s, const Node* nodes,
                                           uint64_t gone) {
     bool bad = false;
     const float x = bounded(p, bad);
     if (drafted)
         add_rest<false>(sum, x, bounded(q, bad), s);
-    else if (!is_gone(v, tokens, gone))
+    else if (!is_gone(v, nodes, gone))
         sum.add(x, 0.f);
 }
 
 // One lane's part of a warp's sum over tokens [begin, end).  PLAIN: probabilities are taken as they are, and the largest
 // of their bits are noted (as unsigned numbers, all that are not in [0, 2] are above those of 2).
-template <typename T, bool VEC, int MODE, bool PLAIN>  // MODE 0: p, 1: max(p - q, 0), 2: max(p - s q, 0)
+template <typename T, bool VEC, int MODE, bool PLAIN, int AHEAD>  // MODE 0: p, 1: max(p - q, 0), 2: max(p - s q, 0)
 __device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int end, Pair s, uint32_t& most, bool& bad) {
     const int lane = threadIdx.x & 31;
     Pair sum;
@@ -184,7 +187,7 @@ __device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int 
             sum.add(a, 0.f);
     };
     if constexpr (VEC) {
-        constexpr int U = 4;
+        constexpr int U = MODE > 0 ? AHEAD : 2 * AHEAD;
         for (int v0 = begin + lane * 4; v0 < end; v0 += U * 128) {
             float a[U][4], c[U][4];
 #pragma unroll
@@ -203,7 +206,7 @@ __device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int 
                 for (int k = 0; k < 4; ++k) term(a[u][k], c[u][k]);
         }
     } else {
-        constexpr int U = 8;
+        constexpr int U = (MODE > 0 ? 2 : 4) * AHEAD;
         for (int v0 = begin + lane; v0 < end; v0 += U * 32) {
             float a[U], c[U];
 #pragma unroll
@@ -220,17 +223,18 @@ __device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int 
     return sum;
 }
 
-template <typename T, bool VEC, int MODE>
+template <typename T, bool VEC, int MODE, int AHEAD>
 __device__ __forceinline__ Pair mode_sum(const T* p, const T* q, int begin, int end, Pair s, bool& bad) {
     uint32_t most = 0;
-    Pair sum = lane_sum<T, VEC, MODE, true>(p, q, begin, end, s, most, bad);
-    if (__any_sync(0xffffffffu, most > 0x40000000u)) sum = lane_sum<T, VEC, MODE, false>(p, q, begin, end, s, most, bad);
+    Pair sum = lane_sum<T, VEC, MODE, true, AHEAD>(p, q, begin, end, s, most, bad);
+    if (__any_sync(0xffffffffu, most > 0x40000000u))
+        sum = lane_sum<T, VEC, MODE, false, 2>(p, q, begin, end, s, most, bad);
     return sum;
 }
 
-// One warp's sum over tokens [begin, end).
-template <typename T, bool VEC>
-__device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, double s, const int* tokens,
+// One warp's sum over tokens [begin, end).  AHEAD: vectors of each row in flight a lane.
+template <typename T, bool VEC, int AHEAD>
+__device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, double s, const Node* nodes,
                                         uint64_t gone, bool& bad) {
     const int lane = threadIdx.x & 31;
     Pair sum;
@@ -239,7 +243,7 @@ __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int e
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = lane + 32 * h;
-            hit |= (gone >> i & 1) && tokens[i] >= begin && tokens[i] < end;
+            hit |= (gone >> i & 1) && nodes[i].tok >= begin && nodes[i].tok < end;
         }
     }
     if (__any_sync(0xffffffffu, hit)) {
@@ -251,15 +255,15 @@ __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int e
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float x = bounded(a[u], bad);
-                sum.add(is_gone(v0 + u * 32, tokens, gone) ? 0.f : x, 0.f);
+                sum.add(is_gone(v0 + u * 32, nodes, gone) ? 0.f : x, 0.f);
             }
         }
     } else if (q == nullptr) {
-        sum = mode_sum<T, VEC, 0>(p, q, begin, end, sum, bad);
+        sum = mode_sum<T, VEC, 0, AHEAD>(p, q, begin, end, sum, bad);
     } else if (s == 1.0) {  // the first to fall: nearly all sums
-        sum = mode_sum<T, VEC, 1>(p, q, begin, end, sum, bad);
+        sum = mode_sum<T, VEC, 1, AHEAD>(p, q, begin, end, sum, bad);
     } else {
-        sum = mode_sum<T, VEC, 2>(p, q, begin, end, pair_of(s), bad);
+        sum = mode_sum<T, VEC, 2, AHEAD>(p, q, begin, end, pair_of(s), bad);
     }
     return warp_sum(sum);
 }
@@ -274,11 +278,16 @@ __device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
     return v;
 }
 
-// The walk of the first CTA.
+// What a walk goes by: the same bits in every CTA.
+struct Tree {
+    int n;
+    Node node[kMaxNodes];
+};
+
 struct Walk {
-    Pair sum[kRuns];  // every warp's sum
-    int tok[kMaxNodes], par[kMaxNodes], path[kMaxNodes];
-    float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];  // at each node's token, in its parent's rows; its random number
+    Tree tree;
+    Pair sum[2][kRuns];  // every warp's sum, of even and of odd rounds
+    int path[kMaxNodes];
     double s, W;
     // Without draft rows: the target's row is summed once, and a token that falls is taken from that sum.  The
     // difference keeps the sum's absolute error, so that where it is small (exact) the row is summed without the tokens.
@@ -290,36 +299,32 @@ struct Walk {
     bool whole;  // the target's row itself is summed, whatever has fallen
 };
 
-// The run of the vocabulary that holds the next token (o.run, o.target), from every warp's sum, less the tokens of the
-// children `weighed`.  A warp; false where the sums have no weight, or not enough to be a difference of sums.
-__device__ __forceinline__ bool draw_run(const Walk& walk, uint64_t weighed, double row_gone, float u, int chunk, Order& o) {
+// The run of the vocabulary that holds the next token (o.run, o.target), from every warp's sum (a lane's `mine`, their
+// sum, the sum up to the lane), less the tokens of the children `weighed`.  A warp; false where nothing is left.
+constexpr int kRunsPerLane = kRuns / 32;
+__device__ __forceinline__ bool draw_run(const Tree& tree, double (&mine)[kRunsPerLane], double part, double upto,
+                                         uint64_t weighed, int chunk, Order& o) {
     const int lane = threadIdx.x & 31;
-    constexpr int PER = (kRuns + 31) / 32;
-    double mine[PER], part = 0.0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) part += mine[k] = walk.sum[lane * PER + k].value();
-    double upto = warp_scan_double(part);
-    double W = __shfl_sync(0xffffffffu, upto, 31);
+    constexpr int PER = kRunsPerLane;
     if (weighed != 0) {
-        if (!((W - row_gone) * 64.0 > W)) return false;
         part = 0.0;
         for (uint64_t m = weighed; m != 0; m &= m - 1) {
             const int c = __ffsll(static_cast<long long>(m)) - 1;
-            const int run = walk.tok[c] / chunk;
+            const int run = tree.node[c].tok / chunk;
 #pragma unroll
             for (int k = 0; k < PER; ++k)
                 if (run == lane * PER + k) {
-                    const double rest = mine[k] - static_cast<double>(walk.p[c]);
+                    const double rest = mine[k] - static_cast<double>(tree.node[c].p);
                     mine[k] = rest > mine[k] * 0x1p-42 ? rest : 0.0;  // (what rounding left is nothing)
                 }
         }
 #pragma unroll
         for (int k = 0; k < PER; ++k) part += mine[k];
         upto = warp_scan_double(part);
-        W = __shfl_sync(0xffffffffu, upto, 31);
     }
+    const double W = __shfl_sync(0xffffffffu, upto, 31);
     if (!(W > 0.0)) return false;
-    const double goal = static_cast<double>(u) * W;
+    const double goal = static_cast<double>(tree.node[0].u) * W;
     int run = -1, last = -1;
     double at = upto - part, from = 0.0;
 #pragma unroll
@@ -345,12 +350,14 @@ __device__ __forceinline__ bool draw_run(const Walk& walk, uint64_t weighed, dou
     return true;
 }
 
-// What comes next: the first CTA's first warp, after the sums that were asked for have come (sums).
-__device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool drafted, int chunk) {
+// What comes next: a CTA's first warp, at the beginning (no sums) and whenever all sums have come.
+__device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, bool drafted, int chunk) {
     const int lane = threadIdx.x & 31;
-    constexpr int PER = (kRuns + 31) / 32;
-    const int par0 = walk.par[lane], par1 = walk.par[lane + 32];
-    const int tok0 = walk.tok[lane], tok1 = walk.tok[lane + 32];
+    constexpr int PER = kRunsPerLane;
+    const Tree& tree = walk.tree;
+    // (nodes past the last have not been given)
+    const int par0 = lane < tree.n ? tree.node[lane].par : -1, par1 = lane + 32 < tree.n ? tree.node[lane + 32].par : -1;
+    const int tok0 = lane < tree.n ? tree.node[lane].tok : -1, tok1 = lane + 32 < tree.n ? tree.node[lane + 32].tok : -1;
     const auto children = [&](int node) {
         return static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == node)) |
                static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
@@ -359,7 +366,7 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
     double s = 0.0, W = 1.0, row_total = 0.0, row_gone = 0.0;
     uint64_t gone = 0, left = 0, weighed = 0;
     bool have_row = false, exact = false, summed = false, whole = false;
-    if (sums) {
+    if (sums != nullptr) {
         x = walk.x, len = walk.len;
         s = walk.s, W = walk.W, row_total = walk.row_total, row_gone = walk.row_gone;
         gone = walk.gone, left = walk.left, weighed = walk.weighed;
@@ -370,13 +377,16 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
     }
     Order o = {};
     o.op = kStop;
-    if (n > 0) {
-        bool ask = false;
-        if (sums) {  // the sums that were asked for
-            double part = 0.0;
+    double mine[PER], part = 0.0, upto = 0.0;
 #pragma unroll
-            for (int k = 0; k < PER; ++k) part += walk.sum[lane * PER + k].value();
-            W = __shfl_sync(0xffffffffu, warp_scan_double(part), 31);
+    for (int k = 0; k < PER; ++k) mine[k] = 0.0;
+    if (tree.n > 0) {
+        bool ask = false;
+        if (sums != nullptr) {  // the sums that were asked for
+#pragma unroll
+            for (int k = 0; k < PER; ++k) part += mine[k] = sums[lane * PER + k].value();
+            upto = warp_scan_double(part);
+            W = __shfl_sync(0xffffffffu, upto, 31);
             summed = true;
             if (!drafted && !exact && !whole) {
                 row_total = W;
@@ -389,16 +399,16 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
         while (left != 0 && !ask) {
             const int c = __ffsll(static_cast<long long>(left)) - 1;
             left &= left - 1;
-            const int t = walk.tok[c];
-            double rest = walk.p[c];
+            const int t = tree.node[c].tok;
+            double rest = tree.node[c].p;
             if (drafted) {
-                rest = fmax(rest - s * static_cast<double>(walk.q[c]), 0.0);
+                rest = fmax(rest - s * static_cast<double>(tree.node[c].q), 0.0);
             } else {
                 const uint64_t same = static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok0 == t)) |
                                       static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok1 == t)) << 32;
                 if (same & gone) rest = 0.0;
             }
-            if (static_cast<double>(walk.u[c]) * W * static_cast<double>(walk.q[c]) < rest) {
+            if (static_cast<double>(tree.node[c].u) * W * static_cast<double>(tree.node[c].q) < rest) {
                 x = c;
                 if (lane == 0) walk.path[len] = c;
                 ++len;
@@ -420,7 +430,7 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
             }
         }
         const bool plain = drafted || exact || whole;  // (the sums are those of what is left)
-        if (!ask && !(summed && draw_run(walk, plain ? 0 : weighed, row_gone, walk.u[0], chunk, o))) {  // no child stands
+        if (!ask && !(summed && draw_run(tree, mine, part, upto, plain ? 0 : weighed, chunk, o))) {  // no child stands
             if (summed) {  // nothing is left: the target's row itself, if that is not it already
                 ask = !whole;
                 s = 0.0, gone = 0;
@@ -429,14 +439,7 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
             }
             whole = true;
         }
-        if (ask) {
-            o.op = kSum;
-            o.last = left == 0;
-            o.u = walk.u[0];
-            o.weighed = drafted || exact || whole ? 0 : weighed;
-            o.row_gone = row_gone;
-            o.fallen = gone;
-        }
+        if (ask) o.op = kSum;
         o.node = x;
         o.s = s;
         // (a plain sum of the row first; without its tokens where it must be exact)
@@ -454,9 +457,10 @@ __device__ __noinline__ Order next_order(Walk& walk, int n, bool sums, bool draf
     return o;
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const VerifyParams p) {
-    __shared__ Walk s_walk;  // the first CTA's
+// AHEAD: vectors of each row in flight a lane.
+template <typename T, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_drafts_kernel(const VerifyParams p) {
+    __shared__ Walk s_walk;
     __shared__ Pair s_warp[kVerifyWarps];
     __shared__ int s_first, s_last, s_any;
     __shared__ Order s_order;
@@ -474,68 +478,63 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
     const T* target = static_cast<const T*>(p.target) + static_cast<int64_t>(b) * p.t_seq;
     const T* draft = p.draft != nullptr ? static_cast<const T*>(p.draft) + static_cast<int64_t>(b) * p.d_seq : nullptr;
     unsigned flags = 0;
-    int n = p.node_counts != nullptr ? p.node_counts[b] : N;
-    int par = tid - 1, tok = -1;
-    float u = 0.f;
-    if (tid < N) {  // (read before n is there)
-        const int64_t at = static_cast<int64_t>(b) * N + tid;
-        tok = p.tokens[at];
-        if (rank == 0) {
+    if (rank == 0 && tid < kMaxNodes) {
+        int n = p.node_counts != nullptr ? p.node_counts[b] : N;
+        int par = tid - 1, tok = -1;
+        float u = 0.f;
+        if (tid < N) {  // (read before n is there)
+            const int64_t at = static_cast<int64_t>(b) * N + tid;
+            tok = p.tokens[at];
             if (p.parents != nullptr) par = p.parents[at];
             u = p.uniforms[at];
         }
-    }
-    if (n < 0 || n > N) {
-        flags |= FDEC_DEVERR_SEQ_LEN;
-        n = min(max(n, 0), N);
-    }
-    if (tid < kMaxNodes) {
-        s_walk.tok[tid] = tid < n && tid > 0 ? tok : -1;
-        if (rank == 0) {
-            if (tid >= n) par = -1;
-            if (par < -1 || par >= tid) {
+        if (n < 0 || n > N) {
+            flags |= FDEC_DEVERR_SEQ_LEN;
+            n = min(max(n, 0), N);
+        }
+        if (tid >= n) par = -1;
+        if (par < -1 || par >= tid) {
+            flags |= FDEC_DEVERR_TREE;
+            par = -1;
+        }
+        float pv = 0.f, qv = 1.f;
+        if (tid > 0 && tid < n && par >= 0) {
+            if (tok < 0 || tok >= p.vocab) {
                 flags |= FDEC_DEVERR_TREE;
                 par = -1;
+            } else {
+                bool bad = false;
+                pv = bounded(value(target + par * p.t_node + tok), bad);
+                if (draft != nullptr) qv = bounded(value(draft + par * p.d_node + tok), bad);
+                if (bad) flags |= FDEC_DEVERR_PROB;
             }
-            u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
-            float pv = 0.f, qv = 1.f;
-            if (tid > 0 && tid < n && par >= 0) {
-                const int t = tok;
-                if (t < 0 || t >= p.vocab) {
-                    flags |= FDEC_DEVERR_TREE;
-                    par = -1;
-                } else {
-                    bool bad = false;
-                    pv = bounded(value(target + par * p.t_node + t), bad);
-                    if (draft != nullptr) qv = bounded(value(draft + par * p.d_node + t), bad);
-                    if (bad) flags |= FDEC_DEVERR_PROB;
-                }
-            }
-            s_walk.par[tid] = tid < n ? par : -1;
-            s_walk.p[tid] = pv;
-            s_walk.q[tid] = qv;
-            s_walk.u[tid] = u;
         }
+        Node& node = s_walk.tree.node[tid];
+        node.tok = tid < n && tid > 0 ? tok : -1;
+        node.par = par;
+        node.p = pv;
+        node.q = qv;
+        node.u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
+        if (tid == 0) s_walk.tree.n = n;
     }
     __syncthreads();
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // and so do the others, whose memory is written next
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs run: their memory is written next
+    if (rank == 0 && warp > 0 && warp < kVerifyCluster) {
+        const int* from = reinterpret_cast<const int*>(&s_walk.tree);
+        int* to = reinterpret_cast<int*>(cluster.map_shared_rank(&s_walk.tree, warp));
+        const int words = 1 + s_walk.tree.n * static_cast<int>(sizeof(Node) / 4);
+        for (int i = lane; i < words; i += 32) to[i] = from[i];
+    }
+    cluster.sync();
 
-    const bool walks = rank == 0 && warp == 0;
-
+    const int n = s_walk.tree.n;
     // (at most two sums for every child and two for the draw)
     for (int round = 0; round < 2 * kMaxNodes + 3; ++round) {
-        if (walks) {
-            __syncwarp();
-            const Order o = next_order(s_walk, n, round > 0, draft != nullptr, p.chunk);
-            if (lane < kVerifyCluster) *cluster.map_shared_rank(&s_order, lane) = o;
-            if (round == 0 && draft == nullptr)
-                for (int r = 1; r < kVerifyCluster; ++r) {
-                    Walk* theirs = cluster.map_shared_rank(&s_walk, r);
-                    theirs->p[lane] = s_walk.p[lane];
-                    theirs->p[lane + 32] = s_walk.p[lane + 32];
-                }
+        if (warp == 0) {
+            const Order next = next_order(s_walk, round > 0 ? s_walk.sum[(round - 1) & 1] : nullptr, draft != nullptr, p.chunk);
+            if (lane == 0) s_order = next;
         }
-        cluster.sync();
+        __syncthreads();
         const Order o = s_order;
         if (o.op != kSum) break;
         const T* prow = target + o.node * p.t_node;
@@ -547,21 +546,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
         bool bad = false;
         if (begin < p.vocab) {
             const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
-            sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tok, o.gone, bad);
+            sum = run_sum<T, VEC, AHEAD>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tree.node, o.gone, bad);
         }
         if (bad) flags |= FDEC_DEVERR_PROB;
-        if (lane < kVerifyCluster) cluster.map_shared_rank(&s_walk, lane)->sum[run] = sum;
+        if (lane < kVerifyCluster) cluster.map_shared_rank(&s_walk, lane)->sum[round & 1][run] = sum;
         cluster.sync();
-        if (o.last) {  // every CTA has all sums and draws alike
-            if (warp == 0) {
-                Order mine = o;
-                mine.gone = o.fallen;
-                const bool drawn = draw_run(s_walk, o.weighed, o.row_gone, o.u, p.chunk, mine);
-                if (lane == 0 && drawn) s_order = mine;
-            }
-            __syncthreads();
-            if (s_order.op == kDraw) break;
-        }
     }
 
     const Order o = s_order;
@@ -571,7 +560,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
             const int steps = n > 0 ? o.place + 1 : 0;
             p.path[out + tid] = tid < steps ? s_walk.path[tid] : -1;
             if (tid + 1 < steps)
-                p.out_tokens[out + tid] = s_walk.tok[s_walk.path[tid + 1]];
+                p.out_tokens[out + tid] = s_walk.tree.node[s_walk.path[tid + 1]].tok;
             else if (o.op != kDraw || tid != o.place)
                 p.out_tokens[out + tid] = -1;
             if (tid == 0) p.path_lens[b] = steps;
@@ -599,7 +588,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
             }
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (v + k < v1) add_token(mine, a[k], c[k], qrow != nullptr, v + k, weight, s_walk.tok, o.gone);
+                if (v + k < v1) add_token(mine, a[k], c[k], qrow != nullptr, v + k, weight, s_walk.tree.node, o.gone);
         }
         const bool some = mine.hi > 0.f;
         const Pair scan = warp_scan(mine);
@@ -626,7 +615,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
             for (int v = v0; v < v1; ++v) {
                 Pair here;
                 add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
-                          s_walk.tok, o.gone);
+                          s_walk.tree.node, o.gone);
                 if (!(here.hi > 0.f)) continue;
                 token = v;
                 before.add(here.hi, here.lo);
@@ -638,7 +627,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const 
             for (int v = tid; v < p.vocab; v += kVerifyThreads) {
                 Pair here;
                 add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
-                          s_walk.tok, o.gone);
+                          s_walk.tree.node, o.gone);
                 if (here.hi > 0.f) atomicMin(&s_any, v);
             }
             __syncthreads();
@@ -656,8 +645,8 @@ bool vectors(const VerifyParams& p) {
     return p.vocab % 4 == 0 && ok(p.target, p.t_seq, p.t_node) && ok(p.draft, p.d_seq, p.d_node);
 }
 
-template <typename T>
-cudaError_t launch_verify(const VerifyParams& p, cudaStream_t s) {
+template <typename T, bool VEC, int AHEAD>
+cudaError_t launch_verify_one(const VerifyParams& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * kVerifyCluster, 1, 1);
     cfg.blockDim = dim3(kVerifyThreads, 1, 1);
@@ -670,19 +659,26 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return vectors<T>(p) ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, true>, p)
-                         : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, false>, p);
+    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, AHEAD>, p);
+}
+
+template <typename T>
+cudaError_t launch_verify(VerifyParams p, int num_sms, cudaStream_t s) {
+    p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
+    // Twice the loads in flight, where the registers are there: two CTAs an SM instead of four.  (16 trees over 50021
+    // tokens 1.5 us less; clusters of 4 CTAs 1.5 us more, of 16 9 more.)
+    const bool deep = static_cast<int64_t>(p.batch) * kVerifyCluster <= num_sms * 2;
+    if (vectors<T>(p)) return deep ? launch_verify_one<T, true, 8>(p, s) : launch_verify_one<T, true, 4>(p, s);
+    return deep ? launch_verify_one<T, false, 8>(p, s) : launch_verify_one<T, false, 4>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(VerifyParams p, int prob_dtype, int num_sms, cudaStream_t s) {
-    (void)num_sms;
-    p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
+cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, int num_sms, cudaStream_t s) {
     switch (prob_dtype) {
-        case FDEC_PROB_F16: return launch_verify<__half>(p, s);
-        case FDEC_PROB_BF16: return launch_verify<__nv_bfloat16>(p, s);
-        case FDEC_PROB_F32: return launch_verify<float>(p, s);
+        case FDEC_PROB_F16: return launch_verify<__half>(p, num_sms, s);
+        case FDEC_PROB_BF16: return launch_verify<__nv_bfloat16>(p, num_sms, s);
+        case FDEC_PROB_F32: return launch_verify<float>(p, num_sms, s);
         default: return cudaErrorInvalidValue;
     }
 }
