@@ -9,10 +9,6 @@
 
 namespace fdec {
 
-constexpr int kColumnThreads = 256;
-constexpr int kColumnsPerThread = 2;
-constexpr int kColumnsPerBlock = kColumnThreads * kColumnsPerThread;
-
 // The cache whose columns block `blk` holds.
 template <int N>
 __device__ __forceinline__ const CacheRows& cache_of(const CacheList<N>& list, int blk) {
@@ -32,7 +28,7 @@ __device__ __forceinline__ const CacheRows& cache_of(const CacheList<N>& list, i
 // row may be stored where a later one was read, not the other way round.
 template <typename V, typename From, typename To>
 __device__ __forceinline__ void move_columns(const CacheRows& c, int blk, int begin, int end, From from, To to) {
-    constexpr int U = 4;
+    constexpr int U = kRowsAhead;
     const int64_t columns = static_cast<int64_t>(c.layers) * c.heads * c.row_vecs;
     uint8_t* col[kColumnsPerThread];
 #pragma unroll

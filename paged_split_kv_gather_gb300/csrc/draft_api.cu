@@ -83,7 +83,7 @@ fdec_status take_caches(const fdec_cache* caches, int num_caches, CacheList<kMax
         r.first_block = static_cast<int>(blocks);
         const int64_t columns = static_cast<int64_t>(c.num_layers) * c.num_heads;
         if (columns > INT32_MAX / r.row_vecs) return fail(FDEC_ERR_UNSUPPORTED, "too many rows at a position");
-        blocks += (columns * r.row_vecs + 511) / 512;
+        blocks += (columns * r.row_vecs + kColumnsPerBlock - 1) / kColumnsPerBlock;
         if (blocks > 1 << 24) return fail(FDEC_ERR_UNSUPPORTED, "too many rows at a position");
         *fewest = std::min(*fewest, c.num_pages);
     }
@@ -285,17 +285,19 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
 
 namespace {
 
-// Workspace of fdec_reserve_pages: two bit sets, the sequences' last pages.
+// Workspace of fdec_reserve_pages: two bit sets, pages in use by blocks, the sequences' last pages.
 struct ReserveLayout {
-    size_t off_shared, off_last, bytes;
-    int words;
+    size_t off_shared, off_taken, off_last, bytes;
+    int words, blocks;
 };
 
 bool reserve_layout(int batch, int64_t num_pages, ReserveLayout* out) {
     if (batch < 1 || num_pages < 1 || num_pages > 1 << 26) return false;
     out->words = static_cast<int>((num_pages + 31) / 32);
     out->off_shared = static_cast<size_t>(out->words) * 4;
-    out->off_last = 2 * out->off_shared;
+    out->blocks = static_cast<int>((num_pages + kCountedPages - 1) / kCountedPages);
+    out->off_taken = 2 * out->off_shared;
+    out->off_last = out->off_taken + static_cast<size_t>(out->blocks) * 4;
     out->bytes = (out->off_last + static_cast<size_t>(batch) * 4 + 255) / 256 * 256;
     return true;
 }
@@ -352,6 +354,8 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.used = reinterpret_cast<unsigned*>(ws);
     p.shared = reinterpret_cast<unsigned*>(ws + l.off_shared);
+    p.taken = reinterpret_cast<int32_t*>(ws + l.off_taken);
+    p.blocks = l.blocks;
     p.last_page = reinterpret_cast<int32_t*>(ws + l.off_last);
     p.err = device_errors;
     p.num_pages = num_pages;

@@ -341,6 +341,10 @@ struct CacheRows {
     int first_block;
 };
 constexpr int kMaxCaches = 128;
+constexpr int kColumnThreads = 256;    // of a block
+constexpr int kColumnsPerThread = 1;
+constexpr int kRowsAhead = 4;          // rows of each column in flight a thread
+constexpr int kColumnsPerBlock = kColumnThreads * kColumnsPerThread;
 template <int N>
 struct CacheList {
     CacheRows c[N];
@@ -370,11 +374,13 @@ struct ReserveParams {
     int32_t* granted;
     unsigned* used;              // [words] a bit a page: some entry in use names it
     unsigned* shared;            // [words] two do
+    int32_t* taken;              // [blocks] pages in use of every kCountedPages, if there are many
     int32_t* last_page;          // [batch] the page of a sequence's (its source's) last, partly filled part
     unsigned* err;
     int64_t num_pages;
-    int words, batch, page_shift;
+    int words, blocks, batch, page_shift;
 };
+constexpr int kCountedPages = 1024;
 cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCaches>& caches, int num_sms,
                                  cudaStream_t s);
 

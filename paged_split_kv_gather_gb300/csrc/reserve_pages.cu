@@ -2,10 +2,13 @@
 // shared ones.
 //
 // The page tables and lengths say which pages are in use; nothing else is kept, so
-// nothing can go out of step with them.  Three launches: clear two bit sets of a bit a page;
-// mark every page that an entry in use names (the second set: pages that two name); then
-// each sequence finds its pages for itself: how many pages the sequences before it need, from
-// the lengths, and which bits are its own, from the first bit set (8 KB for 65536 pages).
+// nothing can go out of step with them.  Three launches, four for large pools: clear two bit
+// sets of a bit a page; mark every page that an entry in use names (the second set: pages that
+// two name); then each sequence finds its pages for itself: how many pages the sequences
+// before it need, from the lengths, and which bits are its own, from the pages in use of every
+// 1024 and the first bit set.  Those numbers come from a launch of their own for pools above
+// 131072 pages (from the marking's atomics they cost 45 us, for 256 sequences and a million
+// pages, each CTA reading all bits 9 us); below, every CTA counts for itself.
 // Its CTAs copy the rows that a fork or a shared last page needs.
 //
 // Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.
@@ -133,6 +136,25 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_mark_kernel(const Res
     if (flags != 0 && p.err != nullptr) atomicOr(p.err, flags);
 }
 
+// Up to so many blocks of pages (131072 pages) every CTA counts what is in use for itself.
+constexpr int kOwnBlocks = 128;
+
+// Pages in use of block j: a warp, a word of the bit set for each lane.
+__device__ __forceinline__ int taken_of(const ReserveParams& p, int j) {
+    const int w = j * (kCountedPages / 32) + (threadIdx.x & 31);
+    return __reduce_add_sync(0xffffffffu, w < p.words ? __popc(p.used[w]) : 0);
+}
+
+__global__ void __launch_bounds__(kReserveThreads) reserve_count_kernel(const ReserveParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warps = gridDim.x * (kReserveThreads / 32);
+    for (int j = blockIdx.x * (kReserveThreads / 32) + (threadIdx.x >> 5); j < p.blocks; j += warps) {
+        const int taken = taken_of(p, j);
+        if ((threadIdx.x & 31) == 0) p.taken[j] = taken;
+    }
+}
+
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* s_part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -150,71 +172,103 @@ template <int N>
 __global__ void __launch_bounds__(kReserveThreads)
     reserve_assign_kernel(const __grid_constant__ ReserveParams p, const __grid_constant__ CacheList<N> caches,
                           int blocks) {
-    __shared__ int64_t s_part[kReserveThreads / 32];
-    __shared__ int s_page;
+    __shared__ int64_t s_part[kReserveThreads / 32], s_at;
+    __shared__ int s_page, s_block, s_taken[kOwnBlocks];
+    __shared__ Request s_request;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / blocks, blk = blockIdx.x % blocks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Request r = request_of(p, b);
+    // A pool's bits that the CTA counts for itself, all asked for at once.
+    const bool own = p.blocks <= kOwnBlocks;
+    constexpr int kOwnWords = kOwnBlocks / (kReserveThreads / 32);
+    unsigned bits_of[kOwnWords];
+#pragma unroll
+    for (int k = 0; k < kOwnWords; ++k) {
+        const int w = (warp + k * (kReserveThreads / 32)) * (kCountedPages / 32) + lane;
+        bits_of[k] = own && w < p.words ? p.used[w] : 0u;
+    }
+    // what this sequence asks for, and what those before it take
+    int64_t start = 0;
+    for (int i = tid; i <= b; i += kReserveThreads) {
+        const Request q = request_of(p, i);
+        if (i == b)
+            s_request = q;
+        else
+            start += q.need();
+    }
+    start = block_sum(start, s_part);
+    const Request r = s_request;
     if (blk == 0 && tid == 0 && r.bad && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
     if (blk != 0 && (r.bad || r.part == 0 || r.need() == 0)) return;  // nothing to copy
 
-    int64_t start = 0;  // pages that the sequences before this one take
     bool enough = true;
     if (r.need() > 0) {
-        for (int i = tid; i < b; i += kReserveThreads) start += request_of(p, i).need();
-        start = block_sum(start, s_part);
-        // The free pages: a run of words for each warp.  First their number, then, in the runs that hold this
-        // sequence's, page by page.
-        constexpr int kWarps = kReserveThreads / 32, U = 4;
-        const int per = ((p.words + kWarps - 1) / kWarps + 127) / 128 * 128;  // words of a warp
-        const int w0 = min(p.words, warp * per), w1 = min(p.words, w0 + per);
-        const auto free_bits = [&](int w) {
-            const int64_t behind = p.num_pages - static_cast<int64_t>(w) * 32;  // bits of the last word past the pool
-            return w < w1 ? ~p.used[w] & (behind >= 32 ? 0xffffffffu : (1u << behind) - 1) : 0u;
-        };
-        int mine = 0;  // (at most 2^26)
-        for (int w = w0 + lane; w < w1; w += 32 * U * 2) {
-            unsigned bits[2 * U];
+        // Free pages by blocks of 1024, a run of blocks for each thread: their number, and the block that holds the
+        // sequence's first.
+        if (own) {
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) bits[u] = free_bits(w + 32 * u);
-#pragma unroll
-            for (int u = 0; u < 2 * U; ++u) mine += __popc(bits[u]);
+            for (int k = 0; k < kOwnWords; ++k) {
+                const int taken = __reduce_add_sync(0xffffffffu, __popc(bits_of[k]));
+                if (lane == 0) s_taken[warp + k * (kReserveThreads / 32)] = taken;
+            }
+            __syncthreads();
         }
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        __syncthreads();
-        if (lane == 0) s_part[warp] = mine;
-        __syncthreads();
-        int64_t total = 0, at = 0;  // free pages; those before this warp's run
+        const auto free_of = [&](int j) {
+            const int64_t behind = p.num_pages - static_cast<int64_t>(j) * kCountedPages;
+            return static_cast<int>(min(behind, static_cast<int64_t>(kCountedPages))) - (own ? s_taken[j] : p.taken[j]);
+        };
+        const int per = (p.blocks + kReserveThreads - 1) / kReserveThreads;
+        const int j0 = min(p.blocks, tid * per), j1 = min(p.blocks, j0 + per);
+        int mine = 0;  // (at most 2^26)
+        for (int j = j0; j < j1; ++j) mine += free_of(j);
+        int upto = mine;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_part[warp] = upto;
+        __syncthreads();
+        int64_t total = 0, at = upto - mine;
+#pragma unroll
+        for (int w = 0; w < kReserveThreads / 32; ++w) {
             if (w < warp) at += s_part[w];
             total += s_part[w];
         }
         const int64_t end = start + r.need();
         enough = end <= total;
-        if (enough && at < end && at + mine > start) {
-            for (int w = w0; w < w1 && at < end; w += 32) {
-                unsigned bits = free_bits(w + lane);
-                const int count = __popc(bits);
-                const int all = __reduce_add_sync(0xffffffffu, count);
-                if (at + all > start) {
-                    int upto = count;
+        if (enough && at <= start && start < at + mine) {
+            int j = j0;
+            for (int here; at + (here = free_of(j)) <= start; ++j) at += here;
+            s_block = j;
+            s_at = at;
+        }
+        __syncthreads();
+        if (enough) {  // from there on, a block for each warp in turn
+            at = s_at;
+            for (int j = s_block; at < end; ++j) {
+                if ((j - s_block) % (kReserveThreads / 32) == warp) {
+                    const int w = j * (kCountedPages / 32) + lane;
+                    const int64_t behind = p.num_pages - static_cast<int64_t>(w) * 32;  // bits from this word on
+                    unsigned bits = behind <= 0 ? 0u : ~p.used[w] & (behind >= 32 ? 0xffffffffu : (1u << behind) - 1);
+                    int before = __popc(bits);
+                    const int count = before;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
-                        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                        if (lane >= o) upto += y;
+                        const int x = __shfl_up_sync(0xffffffffu, before, o);
+                        if (lane >= o) before += x;
                     }
-                    int64_t i = at + upto - count;
+                    int64_t i = at + before - count;
                     for (; bits != 0 && i < end; bits &= bits - 1, ++i) {
                         if (i < start) continue;
-                        const int page = (w + lane) * 32 + __ffs(bits) - 1;
+                        const int page = w * 32 + __ffs(bits) - 1;
                         if (blk == 0) p.page_table[b * p.pt_stride + r.first + (i - start)] = page;
                         if (i == start) s_page = page;
                     }
                 }
-                at += all;
+                at += free_of(j);
             }
         }
     }
@@ -272,6 +326,10 @@ cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCac
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(row_blocks, num_sms * 16 / p.batch));
     e = launch(reserve_mark_kernel, blocks * p.batch, s, p, static_cast<int>(blocks));
     if (e != cudaSuccess) return e;
+    if (p.blocks > kOwnBlocks) {
+        e = launch(reserve_count_kernel, std::min<int64_t>((p.blocks + 7) / 8, num_sms * 4), s, p);
+        if (e != cudaSuccess) return e;
+    }
     return caches.n <= 2 ? launch_assign<2>(p, caches, s) : launch_assign<kMaxCaches>(p, caches, s);
 }
 
