@@ -552,7 +552,8 @@ fdec_status fdec_verify_drafts(const void* target_probs, int64_t target_stride_s
  *   base + layer*stride_layer + page*stride_page + head*stride_head + slot*stride_token
  * (strides in bytes).  Keys, values, codes or block scales of any type are such rows.
  * base, strides and row_bytes are multiples of 8; rows of multiples of 16 on 16-byte
- * boundaries move faster.
+ * boundaries move faster.  No two rows of a call's caches may be the same memory (a stride of
+ * 0, or a cache given twice, is refused).
  */
 typedef struct {
     void* base;

@@ -764,6 +764,8 @@ class TreeDecode:
         batch = len(max_lens)
         if not 1 <= num_nodes <= 64:
             raise ValueError("num_nodes must be between 1 and 64")
+        if kv_dtype not in ("", "fp8"):
+            raise ValueError("drafted rows go into 16-bit and E4M3 caches")
         device = device or "cuda"
         self.batch, self.num_nodes, self.page_size, self.num_pages = batch, num_nodes, page_size, num_pages
         self.prefix = PagedDecode(max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,

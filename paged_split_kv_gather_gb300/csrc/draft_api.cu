@@ -48,8 +48,9 @@ fdec_status check_tree(int batch, int num_nodes) {
     return FDEC_OK;
 }
 
-// The caches of a call that moves rows; *fewest: the fewest pages of any.
-fdec_status take_caches(const fdec_cache* caches, int num_caches, CacheList<kMaxCaches>* out, int64_t* fewest) {
+// The caches of a call that moves rows; *fewest: the fewest pages of any.  Rows are written, so no two may be one.
+fdec_status take_caches(const fdec_cache* caches, int num_caches, int page_size, CacheList<kMaxCaches>* out,
+                        int64_t* fewest) {
     if (num_caches < 0 || num_caches > kMaxCaches) return fail(FDEC_ERR_INVALID_ARG, "between 0 and 128 caches a call");
     if (num_caches > 0 && caches == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null caches");
     *out = {};
@@ -70,6 +71,11 @@ fdec_status take_caches(const fdec_cache* caches, int num_caches, CacheList<kMax
             if (s < 0 || s % 8 != 0) return fail(FDEC_ERR_LAYOUT, "cache strides must be non-negative multiples of 8 bytes");
             wide = wide && s % 16 == 0;
         }
+        if ((c.num_layers > 1 && c.stride_layer == 0) || (c.num_pages > 1 && c.stride_page == 0) ||
+            (c.num_heads > 1 && c.stride_head == 0) || (page_size > 1 && c.stride_token == 0))
+            return fail(FDEC_ERR_LAYOUT, "a cache's rows must not lie on one another (a stride of 0)");
+        for (int j = 0; j < i; ++j)
+            if (caches[j].base == c.base) return fail(FDEC_ERR_INVALID_ARG, "a cache is given twice");
         CacheRows& r = out->c[i];
         r.base = static_cast<uint8_t*>(c.base);
         r.s_layer = c.stride_layer;
@@ -258,11 +264,13 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
         !aligned(seq_lens, 4) || !aligned(device_errors, 4))
         return fail(FDEC_ERR_LAYOUT, "misaligned index array");
     const size_t bytes = static_cast<size_t>(batch) * 4;
-    if (overlap(seq_lens, bytes, prefix_lens, bytes) || overlap(seq_lens, bytes, path_lens, bytes))
-        return fail(FDEC_ERR_INVALID_ARG, "seq_lens overlaps prefix_lens or path_lens");
+    const size_t path_bytes = (static_cast<size_t>(batch - 1) * path_stride + num_nodes) * 4;
+    if (overlap(seq_lens, bytes, prefix_lens, bytes) || overlap(seq_lens, bytes, path_lens, bytes) ||
+        overlap(seq_lens, bytes, path, path_bytes))
+        return fail(FDEC_ERR_INVALID_ARG, "seq_lens overlaps prefix_lens, path or path_lens");
     CacheList<kMaxCaches> list;
     KeepParams p = {};
-    st = take_caches(caches, num_caches, &list, &p.num_pages);
+    st = take_caches(caches, num_caches, page_size, &list, &p.num_pages);
     if (st != FDEC_OK) return st;
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
@@ -341,7 +349,7 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
                                         "fdec_reserve_pages_workspace says");
     CacheList<kMaxCaches> list;
     int64_t fewest = 0;
-    const fdec_status st = take_caches(caches, num_caches, &list, &fewest);
+    const fdec_status st = take_caches(caches, num_caches, page_size, &list, &fewest);
     if (st != FDEC_OK) return st;
     if (num_pages > fewest) return fail(FDEC_ERR_INVALID_ARG, "num_pages is more than a cache has");
     ReserveParams p = {};

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
         }
         __syncthreads();
         const uint64_t odd = s_odd[0] | static_cast<uint64_t>(s_odd[1]) << 32;
-        const int up = kRewrite ? min(14 - (static_cast<int>(s_max >> 7) - 127), 100) : 0;
+        // (110: the factor that undoes it stays a normal number; only values below 2^-112 lose by that)
+        const int up = kRewrite ? min(14 - (static_cast<int>(s_max >> 7) - 127), 110) : 0;
         const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         const float scale = fabsf(p.scale_log2);
         if (kRewrite || odd != 0 || p.scale_log2 < 0.f) {

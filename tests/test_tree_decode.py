@@ -10,7 +10,9 @@ sums of 64 terms (128 u); the split into 16-bit terms leaves 2^-22.  So a row of
 is rounded once more: half a step of the value, or of the smallest normal number.  Tokens, paths, lengths and pages are
 equal; moved rows are equal bit for bit."""
 import math
+import os
 import random
+import re
 
 import numpy as np
 import pytest
@@ -128,7 +130,7 @@ class Tree:
                     k, v = k * self.k_scale, v * self.v_scale
                     q = self.q[b, i, kvh * group:(kvh + 1) * group].double().cpu()
                     z = q @ k.T * self.scale
-                    mag = (q.abs() @ k.abs().T * self.scale).amax(-1) if where else torch.zeros(group).double()
+                    mag = (q.abs() @ k.abs().T * abs(self.scale)).amax(-1) if where else torch.zeros(group).double()
                     rows = slice(kvh * group, (kvh + 1) * group)
                     if self.lse_prefix is not None:
                         before = self.lse_prefix[b, i, rows].double().cpu()
@@ -279,6 +281,49 @@ def test_tree_attention_of_extreme_logits_and_states():
 
 
 @gpu
+@pytest.mark.parametrize("dtype,power", [("bf16", 119), ("bf16", 60), ("bf16", -30), ("bf16", -90), ("bf16", -110),
+                                         ("f16", 13), ("f16", -10)])
+def test_tree_attention_of_values_of_any_size(dtype, power):
+    """A bf16 cache's values are multiplied as f16 values: by a power of two that the largest sets."""
+    for spread in (False, True):  # one row much smaller than the others: no worse than the tolerance of the largest
+        c = Tree(128, 8, 2, 21, 16, 2, dtype, seed=13, counts=[21, 21])
+        c.v = (c.v.double() * 2.0 ** power).to(c.t)
+        if spread:
+            c.v[:, :, ::3] = (c.v[:, :, ::3].double() * 2.0 ** -20).to(c.t)
+        c.o_prefix = c.o_prefix * 2.0 ** power
+        out, lse = c.run()
+        c.check(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,kv", [(128, "bf16", ""), (256, "f16", ""), (128, "bf16", "fp8")])
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-30])
+def test_tree_attention_of_any_scale(d, dtype, kv, scale):
+    c = Tree(d, 8, 2, 37, 16, 2, dtype, kv, seed=14, counts=[37, 20])
+    c.scale = scale
+    out, lse = c.run(scale=scale)
+    c.check(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("hq,hk,nodes,batch", [(16, 8, 16, 70), (8, 8, 3, 90), (24, 3, 64, 160), (32, 4, 33, 115)])
+def test_tree_attention_in_equal_shares(hq, hk, nodes, batch):
+    """More sequences' heads than CTAs are resident: shares that begin inside a head, and span several."""
+    c = Tree(64, hq, hk, nodes, 16, batch, "f16", seed=15)
+    out, lse = c.run()
+    few = random.Random(1).sample(range(batch), 6) + [0, batch - 1]
+    counts = [n if b in few else 0 for b, n in enumerate(c.counts)]
+    c.check(out, lse, counts=counts)
+    # the others against calls of few sequences, which are not shared out
+    for b in range(0, batch, 16):
+        part = slice(b, min(batch, b + 16))
+        o, l2 = torch.full_like(out[part], 3.0), torch.full_like(lse[part], 5.0)
+        fd.fdec_tree_attention(c.q[part], c.k, c.v, i32(c.table[part]), i32(c.prefix[part]), i32(c.parents[part]),
+                               c.o_prefix[part], c.lse_prefix[part], o, l2, 16, node_counts=i32(c.counts[part]))
+        assert torch.equal(o, out[part]) and torch.equal(l2, lse[part])
+
+
+@gpu
 def test_tree_attention_flags_bad_trees_pages_and_lengths():
     def flags(c, parents=None, counts=None, prefix=None, table=None):
         err = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -412,13 +457,15 @@ def drafts_of(g, rng, batch, nodes, vocab, dtype, kind, drafts, noise=0.7):
     return target, draft.cuda() if drafts else None, tokens, parents
 
 
+VERIFY_TREES = [("chain", 1, False), ("chain", 5, True), ("tree", 12, True), ("star", 9, True), ("tree", 26, False),
+                ("star", 64, False)]
+
+
 @gpu
-@pytest.mark.parametrize("vocab", [1, 2, 5, 127, 128, 1000, 4099, 50021, 131072])
-@pytest.mark.parametrize("kind,nodes,drafts", [("chain", 1, False), ("chain", 5, True), ("tree", 12, True),
-                                               ("star", 9, True), ("tree", 26, False), ("star", 64, False)])
+@pytest.mark.parametrize("vocab,kind,nodes,drafts", [
+    (vocab, *tree) for vocab in (1, 2, 5, 127, 128, 1000, 4099, 50021, 131072) for tree in VERIFY_TREES
+    if vocab * tree[1] <= 4_000_000])
 def test_verify_drafts(vocab, kind, nodes, drafts):
-    if vocab * nodes > 4_000_000:
-        pytest.skip("covered by the smaller trees")
     seed = vocab + nodes
     g, rng = torch.Generator().manual_seed(seed), random.Random(seed)
     batch = 4 if vocab > 10000 else 24
@@ -442,6 +489,32 @@ def test_verify_drafts_goes_deep_and_tries_many_children():
     target, draft, tokens, parents = drafts_of(g, rng, 16, 40, 500, "f32", "star", True, noise=6.0)
     lens = check_verify(target, draft, tokens, parents, torch.rand((16, 40), generator=g) * 0.2 + 0.8)
     assert 1 in lens and 2 in lens
+
+
+@gpu
+@pytest.mark.parametrize("vocab,dtype", [(300, "f32"), (4096, "bf16"), (4099, "f16")])
+def test_verify_drafts_of_many_sequences(vocab, dtype):
+    g, rng = torch.Generator().manual_seed(2), random.Random(2)
+    for drafts in (True, False):
+        target, draft, tokens, parents = drafts_of(g, rng, 60, 7, vocab, dtype, "tree", drafts)
+        check_verify(target, draft, tokens, parents, torch.rand((60, 7), generator=g))
+
+
+@gpu
+def test_weights_that_are_nearly_gone():
+    """Children whose tokens take nearly all of the target's weight along: what is left is summed without them."""
+    g = torch.Generator().manual_seed(8)
+    batch, nodes, vocab = 16, 5, 3000
+    rest = torch.softmax(torch.randn((batch, nodes, vocab), generator=g) * 2, -1)
+    for left in (1e-2, 1e-5, 1e-8):
+        p = rest * left
+        p[:, :, 100:104] = (1 - left) / 4
+        u = torch.ones((batch, nodes))
+        u[:, 0] = torch.rand(batch, generator=g)
+        tokens = [[0, 100, 101, 102, 103]] * batch
+        # every child's number is above its chance: only the rest is left, where the fp32 numbers allow that
+        lens = check_verify(p.float().cuda(), None, tokens, [[-1, 0, 0, 0, 0]] * batch, u * (1 - 2.0 ** -24))
+        assert set(lens) <= {1, 2}
 
 
 @gpu
@@ -992,6 +1065,77 @@ def test_calls_use_the_stream_they_are_given():
         fd.fdec_verify_drafts(late, draft, tok, None, u, path, lens, words)
     stream.synchronize()
     assert torch.equal(path.cpu(), want[0]) and torch.equal(words.cpu(), want[2])
+    # pages, then rows, on that stream, lengths written just before
+    pool = torch.randn(12, 2, 16, 64).half().cuda()
+    fresh, table = pool.clone(), i32(np.arange(12).reshape(2, 6))
+    prefix, soon = i32([3, 20]), torch.zeros(2, dtype=torch.int32, device="cuda")
+    kept, path_lens = i32([[0, 4, 9] + [-1] * 13, [2, 3, 15] + [-1] * 13]), i32([3, 2])  # of 16 nodes
+    out, granted, table2 = torch.empty_like(soon), torch.empty_like(soon), i32(np.full((2, 6), -1))
+    ws = torch.empty(fd.fdec_reserve_pages_workspace(2, 12), dtype=torch.uint8, device="cuda")
+    more, none = i32([33, 17]), torch.full((2,), 7, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(2_000_000)
+        soon.copy_(prefix)
+        none.zero_()
+        fd.fdec_keep_path([pool], table, soon, kept, path_lens, out, 16)
+        fd.fdec_reserve_pages(table2, none, more, granted, 12, 16, ws)
+    stream.synchronize()
+    want = keep_reference([fresh], table.cpu().numpy(), [3, 20], kept.tolist(), [3, 2], 16)[0]
+    assert torch.equal(pool, want) and out.tolist() == [6, 22]
+    assert granted.tolist() == [33, 17] and table2[:, :3].tolist() == [[0, 1, 2], [3, 4, -1]]
+
+
+@gpu
+def test_two_captured_graphs_of_one_holder():
+    """The rounds of two batches of one size, captured one after the other with the same workspaces, replayed in turns."""
+    batch, nodes, page, pages, vocab = 3, 6, 16, 64, 200
+    g, rng = torch.Generator().manual_seed(10), random.Random(10)
+    tree = fd.TreeDecode([200] * batch, nodes, page, 8, 2, 64, pages, "f16")
+    sides = []
+    for _ in range(2):
+        target, draft, tokens, parents = drafts_of(g, rng, batch, nodes, vocab, "f32", "tree", False)
+        side = dict(target=target, tokens=i32(tokens), parents=i32(parents), u=torch.rand((batch, nodes), generator=g).cuda(),
+                    table=torch.full((batch, 13), -1, dtype=torch.int32, device="cuda"),
+                    lens=i32([0] * batch), pool=torch.randn(pages, 2, page, 64).half().cuda(),
+                    out=[torch.zeros_like(tree.path), torch.zeros_like(tree.path_lens), torch.zeros_like(tree.path)])
+        sides.append(side)
+
+    def step(s):
+        tree.reserve(s["table"], s["lens"])
+        got = tree.verify(s["target"], None, s["tokens"], s["parents"], s["u"])
+        for a, b in zip(s["out"], got):
+            a.copy_(b)
+        s["lens"].copy_(tree.keep([s["pool"]], s["table"], s["lens"]))
+
+    graphs = []
+    for s in sides:
+        saved = {k: s[k].clone() for k in ("table", "lens", "pool")}
+        step(s)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(s)
+        for k, v in saved.items():
+            s[k].copy_(v)
+    want = [dict(table=s["table"].cpu().numpy(), lens=[0] * batch, pool=s["pool"].clone()) for s in sides]
+    for turn in range(8):
+        which = rng.randrange(2)
+        s, w = sides[which], want[which]
+        graphs[which].replay()
+        torch.cuda.synchronize()
+        w["table"], granted, _ = reserve_reference(w["table"], w["lens"], [n + nodes for n in w["lens"]], None, pages, page)
+        paths = []
+        for b in range(batch):
+            path, words, _ = verify_reference(s["target"][b].cpu().numpy(), None, s["tokens"][b].tolist(),
+                                              s["parents"][b].tolist(), s["u"][b].tolist(), nodes)
+            paths.append(path)
+            assert s["out"][0][b].tolist()[:len(path)] == path and s["out"][2][b].tolist()[:len(words)] == words
+        w["pool"] = keep_reference([w["pool"]], w["table"], w["lens"], paths, [len(p) for p in paths], page)[0]
+        w["lens"] = [n + len(p) for n, p in zip(w["lens"], paths)]
+        assert s["lens"].tolist() == w["lens"] and np.array_equal(s["table"].cpu().numpy(), w["table"])
+        assert torch.equal(s["pool"], w["pool"])
+    assert tree.device_errors() == 0
 
 
 # ------------------------------------------------------------------------------------------------------------ refusals
@@ -1111,6 +1255,15 @@ def test_keep_path_refusals():
     refused("FDEC_ERR_LAYOUT", cpu_keep, caches=[torch.zeros(6, 2, 16, 64, dtype=torch.float16)[..., 1:61]])
     same = torch.zeros(2, dtype=torch.int32)
     refused("FDEC_ERR_INVALID_ARG", cpu_keep, prefix_lens=same, seq_lens=same)
+    path = torch.zeros(8, dtype=torch.int32)
+    refused("FDEC_ERR_INVALID_ARG", cpu_keep, path=path.view(2, 4), seq_lens=path[3:5])
+    pool = torch.zeros(6, 2, 16, 64)
+    refused("FDEC_ERR_INVALID_ARG", cpu_keep, caches=[pool, pool])
+    refused("FDEC_ERR_LAYOUT", cpu_keep, caches=[pool[:1].expand(6, 2, 16, 64)])
+    refused("FDEC_ERR_LAYOUT", cpu_keep, caches=[pool[None].expand(3, 6, 2, 16, 64)])
+    with pytest.raises(ValueError, match="CUDA device"):  # K and V in one tensor are two caches
+        both = torch.zeros(6, 2, 2, 16, 64)
+        cpu_keep(caches=[both[:, 0], both[:, 1]])
     refused("FDEC_ERR_UNSUPPORTED", cpu_keep, path=torch.zeros(2, 65, dtype=torch.int32))
 
 
@@ -1159,3 +1312,16 @@ def test_tree_decode_refuses_what_it_cannot_hold():
         fd.TreeDecode([100], 65, 16, 8, 2, 128, 64)
     with pytest.raises(ValueError):
         fd.TreeDecode([100], 0, 16, 8, 2, 128, 64)
+    with pytest.raises(ValueError):
+        fd.TreeDecode([100], 8, 16, 8, 2, 128, 64, kv_dtype="q8_0")
+
+
+def test_fresh_data_is_read_with_ordinary_loads():
+    """These kernels are resident beside the ones that write their inputs: no read-only loads."""
+    root = os.path.join(os.path.dirname(fd.__file__), "csrc")
+    for name in ("tree_attention.cu", "verify_drafts.cu", "keep_path.cu", "reserve_pages.cu", "cache_rows.cuh"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(root, name)).read())
+        assert "__ldg" not in text and ".nc." not in text, name
+        for body in re.split(r"__global__", text)[1:]:
+            wait = body.index("griddepcontrol.wait")
+            assert "return" not in body[:wait], name  # no way out before the kernel before has completed
