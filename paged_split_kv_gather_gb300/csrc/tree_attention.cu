@@ -125,8 +125,12 @@ __device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
     *reinterpret_cast<uint2*>(at + 16) = make_uint2(v.y, v.w);
 }
 
+// CTAs on an SM: by the registers of S, P and O.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
+// nodes 10.0 us instead of 12.5; but at head_dim 256 16 trees of 13 nodes 8.3 us instead of 7.4.)
+constexpr int tree_ctas(int head_dim, int ks) { return ks == 1 && head_dim <= 128 ? 4 : 3; }
+
 template <int D, bool BF16, bool KV8, int KS>
-__global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention_kernel(const TreeParams p) {
     using S = TreeShape<D>;
     constexpr int kPShift = 8;                 // p x 2^8 is split
     constexpr bool kRewrite = BF16 && !KV8;    // V is not f16 as it is stored
@@ -251,8 +255,11 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
         // columns, each once the one before it has been joined.
         constexpr int CB = D / 64, QD = S::QD;
         const int gq = lane >> 2, t = lane & 3;
-        const int T0 = first + warp;
-        const int my_tiles = T0 < tiles ? (tiles - T0 + kTreeWarps - 1) / kTreeWarps : 0;
+        // With fewer tiles than warps, warps share one: each computes S and takes a part of the columns of O.
+        const int split = tiles - first > 2 ? 1 : min(tiles - first == 2 ? 2 : kTreeWarps, CB);
+        const int T0 = first + warp / split, part = warp % split;
+        const int cb0 = part * CB / split, cb1 = (part + 1) * CB / split;
+        const int my_tiles = T0 < tiles ? (split > 1 ? 1 : (tiles - T0 + kTreeWarps - 1) / kTreeWarps) : 0;
         const uint32_t q_slot = smem_addr(smem) + 2 * 16 * KS * S::PITCH + warp * (S::Q_BYTES + kSlotBytes);
         const uint32_t slot = q_slot + S::Q_BYTES;
         // Lane l: the (token, head) index in out and lse of row l % 16 of a tile (-1 past the last), its node.
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         next_tile(0);
-        request_prefix(0, rows);
+        request_prefix(cb0, rows);
 
         // K and V rows, widened to 16 bits; rows past the tree and unreadable ones are zeros
         constexpr int staged = 16 * KS;
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
                 const auto word = [&](int h, int d) {
                     return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
                 };
-#pragma unroll 4
+#pragma unroll 6
                 for (int d = QD; d < D; d += 32) {
                     const uint32_t a0[4] = {word(0, d), word(1, d), word(0, d + 8), word(1, d + 8)};
                     const uint32_t a1[4] = {word(0, d + 16), word(1, d + 16), word(0, d + 24), word(1, d + 24)};
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
                 w[h] *= inv;
                 vs[h] = v_factor * inv;
             }
-            if (p.lse != nullptr && t == 0) {
+            if (p.lse != nullptr && t == 0 && part == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (out_row[h] >= 0) p.lse[out_row[h]] = lse_out[h];
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
 
             // O in blocks of 64 columns
             const auto finish = [&](int cb, const float (&acc)[8][4]) {
-                if (cb == 0)
+                if (cb == cb0)
                     asm volatile("cp.async.wait_group 1;" ::: "memory");  // (the next queries may be on their way)
                 else
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -545,11 +552,13 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
                             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    if (key >> 3 == 2 * ks + e) {  // (through registers: not an index into memory)
-                                        asm volatile("mov.b32 %0, %1;" : "=r"(hi) : "r"(pf[ks][0][2 * e + h]));
-                                        asm volatile("mov.b32 %0, %1;" : "=r"(lo) : "r"(pf[ks][1][2 * e + h]));
-                                    }
-                            const float2 a = unpack2<false>(hi), c = unpack2<false>(lo);
+                                    // (selected in registers: not an index into memory)
+                                asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %4, %5;\n\t"
+                                             "selp.b32 %0, %2, %0, p;\n\tselp.b32 %1, %3, %1, p;\n\t}"
+                                             : "+r"(hi), "+r"(lo)
+                                             : "r"(pf[ks][0][2 * e + h]), "r"(pf[ks][1][2 * e + h]), "r"(key >> 3),
+                                               "r"(2 * ks + e));
+                        const float2 a = unpack2<false>(hi), c = unpack2<false>(lo);
                             const float pr = __shfl_sync(0xffffffffu, key & 1 ? a.y + c.y : a.x + c.x,
                                                          (lane & ~3) | ((key & 7) >> 1)) * factor * vs[h];
                             const uint64_t seen = out_row[h] < 0 ? 0 : s_anc[known][out_node[h]] & valid;
@@ -602,10 +611,10 @@ __global__ void __launch_bounds__(kTreeThreads, 3) tree_attention_kernel(const T
                     }
                 }
                 __syncwarp();  // and have been read
-                request_prefix(cb + 1 < CB ? cb + 1 : 0, cb + 1 < CB ? rows_now : rows);
+                request_prefix(cb + 1 < cb1 ? cb + 1 : cb0, cb + 1 < cb1 ? rows_now : rows);
             };
 #pragma unroll 1
-            for (int cb = 0; cb < CB; ++cb) {
+            for (int cb = cb0; cb < cb1; ++cb) {
                 float acc[8][4];
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
@@ -643,14 +652,17 @@ cudaError_t launch_tree_one(TreeParams p, int num_sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
     }
-    // Up to as many sequences' KV heads as CTAs are resident: parts of one each, of a tile for every warp or more, as an
-    // equal share that spans two stages two trees (256 heads of 6 tiles: 7.9 us, 11.2 in shares).  Above, equal
-    // shares: whole heads in a second round would leave most of the machine idle (512 heads of 16 tiles: 42 us, 55 a
-    // head a CTA, 56 in parts).
-    const int64_t heads = static_cast<int64_t>(p.batch) * p.hk, slots = static_cast<int64_t>(num_sms) * 3;
+    // Up to as many sequences' KV heads as CTAs are resident, or with fewer tiles in each than a CTA has warps: parts
+    // of one head each, as an equal share that spans two stages two trees (256 heads of 6 tiles: 7.9 us, 11.2 shared).
+    // Else equal shares: whole heads in a second round would leave most of the machine idle (512 heads of 16 tiles:
+    // 42 us, 55 a head a CTA, 56 in parts).
+    const int64_t heads = static_cast<int64_t>(p.batch) * p.hk;
+    const int64_t slots = static_cast<int64_t>(num_sms) * tree_ctas(D, KS);
     const int per_head = (p.nodes * p.group + 15) / 16;
-    const int64_t most = std::min<int64_t>((per_head + kTreeWarps - 1) / kTreeWarps, 2 * slots / heads);
-    p.parts = heads <= slots ? static_cast<int>(most) : 0;
+    const bool whole = heads <= slots || per_head < kTreeWarps;
+    const int64_t wide = std::min<int64_t>((per_head + kTreeWarps - 1) / kTreeWarps, 2 * slots / heads);
+    // (a part for every tile where the machine has room twice over: warps then share the tiles)
+    p.parts = !whole ? 0 : heads * per_head <= slots / 2 ? per_head : static_cast<int>(std::max<int64_t>(1, wide));
     const int64_t grid = p.parts > 0 ? heads * p.parts : slots;
     p.share = static_cast<int>(heads * per_head / slots);
     p.share_more = static_cast<int>(heads * per_head % slots);
