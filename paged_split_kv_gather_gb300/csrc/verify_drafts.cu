@@ -6,7 +6,8 @@
 //   max(max(p - s q, 0) / W - q, 0) = max(p - (s + W) q, 0) / W      (q >= 0),
 // so one number s stands for all of them and every sum reads the same two rows.
 //
-// A cluster of eight CTAs takes one sequence; each warp sums a run of the vocabulary.  The first
+// A cluster of eight CTAs (one, for a small vocabulary) takes one sequence; each warp sums a run
+// of the vocabulary.  The first
 // CTA reads what the walk goes by, all children's p and q among it, and copies it into the
 // others' shared memory; every warp's sum goes to all CTAs.  Each CTA then walks for itself on the
 // same bits, so all of them agree, even on inputs that change under them: a sum costs one
@@ -40,8 +41,9 @@ namespace {
 
 constexpr int kVerifyWarps = 8;
 constexpr int kVerifyThreads = kVerifyWarps * 32;
-constexpr int kVerifyCluster = 8;  // CTAs of a sequence
-constexpr int kRuns = kVerifyCluster * kVerifyWarps;  // of the vocabulary: a warp's each
+constexpr int kMostCtas = 8;  // of a sequence
+// A sequence's CTAs each have kVerifyWarps runs of the vocabulary, a warp's each.
+constexpr int kMostRuns = kMostCtas * kVerifyWarps;
 
 enum Op : int { kSum = 0, kDraw = 1, kStop = 2 };
 
@@ -83,7 +85,7 @@ __device__ __forceinline__ float bounded(float x, bool& bad) {
 
 // A number as a pair of fp32 values.
 struct Pair {
-    float hi = 0.f, lo = 0.f;
+    float hi, lo;
     // + (x + e), e small against x
     __device__ __forceinline__ void add(float x, float e) {
         const float sum = __fadd_rn(hi, x);
@@ -167,12 +169,13 @@ __device__ __forceinline__ void add_token(Pair& sum, float p, float q, bool draf
         sum.add(x, 0.f);
 }
 
-// One lane's part of a warp's sum over tokens [begin, end).  PLAIN: probabilities are taken as they are, and the largest
-// of their bits are noted (as unsigned numbers, all that are not in [0, 2] are above those of 2).
+// One lane's part of a warp's sum over tokens [begin, end).  PLAIN: probabilities are taken as they are, and the
+// largest of their bits are noted (as unsigned numbers, all that are not in [0, 2] are above those of 2).
 template <typename T, bool VEC, int MODE, bool PLAIN, int AHEAD>  // MODE 0: p, 1: max(p - q, 0), 2: max(p - s q, 0)
-__device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int end, Pair s, uint32_t& most, bool& bad) {
+__device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int end, Pair s, uint32_t& most,
+                                         bool& bad) {
     const int lane = threadIdx.x & 31;
-    Pair sum;
+    Pair sum = {};
     const auto term = [&](float a, float c) {
         if constexpr (PLAIN) {
             most = max(most, __float_as_uint(a));
@@ -237,7 +240,7 @@ template <typename T, bool VEC, int AHEAD>
 __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, double s, const Node* nodes,
                                         uint64_t gone, bool& bad) {
     const int lane = threadIdx.x & 31;
-    Pair sum;
+    Pair sum = {};
     bool hit = false;  // a token without weight lies in here
     if (q == nullptr && gone != 0) {
 #pragma unroll
@@ -286,11 +289,11 @@ struct Tree {
 
 struct Walk {
     Tree tree;
-    Pair sum[2][kRuns];  // every warp's sum, of even and of odd rounds
+    Pair sum[2][kMostRuns];  // every warp's sum, of even and of odd rounds
     int path[kMaxNodes];
     double s, W;
     // Without draft rows: the target's row is summed once, and a token that falls is taken from that sum.  The
-    // difference keeps the sum's absolute error, so that where it is small (exact) the row is summed without the tokens.
+    // difference keeps the sum's absolute error: where it is small (exact), the row is summed without the tokens.
     double row_total, row_gone;
     uint64_t weighed;   // the children whose tokens make up row_gone, each token once
     uint64_t gone, left;  // children that have fallen, that are still to try
@@ -301,7 +304,7 @@ struct Walk {
 
 // The run of the vocabulary that holds the next token (o.run, o.target), from every warp's sum (a lane's `mine`, their
 // sum, the sum up to the lane), less the tokens of the children `weighed`.  A warp; false where nothing is left.
-constexpr int kRunsPerLane = kRuns / 32;
+constexpr int kRunsPerLane = kMostRuns / 32;
 __device__ __forceinline__ bool draw_run(const Tree& tree, double (&mine)[kRunsPerLane], double part, double upto,
                                          uint64_t weighed, int chunk, Order& o) {
     const int lane = threadIdx.x & 31;
@@ -350,14 +353,15 @@ __device__ __forceinline__ bool draw_run(const Tree& tree, double (&mine)[kRunsP
     return true;
 }
 
-// What comes next: a CTA's first warp, at the beginning (no sums) and whenever all sums have come.
-__device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, bool drafted, int chunk) {
+// What comes next: a CTA's first warp, at the beginning (no sums) and whenever all sums (`runs` of them) have come.
+__device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs, bool drafted, int chunk) {
     const int lane = threadIdx.x & 31;
     constexpr int PER = kRunsPerLane;
     const Tree& tree = walk.tree;
     // (nodes past the last have not been given)
-    const int par0 = lane < tree.n ? tree.node[lane].par : -1, par1 = lane + 32 < tree.n ? tree.node[lane + 32].par : -1;
-    const int tok0 = lane < tree.n ? tree.node[lane].tok : -1, tok1 = lane + 32 < tree.n ? tree.node[lane + 32].tok : -1;
+    const bool has0 = lane < tree.n, has1 = lane + 32 < tree.n;
+    const int par0 = has0 ? tree.node[lane].par : -1, par1 = has1 ? tree.node[lane + 32].par : -1;
+    const int tok0 = has0 ? tree.node[lane].tok : -1, tok1 = has1 ? tree.node[lane + 32].tok : -1;
     const auto children = [&](int node) {
         return static_cast<uint64_t>(__ballot_sync(0xffffffffu, par0 == node)) |
                static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
@@ -384,7 +388,7 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, bool draf
         bool ask = false;
         if (sums != nullptr) {  // the sums that were asked for
 #pragma unroll
-            for (int k = 0; k < PER; ++k) part += mine[k] = sums[lane * PER + k].value();
+            for (int k = 0; k < PER; ++k) part += mine[k] = lane * PER + k < runs ? sums[lane * PER + k].value() : 0.0;
             upto = warp_scan_double(part);
             W = __shfl_sync(0xffffffffu, upto, 31);
             summed = true;
@@ -457,8 +461,8 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, bool draf
     return o;
 }
 
-// AHEAD: vectors of each row in flight a lane.
-template <typename T, bool VEC, int AHEAD>
+// CTAS: of a sequence.  AHEAD: vectors of each row in flight a lane.
+template <typename T, bool VEC, int CTAS, int AHEAD>
 __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_drafts_kernel(const VerifyParams p) {
     __shared__ Walk s_walk;
     __shared__ Pair s_warp[kVerifyWarps];
@@ -466,14 +470,20 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
     __shared__ Order s_order;
 
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
-    const int b = blockIdx.x / kVerifyCluster;
+    const int rank = CTAS > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    const auto meet = [&] {  // all threads of the sequence's CTAs
+        if constexpr (CTAS > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    const int b = blockIdx.x / CTAS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int N = p.nodes;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
+    if constexpr (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
 
     const T* target = static_cast<const T*>(p.target) + static_cast<int64_t>(b) * p.t_seq;
     const T* draft = p.draft != nullptr ? static_cast<const T*>(p.draft) + static_cast<int64_t>(b) * p.d_seq : nullptr;
@@ -518,20 +528,23 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         if (tid == 0) s_walk.tree.n = n;
     }
     __syncthreads();
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs run: their memory is written next
-    if (rank == 0 && warp > 0 && warp < kVerifyCluster) {
-        const int* from = reinterpret_cast<const int*>(&s_walk.tree);
-        int* to = reinterpret_cast<int*>(cluster.map_shared_rank(&s_walk.tree, warp));
-        const int words = 1 + s_walk.tree.n * static_cast<int>(sizeof(Node) / 4);
-        for (int i = lane; i < words; i += 32) to[i] = from[i];
+    if constexpr (CTAS > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the other CTAs run: their memory is written next
+        if (rank == 0 && warp > 0 && warp < CTAS) {
+            const int* from = reinterpret_cast<const int*>(&s_walk.tree);
+            int* to = reinterpret_cast<int*>(cluster.map_shared_rank(&s_walk.tree, warp));
+            const int words = 1 + s_walk.tree.n * static_cast<int>(sizeof(Node) / 4);
+            for (int i = lane; i < words; i += 32) to[i] = from[i];
+        }
+        cluster.sync();
     }
-    cluster.sync();
 
     const int n = s_walk.tree.n;
     // (at most two sums for every child and two for the draw)
     for (int round = 0; round < 2 * kMaxNodes + 3; ++round) {
         if (warp == 0) {
-            const Order next = next_order(s_walk, round > 0 ? s_walk.sum[(round - 1) & 1] : nullptr, draft != nullptr, p.chunk);
+            const Pair* sums = round > 0 ? s_walk.sum[(round - 1) & 1] : nullptr;
+            const Order next = next_order(s_walk, sums, CTAS * kVerifyWarps, draft != nullptr, p.chunk);
             if (lane == 0) s_order = next;
         }
         __syncthreads();
@@ -542,15 +555,19 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
         const int run = rank * kVerifyWarps + warp;
         const int64_t begin = static_cast<int64_t>(run) * p.chunk;
-        Pair sum;
+        Pair sum = {};
         bool bad = false;
         if (begin < p.vocab) {
             const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
             sum = run_sum<T, VEC, AHEAD>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tree.node, o.gone, bad);
         }
         if (bad) flags |= FDEC_DEVERR_PROB;
-        if (lane < kVerifyCluster) cluster.map_shared_rank(&s_walk, lane)->sum[round & 1][run] = sum;
-        cluster.sync();
+        if constexpr (CTAS > 1) {
+            if (lane < CTAS) cluster.map_shared_rank(&s_walk, lane)->sum[round & 1][run] = sum;
+        } else if (lane == 0) {
+            s_walk.sum[round & 1][run] = sum;
+        }
+        meet();
     }
 
     const Order o = s_order;
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         const int v1 = min(end, v0 + per);
         constexpr int U = 8;
         const Pair weight = pair_of(o.s), target_sum = pair_of(o.target);
-        Pair mine;
+        Pair mine = {};
         for (int v = v0; v < v1; v += U) {
             float a[U], c[U];
 #pragma unroll
@@ -599,7 +616,7 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
             s_any = p.vocab;
         }
         __syncthreads();
-        Pair before;
+        Pair before = {};
         for (int k = 0; k < warp; ++k) before.add(s_warp[k].hi, s_warp[k].lo);
         Pair upto = before;
         upto.add(scan.hi, scan.lo);
@@ -607,13 +624,13 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
             if (upto.above(target_sum)) atomicMin(&s_first, tid);
             atomicMax(&s_last, tid);
         }
-        const float prior_hi = __shfl_up_sync(0xffffffffu, scan.hi, 1), prior_lo = __shfl_up_sync(0xffffffffu, scan.lo, 1);
-        if (lane > 0) before.add(prior_hi, prior_lo);
+        const Pair prior = {__shfl_up_sync(0xffffffffu, scan.hi, 1), __shfl_up_sync(0xffffffffu, scan.lo, 1)};
+        if (lane > 0) before.add(prior.hi, prior.lo);
         __syncthreads();
         if (tid == (s_first < kVerifyThreads ? s_first : s_last)) {
             int token = -1;
             for (int v = v0; v < v1; ++v) {
-                Pair here;
+                Pair here = {};
                 add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
                           s_walk.tree.node, o.gone);
                 if (!(here.hi > 0.f)) continue;
@@ -625,7 +642,7 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         }
         if (s_last < 0) {  // (only by rounding: the run has no weight after all; the first token that has some)
             for (int v = tid; v < p.vocab; v += kVerifyThreads) {
-                Pair here;
+                Pair here = {};
                 add_token(here, value(prow + v), qrow != nullptr ? value(qrow + v) : 0.f, qrow != nullptr, v, weight,
                           s_walk.tree.node, o.gone);
                 if (here.hi > 0.f) atomicMin(&s_any, v);
@@ -645,31 +662,39 @@ bool vectors(const VerifyParams& p) {
     return p.vocab % 4 == 0 && ok(p.target, p.t_seq, p.t_node) && ok(p.draft, p.d_seq, p.d_node);
 }
 
-template <typename T, bool VEC, int AHEAD>
-cudaError_t launch_verify_one(const VerifyParams& p, cudaStream_t s) {
+template <typename T, bool VEC, int CTAS, int AHEAD>
+cudaError_t launch_verify_one(VerifyParams p, cudaStream_t s) {
+    constexpr int kRuns = CTAS * kVerifyWarps;
+    p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * kVerifyCluster, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * CTAS, 1, 1);
     cfg.blockDim = dim3(kVerifyThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kVerifyCluster;
+    attr[1].val.clusterDim.x = CTAS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, AHEAD>, p);
+    cfg.numAttrs = CTAS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, CTAS, AHEAD>, p);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_verify_v(const VerifyParams& p, int num_sms, cudaStream_t s) {
+    // A small vocabulary is one CTA's, which needs no cluster: 64 sequences 10.5 us against 12.2 at 4096 and at 8192
+    // tokens, 16 trees 12.0 against 13.4 and the same; at 16384 tokens 15.8 against 12.8.
+    if (p.vocab <= 8192) return launch_verify_one<T, VEC, 1, 8>(p, s);
+    // Twice the loads in flight, where the registers are there: two CTAs an SM instead of four.  (16 trees over 50021
+    // tokens 1.5 us less; clusters of 4 CTAs 1.5 us more, of 16 9 more.)
+    const bool deep = static_cast<int64_t>(p.batch) * kMostCtas <= num_sms * 2;
+    return deep ? launch_verify_one<T, VEC, kMostCtas, 8>(p, s) : launch_verify_one<T, VEC, kMostCtas, 4>(p, s);
 }
 
 template <typename T>
-cudaError_t launch_verify(VerifyParams p, int num_sms, cudaStream_t s) {
-    p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
-    // Twice the loads in flight, where the registers are there: two CTAs an SM instead of four.  (16 trees over 50021
-    // tokens 1.5 us less; clusters of 4 CTAs 1.5 us more, of 16 9 more.)
-    const bool deep = static_cast<int64_t>(p.batch) * kVerifyCluster <= num_sms * 2;
-    if (vectors<T>(p)) return deep ? launch_verify_one<T, true, 8>(p, s) : launch_verify_one<T, true, 4>(p, s);
-    return deep ? launch_verify_one<T, false, 8>(p, s) : launch_verify_one<T, false, 4>(p, s);
+cudaError_t launch_verify(const VerifyParams& p, int num_sms, cudaStream_t s) {
+    return vectors<T>(p) ? launch_verify_v<T, true>(p, num_sms, s) : launch_verify_v<T, false>(p, num_sms, s);
 }
 
 }  // namespace

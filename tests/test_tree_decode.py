@@ -492,7 +492,8 @@ def test_verify_drafts_goes_deep_and_tries_many_children():
 
 
 @gpu
-@pytest.mark.parametrize("vocab,dtype", [(300, "f32"), (4096, "bf16"), (4099, "f16")])
+@pytest.mark.parametrize("vocab,dtype", [(300, "f32"), (4096, "bf16"), (4099, "f16"), (8192, "f32"), (8196, "f32"),
+                                         (9001, "f32"), (8196, "bf16")])
 def test_verify_drafts_of_many_sequences(vocab, dtype):
     g, rng = torch.Generator().manual_seed(2), random.Random(2)
     for drafts in (True, False):
