@@ -293,9 +293,9 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
 
 namespace {
 
-// Workspace of fdec_reserve_pages: two bit sets, pages in use by blocks, the sequences' last pages.
+// Workspace of fdec_reserve_pages: two bit sets, pages in use by blocks, the sequences' last pages and copies.
 struct ReserveLayout {
-    size_t off_shared, off_taken, off_last, bytes;
+    size_t off_shared, off_taken, off_last, off_copies, bytes;
     int words, blocks;
 };
 
@@ -306,7 +306,8 @@ bool reserve_layout(int batch, int64_t num_pages, ReserveLayout* out) {
     out->blocks = static_cast<int>((num_pages + kCountedPages - 1) / kCountedPages);
     out->off_taken = 2 * out->off_shared;
     out->off_last = out->off_taken + static_cast<size_t>(out->blocks) * 4;
-    out->bytes = (out->off_last + static_cast<size_t>(batch) * 4 + 255) / 256 * 256;
+    out->off_copies = (out->off_last + static_cast<size_t>(batch) * 4 + 15) / 16 * 16;
+    out->bytes = (out->off_copies + static_cast<size_t>(batch) * 16 + 255) / 256 * 256;
     return true;
 }
 
@@ -365,6 +366,7 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
     p.taken = reinterpret_cast<int32_t*>(ws + l.off_taken);
     p.blocks = l.blocks;
     p.last_page = reinterpret_cast<int32_t*>(ws + l.off_last);
+    p.copies = reinterpret_cast<int4*>(ws + l.off_copies);
     p.err = device_errors;
     p.num_pages = num_pages;
     p.words = l.words;

@@ -376,6 +376,7 @@ struct ReserveParams {
     unsigned* shared;            // [words] two do
     int32_t* taken;              // [blocks] pages in use of every kCountedPages, if there are many
     int32_t* last_page;          // [batch] the page of a sequence's (its source's) last, partly filled part
+    int4* copies;                // [batch] (from page, to page, rows, 0)
     unsigned* err;
     int64_t num_pages;
     int words, blocks, batch, page_shift;

@@ -2,16 +2,20 @@
 // shared ones.
 //
 // The page tables and lengths say which pages are in use; nothing else is kept, so
-// nothing can go out of step with them.  Three launches, four for large pools: clear two bit
-// sets of a bit a page; mark every page that an entry in use names (the second set: pages that
+// nothing can go out of step with them.  Three launches, one more for large pools, one more where
+// there are rows to copy: clear two bit sets of a bit a page; mark every page that an entry in use names (the second set: pages that
 // two name); then each sequence finds its pages for itself: how many pages the sequences
 // before it need, from the lengths, and which bits are its own, from the pages in use of every
 // 1024 and the first bit set.  Those numbers come from a launch of their own for pools above
 // 131072 pages (from the marking's atomics they cost 45 us, for 256 sequences and a million
 // pages, each CTA reading all bits 9 us); below, every CTA counts for itself.
-// Its CTAs copy the rows that a fork or a shared last page needs.
+// The rows that a fork or a shared last page needs are copied last.
 //
-// Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.
+// Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.  64
+// sequences and 65536 pages: 8.4 us, the latencies of three dependent launches (clear 1,
+// mark 3, assign 3.5); 256 sequences of 2049 entries and a million pages: 14.0, the marks'
+// atomics among them; 64 forks in 16 layers: 14.1, of them 7.4 the copies (63 MB, 8.5 TB/s
+// of reads and writes that the L2 holds in part).
 #include <algorithm>
 #include <cstdint>
 
@@ -168,15 +172,12 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* s_part) {
     return sum;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kReserveThreads)
-    reserve_assign_kernel(const __grid_constant__ ReserveParams p, const __grid_constant__ CacheList<N> caches,
-                          int blocks) {
+__global__ void __launch_bounds__(kReserveThreads) reserve_assign_kernel(const ReserveParams p) {
     __shared__ int64_t s_part[kReserveThreads / 32], s_at;
     __shared__ int s_page, s_block, s_taken[kOwnBlocks];
     __shared__ Request s_request;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    const int b = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // A pool's bits that the CTA counts for itself, all asked for at once.
@@ -199,8 +200,7 @@ __global__ void __launch_bounds__(kReserveThreads)
     }
     start = block_sum(start, s_part);
     const Request r = s_request;
-    if (blk == 0 && tid == 0 && r.bad && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
-    if (blk != 0 && (r.bad || r.part == 0 || r.need() == 0)) return;  // nothing to copy
+    if (tid == 0 && r.bad && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_SEQ_LEN);
 
     bool enough = true;
     if (r.need() > 0) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kReserveThreads)
                     for (; bits != 0 && i < end; bits &= bits - 1, ++i) {
                         if (i < start) continue;
                         const int page = w * 32 + __ffs(bits) - 1;
-                        if (blk == 0) p.page_table[b * p.pt_stride + r.first + (i - start)] = page;
+                        p.page_table[b * p.pt_stride + r.first + (i - start)] = page;
                         if (i == start) s_page = page;
                     }
                 }
@@ -272,26 +272,36 @@ __global__ void __launch_bounds__(kReserveThreads)
             }
         }
     }
-    if (blk == 0) {
-        if (tid == 0) {
-            p.granted[b] = r.bad || !enough ? p.seq_lens[b] : p.new_lens[b];
-            if (!enough && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_NO_PAGES);
-        }
-        if (!r.bad && enough && r.source != b)  // a fork shares the full pages
-            for (int64_t j = tid; j < r.first; j += kReserveThreads)
-                p.page_table[b * p.pt_stride + j] = p.page_table[r.source * p.pt_stride + j];
+    if (tid == 0) {
+        p.granted[b] = r.bad || !enough ? p.seq_lens[b] : p.new_lens[b];
+        if (!enough && p.err != nullptr) atomicOr(p.err, FDEC_DEVERR_NO_PAGES);
     }
+    if (!r.bad && enough && r.source != b)  // a fork shares the full pages
+        for (int64_t j = tid; j < r.first; j += kReserveThreads)
+            p.page_table[b * p.pt_stride + j] = p.page_table[r.source * p.pt_stride + j];
     __syncthreads();
-    if (caches.n == 0 || r.bad || !enough || r.part == 0 || r.need() == 0) return;
-    const int of = p.last_page[b], page = s_page;
-    if (of < 0) return;  // (flagged as it was marked)
+    if (tid == 0) {
+        const int of = p.last_page[b];  // (a bad one has been flagged)
+        const bool copies = !r.bad && enough && r.part > 0 && r.need() > 0 && of >= 0;
+        p.copies[b] = copies ? make_int4(of, s_page, r.part, 0) : make_int4(0, 0, 0, 0);
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kColumnThreads)
+    reserve_copy_kernel(const __grid_constant__ ReserveParams p, const __grid_constant__ CacheList<N> caches, int blocks) {
+    const int b = blockIdx.x / blocks, blk = blockIdx.x % blocks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 copy = p.copies[b];
+    if (copy.z == 0) return;
     const CacheRows& c = cache_of(caches, blk);
-    const auto from = [&](int i) { return make_int2(of, i); };
-    const auto to = [&](int i) { return make_int2(page, i); };
+    const auto from = [&](int i) { return make_int2(copy.x, i); };
+    const auto to = [&](int i) { return make_int2(copy.y, i); };
     if (c.wide)
-        move_columns<uint4>(c, blk, 0, r.part, from, to);
+        move_columns<uint4>(c, blk, 0, copy.z, from, to);
     else
-        move_columns<uint2>(c, blk, 0, r.part, from, to);
+        move_columns<uint2>(c, blk, 0, copy.z, from, to);
 }
 
 template <typename Kernel, typename... Args>
@@ -310,9 +320,9 @@ cudaError_t launch(Kernel kernel, int64_t grid, cudaStream_t s, const Args&... a
 }
 
 template <int N>
-cudaError_t launch_assign(const ReserveParams& p, const CacheList<kMaxCaches>& caches, cudaStream_t s) {
-    const int64_t blocks = std::max<int64_t>(1, column_blocks(caches));
-    return launch(reserve_assign_kernel<N>, blocks * p.batch, s, p, shorter<N>(caches), static_cast<int>(blocks));
+cudaError_t launch_copy(const ReserveParams& p, const CacheList<kMaxCaches>& caches, cudaStream_t s) {
+    const int64_t blocks = column_blocks(caches);
+    return launch(reserve_copy_kernel<N>, blocks * p.batch, s, p, shorter<N>(caches), static_cast<int>(blocks));
 }
 
 }  // namespace
@@ -330,7 +340,9 @@ cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCac
         e = launch(reserve_count_kernel, std::min<int64_t>((p.blocks + 7) / 8, num_sms * 4), s, p);
         if (e != cudaSuccess) return e;
     }
-    return caches.n <= 2 ? launch_assign<2>(p, caches, s) : launch_assign<kMaxCaches>(p, caches, s);
+    e = launch(reserve_assign_kernel, p.batch, s, p);
+    if (e != cudaSuccess || caches.n == 0) return e;
+    return caches.n <= 2 ? launch_copy<2>(p, caches, s) : launch_copy<kMaxCaches>(p, caches, s);
 }
 
 }  // namespace fdec
