@@ -143,8 +143,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
     __shared__ int s_count[kTreeWarps];
     __shared__ unsigned s_max, s_odd[2];
 
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int N = p.nodes, g = p.group;
     const int tiles_max = (N * g + 15) / 16;  // of a sequence's KV head
 
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
             nodes = it < my_tiles && r < R ? r / g : 0;
             rows = it < my_tiles && r < R ? (b * N + nodes) * p.hq + kvh * g + (r - nodes * g) : -1;
             if (it < my_tiles) {
-                const uint16_t* mine = query(max(rows, 0), nodes);
+                const uint16_t* mine = rows >= 0 ? query(rows, nodes) : p.q;
                 constexpr int CH = QD / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
 #pragma unroll
                 for (int k = 0; k < 16 / RPI; ++k) {
@@ -439,8 +438,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     add_scores<BF16, KS, false>(s, a0, a1, k_addr + c * 64, S::PITCH);
             }
             if constexpr (D > QD) {  // the other dims from where they are
-                const uint16_t* from[2] = {query(max(row[0], 0), node[0]) + 2 * t,
-                                           query(max(row[1], 0), node[1]) + 2 * t};
+                const uint16_t* from[2] = {(row[0] >= 0 ? query(row[0], node[0]) : p.q) + 2 * t,
+                                           (row[1] >= 0 ? query(row[1], node[1]) : p.q) + 2 * t};
                 const auto word = [&](int h, int d) {
                     return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
                 };

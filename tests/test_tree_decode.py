@@ -889,6 +889,46 @@ def test_reserve_pages_of_odd_pools(num_pages):
     assert err == 0 and granted == want_granted == new and np.array_equal(got, want)
 
 
+@gpu
+def test_offsets_past_32_bits():
+    """Pools of more than 4 GB of which the last pages are used (2 x 4.6 GB)."""
+    hk, page, d, pages = 2, 128, 128, 70000
+    k, v = (torch.empty((pages, hk, page, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    used = [pages - 1 - i for i in range(6)]
+    g = torch.Generator().manual_seed(1)
+    for x in (k, v):
+        x[used] = torch.randn((6, hk, page, d), generator=g).bfloat16().cuda()
+    c = Tree(d, 8, hk, 20, page, 2, seed=16, counts=[20, 20], prefix=[120, 250])
+    c.k, c.v = k, v
+    c.table = np.array([[used[0], used[1], -1], [-1, used[2], used[3]]], dtype=np.int32)
+    c.check(*c.run())
+    table = np.array([used[:2], used[2:4]], dtype=np.int32)
+    path, lens = np.array([[0, 3, 9, 19] + [-1] * 16, [1, 2] + [-1] * 18], dtype=np.int32), [4, 2]
+    small = [x[used].clone() for x in (k, v)]
+    want = keep_reference(small, np.array([[0, 1], [2, 3]]), [120, 100], path.tolist(), lens, page)
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    fd.fdec_keep_path((k, v), i32(table), i32([120, 100]), i32(path), i32(lens), out, page)
+    assert torch.equal(k[used], want[0]) and torch.equal(v[used], want[1])
+    # a fork whose last page is the pool's last free one: all others but two are in use
+    width = pages // 4
+    table = np.full((5, width), -1, dtype=np.int32)
+    order = [p for p in range(pages) if p != used[4]]
+    for b in range(4):
+        mine = order[b * width:(b + 1) * width]
+        table[b, :len(mine)] = mine
+    lens = [width * page] * 3 + [(len(order) - 3 * width) * page - 5, 0]
+    table[3, len(order) - 3 * width - 1] = used[0]
+    table[3, len(order) - 3 * width:] = -1
+    first = [x[used[0], :, :page - 5].clone() for x in (k, v)]
+    got, granted, err = run_reserve(table, lens, lens[:4] + [lens[3]], [-1, -1, -1, -1, 3], pages, page, caches=(k, v))
+    want, want_granted, copies = reserve_reference(table, lens, lens[:4] + [lens[3]], [-1, -1, -1, -1, 3], pages, page)
+    assert err == 0 and granted == want_granted and np.array_equal(got, want)
+    (_, of, to, rows), = copies
+    assert of == used[0] and rows == page - 5
+    for x, w in zip((k, v), first):
+        assert torch.equal(x[to, :, :rows], w)
+
+
 # ------------------------------------------------------------------------------------------------------- a whole round
 
 def causal_reference(q, k, v, scale, line):
