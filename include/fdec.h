@@ -463,9 +463,9 @@ fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_
  *   fdec_tree_attention     attention to the node itself and its ancestors, joined with it
  *   fdec_verify_drafts      the nodes that stand, and the next token
  *   fdec_keep_path          their keys and values moved behind the prefix, in all layers
- * A chain of drafted tokens is the tree with parents[i] = i - 1.  Each is one to three
- * kernel launches, allocates nothing, and may be captured in a CUDA graph; the kernels
- * start as programmatic dependents, as those above do.  (The pages have no counterpart of
+ * A chain of drafted tokens is the tree with parents[i] = i - 1.  Each is one kernel
+ * launch (fdec_reserve_pages three to five), allocates nothing, and may be captured in a CUDA
+ * graph; the kernels start as programmatic dependents, as those above do.  (The pages have no counterpart of
  * these four; their speculative decoding is the multi-token query of fdec_run.)
  *
  * num_nodes, the nodes per sequence that arrays have room for, is in [1, 64].  node_counts:
@@ -494,7 +494,7 @@ fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_
  *      with lse = -inf counts for nothing, whatever its o.
  *   out: contiguous, 16-byte aligned; out_type FDEC_OUT_F32 or FDEC_OUT_SAME; lse: float32 or
  *      NULL.  out may be o_prefix (FDEC_OUT_F32) and lse lse_prefix; they must not overlap
- *      otherwise.  Rows of nodes past node_counts are not written.  A row that sees nothing
+ *      otherwise, and not with q.  Rows of nodes past node_counts are not written.  A row that sees nothing
  *      gives out = 0 and lse = -inf.  Values of rows that a node does not see never reach it,
  *      NaN and infinities among them.
  */

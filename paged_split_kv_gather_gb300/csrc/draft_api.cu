@@ -149,6 +149,7 @@ fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_s
     if (o_prefix != nullptr && !(out == o_prefix && out_type == FDEC_OUT_F32) &&
         overlap(out, out_bytes, o_prefix, rows * head_dim * 4))
         return fail(FDEC_ERR_INVALID_ARG, "out overlaps o_prefix and is not o_prefix in fp32");
+    if (out == q) return fail(FDEC_ERR_INVALID_ARG, "out must not be q");
     if (lse != nullptr && lse_prefix != nullptr && lse != lse_prefix && overlap(lse, rows * 4, lse_prefix, rows * 4))
         return fail(FDEC_ERR_INVALID_ARG, "lse overlaps lse_prefix and is not lse_prefix");
     const int eb = kv8 ? 1 : 2;
@@ -284,9 +285,7 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
     p.nodes = num_nodes;
     p.page_shift = page_shift_of(page_size);
     if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
-    int num_sms = 0;
-    cudaError_t e = current_num_sms(&num_sms);
-    if (e == cudaSuccess) e = launch_keep_path(p, list, num_sms, stream);
+    const cudaError_t e = launch_keep_path(p, list, stream);
     if (e != cudaSuccess) return fail_cuda(e, "launching the path's moves");
     return FDEC_OK;
 }

@@ -327,7 +327,7 @@ struct VerifyParams {
     int32_t* out_tokens;
     unsigned* err;
     int batch, nodes, vocab;
-    int chunk;                   // elements of a warp, set by the launcher
+    int chunk;                   // tokens of a warp, set by the launcher
 };
 cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, int num_sms, cudaStream_t s);
 
@@ -363,7 +363,7 @@ struct KeepParams {
     int64_t num_pages;           // the fewest of any cache
     int batch, nodes, page_shift;
 };
-cudaError_t launch_keep_path(const KeepParams& p, const CacheList<kMaxCaches>& caches, int num_sms, cudaStream_t s);
+cudaError_t launch_keep_path(const KeepParams& p, const CacheList<kMaxCaches>& caches, cudaStream_t s);
 
 struct ReserveParams {
     int32_t* page_table;

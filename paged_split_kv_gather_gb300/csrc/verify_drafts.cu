@@ -291,7 +291,7 @@ struct Walk {
     Tree tree;
     Pair sum[2][kMostRuns];  // every warp's sum, of even and of odd rounds
     int path[kMaxNodes];
-    double s, W;
+    double s;
     // Without draft rows: the target's row is summed once, and a token that falls is taken from that sum.  The
     // difference keeps the sum's absolute error: where it is small (exact), the row is summed without the tokens.
     double row_total, row_gone;
@@ -372,7 +372,7 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs,
     bool have_row = false, exact = false, summed = false, whole = false;
     if (sums != nullptr) {
         x = walk.x, len = walk.len;
-        s = walk.s, W = walk.W, row_total = walk.row_total, row_gone = walk.row_gone;
+        s = walk.s, row_total = walk.row_total, row_gone = walk.row_gone;
         gone = walk.gone, left = walk.left, weighed = walk.weighed;
         have_row = walk.have_row, exact = walk.exact, whole = walk.whole;
     } else {
@@ -453,7 +453,7 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs,
     __syncwarp();
     if (lane == 0) {
         walk.x = x, walk.len = len;
-        walk.s = s, walk.W = W, walk.row_total = row_total, walk.row_gone = row_gone;
+        walk.s = s, walk.row_total = row_total, walk.row_gone = row_gone;
         walk.gone = gone, walk.left = left, walk.weighed = weighed;
         walk.have_row = have_row, walk.exact = exact, walk.whole = whole;
     }

@@ -1229,6 +1229,8 @@ def test_tree_attention_refusals():
     refused("FDEC_ERR_LAYOUT", cpu_tree, q=torch.zeros(2 * 4 * 8 * 128 + 1, dtype=torch.bfloat16)[1:].view(2, 4, 8, 128))
     both = torch.zeros(2 * 2 * 4 * 8 * 128)
     refused("FDEC_ERR_INVALID_ARG", cpu_tree, o_prefix=both[:8192].view(2, 4, 8, 128), out=both[4096:12288].view(2, 4, 8, 128))
+    q = torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16)
+    refused("FDEC_ERR_INVALID_ARG", cpu_tree, q=q, out=q)
     some = torch.zeros(8192)
     refused("FDEC_ERR_INVALID_ARG", cpu_tree, o_prefix=some.view(2, 4, 8, 128),
             out=some.view(torch.bfloat16)[:8192].view(2, 4, 8, 128))  # a 16-bit result over the fp32 state
