@@ -493,10 +493,10 @@ fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_
  *      [batch, num_nodes, Hq], as fdec_run writes them; or both NULL (no prefix).  A state
  *      with lse = -inf counts for nothing, whatever its o.
  *   out: contiguous, 16-byte aligned; out_type FDEC_OUT_F32 or FDEC_OUT_SAME; lse: float32 or
- *      NULL.  out may be o_prefix (FDEC_OUT_F32) and lse lse_prefix; they must not overlap
- *      otherwise, and not with q.  Rows of nodes past node_counts are not written.  A row that sees nothing
- *      gives out = 0 and lse = -inf.  Values of rows that a node does not see never reach it,
- *      NaN and infinities among them.
+ *      NULL.  out may be o_prefix (FDEC_OUT_F32) and lse lse_prefix; the two overlap nothing
+ *      else.  Rows of nodes past node_counts are not written.  A row that sees nothing gives
+ *      out = 0 and lse = -inf.  Values of rows that a node does not see never reach it, NaN
+ *      and infinities among them.
  */
 fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_stride_head, fdec_kv_desc k,
                                 fdec_kv_desc v, const int32_t* page_table, int64_t page_table_stride,
@@ -616,7 +616,9 @@ fdec_status fdec_reserve_pages_workspace(int batch, int64_t num_pages, size_t* w
  *   sources: int32 device [batch], a negative one for none; or NULL.  A bad length or source
  *      sets FDEC_DEVERR_SEQ_LEN, and that sequence is left alone.
  *   granted: int32 device [batch]: new_lens[b], or seq_lens[b] where it was refused; must not
- *      overlap the other arrays.
+ *      overlap the other arrays.  What a refused row's entries past its length name may be
+ *      another sequence's by now: no rows are to be appended there (a node_count of
+ *      granted[b] - seq_lens[b], positions below 0).
  *   num_pages: pages of the pool, at most what every cache has, and at most 2^26.
  *   caches: the rows to copy, num_caches of them (0: only page numbers are dealt with).
  *   workspace: see fdec_reserve_pages_workspace; 256-byte aligned, not shared by calls that

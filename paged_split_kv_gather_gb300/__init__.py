@@ -8,6 +8,7 @@ There is no CPU fallback: if the library is not built, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import math
@@ -753,7 +754,10 @@ def fdec_reserve_pages(page_table, seq_lens, new_lens, granted, num_pages: int, 
 class TreeDecode:
     """Rounds of speculative decoding of a batch, plans and buffers allocated once: pages for the drafted nodes, per
     layer their rows and attention, the verification, and the accepted path's rows moved behind the prefix.  Every
-    method only launches kernels, so a whole round can be captured in a CUDA graph.
+    method only launches kernels, so a whole round can be captured in a CUDA graph.  A sequence for which reserve() finds
+    no pages (or whose length is bad) has no nodes in that round: no row of it is written, its path is empty, its length
+    stays (DEVERR_NO_PAGES, and DEVERR_SEQ_LEN for the rows not written).  With a stream of its own, a call's inputs must
+    be ready on it.
 
     max_lens: the longest prefix that each sequence gets; num_nodes: the nodes of a tree; num_pages: of the pool."""
 
@@ -779,12 +783,35 @@ class TreeDecode:
                                                        for _ in range(3))
         self.errors = torch.zeros(1, dtype=torch.int32, device=device)
         self.batch_indices = torch.arange(batch, dtype=torch.int32, device=device).repeat_interleave(num_nodes)
+        # the nodes that each sequence has pages for, and their positions behind the prefix (below 0 without pages)
+        self.counts = torch.full((batch,), num_nodes, dtype=torch.int32, device=device)
         self.nodes = torch.arange(num_nodes, dtype=torch.int32, device=device)
+        self.offsets = self.nodes.repeat(batch, 1)
+        self.nowhere = torch.full((1,), -2**31, dtype=torch.int32, device=device)
+
+    def _on(self, stream):
+        """torch's own kernels (sums of lengths) go to the call's stream."""
+        import torch
+
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=self.errors.device))
+
+    def _counts(self, node_counts):
+        import torch
+
+        return self.counts if node_counts is None else torch.minimum(node_counts, self.counts)
 
     def reserve(self, page_table, prefix_lens, caches=(), sources=None, stream=None):
-        """Pages for the nodes behind prefix_lens; returns the lengths granted (prefix_lens[b] + num_nodes)."""
-        fdec_reserve_pages(page_table, prefix_lens, prefix_lens + self.num_nodes, self.granted, self.num_pages,
-                           self.page_size, self.workspace, sources, caches, self.errors, stream)
+        """Pages for the nodes behind prefix_lens; returns the lengths granted: prefix_lens[b] + num_nodes, or
+        prefix_lens[b] where there are no pages."""
+        import torch
+
+        with self._on(stream):
+            fdec_reserve_pages(page_table, prefix_lens, prefix_lens + self.num_nodes, self.granted, self.num_pages,
+                               self.page_size, self.workspace, sources, caches, self.errors, stream)
+            torch.sub(self.granted, prefix_lens, out=self.counts)
+            torch.where(self.counts[:, None] > 0, self.nodes, self.nowhere, out=self.offsets)
         return self.granted
 
     def attend(self, q, k_new, v_new, q_weight, k_weight, cos_sin, k, v, page_table, prefix_lens, parents, depths, out,
@@ -794,21 +821,23 @@ class TreeDecode:
         n, hq, d = q.shape
         if depths is None and parents is not None:
             raise ValueError("a tree's rows are rotated by the depths of its nodes")
-        positions = prefix_lens[:, None] + self.nodes
-        turns = None if depths is None else (prefix_lens[:, None] + depths).reshape(-1)
-        fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, self.batch_indices, positions.reshape(-1), q,
-                              k, v, page_table, self.page_size, eps, interleaved, turns, k_scale, v_scale, self.errors,
-                              stream)
-        rows = q.view(self.batch, self.num_nodes, hq, d)
-        self.prefix.run(rows, k, v, page_table, prefix_lens, self.o, self.state_lse, scale, stream, k_scale, v_scale)
-        fdec_tree_attention(rows, k, v, page_table, prefix_lens, parents, self.o, self.state_lse, out, lse, self.page_size,
-                            node_counts, scale, k_scale, v_scale, self.errors, stream)
+        with self._on(stream):
+            positions = (prefix_lens[:, None] + self.offsets).reshape(-1)
+            turns = None if depths is None else (prefix_lens[:, None] + depths).reshape(-1)
+            fdec_norm_rope_append(q, k_new, v_new, q_weight, k_weight, cos_sin, self.batch_indices, positions, q, k, v,
+                                  page_table, self.page_size, eps, interleaved, turns, k_scale, v_scale, self.errors,
+                                  stream)
+            rows = q.view(self.batch, self.num_nodes, hq, d)
+            self.prefix.run(rows, k, v, page_table, prefix_lens, self.o, self.state_lse, scale, stream, k_scale, v_scale)
+            fdec_tree_attention(rows, k, v, page_table, prefix_lens, parents, self.o, self.state_lse, out, lse,
+                                self.page_size, self._counts(node_counts), scale, k_scale, v_scale, self.errors, stream)
         return out
 
     def verify(self, target_probs, draft_probs, tokens, parents, uniforms, node_counts=None, stream=None):
         """Returns (path, path_lens, tokens), the holder's own tensors."""
-        fdec_verify_drafts(target_probs, draft_probs, tokens, parents, uniforms, self.path, self.path_lens, self.tokens,
-                           node_counts, self.errors, stream)
+        with self._on(stream):
+            fdec_verify_drafts(target_probs, draft_probs, tokens, parents, uniforms, self.path, self.path_lens, self.tokens,
+                               self._counts(node_counts), self.errors, stream)
         return self.path, self.path_lens, self.tokens
 
     def keep(self, caches, page_table, prefix_lens, stream=None):
@@ -820,7 +849,8 @@ class TreeDecode:
 
     def device_errors(self, clear=True, stream=None) -> int:
         """The FDEC_DEVERR_* bits of the calls so far (synchronises)."""
-        flags = int(self.errors.item())
-        if clear:
-            self.errors.zero_()
+        with self._on(stream):
+            flags = int(self.errors.item())
+            if clear:
+                self.errors.zero_()
         return flags | self.prefix.device_errors(clear, stream)

@@ -149,7 +149,14 @@ fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_s
     if (o_prefix != nullptr && !(out == o_prefix && out_type == FDEC_OUT_F32) &&
         overlap(out, out_bytes, o_prefix, rows * head_dim * 4))
         return fail(FDEC_ERR_INVALID_ARG, "out overlaps o_prefix and is not o_prefix in fp32");
-    if (out == q) return fail(FDEC_ERR_INVALID_ARG, "out must not be q");
+    const size_t q_bytes = (static_cast<size_t>(batch) * num_nodes - 1) * q_stride_tok * 2 +
+                           static_cast<size_t>(num_qo_heads - 1) * q_stride_head * 2 + head_dim * 2;
+    if (overlap(out, out_bytes, q, q_bytes)) return fail(FDEC_ERR_INVALID_ARG, "out overlaps q");
+    if (lse != nullptr && (overlap(lse, rows * 4, out, out_bytes) || overlap(lse, rows * 4, q, q_bytes) ||
+                           (o_prefix != nullptr && overlap(lse, rows * 4, o_prefix, rows * head_dim * 4))))
+        return fail(FDEC_ERR_INVALID_ARG, "lse overlaps out, q or o_prefix");
+    if (lse_prefix != nullptr && overlap(out, out_bytes, lse_prefix, rows * 4))
+        return fail(FDEC_ERR_INVALID_ARG, "out overlaps lse_prefix");
     if (lse != nullptr && lse_prefix != nullptr && lse != lse_prefix && overlap(lse, rows * 4, lse_prefix, rows * 4))
         return fail(FDEC_ERR_INVALID_ARG, "lse overlaps lse_prefix and is not lse_prefix");
     const int eb = kv8 ? 1 : 2;

@@ -1179,6 +1179,95 @@ def test_two_captured_graphs_of_one_holder():
     assert tree.device_errors() == 0
 
 
+@gpu
+def test_a_sequence_without_pages_stands_still():
+    """Its old entries name pages that are others' by now: no row is written there, and its length stays."""
+    batch, nodes, page, hq, hk, d, vocab, pages = 3, 9, 16, 8, 2, 128, 64, 8
+    torch.manual_seed(3)
+    k = torch.randn(pages, hk, page, d, device="cuda").bfloat16()
+    v = torch.randn(pages, hk, page, d, device="cuda").bfloat16()
+    tree = fd.TreeDecode([60] * batch, nodes, page, hq, hk, d, pages, "bf16")
+    lens = i32([30, 31, 32])
+    table = i32([[0, 1, 2, 3], [2, 3, 0, 1], [4, 5, 0, 1]])  # entries past the lengths: another's pages
+    qkv = torch.randn(batch * nodes, hq + 2 * hk, d, device="cuda").bfloat16()
+    fresh = qkv.clone()
+    cos_sin = torch.cat([torch.ones(200, d // 2), torch.zeros(200, d // 2)], 1).cuda()
+    target = torch.softmax(torch.randn(batch, nodes, vocab, device="cuda"), -1)
+    tokens, u = torch.zeros(batch, nodes, dtype=torch.int32, device="cuda"), torch.rand(batch, nodes, device="cuda")
+    counts = i32([nodes, nodes - 2, nodes])
+    out = torch.full((batch, nodes, hq, d), 7.0, device="cuda")
+
+    def round_of():
+        granted = tree.reserve(table, lens, (k, v)).tolist()
+        tree.attend(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], None, None, cos_sin, k, v, table, lens, None, None,
+                    out, node_counts=counts)
+        path, path_lens, words = tree.verify(target, None, tokens, None, u, counts)
+        return granted, path.tolist(), path_lens.tolist(), words.tolist(), tree.keep((k, v), table, lens).tolist()
+
+    before_k, before_v = k.clone(), v.clone()
+    granted, path, path_lens, words, kept = round_of()
+    assert granted == [39, 40, 32]  # two pages were free
+    assert tree.device_errors() == fd.DEVERR_NO_PAGES | fd.DEVERR_SEQ_LEN
+    assert path[2] == [-1] * nodes and path_lens[2] == 0 and words[2] == [-1] * nodes and kept[2] == 32
+    assert min(path_lens[:2]) >= 1 and kept[:2] == [30 + path_lens[0], 31 + path_lens[1]]
+    assert torch.equal(qkv[2 * nodes:, :hq], fresh[2 * nodes:, :hq]) and (out[2] == 7).all()
+    assert (out[0] != 7).all() and (out[1, :nodes - 2] != 7).all() and (out[1, nodes - 2:] == 7).all()
+    for pool, before in ((k, before_k), (v, before_v)):
+        changed = (pool != before).any(-1).any(1)  # [page, slot]
+        assert not changed[[0, 2, 4, 5]].any()
+        assert not changed[1, :14].any() and not changed[3, :15].any()
+    for b in range(2):
+        at = torch.arange(path_lens[b], device="cuda") + int(lens[b])
+        rows = torch.tensor(path[b][:path_lens[b]], device="cuda") + b * nodes
+        assert torch.equal(v[table[b].long()[at // page], :, at % page], fresh[rows, hq + hk:])
+    lens.copy_(i32([0, kept[1], 32]))  # a sequence has ended: its pages are there for the third
+    granted, path, path_lens, words, kept = round_of()
+    assert granted[2] == 41 and path_lens[2] >= 1 and kept[2] == 32 + path_lens[2] and (out[2] != 7).all()
+    assert tree.device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_round_on_a_stream_of_its_own(handle):
+    """The current stream is busy meanwhile: nothing of the round waits for it."""
+    batch, nodes, page, hq, hk, d, vocab, pages = 2, 5, 16, 4, 2, 64, 32, 16
+    torch.manual_seed(4)
+    k = torch.randn(pages, hk, page, d, device="cuda").half()
+    v = torch.randn(pages, hk, page, d, device="cuda").half()
+    tree = fd.TreeDecode([60] * batch, nodes, page, hq, hk, d, pages, "f16")
+    lens, table = i32([20, 16]), i32([[3, 1, 0, 0], [2, 0, 0, 0]])
+    qkv = torch.randn(batch * nodes, hq + 2 * hk, d, device="cuda").half()
+    cos_sin = torch.randn(100, d, device="cuda")
+    parents, depths = i32([[-1, 0, 0, 1, 1]] * batch), i32([[0, 1, 1, 2, 2]] * batch)
+    target = torch.softmax(torch.randn(batch, nodes, vocab, device="cuda"), -1)
+    tokens, u = i32([[0, 1, 2, 3, 4]] * batch), torch.rand(batch, nodes, device="cuda")
+    counts = i32([5, 4])
+
+    def round_of(stream):
+        state = [x.clone() for x in (k, v, table, qkv)]
+        out = torch.zeros(batch, nodes, hq, d, device="cuda")
+        torch.cuda.synchronize()
+        if stream is not None:
+            torch.cuda._sleep(200_000_000)
+        kk, vv, tt, x = state
+        tree.reserve(tt, lens, (kk, vv), stream=stream)
+        tree.attend(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], None, None, cos_sin, kk, vv, tt, lens, parents, depths, out,
+                    node_counts=counts, stream=stream)
+        tree.verify(target, None, tokens, parents, u, counts, stream=stream)
+        tree.keep((kk, vv), tt, lens, stream=stream)
+        errors = tree.device_errors(stream=stream)
+        busy = stream is not None and not torch.cuda.current_stream().query()
+        torch.cuda.synchronize()
+        return [*state, out, tree.path.clone(), tree.path_lens.clone(), tree.tokens.clone(), tree.seq_lens.clone()], errors, busy
+
+    want, errors, _ = round_of(None)
+    assert errors == 0
+    side = torch.cuda.Stream()
+    got, errors, busy = round_of(side.cuda_stream if handle else side)
+    assert errors == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert busy  # (the round ended first)
+
+
 # ------------------------------------------------------------------------------------------------------------ refusals
 
 def cpu_tree(**kw):
@@ -1231,6 +1320,14 @@ def test_tree_attention_refusals():
     refused("FDEC_ERR_INVALID_ARG", cpu_tree, o_prefix=both[:8192].view(2, 4, 8, 128), out=both[4096:12288].view(2, 4, 8, 128))
     q = torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16)
     refused("FDEC_ERR_INVALID_ARG", cpu_tree, q=q, out=q)
+    half = torch.zeros(2 * 8192, dtype=torch.bfloat16)
+    refused("FDEC_ERR_INVALID_ARG", cpu_tree, q=half[:8192].view(2, 4, 8, 128), out=half[8064:16256].view(2, 4, 8, 128))
+    # (the last row of a strided q overlaps)
+    wide = torch.zeros(8 * 3 * 1024 + 8192, dtype=torch.bfloat16)
+    refused("FDEC_ERR_INVALID_ARG", cpu_tree, q=wide[:8 * 3 * 1024].view(2, 4, 24, 128)[:, :, :8],
+            out=wide[7 * 3 * 1024:][:8192].view(2, 4, 8, 128))
+    f = torch.zeros(8192 + 64)
+    refused("FDEC_ERR_INVALID_ARG", cpu_tree, out=f[:8192].view(2, 4, 8, 128), lse=f[8160:8224].view(2, 4, 8))
     some = torch.zeros(8192)
     refused("FDEC_ERR_INVALID_ARG", cpu_tree, o_prefix=some.view(2, 4, 8, 128),
             out=some.view(torch.bfloat16)[:8192].view(2, 4, 8, 128))  # a 16-bit result over the fp32 state
