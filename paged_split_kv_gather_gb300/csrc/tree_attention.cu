@@ -172,21 +172,36 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         if (tid == 0) s_max = s_odd[0] = s_odd[1] = 0;
 
         if (run % kTreeWarps == 0) {
-            // a warp for each of the next runs
-            const int bh_of = bh + warp;
-            if (bh_of == bh || bh_of * tiles_max < share_end) {
-                const int b_of = bh_of / p.hk, kvh_of = bh_of - b_of * p.hk;
-                const bool reports = (warp > 0 || first == 0) && kvh_of == 0 && p.err != nullptr;  // one CTA a sequence
+            // Warp w takes the rows of the run w from here and, meanwhile, the ancestors of the run w + 1: of a single run
+            // two warps share the work.
+            constexpr int H = KS > 2 ? 2 : 1;  // halves of the 64 nodes that there can be
+            const int w_anc = (warp + 1) % kTreeWarps;
+            const int bh_rows = bh + warp, bh_anc = bh + w_anc;
+            const bool has_rows = bh_rows == bh || bh_rows * tiles_max < share_end;
+            const bool has_anc = bh_anc == bh || bh_anc * tiles_max < share_end;
+            const auto reports = [&](int bh_of) {  // one CTA a sequence
+                return p.err != nullptr && bh_of % p.hk == 0 && (bh_of > bh || first == 0);
+            };
+            int up[H], n_anc = N;
+            if (has_anc) {
+                const int b_of = bh_anc / p.hk;
+                if (p.node_counts != nullptr) n_anc = p.node_counts[b_of];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int i = lane + 32 * h;
+                    up[h] = p.parents == nullptr ? i - 1 : i < N ? p.parents[static_cast<int64_t>(b_of) * N + i] : -1;
+                }
+            }
+            if (has_rows) {
+                const int b_of = bh_rows / p.hk, kvh_of = bh_rows - b_of * p.hk;
                 unsigned flags = 0;
                 int n = p.node_counts != nullptr ? p.node_counts[b_of] : N;
                 int64_t prefix = p.prefix_lens[b_of];
-                int up[2];
-                int64_t page[2], slot_of[2];
-                bool behind[2];  // past the page table
+                int64_t page[H], slot_of[H];
+                bool behind[H];  // past the page table
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < H; ++h) {
                     const int i = lane + 32 * h;
-                    up[h] = p.parents == nullptr ? i - 1 : i < N ? p.parents[static_cast<int64_t>(b_of) * N + i] : -1;
                     const int64_t pos = max(prefix, static_cast<int64_t>(0)) + i, pi = pos >> p.page_shift;
                     slot_of[h] = pos & ((1 << p.page_shift) - 1);
                     behind[h] = pi >= p.pt_stride;
@@ -197,49 +212,66 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     n = min(max(n, 0), N);
                 }
                 if (prefix < 0 && n > 0) flags |= FDEC_DEVERR_SEQ_LEN;
-                uint64_t anc[2], valid = 0;
+                uint64_t valid = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < H; ++h) {
                     const int i = lane + 32 * h;
-                    if (up[h] < -1 || up[h] >= i) {
-                        if (i < n) flags |= FDEC_DEVERR_TREE;
-                        up[h] = -1;
-                    }
-                    anc[h] = uint64_t{1} << i;
                     const bool ok = i < n && page[h] >= 0 && page[h] < p.k_pages && page[h] < p.v_pages;
                     if (i < n && !ok) flags |= behind[h] ? FDEC_DEVERR_SEQ_LEN : FDEC_DEVERR_PAGE_ID;
                     valid |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * h);
                     s_k[warp][i] = page[h] * p.k_sp + slot_of[h] * p.k_st + kvh_of * p.k_sh;
                     s_v[warp][i] = page[h] * p.v_sp + slot_of[h] * p.v_st + kvh_of * p.v_sh;
                 }
-                // ancestors: bits of a node's path, by pointer doubling (a path has at most 63 steps)
-#pragma unroll
-                for (int step = 0; step < 6; ++step) {
-                    uint64_t a[2];
-                    int u[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int from = up[h] & 31;
-                        const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], from);
-                        const uint64_t a1 = __shfl_sync(0xffffffffu, anc[1], from);
-                        const int u0 = __shfl_sync(0xffffffffu, up[0], from);
-                        const int u1 = __shfl_sync(0xffffffffu, up[1], from);
-                        a[h] = up[h] < 0 ? 0 : up[h] < 32 ? a0 : a1;
-                        u[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        anc[h] |= a[h];
-                        up[h] = u[h];
-                    }
-                }
-                s_anc[warp][lane] = anc[0];
-                s_anc[warp][lane + 32] = anc[1];
                 if (lane == 0) {
                     s_valid[warp] = valid;
                     s_count[warp] = n;
                 }
-                if (reports && flags != 0) atomicOr(p.err, flags);
+                if (flags != 0 && reports(bh_rows)) atomicOr(p.err, flags);
+            }
+            if (has_anc) {
+                uint64_t anc[H];
+                bool bad = false;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int i = lane + 32 * h;
+                    if (up[h] < -1 || up[h] >= i) {
+                        bad |= i < min(n_anc, N);
+                        up[h] = -1;
+                    }
+                    anc[h] = uint64_t{1} << i;
+                }
+                // ancestors: bits of a node's path, by pointer doubling (a path has at most 16 KS - 1 steps)
+#pragma unroll 1
+                for (int step = 0; step < 6; ++step) {
+                    bool rest = false;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) rest |= up[h] >= 0;
+                    if (!__any_sync(0xffffffffu, rest)) break;
+                    uint64_t a[H];
+                    int u[H];
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const int from = up[h] & 31;
+                        uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], from);
+                        int u0 = __shfl_sync(0xffffffffu, up[0], from);
+                        if constexpr (H > 1) {
+                            const uint64_t a1 = __shfl_sync(0xffffffffu, anc[H - 1], from);
+                            const int u1 = __shfl_sync(0xffffffffu, up[H - 1], from);
+                            a0 = up[h] < 32 ? a0 : a1;
+                            u0 = up[h] < 32 ? u0 : u1;
+                        }
+                        a[h] = up[h] < 0 ? 0 : a0;
+                        u[h] = up[h] < 0 ? -1 : u0;
+                    }
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        anc[h] |= a[h];
+                        up[h] = u[h];
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h) s_anc[w_anc][lane + 32 * h] = anc[h];
+                if (bad && reports(bh_anc)) atomicOr(p.err, FDEC_DEVERR_TREE);
             }
         }
         __syncthreads();
@@ -310,9 +342,6 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        next_tile(0);
-        request_prefix(cb0, rows);
-
         // K and V rows, widened to 16 bits; rows past the tree and unreadable ones are zeros
         constexpr int staged = 16 * KS;
         uint8_t* sm_k = smem;
@@ -344,6 +373,10 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     kk[u] = *reinterpret_cast<const uint4*>(p.k_base + s_k[known][j] + (c - j * CH) * 16);
                     vv[u] = *reinterpret_cast<const uint4*>(p.v_base + s_v[known][j] + (c - j * CH) * 16);
                 }
+            }
+            if (i0 == 0) {
+                next_tile(0);
+                request_prefix(cb0, rows);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
