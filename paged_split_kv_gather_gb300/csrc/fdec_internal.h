@@ -306,6 +306,7 @@ struct TreeParams {
     float v_scale;
     // Set by the launcher: CTAs of a sequence's KV head, or 0: shares of so many tiles, one more in the first.
     int parts, share, share_more;
+    uint64_t group_inv;  // set by the launcher: ceil(2^40 / group)
 };
 cudaError_t launch_tree_attention(const TreeParams& p, int head_dim, bool bf16, bool kv8, int num_sms, cudaStream_t s);
 

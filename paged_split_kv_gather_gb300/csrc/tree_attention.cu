@@ -148,26 +148,32 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
     const int tiles_max = (N * g + 15) / 16;  // of a sequence's KV head
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // The CTA's tiles: a part of a sequence's KV head, or an equal share of all tiles, a run of them for each sequence
     // and KV head in it.
-    int at_tile, share_end;
+    int bh, first, left;  // sequence and KV head, its first tile of a run, tiles from there on
     const int c = blockIdx.x;
     if (p.parts > 0) {
-        const int head = c / p.parts, part = c - head * p.parts;
-        at_tile = head * tiles_max + tiles_max * part / p.parts;
-        share_end = head * tiles_max + tiles_max * (part + 1) / p.parts;
+        bh = c / p.parts;
+        const int part = c - bh * p.parts;
+        first = tiles_max * part / p.parts;
+        left = tiles_max * (part + 1) / p.parts - first;
     } else {
-        at_tile = c * p.share + min(c, p.share_more);
-        share_end = at_tile + p.share + (c < p.share_more);
+        const int at_tile = c * p.share + min(c, p.share_more);
+        bh = at_tile / tiles_max;
+        first = at_tile - bh * tiles_max;
+        left = p.share + (c < p.share_more);
     }
-    for (int run = 0; at_tile < share_end; ++run) {
-        const int bh = at_tile / tiles_max;
-        const int b = bh / p.hk, kvh = bh - b * p.hk;
-        const int first = at_tile - bh * tiles_max;
-        const int count = min(share_end - at_tile, tiles_max - first);
-        at_tile += count;
+    int b = bh / p.hk, kvh = bh - b * p.hk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const auto next_run = [&] {
+        left -= tiles_max - first;
+        first = 0;
+        ++bh;
+        if (++kvh == p.hk) kvh = 0, ++b;
+    };
+    for (int run = 0; left > 0; ++run, next_run()) {
+        const int count = min(left, tiles_max - first);
         __syncthreads();  // what was staged before has been read
         if (tid == 0) s_max = s_odd[0] = s_odd[1] = 0;
 
@@ -176,15 +182,15 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
             // two warps share the work.
             constexpr int H = KS > 2 ? 2 : 1;  // halves of the 64 nodes that there can be
             const int w_anc = (warp + 1) % kTreeWarps;
-            const int bh_rows = bh + warp, bh_anc = bh + w_anc;
-            const bool has_rows = bh_rows == bh || bh_rows * tiles_max < share_end;
-            const bool has_anc = bh_anc == bh || bh_anc * tiles_max < share_end;
-            const auto reports = [&](int bh_of) {  // one CTA a sequence
-                return p.err != nullptr && bh_of % p.hk == 0 && (bh_of > bh || first == 0);
+            const auto has = [&](int ahead) { return ahead == 0 || ahead * tiles_max < first + left; };
+            const auto seq_of = [&](int ahead) { return ahead == 0 ? b : (bh + ahead) / p.hk; };
+            const bool has_rows = has(warp), has_anc = has(w_anc);
+            const auto reports = [&](int ahead, int b_of) {  // one CTA a sequence
+                return p.err != nullptr && bh + ahead == b_of * p.hk && (ahead > 0 || first == 0);
             };
             int up[H], n_anc = N;
             if (has_anc) {
-                const int b_of = bh_anc / p.hk;
+                const int b_of = seq_of(w_anc);
                 if (p.node_counts != nullptr) n_anc = p.node_counts[b_of];
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                 }
             }
             if (has_rows) {
-                const int b_of = bh_rows / p.hk, kvh_of = bh_rows - b_of * p.hk;
+                const int b_of = seq_of(warp), kvh_of = bh + warp - b_of * p.hk;
                 unsigned flags = 0;
                 int n = p.node_counts != nullptr ? p.node_counts[b_of] : N;
                 int64_t prefix = p.prefix_lens[b_of];
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     s_valid[warp] = valid;
                     s_count[warp] = n;
                 }
-                if (flags != 0 && reports(bh_rows)) atomicOr(p.err, flags);
+                if (flags != 0 && reports(warp, b_of)) atomicOr(p.err, flags);
             }
             if (has_anc) {
                 uint64_t anc[H];
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                 }
 #pragma unroll
                 for (int h = 0; h < H; ++h) s_anc[w_anc][lane + 32 * h] = anc[h];
-                if (bad && reports(bh_anc)) atomicOr(p.err, FDEC_DEVERR_TREE);
+                if (bad && reports(w_anc, seq_of(w_anc))) atomicOr(p.err, FDEC_DEVERR_TREE);
             }
         }
         __syncthreads();
@@ -290,6 +296,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         const int split = tiles - first > 2 ? 1 : min(tiles - first == 2 ? 2 : kTreeWarps, CB);
         const int T0 = first + warp / split, part = warp % split;
         const int cb0 = part * CB / split, cb1 = (part + 1) * CB / split;
+        // Heads of more than QD dims: S, too, in parts, blocks of 32 dims [d0, d1), added up through shared memory.
+        constexpr bool kAddParts = D > QD;
+        const int d0 = kAddParts ? part * (D / 32) / split : 0, d1 = kAddParts ? (part + 1) * (D / 32) / split : D / 32;
         const int my_tiles = T0 < tiles ? (split > 1 ? 1 : (tiles - T0 + kTreeWarps - 1) / kTreeWarps) : 0;
         const uint32_t q_slot = smem_addr(smem) + 2 * 16 * KS * S::PITCH + warp * (S::Q_BYTES + kSlotBytes);
         const uint32_t slot = q_slot + S::Q_BYTES;
@@ -303,7 +312,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         };
         const auto next_tile = [&](int it) {
             const int r = (T0 + it * kTreeWarps) * 16 + (lane & 15);
-            nodes = it < my_tiles && r < R ? r / g : 0;
+            // (r / g: r is below 2^22 and g at most 2^16, so what group_inv has too much stays below 2^38 / 2^40 / g)
+            nodes = it < my_tiles && r < R ? static_cast<int>(static_cast<uint64_t>(r) * p.group_inv >> 40) : 0;
             rows = it < my_tiles && r < R ? (b * N + nodes) * p.hq + kvh * g + (r - nodes * g) : -1;
             if (it < my_tiles) {
                 const uint16_t* mine = rows >= 0 ? query(rows, nodes) : p.q;
@@ -313,10 +323,11 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     const int r = k * RPI + lane / CH, c = lane % CH;
                     const uint16_t* from = reinterpret_cast<const uint16_t*>(
                         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
-                    const int there = __shfl_sync(0xffffffffu, rows, r) >= 0 ? 16 : 0;  // (zeros past the last row)
+                    // (zeros past the last row, and past the part's dims)
+                    const bool there = __shfl_sync(0xffffffffu, rows, r) >= 0 && (!kAddParts || d0 * 4 + c < d1 * 4);
                     const uint32_t to = q_slot + r * QD * 2 + (c ^ (r & 7)) * 16;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + c * 8),
-                                 "r"(there)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                                 "l"(there ? from + d0 * 32 + c * 8 : p.q), "r"(there ? 16 : 0)
                                  : "memory");
                 }
             }
@@ -466,21 +477,41 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                 ldmatrix_x4(q_addr + ((4 * c + (lane >> 4)) ^ (lane & 7)) * 16, a0[0], a0[1], a0[2], a0[3]);
                 ldmatrix_x4(q_addr + ((4 * c + 2 + (lane >> 4)) ^ (lane & 7)) * 16, a1[0], a1[1], a1[2], a1[3]);
                 if (c == 0)
-                    add_scores<BF16, KS, true>(s, a0, a1, k_addr, S::PITCH);
-                else
-                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + c * 64, S::PITCH);
+                    add_scores<BF16, KS, true>(s, a0, a1, k_addr + d0 * 64, S::PITCH);
+                else if (!kAddParts || d0 + c < d1)
+                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + (d0 + c) * 64, S::PITCH);
             }
-            if constexpr (D > QD) {  // the other dims from where they are
+            if constexpr (kAddParts) {  // the other dims from where they are
                 const uint16_t* from[2] = {(row[0] >= 0 ? query(row[0], node[0]) : p.q) + 2 * t,
                                            (row[1] >= 0 ? query(row[1], node[1]) : p.q) + 2 * t};
                 const auto word = [&](int h, int d) {
                     return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
                 };
 #pragma unroll 6
-                for (int d = QD; d < D; d += 32) {
+                for (int d = d0 * 32 + QD; d < d1 * 32; d += 32) {
                     const uint32_t a0[4] = {word(0, d), word(1, d), word(0, d + 8), word(1, d + 8)};
                     const uint32_t a1[4] = {word(0, d + 16), word(1, d + 16), word(0, d + 24), word(1, d + 24)};
                     add_scores<BF16, KS, false>(s, a0, a1, k_addr + d * 2, S::PITCH);
+                }
+                if (split > 1) {  // (where the queries lay)
+                    const uint32_t at = lane * 16;
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(q_slot + at + j * 512), "f"(s[j][0]),
+                                     "f"(s[j][1]), "f"(s[j][2]), "f"(s[j][3])
+                                     : "memory");
+                    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / split), "r"(32 * split) : "memory");
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+                    for (int k = 0; k < split; ++k) {  // (every warp in the same order)
+                        const uint32_t from = q_slot + (k - part) * (S::Q_BYTES + kSlotBytes) + at;
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const float4 x = lds128f<0>(from + j * 512);
+                            s[j][0] += x.x, s[j][1] += x.y, s[j][2] += x.z, s[j][3] += x.w;
+                        }
+                    }
                 }
             }
 
@@ -536,7 +567,12 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
             const bool states = !__any_sync(0xffffffffu, empty[0] || empty[1]);
             const int rows_now = rows;
             __syncwarp();  // the queries have been read
-            next_tile(it + 1);
+            if (it + 1 < my_tiles) {
+                next_tile(it + 1);
+            } else {
+                rows = -1;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
 
             uint32_t pf[KS][2][4];
 #pragma unroll
@@ -698,6 +734,7 @@ cudaError_t launch_tree_one(TreeParams p, int num_sms, cudaStream_t s) {
     const int64_t grid = p.parts > 0 ? heads * p.parts : slots;
     p.share = static_cast<int>(heads * per_head / slots);
     p.share_more = static_cast<int>(heads * per_head % slots);
+    p.group_inv = ((uint64_t{1} << 40) + p.group - 1) / p.group;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(kTreeThreads, 1, 1);
