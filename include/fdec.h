@@ -522,7 +522,7 @@ enum { FDEC_PROB_F16 = 0, FDEC_PROB_BF16 = 1, FDEC_PROB_F32 = 2 };
  * the target's own.  Without draft_probs the children count as given (the draft's most likely
  * tokens, say): q is 1 at the token tried, so c stands if uniforms[c] * W < p(t), and else
  * loses its weight, W = the sum of p without the tokens tried.  Sums are carried in pairs of
- * fp32 and in fp64: about 46 bits.
+ * fp32 values: about 46 bits.
  *   target_probs: device [batch][num_nodes][vocab] of prob_dtype: element (b, i, v) at
  *      target_probs + b * target_stride_seq + i * target_stride_node + v (elements).
  *      Probabilities count as clamped to [0, 2] and NaN as 0; one that is not in there, where

@@ -47,16 +47,6 @@ constexpr int kMostRuns = kMostCtas * kVerifyWarps;
 
 enum Op : int { kSum = 0, kDraw = 1, kStop = 2 };
 
-struct Order {       // what comes next
-    int op;
-    int node;        // whose rows
-    int run;         // kDraw: the warp's run of the vocabulary that holds the token
-    int place;       // index of the next token in out_tokens
-    double s;        // weight of q
-    double target;   // kDraw: cumulative weight to pass, from the run's begin
-    uint64_t gone;   // without draft rows: children whose tokens have lost their weight
-};
-
 __device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ float value(const __half* p) { return __half2float(*p); }
 __device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -94,20 +84,38 @@ struct Pair {
         hi = sum;
         lo = __fadd_rn(lo, __fadd_rn(err, e));
     }
-    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+    __device__ __forceinline__ Pair plus(Pair x) const {  // lo small against hi again, whatever has cancelled
+        Pair d = *this;
+        d.add(x.hi, x.lo);
+        const float sum = __fadd_rn(d.hi, d.lo);
+        return {sum, __fadd_rn(__fsub_rn(d.hi, sum), d.lo)};
+    }
+    __device__ __forceinline__ Pair minus(Pair x) const { return plus({-x.hi, -x.lo}); }
+    __device__ __forceinline__ Pair times(float x) const {
+        const float t = __fmul_rn(hi, x);
+        return {t, __fmaf_rn(lo, x, __fmaf_rn(hi, x, -t))};
+    }
+    __device__ __forceinline__ Pair times(Pair x) const {
+        const float t = __fmul_rn(hi, x.hi);
+        return {t, __fmaf_rn(lo, x.hi, __fmaf_rn(hi, x.lo, __fmaf_rn(hi, x.hi, -t)))};
+    }
+    __device__ __forceinline__ bool positive() const { return __fadd_rn(hi, lo) > 0.f; }
     __device__ __forceinline__ bool above(Pair x) const {
         Pair d = *this;
         d.add(-x.hi, -x.lo);
-        return __fadd_rn(d.hi, d.lo) > 0.f;
+        return d.positive();
     }
 };
 
-__device__ __forceinline__ Pair pair_of(double x) {
-    Pair p;
-    p.hi = static_cast<float>(x);
-    p.lo = static_cast<float>(x - static_cast<double>(p.hi));
-    return p;
-}
+struct Order {       // what comes next
+    int op;
+    int node;        // whose rows
+    int run;         // kDraw: the warp's run of the vocabulary that holds the token
+    int place;       // index of the next token in out_tokens
+    Pair s;          // weight of q
+    Pair target;     // kDraw: cumulative weight to pass, from the run's begin
+    uint64_t gone;   // without draft rows: children whose tokens have lost their weight
+};
 
 __device__ __forceinline__ Pair warp_sum(Pair v) {
 #pragma unroll
@@ -237,7 +245,7 @@ __device__ __forceinline__ Pair mode_sum(const T* p, const T* q, int begin, int 
 
 // One warp's sum over tokens [begin, end).  AHEAD: vectors of each row in flight a lane.
 template <typename T, bool VEC, int AHEAD>
-__device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, double s, const Node* nodes,
+__device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, Pair s, const Node* nodes,
                                         uint64_t gone, bool& bad) {
     const int lane = threadIdx.x & 31;
     Pair sum = {};
@@ -263,22 +271,12 @@ __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int e
         }
     } else if (q == nullptr) {
         sum = mode_sum<T, VEC, 0, AHEAD>(p, q, begin, end, sum, bad);
-    } else if (s == 1.0) {  // the first to fall: nearly all sums
+    } else if (s.hi == 1.f && s.lo == 0.f) {  // the first to fall: nearly all sums
         sum = mode_sum<T, VEC, 1, AHEAD>(p, q, begin, end, sum, bad);
     } else {
-        sum = mode_sum<T, VEC, 2, AHEAD>(p, q, begin, end, pair_of(s), bad);
+        sum = mode_sum<T, VEC, 2, AHEAD>(p, q, begin, end, s, bad);
     }
     return warp_sum(sum);
-}
-
-__device__ __forceinline__ double warp_scan_double(double v) {  // inclusive
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-    }
-    return v;
 }
 
 // What a walk goes by: the same bits in every CTA.
@@ -291,10 +289,10 @@ struct Walk {
     Tree tree;
     Pair sum[2][kMostRuns];  // every warp's sum, of even and of odd rounds
     int path[kMaxNodes];
-    double s;
+    Pair s;
     // Without draft rows: the target's row is summed once, and a token that falls is taken from that sum.  The
     // difference keeps the sum's absolute error: where it is small (exact), the row is summed without the tokens.
-    double row_total, row_gone;
+    Pair row_total, row_gone;
     uint64_t weighed;   // the children whose tokens make up row_gone, each token once
     uint64_t gone, left;  // children that have fallen, that are still to try
     int x, len;
@@ -305,39 +303,43 @@ struct Walk {
 // The run of the vocabulary that holds the next token (o.run, o.target), from every warp's sum (a lane's `mine`, their
 // sum, the sum up to the lane), less the tokens of the children `weighed`.  A warp; false where nothing is left.
 constexpr int kRunsPerLane = kMostRuns / 32;
-__device__ __forceinline__ bool draw_run(const Tree& tree, double (&mine)[kRunsPerLane], double part, double upto,
-                                         uint64_t weighed, int chunk, Order& o) {
+__device__ __forceinline__ bool draw_run(const Tree& tree, Pair (&mine)[kRunsPerLane], Pair upto, uint64_t weighed,
+                                         int chunk, Order& o) {
     const int lane = threadIdx.x & 31;
     constexpr int PER = kRunsPerLane;
     if (weighed != 0) {
-        part = 0.0;
         for (uint64_t m = weighed; m != 0; m &= m - 1) {
             const int c = __ffsll(static_cast<long long>(m)) - 1;
             const int run = tree.node[c].tok / chunk;
 #pragma unroll
             for (int k = 0; k < PER; ++k)
                 if (run == lane * PER + k) {
-                    const double rest = mine[k] - static_cast<double>(tree.node[c].p);
-                    mine[k] = rest > mine[k] * 0x1p-42 ? rest : 0.0;  // (what rounding left is nothing)
+                    const Pair rest = mine[k].minus({tree.node[c].p, 0.f});
+                    mine[k] = rest.hi > mine[k].hi * 0x1p-42f ? rest : Pair{0.f, 0.f};  // (what rounding left is nothing)
                 }
         }
+        Pair part = mine[0];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) part += mine[k];
-        upto = warp_scan_double(part);
+        for (int k = 1; k < PER; ++k) part.add(mine[k].hi, mine[k].lo);
+        upto = warp_scan(part);
     }
-    const double W = __shfl_sync(0xffffffffu, upto, 31);
-    if (!(W > 0.0)) return false;
-    const double goal = static_cast<double>(tree.node[0].u) * W;
+    const Pair W = {__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
+    if (!W.positive()) return false;
+    const Pair goal = W.times(tree.node[0].u);
     int run = -1, last = -1;
-    double at = upto - part, from = 0.0;
+    Pair at = {__shfl_up_sync(0xffffffffu, upto.hi, 1), __shfl_up_sync(0xffffffffu, upto.lo, 1)}, from = {0.f, 0.f};
+    if (lane == 0) at = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        if (mine[k] > 0.0) last = lane * PER + k;
-        if (run < 0 && mine[k] > 0.0 && at + mine[k] > goal) {
-            run = lane * PER + k;
-            from = at;
+        const Pair before = at;
+        at.add(mine[k].hi, mine[k].lo);
+        if (mine[k].hi > 0.f) {
+            last = lane * PER + k;
+            if (run < 0 && at.above(goal)) {
+                run = last;
+                from = before;
+            }
         }
-        at += mine[k];
     }
     const unsigned found = __ballot_sync(0xffffffffu, run >= 0);
     const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
@@ -345,10 +347,10 @@ __device__ __forceinline__ bool draw_run(const Tree& tree, double (&mine)[kRunsP
     if (found != 0) {
         const int who = __ffs(found) - 1;
         o.run = __shfl_sync(0xffffffffu, run, who);
-        o.target = goal - __shfl_sync(0xffffffffu, from, who);
+        o.target = goal.minus({__shfl_sync(0xffffffffu, from.hi, who), __shfl_sync(0xffffffffu, from.lo, who)});
     } else {  // (only by rounding: the last run with weight, its last token)
         o.run = __shfl_sync(0xffffffffu, last, 31 - __clz(any));
-        o.target = 4.0 * W;
+        o.target = W.times(4.f);
     }
     return true;
 }
@@ -367,7 +369,7 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs,
                static_cast<uint64_t>(__ballot_sync(0xffffffffu, par1 == node)) << 32;
     };
     int x = 0, len = 1;
-    double s = 0.0, W = 1.0, row_total = 0.0, row_gone = 0.0;
+    Pair s = {0.f, 0.f}, W = {1.f, 0.f}, row_total = {0.f, 0.f}, row_gone = {0.f, 0.f};
     uint64_t gone = 0, left = 0, weighed = 0;
     bool have_row = false, exact = false, summed = false, whole = false;
     if (sums != nullptr) {
@@ -381,63 +383,64 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs,
     }
     Order o = {};
     o.op = kStop;
-    double mine[PER], part = 0.0, upto = 0.0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) mine[k] = 0.0;
+    Pair mine[PER] = {}, upto = {0.f, 0.f};
     if (tree.n > 0) {
         bool ask = false;
         if (sums != nullptr) {  // the sums that were asked for
 #pragma unroll
-            for (int k = 0; k < PER; ++k) part += mine[k] = lane * PER + k < runs ? sums[lane * PER + k].value() : 0.0;
-            upto = warp_scan_double(part);
-            W = __shfl_sync(0xffffffffu, upto, 31);
+            for (int k = 0; k < PER; ++k) {
+                if (lane * PER + k < runs) mine[k] = sums[lane * PER + k];
+                upto.add(mine[k].hi, mine[k].lo);
+            }
+            upto = warp_scan(upto);
+            W = {__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
             summed = true;
             if (!drafted && !exact && !whole) {
                 row_total = W;
                 have_row = true;
-                W = row_total - row_gone;
-                if (!(W * 64.0 > row_total)) ask = exact = true;
+                W = row_total.minus(row_gone);
+                if (!(W.hi * 64.f > row_total.hi)) ask = exact = true;
             }
-            if (!ask && !(W > 0.0)) left = 0;
+            if (!ask && !W.positive()) left = 0;
         }
         while (left != 0 && !ask) {
             const int c = __ffsll(static_cast<long long>(left)) - 1;
             left &= left - 1;
             const int t = tree.node[c].tok;
-            double rest = tree.node[c].p;
+            const float q = tree.node[c].q;
+            Pair rest = {tree.node[c].p, 0.f};
             if (drafted) {
-                rest = fmax(rest - s * static_cast<double>(tree.node[c].q), 0.0);
+                rest = rest.minus(s.times(q));
+                if (!rest.positive()) rest = {0.f, 0.f};
             } else {
                 const uint64_t same = static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok0 == t)) |
                                       static_cast<uint64_t>(__ballot_sync(0xffffffffu, tok1 == t)) << 32;
-                if (same & gone) rest = 0.0;
+                if (same & gone) rest = {0.f, 0.f};
             }
-            if (static_cast<double>(tree.node[c].u) * W * static_cast<double>(tree.node[c].q) < rest) {
+            if (rest.above(W.times(Pair{tree.node[c].u, 0.f}.times(q)))) {
                 x = c;
                 if (lane == 0) walk.path[len] = c;
                 ++len;
-                s = 0.0, W = 1.0, gone = 0, summed = false;
-                row_gone = 0.0, weighed = 0, have_row = exact = false;
+                s = {0.f, 0.f}, W = {1.f, 0.f}, gone = 0, summed = false;
+                row_gone = {0.f, 0.f}, weighed = 0, have_row = exact = false;
                 left = children(c);
             } else {
-                s += W;
+                s = s.plus(W);
                 gone |= uint64_t{1} << c;
-                if (!drafted && rest > 0.0) {
-                    row_gone += rest;
+                if (!drafted && rest.hi > 0.f) {
+                    row_gone = row_gone.plus(rest);
                     weighed |= uint64_t{1} << c;
                 }
-                if (!drafted && have_row && !exact && (row_total - row_gone) * 64.0 > row_total)
-                    W = row_total - row_gone;
-                else
-                    ask = true;
+                W = row_total.minus(row_gone);
+                if (drafted || !have_row || exact || !(W.hi * 64.f > row_total.hi)) ask = true;
                 if (ask && have_row) exact = true;
             }
         }
         const bool plain = drafted || exact || whole;  // (the sums are those of what is left)
-        if (!ask && !(summed && draw_run(tree, mine, part, upto, plain ? 0 : weighed, chunk, o))) {  // no child stands
+        if (!ask && !(summed && draw_run(tree, mine, upto, plain ? 0 : weighed, chunk, o))) {  // no child stands
             if (summed) {  // nothing is left: the target's row itself, if that is not it already
                 ask = !whole;
-                s = 0.0, gone = 0;
+                s = {0.f, 0.f}, gone = 0;
             } else {  // no child has fallen here
                 ask = true;
             }
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         if (o.op != kSum) break;
         const T* prow = target + o.node * p.t_node;
         // (the target's row itself needs no q; a leaf has none)
-        const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
+        const T* qrow = draft != nullptr && o.s.hi != 0.f ? draft + o.node * p.d_node : nullptr;
         const int run = rank * kVerifyWarps + warp;
         const int64_t begin = static_cast<int64_t>(run) * p.chunk;
         Pair sum = {};
@@ -587,14 +590,14 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
     if (o.op == kDraw && o.run / kVerifyWarps == rank) {
         // the run's tokens, a stretch for each thread in their order
         const T* prow = target + o.node * p.t_node;
-        const T* qrow = draft != nullptr && o.s != 0.0 ? draft + o.node * p.d_node : nullptr;
+        const T* qrow = draft != nullptr && o.s.hi != 0.f ? draft + o.node * p.d_node : nullptr;
         const int64_t begin = static_cast<int64_t>(o.run) * p.chunk;
         const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
         const int per = (p.chunk + kVerifyThreads - 1) / kVerifyThreads;
         const int v0 = static_cast<int>(min(static_cast<int64_t>(end), begin + static_cast<int64_t>(tid) * per));
         const int v1 = min(end, v0 + per);
         constexpr int U = 8;
-        const Pair weight = pair_of(o.s), target_sum = pair_of(o.target);
+        const Pair weight = o.s, target_sum = o.target;
         Pair mine = {};
         for (int v = v0; v < v1; v += U) {
             float a[U], c[U];
