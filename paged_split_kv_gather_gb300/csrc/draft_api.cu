@@ -247,9 +247,7 @@ fdec_status fdec_verify_drafts(const void* target_probs, int64_t target_stride_s
     p.nodes = num_nodes;
     p.vocab = vocab;
     if (checks_only()) return static_cast<fdec_status>(kChecksOnly);
-    int num_sms = 0;
-    cudaError_t e = current_num_sms(&num_sms);
-    if (e == cudaSuccess) e = launch_verify_drafts(p, prob_dtype, num_sms, stream);
+    const cudaError_t e = launch_verify_drafts(p, prob_dtype, stream);
     if (e != cudaSuccess) return fail_cuda(e, "launching the verification");
     return FDEC_OK;
 }

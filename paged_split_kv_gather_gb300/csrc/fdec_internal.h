@@ -330,7 +330,7 @@ struct VerifyParams {
     int batch, nodes, vocab;
     int chunk;                   // tokens of a warp, set by the launcher
 };
-cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, cudaStream_t s);
 
 // Caches of a call that moves rows, as kernel arguments.  first_block: blocks of columns
 // of the caches before this one.

@@ -12,8 +12,10 @@
 // Bytes: 2 D of q, 4 D of o_p, 4 D or 2 D of the result for a query row, against 4 D x 64
 // operations or less: bound by HBM, if anything hides the latencies.  Queries and o_p are
 // therefore copied into shared memory a tile and a block ahead (requested where they are
-// used, or held in registers, 64 trees of 64 nodes took 73 and 52 us; now 42, 4.4 TB/s, with
-// the L1 pipe 60 % busy).  mma.sync keeps S and P in registers; a tcgen05 tile of 128 rows
+// used, or held in registers, 64 trees of 64 nodes took 73 and 52 us; now 40.4, 4.6 TB/s, with
+// the L1 pipe 60 % busy).  Few small trees are latencies: lengths, page ids, keys and values
+// are three dependent reads (of 3.7 us for one tree; 1 us for the first two), which is why the
+// rest is asked for behind them and the ancestors are another warp's.  mma.sync keeps S and P in registers; a tcgen05 tile of 128 rows
 // would be mostly empty for trees of a few nodes, and the tensor pipe is not what bounds.
 //
 // P V multiplies f16 values: V as f16, and each probability as two f16 values (22 bits,
@@ -126,7 +128,7 @@ __device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
 }
 
 // CTAs on an SM: by the registers of S, P and O.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
-// nodes 10.0 us instead of 12.5; but at head_dim 256 16 trees of 13 nodes 8.3 us instead of 7.4.)
+// nodes 8.4 us instead of 10.6; but at head_dim 256 16 trees of 13 nodes 6.5 us instead of 6.0.)
 constexpr int tree_ctas(int head_dim, int ks) { return ks == 1 && head_dim <= 128 ? 4 : 3; }
 
 template <int D, bool BF16, bool KV8, int KS>
@@ -296,7 +298,8 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         const int split = tiles - first > 2 ? 1 : min(tiles - first == 2 ? 2 : kTreeWarps, CB);
         const int T0 = first + warp / split, part = warp % split;
         const int cb0 = part * CB / split, cb1 = (part + 1) * CB / split;
-        // Heads of more than QD dims: S, too, in parts, blocks of 32 dims [d0, d1), added up through shared memory.
+        // Heads of more than QD dims: S, too, in parts, blocks of 32 dims [d0, d1), added up through shared memory (16
+        // trees of 13 nodes, head_dim 256, 6.0 us instead of 6.9; at 128 dims the sums would cost what they save).
         constexpr bool kAddParts = D > QD;
         const int d0 = kAddParts ? part * (D / 32) / split : 0, d1 = kAddParts ? (part + 1) * (D / 32) / split : D / 32;
         const int my_tiles = T0 < tiles ? (split > 1 ? 1 : (tiles - T0 + kTreeWarps - 1) / kTreeWarps) : 0;
@@ -721,9 +724,9 @@ cudaError_t launch_tree_one(TreeParams p, int num_sms, cudaStream_t s) {
         if (dev < 64) __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
     }
     // Up to as many sequences' KV heads as CTAs are resident, or with fewer tiles in each than a CTA has warps: parts
-    // of one head each, as an equal share that spans two stages two trees (256 heads of 6 tiles: 7.9 us, 11.2 shared).
+    // of one head each, as an equal share that spans two stages two trees (256 heads of 6 tiles: 7.0 us, 9.0 shared).
     // Else equal shares: whole heads in a second round would leave most of the machine idle (512 heads of 16 tiles:
-    // 42 us, 55 a head a CTA, 56 in parts).
+    // 40 us, 49 a head a CTA).
     const int64_t heads = static_cast<int64_t>(p.batch) * p.hk;
     const int64_t slots = static_cast<int64_t>(num_sms) * tree_ctas(D, KS);
     const int per_head = (p.nodes * p.group + 15) / 16;

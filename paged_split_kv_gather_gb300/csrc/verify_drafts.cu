@@ -12,18 +12,19 @@
 // others' shared memory; every warp's sum goes to all CTAs.  Each CTA then walks for itself on the
 // same bits, so all of them agree, even on inputs that change under them: a sum costs one
 // barrier of the cluster, and the draw none.  (Orders of the first CTA to the others, a second
-// barrier a sum: 17.2 us instead of 14.6 for 16 trees.)
+// barrier a sum: 2.6 us more for 16 trees.)
 //
 // A token is the first whose cumulative weight passes u W, among 10^5 borders, so sums of
 // fp32 rounding would often give another token than exact ones.  Each term p - s q is
 // taken as a pair of fp32 values (Dekker's and Knuth's error-free sums and products) and
 // added up in pairs, about 46 bits, 13 to 20 fp32 instructions a term.  fp64 units do two
-// products a clock and SM here: with the warps' sums and the search in a run in fp64 alone,
-// 64 rows of 131072 took 31 us instead of 21.
+// products a clock and SM here: with the warps' sums and the search in a run in fp64, 64 rows
+// of 131072 took 31 us instead of 21, and with the walk, which one warp does while the others
+// wait, in fp64 16 trees 14.6 instead of 11.5.
 //
 // Bytes: the rows p and q of the last node, once from HBM.  64 sequences, p and q of 131072 in
-// fp32: 20 us, 3.0 TB/s; all sequences read their tokens, sum and search at the same time,
-// so 8 us of latencies (what one sequence takes) come on top of the 9 us for the bytes.
+// fp32: 18.5 us, 3.3 TB/s; all sequences read their tokens, sum and search at the same time,
+// so most of the 7 us that one sequence takes come on top of the 9 us for the bytes.
 #include <algorithm>
 #include <cstdint>
 
@@ -44,6 +45,10 @@ constexpr int kVerifyThreads = kVerifyWarps * 32;
 constexpr int kMostCtas = 8;  // of a sequence
 // A sequence's CTAs each have kVerifyWarps runs of the vocabulary, a warp's each.
 constexpr int kMostRuns = kMostCtas * kVerifyWarps;
+
+// Vectors of each row in flight a lane.  (Eight, with two CTAs an SM instead of four: one sequence of 32768 tokens 7.1 us
+// instead of 6.7, 64 of 4096 7.7 instead of 7.1; 16 trees over 50021 tokens 11.5 instead of 11.7.)
+constexpr int kAhead = 4;
 
 enum Op : int { kSum = 0, kDraw = 1, kStop = 2 };
 
@@ -234,17 +239,17 @@ __device__ __forceinline__ Pair lane_sum(const T* p, const T* q, int begin, int 
     return sum;
 }
 
-template <typename T, bool VEC, int MODE, int AHEAD>
+template <typename T, bool VEC, int MODE>
 __device__ __forceinline__ Pair mode_sum(const T* p, const T* q, int begin, int end, Pair s, bool& bad) {
     uint32_t most = 0;
-    Pair sum = lane_sum<T, VEC, MODE, true, AHEAD>(p, q, begin, end, s, most, bad);
+    Pair sum = lane_sum<T, VEC, MODE, true, kAhead>(p, q, begin, end, s, most, bad);
     if (__any_sync(0xffffffffu, most > 0x40000000u))
         sum = lane_sum<T, VEC, MODE, false, 2>(p, q, begin, end, s, most, bad);
     return sum;
 }
 
-// One warp's sum over tokens [begin, end).  AHEAD: vectors of each row in flight a lane.
-template <typename T, bool VEC, int AHEAD>
+// One warp's sum over tokens [begin, end).
+template <typename T, bool VEC>
 __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int end, Pair s, const Node* nodes,
                                         uint64_t gone, bool& bad) {
     const int lane = threadIdx.x & 31;
@@ -270,11 +275,11 @@ __device__ __forceinline__ Pair run_sum(const T* p, const T* q, int begin, int e
             }
         }
     } else if (q == nullptr) {
-        sum = mode_sum<T, VEC, 0, AHEAD>(p, q, begin, end, sum, bad);
+        sum = mode_sum<T, VEC, 0>(p, q, begin, end, sum, bad);
     } else if (s.hi == 1.f && s.lo == 0.f) {  // the first to fall: nearly all sums
-        sum = mode_sum<T, VEC, 1, AHEAD>(p, q, begin, end, sum, bad);
+        sum = mode_sum<T, VEC, 1>(p, q, begin, end, sum, bad);
     } else {
-        sum = mode_sum<T, VEC, 2, AHEAD>(p, q, begin, end, s, bad);
+        sum = mode_sum<T, VEC, 2>(p, q, begin, end, s, bad);
     }
     return warp_sum(sum);
 }
@@ -464,9 +469,9 @@ __device__ __noinline__ Order next_order(Walk& walk, const Pair* sums, int runs,
     return o;
 }
 
-// CTAS: of a sequence.  AHEAD: vectors of each row in flight a lane.
-template <typename T, bool VEC, int CTAS, int AHEAD>
-__global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_drafts_kernel(const VerifyParams p) {
+// CTAS: of a sequence.
+template <typename T, bool VEC, int CTAS>
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_drafts_kernel(const VerifyParams p) {
     __shared__ Walk s_walk;
     __shared__ Pair s_warp[kVerifyWarps];
     __shared__ int s_first, s_last, s_any;
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kVerifyThreads, AHEAD == 4 ? 4 : 2) verify_dra
         bool bad = false;
         if (begin < p.vocab) {
             const int end = static_cast<int>(min(static_cast<int64_t>(p.vocab), begin + p.chunk));
-            sum = run_sum<T, VEC, AHEAD>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tree.node, o.gone, bad);
+            sum = run_sum<T, VEC>(prow, qrow, static_cast<int>(begin), end, o.s, s_walk.tree.node, o.gone, bad);
         }
         if (bad) flags |= FDEC_DEVERR_PROB;
         if constexpr (CTAS > 1) {
@@ -665,7 +670,7 @@ bool vectors(const VerifyParams& p) {
     return p.vocab % 4 == 0 && ok(p.target, p.t_seq, p.t_node) && ok(p.draft, p.d_seq, p.d_node);
 }
 
-template <typename T, bool VEC, int CTAS, int AHEAD>
+template <typename T, bool VEC, int CTAS>
 cudaError_t launch_verify_one(VerifyParams p, cudaStream_t s) {
     constexpr int kRuns = CTAS * kVerifyWarps;
     p.chunk = ((p.vocab + kRuns - 1) / kRuns + 127) / 128 * 128;
@@ -681,32 +686,31 @@ cudaError_t launch_verify_one(VerifyParams p, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CTAS > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, CTAS, AHEAD>, p);
+    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, VEC, CTAS>, p);
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_verify_v(const VerifyParams& p, int num_sms, cudaStream_t s) {
-    // A small vocabulary is one CTA's, which needs no cluster: 64 sequences 10.5 us against 12.2 at 4096 and at 8192
-    // tokens, 16 trees 12.0 against 13.4 and the same; at 16384 tokens 15.8 against 12.8.
-    if (p.vocab <= 8192) return launch_verify_one<T, VEC, 1, 8>(p, s);
-    // Twice the loads in flight, where the registers are there: two CTAs an SM instead of four.  (16 trees over 50021
-    // tokens 1.5 us less; clusters of 4 CTAs 1.5 us more, of 16 9 more.)
-    const bool deep = static_cast<int64_t>(p.batch) * kMostCtas <= num_sms * 2;
-    return deep ? launch_verify_one<T, VEC, kMostCtas, 8>(p, s) : launch_verify_one<T, VEC, kMostCtas, 4>(p, s);
+cudaError_t launch_verify_v(const VerifyParams& p, cudaStream_t s) {
+    // A small vocabulary is one CTA's, which needs no cluster: 64 sequences 7.1 us against 9.3 at 4096 and 7.7 against 9.4 at
+    // 8192 tokens, 16 trees 8.7 against 10.5 and 9.7 against 10.2; at 16384 tokens (eight vectors ahead) 9.6 against 9.5
+    // and 12.8 against 10.3.
+    // (Clusters of 4 CTAs 1.5 us more for 16 trees over 50021 tokens, of 16 9 more.)
+    if (p.vocab <= 8192) return launch_verify_one<T, VEC, 1>(p, s);
+    return launch_verify_one<T, VEC, kMostCtas>(p, s);
 }
 
 template <typename T>
-cudaError_t launch_verify(const VerifyParams& p, int num_sms, cudaStream_t s) {
-    return vectors<T>(p) ? launch_verify_v<T, true>(p, num_sms, s) : launch_verify_v<T, false>(p, num_sms, s);
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t s) {
+    return vectors<T>(p) ? launch_verify_v<T, true>(p, s) : launch_verify_v<T, false>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, int num_sms, cudaStream_t s) {
+cudaError_t launch_verify_drafts(const VerifyParams& p, int prob_dtype, cudaStream_t s) {
     switch (prob_dtype) {
-        case FDEC_PROB_F16: return launch_verify<__half>(p, num_sms, s);
-        case FDEC_PROB_BF16: return launch_verify<__nv_bfloat16>(p, num_sms, s);
-        case FDEC_PROB_F32: return launch_verify<float>(p, num_sms, s);
+        case FDEC_PROB_F16: return launch_verify<__half>(p, s);
+        case FDEC_PROB_BF16: return launch_verify<__nv_bfloat16>(p, s);
+        case FDEC_PROB_F32: return launch_verify<float>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }
