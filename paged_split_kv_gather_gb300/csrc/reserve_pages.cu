@@ -12,8 +12,8 @@
 // The rows that a fork or a shared last page needs are copied last.
 //
 // Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.  64
-// sequences and 65536 pages: 8.4 us, the latencies of three dependent launches (clear 1,
-// mark 3, assign 3.5); 256 sequences of 2049 entries and a million pages: 14.0, the marks'
+// sequences and 65536 pages: 8.4 to 8.8 us, the latencies of three dependent launches (clear 1,
+// mark 3, assign 3.5); 256 sequences of 2049 entries and a million pages: 14.0 to 14.8, the marks'
 // atomics among them; 64 forks in 16 layers: 14.1, of them 7.4 the copies (63 MB, 8.5 TB/s
 // of reads and writes that the L2 holds in part).
 #include <algorithm>
