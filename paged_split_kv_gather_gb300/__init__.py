@@ -802,14 +802,16 @@ class TreeDecode:
 
         return self.counts if node_counts is None else torch.minimum(node_counts, self.counts)
 
-    def reserve(self, page_table, prefix_lens, caches=(), sources=None, stream=None):
+    def reserve(self, page_table, prefix_lens, caches=(), stream=None):
         """Pages for the nodes behind prefix_lens; returns the lengths granted: prefix_lens[b] + num_nodes, or
-        prefix_lens[b] where there are no pages."""
+        prefix_lens[b] where there are no pages.  (Forks come before the round, with fdec_reserve_pages: a fork's prefix
+        is its source's, not the 0 that it has now.)  caches: all layers' keys and values, whose rows are copied where a
+        partly filled last page is shared."""
         import torch
 
         with self._on(stream):
             fdec_reserve_pages(page_table, prefix_lens, prefix_lens + self.num_nodes, self.granted, self.num_pages,
-                               self.page_size, self.workspace, sources, caches, self.errors, stream)
+                               self.page_size, self.workspace, None, caches, self.errors, stream)
             torch.sub(self.granted, prefix_lens, out=self.counts)
             torch.where(self.counts[:, None] > 0, self.nodes, self.nowhere, out=self.offsets)
         return self.granted

@@ -9,6 +9,7 @@ sums of 64 terms (128 u); the split into 16-bit terms leaves 2^-22.  So a row of
 (2 e + 8 u zmax + 200 u) times the largest value it averages, and lse by e + 3 u zmax + 140 u + u |lse|.  A 16-bit result
 is rounded once more: half a step of the value, or of the smallest normal number.  Tokens, paths, lengths and pages are
 equal; moved rows are equal bit for bit."""
+import inspect
 import math
 import os
 import random
@@ -1445,6 +1446,11 @@ def test_reserve_pages_refusals():
 def test_workspace_is_at_most_what_is_said():
     for batch, pages in ((1, 1), (64, 65536), (300, 8193), (65536, 1 << 26)):
         assert fd.fdec_reserve_pages_workspace(batch, pages) <= 4 * pages + 256 * batch + 256
+
+
+def test_a_round_makes_no_forks():
+    """A fork's prefix would be the 0 that it has, and its nodes' rows would go into the pages it shares."""
+    assert "sources" not in inspect.signature(fd.TreeDecode.reserve).parameters
 
 
 def test_tree_decode_refuses_what_it_cannot_hold():
