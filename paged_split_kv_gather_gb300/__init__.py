@@ -795,7 +795,11 @@ class TreeDecode:
 
         if stream is None:
             return contextlib.nullcontext()
-        return torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=self.errors.device))
+        if not isinstance(stream, torch.cuda.Stream):
+            handle, device = _stream_handle(stream), self.errors.device
+            # (0 and 1 name the default stream, which torch takes no handle for)
+            stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+        return torch.cuda.stream(stream)
 
     def _counts(self, node_counts):
         import torch

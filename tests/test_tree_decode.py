@@ -1228,8 +1228,9 @@ def test_a_sequence_without_pages_stands_still():
 
 
 @gpu
+@pytest.mark.parametrize("default", [False, True])
 @pytest.mark.parametrize("handle", [False, True])
-def test_a_round_on_a_stream_of_its_own(handle):
+def test_a_round_on_a_stream_of_its_own(handle, default):
     """The current stream is busy meanwhile: nothing of the round waits for it."""
     batch, nodes, page, hq, hk, d, vocab, pages = 2, 5, 16, 4, 2, 64, 32, 16
     torch.manual_seed(4)
@@ -1263,8 +1264,10 @@ def test_a_round_on_a_stream_of_its_own(handle):
 
     want, errors, _ = round_of(None)
     assert errors == 0
-    side = torch.cuda.Stream()
-    got, errors, busy = round_of(side.cuda_stream if handle else side)
+    side, main = torch.cuda.Stream(), torch.cuda.default_stream()
+    own, current = (main, side) if default else (side, main)
+    with torch.cuda.stream(current):
+        got, errors, busy = round_of(own.cuda_stream if handle else own)
     assert errors == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
     assert busy  # (the round ended first)
 
