@@ -33,6 +33,7 @@
 #include "../../include/fdec.h"
 #include "device_utils.cuh"
 #include "fdec_internal.h"
+#include "pair_sums.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -78,40 +79,6 @@ __device__ __forceinline__ float bounded(float x, bool& bad) {
     return y;
 }
 
-// A number as a pair of fp32 values.
-struct Pair {
-    float hi, lo;
-    // + (x + e), e small against x
-    __device__ __forceinline__ void add(float x, float e) {
-        const float sum = __fadd_rn(hi, x);
-        const float back = __fsub_rn(sum, hi);
-        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, back)), __fsub_rn(x, back));
-        hi = sum;
-        lo = __fadd_rn(lo, __fadd_rn(err, e));
-    }
-    __device__ __forceinline__ Pair plus(Pair x) const {  // lo small against hi again, whatever has cancelled
-        Pair d = *this;
-        d.add(x.hi, x.lo);
-        const float sum = __fadd_rn(d.hi, d.lo);
-        return {sum, __fadd_rn(__fsub_rn(d.hi, sum), d.lo)};
-    }
-    __device__ __forceinline__ Pair minus(Pair x) const { return plus({-x.hi, -x.lo}); }
-    __device__ __forceinline__ Pair times(float x) const {
-        const float t = __fmul_rn(hi, x);
-        return {t, __fmaf_rn(lo, x, __fmaf_rn(hi, x, -t))};
-    }
-    __device__ __forceinline__ Pair times(Pair x) const {
-        const float t = __fmul_rn(hi, x.hi);
-        return {t, __fmaf_rn(lo, x.hi, __fmaf_rn(hi, x.lo, __fmaf_rn(hi, x.hi, -t)))};
-    }
-    __device__ __forceinline__ bool positive() const { return __fadd_rn(hi, lo) > 0.f; }
-    __device__ __forceinline__ bool above(Pair x) const {
-        Pair d = *this;
-        d.add(-x.hi, -x.lo);
-        return d.positive();
-    }
-};
-
 struct Order {       // what comes next
     int op;
     int node;        // whose rows
@@ -121,42 +88,6 @@ struct Order {       // what comes next
     Pair target;     // kDraw: cumulative weight to pass, from the run's begin
     uint64_t gone;   // without draft rows: children whose tokens have lost their weight
 };
-
-__device__ __forceinline__ Pair warp_sum(Pair v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float hi = __shfl_xor_sync(0xffffffffu, v.hi, o), lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
-        v.add(hi, lo);
-    }
-    return v;
-}
-
-__device__ __forceinline__ Pair warp_scan(Pair v) {  // inclusive
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float hi = __shfl_up_sync(0xffffffffu, v.hi, o), lo = __shfl_up_sync(0xffffffffu, v.lo, o);
-        if (lane >= o) v.add(hi, lo);
-    }
-    return v;
-}
-
-// max(p - s q, 0) added to a sum.  UNIT: s is 1.
-template <bool UNIT>
-__device__ __forceinline__ void add_rest(Pair& sum, float p, float q, Pair s) {
-    if constexpr (UNIT) {
-        const float t = fminf(q, p);
-        const float d = __fsub_rn(p, t);
-        sum.add(d, __fsub_rn(__fsub_rn(p, d), t));  // (exact: p >= t >= 0)
-    } else {
-        const float t = __fmul_rn(s.hi, q);
-        const float te = __fmaf_rn(s.lo, q, __fmaf_rn(s.hi, q, -t));
-        float d = __fsub_rn(p, t);
-        float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), t), te);  // exact where p >= t, and else d < 0
-        if (!(__fadd_rn(d, e) > 0.f)) d = e = 0.f;
-        sum.add(d, e);
-    }
-}
 
 // A drafted token as the walk sees it.
 struct Node {
