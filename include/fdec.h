@@ -495,8 +495,8 @@ fdec_status fdec_run_selected(fdec_plan_t plan, const void* q, int64_t q_stride_
  *   out: contiguous, 16-byte aligned; out_type FDEC_OUT_F32 or FDEC_OUT_SAME; lse: float32 or
  *      NULL.  out may be o_prefix (FDEC_OUT_F32) and lse lse_prefix; the two overlap nothing
  *      else.  Rows of nodes past node_counts are not written.  A row that sees nothing gives
- *      out = 0 and lse = -inf.  Values of rows that a node does not see never reach it, NaN
- *      and infinities among them.
+ *      out = 0 and lse = -inf.  Values of rows that a node does not see never reach it, NaN,
+ *      infinities and values of any other size among them.
  */
 fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_stride_head, fdec_kv_desc k,
                                 fdec_kv_desc v, const int32_t* page_table, int64_t page_table_stride,

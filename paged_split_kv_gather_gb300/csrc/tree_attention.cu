@@ -23,7 +23,10 @@
 // sums; one value would leave 2^-12.  f16 and E4M3 values are f16 values; a bf16 cache's are
 // rewritten as they are staged, times the power of two that brings the largest of the tree's
 // below 2^15: exact but for values 2^-29 of that and less, which are off by 2^-40 of it.
-// (As bf16, a probability would take three values: 1.5 times the products.)
+// That holds while the tree's values are of one size (kSpread); where they are not, a large
+// row that a node does not see, or hardly, would cost it the bits of the others.  V then stays
+// bf16, which is exact, and a probability, normalised first, is three bf16 values (24 bits of
+// its own size, however small): 1.5 times the products, 43.3 us instead of 40.5 for 64 trees of 64.
 #include <algorithm>
 #include <cstdint>
 
@@ -70,6 +73,16 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
         }
     }
     return make_uint2(w[0], w[1]);
+}
+
+// x, y as sums of three bf16 values each.
+__device__ __forceinline__ void split_three(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack2<true>(x, y);
+    const float2 h = unpack2<true>(hi);
+    x -= h.x, y -= h.y;
+    mid = pack2<true>(x, y);
+    const float2 m = unpack2<true>(mid);
+    lo = pack2<true>(x - m.x, y - m.y);
 }
 
 // The bits of the larger magnitude in each half (infinities and NaN are the largest).
@@ -127,6 +140,11 @@ __device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
     *reinterpret_cast<uint2*>(at + 16) = make_uint2(v.y, v.w);
 }
 
+// A bf16 cache's values count as of one size while the largest is less than 2^(kSpread + 1) times the largest of any
+// eight neighbours (that are not all zeros).  Up to there the 2^-33 that a probability's split may be off cost a node
+// 2^-24, half a step of fp32, of what the rows that it does see hold in those columns.
+constexpr unsigned kSpread = 8;
+
 // CTAs on an SM: by the registers of S, P and O.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
 // nodes 8.4 us instead of 10.6; but at head_dim 256 16 trees of 13 nodes 6.5 us instead of 6.0.)
 constexpr int tree_ctas(int head_dim, int ks) { return ks == 1 && head_dim <= 128 ? 4 : 3; }
@@ -143,7 +161,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
     __shared__ int64_t s_k[kTreeWarps][kMaxNodes], s_v[kTreeWarps][kMaxNodes];  // byte offsets of the nodes' rows
     __shared__ uint64_t s_valid[kTreeWarps];                                    // nodes whose rows can be read
     __shared__ int s_count[kTreeWarps];
-    __shared__ unsigned s_max, s_odd[2];
+    __shared__ unsigned s_max, s_min, s_odd[2];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int N = p.nodes, g = p.group;
@@ -177,7 +195,10 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
     for (int run = 0; left > 0; ++run, next_run()) {
         const int count = min(left, tiles_max - first);
         __syncthreads();  // what was staged before has been read
-        if (tid == 0) s_max = s_odd[0] = s_odd[1] = 0;
+        if (tid == 0) {
+            s_max = s_odd[0] = s_odd[1] = 0;
+            s_min = 0xffffffffu;
+        }
 
         if (run % kTreeWarps == 0) {
             // Warp w takes the rows of the run w from here and, meanwhile, the ancestors of the run w + 1: of a single run
@@ -362,13 +383,17 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         uint8_t* sm_v = smem + staged * S::PITCH;
         // Rows of V with an infinite or NaN value are not multiplied as the others (0 times it would reach every row):
         // they are zeros in shared memory, and are added for the rows that see them.
-        uint32_t most = 0;  // the largest finite magnitude of V's, if not of those
+        // Of eight values each, if not of those rows: the largest magnitude, and the least of those that are
+        // not 0, less 1.
+        uint32_t most = 0, least = 0xffffffffu;
         const auto note = [&](int j, uint32_t two) {
             const uint32_t x = max(two & 0xffffu, two >> 16);
-            if (x >= kInf)
+            if (x >= kInf) {
                 atomicOr(&s_odd[j >> 5], 1u << (j & 31));
-            else
+            } else {
                 most = max(most, x);
+                least = min(least, x - 1);
+            }
         };
         constexpr int CH = KV8 ? D / 16 : D / 8;  // 16-byte chunks of a stored row
         constexpr int PER = (staged * CH + kTreeThreads - 1) / kTreeThreads;  // of a thread
@@ -420,13 +445,19 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         }
         if constexpr (kRewrite) {
             most = __reduce_max_sync(0xffffffffu, most);
-            if (lane == 0) atomicMax(&s_max, most);
+            least = __reduce_min_sync(0xffffffffu, least);
+            if (lane == 0) {
+                atomicMax(&s_max, most);
+                atomicMin(&s_min, least);
+            }
         }
         __syncthreads();
         const uint64_t odd = s_odd[0] | static_cast<uint64_t>(s_odd[1]) << 32;
         // (110: the factor that undoes it stays a normal number; only values below 2^-112 lose by that)
         const int up = kRewrite ? min(14 - (static_cast<int>(s_max >> 7) - 127), 110) : 0;
         const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        // V stays bf16; a row that is not finite is added with its fp32 probabilities
+        const bool wide = kRewrite && (odd != 0 || (s_max >> 7) > ((s_min + 1) >> 7) + kSpread);
         const float scale = fabsf(p.scale_log2);
         if (kRewrite || odd != 0 || p.scale_log2 < 0.f) {
             if constexpr (kRewrite) {
@@ -440,8 +471,9 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     };
                     if constexpr (kHeld) {
                         const uint4 v = held[i];
-                        put_values(sm_v + j * S::PITCH, c - j * CH, make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w)));
-                    } else {
+                        put_values(sm_v + j * S::PITCH, c - j * CH,
+                                   wide ? v : make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w)));
+                    } else if (!wide) {
                         uint4* at = reinterpret_cast<uint4*>(sm_v + j * S::PITCH + (c - j * CH) * 16);
                         const uint4 v = *at;
                         *at = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
@@ -469,244 +501,285 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
         const uint32_t q_addr = q_slot + q_row * QD * 2;
         const uint32_t v_addr = smem_addr(sm_v) + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::PITCH + (lane >> 4) * 16;
         const bool f32 = p.out_type == kOutF32;
-        for (int it = 0; it < my_tiles; ++it) {
-            constexpr int NT = 2 * KS;
-            float s[NT][4];
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncwarp();  // the tile's queries are there (the prefix's first block may not be)
+        // The warp's tiles.  RAW: probabilities are kept in fp32, for V in bf16 and for rows that are not finite
+        // (a body of its own: with branches in one body, 64 trees of 64 nodes took 1 % longer, at head_dim 192
+        // 96 of them 8 %).
+        const auto walk = [&](auto raw) {
+            constexpr bool RAW = decltype(raw)::value;
+            for (int it = 0; it < my_tiles; ++it) {
+                constexpr int NT = 2 * KS;
+                float s[NT][4];
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                __syncwarp();  // the tile's queries are there (the prefix's first block may not be)
 #pragma unroll
-            for (int c = 0; c < QD / 32; ++c) {  // S = Q K^T, 32 dims at a time
-                uint32_t a0[4], a1[4];
-                ldmatrix_x4(q_addr + ((4 * c + (lane >> 4)) ^ (lane & 7)) * 16, a0[0], a0[1], a0[2], a0[3]);
-                ldmatrix_x4(q_addr + ((4 * c + 2 + (lane >> 4)) ^ (lane & 7)) * 16, a1[0], a1[1], a1[2], a1[3]);
-                if (c == 0)
-                    add_scores<BF16, KS, true>(s, a0, a1, k_addr + d0 * 64, S::PITCH);
-                else if (!kAddParts || d0 + c < d1)
-                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + (d0 + c) * 64, S::PITCH);
-            }
-            if constexpr (kAddParts) {  // the other dims from where they are
-                const uint16_t* from[2] = {(row[0] >= 0 ? query(row[0], node[0]) : p.q) + 2 * t,
-                                           (row[1] >= 0 ? query(row[1], node[1]) : p.q) + 2 * t};
-                const auto word = [&](int h, int d) {
-                    return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
-                };
+                for (int c = 0; c < QD / 32; ++c) {  // S = Q K^T, 32 dims at a time
+                    uint32_t a0[4], a1[4];
+                    ldmatrix_x4(q_addr + ((4 * c + (lane >> 4)) ^ (lane & 7)) * 16, a0[0], a0[1], a0[2], a0[3]);
+                    ldmatrix_x4(q_addr + ((4 * c + 2 + (lane >> 4)) ^ (lane & 7)) * 16, a1[0], a1[1], a1[2], a1[3]);
+                    if (c == 0)
+                        add_scores<BF16, KS, true>(s, a0, a1, k_addr + d0 * 64, S::PITCH);
+                    else if (!kAddParts || d0 + c < d1)
+                        add_scores<BF16, KS, false>(s, a0, a1, k_addr + (d0 + c) * 64, S::PITCH);
+                }
+                if constexpr (kAddParts) {  // the other dims from where they are
+                    const uint16_t* from[2] = {(row[0] >= 0 ? query(row[0], node[0]) : p.q) + 2 * t,
+                                               (row[1] >= 0 ? query(row[1], node[1]) : p.q) + 2 * t};
+                    const auto word = [&](int h, int d) {
+                        return row[h] >= 0 ? *reinterpret_cast<const uint32_t*>(from[h] + d) : 0u;
+                    };
 #pragma unroll 6
-                for (int d = d0 * 32 + QD; d < d1 * 32; d += 32) {
-                    const uint32_t a0[4] = {word(0, d), word(1, d), word(0, d + 8), word(1, d + 8)};
-                    const uint32_t a1[4] = {word(0, d + 16), word(1, d + 16), word(0, d + 24), word(1, d + 24)};
-                    add_scores<BF16, KS, false>(s, a0, a1, k_addr + d * 2, S::PITCH);
-                }
-                if (split > 1) {  // (where the queries lay)
-                    const uint32_t at = lane * 16;
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(q_slot + at + j * 512), "f"(s[j][0]),
-                                     "f"(s[j][1]), "f"(s[j][2]), "f"(s[j][3])
-                                     : "memory");
-                    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / split), "r"(32 * split) : "memory");
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-                    for (int k = 0; k < split; ++k) {  // (every warp in the same order)
-                        const uint32_t from = q_slot + (k - part) * (S::Q_BYTES + kSlotBytes) + at;
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const float4 x = lds128f<0>(from + j * 512);
-                            s[j][0] += x.x, s[j][1] += x.y, s[j][2] += x.z, s[j][3] += x.w;
-                        }
+                    for (int d = d0 * 32 + QD; d < d1 * 32; d += 32) {
+                        const uint32_t a0[4] = {word(0, d), word(1, d), word(0, d + 8), word(1, d + 8)};
+                        const uint32_t a1[4] = {word(0, d + 16), word(1, d + 16), word(0, d + 24), word(1, d + 24)};
+                        add_scores<BF16, KS, false>(s, a0, a1, k_addr + d * 2, S::PITCH);
                     }
-                }
-            }
-
-            float w[2], vs[2], lse_out[2];
-            const int out_row[2] = {row[0], row[1]}, out_node[2] = {node[0], node[1]};
+                    if (split > 1) {  // (where the queries lay)
+                        const uint32_t at = lane * 16;
+                        __syncwarp();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint64_t vis = row[h] < 0 ? 0 : s_anc[known][node[h]] & valid;
-                const float before = lse_in[h] * 1.4426950408889634f;
-                // the lane's columns of a tile of 8 keys are 2t and 2t + 1
-                const uint64_t mine = vis >> (2 * t);
-                const uint32_t bits[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
-                float top = -INFINITY;
+                        for (int j = 0; j < NT; ++j)
+                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(q_slot + at + j * 512),
+                                         "f"(s[j][0]), "f"(s[j][1]), "f"(s[j][2]), "f"(s[j][3])
+                                         : "memory");
+                        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / split), "r"(32 * split) : "memory");
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
+                        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+                        for (int k = 0; k < split; ++k) {  // (every warp in the same order)
+                            const uint32_t from = q_slot + (k - part) * (S::Q_BYTES + kSlotBytes) + at;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& z = s[j][2 * h + e];
-                        if (!(bits[j >> 2] & (1u << ((j & 3) * 8 + e)))) z = -INFINITY;
-                        top = fmaxf(top, z);
-                    }
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                top = fmaxf(top * scale, before);
-                const float m = top == -INFINITY ? 0.f : top;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& z = s[j][2 * h + e];
-                        z = exp2_approx(fmaf(z, scale, kPShift - m));
-                        sum += z;
-                    }
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                w[h] = exp2_approx(before - m);
-                sum = sum * (1.f / (1 << kPShift)) + w[h];
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                lse_out[h] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
-                w[h] *= inv;
-                vs[h] = v_factor * inv;
-            }
-            if (p.lse != nullptr && t == 0 && part == 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (out_row[h] >= 0) p.lse[out_row[h]] = lse_out[h];
-            }
-            // an empty state counts for nothing, whatever its values
-            const bool empty[2] = {row[0] >= 0 && lse_in[0] == -INFINITY, row[1] >= 0 && lse_in[1] == -INFINITY};
-            const bool states = !__any_sync(0xffffffffu, empty[0] || empty[1]);
-            const int rows_now = rows;
-            __syncwarp();  // the queries have been read
-            if (it + 1 < my_tiles) {
-                next_tile(it + 1);
-            } else {
-                rows = -1;
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-
-            uint32_t pf[KS][2][4];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    split_two(s[2 * ks + (e >> 1)][2 * (e & 1)], s[2 * ks + (e >> 1)][2 * (e & 1) + 1], pf[ks][0][e],
-                              pf[ks][1][e]);
-            }
-
-            // O in blocks of 64 columns
-            const auto finish = [&](int cb, const float (&acc)[8][4]) {
-                if (cb == cb0)
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");  // (the next queries may be on their way)
-                else
-                    asm volatile("cp.async.wait_group 0;" ::: "memory");
-                __syncwarp();  // the warp's copies of the block are there
-                // the lane's columns 16 j + 4 t .. + 3 of the block: its products' tiles 2 j and 2 j + 1
-                const uint32_t from = slot + gq * 256 + t * 16;
-                const auto place = [&](int h, int j) { return from + h * 2048 + (j ^ (gq & 1)) * 64; };
-                if (!states) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (empty[h]) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(place(h, j)), "f"(0.f)
-                                             : "memory");
-                        }
-                }
-                // Rows of V that are not finite: their share is added to the state's, which is weighed here.
-                if (odd != 0) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float4 o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 x = lds128f<0>(place(h, j));
-                            o[j] = make_float4(w[h] * x.x, w[h] * x.y, w[h] * x.z, w[h] * x.w);
-                        }
-                        for (uint64_t rest = odd; rest != 0; rest &= rest - 1) {
-                            const int key = __ffsll(static_cast<long long>(rest)) - 1;
-                            uint32_t hi = 0, lo = 0;
-#pragma unroll
-                            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    // (selected in registers: not an index into memory)
-                                asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %4, %5;\n\t"
-                                             "selp.b32 %0, %2, %0, p;\n\tselp.b32 %1, %3, %1, p;\n\t}"
-                                             : "+r"(hi), "+r"(lo)
-                                             : "r"(pf[ks][0][2 * e + h]), "r"(pf[ks][1][2 * e + h]), "r"(key >> 3),
-                                               "r"(2 * ks + e));
-                        const float2 a = unpack2<false>(hi), c = unpack2<false>(lo);
-                            const float pr = __shfl_sync(0xffffffffu, key & 1 ? a.y + c.y : a.x + c.x,
-                                                         (lane & ~3) | ((key & 7) >> 1)) * factor * vs[h];
-                            const uint64_t seen = out_row[h] < 0 ? 0 : s_anc[known][out_node[h]] & valid;
-                            if (!(seen >> key & 1)) continue;
-                            const uint8_t* v_row = p.v_base + s_v[known][key] + (cb * 64 + 4 * t) * (KV8 ? 1 : 2);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint2 v;
-                                if constexpr (KV8)
-                                    v = widen4<false>(*reinterpret_cast<const uint32_t*>(v_row + j * 16));
-                                else
-                                    v = *reinterpret_cast<const uint2*>(v_row + j * 32);
-                                const float2 x = unpack2<BF16 && !KV8>(v.x), y = unpack2<BF16 && !KV8>(v.y);
-                                o[j].x += pr * x.x;
-                                o[j].y += pr * x.y;
-                                o[j].z += pr * y.x;
-                                o[j].w += pr * y.y;
+                            for (int j = 0; j < NT; ++j) {
+                                const float4 x = lds128f<0>(from + j * 512);
+                                s[j][0] += x.x, s[j][1] += x.y, s[j][2] += x.z, s[j][3] += x.w;
                             }
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(place(h, j)), "f"(o[j].x),
-                                         "f"(o[j].y), "f"(o[j].z), "f"(o[j].w)
-                                         : "memory");
                     }
                 }
-                const float weight[2] = {odd != 0 ? 1.f : w[0], odd != 0 ? 1.f : w[1]};
+
+                float w[2], vs[2], norm[2], lse_out[2];
+                const int out_row[2] = {row[0], row[1]}, out_node[2] = {node[0], node[1]};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (out_row[h] < 0) continue;
-                    const int64_t at = static_cast<int64_t>(out_row[h]) * D + cb * 64 + 4 * t;
-                    const auto joined = [&](int j) {
-                        const float4 o = lds128f<0>(place(h, j));
-                        return make_float4(vs[h] * acc[2 * j][2 * h] + weight[h] * o.x,
-                                           vs[h] * acc[2 * j][2 * h + 1] + weight[h] * o.y,
-                                           vs[h] * acc[2 * j + 1][2 * h] + weight[h] * o.z,
-                                           vs[h] * acc[2 * j + 1][2 * h + 1] + weight[h] * o.w);
-                    };
-                    if (f32) {
+                    const uint64_t vis = row[h] < 0 ? 0 : s_anc[known][node[h]] & valid;
+                    const float before = lse_in[h] * 1.4426950408889634f;
+                    // the lane's columns of a tile of 8 keys are 2t and 2t + 1
+                    const uint64_t mine = vis >> (2 * t);
+                    const uint32_t bits[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
+                    float top = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(p.out + at + j * 16) = joined(j);
-                    } else {
-                        uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at;
+                    for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 x = joined(j);
-                            *reinterpret_cast<uint2*>(out + j * 16) =
-                                make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+                        for (int e = 0; e < 2; ++e) {
+                            float& z = s[j][2 * h + e];
+                            if (!(bits[j >> 2] & (1u << ((j & 3) * 8 + e)))) z = -INFINITY;
+                            top = fmaxf(top, z);
                         }
                     }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = fmaxf(top * scale, before);
+                    const float m = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& z = s[j][2 * h + e];
+                            z = exp2_approx(fmaf(z, scale, kPShift - m));
+                            sum += z;
+                        }
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    w[h] = exp2_approx(before - m);
+                    sum = sum * (1.f / (1 << kPShift)) + w[h];
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    lse_out[h] = sum == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(sum);
+                    w[h] *= inv;
+                    vs[h] = RAW && kRewrite ? p.v_scale : v_factor * inv;
+                    norm[h] = inv * (1.f / (1 << kPShift));
                 }
-                __syncwarp();  // and have been read
-                request_prefix(cb + 1 < cb1 ? cb + 1 : cb0, cb + 1 < cb1 ? rows_now : rows);
-            };
-#pragma unroll 1
-            for (int cb = cb0; cb < cb1; ++cb) {
-                float acc[8][4];
+                if (p.lse != nullptr && t == 0 && part == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (out_row[h] >= 0) p.lse[out_row[h]] = lse_out[h];
+                }
+                // an empty state counts for nothing, whatever its values
+                const bool empty[2] = {row[0] >= 0 && lse_in[0] == -INFINITY, row[1] >= 0 && lse_in[1] == -INFINITY};
+                const bool states = !__any_sync(0xffffffffu, empty[0] || empty[1]);
+                const int rows_now = rows;
+                __syncwarp();  // the queries have been read
+                if (it + 1 < my_tiles) {
+                    next_tile(it + 1);
+                } else {
+                    rows = -1;
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                }
+
+                // Two probabilities as their f16 high and low parts, or (raw) as they are in fp32.
+                uint32_t pf[KS][2][4];
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-                    for (int dp = 0; dp < 4; ++dp) {
-                        uint32_t r0, r1, r2, r3;
-                        ldmatrix_x4_trans(v_addr + ks * 16 * S::PITCH + cb * 128 + dp * 32, r0, r1, r2, r3);
-                        if (ks == 0) {
-                            mma_16816_new<false>(acc[2 * dp], pf[ks][1], r0, r1);
-                            mma_16816_new<false>(acc[2 * dp + 1], pf[ks][1], r2, r3);
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[2 * ks + (e >> 1)][2 * (e & 1)], y = s[2 * ks + (e >> 1)][2 * (e & 1) + 1];
+                        if constexpr (RAW) {
+                            if constexpr (kRewrite) x *= norm[e & 1], y *= norm[e & 1];
+                            pf[ks][0][e] = __float_as_uint(x);
+                            pf[ks][1][e] = __float_as_uint(y);
                         } else {
-                            mma_16816<false>(acc[2 * dp], pf[ks][1], r0, r1);
-                            mma_16816<false>(acc[2 * dp + 1], pf[ks][1], r2, r3);
+                            split_two(x, y, pf[ks][0][e], pf[ks][1][e]);
                         }
-                        mma_16816<false>(acc[2 * dp], pf[ks][0], r0, r1);
-                        mma_16816<false>(acc[2 * dp + 1], pf[ks][0], r2, r3);
                     }
                 }
-                finish(cb, acc);
+
+                // O in blocks of 64 columns
+                const auto finish = [&](int cb, const float (&acc)[8][4]) {
+                    if (cb == cb0)
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");  // (the next queries may be on their way)
+                    else
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();  // the warp's copies of the block are there
+                    // the lane's columns 16 j + 4 t .. + 3 of the block: its products' tiles 2 j and 2 j + 1
+                    const uint32_t from = slot + gq * 256 + t * 16;
+                    const auto place = [&](int h, int j) { return from + h * 2048 + (j ^ (gq & 1)) * 64; };
+                    if (!states) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (empty[h]) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(place(h, j)), "f"(0.f)
+                                                 : "memory");
+                            }
+                    }
+                    // Rows of V that are not finite: their share is added to the state's, which is weighed here.
+                    if (RAW && odd != 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float4 o[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 x = lds128f<0>(place(h, j));
+                                o[j] = make_float4(w[h] * x.x, w[h] * x.y, w[h] * x.z, w[h] * x.w);
+                            }
+                            for (uint64_t rest = odd; rest != 0; rest &= rest - 1) {
+                                const int key = __ffsll(static_cast<long long>(rest)) - 1;
+                                uint32_t even = 0, uneven = 0;
+#pragma unroll
+                                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        // (selected in registers: not an index into memory)
+                                        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %4, %5;\n\t"
+                                                     "selp.b32 %0, %2, %0, p;\n\tselp.b32 %1, %3, %1, p;\n\t}"
+                                                     : "+r"(even), "+r"(uneven)
+                                                     : "r"(pf[ks][0][2 * e + h]), "r"(pf[ks][1][2 * e + h]),
+                                                       "r"(key >> 3), "r"(2 * ks + e));
+                                const float pr = __shfl_sync(0xffffffffu, __uint_as_float(key & 1 ? uneven : even),
+                                                             (lane & ~3) | ((key & 7) >> 1)) * vs[h];
+                                const uint64_t seen = out_row[h] < 0 ? 0 : s_anc[known][out_node[h]] & valid;
+                                if (!(seen >> key & 1)) continue;
+                                const uint8_t* v_row = p.v_base + s_v[known][key] + (cb * 64 + 4 * t) * (KV8 ? 1 : 2);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    uint2 v;
+                                    if constexpr (KV8)
+                                        v = widen4<false>(*reinterpret_cast<const uint32_t*>(v_row + j * 16));
+                                    else
+                                        v = *reinterpret_cast<const uint2*>(v_row + j * 32);
+                                    const float2 x = unpack2<BF16 && !KV8>(v.x), y = unpack2<BF16 && !KV8>(v.y);
+                                    o[j].x += pr * x.x;
+                                    o[j].y += pr * x.y;
+                                    o[j].z += pr * y.x;
+                                    o[j].w += pr * y.y;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(place(h, j)), "f"(o[j].x),
+                                             "f"(o[j].y), "f"(o[j].z), "f"(o[j].w)
+                                             : "memory");
+                        }
+                    }
+                    const float weight[2] = {RAW && odd != 0 ? 1.f : w[0], RAW && odd != 0 ? 1.f : w[1]};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (out_row[h] < 0) continue;
+                        const int64_t at = static_cast<int64_t>(out_row[h]) * D + cb * 64 + 4 * t;
+                        const auto joined = [&](int j) {
+                            const float4 o = lds128f<0>(place(h, j));
+                            return make_float4(vs[h] * acc[2 * j][2 * h] + weight[h] * o.x,
+                                               vs[h] * acc[2 * j][2 * h + 1] + weight[h] * o.y,
+                                               vs[h] * acc[2 * j + 1][2 * h] + weight[h] * o.z,
+                                               vs[h] * acc[2 * j + 1][2 * h + 1] + weight[h] * o.w);
+                        };
+                        if (f32) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(p.out + at + j * 16) = joined(j);
+                        } else {
+                            uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 x = joined(j);
+                                *reinterpret_cast<uint2*>(out + j * 16) =
+                                    make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+                            }
+                        }
+                    }
+                    __syncwarp();  // and have been read
+                    request_prefix(cb + 1 < cb1 ? cb + 1 : cb0, cb + 1 < cb1 ? rows_now : rows);
+                };
+#pragma unroll 1
+                for (int cb = cb0; cb < cb1; ++cb) {
+                    float acc[8][4];
+                    // acc (+)= P V of 16 keys: P in N parts, the smallest first.
+                    const auto products = [&](auto bf16, int ks, const auto& part) {
+                        constexpr bool kBF16 = decltype(bf16)::value;
+                        constexpr int N = sizeof(part) / sizeof(part[0]);
+#pragma unroll
+                        for (int dp = 0; dp < 4; ++dp) {
+                            uint32_t r0, r1, r2, r3;
+                            ldmatrix_x4_trans(v_addr + ks * 16 * S::PITCH + cb * 128 + dp * 32, r0, r1, r2, r3);
+                            if (ks == 0) {
+                                mma_16816_new<kBF16>(acc[2 * dp], part[N - 1], r0, r1);
+                                mma_16816_new<kBF16>(acc[2 * dp + 1], part[N - 1], r2, r3);
+                            } else {
+                                mma_16816<kBF16>(acc[2 * dp], part[N - 1], r0, r1);
+                                mma_16816<kBF16>(acc[2 * dp + 1], part[N - 1], r2, r3);
+                            }
+#pragma unroll
+                            for (int i = N - 2; i >= 0; --i) {
+                                mma_16816<kBF16>(acc[2 * dp], part[i], r0, r1);
+                                mma_16816<kBF16>(acc[2 * dp + 1], part[i], r2, r3);
+                            }
+                        }
+                    };
+                    if constexpr (RAW) {
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            uint32_t part[kRewrite ? 3 : 2][4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float x = __uint_as_float(pf[ks][0][e]), y = __uint_as_float(pf[ks][1][e]);
+                                if constexpr (kRewrite)
+                                    split_three(x, y, part[0][e], part[1][e], part[2][e]);
+                                else
+                                    split_two(x, y, part[0][e], part[1][e]);
+                            }
+                            products(std::bool_constant<kRewrite>{}, ks, part);
+                        }
+                    } else {
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) products(std::false_type{}, ks, pf[ks]);
+                    }
+                    finish(cb, acc);
+                }
             }
-        }
+        };
+        if (kRewrite ? wide : odd != 0)
+            walk(std::true_type{});
+        else
+            walk(std::false_type{});
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 }

@@ -1,5 +1,6 @@
 """Drafting operators where they can go wrong: inputs that no test of the operators' ranges reaches."""
 import ctypes
+import math
 import os
 import random
 import subprocess
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from test_tree_decode import i32, run_verify
+from test_tree_decode import DT, U, Tree, i32, path_of, run_verify
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 gpu = pytest.mark.gpu
@@ -117,3 +118,107 @@ def test_decisions_too_near_to_tell_are_one_path_and_its_token(vocab):
     for _ in range(20):
         again = run_verify(target, None, tokens, parents, u)
         assert all(torch.equal(a, b) for a, b in zip(got[:3], again[:3]))
+
+
+# ------------------------------------------------------------------------------------- tree attention: large and small
+
+def check_every_value(c, out, lse):
+    """As Tree.check, but each value within the tolerance of what it is the sum of itself: an error of a probability,
+    relative to it, moves a column by that part of the column's own terms.  (Probabilities below 2^-125 may be 0.)"""
+    group = c.hq // c.hk
+    half, tiny = (0.0, 0.0) if out.dtype == torch.float32 else (torch.finfo(out.dtype).eps / 2, torch.finfo(out.dtype).tiny)
+    for b in range(c.batch):
+        for i in range(c.counts[b]):
+            at = [c.prefix[b] + j for j in path_of(c.parents[b], i)]
+            where = [(int(c.table[b, p // c.page]), p % c.page) for p in at]
+            for kvh in range(c.hk):
+                k, v = (torch.stack([x[pg, kvh, sl].double() for pg, sl in where]).cpu() for x in (c.k, c.v))
+                rows = slice(kvh * group, (kvh + 1) * group)
+                q = c.q[b, i, rows].double().cpu()
+                z = q @ k.T * c.scale
+                e = (2 * c.d + 4) * U * (q.abs() @ k.abs().T * abs(c.scale)).amax(-1)
+                if c.lse_prefix is None:
+                    before, o = torch.full((group,), -math.inf).double(), torch.zeros(group, c.d).double()
+                else:
+                    before, o = c.lse_prefix[b, i, rows].double().cpu(), c.o_prefix[b, i, rows].double().cpu()
+                    o = torch.where(before[:, None] == -math.inf, 0.0, o)
+                total = torch.logaddexp(torch.logsumexp(z, -1), before)
+                p, w = torch.exp(z - total[:, None]), torch.exp(before - total)[:, None]
+                want, size = p @ v + w * o, p @ v.abs() + w * o.abs()
+                zmax = torch.maximum(z.abs().amax(-1), torch.where(before == -math.inf, 0.0, before).abs())
+                tol = (2 * e + 8 * U * zmax + 200 * U)[:, None] * size + 2.0 ** -125 * v.abs().sum(0)
+                limit = tol + half * torch.maximum(want.abs() + tol, torch.tensor(tiny).double())
+                off = (out[b, i, rows].double().cpu() - want).abs()
+                assert (off <= limit).all(), (b, i, kvh, (off / limit).max().item())
+                near = e + 3 * U * zmax + 140 * U + U * total.abs()
+                assert ((lse[b, i, rows].double().cpu() - total).abs() <= near).all()
+
+
+def outlier(c, b, node, power, logit=None, columns=slice(None)):
+    """Node's value row times 2^power; its key such that every query's logit is about `logit` (queries' first dim is 8)."""
+    p = c.prefix[b] + node
+    at = int(c.table[b, p // c.page]), slice(None), p % c.page
+    row = c.v[at].double()
+    row[:, columns] *= 2.0 ** power
+    c.v[at] = row.to(c.v.dtype)
+    if logit is not None:
+        key = torch.zeros_like(c.k[at])
+        key[:, 0] = logit / (c.scale * 8.0)
+        c.k[at] = key
+
+
+@gpu
+@pytest.mark.parametrize("d,hq,hk,nodes", [(128, 8, 2, 13), (64, 4, 2, 40), (192, 4, 1, 20), (256, 4, 2, 64), (512, 2, 1, 33)])
+@pytest.mark.parametrize("power", [9, 12, 30, 40, 100])
+def test_large_rows_cost_the_others_nothing(d, hq, hk, nodes, power):
+    """A value row far above the others: nodes that do not see it have their own rows' accuracy, those that do see it,
+    with a weight near 0 among them, that of what it adds."""
+    for state, out_type, logit in ((True, torch.float32, None), (False, torch.float32, -30.0), (True, torch.bfloat16, -70.0)):
+        c = Tree(d, hq, hk, nodes, 16, 2, "bf16", seed=power + nodes, counts=[nodes, nodes - 1], state=state)
+        c.q[..., 0] = 8.0
+        outlier(c, 0, 2, power, logit)
+        outlier(c, 1, nodes - 2, power, logit, columns=slice(5, 6))  # a leaf's, one column
+        if nodes > 30:
+            outlier(c, 1, 1, -power)
+            outlier(c, 1, 0, 20, -25.0)
+        if power >= 12:
+            check_every_value(c, *c.run(out=torch.full(c.q.shape, 3.0, dtype=out_type, device="cuda")))
+        else:  # (of one size: within the rows' tolerance)
+            c.check(*c.run(out=torch.full(c.q.shape, 3.0, dtype=out_type, device="cuda")))
+
+
+@gpu
+def test_a_large_row_that_a_node_does_not_see_with_an_empty_prefix():
+    """One sibling's value is 1e30, the other's 1: the result is 1, whatever the sibling's."""
+    for nodes in (3, 20, 64):
+        c = Tree(128, 4, 1, nodes, 16, 1, "bf16", seed=1, kind="star", counts=[nodes], prefix=[0])
+        c.v.fill_(1.0)
+        plain, lse = c.run()
+        outlier(c, 0, 1, 100)
+        out, lse2 = c.run()
+        seen = torch.zeros(nodes, dtype=torch.bool)
+        seen[1] = True
+        assert (out[0, ~seen] - 1).abs().max() <= 200 * U and (out[0, 1] > 1e26).all()
+        assert (out[0, ~seen] - plain[0, ~seen]).abs().max() <= 200 * U and torch.equal(lse, lse2)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,kv", [(128, "bf16", ""), (128, "f16", ""), (256, "bf16", "fp8"), (512, "bf16", "")])
+def test_infinite_values_of_hardly_any_weight_stay_infinite(d, dtype, kv):
+    c = Tree(d, 6, 2, 22, 16, 2, dtype, kv, seed=9, counts=[22, 22])
+    if kv:  # (E4M3 has no infinity)
+        value = math.nan
+    else:
+        value = math.inf
+    c.q[..., 0] = 8.0
+    outlier(c, 1, 3, 0, -30.0)
+    p = c.prefix[1] + 3
+    c.v[int(c.table[1, p // 16]), 0, p % 16] = torch.tensor(value).to(c.v.dtype)
+    out, lse = c.run()
+    for i in range(22):
+        rows = out[1, i, :3]
+        if 3 in path_of(c.parents[1], i):
+            assert (torch.isnan(rows) if kv else rows == math.inf).all(), i
+        else:
+            assert torch.isfinite(rows).all()
+    assert torch.isfinite(out[1, :, 3:]).all() and torch.isfinite(lse[1]).all()
