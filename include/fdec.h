@@ -581,8 +581,10 @@ enum { FDEC_MAX_CACHES = 128 };
  *   path_lens: int32 device [batch]; outside [0, num_nodes]: FDEC_DEVERR_SEQ_LEN, clamped.
  *      A path that is not increasing, or goes past num_nodes - 1, sets FDEC_DEVERR_TREE and
  *      counts up to there.
- *   prefix_lens, page_table, device_errors: as for fdec_tree_attention; a row in a bad page
- *      (for any of the caches) or past the page table is not moved.
+ *   prefix_lens: int32 device [batch]; a negative one sets FDEC_DEVERR_SEQ_LEN, nothing of
+ *      that sequence moves, and seq_lens[b] = prefix_lens[b].
+ *   page_table, device_errors: as for fdec_tree_attention; a row in a bad page (for any of
+ *      the caches) or past the page table is not moved.
  *   seq_lens: int32 device [batch]; must not overlap prefix_lens.
  * The pages that hold the moved rows must belong to one sequence alone (fdec_reserve_pages
  * sees to that).

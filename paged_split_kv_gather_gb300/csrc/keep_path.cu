@@ -32,16 +32,19 @@ __global__ void __launch_bounds__(kColumnThreads)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid < 32) {
         unsigned flags = 0;
-        int64_t prefix = p.prefix_lens[b];
+        const int64_t prefix = p.prefix_lens[b];
         int n = p.path_lens[b];
         int node[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             node[h] = lane + 32 * h < p.nodes ? p.path[b * p.path_stride + lane + 32 * h] : p.nodes;
-        if (prefix < 0 || n < 0 || n > p.nodes) {
+        if (n < 0 || n > p.nodes) {
             flags |= FDEC_DEVERR_SEQ_LEN;
-            prefix = max(prefix, static_cast<int64_t>(0));
             n = min(max(n, 0), p.nodes);
+        }
+        if (prefix < 0) {  // (the length stays bad, for whoever reads it next)
+            flags |= FDEC_DEVERR_SEQ_LEN;
+            n = 0;
         }
         // up to the first entry that is out of order; the first that moves
         const int below0 = __shfl_up_sync(0xffffffffu, node[0], 1), last0 = __shfl_sync(0xffffffffu, node[0], 31);

@@ -222,3 +222,57 @@ def test_infinite_values_of_hardly_any_weight_stay_infinite(d, dtype, kv):
         else:
             assert torch.isfinite(rows).all()
     assert torch.isfinite(out[1, :, 3:]).all() and torch.isfinite(lse[1]).all()
+
+
+# ---------------------------------------------------------------------------------------- lengths that are none
+
+@gpu
+def test_keep_path_leaves_a_bad_length_as_it_is():
+    pool = torch.randn(8, 2, 16, 64).half().cuda()
+    before, out = pool.clone(), torch.full((3,), 9, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    path = i32([[1, 3, -1, -1]] * 3)
+    fd.fdec_keep_path([pool], i32(np.arange(6).reshape(3, 2)), i32([-7, 4, -(2 ** 31)]), path, i32([2, 2, 2]), out, 16,
+                      device_errors=err)
+    assert out.tolist() == [-7, 6, -(2 ** 31)] and int(err.item()) == fd.DEVERR_SEQ_LEN
+    assert torch.equal(pool[[0, 1, 4, 5, 6, 7]], before[[0, 1, 4, 5, 6, 7]])
+    assert torch.equal(pool[2, :, 4], before[2, :, 5]) and torch.equal(pool[2, :, 5], before[2, :, 7])
+
+
+@gpu
+def test_a_round_of_sequences_with_bad_lengths():
+    """Negative, past the page table, and so near its end that the nodes have no room: no nodes, nothing written, the
+    length stays; the other sequence's round is as ever."""
+    batch, nodes, page, hq, hk, d, vocab, pages = 5, 6, 16, 4, 2, 64, 32, 40
+    torch.manual_seed(5)
+    k = torch.randn(pages, hk, page, d, device="cuda").half()
+    v = torch.randn(pages, hk, page, d, device="cuda").half()
+    tree = fd.TreeDecode([60] * batch, nodes, page, hq, hk, d, pages, "f16")
+    lengths = [-1, 20, 65, 61, 2 ** 31 - 2]
+    lens = i32(lengths)
+    table = i32(np.arange(batch * 4).reshape(batch, 4))
+    qkv = torch.randn(batch * nodes, hq + 2 * hk, d, device="cuda").half()
+    fresh, cos_sin = qkv.clone(), torch.cat([torch.ones(100, d // 2), torch.zeros(100, d // 2)], 1).cuda()
+    target = torch.softmax(torch.randn(batch, nodes, vocab, device="cuda"), -1)
+    tokens, u = torch.zeros(batch, nodes, dtype=torch.int32, device="cuda"), torch.rand(batch, nodes, device="cuda")
+    parents, depths = i32([[-1] + [0] * (nodes - 1)] * batch), i32([[0] + [1] * (nodes - 1)] * batch)
+    out = torch.full((batch, nodes, hq, d), 7.0, device="cuda")
+    for rotated in (cos_sin, None):
+        before = k.clone(), v.clone()
+        qkv.copy_(fresh)
+        assert tree.reserve(table, lens, (k, v)).tolist() == [lengths[0], 26, *lengths[2:]]
+        tree.attend(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], None, None, rotated, k, v, table, lens, parents,
+                    depths, out)
+        path, path_lens, words = tree.verify(target, None, tokens, parents, u)
+        kept = tree.keep((k, v), table, lens).tolist()
+        assert tree.device_errors() & fd.DEVERR_SEQ_LEN
+        for b in (0, 2, 3, 4):
+            assert (path[b] == -1).all() and path_lens[b] == 0 and (words[b] == -1).all() and kept[b] == lengths[b]
+            assert (out[b] == 7).all() and torch.equal(qkv[b * nodes:(b + 1) * nodes, :hq],
+                                                       fresh[b * nodes:(b + 1) * nodes, :hq])
+        assert kept[1] == 20 + int(path_lens[1]) and path_lens[1] >= 1 and (out[1] != 7).all()
+        mine = int(table[1, 1])
+        for pool, old in zip((k, v), before):
+            changed = (pool != old).any(-1).any(1)
+            changed[mine] = False
+            assert not changed.any()
