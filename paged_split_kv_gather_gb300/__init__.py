@@ -788,6 +788,7 @@ class TreeDecode:
         self.nodes = torch.arange(num_nodes, dtype=torch.int32, device=device)
         self.offsets = self.nodes.repeat(batch, 1)
         self.nowhere = torch.full((1,), -2**31, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(self.errors.device).synchronize()  # calls may come on any stream
 
     def _on(self, stream):
         """torch's own kernels (sums of lengths) go to the call's stream."""

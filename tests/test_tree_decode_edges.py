@@ -276,3 +276,28 @@ def test_a_round_of_sequences_with_bad_lengths():
             changed = (pool != old).any(-1).any(1)
             changed[mine] = False
             assert not changed.any()
+
+
+# ------------------------------------------------------------------------------------------------ the holder's streams
+
+@gpu
+def test_a_new_holder_can_be_used_on_any_stream(monkeypatch):
+    """What the constructor fills is there when it returns, however busy the stream that filled it."""
+    plan = fd.PagedDecode.__init__
+
+    def busy(self, *a, **kw):
+        plan(self, *a, **kw)
+        torch.cuda._sleep(200_000_000)
+
+    monkeypatch.setattr(fd.PagedDecode, "__init__", busy)
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own):
+        rubbish = [torch.full((n,), 99, dtype=torch.int32, device="cuda") for n in (1, 3, 6, 18)] * 4
+        del rubbish  # (what the holder's tensors are made of)
+        tree = fd.TreeDecode([60] * 3, 6, 16, 4, 2, 64, 32, "f16")
+        assert own.query()
+    with torch.cuda.stream(side):
+        assert tree.counts.tolist() == [6] * 3 and tree.errors.tolist() == [0] and tree.nowhere.tolist() == [-2 ** 31]
+        assert tree.offsets.tolist() == [list(range(6))] * 3 and tree.nodes.tolist() == list(range(6))
+        assert tree.batch_indices.tolist() == [0] * 6 + [1] * 6 + [2] * 6
