@@ -8,7 +8,6 @@ There is no CPU fallback: if the library is not built, the first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import importlib.util
 import math
@@ -770,10 +769,11 @@ class TreeDecode:
             raise ValueError("num_nodes must be between 1 and 64")
         if kv_dtype not in ("", "fp8"):
             raise ValueError("drafted rows go into 16-bit and E4M3 caches")
-        device = device or "cuda"
+        device = torch.device(device or "cuda")
         self.batch, self.num_nodes, self.page_size, self.num_pages = batch, num_nodes, page_size, num_pages
-        self.prefix = PagedDecode(max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,
-                                  device=device, page_lists=False, kv_dtype=kv_dtype)
+        with torch.cuda.device(device):
+            self.prefix = PagedDecode(max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,
+                                      device=device, page_lists=False, kv_dtype=kv_dtype)
         self.workspace = torch.empty(fdec_reserve_pages_workspace(batch, num_pages), dtype=torch.uint8, device=device)
         self.o = torch.empty((batch, num_nodes, num_qo_heads, head_dim), device=device)
         self.state_lse = torch.empty((batch, num_nodes, num_qo_heads), device=device)
@@ -791,11 +791,11 @@ class TreeDecode:
         torch.cuda.current_stream(self.errors.device).synchronize()  # calls may come on any stream
 
     def _on(self, stream):
-        """torch's own kernels (sums of lengths) go to the call's stream."""
+        """The holder's device, whichever is current; torch's own kernels (sums of lengths) go to the call's stream."""
         import torch
 
         if stream is None:
-            return contextlib.nullcontext()
+            return torch.cuda.device(self.errors.device)
         if not isinstance(stream, torch.cuda.Stream):
             handle, device = _stream_handle(stream), self.errors.device
             # (0 and 1 name the default stream, which torch takes no handle for)
@@ -860,4 +860,4 @@ class TreeDecode:
             flags = int(self.errors.item())
             if clear:
                 self.errors.zero_()
-        return flags | self.prefix.device_errors(clear, stream)
+            return flags | self.prefix.device_errors(clear, stream)

@@ -4,6 +4,7 @@ import math
 import os
 import random
 import subprocess
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -301,3 +302,44 @@ def test_a_new_holder_can_be_used_on_any_stream(monkeypatch):
         assert tree.counts.tolist() == [6] * 3 and tree.errors.tolist() == [0] and tree.nowhere.tolist() == [-2 ** 31]
         assert tree.offsets.tolist() == [list(range(6))] * 3 and tree.nodes.tolist() == list(range(6))
         assert tree.batch_indices.tolist() == [0] * 6 + [1] * 6 + [2] * 6
+
+
+def test_a_holder_works_on_its_own_device(monkeypatch):
+    """Whichever device is current: every call that goes by the current one is made with the holder's."""
+    current, seen = ["cuda:0"], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = str(device)
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def call(name, result=None):
+        def f(*_, **__):
+            seen.append((name, current[-1]))
+            return result
+        return f
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in ("fdec_norm_rope_append", "fdec_tree_attention", "fdec_verify_drafts", "fdec_reserve_pages"):
+        monkeypatch.setattr(fd, name, call(name))
+    tree = fd.TreeDecode.__new__(fd.TreeDecode)
+    tree.batch, tree.num_nodes, tree.page_size, tree.num_pages = 1, 2, 16, 8
+    tree.errors = SimpleNamespace(device=torch.device("cuda:1"), item=lambda: 0, zero_=lambda: None)
+    tree.prefix = SimpleNamespace(run=call("run"), device_errors=call("device_errors", 0))
+    tree.nodes, tree.nowhere = torch.arange(2, dtype=torch.int32), torch.full((1,), -1, dtype=torch.int32)
+    tree.offsets, tree.counts = tree.nodes.repeat(1, 1), torch.full((1,), 2, dtype=torch.int32)
+    tree.batch_indices = tree.o = tree.state_lse = tree.workspace = tree.path = tree.path_lens = tree.tokens = None
+    tree.granted = lens = torch.zeros(1, dtype=torch.int32)
+    rows = torch.zeros(2, 1, 64)
+    tree.reserve(None, lens)
+    tree.attend(rows, rows, rows, None, None, None, None, None, None, lens, None, None, None)
+    tree.verify(None, None, None, None, None)
+    assert tree.device_errors() == 0
+    assert [name for name, _ in seen] == ["fdec_reserve_pages", "fdec_norm_rope_append", "run", "fdec_tree_attention",
+                                          "fdec_verify_drafts", "device_errors"]
+    assert {device for _, device in seen} == {"cuda:1"} and current == ["cuda:0"]
