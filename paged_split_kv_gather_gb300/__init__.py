@@ -692,7 +692,7 @@ def _draft():
             if _draft_binding is None:
                 _draft_binding = _marshalling("_draft_binding", (
                     lib.fdec_tree_attention, lib.fdec_verify_drafts, lib.fdec_keep_path, lib.fdec_reserve_pages,
-                    lib.fdec_internal_checks_only))
+                    lib.fdec_internal_table_columns, lib.fdec_internal_checks_only))
     return _draft_binding
 
 

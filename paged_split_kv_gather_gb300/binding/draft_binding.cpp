@@ -11,6 +11,20 @@ decltype(&fdec_tree_attention) g_tree_attention = nullptr;
 decltype(&fdec_verify_drafts) g_verify_drafts = nullptr;
 decltype(&fdec_keep_path) g_keep_path = nullptr;
 decltype(&fdec_reserve_pages) g_reserve_pages = nullptr;
+void (*g_table_columns)(int64_t) = nullptr;
+
+// The calls of its scope look at the columns of a page table's view only: between its rows, and behind the last one,
+// lies what is not the view's.
+struct Columns {
+    explicit Columns(const Tensor& table) : some(table.size(0) > 1 && table.stride(0) > table.size(1)) {
+        if (some) g_table_columns(table.size(1));
+    }
+    ~Columns() {
+        if (some) g_table_columns(-1);
+    }
+    Columns(const Columns&) = delete;
+    const bool some;
+};
 
 // An int32 tensor [batch][nodes], contiguous.
 int32_t* grid(const Tensor& t, int64_t batch, int64_t nodes, const char* what) {
@@ -98,6 +112,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                  "lse and lse_prefix must be contiguous float32 [B, N, Hq]");
         on(q, {&k, &v, &table, &prefix, &counts, &parents, &o_prefix, &lse_prefix, &out, &lse, &errors});
         const double scale = a[12] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : real(a[12]);
+        const Columns columns(table);
         return on_device(q, a[16], [&](cudaStream_t stream) {
             return g_tree_attention(q.data_ptr(), tok, head, pool(k), pool(v), table_p, table_stride(table), prefix_p,
                                     counts_p, parents_p, as_int(b), as_int(n), page_size, as_int(hq), as_int(k.size(1)),
@@ -171,6 +186,7 @@ PyObject* keep_path(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         int32_t* lens_p = line(lens, b, "seq_lens");
         on(table, {&prefix, &path, &path_lens, &lens, &errors});
         on_all(table, kept);
+        const Columns columns(table);
         return on_device(table, a[8], [&](cudaStream_t stream) {
             return g_keep_path(caches.data(), as_int(static_cast<int64_t>(caches.size())), table_p, as_int(b),
                                table_stride(table), page_size, prefix_p, path_p, table_stride(path), path_lens_p,
@@ -199,6 +215,7 @@ PyObject* reserve_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         need(ws.is_contiguous(), "workspace must be contiguous");
         on(table, {&lens, &want, &granted, &ws, &sources, &errors});
         on_all(table, kept);
+        const Columns columns(table);
         return on_device(table, a[10], [&](cudaStream_t stream) {
             return g_reserve_pages(static_cast<int32_t*>(table.data_ptr()), as_int(b), table_stride(table), page_size,
                                    lens_p, want_p, sources_p, granted_p, num_pages, caches.data(),
@@ -208,12 +225,12 @@ PyObject* reserve_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// The addresses of fdec_tree_attention, fdec_verify_drafts, fdec_keep_path, fdec_reserve_pages and
-// fdec_internal_checks_only.
+// The addresses of fdec_tree_attention, fdec_verify_drafts, fdec_keep_path, fdec_reserve_pages,
+// fdec_internal_table_columns and fdec_internal_checks_only.
 PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    if (!has(n_args, 5)) return nullptr;
-    void* p[5];
-    for (int i = 0; i < 5; ++i) {
+    if (!has(n_args, 6)) return nullptr;
+    void* p[6];
+    for (int i = 0; i < 6; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -221,7 +238,8 @@ PyObject* set_entries(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     g_verify_drafts = reinterpret_cast<decltype(&fdec_verify_drafts)>(p[1]);
     g_keep_path = reinterpret_cast<decltype(&fdec_keep_path)>(p[2]);
     g_reserve_pages = reinterpret_cast<decltype(&fdec_reserve_pages)>(p[3]);
-    g_checks_only = reinterpret_cast<decltype(g_checks_only)>(p[4]);
+    g_table_columns = reinterpret_cast<decltype(g_table_columns)>(p[4]);
+    g_checks_only = reinterpret_cast<decltype(g_checks_only)>(p[5]);
     Py_RETURN_NONE;
 }
 

@@ -176,6 +176,7 @@ fdec_status fdec_tree_attention(const void* q, int64_t q_stride_tok, int64_t q_s
     p.v_st = v.stride_token * eb;
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
+    p.pt_cols = table_columns(page_table_stride);
     p.prefix_lens = prefix_lens;
     p.node_counts = node_counts;
     p.parents = parents;
@@ -280,6 +281,7 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
     if (st != FDEC_OK) return st;
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
+    p.pt_cols = table_columns(page_table_stride);
     p.prefix_lens = prefix_lens;
     p.path = path;
     p.path_stride = path_stride;
@@ -360,6 +362,7 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
     ReserveParams p = {};
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
+    p.pt_cols = table_columns(page_table_stride);
     p.seq_lens = seq_lens;
     p.new_lens = new_lens;
     p.sources = sources;

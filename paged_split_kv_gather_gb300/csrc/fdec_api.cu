@@ -103,6 +103,12 @@ static thread_local bool g_checks_only = false;
 
 bool checks_only() noexcept { return g_checks_only; }
 
+static thread_local int64_t g_table_columns = -1;  // below 0: a whole row
+
+int64_t table_columns(int64_t stride) noexcept {
+    return g_table_columns >= 0 && g_table_columns < stride ? g_table_columns : stride;
+}
+
 cudaError_t current_num_sms(int* num_sms) {
     static std::atomic<int> sms[64];  // 0 = not yet queried
     int dev = 0;
@@ -1044,6 +1050,9 @@ fdec_status fdec_run_q8_0(fdec_plan_t p, const void* q, int64_t q_stride_tok, in
 
 // Not part of the ABI: see checks_only.
 void fdec_internal_checks_only(int on) { fdec::g_checks_only = on != 0; }
+
+// Not part of the ABI: see table_columns.
+void fdec_internal_table_columns(int64_t columns) { fdec::g_table_columns = columns; }
 
 fdec_status fdec_run_selected(fdec_plan_t p, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
                               fdec_kv_desc k, fdec_kv_desc v, const int32_t* page_ids, int64_t page_ids_stride,

@@ -292,7 +292,7 @@ struct TreeParams {
     const uint8_t* v_base;
     int64_t v_pages, v_sp, v_sh, v_st;
     const int32_t* page_table;
-    int64_t pt_stride;
+    int64_t pt_stride, pt_cols;
     const int32_t* prefix_lens;
     const int32_t* node_counts;  // null: nodes each
     const int32_t* parents;      // null: a chain
@@ -354,7 +354,7 @@ struct CacheList {
 
 struct KeepParams {
     const int32_t* page_table;
-    int64_t pt_stride;
+    int64_t pt_stride, pt_cols;
     const int32_t* prefix_lens;
     const int32_t* path;
     int64_t path_stride;
@@ -368,7 +368,7 @@ cudaError_t launch_keep_path(const KeepParams& p, const CacheList<kMaxCaches>& c
 
 struct ReserveParams {
     int32_t* page_table;
-    int64_t pt_stride;
+    int64_t pt_stride, pt_cols;
     const int32_t* seq_lens;
     const int32_t* new_lens;
     const int32_t* sources;      // or null
@@ -396,6 +396,9 @@ void clear_failure() noexcept;
 // check of theirs (see sparse_binding.cpp).
 constexpr int kChecksOnly = -1;
 bool checks_only() noexcept;
+// Columns of this thread's page tables: a row's stride, or fewer where the binding was given a
+// view of some columns (what lies between its rows is another's).
+int64_t table_columns(int64_t stride) noexcept;
 // SM count of the current device, queried once per device.
 cudaError_t current_num_sms(int* num_sms);
 // One task given by value (p.tasks must be null): used by fdec_merge_states.

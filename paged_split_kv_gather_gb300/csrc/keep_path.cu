@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kColumnThreads)
             for (int k = 0; k < 2; ++k) {
                 const int64_t pos = prefix + (k == 0 ? node[h] : i), pi = pos >> p.page_shift;
                 at[k] = make_int2(-1, static_cast<int>(pos & ((1 << p.page_shift) - 1)));
-                if (pi >= p.pt_stride) {
+                if (pi >= p.pt_cols) {
                     flags |= FDEC_DEVERR_SEQ_LEN;
                     ok = false;
                 } else {

@@ -40,7 +40,7 @@ struct Request {
 };
 
 __device__ __forceinline__ bool length_ok(const ReserveParams& p, int64_t n) {
-    return n >= 0 && n <= p.pt_stride << p.page_shift;
+    return n >= 0 && n <= p.pt_cols << p.page_shift;
 }
 
 // The sequence's source (itself if none) and the positions it begins with; source -1: bad.
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_mark_kernel(const Res
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t* row = p.page_table + b * p.pt_stride;
-    const int64_t room = p.pt_stride << p.page_shift;
+    const int64_t room = p.pt_cols << p.page_shift;
     int64_t len = p.seq_lens[b];
     unsigned flags = 0;
     if (!length_ok(p, len)) {
@@ -332,7 +332,7 @@ cudaError_t launch_reserve_pages(const ReserveParams& p, const CacheList<kMaxCac
     const int64_t clear = std::min<int64_t>((p.words + kReserveThreads - 1) / kReserveThreads, num_sms * 4);
     cudaError_t e = launch(reserve_clear_kernel, clear, s, p);
     if (e != cudaSuccess) return e;
-    const int64_t row_blocks = (p.pt_stride + kReserveThreads * 4 - 1) / (kReserveThreads * 4);
+    const int64_t row_blocks = (p.pt_cols + kReserveThreads * 4 - 1) / (kReserveThreads * 4);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(row_blocks, num_sms * 16 / p.batch));
     e = launch(reserve_mark_kernel, blocks * p.batch, s, p, static_cast<int>(blocks));
     if (e != cudaSuccess) return e;

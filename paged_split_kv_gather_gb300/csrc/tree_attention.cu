@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
                     const int i = lane + 32 * h;
                     const int64_t pos = max(prefix, static_cast<int64_t>(0)) + i, pi = pos >> p.page_shift;
                     slot_of[h] = pos & ((1 << p.page_shift) - 1);
-                    behind[h] = pi >= p.pt_stride;
+                    behind[h] = pi >= p.pt_cols;
                     page[h] = i < N && !behind[h] ? p.page_table[static_cast<int64_t>(b_of) * p.pt_stride + pi] : -1;
                 }
                 if (n < 0 || n > N) {

@@ -343,3 +343,59 @@ def test_a_holder_works_on_its_own_device(monkeypatch):
     assert [name for name, _ in seen] == ["fdec_reserve_pages", "fdec_norm_rope_append", "run", "fdec_tree_attention",
                                           "fdec_verify_drafts", "device_errors"]
     assert {device for _, device in seen} == {"cuda:1"} and current == ["cuda:0"]
+
+
+# ------------------------------------------------------------------------------- page tables that are views of columns
+
+@gpu
+def test_columns_that_are_not_the_views_are_neither_read_nor_written():
+    """Tables within wider ones: a length past the view's columns is one past the page table, also in the last row."""
+    page, width = 16, 3
+    whole = i32(np.full((4, 8), 77))
+    table = whole[1:3, 2:2 + width]
+    table.copy_(i32([[0, 1, 2], [3, 4, 5]]))
+    before = whole.clone()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def flags():
+        got = int(err.item())
+        err.zero_()
+        return got
+
+    granted = torch.empty(2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fd.fdec_reserve_pages_workspace(2, 64), dtype=torch.uint8, device="cuda")
+
+    def reserve(lens, new, sources=None):
+        fd.fdec_reserve_pages(table, i32(lens), i32(new), granted, 64, page, ws, device_errors=err,
+                              sources=None if sources is None else i32(sources))
+        return granted.tolist()
+
+    assert reserve([30, 20], [49, 49]) == [30, 20] and flags() == fd.DEVERR_SEQ_LEN and torch.equal(whole, before)
+    assert reserve([49, 20], [49, 20]) == [49, 20] and flags() == fd.DEVERR_SEQ_LEN  # (marks its own columns only)
+    assert reserve([0, 20], [49, 30], [1, -1])[0] == 0 and flags() == fd.DEVERR_SEQ_LEN
+    assert torch.equal(whole, before)
+    assert reserve([17, 20], [48, 48]) == [48, 48] and flags() == 0
+    assert table.tolist() == [[0, 1, 2], [3, 4, 5]] and (whole[:, :2] == 77).all() and (whole[:, 5:] == 77).all()
+
+    for path, upto, flag in (([0, 2, 5, 9], 2, fd.DEVERR_TREE),  # (of four nodes: it ends before the 5)
+                             ([0, 2, 5, 9] + [-1] * 6, 3, fd.DEVERR_SEQ_LEN)):
+        pool = torch.randn(6, 1, page, 64).half().cuda()
+        kept, out = pool.clone(), torch.empty(2, dtype=torch.int32, device="cuda")
+        fd.fdec_keep_path([pool], table, i32([44, 44]), i32([path] * 2), i32([3, 3]), out, page, device_errors=err)
+        assert flags() == flag and out.tolist() == [44 + upto] * 2
+        for b in range(2):
+            last = kept[3 * b + 2]
+            last[:, 13] = last[:, 14]  # (the third row lies past the view)
+        assert torch.equal(pool, kept)
+
+    c = Tree(64, 4, 2, 8, page, 2, "f16", seed=3, counts=[8, 8], prefix=[20, 40])
+    wide = i32(np.full((3, 9), c.k.shape[0] - 1))
+    view = wide[1:, 1:1 + 3]
+    view.copy_(i32(c.table[:, :3]))
+    out, lse = torch.zeros(c.q.shape, device="cuda"), torch.zeros(c.q.shape[:3], device="cuda")
+    c.prefix = [20, 44]
+    c.table = np.concatenate([c.table[:, :3], np.full((2, 1), -1, dtype=np.int32)], 1)
+    fd.fdec_tree_attention(c.q, c.k, c.v, view, i32(c.prefix), i32(c.parents), c.o_prefix, c.lse_prefix, out, lse, page,
+                           device_errors=err)
+    assert flags() == fd.DEVERR_SEQ_LEN
+    c.check(out, lse, unseen={(1, j) for j in range(4, 8)})
