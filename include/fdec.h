@@ -537,7 +537,8 @@ enum { FDEC_PROB_F16 = 0, FDEC_PROB_BF16 = 1, FDEC_PROB_F32 = 2 };
  *   path_lens: int32 device [batch], their number (node 0 among them; 0 without nodes).
  *   out_tokens: int32 device [batch][num_nodes]: the tokens of path[1..], then the next
  *      token (-1 if the target's row is all zeros: FDEC_DEVERR_PROB), then -1.
- * vocab in [1, 2^24].
+ * The last three may be arrays of the same shape that are read here (path parents, out_tokens
+ * tokens, path_lens node_counts), and overlap nothing else.  vocab in [1, 2^24].
  */
 fdec_status fdec_verify_drafts(const void* target_probs, int64_t target_stride_seq, int64_t target_stride_node,
                                const void* draft_probs, int64_t draft_stride_seq, int64_t draft_stride_node,
@@ -585,7 +586,7 @@ enum { FDEC_MAX_CACHES = 128 };
  *      that sequence moves, and seq_lens[b] = prefix_lens[b].
  *   page_table, device_errors: as for fdec_tree_attention; a row in a bad page (for any of
  *      the caches) or past the page table is not moved.
- *   seq_lens: int32 device [batch]; must not overlap prefix_lens.
+ *   seq_lens: int32 device [batch]; must not overlap the other arrays.
  * The pages that hold the moved rows must belong to one sequence alone (fdec_reserve_pages
  * sees to that).
  */
@@ -618,7 +619,7 @@ fdec_status fdec_reserve_pages_workspace(int batch, int64_t num_pages, size_t* w
  *   sources: int32 device [batch], a negative one for none; or NULL.  A bad length or source
  *      sets FDEC_DEVERR_SEQ_LEN, and that sequence is left alone.
  *   granted: int32 device [batch]: new_lens[b], or seq_lens[b] where it was refused; must not
- *      overlap the other arrays.  What a refused row's entries past its length name may be
+ *      overlap the other arrays (nor page_table those that are read).  What a refused row's entries past its length name may be
  *      another sequence's by now: no rows are to be appended there (a node_count of
  *      granted[b] - seq_lens[b], positions below 0).
  *   num_pages: pages of the pool, at most what every cache has, and at most 2^26.

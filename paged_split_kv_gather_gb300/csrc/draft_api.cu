@@ -29,6 +29,25 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
     return x < y + b_bytes && y < x + a_bytes;
 }
 
+struct Span {
+    const void* base;  // or null
+    size_t bytes;
+};
+
+bool clash(Span a, Span b) {
+    return a.base != nullptr && b.base != nullptr && overlap(a.base, a.bytes, b.base, b.bytes);
+}
+
+template <size_t N>
+bool clash(Span a, const Span (&others)[N]) {
+    return std::any_of(others, others + N, [&](Span b) { return clash(a, b); });
+}
+
+// Bytes of `rows` rows of int32, `cols` of `stride` entries each.
+size_t table_bytes(int64_t rows, int64_t stride, int64_t cols) {
+    return (static_cast<size_t>(rows - 1) * stride + cols) * 4;
+}
+
 // A pool of rows of 16-byte multiples (eb bytes an element).
 fdec_status check_pool(const fdec_kv_desc& d, int eb) {
     if (d.base == nullptr) return fail(FDEC_ERR_INVALID_ARG, "null pool");
@@ -229,6 +248,29 @@ fdec_status fdec_verify_drafts(const void* target_probs, int64_t target_stride_s
     if (!aligned(tokens, 4) || !aligned(parents, 4) || !aligned(node_counts, 4) || !aligned(uniforms, 4) ||
         !aligned(path, 4) || !aligned(path_lens, 4) || !aligned(out_tokens, 4) || !aligned(device_errors, 4))
         return fail(FDEC_ERR_LAYOUT, "misaligned array");
+    // Every sequence's nodes are read before its results are written: arrays of one shape may be the same one.
+    const size_t line = static_cast<size_t>(batch) * 4, grid = line * num_nodes;
+    const Span nodes[3] = {{tokens, grid}, {parents, grid}, {uniforms, grid}};
+    const auto probs = [&](const void* base, int64_t seq, int64_t node, int rows) {
+        return Span{base, (static_cast<size_t>(batch - 1) * seq + static_cast<size_t>(rows - 1) * node + vocab) * eb};
+    };
+    const Span rows[2] = {probs(target_probs, target_stride_seq, target_stride_node, num_nodes),
+                          num_nodes == 1 ? Span{}
+                                         : probs(draft_probs, draft_stride_seq, draft_stride_node, num_nodes - 1)};
+    for (const void* result : {static_cast<const void*>(path), static_cast<const void*>(out_tokens)}) {
+        const Span r = {result, grid};
+        for (const Span& in : nodes)
+            if (in.base != result && clash(r, in))
+                return fail(FDEC_ERR_INVALID_ARG, "path or out_tokens overlaps tokens, parents or uniforms and is not "
+                                                  "that array");
+        if (clash(r, Span{node_counts, line}) || clash(r, rows))
+            return fail(FDEC_ERR_INVALID_ARG, "path or out_tokens overlaps node_counts or probabilities");
+    }
+    const Span lens = {path_lens, line};
+    if (clash(lens, nodes) || clash(lens, rows) || (node_counts != path_lens && clash(lens, Span{node_counts, line})))
+        return fail(FDEC_ERR_INVALID_ARG, "path_lens overlaps an input and is not node_counts");
+    if (clash(Span{path, grid}, Span{out_tokens, grid}) || clash(lens, {Span{path, grid}, Span{out_tokens, grid}}))
+        return fail(FDEC_ERR_INVALID_ARG, "path, path_lens and out_tokens must not overlap");
     VerifyParams p = {};
     p.target = target_probs;
     p.t_seq = target_stride_seq;
@@ -271,17 +313,18 @@ fdec_status fdec_keep_path(const fdec_cache* caches, int num_caches, const int32
         !aligned(seq_lens, 4) || !aligned(device_errors, 4))
         return fail(FDEC_ERR_LAYOUT, "misaligned index array");
     const size_t bytes = static_cast<size_t>(batch) * 4;
-    const size_t path_bytes = (static_cast<size_t>(batch - 1) * path_stride + num_nodes) * 4;
-    if (overlap(seq_lens, bytes, prefix_lens, bytes) || overlap(seq_lens, bytes, path_lens, bytes) ||
-        overlap(seq_lens, bytes, path, path_bytes))
-        return fail(FDEC_ERR_INVALID_ARG, "seq_lens overlaps prefix_lens, path or path_lens");
+    const int64_t cols = table_columns(page_table_stride);
+    if (clash(Span{seq_lens, bytes}, {Span{prefix_lens, bytes}, Span{path_lens, bytes},
+                                      Span{path, table_bytes(batch, path_stride, num_nodes)},
+                                      Span{page_table, table_bytes(batch, page_table_stride, cols)}}))
+        return fail(FDEC_ERR_INVALID_ARG, "seq_lens overlaps prefix_lens, path, path_lens or page_table");
     CacheList<kMaxCaches> list;
     KeepParams p = {};
     st = take_caches(caches, num_caches, page_size, &list, &p.num_pages);
     if (st != FDEC_OK) return st;
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
-    p.pt_cols = table_columns(page_table_stride);
+    p.pt_cols = cols;
     p.prefix_lens = prefix_lens;
     p.path = path;
     p.path_stride = path_stride;
@@ -348,12 +391,18 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
         !aligned(granted, 4) || !aligned(device_errors, 4))
         return fail(FDEC_ERR_LAYOUT, "misaligned index array");
     const size_t bytes = static_cast<size_t>(batch) * 4;
-    if (overlap(granted, bytes, seq_lens, bytes) || overlap(granted, bytes, new_lens, bytes) ||
-        (sources != nullptr && overlap(granted, bytes, sources, bytes)))
-        return fail(FDEC_ERR_INVALID_ARG, "granted overlaps seq_lens, new_lens or sources");
+    const int64_t cols = table_columns(page_table_stride);
+    const Span inputs[3] = {{seq_lens, bytes}, {new_lens, bytes}, {sources, bytes}};
+    const Span table = {page_table, table_bytes(batch, page_table_stride, cols)};
+    if (clash(Span{granted, bytes}, inputs) || clash(Span{granted, bytes}, table))
+        return fail(FDEC_ERR_INVALID_ARG, "granted overlaps seq_lens, new_lens, sources or page_table");
+    if (clash(table, inputs))
+        return fail(FDEC_ERR_INVALID_ARG, "page_table overlaps seq_lens, new_lens or sources");
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < l.bytes)
         return fail(FDEC_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than "
                                         "fdec_reserve_pages_workspace says");
+    if (clash(Span{workspace, l.bytes}, inputs) || clash(Span{workspace, l.bytes}, {table, Span{granted, bytes}}))
+        return fail(FDEC_ERR_INVALID_ARG, "workspace overlaps another array");
     CacheList<kMaxCaches> list;
     int64_t fewest = 0;
     const fdec_status st = take_caches(caches, num_caches, page_size, &list, &fewest);
@@ -362,7 +411,7 @@ fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_tabl
     ReserveParams p = {};
     p.page_table = page_table;
     p.pt_stride = page_table_stride;
-    p.pt_cols = table_columns(page_table_stride);
+    p.pt_cols = cols;
     p.seq_lens = seq_lens;
     p.new_lens = new_lens;
     p.sources = sources;

@@ -11,7 +11,8 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from test_tree_decode import DT, U, Tree, i32, path_of, run_verify
+from test_tree_decode import (U, Tree, aligned_workspace, cpu_keep, cpu_reserve, cpu_verify, drafts_of, i32, path_of,
+                              refused, run_verify)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 gpu = pytest.mark.gpu
@@ -399,3 +400,64 @@ def test_columns_that_are_not_the_views_are_neither_read_nor_written():
                            device_errors=err)
     assert flags() == fd.DEVERR_SEQ_LEN
     c.check(out, lse, unseen={(1, j) for j in range(4, 8)})
+
+
+# ------------------------------------------------------------------------------------------- arrays that are one another's
+
+def test_verify_drafts_refuses_results_on_one_another_or_on_inputs():
+    with pytest.raises(ValueError, match="CUDA device"):  # each sequence's inputs are read first
+        x, y, z = (torch.zeros(2, 4, dtype=torch.int32) for _ in range(3))
+        n = torch.zeros(2, dtype=torch.int32)
+        cpu_verify(tokens=x, out_tokens=x, parents=y, path=y, node_counts=n, path_lens=n)
+    grid, line = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    many = torch.zeros(64, dtype=torch.int32)
+    some = {"path": many[8:16].view(2, 4), "out_tokens": many[24:32].view(2, 4), "path_lens": many[40:42]}
+    spans = {"path": (8, 16), "out_tokens": (24, 32), "path_lens": (40, 42)}
+    refused("FDEC_ERR_INVALID_ARG", cpu_verify, path=grid, out_tokens=grid)
+    for name, (a, b) in spans.items():
+        for at in (a - 3, a + 1, b - 1):
+            near = many[at:at + 8].view(2, 4)
+            for other in ("tokens", "parents", "uniforms"):
+                view = near.view(torch.float32) if other == "uniforms" else near
+                refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, other: view})
+            if name != "path_lens":
+                refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, "path_lens": many[a + 2:a + 4]})
+                refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, "node_counts": many[a:a + 2]})
+        refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, "node_counts": many[b - 1:b + 1]})
+        probs = many[a - 2:].view(torch.float32)[:8].view(2, 4, 1)
+        refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, "target_probs": probs, "draft_probs": None})
+        refused("FDEC_ERR_INVALID_ARG", cpu_verify, **{**some, "target_probs": torch.zeros(2, 4, 1), "draft_probs": probs})
+    # the row behind the drafts' last is nobody's
+    with pytest.raises(ValueError, match="CUDA device"):
+        probs = torch.zeros(2 * 4 * 10 + 4)
+        cpu_verify(draft_probs=probs[:80].view(2, 4, 10)[:, :3], path_lens=probs.view(torch.int32)[70:72])
+
+
+def test_kept_lengths_and_granted_ones_have_arrays_of_their_own():
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    refused("FDEC_ERR_INVALID_ARG", cpu_keep, page_table=table, seq_lens=table.view(-1)[4:6])
+    refused("FDEC_ERR_INVALID_ARG", cpu_reserve, page_table=table, granted=table.view(-1)[:2])
+    for name in ("seq_lens", "new_lens", "sources"):
+        refused("FDEC_ERR_INVALID_ARG", cpu_reserve, page_table=table, **{name: table.view(-1)[3:5]})
+    ws = aligned_workspace(2, 64)
+    words = ws.view(torch.int32)
+    for name in ("seq_lens", "new_lens", "sources", "granted"):
+        refused("FDEC_ERR_INVALID_ARG", cpu_reserve, workspace=ws, **{name: words[3:5]})
+    refused("FDEC_ERR_INVALID_ARG", cpu_reserve, workspace=ws, page_table=words[-6:].view(2, 3))
+    # a row of a wider table, and what lies beside the view
+    wide = torch.zeros(2, 8, dtype=torch.int32)
+    refused("FDEC_ERR_INVALID_ARG", cpu_reserve, page_table=wide[:, 2:5], granted=wide[1, 4:6])
+    with pytest.raises(ValueError, match="CUDA device"):
+        cpu_reserve(page_table=wide[:, 2:5], granted=wide[1, 5:7])
+
+
+@gpu
+@pytest.mark.parametrize("vocab", [500, 9000])
+def test_verify_drafts_in_place_of_what_it_reads(vocab):
+    g, rng = torch.Generator().manual_seed(vocab), random.Random(vocab)
+    target, draft, tokens, parents = drafts_of(g, rng, 9, 7, vocab, "f32", "tree", True)
+    u, counts = torch.rand((9, 7), generator=g), [7, 0, 3, 7, 1, 6, 7, 7, 2]
+    want = run_verify(target, draft, tokens, parents, u, counts)
+    tok, par, n = i32(tokens), i32(parents), i32(counts)
+    fd.fdec_verify_drafts(target, draft, tok, par, u.cuda(), par, n, tok, node_counts=n)
+    assert torch.equal(par.cpu(), want[0]) and torch.equal(n.cpu(), want[1]) and torch.equal(tok.cpu(), want[2])
