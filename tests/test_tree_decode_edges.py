@@ -11,8 +11,8 @@ import pytest
 import torch
 
 import paged_split_kv_gather_gb300 as fd
-from test_tree_decode import (U, Tree, aligned_workspace, cpu_keep, cpu_reserve, cpu_verify, drafts_of, i32, path_of,
-                              refused, run_verify)
+from test_tree_decode import (U, Tree, aligned_workspace, check_verify, cpu_keep, cpu_reserve, cpu_verify, drafts_of, i32,
+                              path_of, refused, run_verify)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 gpu = pytest.mark.gpu
@@ -461,3 +461,24 @@ def test_verify_drafts_in_place_of_what_it_reads(vocab):
     tok, par, n = i32(tokens), i32(parents), i32(counts)
     fd.fdec_verify_drafts(target, draft, tok, par, u.cuda(), par, n, tok, node_counts=n)
     assert torch.equal(par.cpu(), want[0]) and torch.equal(n.cpu(), want[1]) and torch.equal(tok.cpu(), want[2])
+
+
+@gpu
+@pytest.mark.parametrize("left,stands", [(1e-2, False), (1e-5, False), (1e-8, True)])
+def test_heavy_tokens_fall_and_the_rest_is_drawn_from(left, stands):
+    """Four children hold (1 - left) / 4 each.  The last is tried with W = (1 - left) / 4 + left, all numbers 1 - 2^-24: it
+    falls where left > 2^-24 / 4 = 1.5e-8, and the next token is one of the rest; else it stands."""
+    g = torch.Generator().manual_seed(8)
+    batch, nodes, vocab = 16, 5, 3000
+    p = torch.softmax(torch.randn((batch, nodes, vocab), generator=g) * 2, -1) * left
+    p[:, :, 100:104] = (1 - left) / 4
+    u = torch.ones((batch, nodes)) * (1 - 2.0 ** -24)
+    u[:, 0] = torch.rand(batch, generator=g)
+    tokens, parents = [[0, 100, 101, 102, 103]] * batch, [[-1, 0, 0, 0, 0]] * batch
+    target = p.float().cuda()
+    assert set(check_verify(target, None, tokens, parents, u)) == ({2} if stands else {1})
+    path, _, words, _ = run_verify(target, None, tokens, parents, u)
+    if stands:
+        assert path[:, :2].tolist() == [[0, 4]] * batch and (words[:, 0] == 103).all()
+    else:
+        assert ((words[:, 0] < 100) | (words[:, 0] > 103)).all() and (words[:, 0] >= 0).all()
