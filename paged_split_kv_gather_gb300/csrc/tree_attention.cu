@@ -145,7 +145,7 @@ __device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
 // 2^-24, half a step of fp32, of what the rows that it does see hold in those columns.
 constexpr unsigned kSpread = 8;
 
-// CTAs on an SM: by the registers of S, P and O.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
+// CTAs on an SM that the registers of S, P and O are to allow.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
 // nodes 8.4 us instead of 10.6; but at head_dim 256 16 trees of 13 nodes 6.5 us instead of 6.0.)
 constexpr int tree_ctas(int head_dim, int ks) { return ks == 1 && head_dim <= 128 ? 4 : 3; }
 
@@ -786,22 +786,29 @@ __global__ void __launch_bounds__(kTreeThreads, tree_ctas(D, KS)) tree_attention
 
 template <int D, bool BF16, bool KV8, int KS>
 cudaError_t launch_tree_one(TreeParams p, int num_sms, cudaStream_t s) {
-    static unsigned long long attr_done = 0;  // one bit per device
+    constexpr int kDevices = 64;
+    static int resident_on[kDevices] = {};  // CTAs on an SM, 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-        e = cudaFuncSetAttribute(tree_attention_kernel<D, BF16, KV8, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(TreeShape<D>::smem(16 * KS)));
+    int resident = dev < kDevices ? __atomic_load_n(&resident_on[dev], __ATOMIC_ACQUIRE) : 0;
+    if (resident == 0) {
+        const auto kernel = tree_attention_kernel<D, BF16, KV8, KS>;
+        const size_t smem = TreeShape<D>::smem(16 * KS);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, kTreeThreads, smem);
         if (e != cudaSuccess) return e;
-        if (dev < 64) __atomic_fetch_or(&attr_done, 1ull << dev, __ATOMIC_RELEASE);
+        resident = std::max(resident, 1);
+        if (dev < kDevices) __atomic_store_n(&resident_on[dev], resident, __ATOMIC_RELEASE);
     }
     // Up to as many sequences' KV heads as CTAs are resident, or with fewer tiles in each than a CTA has warps: parts
     // of one head each, as an equal share that spans two stages two trees (256 heads of 6 tiles: 7.0 us, 9.0 shared).
     // Else equal shares: whole heads in a second round would leave most of the machine idle (512 heads of 16 tiles:
-    // 40 us, 49 a head a CTA).
+    // 40 us, 49 a head a CTA).  What is resident is asked for, as shared memory holds fewer CTAs than registers where
+    // heads of more than 128 dims meet more than 32 nodes (768 heads of 16 tiles, head_dim 192: 109 us; 140 with three
+    // CTAs an SM taken for granted, of which two fit).
     const int64_t heads = static_cast<int64_t>(p.batch) * p.hk;
-    const int64_t slots = static_cast<int64_t>(num_sms) * tree_ctas(D, KS);
+    const int64_t slots = static_cast<int64_t>(num_sms) * resident;
     const int per_head = (p.nodes * p.group + 15) / 16;
     const bool whole = heads <= slots || per_head < kTreeWarps;
     const int64_t wide = std::min<int64_t>((per_head + kTreeWarps - 1) / kTreeWarps, 2 * slots / heads);

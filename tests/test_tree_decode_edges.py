@@ -482,3 +482,27 @@ def test_heavy_tokens_fall_and_the_rest_is_drawn_from(left, stands):
         assert path[:, :2].tolist() == [[0, 4]] * batch and (words[:, 0] == 103).all()
     else:
         assert ((words[:, 0] < 100) | (words[:, 0] > 103)).all() and (words[:, 0] >= 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("d,hq,hk,nodes,batch", [(192, 16, 4, 64, 80), (256, 12, 4, 35, 90), (512, 4, 2, 40, 80),
+                                                 (512, 8, 2, 20, 160)])
+def test_tree_attention_in_equal_shares_of_large_heads(d, hq, hk, nodes, batch):
+    """More sequences' heads than CTAs are resident, where shared memory bounds those: shares span sequences."""
+    c = Tree(d, hq, hk, nodes, 16, batch, "bf16", seed=17)
+    out, lse = c.run()
+    few = random.Random(2).sample(range(batch), 3) + [0, batch - 1]
+    c.check(out, lse, counts=[n if b in few else 0 for b, n in enumerate(c.counts)])
+    for b in range(0, batch, 8):  # the others against calls of few sequences, summed in another order
+        part = slice(b, min(batch, b + 8))
+        o, l2 = torch.full_like(out[part], 3.0), torch.full_like(lse[part], 5.0)
+        fd.fdec_tree_attention(c.q[part], c.k, c.v, i32(c.table[part]), i32(c.prefix[part]), i32(c.parents[part]),
+                               c.o_prefix[part], c.lse_prefix[part], o, l2, 16, node_counts=i32(c.counts[part]))
+        # (sum |q_d k_d| is at most |q| |k|; twice the module's tolerance, for the two calls)
+        most = c.scale * float((c.q[part].double().norm(dim=-1).max() * c.k.double().norm(dim=-1).max()).item())
+        most, largest = max(most, 12.0), max(float(c.v.abs().max()), float(c.o_prefix.nan_to_num(0).abs().max()))
+        e = (2 * d + 4) * U * most
+        assert (o - out[part]).abs().nan_to_num(0).max() <= 2 * (2 * e + 8 * U * most + 200 * U) * largest
+        assert torch.equal(torch.isnan(o), torch.isnan(out[part]))
+        assert torch.equal((l2 == -math.inf), (lse[part] == -math.inf))
+        assert (l2 - lse[part]).nan_to_num(0).abs().max() <= 2 * (e + 4 * U * (most + 8) + 140 * U)
