@@ -30,36 +30,24 @@ template <typename V, typename From, typename To>
 __device__ __forceinline__ void move_columns(const CacheRows& c, int blk, int begin, int end, From from, To to) {
     constexpr int U = kRowsAhead;
     const int64_t columns = static_cast<int64_t>(c.layers) * c.heads * c.row_vecs;
-    uint8_t* col[kColumnsPerThread];
-#pragma unroll
-    for (int k = 0; k < kColumnsPerThread; ++k) {
-        const int64_t x = static_cast<int64_t>(blk - c.first_block) * kColumnsPerBlock + k * kColumnThreads + threadIdx.x;
-        col[k] = nullptr;
-        if (x < columns) {
-            const int64_t lh = x / c.row_vecs;
-            const int64_t layer = lh / c.heads;
-            col[k] = c.base + layer * c.s_layer + (lh - layer * c.heads) * c.s_head + (x - lh * c.row_vecs) * sizeof(V);
-        }
-    }
+    const int64_t x = static_cast<int64_t>(blk - c.first_block) * kColumnThreads + threadIdx.x;
+    if (x >= columns) return;
+    const int64_t lh = x / c.row_vecs;
+    const int64_t layer = lh / c.heads;
+    uint8_t* col = c.base + layer * c.s_layer + (lh - layer * c.heads) * c.s_head + (x - lh * c.row_vecs) * sizeof(V);
     for (int i0 = begin; i0 < end; i0 += U) {
-        V val[U][kColumnsPerThread];
+        V val[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i0 + u >= end) break;
             const int2 f = from(i0 + u);  // (page, slot), page < 0: not moved
-#pragma unroll
-            for (int k = 0; k < kColumnsPerThread; ++k)
-                if (f.x >= 0 && col[k] != nullptr)
-                    val[u][k] = *reinterpret_cast<const V*>(col[k] + f.x * c.s_page + f.y * c.s_token);
+            if (f.x >= 0) val[u] = *reinterpret_cast<const V*>(col + f.x * c.s_page + f.y * c.s_token);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i0 + u >= end) break;
             const int2 f = from(i0 + u), t = to(i0 + u);
-#pragma unroll
-            for (int k = 0; k < kColumnsPerThread; ++k)
-                if (f.x >= 0 && col[k] != nullptr)
-                    *reinterpret_cast<V*>(col[k] + t.x * c.s_page + t.y * c.s_token) = val[u][k];
+            if (f.x >= 0) *reinterpret_cast<V*>(col + t.x * c.s_page + t.y * c.s_token) = val[u];
         }
     }
 }
@@ -78,7 +66,7 @@ inline int64_t column_blocks(const CacheList<kMaxCaches>& list) {
     if (list.n == 0) return 0;
     const CacheRows& c = list.c[list.n - 1];
     const int64_t columns = static_cast<int64_t>(c.layers) * c.heads * c.row_vecs;
-    return c.first_block + (columns + kColumnsPerBlock - 1) / kColumnsPerBlock;
+    return c.first_block + (columns + kColumnThreads - 1) / kColumnThreads;
 }
 
 }  // namespace fdec

@@ -108,7 +108,7 @@ fdec_status take_caches(const fdec_cache* caches, int num_caches, int page_size,
         r.first_block = static_cast<int>(blocks);
         const int64_t columns = static_cast<int64_t>(c.num_layers) * c.num_heads;
         if (columns > INT32_MAX / r.row_vecs) return fail(FDEC_ERR_UNSUPPORTED, "too many rows at a position");
-        blocks += (columns * r.row_vecs + kColumnsPerBlock - 1) / kColumnsPerBlock;
+        blocks += (columns * r.row_vecs + kColumnThreads - 1) / kColumnThreads;
         if (blocks > 1 << 24) return fail(FDEC_ERR_UNSUPPORTED, "too many rows at a position");
         *fewest = std::min(*fewest, c.num_pages);
     }

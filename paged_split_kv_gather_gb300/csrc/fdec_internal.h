@@ -342,10 +342,8 @@ struct CacheRows {
     int first_block;
 };
 constexpr int kMaxCaches = 128;
-constexpr int kColumnThreads = 256;    // of a block
-constexpr int kColumnsPerThread = 1;
-constexpr int kRowsAhead = 4;          // rows of each column in flight a thread
-constexpr int kColumnsPerBlock = kColumnThreads * kColumnsPerThread;
+constexpr int kColumnThreads = 256;  // of a block, a column each
+constexpr int kRowsAhead = 4;        // rows of a column in flight
 template <int N>
 struct CacheList {
     CacheRows c[N];
