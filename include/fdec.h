@@ -626,6 +626,9 @@ fdec_status fdec_reserve_pages_workspace(int batch, int64_t num_pages, size_t* w
  *   caches: the rows to copy, num_caches of them (0: only page numbers are dealt with).
  *   workspace: see fdec_reserve_pages_workspace; 256-byte aligned, not shared by calls that
  *      may overlap; its contents do not matter.
+ * batch at most 65536.  Every sequence counts what those before it ask for, so the time grows
+ * with the square of large batches: 21 us for 1024 sequences that grow by a page, 60 us for
+ * 4096, 0.5 ms for 16384, 7.3 ms for 65536.
  */
 fdec_status fdec_reserve_pages(int32_t* page_table, int batch, int64_t page_table_stride, int page_size,
                                const int32_t* seq_lens, const int32_t* new_lens, const int32_t* sources,

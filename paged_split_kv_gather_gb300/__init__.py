@@ -811,7 +811,7 @@ class TreeDecode:
         """Pages for the nodes behind prefix_lens; returns the lengths granted: prefix_lens[b] + num_nodes, or
         prefix_lens[b] where there are no pages.  (Forks come before the round, with fdec_reserve_pages: a fork's prefix
         is its source's, not the 0 that it has now.)  caches: all layers' keys and values, whose rows are copied where a
-        partly filled last page is shared."""
+        partly filled last page is shared (left out, such a page's rows are not there: only where no sequence is a fork)."""
         import torch
 
         with self._on(stream):

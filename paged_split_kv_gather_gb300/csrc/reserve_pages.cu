@@ -10,6 +10,8 @@
 // 131072 pages (from the marking's atomics they cost 45 us, for 256 sequences and a million
 // pages, each CTA reading all bits 9 us); below, every CTA counts for itself.
 // The rows that a fork or a shared last page needs are copied last.
+// (Each sequence goes through the requests of those before it: of a page each, called one by one, 64 sequences take
+// 13.4 us, 256 14.6, 1024 21, 4096 60 and 65536 7.3 ms.)
 //
 // Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.  64
 // sequences and 65536 pages: 8.4 to 8.8 us, the latencies of three dependent launches (clear 1,

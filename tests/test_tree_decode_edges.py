@@ -12,7 +12,7 @@ import torch
 
 import paged_split_kv_gather_gb300 as fd
 from test_tree_decode import (U, Tree, aligned_workspace, check_verify, cpu_keep, cpu_reserve, cpu_verify, drafts_of, i32,
-                              path_of, refused, run_verify)
+                              path_of, refused, reserve_case, reserve_reference, run_reserve, run_verify)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 gpu = pytest.mark.gpu
@@ -506,3 +506,24 @@ def test_tree_attention_in_equal_shares_of_large_heads(d, hq, hk, nodes, batch):
         assert torch.equal(torch.isnan(o), torch.isnan(out[part]))
         assert torch.equal((l2 == -math.inf), (lse[part] == -math.inf))
         assert (l2 - lse[part]).nan_to_num(0).abs().max() <= 2 * (e + 4 * U * (most + 8) + 140 * U)
+
+
+# ------------------------------------------------------------------------------------------------------ large batches
+
+@gpu
+@pytest.mark.parametrize("batch,width,page,spare", [(4099, 6, 16, 3000), (65536, 3, 16, 40000)])
+def test_reserve_pages_of_large_batches(batch, width, page, spare):
+    rng = random.Random(batch)
+    table, lens, num_pages = reserve_case(rng, batch, width, page, spare, True)
+    new = [min(width * page, max(0, n + rng.choice([0, 1, 7, page, 3 * page, -5]))) for n in lens]
+    got, granted, err = run_reserve(table, lens, new, None, num_pages, page)
+    want, want_granted, _ = reserve_reference(table, lens, new, None, num_pages, page)
+    short = any(g < n for g, n, l in zip(want_granted, new, lens) if n > l)
+    assert err == (fd.DEVERR_NO_PAGES if short else 0)
+    assert granted == want_granted and np.array_equal(got, want)
+
+
+def test_reserve_pages_refuses_larger_batches():
+    lens = [torch.zeros(65537, dtype=torch.int32) for _ in range(3)]
+    refused("FDEC_ERR_UNSUPPORTED", cpu_reserve, page_table=torch.zeros(65537, 1, dtype=torch.int32), seq_lens=lens[0],
+            new_lens=lens[1], granted=lens[2], workspace=aligned_workspace(65537, 64))
