@@ -170,12 +170,14 @@ def outlier(c, b, node, power, logit=None, columns=slice(None)):
 
 
 @gpu
-@pytest.mark.parametrize("d,hq,hk,nodes", [(128, 8, 2, 13), (64, 4, 2, 40), (192, 4, 1, 20), (256, 4, 2, 64), (512, 2, 1, 33)])
+@pytest.mark.parametrize("d,hq,hk,nodes", [(128, 8, 2, 13), (64, 4, 2, 40), (192, 4, 1, 20), (256, 4, 2, 64),
+                                           (512, 2, 1, 33)])
 @pytest.mark.parametrize("power", [9, 12, 30, 40, 100])
 def test_large_rows_cost_the_others_nothing(d, hq, hk, nodes, power):
     """A value row far above the others: nodes that do not see it have their own rows' accuracy, those that do see it,
     with a weight near 0 among them, that of what it adds."""
-    for state, out_type, logit in ((True, torch.float32, None), (False, torch.float32, -30.0), (True, torch.bfloat16, -70.0)):
+    for state, out_type, logit in ((True, torch.float32, None), (False, torch.float32, -30.0),
+                                   (True, torch.bfloat16, -70.0)):
         c = Tree(d, hq, hk, nodes, 16, 2, "bf16", seed=power + nodes, counts=[nodes, nodes - 1], state=state)
         c.q[..., 0] = 8.0
         outlier(c, 0, 2, power, logit)
@@ -527,3 +529,47 @@ def test_reserve_pages_refuses_larger_batches():
     lens = [torch.zeros(65537, dtype=torch.int32) for _ in range(3)]
     refused("FDEC_ERR_UNSUPPORTED", cpu_reserve, page_table=torch.zeros(65537, 1, dtype=torch.int32), seq_lens=lens[0],
             new_lens=lens[1], granted=lens[2], workspace=aligned_workspace(65537, 64))
+
+
+# ------------------------------------------------------------------------------------------- the holder and its operators
+
+@gpu
+@pytest.mark.parametrize("kv", ["fp8", ""])
+@pytest.mark.parametrize("interleaved,chain,out_type", [(True, False, torch.bfloat16), (False, True, torch.float32)])
+def test_a_layer_of_the_holder_is_its_operators(kv, interleaved, chain, out_type):
+    """Weights, both rotations, E4M3 caches with scales, 16-bit results, lse, node counts: bit for bit the calls by hand."""
+    batch, nodes, page, hq, hk, d, pages = 3, 7, 16, 8, 2, 128, 40
+    g = torch.Generator().manual_seed(21)
+    rand = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    kv_type = torch.float8_e4m3fn if kv else torch.bfloat16
+    k, v = ((rand(pages, hk, page, d) * (8 if kv else 1)).to(kv_type) for _ in range(2))
+    scales = dict(k_scale=0.04, v_scale=0.3) if kv else dict(k_scale=1.0, v_scale=1.0)
+    qkv, weights = rand(batch * nodes, hq + 2 * hk, d).bfloat16(), [1 + 0.1 * rand(d).bfloat16() for _ in range(2)]
+    cos_sin = rand(200, d)
+    prefix, table = i32([50, 0, 33]), i32(np.arange(batch * 5).reshape(batch, 5))
+    parents = None if chain else i32([[-1, 0, 0, 1, 1, 2, 5]] * batch)
+    depths = None if chain else i32([[0, 1, 1, 2, 2, 2, 3]] * batch)
+    counts = i32([7, 4, 0])
+    tree = fd.TreeDecode([60] * batch, nodes, page, hq, hk, d, pages, "bf16", kv_dtype=kv)
+    x, kk, vv = qkv.clone(), k.clone(), v.clone()
+    out = torch.full((batch, nodes, hq, d), 5.0, dtype=out_type, device="cuda")
+    lse = torch.full((batch, nodes, hq), 5.0, device="cuda")
+    assert tree.reserve(table, prefix, (kk, vv)).tolist() == [57, 7, 40]
+    tree.attend(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], *weights, cos_sin, kk, vv, table, prefix, parents, depths, out,
+                lse, counts, interleaved=interleaved, **scales)
+    assert tree.device_errors() == 0
+    y, k2, v2 = qkv.clone(), k.clone(), v.clone()
+    at = prefix[:, None] + torch.arange(nodes, dtype=torch.int32, device="cuda")
+    turns = at if chain else prefix[:, None] + depths
+    seqs = torch.arange(batch, dtype=torch.int32, device="cuda").repeat_interleave(nodes)
+    fd.fdec_norm_rope_append(y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:], *weights, cos_sin, seqs, at.reshape(-1),
+                             y[:, :hq], k2, v2, table, page, 1e-6, interleaved, turns.reshape(-1), **scales)
+    rows = y[:, :hq].view(batch, nodes, hq, d)
+    o, l = torch.empty((batch, nodes, hq, d), device="cuda"), torch.empty((batch, nodes, hq), device="cuda")
+    plain = fd.PagedDecode([60] * batch, nodes, page, hq, hk, d, "bf16", kv_dtype=kv)
+    plain.run(rows, k2, v2, table, prefix, o, l, **scales)
+    want, want_lse = torch.full_like(out, 5.0), torch.full_like(lse, 5.0)
+    fd.fdec_tree_attention(rows, k2, v2, table, prefix, parents, o, l, want, want_lse, page, node_counts=counts, **scales)
+    for a, b in ((out, want), (lse, want_lse), (kk, k2), (vv, v2), (x, y)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert (out[2] == 5).all() and (out[1, 4:] == 5).all() and not (kk.view(torch.uint8) == k.view(torch.uint8)).all()
