@@ -7,7 +7,7 @@
 // aside.  The first entries that are in place are not touched.
 //
 // Bytes: every moved row, read and written once.  64 sequences, 32 layers of 8 heads of 128
-// (44 MB): 11.0 us, 4.0 TB/s; before the first row moves a CTA has read the path, then the
+// (44 MB): 10.6 us, 4.2 TB/s, replayed from a graph; before the first row moves a CTA has read the path, then the
 // page table, and 2048 CTAs are three rounds of the machine.  (Two columns a thread 12.0 us,
 // four 13.9; five, six and eight CTAs an SM instead of four 10.9 to 11.7; CTAs that walk over
 // several blocks of columns, the path read once, 13.8 to 17.5.)

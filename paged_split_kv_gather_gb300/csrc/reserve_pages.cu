@@ -14,9 +14,9 @@
 // 13.4 us, 256 14.6, 1024 21, 4096 60 and 65536 7.3 ms.)
 //
 // Bytes: the entries in use, a bit or two a page, and the copied rows, read and written.  64
-// sequences and 65536 pages: 8.4 to 8.8 us, the latencies of three dependent launches (clear 1,
-// mark 3, assign 3.5); 256 sequences of 2049 entries and a million pages: 14.0 to 14.8, the marks'
-// atomics among them; 64 forks in 16 layers: 14.1, of them 7.4 the copies (63 MB, 8.5 TB/s
+// sequences and 65536 pages: 8.9 us, the latencies of three dependent launches (clear 1,
+// mark 3, assign 3.5); 256 sequences of 2049 entries and a million pages: 14.8, the marks'
+// atomics among them; 64 forks in 16 layers: 13.9, of them 7.4 the copies (63 MB, 8.5 TB/s
 // of reads and writes that the L2 holds in part).
 #include <algorithm>
 #include <cstdint>

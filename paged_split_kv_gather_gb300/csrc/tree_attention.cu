@@ -12,8 +12,8 @@
 // Bytes: 2 D of q, 4 D of o_p, 4 D or 2 D of the result for a query row, against 4 D x 64
 // operations or less: bound by HBM, if anything hides the latencies.  Queries and o_p are
 // therefore copied into shared memory a tile and a block ahead (requested where they are
-// used, or held in registers, 64 trees of 64 nodes took 73 and 52 us; now 40.4, 4.6 TB/s, with
-// the L1 pipe 60 % busy).  Few small trees are latencies: lengths, page ids, keys and values
+// used, or held in registers, 64 trees of 64 nodes took 73 and 52 us; now 40.5, 4.6 TB/s, with
+// the L1 pipe 56 % busy).  Few small trees are latencies: lengths, page ids, keys and values
 // are three dependent reads (of 3.7 us for one tree; 1 us for the first two), which is why the
 // rest is asked for behind them and the ancestors are another warp's.  mma.sync keeps S and P in registers; a tcgen05 tile of 128 rows
 // would be mostly empty for trees of a few nodes, and the tensor pipe is not what bounds.

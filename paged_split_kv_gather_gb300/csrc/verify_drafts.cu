@@ -23,7 +23,7 @@
 // wait, in fp64 16 trees 14.6 instead of 11.5.
 //
 // Bytes: the rows p and q of the last node, once from HBM.  64 sequences, p and q of 131072 in
-// fp32: 18.5 us, 3.3 TB/s; all sequences read their tokens, sum and search at the same time,
+// fp32: 18.6 us, 3.2 TB/s; all sequences read their tokens, sum and search at the same time,
 // so most of the 7 us that one sequence takes come on top of the 9 us for the bytes.
 #include <algorithm>
 #include <cstdint>
