@@ -771,6 +771,7 @@ class TreeDecode:
             raise ValueError("drafted rows go into 16-bit and E4M3 caches")
         device = torch.device(device or "cuda")
         self.batch, self.num_nodes, self.page_size, self.num_pages = batch, num_nodes, page_size, num_pages
+        self.max_pages = max(-(-int(n) // page_size) for n in max_lens)
         with torch.cuda.device(device):
             self.prefix = PagedDecode(max_lens, num_nodes, page_size, num_qo_heads, num_kv_heads, head_dim, dtype,
                                       device=device, page_lists=False, kv_dtype=kv_dtype)
@@ -828,6 +829,8 @@ class TreeDecode:
         n, hq, d = q.shape
         if depths is None and parents is not None:
             raise ValueError("a tree's rows are rotated by the depths of its nodes")
+        if page_table.shape[1] < self.max_pages:  # (a view's rows are further apart than they are wide)
+            raise ValueError(f"page_table has {page_table.shape[1]} columns, max_lens need {self.max_pages}")
         with self._on(stream):
             positions = (prefix_lens[:, None] + self.offsets).reshape(-1)
             turns = None if depths is None else (prefix_lens[:, None] + depths).reshape(-1)

@@ -331,16 +331,16 @@ def test_a_holder_works_on_its_own_device(monkeypatch):
     for name in ("fdec_norm_rope_append", "fdec_tree_attention", "fdec_verify_drafts", "fdec_reserve_pages"):
         monkeypatch.setattr(fd, name, call(name))
     tree = fd.TreeDecode.__new__(fd.TreeDecode)
-    tree.batch, tree.num_nodes, tree.page_size, tree.num_pages = 1, 2, 16, 8
+    tree.batch, tree.num_nodes, tree.page_size, tree.num_pages, tree.max_pages = 1, 2, 16, 8, 2
     tree.errors = SimpleNamespace(device=torch.device("cuda:1"), item=lambda: 0, zero_=lambda: None)
     tree.prefix = SimpleNamespace(run=call("run"), device_errors=call("device_errors", 0))
     tree.nodes, tree.nowhere = torch.arange(2, dtype=torch.int32), torch.full((1,), -1, dtype=torch.int32)
     tree.offsets, tree.counts = tree.nodes.repeat(1, 1), torch.full((1,), 2, dtype=torch.int32)
     tree.batch_indices = tree.o = tree.state_lse = tree.workspace = tree.path = tree.path_lens = tree.tokens = None
     tree.granted = lens = torch.zeros(1, dtype=torch.int32)
-    rows = torch.zeros(2, 1, 64)
+    rows, table = torch.zeros(2, 1, 64), torch.zeros(1, 2, dtype=torch.int32)
     tree.reserve(None, lens)
-    tree.attend(rows, rows, rows, None, None, None, None, None, None, lens, None, None, None)
+    tree.attend(rows, rows, rows, None, None, None, None, None, table, lens, None, None, None)
     tree.verify(None, None, None, None, None)
     assert tree.device_errors() == 0
     assert [name for name, _ in seen] == ["fdec_reserve_pages", "fdec_norm_rope_append", "run", "fdec_tree_attention",
@@ -573,3 +573,14 @@ def test_a_layer_of_the_holder_is_its_operators(kv, interleaved, chain, out_type
     for a, b in ((out, want), (lse, want_lse), (kk, k2), (vv, v2), (x, y)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert (out[2] == 5).all() and (out[1, 4:] == 5).all() and not (kk.view(torch.uint8) == k.view(torch.uint8)).all()
+
+
+def test_a_holder_refuses_tables_of_fewer_columns_than_its_longest_prefix_needs():
+    """A view of a wide table passes for one by its stride."""
+    tree = fd.TreeDecode.__new__(fd.TreeDecode)
+    tree.max_pages = 4
+    wide = torch.zeros(2, 8, dtype=torch.int32)
+    rows = torch.zeros(2, 1, 64)
+    with pytest.raises(ValueError, match="columns"):
+        tree.attend(rows, rows, rows, None, None, None, None, None, wide[:, 5:], torch.zeros(2, dtype=torch.int32), None, None,
+                    None)
