@@ -145,8 +145,8 @@ __device__ __forceinline__ void put_values(uint8_t* row, int c, uint4 v) {
 // 2^-24, half a step of fp32, of what the rows that it does see hold in those columns.
 constexpr unsigned kSpread = 8;
 
-// CTAs on an SM that the registers of S, P and O are to allow.  (A fourth, with 128 registers a thread: 512 heads of 4 tiles of 16
-// nodes 8.4 us instead of 10.6; but at head_dim 256 16 trees of 13 nodes 6.5 us instead of 6.0.)
+// CTAs on an SM that the registers of S, P and O are to allow.  (A fourth, with 128 registers a thread: 512 heads of 4
+// tiles of 16 nodes 8.4 us instead of 10.6; but at head_dim 256 16 trees of 13 nodes 6.5 us instead of 6.0.)
 constexpr int tree_ctas(int head_dim, int ks) { return ks == 1 && head_dim <= 128 ? 4 : 3; }
 
 template <int D, bool BF16, bool KV8, int KS>
